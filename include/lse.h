@@ -383,6 +383,138 @@ LSE_API lse_status lse_last_cuda_error(int *cuda_err);
 LSE_API lse_status lse_forward_split_static(const void *x, lse_dtype dtype, int64_t B, int64_t N,
                                             int64_t row_stride, float *out, lse_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Operators at the vocabulary-sized ends of a language model's step: token
+ * statistics of the logits and their gradient, the norm and clipping of the
+ * gradients, and the embedding rows and their gradient.  Conventions, status
+ * codes and streams as above.
+ * ------------------------------------------------------------------------ */
+
+#define LSE_MAX_TOP_K 32
+
+/*
+ * lse_token_stats -- for every row of logits, with p = softmax(x[b, :]):
+ *
+ *     logprob[b] = x[b, target[b]] - lse[b]          lse[b] as in lse_forward
+ *     entropy[b] = -sum_n p_n log p_n                (0 log 0 = 0; in nats)
+ *     top        = the top_k largest logits: top_logprob[b, k] =
+ *                  x[b, top_index[b, k]] - lse[b], largest first, equal values
+ *                  by the lower column
+ *
+ *   target       B int64 columns, or NULL together with logprob; one outside
+ *                [0, N) gives logprob NaN (it is never read).
+ *   top_k        0 .. LSE_MAX_TOP_K; 0 asks for no alternatives (then
+ *                top_logprob and top_index may be NULL).  N <= INT32_MAX else.
+ *   logprob, entropy, lse_out   B floats each, or NULL when not wanted; at
+ *                least one output must be asked for.
+ *   top_logprob, top_index      [B, top_k] floats and int64, row-major.
+ * Entries beyond the row (top_k > N) hold index -1 and log-probability -inf.
+ * Among equal values -0 equals +0; a NaN ranks above every number.  entropy is
+ * NaN for a row that is no distribution: one that holds a NaN or +inf, or
+ * nothing but -inf (or N == 0).  Log-probabilities follow IEEE arithmetic on
+ * x - lse, so they are NaN in a row of only -inf.
+ * Results do not depend on scheduling: equal inputs give equal bits.
+ */
+LSE_API lse_status lse_token_stats(const void *x, lse_dtype dtype, int64_t B, int64_t N,
+                                   int64_t row_stride, const int64_t *target, int64_t top_k,
+                                   float *logprob, float *entropy, float *lse_out,
+                                   float *top_logprob, int64_t *top_index, lse_stream_t stream);
+
+/*
+ * lse_token_stats_backward -- the gradient of lse_token_stats' outputs:
+ *
+ *     dx_n = p_n (g_lse - g_lp - sum_k g_top_k - g_H (log p_n + H))
+ *            + g_lp [n = target] + sum_k g_top_k [n = top_index_k]
+ *
+ * with p_n = exp(x_n - lse), H the entropy, and a masked element's (p_n = 0)
+ * term zero.  One read of x, one write of dx.
+ *   lse, entropy, top_index   the forward's outputs (entropy only with
+ *                grad_entropy, top_index only with grad_top).
+ *   grad_logprob, grad_entropy, grad_lse   B floats each; grad_top [B, top_k].
+ *                NULL stands for zeros.
+ *   dx           as for lse_backward: x's element type, rows dx_row_stride
+ *                apart, computed in f32 and rounded to nearest-even on store;
+ *                may be x itself (same row_stride), other overlaps undefined.
+ * The gradient of a logprob whose target lies outside [0, N), or of an
+ * alternative whose index does, is dropped.  A row whose gradients are all zero
+ * or dropped gets zeros whatever it holds (it is not read); other rows follow
+ * IEEE arithmetic on the formula.
+ */
+LSE_API lse_status lse_token_stats_backward(
+    const void *x, lse_dtype dtype, int64_t B, int64_t N, int64_t row_stride, const float *lse,
+    const float *entropy, const int64_t *target, const int64_t *top_index, int64_t top_k,
+    const float *grad_logprob, const float *grad_entropy, const float *grad_top,
+    const float *grad_lse, void *dx, int64_t dx_row_stride, lse_stream_t stream);
+
+/* One tensor of a gradient list: numel contiguous elements. */
+typedef struct {
+    const void *data;  /* device pointer, aligned to its element size */
+    void *out;         /* lse_grad_clip: where the clipped values go; NULL or
+                          data itself = in place                              */
+    int64_t numel;
+    int32_t dtype;     /* lse_dtype, each tensor its own */
+} lse_tensor;
+
+/*
+ * lse_grad_norm -- norm[0] = sqrt(sum over all tensors and elements of g^2).
+ *   tensors      HOST array of `count` descriptors, read during the call.
+ *   norm         device pointer to one float.
+ * Squares are summed without overflow or underflow over the whole f32 range
+ * (the result is +inf only where the norm itself exceeds it, or a gradient is
+ * infinite); a NaN gradient gives NaN.  No elements give 0.  The summation
+ * order is fixed by the sizes alone.  Takes a few KB of stream-ordered scratch.
+ */
+LSE_API lse_status lse_grad_norm(const lse_tensor *tensors, int64_t count, float *norm,
+                                 lse_stream_t stream);
+
+/*
+ * lse_grad_clip -- norm[0] as lse_grad_norm, and every gradient times
+ *
+ *     c = min(1, max_norm / (norm + eps)),
+ *
+ * computed in f32 and rounded to nearest-even on store.  max_norm >= 0 and
+ * eps >= 0.  Tensors clipped in place are not written when c = 1; those with an
+ * `out` of their own are copied then.  An infinite norm gives c = 0 and a NaN
+ * norm c = NaN, so infinite and NaN gradients become NaN.  Distinct tensors
+ * and outs must not overlap.
+ */
+LSE_API lse_status lse_grad_clip(const lse_tensor *tensors, int64_t count, float max_norm,
+                                 float eps, float *norm, lse_stream_t stream);
+
+/*
+ * lse_embedding -- out[t, :] = scale * table[ids[t], :], t < T, D columns.
+ *   table        V rows of D elements, table_stride apart (elements, >= D).
+ *   ids          device pointer to T int64; one outside [0, V) gives a row of
+ *                NaN (the table is not read for it).
+ *   out          T rows of the table's element type, out_stride apart (>= D);
+ *                computed in f32 and rounded to nearest-even on store; must
+ *                not overlap the table.
+ */
+LSE_API lse_status lse_embedding(const void *table, lse_dtype dtype, int64_t V, int64_t D,
+                                 int64_t table_stride, const int64_t *ids, int64_t T, float scale,
+                                 void *out, int64_t out_stride, lse_stream_t stream);
+
+/*
+ * lse_embedding_backward -- the table's gradient:
+ *
+ *     dtable[v, :] = scale * sum over t with ids[t] = v of grad[t, :]
+ *
+ * (plus the dtable[v, :] that was there, when accumulate is nonzero).  Tokens
+ * are sorted by id and summed in f32 in an order that the sizes and ids alone
+ * fix (so equal inputs give equal bits), and rounded once.  Rows without a
+ * token are zeroed, or left as they are with accumulate.
+ *   padding      tokens with this id add nothing (-1: none is left out);
+ *                neither do ids outside [0, V).
+ *   dtable       V rows of D elements of dtable_dtype, which is dtype or
+ *                LSE_F32, dtable_stride apart (>= D).
+ * T, V <= INT32_MAX.  Takes stream-ordered scratch.
+ */
+LSE_API lse_status lse_embedding_backward(const void *grad, lse_dtype dtype, int64_t T, int64_t D,
+                                          int64_t grad_stride, const int64_t *ids, int64_t V,
+                                          float scale, int64_t padding, void *dtable,
+                                          lse_dtype dtable_dtype, int64_t dtable_stride,
+                                          int accumulate, lse_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -12,6 +12,7 @@ from ._binding import (  # noqa: F401
     PATHS,
     LseError,
     LsePlan,
+    LseTensor,
     library_path,
     load,
     logsumexp,
@@ -36,4 +37,17 @@ from ._binding import (  # noqa: F401
     lse_trim_memory,
     lse_wait_timeouts,
     status_string,
+)
+from ._model_ops import (  # noqa: F401
+    MAX_TOP_K,
+    GradList,
+    TokenStats,
+    embedding,
+    lse_embedding,
+    lse_embedding_backward,
+    lse_grad_clip,
+    lse_grad_norm,
+    lse_token_stats,
+    lse_token_stats_backward,
+    token_stats,
 )

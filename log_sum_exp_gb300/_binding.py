@@ -25,7 +25,9 @@ ABI_FUNCTIONS = ["lse_forward", "lse_plan_query", "lse_forward_plan", "lse_forwa
                  "lse_forward_host", "lse_token_logprob", "lse_token_logprob_plan",
                  "lse_backward", "lse_forward_strided", "lse_backward_strided",
                  "lse_trim_memory", "lse_wait_timeouts", "lse_set_wait_limit", "lse_status_string",
-                 "lse_last_cuda_error", "lse_forward_split_static"]
+                 "lse_last_cuda_error", "lse_forward_split_static",
+                 "lse_token_stats", "lse_token_stats_backward", "lse_grad_norm", "lse_grad_clip",
+                 "lse_embedding", "lse_embedding_backward"]
 
 
 class LsePlan(ctypes.Structure):
@@ -47,6 +49,16 @@ class LsePlan(ctypes.Structure):
         d = {name: getattr(self, name) for name, _ in self._fields_}
         d["path"] = PATH_NAMES.get(self.path, self.path)
         return d
+
+
+class LseTensor(ctypes.Structure):
+    """Mirror of ``lse_tensor``."""
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("numel", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+    ]
 
 
 class LseError(RuntimeError):
@@ -105,6 +117,21 @@ def load() -> ctypes.CDLL:
         lib.lse_backward_strided.argtypes = [vp, i32, i64, i64, i64, i64, i64, vp, vp, vp, i64,
                                              i64, vp]
         lib.lse_backward_strided.restype = i32
+        f32 = ctypes.c_float
+        lib.lse_token_stats.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, vp, vp, vp, vp, vp]
+        lib.lse_token_stats.restype = i32
+        lib.lse_token_stats_backward.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp, i64, vp,
+                                                 vp, vp, vp, vp, i64, vp]
+        lib.lse_token_stats_backward.restype = i32
+        lib.lse_grad_norm.argtypes = [vp, i64, vp, vp]
+        lib.lse_grad_norm.restype = i32
+        lib.lse_grad_clip.argtypes = [vp, i64, f32, f32, vp, vp]
+        lib.lse_grad_clip.restype = i32
+        lib.lse_embedding.argtypes = [vp, i32, i64, i64, i64, vp, i64, f32, vp, i64, vp]
+        lib.lse_embedding.restype = i32
+        lib.lse_embedding_backward.argtypes = [vp, i32, i64, i64, i64, vp, i64, f32, i64, vp, i32,
+                                               i64, i32, vp]
+        lib.lse_embedding_backward.restype = i32
         lib.lse_wait_timeouts.argtypes = [ctypes.POINTER(ctypes.c_ulonglong)]
         lib.lse_wait_timeouts.restype = i32
         lib.lse_set_wait_limit.argtypes = [ctypes.c_uint32]

@@ -555,6 +555,23 @@ void record_cuda_error(cudaError_t e) {
     cudaGetLastError();
 }
 
+lse_status device_sms(int* sms) {
+    int dev = 0;
+    const DeviceInfo* info = nullptr;
+    const lse_status st = device_info(&dev, &info);
+    if (st == LSE_OK) *sms = info->sms;
+    return st;
+}
+
+lse_status take_scratch(void** p, size_t bytes, cudaStream_t stream) {
+    int dev = 0;
+    const DeviceInfo* info = nullptr;
+    const lse_status st = device_info(&dev, &info);
+    if (st != LSE_OK) return st;
+    const cudaError_t e = scratch_alloc(*info, p, bytes, stream);
+    return e == cudaSuccess ? LSE_OK : cuda_fail(e, LSE_ERR_ALLOC);
+}
+
 cudaError_t launch_fill_neg_inf(float* out, float* logprob, int64_t B, cudaStream_t stream) {
     int64_t grid = ceil_div(B, 256);
     if (grid > 65536) grid = 65536;

@@ -191,6 +191,17 @@ uint32_t default_stage_wait_polls();
 
 // Sets the calling thread's error reported by lse_last_cuda_error.
 void record_cuda_error(cudaError_t e);
+// The status of a finished launch (records the error of a failed one).
+inline lse_status cuda_status(cudaError_t e) {
+    if (e == cudaSuccess) return LSE_OK;
+    record_cuda_error(e);
+    return LSE_ERR_CUDA;
+}
+// SMs of the current device.
+lse_status device_sms(int* sms);
+// Stream-ordered scratch of the current device from the library pool (the
+// default pool while `stream` is captured); free with cudaFreeAsync.
+lse_status take_scratch(void** p, size_t bytes, cudaStream_t stream);
 
 // The argument checks of the row entry points (lse_api.cu): dtype, B, N,
 // row_stride, NULL and alignment of x and out, int64 byte extent.
