@@ -20,6 +20,7 @@
 #include <cuda_runtime.h>
 
 #include "lse_device.cuh"
+#include "lse_edges.cuh"
 #include "lse_internal.h"
 #include "lse_topk.cuh"
 
@@ -36,6 +37,8 @@ struct StatsArgs {
     float* lse;
     float* top_logprob;  // [B, K]
     int64_t* top_index;
+    int cluster;         // CTAs that share a row
+    int chunk_batches;   // batches of a chunk of the long-row kernel
 };
 
 struct StatsBackwardArgs {
@@ -87,6 +90,10 @@ __device__ __forceinline__ StatAcc stat_warp_merge(StatAcc a) {
         b.u = __shfl_xor_sync(0xffffffffu, a.u, off);
         a = stat_merge(a, b);
     }
+    // The two sides of a merge may round differently: lane 0's result for all.
+    a.m = __shfl_sync(0xffffffffu, a.m, 0);
+    a.s = __shfl_sync(0xffffffffu, a.s, 0);
+    a.u = __shfl_sync(0xffffffffu, a.u, 0);
     return a;
 }
 
@@ -96,105 +103,469 @@ __device__ __forceinline__ float stat_entropy(StatAcc a) {
     return kLn2 * (lg2(a.s) + a.u / a.s);
 }
 
-constexpr int kStatThreads = 256;
-constexpr int kStatWarps = kStatThreads / 32;
-constexpr int kScanElems = 4;  // elements per thread and tile of the top-K scan
 
-// The K largest keys of a row, in row order: a running list, and per tile the
-// elements above its K-th key, which warps sort and merge into it.  Equal values
-// later in the row rank lower, so they are not taken up again.
-template <int DT>
-__device__ __forceinline__ void scan_topk(const void* rp, int64_t N, int K, uint64_t* list,
-                                          uint64_t* found, int* count, uint64_t* warp_list) {
-    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-    if (tid < 32) list[tid] = 0;
-    __syncthreads();
-    for (int64_t base = 0; base < N; base += kStatThreads * kScanElems) {
-        const uint64_t bar = list[K - 1];
-        if (tid == 0) *count = 0;
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < kScanElems; ++j) {
-            const int64_t i = base + tid + j * kStatThreads;
-            if (i < N) {
-                const uint64_t k = topk_key(load_elem<DT>(rp, i), static_cast<uint32_t>(i));
-                if (k > bar) found[atomicAdd(count, 1)] = k;
-            }
-        }
-        __syncthreads();
-        const int n = *count;
-        if (n == 0) continue;
-        uint64_t best = 0;
-        for (int at = wid * 32; at < n; at += kStatThreads)
-            best = list_merge(best, list_sort(at + lane < n ? found[at + lane] : 0, lane), lane);
-        warp_list[tid] = best;
-        __syncthreads();
-        if (wid == 0) {
-            uint64_t k = list[lane];
-            for (int w = 0; w < kStatWarps; ++w) k = list_merge(k, warp_list[w * 32 + lane], lane);
-            list[lane] = k;
-        }
-        __syncthreads();
+// x - lse as (x - max) - log sum exp(x - max): next to a large maximum lse itself
+// has few digits left for the logarithm.
+__device__ __forceinline__ float stat_logprob(float x, StatAcc a, float lse) {
+    if (a.s != a.s || !(fabsf(a.m) < __int_as_float(0x7f800000))) return x - lse;
+    return (x - a.m) - kLn2 * lg2(a.s);
+}
+
+// Raise the running maximum to cm, rescaling both sums once.
+__device__ __forceinline__ void stat_raise(StatAcc& a, float& mu, float cm) {
+    if (cm > a.m) {
+        mu = shift_of(cm);
+        a = stat_shift(a, mu);
+        a.m = cm;
     }
 }
 
-// A CTA per row.
+// Add sum 2^z and sum 2^z (-z) over W raw words, two elements at a time (packed
+// FP32) into two pairs of accumulators each.  The clamp keeps 0 * inf out of u; a
+// NaN element stays in s, which decides.
+template <int DT, int W>
+__device__ __forceinline__ void stat_add_words(StatAcc& a, float mu, const uint32_t (&w)[W]) {
+    const uint64_t mu2 = f2_pack(mu, mu), log2e2 = f2_pack(kLog2e, kLog2e);
+    uint64_t s[2] = {0ull, 0ull}, u[2] = {0ull, 0ull};
+#pragma unroll
+    for (int i = 0; i < W; i += DT == kF32 ? 2 : 1) {
+        uint64_t x;
+        if constexpr (DT == kF32) x = f2_pack(__uint_as_float(w[i]), __uint_as_float(w[i + 1]));
+        else x = f2_pack(word_lo<DT>(w[i]), word_hi<DT>(w[i]));
+        const int k = DT == kF32 ? (i >> 1) & 1 : i & 1;
+        float z0, z1;
+        f2_unpack(f2_mul(f2_sub(x, mu2), log2e2), z0, z1);
+        const uint64_t e = f2_pack(ex2(z0), ex2(z1));
+        s[k] = f2_add(s[k], e);
+        u[k] = f2_fma(e, f2_pack(fmaxf(z0, kFarBelow), fmaxf(z1, kFarBelow)), u[k]);
+    }
+    float s0, s1, s2, s3, u0, u1, u2, u3;
+    f2_unpack(s[0], s0, s1);
+    f2_unpack(s[1], s2, s3);
+    f2_unpack(u[0], u0, u1);
+    f2_unpack(u[1], u2, u3);
+    a.s += (s0 + s1) + (s2 + s3);
+    a.u -= (u0 + u1) + (u2 + u3);
+}
+
+// ---------------------------------------------------------------------------
+// Rows as 16-byte vectors: the aligned vectors that cover the row, the elements
+// outside it masked with -inf.
+// ---------------------------------------------------------------------------
+struct Row {
+    const char* a0;    // 16-byte boundary at or before the row
+    uint32_t off;      // bytes from there to the row
+    int64_t end;       // the row's end, bytes from a0
+    int64_t vectors;
+};
+
 template <int DT>
-__global__ void __launch_bounds__(kStatThreads)
-lse_stats_kernel(const StatsArgs a) {
-    __shared__ uint64_t list[32], warp_list[kStatThreads], found[kStatThreads * kScanElems];
-    __shared__ float part[3][kStatWarps];
-    __shared__ float row_lse;
-    __shared__ int count;
-    pdl_trigger();
-    pdl_wait();
+__device__ __forceinline__ Row make_row(const void* x, int64_t row, int64_t row_stride, int64_t N) {
+    const char* rp = static_cast<const char*>(x) + row * row_stride * DType<DT>::bytes;
+    Row r;
+    r.off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(rp) & 15u);
+    r.a0 = rp - r.off;
+    r.end = r.off + N * DType<DT>::bytes;
+    r.vectors = N > 0 ? (r.end + 15) >> 4 : 0;
+    return r;
+}
+
+// Vector k of the row into 4 words of w; -inf past `limit`.
+template <int DT>
+__device__ __forceinline__ void load_vector(const Row& r, int64_t k, int64_t limit, uint32_t* w) {
+    if (k < limit) {
+        const uint4 v = ldg_stream16(r.a0 + k * 16);
+        w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    } else {
+        w[0] = w[1] = w[2] = w[3] = neg_inf_word<DT>();
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void mask_vector(const Row& r, int64_t k, uint32_t* w) {
+    uint32_t q[4] = {w[0], w[1], w[2], w[3]};
+    if (k == 0) mask_prefix<DT>(q, static_cast<int>(r.off));
+    if (k == r.vectors - 1) mask_suffix<DT>(q, static_cast<int>(r.end - k * 16));
+    w[0] = q[0]; w[1] = q[1]; w[2] = q[2]; w[3] = q[3];
+}
+
+// The column of element i of vector k (out of [0, N) for the masked ones).
+template <int DT>
+__device__ __forceinline__ int64_t column_of(const Row& r, int64_t k, int i) {
+    return (k * 16 - static_cast<int64_t>(r.off)) / DType<DT>::bytes + i;
+}
+
+// ---------------------------------------------------------------------------
+// The K largest keys.
+//
+// While the row streams by, nothing is kept of it but the maximum of every
+// thread's chunk (a few vectors).  The K-th largest of the maxima of 32 groups of
+// threads is a bound that at least K elements reach, so the K largest are among
+// the elements that reach it -- for values in no particular order a few more than
+// K.  Only the chunks whose maximum reaches the bound are read again, and each
+// element found there takes the place that the number of larger ones gives it.
+// Rows where this finds too many (long runs of equal values), too few (nearly
+// everything masked with -inf) or a NaN are scanned once more in full.
+// ---------------------------------------------------------------------------
+
+// K-th largest of the warp's 32 values.
+__device__ __forceinline__ float kth_largest(float v, int K, int lane) {
+#pragma unroll
+    for (int size = 2; size <= 32; size <<= 1) {
+#pragma unroll
+        for (int stride = size >> 1; stride > 0; stride >>= 1) {
+            const float o = __shfl_xor_sync(0xffffffffu, v, stride);
+            v = ((lane & stride) == 0) == ((lane & size) == 0) ? fmaxf(v, o) : fminf(v, o);
+        }
+    }
+    return __shfl_sync(0xffffffffu, v, K - 1);
+}
+
+// A warp's list of the K largest keys of vectors [k0, k1), read in order.  Past
+// the first few vectors nearly every one is dismissed by its values alone: none
+// above the K-th so far (an equal one later in the row ranks lower).
+template <int DT>
+__device__ __forceinline__ uint64_t scan_vectors(const Row& r, int64_t k0, int64_t k1, int64_t N,
+                                                 int K, int lane) {
+    constexpr int EPV = 16 / DType<DT>::bytes;
+    uint64_t best = 0, bar = 0;
+    float bar_value = __int_as_float(kNegInfF32);
+    bool full = false;  // K keys found: values equal to the K-th no longer count
+    for (int64_t k = k0; k < k1; k += 32) {
+        uint32_t w[4];
+        load_vector<DT>(r, k + lane, k1, w);
+        bool any = false;
+#pragma unroll
+        for (int i = 0; i < EPV; ++i) {
+            const float x = word_elem<DT>(w, i);
+            any |= !full || x > bar_value || x != x;
+        }
+        if (!__any_sync(0xffffffffu, any)) continue;
+#pragma unroll 1
+        for (int i = 0; i < EPV; ++i) {
+            const int64_t col = column_of<DT>(r, k + lane, i);
+            uint64_t key = 0;
+            if (k + lane < k1 && col >= 0 && col < N) key = topk_key(word_elem<DT>(w, i), static_cast<uint32_t>(col));
+            if (!__any_sync(0xffffffffu, key > bar)) continue;
+            best = list_merge(best, list_sort(key, lane), lane);
+            bar = __shfl_sync(0xffffffffu, best, K - 1);
+            full = bar != 0;
+            bar_value = full ? key_value(bar) : bar_value;
+        }
+    }
+    return best;
+}
+
+// Writes of one row's results.
+struct StatsOut {
+    __device__ static void row(const StatsArgs& a, int64_t row, StatAcc acc, float xt, float lse) {
+        if (a.lse) a.lse[row] = lse;
+        if (a.entropy) a.entropy[row] = stat_entropy(acc);
+        if (a.logprob) a.logprob[row] = stat_logprob(xt, acc, lse);
+    }
+    __device__ static void top(const StatsArgs& a, int64_t row, int place, uint64_t key, StatAcc acc, float lse) {
+        a.top_index[row * a.K + place] = key ? key_column(key) : -1;
+        a.top_logprob[row * a.K + place] =
+            key ? stat_logprob(key_value(key), acc, lse) : __int_as_float(kNegInfF32);
+    }
+};
+
+// Cluster barrier and the place of a shared variable in another CTA of the cluster.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+template <typename V>
+__device__ __forceinline__ V* cluster_map(V* p, uint32_t cta) {
+    uint64_t q;
+    asm("mapa.u64 %0, %1, %2;" : "=l"(q) : "l"(reinterpret_cast<uint64_t>(p)), "r"(cta));
+    return reinterpret_cast<V*>(q);
+}
+
+// ---------------------------------------------------------------------------
+// Long rows: a CTA per row, or a cluster of CTAs that share one.
+// ---------------------------------------------------------------------------
+constexpr int kStatU = 8;         // vectors per thread and batch
+constexpr int kStatChunks = 16;   // chunk maxima kept per thread
+constexpr int kChunkList = 256;   // chunks that may be read again
+constexpr int kFoundList = 512;   // elements that may reach the bound (32 per warp at least)
+constexpr int kMaxCluster = 16;
+
+template <int T, bool CLUSTER>
+struct StatsShared {
+    float chunk_max[kStatChunks * T];
+    uint64_t found[kFoundList];
+    uint64_t own[kMaxTopK];
+    uint64_t keys[CLUSTER ? kMaxCluster * kMaxTopK : 1];  // in the cluster's first CTA
+    float acc[3][CLUSTER ? kMaxCluster : 1];
+    float part[3][T / 32];
+    float group_max[32];
+    int chunk[kChunkList];
+    int chunks, founds;
+};
+
+// `n` keys of `from`, all different but for the empty ones, to the places that
+// their ranks give them; places past the last key stay empty.
+template <int T, typename PUT>
+__device__ __forceinline__ void place_keys(const uint64_t* from, int n, int K, PUT put) {
+    for (int i = threadIdx.x; i < n; i += T) {
+        const uint64_t key = from[i];
+        if (key == 0) continue;
+        int rank = 0;
+        for (int j = 0; j < n; ++j) rank += from[j] > key;
+        if (rank < K) put(rank, key);
+    }
+}
+
+template <int DT, int T, bool CLUSTER>
+__global__ void __launch_bounds__(T, 1024 / T)
+lse_stats_kernel(const __grid_constant__ StatsArgs a) {
+    constexpr int U = kStatU, NW = T / 32, EPV = 16 / DType<DT>::bytes;
+    __shared__ StatsShared<T, CLUSTER> sh;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-    for (int64_t row = blockIdx.x; row < a.B; row += gridDim.x) {
-        const char* rp = static_cast<const char*>(a.x) + row * a.row_stride * DType<DT>::bytes;
-        StatAcc acc = stat_identity();
-        for (int64_t i = tid; i < a.N; i += kStatThreads) {
-            const float x = load_elem<DT>(rp, i);
-            if (x > acc.m) {
-                acc = stat_shift(acc, shift_of(x));
-                acc.m = x;
+    pdl_trigger();
+    if (CLUSTER) cluster_arrive();  // (waited for before the first remote store)
+    pdl_wait();
+
+    const int P = CLUSTER ? a.cluster : 1;
+    const int64_t row = blockIdx.x / P;
+    const int seg = static_cast<int>(blockIdx.x - row * P);
+    const Row r = make_row<DT>(a.x, row, a.row_stride, a.N);
+    const int64_t per = CLUSTER ? (r.vectors + P - 1) / P : r.vectors;
+    const int64_t k_begin = seg * per < r.vectors ? seg * per : r.vectors;
+    const int64_t k_end = k_begin + per < r.vectors ? k_begin + per : r.vectors;
+
+    StatAcc acc = stat_identity();
+    float mu = 0.0f;
+    const bool gather = a.logprob != nullptr && seg == 0 && tid == 0;
+    const int64_t target = gather ? __ldg(a.target + row) : -1;
+    float xt = __int_as_float(0x7fc00000);
+    if (target >= 0 && target < a.N) xt = load_elem<DT>(r.a0 + r.off, target);
+
+    // The row, in batches of U vectors per thread; a chunk is chunk_batches of them.
+    {
+        float chunk_max = __int_as_float(kNegInfF32);
+        int chunk = 0, in_chunk = 0;
+        for (int64_t k = k_begin + tid; k - tid < k_end; k += U * T) {
+            uint32_t w[4 * U];
+            if (k - tid + U * T <= k_end) {
+#pragma unroll
+                for (int j = 0; j < U; ++j) {
+                    const uint4 v = ldg_stream16(r.a0 + (k + j * T) * 16);
+                    w[4 * j] = v.x; w[4 * j + 1] = v.y; w[4 * j + 2] = v.z; w[4 * j + 3] = v.w;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < U; ++j) load_vector<DT>(r, k + j * T, k_end, &w[4 * j]);
             }
-            const float z = (x - shift_of(acc.m)) * kLog2e;
-            const float e = ex2(z);
-            acc.s += e;
-            acc.u = fmaf(-e, fmaxf(z, kFarBelow), acc.u);
-        }
-        acc = stat_warp_merge(acc);
-        if (lane == 0) {
-            part[0][wid] = acc.m;
-            part[1][wid] = acc.s;
-            part[2][wid] = acc.u;
-        }
-        __syncthreads();
-        if (tid == 0) {
-            acc = stat_identity();
-            for (int w = 0; w < kStatWarps; ++w)
-                acc = stat_merge(acc, StatAcc{part[0][w], part[1][w], part[2][w]});
-            const float l = acc_finalize(Acc{acc.m, acc.s});
-            row_lse = l;
-            if (a.lse) a.lse[row] = l;
-            if (a.entropy) a.entropy[row] = stat_entropy(acc);
-            if (a.logprob) {
-                const int64_t t = a.target[row];
-                a.logprob[row] = t >= 0 && t < a.N ? load_elem<DT>(rp, t) - l : __int_as_float(0x7fc00000);
+            if (k == 0 || (k - tid <= r.vectors - 1 && r.vectors - 1 < k - tid + U * T)) {
+#pragma unroll
+                for (int j = 0; j < U; ++j) {
+                    if (k + j * T == 0 || k + j * T == r.vectors - 1) mask_vector<DT>(r, k + j * T, &w[4 * j]);
+                }
+            }
+            const float cm = words_max<DT, 4 * U>(w);
+            stat_raise(acc, mu, cm);
+            stat_add_words<DT, 4 * U>(acc, mu, w);
+            chunk_max = fmaxf(chunk_max, cm);
+            if (++in_chunk == a.chunk_batches) {
+                sh.chunk_max[chunk * T + tid] = chunk_max;
+                chunk_max = __int_as_float(kNegInfF32);
+                in_chunk = 0;
+                ++chunk;
             }
         }
-        __syncthreads();
-        if (a.K > 0) {
-            scan_topk<DT>(rp, a.N, a.K, list, found, &count, warp_list);
-            if (tid < a.K) {
-                const uint64_t k = list[tid];
-                a.top_index[row * a.K + tid] = k ? key_column(k) : -1;
-                a.top_logprob[row * a.K + tid] = k ? key_value(k) - row_lse : __int_as_float(kNegInfF32);
+        if (in_chunk > 0) sh.chunk_max[chunk * T + tid] = chunk_max;
+    }
+    float group = acc.m;  // maximum of T / 32 neighbouring threads
+#pragma unroll
+    for (int off = NW / 2; off > 0; off >>= 1) group = fmaxf(group, __shfl_xor_sync(0xffffffffu, group, off));
+    if (tid % NW == 0) sh.group_max[tid / NW] = group;
+    const float thread_max = acc.m;
+    acc = stat_warp_merge(acc);
+    if (lane == 0) {
+        sh.part[0][wid] = acc.m;
+        sh.part[1][wid] = acc.s;
+        sh.part[2][wid] = acc.u;
+    }
+    if (tid == 0) sh.chunks = sh.founds = 0;
+    if (CLUSTER && tid < kMaxTopK) sh.own[tid] = 0;
+    __syncthreads();
+    // Every warp merges the partials (the same order everywhere).
+    acc = lane < NW ? StatAcc{sh.part[0][lane], sh.part[1][lane], sh.part[2][lane]} : stat_identity();
+    acc = stat_warp_merge(acc);
+    const float lse = acc_finalize(Acc{acc.m, acc.s});
+    if (!CLUSTER && tid == 0) StatsOut::row(a, row, acc, xt, lse);
+
+    if (a.K > 0) {
+        const int batches = static_cast<int>((k_end - k_begin + U * T - 1) / (U * T));
+        const int chunks = (batches + a.chunk_batches - 1) / a.chunk_batches;
+        const float bound = kth_largest(sh.group_max[lane], a.K, lane);
+        bool scan = acc.s != acc.s || bound == __int_as_float(kNegInfF32);  // NaN, or too few left
+        if (!scan) {
+            if (thread_max >= bound) {
+                for (int c = 0; c < chunks; ++c)
+                    if (sh.chunk_max[c * T + tid] >= bound) {
+                        const int at = atomicAdd(&sh.chunks, 1);
+                        if (at < kChunkList) sh.chunk[at] = c * T + tid;
+                    }
             }
             __syncthreads();
+            const int n = sh.chunks;
+            scan = n > kChunkList;
+            if (!scan) {
+                // A thread per vector: U * chunk_batches vectors of each chunk.
+                const int per_chunk = U * a.chunk_batches;
+                for (int i = tid; i < n * per_chunk; i += T) {
+                    const int c = sh.chunk[i / per_chunk];
+                    const int64_t k = k_begin + static_cast<int64_t>(c / T) * (per_chunk * T) + c % T +
+                                      static_cast<int64_t>(i % per_chunk) * T;
+                    if (k >= k_end) continue;
+                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(r.a0 + k * 16));
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int e = 0; e < EPV; ++e) {
+                        const float x = word_elem<DT>(w, e);
+                        const int64_t col = column_of<DT>(r, k, e);
+                        if (x >= bound && col >= 0 && col < a.N) {
+                            const int at = atomicAdd(&sh.founds, 1);
+                            if (at < kFoundList) sh.found[at] = topk_key(x, static_cast<uint32_t>(col));
+                        }
+                    }
+                }
+                __syncthreads();
+                scan = sh.founds > kFoundList;
+            }
+        }
+        const int n = scan ? T : sh.founds;
+        if (scan) {  // a part of the vectors per warp, in order
+            __syncthreads();
+            const int64_t share = (k_end - k_begin + NW - 1) / NW;
+            const int64_t k0 = k_begin + wid * share < k_end ? k_begin + wid * share : k_end;
+            const int64_t k1 = k0 + share < k_end ? k0 + share : k_end;
+            sh.found[tid] = scan_vectors<DT>(r, k0, k1, a.N, a.K, lane);
+            __syncthreads();
+        }
+        if (!CLUSTER) {
+            place_keys<T>(sh.found, n, a.K, [&](int place, uint64_t key) { StatsOut::top(a, row, place, key, acc, lse); });
+        } else {
+            // A part may hold fewer than K elements: its last places stay empty.
+            place_keys<T>(sh.found, n, a.K, [&](int place, uint64_t key) { sh.own[place] = key; });
+            __syncthreads();
+            cluster_wait();
+            if (tid < a.K) cluster_map(sh.keys, 0)[seg * a.K + tid] = sh.own[tid];
+        }
+    } else if (CLUSTER) {
+        cluster_wait();
+    }
+    if (CLUSTER) {
+        if (tid == 0) {
+            float* to = cluster_map(&sh.acc[0][0], 0) + seg;
+            to[0] = acc.m;
+            to[kMaxCluster] = acc.s;
+            to[2 * kMaxCluster] = acc.u;
+        }
+        cluster_arrive();
+        if (seg != 0) return;
+        cluster_wait();
+        acc = lane < P ? StatAcc{sh.acc[0][lane], sh.acc[1][lane], sh.acc[2][lane]} : stat_identity();
+        acc = stat_warp_merge(acc);
+        const float row_lse = acc_finalize(Acc{acc.m, acc.s});
+        if (tid == 0) StatsOut::row(a, row, acc, xt, row_lse);
+        if (a.K > 0) {
+            place_keys<T>(sh.keys, P * a.K, a.K, [&](int place, uint64_t key) { StatsOut::top(a, row, place, key, acc, row_lse); });
         }
     }
 }
+
+// ---------------------------------------------------------------------------
+// Short rows: a warp per row, which it holds in registers (V vectors per lane).
+// ---------------------------------------------------------------------------
+constexpr int kShortThreads = 256;
+constexpr int kShortWarps = kShortThreads / 32;
+constexpr int kShortFound = 96;   // elements that may reach the bound
+
+template <int DT, int V>
+__global__ void __launch_bounds__(kShortThreads, V <= 4 ? 5 : 4)
+lse_stats_short_kernel(const __grid_constant__ StatsArgs a) {
+    constexpr int EPV = 16 / DType<DT>::bytes;
+    __shared__ uint64_t found_all[kShortWarps][kShortFound];
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    uint64_t* found = found_all[wid];
+    pdl_trigger();
+    pdl_wait();
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * kShortWarps + wid; row < a.B;
+         row += static_cast<int64_t>(gridDim.x) * kShortWarps) {
+        const Row r = make_row<DT>(a.x, row, a.row_stride, a.N);
+        uint32_t w[4 * V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) load_vector<DT>(r, lane + 32 * j, r.vectors, &w[4 * j]);
+        float xt = __int_as_float(0x7fc00000);
+        if (a.logprob && lane == 0) {
+            const int64_t t = __ldg(a.target + row);
+            if (t >= 0 && t < a.N) xt = load_elem<DT>(r.a0 + r.off, t);
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int64_t k = lane + 32 * j;
+            if (k == 0 || k == r.vectors - 1) mask_vector<DT>(r, k, &w[4 * j]);
+        }
+        const float lane_max = words_max<DT, 4 * V>(w);
+        float m = lane_max;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        StatAcc acc{m, 0.0f, 0.0f};
+        stat_add_words<DT, 4 * V>(acc, shift_of(m), w);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            acc.s += __shfl_xor_sync(0xffffffffu, acc.s, off);
+            acc.u += __shfl_xor_sync(0xffffffffu, acc.u, off);
+        }
+        const float lse = acc_finalize(Acc{acc.m, acc.s});
+        if (lane == 0) StatsOut::row(a, row, acc, xt, lse);
+        if (a.K == 0) continue;
+
+        const float bound = kth_largest(lane_max, a.K, lane);
+        bool scan = acc.s != acc.s || bound == __int_as_float(kNegInfF32);
+        int n = 0;
+        if (!scan) {
+            // Lanes with elements at or above the bound take places in turn.
+            int mine = 0;
+#pragma unroll
+            for (int i = 0; i < V * EPV; ++i) mine += word_elem<DT>(&w[i / EPV * 4], i % EPV) >= bound;
+            int before = mine;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, before, off);
+                if (lane >= off) before += o;
+            }
+            n = __shfl_sync(0xffffffffu, before, 31);
+            scan = n > kShortFound;
+            if (!scan && mine > 0) {
+                int at = before - mine;
+#pragma unroll
+                for (int i = 0; i < V * EPV; ++i) {
+                    const float x = word_elem<DT>(&w[i / EPV * 4], i % EPV);
+                    if (x >= bound)
+                        found[at++] = topk_key(x, static_cast<uint32_t>(column_of<DT>(r, lane + 32 * (i / EPV), i % EPV)));
+                }
+            }
+            __syncwarp();
+        }
+        if (scan) {
+            const uint64_t key = scan_vectors<DT>(r, 0, r.vectors, a.N, a.K, lane);
+            if (lane < a.K) StatsOut::top(a, row, lane, key, acc, lse);
+        } else {
+            for (int i = lane; i < n; i += 32) {
+                const uint64_t key = found[i];
+                int rank = 0;
+                for (int j = 0; j < n; ++j) rank += found[j] > key;
+                if (rank < a.K) StatsOut::top(a, row, rank, key, acc, lse);
+            }
+        }
+        __syncwarp();
+    }
+}
+
+constexpr int kStatThreads = 256;
 
 template <int DT>
 __device__ __forceinline__ void put_elem(void* row, int64_t i, float v) {
@@ -250,6 +621,83 @@ lse_stats_backward_kernel(const StatsBackwardArgs a) {
     }
 }
 
+template <int DT, int T, bool CLUSTER>
+cudaError_t launch_stats_long(const StatsArgs& a, cudaStream_t stream) {
+    const auto kernel = lse_stats_kernel<DT, T, CLUSTER>;
+    const dim3 grid(static_cast<unsigned>(a.B * a.cluster));
+    if (!CLUSTER) return launch_pdl(kernel, grid, dim3(T), stream, a);
+    cudaLaunchAttribute attr[2] = {};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = a.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(T);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    cudaError_t e = cudaSuccess;
+    if (a.cluster > 8)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kernel, a);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+template <int DT>
+cudaError_t launch_stats_short(const StatsArgs& a, int V, int sms, cudaStream_t stream) {
+    const int64_t ctas = (a.B + kShortWarps - 1) / kShortWarps;
+    const int64_t most = static_cast<int64_t>(sms) * 64;
+    const dim3 grid(static_cast<unsigned>(ctas < most ? ctas : most)), block(kShortThreads);
+    switch (V) {
+    case 1: return launch_pdl(lse_stats_short_kernel<DT, 1>, grid, block, stream, a);
+    case 2: return launch_pdl(lse_stats_short_kernel<DT, 2>, grid, block, stream, a);
+    case 3: return launch_pdl(lse_stats_short_kernel<DT, 3>, grid, block, stream, a);
+    case 4: return launch_pdl(lse_stats_short_kernel<DT, 4>, grid, block, stream, a);
+    case 5:
+    case 6: return launch_pdl(lse_stats_short_kernel<DT, 6>, grid, block, stream, a);
+    default: return launch_pdl(lse_stats_short_kernel<DT, 8>, grid, block, stream, a);
+    }
+}
+
+// The mapping of a call: rows of up to 256 vectors take a warp each; longer ones a
+// CTA, or a cluster of CTAs while the rows alone would leave SMs without work.
+template <int DT>
+cudaError_t launch_stats(StatsArgs a, int sms, cudaStream_t stream) {
+    const int eb = DType<DT>::bytes;
+    const bool aligned = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (a.row_stride * eb) % 16 == 0;
+    const int64_t vectors = (a.N * eb + 15) / 16 + (aligned ? 0 : 1);  // at most
+    a.cluster = 1;
+    a.chunk_batches = 1;
+    if (vectors <= 32 * 8) return launch_stats_short<DT>(a, static_cast<int>((vectors + 31) / 32), sms, stream);
+    // Threads of a CTA: enough for one batch of the row each; at most 128 when rows
+    // are plentiful, so that rows at their ends overlap with rows under way.
+    int T = 512;
+    while (T > 128 && vectors < 2LL * kStatU * T) T /= 2;
+    if (a.B >= 4LL * sms) T = 128;
+    int P = 1;
+    if (a.B < sms) {
+        while (P < kMaxCluster && a.B * P * 2 <= 2LL * sms && vectors >= 2LL * P * kStatU * 128) P *= 2;
+        while (T > 128 && vectors < 1LL * P * kStatU * T) T /= 2;
+    }
+    a.cluster = P;
+    const int64_t batches = ((vectors + P - 1) / P + kStatU * T - 1) / (kStatU * T);
+    a.chunk_batches = static_cast<int>((batches + kStatChunks - 1) / kStatChunks);
+    if (P > 1) {
+        switch (T) {
+        case 128: return launch_stats_long<DT, 128, true>(a, stream);
+        case 256: return launch_stats_long<DT, 256, true>(a, stream);
+        default: return launch_stats_long<DT, 512, true>(a, stream);
+        }
+    }
+    switch (T) {
+    case 128: return launch_stats_long<DT, 128, false>(a, stream);
+    case 256: return launch_stats_long<DT, 256, false>(a, stream);
+    default: return launch_stats_long<DT, 512, false>(a, stream);
+    }
+}
+
 unsigned row_grid(int64_t B) { return static_cast<unsigned>(B < INT_MAX ? B : INT_MAX); }
 
 // The checks that the forward and the backward share beyond check_args.
@@ -290,10 +738,12 @@ lse_status lse_token_stats(const void* x, lse_dtype dtype, int64_t B, int64_t N,
     a.lse = lse_out;
     a.top_logprob = top_logprob;
     a.top_index = top_index;
-    const auto kernel = dtype == LSE_F32 ? lse_stats_kernel<kF32>
-                        : dtype == LSE_BF16 ? lse_stats_kernel<kBF16> : lse_stats_kernel<kF16>;
-    return cuda_status(launch_pdl(kernel, dim3(row_grid(B)), dim3(kStatThreads),
-                                  reinterpret_cast<cudaStream_t>(stream), a));
+    int sms = 0;
+    if ((st = device_sms(&sms)) != LSE_OK) return st;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (N > 1024 && B > INT_MAX) return LSE_ERR_INVALID_ARG;  // a CTA per row
+    return cuda_status(dtype == LSE_F32 ? launch_stats<kF32>(a, sms, s)
+                       : dtype == LSE_BF16 ? launch_stats<kBF16>(a, sms, s) : launch_stats<kF16>(a, sms, s));
 }
 
 lse_status lse_token_stats_backward(const void* x, lse_dtype dtype, int64_t B, int64_t N,
