@@ -16,6 +16,7 @@
 // below by kFarBelow, 0 to u.
 #include <climits>
 #include <cstdint>
+#include <cstdlib>
 
 #include <cuda_runtime.h>
 
@@ -208,17 +209,19 @@ __device__ __forceinline__ int64_t column_of(const Row& r, int64_t k, int i) {
 // everything masked with -inf) or a NaN are scanned once more in full.
 // ---------------------------------------------------------------------------
 
-// K-th largest of the warp's 32 values.
+// K-th largest of the G values of a group of G lanes (bitonic sort), K <= G.
+template <int G = 32>
 __device__ __forceinline__ float kth_largest(float v, int K, int lane) {
 #pragma unroll
-    for (int size = 2; size <= 32; size <<= 1) {
+    for (int size = 2; size <= G; size <<= 1) {
 #pragma unroll
         for (int stride = size >> 1; stride > 0; stride >>= 1) {
             const float o = __shfl_xor_sync(0xffffffffu, v, stride);
-            v = ((lane & stride) == 0) == ((lane & size) == 0) ? fmaxf(v, o) : fminf(v, o);
+            const bool high = ((lane & stride) == 0) == (size == G || (lane & size) == 0);
+            v = high ? fmaxf(v, o) : fminf(v, o);
         }
     }
-    return __shfl_sync(0xffffffffu, v, K - 1);
+    return __shfl_sync(0xffffffffu, v, K - 1, G);
 }
 
 // A warp's list of the K largest keys of vectors [k0, k1), read in order.  Past
@@ -286,8 +289,8 @@ __device__ __forceinline__ V* cluster_map(V* p, uint32_t cta) {
 constexpr int kStatU = 8;         // vectors per thread and batch
 constexpr int kStatChunks = 16;   // chunk maxima kept per thread
 constexpr int kChunkList = 256;   // chunks that may be read again
-constexpr int kFoundList = 512;   // elements that may reach the bound (32 per warp at least)
 constexpr int kMaxCluster = 16;
+constexpr int kFoundList = kMaxCluster * kMaxTopK;  // elements that may reach the bound; lists of a cluster
 
 template <int T, bool CLUSTER>
 struct StatsShared {
@@ -471,95 +474,156 @@ lse_stats_kernel(const __grid_constant__ StatsArgs a) {
         const float row_lse = acc_finalize(Acc{acc.m, acc.s});
         if (tid == 0) StatsOut::row(a, row, acc, xt, row_lse);
         if (a.K > 0) {
-            place_keys<T>(sh.keys, P * a.K, a.K, [&](int place, uint64_t key) { StatsOut::top(a, row, place, key, acc, row_lse); });
+            // The first 32 / P keys of the parts' lists are 32 keys: the K-th largest of
+            // their values is a bound again, and warp 0 ranks what reaches it.
+            if (wid == 0) {
+                const int each = 32 / P, n = P * a.K;
+                const uint64_t head = lane % each < a.K ? sh.keys[lane / each * a.K + lane % each] : 0;
+                const float bound = kth_largest(head ? key_value(head) : __int_as_float(kNegInfF32), a.K, lane);
+                int founds = 0;
+                for (int i = 0; i < n; i += 32) {
+                    const uint64_t key = i + lane < n ? sh.keys[i + lane] : 0;
+                    // (a NaN reaches every bound)
+                    const bool in = key != 0 && !(key_value(key) < bound);
+                    const uint32_t who = __ballot_sync(0xffffffffu, in);
+                    if (in) sh.found[founds + __popc(who & ((1u << lane) - 1))] = key;
+                    founds += __popc(who);
+                }
+                __syncwarp();
+                for (int i = lane; i < founds; i += 32) {
+                    const uint64_t key = sh.found[i];
+                    int rank = 0;
+                    for (int j = 0; j < founds; ++j) rank += sh.found[j] > key;
+                    if (rank < a.K) StatsOut::top(a, row, rank, key, acc, row_lse);
+                }
+            }
         }
     }
 }
 
 // ---------------------------------------------------------------------------
-// Short rows: a warp per row, which it holds in registers (V vectors per lane).
+// Short rows: G lanes per row, which hold it in registers (V vectors per lane).
 // ---------------------------------------------------------------------------
 constexpr int kShortThreads = 256;
 constexpr int kShortWarps = kShortThreads / 32;
-constexpr int kShortFound = 96;   // elements that may reach the bound
+constexpr int kShortFound = 192;  // elements of a warp's rows that may reach their bounds
 
-template <int DT, int V>
-__global__ void __launch_bounds__(kShortThreads, V <= 4 ? 5 : 4)
+template <int DT, int G, int V>
+__global__ void __launch_bounds__(kShortThreads, V <= 4 ? 5 : V <= 6 ? 4 : 3)
 lse_stats_short_kernel(const __grid_constant__ StatsArgs a) {
-    constexpr int EPV = 16 / DType<DT>::bytes;
+    constexpr int EB = DType<DT>::bytes, EPV = 16 / EB, RPW = 32 / G;
+    constexpr int kCap = kShortFound / RPW;  // per row
     __shared__ uint64_t found_all[kShortWarps][kShortFound];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    uint64_t* found = found_all[wid];
+    const int sub = lane & (G - 1), group = lane / G;
+    uint64_t* found = found_all[wid] + group * kCap;
     pdl_trigger();
     pdl_wait();
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * kShortWarps + wid; row < a.B;
-         row += static_cast<int64_t>(gridDim.x) * kShortWarps) {
-        const Row r = make_row<DT>(a.x, row, a.row_stride, a.N);
+    for (int64_t row0 = (static_cast<int64_t>(blockIdx.x) * kShortWarps + wid) * RPW; row0 < a.B;
+         row0 += static_cast<int64_t>(gridDim.x) * kShortWarps * RPW) {
+        const int64_t row = row0 + group;
+        const bool live = RPW == 1 || row < a.B;
+        // Short rows: everything inside one fits 32 bits.
+        const char* rp = static_cast<const char*>(a.x) + row * a.row_stride * EB;
+        const int off = static_cast<int>(reinterpret_cast<uintptr_t>(rp) & 15u);
+        const char* a0 = rp - off;
+        const int end = off + static_cast<int>(a.N) * EB;
+        const int vectors = live && a.N > 0 ? (end + 15) >> 4 : 0;
         uint32_t w[4 * V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) load_vector<DT>(r, lane + 32 * j, r.vectors, &w[4 * j]);
-        float xt = __int_as_float(0x7fc00000);
-        if (a.logprob && lane == 0) {
-            const int64_t t = __ldg(a.target + row);
-            if (t >= 0 && t < a.N) xt = load_elem<DT>(r.a0 + r.off, t);
-        }
-#pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int64_t k = lane + 32 * j;
-            if (k == 0 || k == r.vectors - 1) mask_vector<DT>(r, k, &w[4 * j]);
+            if (sub + G * j < vectors) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(a0 + (sub + G * j) * 16));
+                w[4 * j] = v.x; w[4 * j + 1] = v.y; w[4 * j + 2] = v.z; w[4 * j + 3] = v.w;
+            } else {
+                w[4 * j] = w[4 * j + 1] = w[4 * j + 2] = w[4 * j + 3] = neg_inf_word<DT>();
+            }
+        }
+        float xt = __int_as_float(0x7fc00000);
+        if (a.logprob && sub == 0 && live) {
+            const int64_t t = __ldg(a.target + row);
+            if (t >= 0 && t < a.N) xt = load_elem<DT>(rp, t);
+        }
+        if (off != 0 && sub == 0) {
+            uint32_t q[4] = {w[0], w[1], w[2], w[3]};
+            mask_prefix<DT>(q, off);
+            w[0] = q[0]; w[1] = q[1]; w[2] = q[2]; w[3] = q[3];
+        }
+        if ((end & 15) != 0) {
+            const int last = vectors - 1;
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (sub + G * j == last) {
+                    uint32_t q[4] = {w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]};
+                    mask_suffix<DT>(q, end - last * 16);
+                    w[4 * j] = q[0]; w[4 * j + 1] = q[1]; w[4 * j + 2] = q[2]; w[4 * j + 3] = q[3];
+                }
         }
         const float lane_max = words_max<DT, 4 * V>(w);
         float m = lane_max;
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        for (int off2 = G / 2; off2 > 0; off2 >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off2));
         StatAcc acc{m, 0.0f, 0.0f};
         stat_add_words<DT, 4 * V>(acc, shift_of(m), w);
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) {
-            acc.s += __shfl_xor_sync(0xffffffffu, acc.s, off);
-            acc.u += __shfl_xor_sync(0xffffffffu, acc.u, off);
+        for (int off2 = G / 2; off2 > 0; off2 >>= 1) {
+            acc.s += __shfl_xor_sync(0xffffffffu, acc.s, off2);
+            acc.u += __shfl_xor_sync(0xffffffffu, acc.u, off2);
         }
         const float lse = acc_finalize(Acc{acc.m, acc.s});
-        if (lane == 0) StatsOut::row(a, row, acc, xt, lse);
+        if (sub == 0 && live) StatsOut::row(a, row, acc, xt, lse);
         if (a.K == 0) continue;
 
-        const float bound = kth_largest(lane_max, a.K, lane);
+        const float bound = kth_largest<G>(lane_max, a.K, lane);
         bool scan = acc.s != acc.s || bound == __int_as_float(kNegInfF32);
+        // Which of the lane's elements reach the bound, one bit each; then one of them
+        // per lane and round goes to the row's list, in turn within the round.
+        uint64_t mine = 0;
+#pragma unroll
+        for (int i = 0; i < V * EPV; ++i)
+            mine |= static_cast<uint64_t>(word_elem<DT>(&w[i / EPV * 4], i % EPV) >= bound) << i;
+        if (scan || !live) mine = 0;
         int n = 0;
-        if (!scan) {
-            // Lanes with elements at or above the bound take places in turn.
-            int mine = 0;
-#pragma unroll
-            for (int i = 0; i < V * EPV; ++i) mine += word_elem<DT>(&w[i / EPV * 4], i % EPV) >= bound;
-            int before = mine;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int o = __shfl_up_sync(0xffffffffu, before, off);
-                if (lane >= off) before += o;
+        const int column0 = (sub * 16 - off) / EB;
+        const uint32_t group_bits = G == 32 ? 0xffffffffu : ((1u << (G & 31)) - 1) << (group * G);
+        const uint32_t before = group_bits & ((1u << lane) - 1);
+        for (uint32_t who; (who = __ballot_sync(0xffffffffu, mine != 0)) != 0;) {
+            if (mine != 0) {
+                const int i = __ffsll(static_cast<long long>(mine)) - 1;
+                mine &= mine - 1;
+                const int at = n + __popc(who & before);
+                if (at < kCap) found[at] = static_cast<uint64_t>(column0 + (i / EPV) * (G * EPV) + i % EPV);
             }
-            n = __shfl_sync(0xffffffffu, before, 31);
-            scan = n > kShortFound;
-            if (!scan && mine > 0) {
-                int at = before - mine;
-#pragma unroll
-                for (int i = 0; i < V * EPV; ++i) {
-                    const float x = word_elem<DT>(&w[i / EPV * 4], i % EPV);
-                    if (x >= bound)
-                        found[at++] = topk_key(x, static_cast<uint32_t>(column_of<DT>(r, lane + 32 * (i / EPV), i % EPV)));
-                }
-            }
-            __syncwarp();
+            n += __popc(who & group_bits);
         }
-        if (scan) {
-            const uint64_t key = scan_vectors<DT>(r, 0, r.vectors, a.N, a.K, lane);
-            if (lane < a.K) StatsOut::top(a, row, lane, key, acc, lse);
-        } else {
-            for (int i = lane; i < n; i += 32) {
+        scan |= n > kCap;
+        __syncwarp();
+        if (!scan) {  // the values again, from L1
+            for (int i = sub; i < n; i += G) {
+                const int col = static_cast<int>(found[i]);
+                found[i] = topk_key(load_elem<DT>(rp, col), static_cast<uint32_t>(col));
+            }
+        }
+        __syncwarp();
+        if (!scan) {
+            for (int i = sub; i < n; i += G) {
                 const uint64_t key = found[i];
                 int rank = 0;
                 for (int j = 0; j < n; ++j) rank += found[j] > key;
                 if (rank < a.K) StatsOut::top(a, row, rank, key, acc, lse);
             }
+        }
+        // Rows that need the scan, by the whole warp in turn.
+        uint32_t todo = __ballot_sync(0xffffffffu, scan && live && sub == 0);
+        while (todo != 0) {
+            const int q = __ffs(todo) - 1;
+            todo &= todo - 1;
+            const Row r = make_row<DT>(a.x, row0 + q / G, a.row_stride, a.N);
+            const uint64_t key = scan_vectors<DT>(r, 0, r.vectors, a.N, a.K, lane);
+            const StatAcc of{__shfl_sync(0xffffffffu, acc.m, q), __shfl_sync(0xffffffffu, acc.s, q),
+                             __shfl_sync(0xffffffffu, acc.u, q)};
+            const float of_lse = __shfl_sync(0xffffffffu, lse, q);
+            if (lane < a.K) StatsOut::top(a, row0 + q / G, lane, key, of, of_lse);
         }
         __syncwarp();
     }
@@ -645,19 +709,21 @@ cudaError_t launch_stats_long(const StatsArgs& a, cudaStream_t stream) {
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-template <int DT>
+template <int DT, int G>
 cudaError_t launch_stats_short(const StatsArgs& a, int V, int sms, cudaStream_t stream) {
-    const int64_t ctas = (a.B + kShortWarps - 1) / kShortWarps;
+    const int64_t rows = kShortWarps * (32 / G);
+    const int64_t ctas = (a.B + rows - 1) / rows;
     const int64_t most = static_cast<int64_t>(sms) * 64;
     const dim3 grid(static_cast<unsigned>(ctas < most ? ctas : most)), block(kShortThreads);
     switch (V) {
-    case 1: return launch_pdl(lse_stats_short_kernel<DT, 1>, grid, block, stream, a);
-    case 2: return launch_pdl(lse_stats_short_kernel<DT, 2>, grid, block, stream, a);
-    case 3: return launch_pdl(lse_stats_short_kernel<DT, 3>, grid, block, stream, a);
-    case 4: return launch_pdl(lse_stats_short_kernel<DT, 4>, grid, block, stream, a);
-    case 5:
-    case 6: return launch_pdl(lse_stats_short_kernel<DT, 6>, grid, block, stream, a);
-    default: return launch_pdl(lse_stats_short_kernel<DT, 8>, grid, block, stream, a);
+    case 0:
+    case 1: return launch_pdl(lse_stats_short_kernel<DT, G, 1>, grid, block, stream, a);
+    case 2: return launch_pdl(lse_stats_short_kernel<DT, G, 2>, grid, block, stream, a);
+    case 3: return launch_pdl(lse_stats_short_kernel<DT, G, 3>, grid, block, stream, a);
+    case 4: return launch_pdl(lse_stats_short_kernel<DT, G, 4>, grid, block, stream, a);
+    case 5: return launch_pdl(lse_stats_short_kernel<DT, G, 5>, grid, block, stream, a);
+    case 6: return launch_pdl(lse_stats_short_kernel<DT, G, 6>, grid, block, stream, a);
+    default: return launch_pdl(lse_stats_short_kernel<DT, G, 8>, grid, block, stream, a);
     }
 }
 
@@ -670,7 +736,16 @@ cudaError_t launch_stats(StatsArgs a, int sms, cudaStream_t stream) {
     const int64_t vectors = (a.N * eb + 15) / 16 + (aligned ? 0 : 1);  // at most
     a.cluster = 1;
     a.chunk_batches = 1;
-    if (vectors <= 32 * 8) return launch_stats_short<DT>(a, static_cast<int>((vectors + 31) / 32), sms, stream);
+    if (vectors <= 32 * 8) {
+        int G = 32;
+        if (vectors <= 16 * 8 && a.K <= 8) G = 16;
+        if (vectors <= 8 * 8 && a.K <= 4) G = 8;
+        if (const char* e = getenv("LSE_G")) G = atoi(e);
+        const int V = static_cast<int>((vectors + G - 1) / G);
+        return G == 8 ? launch_stats_short<DT, 8>(a, V, sms, stream)
+               : G == 16 ? launch_stats_short<DT, 16>(a, V, sms, stream)
+                         : launch_stats_short<DT, 32>(a, V, sms, stream);
+    }
     // Threads of a CTA: enough for one batch of the row each; at most 128 when rows
     // are plentiful, so that rows at their ends overlap with rows under way.
     int T = 512;
@@ -681,6 +756,8 @@ cudaError_t launch_stats(StatsArgs a, int sms, cudaStream_t stream) {
         while (P < kMaxCluster && a.B * P * 2 <= 2LL * sms && vectors >= 2LL * P * kStatU * 128) P *= 2;
         while (T > 128 && vectors < 1LL * P * kStatU * T) T /= 2;
     }
+    if (const char* e = getenv("LSE_T")) T = atoi(e);
+    if (const char* e = getenv("LSE_P")) P = atoi(e);
     a.cluster = P;
     const int64_t batches = ((vectors + P - 1) / P + kStatU * T - 1) / (kStatU * T);
     a.chunk_batches = static_cast<int>((batches + kStatChunks - 1) / kStatChunks);
