@@ -70,27 +70,42 @@ def lse_token_stats(x, target=None, top_k=0, entropy=True, stream=None) -> Token
     torch = _torch()
     if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor")
-    dt = _dtype_name(x)
+    dt = DTYPES[_dtype_name(x)]
     B, N, row_stride = _rows(x)
     if not 0 <= top_k <= MAX_TOP_K:
         raise ValueError(f"top_k must lie in 0 .. {MAX_TOP_K}")
+    device = x.device
     if target is not None:
-        _need_vector(target, "target", torch.int64, B, x.device)
-    lead = () if x.dim() == 1 else (B,)
-    with _on_device(x.device):
-        with _allocating(stream):
-            rows = torch.empty((3, B), dtype=torch.float32, device=x.device)
-            top_lp = torch.empty((B, top_k), dtype=torch.float32, device=x.device) if top_k else None
-            top_i = torch.empty((B, top_k), dtype=torch.int64, device=x.device) if top_k else None
-        logprob = rows[0] if target is not None else None
-        ent = rows[1] if entropy else None
-        _check(load().lse_token_stats(_ptr(x), DTYPES[dt], B, N, row_stride, _ptr(target), top_k,
-                                      _ptr(logprob), _ptr(ent), _ptr(rows[2]), _ptr(top_lp),
-                                      _ptr(top_i), _stream_handle(stream, x.device) or None),
-               "lse_token_stats")
-    shaped = [None if t is None else t.reshape(lead) for t in (logprob, ent, rows[2])]
-    tops = [None if t is None else t.reshape(lead + (top_k,)) for t in (top_lp, top_i)]
-    return TokenStats(*shaped, *tops)
+        _need_vector(target, "target", torch.int64, B, device)
+    if stream is not None or torch.cuda.current_device() != device.index:
+        with _on_device(device), _allocating(stream):
+            out = _stats_call(torch, x, dt, B, N, row_stride, target, top_k, entropy, stream, device)
+    else:
+        out = _stats_call(torch, x, dt, B, N, row_stride, target, top_k, entropy, None, device)
+    if x.dim() == 1:
+        out = [None if t is None else t[0] for t in out]
+    return TokenStats(*out)
+
+
+def _stats_call(torch, x, dt, B, N, row_stride, target, top_k, entropy, stream, device):
+    # One allocation per output: views of a shared one cost more host time.
+    empty, f32 = torch.empty, torch.float32
+    lse = empty(B, dtype=f32, device=device)
+    logprob = ent = top_lp = top_i = p_t = p_logprob = p_ent = p_lp = p_i = None
+    if target is not None:
+        logprob = empty(B, dtype=f32, device=device)
+        p_t, p_logprob = target.data_ptr(), logprob.data_ptr()
+    if entropy:
+        ent = empty(B, dtype=f32, device=device)
+        p_ent = ent.data_ptr()
+    if top_k:
+        top_lp = empty((B, top_k), dtype=f32, device=device)
+        top_i = empty((B, top_k), dtype=torch.int64, device=device)
+        p_lp, p_i = top_lp.data_ptr(), top_i.data_ptr()
+    _check(load().lse_token_stats(x.data_ptr(), dt, B, N, row_stride, p_t, top_k, p_logprob, p_ent,
+                                  lse.data_ptr(), p_lp, p_i, _stream_handle(stream, device)),
+           "lse_token_stats")
+    return logprob, ent, lse, top_lp, top_i
 
 
 def lse_token_stats_backward(x, stats: TokenStats, target=None, grad_logprob=None,

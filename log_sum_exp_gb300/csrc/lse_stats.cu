@@ -12,8 +12,7 @@
 //
 // a sum of two non-negative terms, so nothing cancels.  (m, s, u) is kept online:
 // raising the maximum by d (in units of z) turns u into (u + d s) 2^-d and s into
-// s 2^-d.  A masked element (z = -inf) adds 2^z = 0 to s and, with z bounded
-// below by kFarBelow, 0 to u.
+// s 2^-d.
 #include <climits>
 #include <cstdint>
 #include <cstdlib>
@@ -39,7 +38,7 @@ struct StatsArgs {
     float* top_logprob;  // [B, K]
     int64_t* top_index;
     int cluster;         // CTAs that share a row
-    int chunk_batches;   // batches of a chunk of the long-row kernel
+    int chunk_shift;     // log2 of the batches of a chunk (long rows)
 };
 
 struct StatsBackwardArgs {
@@ -58,8 +57,38 @@ struct StatsBackwardArgs {
     int64_t dx_row_stride;
 };
 
+// Two floats -> packed 16-bit pair, nearest-even.
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t r;
+    if constexpr (DT == kBF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // Below this many octaves of the maximum an exponential is 0 in f32.
 constexpr float kFarBelow = -16384.0f;
+
+// The exponentials' argument is z = x log2 e - c, c = fl(mu log2 e), by one FMA, so
+// every term carries the factor 2^r, r = mu log2 e - c, which the logarithm takes
+// out again; the entropy does not change with it.  Beyond |mu| = 2^24 (r would
+// exceed an octave), and for f16 where mu is next to the lowest value, z is
+// (x - mu) log2 e in two steps and r is 0.
+struct Shift {
+    float mu, c;
+    bool two_step;
+};
+
+template <int DT>
+__device__ __forceinline__ Shift make_shift(float m) {
+    const float mu = shift_of(m);
+    return Shift{mu, mu * kLog2e, fabsf(mu) > 0x1.0p24f || (DT == kF16 && mu < -60000.0f)};
+}
+template <int DT>
+__device__ __forceinline__ float shift_residue(float m) {
+    const Shift h = make_shift<DT>(m);
+    return h.two_step ? 0.0f : fmaf(h.mu, kLog2e, -h.c);
+}
 
 struct StatAcc {
     float m, s, u;
@@ -67,78 +96,100 @@ struct StatAcc {
 
 __device__ __forceinline__ StatAcc stat_identity() { return StatAcc{__int_as_float(kNegInfF32), 0.0f, 0.0f}; }
 
-// The accumulator against another shift mu >= its own: its sums scaled by 2^-d.
-__device__ __forceinline__ StatAcc stat_shift(StatAcc a, float mu) {
-    const float d = fminf((mu - a.m) * kLog2e, -kFarBelow);
+// The sums against the shift of another maximum m >= the accumulator's own, which is
+// d octaves higher: s 2^-d and (u + d s) 2^-d.
+template <int DT>
+__device__ __forceinline__ StatAcc stat_shift(StatAcc a, float m) {
+    float d = (shift_of(m) - a.m) * kLog2e + (shift_residue<DT>(a.m) - shift_residue<DT>(m));
+    d = fminf(d, -kFarBelow);  // (from no maximum at all: +inf)
     const float f = ex2(-d);
-    return StatAcc{a.m, a.s * f, fmaf(d, a.s, a.u) * f};
+    return StatAcc{m, a.s * f, fmaf(d, a.s, a.u) * f};
 }
 
-__device__ __forceinline__ StatAcc stat_merge(StatAcc a, StatAcc b) {
-    const float m = fmaxf(a.m, b.m);
-    const float mu = shift_of(m);
-    a = stat_shift(a, mu);
-    b = stat_shift(b, mu);
-    return StatAcc{m, a.s + b.s, a.u + b.u};
-}
-
-__device__ __forceinline__ StatAcc stat_warp_merge(StatAcc a) {
+// One accumulator of those of `WIDTH` neighbouring lanes, the same in all of them.
+template <int DT, int WIDTH>
+__device__ __forceinline__ StatAcc stat_lanes_merge(StatAcc a) {
+    float m = a.m;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        StatAcc b;
-        b.m = __shfl_xor_sync(0xffffffffu, a.m, off);
-        b.s = __shfl_xor_sync(0xffffffffu, a.s, off);
-        b.u = __shfl_xor_sync(0xffffffffu, a.u, off);
-        a = stat_merge(a, b);
+    for (int off = 1; off < WIDTH; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    a = stat_shift<DT>(a, m);
+#pragma unroll
+    for (int off = 1; off < WIDTH; off <<= 1) {
+        a.s += __shfl_xor_sync(0xffffffffu, a.s, off);
+        a.u += __shfl_xor_sync(0xffffffffu, a.u, off);
     }
-    // The two sides of a merge may round differently: lane 0's result for all.
-    a.m = __shfl_sync(0xffffffffu, a.m, 0);
-    a.s = __shfl_sync(0xffffffffu, a.s, 0);
-    a.u = __shfl_sync(0xffffffffu, a.u, 0);
     return a;
 }
 
-// NaN for a row that is no distribution: a NaN or +inf in it, or nothing but -inf.
-__device__ __forceinline__ float stat_entropy(StatAcc a) {
-    if (!(fabsf(a.m) < __int_as_float(0x7f800000))) return __int_as_float(0x7fc00000);
-    return kLn2 * (lg2(a.s) + a.u / a.s);
+// What the outputs of a row are made from.
+struct RowStats {
+    float m;     // maximum
+    float lse;
+    float logs;  // log sum exp(x - m); NaN where the row is no distribution
+};
+
+template <int DT>
+__device__ __forceinline__ RowStats row_stats(StatAcc a) {
+    RowStats r{a.m, a.s, __int_as_float(0x7fc00000)};
+    if (a.s != a.s) return r;  // NaN in the row
+    r.lse = a.m;               // +inf in it, or nothing but -inf
+    if (!(fabsf(a.m) < __int_as_float(0x7f800000))) return r;
+    r.logs = kLn2 * (lg2(a.s) - shift_residue<DT>(a.m));
+    r.lse = a.m + r.logs;
+    return r;
 }
 
+// NaN for a row that is no distribution.
+__device__ __forceinline__ float stat_entropy(StatAcc a, const RowStats& r) {
+    return r.logs != r.logs ? r.logs : kLn2 * (lg2(a.s) + a.u / a.s);
+}
 
 // x - lse as (x - max) - log sum exp(x - max): next to a large maximum lse itself
 // has few digits left for the logarithm.
-__device__ __forceinline__ float stat_logprob(float x, StatAcc a, float lse) {
-    if (a.s != a.s || !(fabsf(a.m) < __int_as_float(0x7f800000))) return x - lse;
-    return (x - a.m) - kLn2 * lg2(a.s);
+__device__ __forceinline__ float stat_logprob(float x, const RowStats& r) {
+    return r.logs != r.logs ? x - r.lse : (x - r.m) - r.logs;
 }
 
-// Raise the running maximum to cm, rescaling both sums once.
-__device__ __forceinline__ void stat_raise(StatAcc& a, float& mu, float cm) {
-    if (cm > a.m) {
-        mu = shift_of(cm);
-        a = stat_shift(a, mu);
-        a.m = cm;
-    }
+// The larger of each packed 16-bit pair; a NaN stays.
+template <int DT>
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+    uint32_t d;
+    if constexpr (DT == kBF16) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
 
 // Add sum 2^z and sum 2^z (-z) over W raw words, two elements at a time (packed
-// FP32) into two pairs of accumulators each.  The clamp keeps 0 * inf out of u; a
-// NaN element stays in s, which decides.
-template <int DT, int W>
-__device__ __forceinline__ void stat_add_words(StatAcc& a, float mu, const uint32_t (&w)[W]) {
-    const uint64_t mu2 = f2_pack(mu, mu), log2e2 = f2_pack(kLog2e, kLog2e);
+// FP32).  A masked element (z = -inf) must add 0 to u and not 0 * inf: f32 words
+// bound z from below, 16-bit ones the packed pair itself, 100 or more below mu, at
+// half the instructions.  A NaN stays in s, which decides.
+template <int DT, int W, bool TWO_STEP>
+__device__ __forceinline__ void stat_sum_words(StatAcc& a, const Shift& h, const uint32_t (&w)[W]) {
+    const uint64_t log2e2 = f2_pack(kLog2e, kLog2e);
+    const uint64_t sub2 = TWO_STEP ? f2_pack(h.mu, h.mu) : f2_pack(-h.c, -h.c);
+    uint32_t floor2 = 0;
+    if constexpr (!TWO_STEP && DT != kF32) {
+        const float low = h.mu - fmaf(fabsf(h.mu), 0x1.0p-6f, 200.0f);
+        floor2 = pack2<DT>(low, low);
+    }
     uint64_t s[2] = {0ull, 0ull}, u[2] = {0ull, 0ull};
 #pragma unroll
     for (int i = 0; i < W; i += DT == kF32 ? 2 : 1) {
         uint64_t x;
-        if constexpr (DT == kF32) x = f2_pack(__uint_as_float(w[i]), __uint_as_float(w[i + 1]));
-        else x = f2_pack(word_lo<DT>(w[i]), word_hi<DT>(w[i]));
+        if constexpr (DT == kF32) {
+            x = f2_pack(__uint_as_float(w[i]), __uint_as_float(w[i + 1]));
+        } else {
+            const uint32_t v = TWO_STEP ? w[i] : max2_nan<DT>(w[i], floor2);
+            x = f2_pack(word_lo<DT>(v), word_hi<DT>(v));
+        }
         const int k = DT == kF32 ? (i >> 1) & 1 : i & 1;
+        const uint64_t z = TWO_STEP ? f2_mul(f2_sub(x, sub2), log2e2) : f2_fma(x, log2e2, sub2);
         float z0, z1;
-        f2_unpack(f2_mul(f2_sub(x, mu2), log2e2), z0, z1);
+        f2_unpack(z, z0, z1);
         const uint64_t e = f2_pack(ex2(z0), ex2(z1));
         s[k] = f2_add(s[k], e);
-        u[k] = f2_fma(e, f2_pack(fmaxf(z0, kFarBelow), fmaxf(z1, kFarBelow)), u[k]);
+        if constexpr (TWO_STEP || DT == kF32) u[k] = f2_fma(e, f2_pack(fmaxf(z0, kFarBelow), fmaxf(z1, kFarBelow)), u[k]);
+        else u[k] = f2_fma(e, z, u[k]);
     }
     float s0, s1, s2, s3, u0, u1, u2, u3;
     f2_unpack(s[0], s0, s1);
@@ -147,6 +198,12 @@ __device__ __forceinline__ void stat_add_words(StatAcc& a, float mu, const uint3
     f2_unpack(u[1], u2, u3);
     a.s += (s0 + s1) + (s2 + s3);
     a.u -= (u0 + u1) + (u2 + u3);
+}
+
+template <int DT, int W>
+__device__ __forceinline__ void stat_add_words(StatAcc& a, const Shift& h, const uint32_t (&w)[W]) {
+    if (h.two_step) stat_sum_words<DT, W, true>(a, h, w);
+    else stat_sum_words<DT, W, false>(a, h, w);
 }
 
 // ---------------------------------------------------------------------------
@@ -224,6 +281,31 @@ __device__ __forceinline__ float kth_largest(float v, int K, int lane) {
     return __shfl_sync(0xffffffffu, v, K - 1, G);
 }
 
+// The same for 32 values in shared memory (16-byte aligned): the smallest of those
+// that fewer than K exceed.
+__device__ __forceinline__ float kth_largest_of(const float* v32, int K, int lane) {
+    const float v = v32[lane];
+    int above = 0;
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+        const float4 o = *reinterpret_cast<const float4*>(v32 + j);
+        above += (o.x > v) + (o.y > v) + (o.z > v) + (o.w > v);
+    }
+    return order_value(__reduce_min_sync(0xffffffffu, above < K ? order_bits(v) : 0xffffffffu));
+}
+
+// Element e of W / 4 vectors held in registers, e not known at compile time.
+template <int DT, int W>
+__device__ __forceinline__ float pick_elem(const uint32_t (&w)[W], int e) {
+    constexpr int EPW = 4 / DType<DT>::bytes;
+    const int q = e / EPW;
+    uint32_t v = w[0];
+#pragma unroll
+    for (int i = 1; i < W; ++i) v = q == i ? w[i] : v;
+    if constexpr (DT == kF32) return __uint_as_float(v);
+    else return (e & 1) ? word_hi<DT>(v) : word_lo<DT>(v);
+}
+
 // A warp's list of the K largest keys of vectors [k0, k1), read in order.  Past
 // the first few vectors nearly every one is dismissed by its values alone: none
 // above the K-th so far (an equal one later in the row ranks lower).
@@ -260,18 +342,31 @@ __device__ __forceinline__ uint64_t scan_vectors(const Row& r, int64_t k0, int64
 }
 
 // Writes of one row's results.
-struct StatsOut {
-    __device__ static void row(const StatsArgs& a, int64_t row, StatAcc acc, float xt, float lse) {
-        if (a.lse) a.lse[row] = lse;
-        if (a.entropy) a.entropy[row] = stat_entropy(acc);
-        if (a.logprob) a.logprob[row] = stat_logprob(xt, acc, lse);
+__device__ __forceinline__ void put_row(const StatsArgs& a, int64_t row, const StatAcc& acc, const RowStats& r, float xt) {
+    if (a.lse) a.lse[row] = r.lse;
+    if (a.entropy) a.entropy[row] = stat_entropy(acc, r);
+    if (a.logprob) a.logprob[row] = stat_logprob(xt, r);
+}
+__device__ __forceinline__ void put_top(const StatsArgs& a, int64_t row, int place, uint64_t key, const RowStats& r) {
+    a.top_index[row * a.K + place] = key ? key_column(key) : -1;
+    a.top_logprob[row * a.K + place] = key ? stat_logprob(key_value(key), r) : __int_as_float(kNegInfF32);
+}
+
+// The keys of from[0, n) (all different; 0 is none) that fewer than K of them exceed:
+// put(place, key) for each.  Called by whole warps; four lanes count for one key.
+template <typename PUT>
+__device__ __forceinline__ void rank_keys(const uint64_t* from, int n, int K, int tid, int threads, PUT put) {
+    for (int i0 = 0; i0 < n; i0 += threads / 4) {
+        const int i = i0 + (tid >> 2);
+        const uint64_t key = i < n ? from[i] : 0;
+        int rank = 0;
+#pragma unroll 4
+        for (int j = tid & 3; j < n; j += 4) rank += from[j] > key;
+        rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+        rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+        if ((tid & 3) == 0 && key != 0 && rank < K) put(rank, key);
     }
-    __device__ static void top(const StatsArgs& a, int64_t row, int place, uint64_t key, StatAcc acc, float lse) {
-        a.top_index[row * a.K + place] = key ? key_column(key) : -1;
-        a.top_logprob[row * a.K + place] =
-            key ? stat_logprob(key_value(key), acc, lse) : __int_as_float(kNegInfF32);
-    }
-};
+}
 
 // Cluster barrier and the place of a shared variable in another CTA of the cluster.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
@@ -288,41 +383,36 @@ __device__ __forceinline__ V* cluster_map(V* p, uint32_t cta) {
 // ---------------------------------------------------------------------------
 constexpr int kStatU = 8;         // vectors per thread and batch
 constexpr int kStatChunks = 16;   // chunk maxima kept per thread
-constexpr int kChunkList = 256;   // chunks that may be read again
+constexpr int kChunkList = 64;    // chunks that a warp may read again
 constexpr int kMaxCluster = 16;
-constexpr int kFoundList = kMaxCluster * kMaxTopK;  // elements that may reach the bound; lists of a cluster
+constexpr int kFoundList = 512;   // elements that may reach the bound
+constexpr int kPartKeys = 48;     // keys that a part hands on as it found them
 
 template <int T, bool CLUSTER>
 struct StatsShared {
-    float chunk_max[kStatChunks * T];
+    float4 group_max4[8];
+    alignas(16) float chunk_max[kStatChunks * T];
     uint64_t found[kFoundList];
     uint64_t own[kMaxTopK];
-    uint64_t keys[CLUSTER ? kMaxCluster * kMaxTopK : 1];  // in the cluster's first CTA
+    // In the cluster's first CTA: the parts' keys, how many, their accumulators, and
+    // the maxima of 32 groups of threads of the whole cluster.
+    uint64_t keys[CLUSTER ? kMaxCluster * kPartKeys : 1];
+    int key_count[CLUSTER ? kMaxCluster : 1];
     float acc[3][CLUSTER ? kMaxCluster : 1];
+    float4 cluster_max4[CLUSTER ? 8 : 1];
     float part[3][T / 32];
-    float group_max[32];
-    int chunk[kChunkList];
-    int chunks, founds;
+    RowStats row;
+    int16_t chunk[T / 32][kChunkList];
+    int founds;
+    int overflow;
 };
-
-// `n` keys of `from`, all different but for the empty ones, to the places that
-// their ranks give them; places past the last key stay empty.
-template <int T, typename PUT>
-__device__ __forceinline__ void place_keys(const uint64_t* from, int n, int K, PUT put) {
-    for (int i = threadIdx.x; i < n; i += T) {
-        const uint64_t key = from[i];
-        if (key == 0) continue;
-        int rank = 0;
-        for (int j = 0; j < n; ++j) rank += from[j] > key;
-        if (rank < K) put(rank, key);
-    }
-}
 
 template <int DT, int T, bool CLUSTER>
 __global__ void __launch_bounds__(T, 1024 / T)
 lse_stats_kernel(const __grid_constant__ StatsArgs a) {
     constexpr int U = kStatU, NW = T / 32, EPV = 16 / DType<DT>::bytes;
     __shared__ StatsShared<T, CLUSTER> sh;
+    float* const group_max = reinterpret_cast<float*>(sh.group_max4);
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     pdl_trigger();
     if (CLUSTER) cluster_arrive();  // (waited for before the first remote store)
@@ -336,16 +426,18 @@ lse_stats_kernel(const __grid_constant__ StatsArgs a) {
     const int64_t k_begin = seg * per < r.vectors ? seg * per : r.vectors;
     const int64_t k_end = k_begin + per < r.vectors ? k_begin + per : r.vectors;
 
-    StatAcc acc = stat_identity();
-    float mu = 0.0f;
     const bool gather = a.logprob != nullptr && seg == 0 && tid == 0;
     const int64_t target = gather ? __ldg(a.target + row) : -1;
     float xt = __int_as_float(0x7fc00000);
     if (target >= 0 && target < a.N) xt = load_elem<DT>(r.a0 + r.off, target);
+    if (tid == 0) sh.founds = sh.overflow = 0;
+    if (CLUSTER && tid < kMaxTopK) sh.own[tid] = 0;
 
-    // The row, in batches of U vectors per thread; a chunk is chunk_batches of them.
+    // The row, in batches of U vectors per thread; a chunk is 2^chunk_shift of them.
+    StatAcc acc = stat_identity();
     {
-        float chunk_max = __int_as_float(kNegInfF32);
+        Shift shift = make_shift<DT>(acc.m);
+        float chunk_max = acc.m;
         int chunk = 0, in_chunk = 0;
         for (int64_t k = k_begin + tid; k - tid < k_end; k += U * T) {
             uint32_t w[4 * U];
@@ -366,10 +458,13 @@ lse_stats_kernel(const __grid_constant__ StatsArgs a) {
                 }
             }
             const float cm = words_max<DT, 4 * U>(w);
-            stat_raise(acc, mu, cm);
-            stat_add_words<DT, 4 * U>(acc, mu, w);
+            if (cm > acc.m) {
+                acc = stat_shift<DT>(acc, cm);
+                shift = make_shift<DT>(cm);
+            }
+            stat_add_words<DT, 4 * U>(acc, shift, w);
             chunk_max = fmaxf(chunk_max, cm);
-            if (++in_chunk == a.chunk_batches) {
+            if (++in_chunk == 1 << a.chunk_shift) {
                 sh.chunk_max[chunk * T + tid] = chunk_max;
                 chunk_max = __int_as_float(kNegInfF32);
                 in_chunk = 0;
@@ -378,66 +473,98 @@ lse_stats_kernel(const __grid_constant__ StatsArgs a) {
         }
         if (in_chunk > 0) sh.chunk_max[chunk * T + tid] = chunk_max;
     }
-    float group = acc.m;  // maximum of T / 32 neighbouring threads
+    float warp_max = acc.m;  // on the way to it, the maximum of NW neighbouring threads
 #pragma unroll
-    for (int off = NW / 2; off > 0; off >>= 1) group = fmaxf(group, __shfl_xor_sync(0xffffffffu, group, off));
-    if (tid % NW == 0) sh.group_max[tid / NW] = group;
-    const float thread_max = acc.m;
-    acc = stat_warp_merge(acc);
+    for (int off = 1; off < 32; off <<= 1) {
+        if (off == NW && tid % NW == 0) group_max[tid / NW] = warp_max;
+        warp_max = fmaxf(warp_max, __shfl_xor_sync(0xffffffffu, warp_max, off));
+    }
+    acc = stat_shift<DT>(acc, warp_max);
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        acc.s += __shfl_xor_sync(0xffffffffu, acc.s, off);
+        acc.u += __shfl_xor_sync(0xffffffffu, acc.u, off);
+    }
     if (lane == 0) {
         sh.part[0][wid] = acc.m;
         sh.part[1][wid] = acc.s;
         sh.part[2][wid] = acc.u;
     }
-    if (tid == 0) sh.chunks = sh.founds = 0;
-    if (CLUSTER && tid < kMaxTopK) sh.own[tid] = 0;
     __syncthreads();
-    // Every warp merges the partials (the same order everywhere).
-    acc = lane < NW ? StatAcc{sh.part[0][lane], sh.part[1][lane], sh.part[2][lane]} : stat_identity();
-    acc = stat_warp_merge(acc);
-    const float lse = acc_finalize(Acc{acc.m, acc.s});
-    if (!CLUSTER && tid == 0) StatsOut::row(a, row, acc, xt, lse);
+    bool nan = false;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) nan |= sh.part[1][w] != sh.part[1][w];
+    if (wid == 0) {
+        acc = lane < NW ? StatAcc{sh.part[0][lane], sh.part[1][lane], sh.part[2][lane]} : stat_identity();
+        acc = stat_lanes_merge<DT, NW>(acc);
+        if (!CLUSTER && lane == 0) {
+            const RowStats rs = row_stats<DT>(acc);
+            sh.row = rs;
+            put_row(a, row, acc, rs, xt);
+        }
+    }
 
     if (a.K > 0) {
-        const int batches = static_cast<int>((k_end - k_begin + U * T - 1) / (U * T));
-        const int chunks = (batches + a.chunk_batches - 1) / a.chunk_batches;
-        const float bound = kth_largest(sh.group_max[lane], a.K, lane);
-        bool scan = acc.s != acc.s || bound == __int_as_float(kNegInfF32);  // NaN, or too few left
-        if (!scan) {
-            if (thread_max >= bound) {
-                for (int c = 0; c < chunks; ++c)
-                    if (sh.chunk_max[c * T + tid] >= bound) {
-                        const int at = atomicAdd(&sh.chunks, 1);
-                        if (at < kChunkList) sh.chunk[at] = c * T + tid;
-                    }
+        const float bound = kth_largest_of(group_max, a.K, lane);
+        bool scan = nan || bound == __int_as_float(kNegInfF32);  // NaN, or too few left
+        if (!scan && warp_max >= bound) {
+            const int per_shift = 3 + a.chunk_shift;  // log2 of a chunk's vectors
+            const int chunks = static_cast<int>((k_end - k_begin + (static_cast<int64_t>(T) << per_shift) - 1) >> per_shift) / T;
+            int n = 0;
+#pragma unroll 4
+            for (int c = 0; c < chunks; ++c) {
+                const bool in = sh.chunk_max[c * T + tid] >= bound;
+                const uint32_t who = __ballot_sync(0xffffffffu, in);
+                const int at = n + __popc(who & ((1u << lane) - 1));
+                if (in && at < kChunkList) sh.chunk[wid][at] = static_cast<int16_t>(c * 32 + lane);
+                n += __popc(who);
             }
-            __syncthreads();
-            const int n = sh.chunks;
-            scan = n > kChunkList;
-            if (!scan) {
-                // A thread per vector: U * chunk_batches vectors of each chunk.
-                const int per_chunk = U * a.chunk_batches;
-                for (int i = tid; i < n * per_chunk; i += T) {
-                    const int c = sh.chunk[i / per_chunk];
-                    const int64_t k = k_begin + static_cast<int64_t>(c / T) * (per_chunk * T) + c % T +
-                                      static_cast<int64_t>(i % per_chunk) * T;
-                    if (k >= k_end) continue;
-                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(r.a0 + k * 16));
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            if (n > kChunkList) {
+                n = 0;
+                sh.overflow = 1;
+            }
+            __syncwarp();
+            const int items = n << per_shift;
+            // Two vectors of the chunks per lane and round.
+            for (int i0 = 0; i0 < items; i0 += 64) {
+                uint32_t w[8];
+                uint32_t col[2];  // of each vector's first element (wraps below the row's first)
 #pragma unroll
-                    for (int e = 0; e < EPV; ++e) {
-                        const float x = word_elem<DT>(w, e);
-                        const int64_t col = column_of<DT>(r, k, e);
-                        if (x >= bound && col >= 0 && col < a.N) {
-                            const int at = atomicAdd(&sh.founds, 1);
-                            if (at < kFoundList) sh.found[at] = topk_key(x, static_cast<uint32_t>(col));
-                        }
-                    }
+                for (int h = 0; h < 2; ++h) {
+                    const int i = i0 + 32 * h + lane;
+                    const int c = i < items ? sh.chunk[wid][i >> per_shift] : 0;
+                    // (a part's vectors fit 32 bits: N does)
+                    const int k = ((c >> 5) << per_shift) * T + wid * 32 + (c & 31) + (i & ((1 << per_shift) - 1)) * T;
+                    load_vector<DT>(r, k_begin + k, i < items ? k_end : 0, &w[4 * h]);
+                    col[h] = static_cast<uint32_t>(column_of<DT>(r, k_begin + k, 0));
                 }
-                __syncthreads();
-                scan = sh.founds > kFoundList;
+                uint32_t mine = 0;
+#pragma unroll
+                for (int e = 0; e < 2 * EPV; ++e)
+                    mine |= (word_elem<DT>(&w[e / EPV * 4], e % EPV) >= bound ? 1u : 0u) << e;
+                const uint32_t inside = static_cast<uint32_t>(a.N) - EPV;
+                if (col[0] > inside || col[1] > inside) {  // the row's ends: elements outside it
+#pragma unroll
+                    for (int e = 0; e < 2 * EPV; ++e)
+                        if (col[e / EPV] + e % EPV >= a.N) mine &= ~(1u << e);
+                }
+                const int total = __reduce_add_sync(0xffffffffu, __popc(mine));
+                if (total == 0) continue;
+                int at = 0;
+                if (lane == 0) at = atomicAdd(&sh.founds, total);
+                at = __shfl_sync(0xffffffffu, at, 0);
+                for (uint32_t who; (who = __ballot_sync(0xffffffffu, mine != 0)) != 0; at += __popc(who)) {
+                    if (mine == 0) continue;
+                    const int e = __ffs(mine) - 1;
+                    mine &= mine - 1;
+                    const int place = at + __popc(who & ((1u << lane) - 1));
+                    if (place < kFoundList)
+                        sh.found[place] = topk_key(pick_elem<DT, 8>(w, e), (e < EPV ? col[0] : col[1] - EPV) + e);
+                }
             }
         }
+        __syncthreads();
+        scan = scan || sh.overflow != 0 || sh.founds > kFoundList;
         const int n = scan ? T : sh.founds;
         if (scan) {  // a part of the vectors per warp, in order
             __syncthreads();
@@ -448,13 +575,26 @@ lse_stats_kernel(const __grid_constant__ StatsArgs a) {
             __syncthreads();
         }
         if (!CLUSTER) {
-            place_keys<T>(sh.found, n, a.K, [&](int place, uint64_t key) { StatsOut::top(a, row, place, key, acc, lse); });
-        } else {
-            // A part may hold fewer than K elements: its last places stay empty.
-            place_keys<T>(sh.found, n, a.K, [&](int place, uint64_t key) { sh.own[place] = key; });
+            const RowStats rs = sh.row;
+            rank_keys(sh.found, n, a.K, tid, T, [&](int place, uint64_t key) { put_top(a, row, place, key, rs); });
+            return;
+        }
+        // A part hands on what it found, or the K largest of many.
+        int count = n;
+        const uint64_t* from = sh.found;
+        if (n > kPartKeys) {
+            rank_keys(sh.found, n, a.K, tid, T, [&](int place, uint64_t key) { sh.own[place] = key; });
+            count = a.K;
+            from = sh.own;
             __syncthreads();
-            cluster_wait();
-            if (tid < a.K) cluster_map(sh.keys, 0)[seg * a.K + tid] = sh.own[tid];
+        }
+        cluster_wait();
+        if (tid < count) cluster_map(sh.keys, 0)[seg * kPartKeys + tid] = from[tid];
+        if (tid == 0) cluster_map(sh.key_count, 0)[seg] = count;
+        if (tid >= T - 32 && lane < 32 / P) {  // its threads in 32 / P groups
+            float m = group_max[lane * P];
+            for (int i = 1; i < P; ++i) m = fmaxf(m, group_max[lane * P + i]);
+            reinterpret_cast<float*>(cluster_map(sh.cluster_max4, 0))[seg * (32 / P) + lane] = m;
         }
     } else if (CLUSTER) {
         cluster_wait();
@@ -469,35 +609,36 @@ lse_stats_kernel(const __grid_constant__ StatsArgs a) {
         cluster_arrive();
         if (seg != 0) return;
         cluster_wait();
-        acc = lane < P ? StatAcc{sh.acc[0][lane], sh.acc[1][lane], sh.acc[2][lane]} : stat_identity();
-        acc = stat_warp_merge(acc);
-        const float row_lse = acc_finalize(Acc{acc.m, acc.s});
-        if (tid == 0) StatsOut::row(a, row, acc, xt, row_lse);
-        if (a.K > 0) {
-            // The first 32 / P keys of the parts' lists are 32 keys: the K-th largest of
-            // their values is a bound again, and warp 0 ranks what reaches it.
-            if (wid == 0) {
-                const int each = 32 / P, n = P * a.K;
-                const uint64_t head = lane % each < a.K ? sh.keys[lane / each * a.K + lane % each] : 0;
-                const float bound = kth_largest(head ? key_value(head) : __int_as_float(kNegInfF32), a.K, lane);
-                int founds = 0;
-                for (int i = 0; i < n; i += 32) {
-                    const uint64_t key = i + lane < n ? sh.keys[i + lane] : 0;
-                    // (a NaN reaches every bound)
-                    const bool in = key != 0 && !(key_value(key) < bound);
-                    const uint32_t who = __ballot_sync(0xffffffffu, in);
-                    if (in) sh.found[founds + __popc(who & ((1u << lane) - 1))] = key;
-                    founds += __popc(who);
-                }
-                __syncwarp();
-                for (int i = lane; i < founds; i += 32) {
-                    const uint64_t key = sh.found[i];
-                    int rank = 0;
-                    for (int j = 0; j < founds; ++j) rank += sh.found[j] > key;
-                    if (rank < a.K) StatsOut::top(a, row, rank, key, acc, row_lse);
-                }
+        if (wid == 0) {
+            acc = lane < P ? StatAcc{sh.acc[0][lane], sh.acc[1][lane], sh.acc[2][lane]} : stat_identity();
+            acc = stat_lanes_merge<DT, kMaxCluster>(acc);
+            if (lane == 0) {
+                const RowStats rs = row_stats<DT>(acc);
+                sh.row = rs;
+                put_row(a, row, acc, rs, xt);
             }
         }
+        if (a.K == 0) return;
+        // Of the parts' keys, those that reach the bound of the whole row.
+        static_assert(kMaxCluster * kPartKeys * 8 <= kStatChunks * 128 * 4 && kPartKeys % 16 == 0, "whole warps");
+        uint64_t* reached = reinterpret_cast<uint64_t*>(sh.chunk_max);  // (no longer needed)
+        if (tid == 0) sh.founds = 0;
+        const float bound = kth_largest_of(reinterpret_cast<const float*>(sh.cluster_max4), a.K, lane);
+        __syncthreads();
+        for (int i = tid; i < P * kPartKeys; i += T) {
+            const int part = i / kPartKeys;
+            const uint64_t key = i - part * kPartKeys < sh.key_count[part] ? sh.keys[i] : 0;
+            const bool in = key != 0 && !(key_value(key) < bound);  // (a NaN reaches every bound)
+            const uint32_t who = __ballot_sync(0xffffffffu, in);
+            if (who == 0) continue;
+            int at = 0;
+            if (lane == 0) at = atomicAdd(&sh.founds, __popc(who));
+            at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1));
+            if (in) reached[at] = key;
+        }
+        __syncthreads();
+        const RowStats rs = sh.row;
+        rank_keys(reached, sh.founds, a.K, tid, T, [&](int place, uint64_t key) { put_top(a, row, place, key, rs); });
     }
 }
 
@@ -564,14 +705,14 @@ lse_stats_short_kernel(const __grid_constant__ StatsArgs a) {
 #pragma unroll
         for (int off2 = G / 2; off2 > 0; off2 >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off2));
         StatAcc acc{m, 0.0f, 0.0f};
-        stat_add_words<DT, 4 * V>(acc, shift_of(m), w);
+        stat_add_words<DT, 4 * V>(acc, make_shift<DT>(m), w);
 #pragma unroll
         for (int off2 = G / 2; off2 > 0; off2 >>= 1) {
             acc.s += __shfl_xor_sync(0xffffffffu, acc.s, off2);
             acc.u += __shfl_xor_sync(0xffffffffu, acc.u, off2);
         }
-        const float lse = acc_finalize(Acc{acc.m, acc.s});
-        if (sub == 0 && live) StatsOut::row(a, row, acc, xt, lse);
+        const RowStats rs = row_stats<DT>(acc);
+        if (sub == 0 && live) put_row(a, row, acc, rs, xt);
         if (a.K == 0) continue;
 
         const float bound = kth_largest<G>(lane_max, a.K, lane);
@@ -609,8 +750,9 @@ lse_stats_short_kernel(const __grid_constant__ StatsArgs a) {
             for (int i = sub; i < n; i += G) {
                 const uint64_t key = found[i];
                 int rank = 0;
+#pragma unroll 4
                 for (int j = 0; j < n; ++j) rank += found[j] > key;
-                if (rank < a.K) StatsOut::top(a, row, rank, key, acc, lse);
+                if (rank < a.K) put_top(a, row, rank, key, rs);
             }
         }
         // Rows that need the scan, by the whole warp in turn.
@@ -620,10 +762,9 @@ lse_stats_short_kernel(const __grid_constant__ StatsArgs a) {
             todo &= todo - 1;
             const Row r = make_row<DT>(a.x, row0 + q / G, a.row_stride, a.N);
             const uint64_t key = scan_vectors<DT>(r, 0, r.vectors, a.N, a.K, lane);
-            const StatAcc of{__shfl_sync(0xffffffffu, acc.m, q), __shfl_sync(0xffffffffu, acc.s, q),
-                             __shfl_sync(0xffffffffu, acc.u, q)};
-            const float of_lse = __shfl_sync(0xffffffffu, lse, q);
-            if (lane < a.K) StatsOut::top(a, row0 + q / G, lane, key, of, of_lse);
+            const RowStats of{__shfl_sync(0xffffffffu, rs.m, q), __shfl_sync(0xffffffffu, rs.lse, q),
+                              __shfl_sync(0xffffffffu, rs.logs, q)};
+            if (lane < a.K) put_top(a, row0 + q / G, lane, key, of);
         }
         __syncwarp();
     }
@@ -735,7 +876,7 @@ cudaError_t launch_stats(StatsArgs a, int sms, cudaStream_t stream) {
     const bool aligned = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (a.row_stride * eb) % 16 == 0;
     const int64_t vectors = (a.N * eb + 15) / 16 + (aligned ? 0 : 1);  // at most
     a.cluster = 1;
-    a.chunk_batches = 1;
+    a.chunk_shift = 0;
     if (vectors <= 32 * 8) {
         int G = 32;
         if (vectors <= 16 * 8 && a.K <= 8) G = 16;
@@ -758,15 +899,12 @@ cudaError_t launch_stats(StatsArgs a, int sms, cudaStream_t stream) {
     }
     if (const char* e = getenv("LSE_T")) T = atoi(e);
     if (const char* e = getenv("LSE_P")) P = atoi(e);
+    if (P > 1 && T > 256) T = 256;
     a.cluster = P;
     const int64_t batches = ((vectors + P - 1) / P + kStatU * T - 1) / (kStatU * T);
-    a.chunk_batches = static_cast<int>((batches + kStatChunks - 1) / kStatChunks);
+    while ((batches + (1LL << a.chunk_shift) - 1) >> a.chunk_shift > kStatChunks) ++a.chunk_shift;
     if (P > 1) {
-        switch (T) {
-        case 128: return launch_stats_long<DT, 128, true>(a, stream);
-        case 256: return launch_stats_long<DT, 256, true>(a, stream);
-        default: return launch_stats_long<DT, 512, true>(a, stream);
-        }
+        return T == 128 ? launch_stats_long<DT, 128, true>(a, stream) : launch_stats_long<DT, 256, true>(a, stream);
     }
     switch (T) {
     case 128: return launch_stats_long<DT, 128, false>(a, stream);
