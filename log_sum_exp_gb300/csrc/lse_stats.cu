@@ -15,7 +15,6 @@
 // s 2^-d.
 #include <climits>
 #include <cstdint>
-#include <cstdlib>
 
 #include <cuda_runtime.h>
 
@@ -353,18 +352,18 @@ __device__ __forceinline__ void put_top(const StatsArgs& a, int64_t row, int pla
 }
 
 // The keys of from[0, n) (all different; 0 is none) that fewer than K of them exceed:
-// put(place, key) for each.  Called by whole warps; four lanes count for one key.
-template <typename PUT>
+// put(place, key) for each.  Called by whole warps; LANES lanes count for one key.
+template <int LANES, typename PUT>
 __device__ __forceinline__ void rank_keys(const uint64_t* from, int n, int K, int tid, int threads, PUT put) {
-    for (int i0 = 0; i0 < n; i0 += threads / 4) {
-        const int i = i0 + (tid >> 2);
+    for (int i0 = 0; i0 < n; i0 += threads / LANES) {
+        const int i = i0 + tid / LANES;
         const uint64_t key = i < n ? from[i] : 0;
         int rank = 0;
 #pragma unroll 4
-        for (int j = tid & 3; j < n; j += 4) rank += from[j] > key;
-        rank += __shfl_xor_sync(0xffffffffu, rank, 1);
-        rank += __shfl_xor_sync(0xffffffffu, rank, 2);
-        if ((tid & 3) == 0 && key != 0 && rank < K) put(rank, key);
+        for (int j = tid % LANES; j < n; j += LANES) rank += from[j] > key;
+#pragma unroll
+        for (int off = 1; off < LANES; off <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, off);
+        if (tid % LANES == 0 && key != 0 && rank < K) put(rank, key);
     }
 }
 
@@ -385,11 +384,12 @@ constexpr int kStatU = 8;         // vectors per thread and batch
 constexpr int kStatChunks = 16;   // chunk maxima kept per thread
 constexpr int kChunkList = 64;    // chunks that a warp may read again
 constexpr int kMaxCluster = 16;
-constexpr int kFoundList = 512;   // elements that may reach the bound
+constexpr int kUnitsPerCta = 8;   // one-warp rows per CTA
 constexpr int kPartKeys = 48;     // keys that a part hands on as it found them
 
 template <int T, bool CLUSTER>
 struct StatsShared {
+    static constexpr int kFoundList = T == 32 ? 192 : 512;  // elements that may reach the bound
     float4 group_max4[8];
     alignas(16) float chunk_max[kStatChunks * T];
     uint64_t found[kFoundList];
@@ -407,20 +407,29 @@ struct StatsShared {
     int overflow;
 };
 
+// T threads per row: a CTA, or (32) one of the kUnitsPerCta warps of a CTA, which then
+// need no barrier and overlap one row's end with other rows' loads.
 template <int DT, int T, bool CLUSTER>
-__global__ void __launch_bounds__(T, 1024 / T)
+__global__ void __launch_bounds__(T == 32 ? 32 * kUnitsPerCta : T, T == 32 ? 32 / kUnitsPerCta : 1024 / T)
 lse_stats_kernel(const __grid_constant__ StatsArgs a) {
-    constexpr int U = kStatU, NW = T / 32, EPV = 16 / DType<DT>::bytes;
-    __shared__ StatsShared<T, CLUSTER> sh;
+    constexpr int U = kStatU, NW = T / 32, EPV = 16 / DType<DT>::bytes, UNITS = T == 32 ? kUnitsPerCta : 1;
+    __shared__ StatsShared<T, CLUSTER> sh_units[UNITS];
+    StatsShared<T, CLUSTER>& sh = sh_units[UNITS > 1 ? threadIdx.x / 32 : 0];
+    constexpr int kFoundList = StatsShared<T, CLUSTER>::kFoundList;
     float* const group_max = reinterpret_cast<float*>(sh.group_max4);
-    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const int tid = UNITS > 1 ? threadIdx.x & 31 : threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const auto sync = [] {
+        if (T == 32) __syncwarp();
+        else __syncthreads();
+    };
     pdl_trigger();
     if (CLUSTER) cluster_arrive();  // (waited for before the first remote store)
     pdl_wait();
 
     const int P = CLUSTER ? a.cluster : 1;
-    const int64_t row = blockIdx.x / P;
-    const int seg = static_cast<int>(blockIdx.x - row * P);
+    const int64_t row = UNITS > 1 ? static_cast<int64_t>(blockIdx.x) * UNITS + threadIdx.x / 32 : blockIdx.x / P;
+    if (UNITS > 1 && row >= a.B) return;
+    const int seg = CLUSTER ? static_cast<int>(blockIdx.x - row * P) : 0;
     const Row r = make_row<DT>(a.x, row, a.row_stride, a.N);
     const int64_t per = CLUSTER ? (r.vectors + P - 1) / P : r.vectors;
     const int64_t k_begin = seg * per < r.vectors ? seg * per : r.vectors;
@@ -476,7 +485,7 @@ lse_stats_kernel(const __grid_constant__ StatsArgs a) {
     float warp_max = acc.m;  // on the way to it, the maximum of NW neighbouring threads
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        if (off == NW && tid % NW == 0) group_max[tid / NW] = warp_max;
+        if (off == NW && tid % NW == 0) group_max[tid / NW] = warp_max;  // (NW = 1: each lane's own)
         warp_max = fmaxf(warp_max, __shfl_xor_sync(0xffffffffu, warp_max, off));
     }
     acc = stat_shift<DT>(acc, warp_max);
@@ -490,7 +499,7 @@ lse_stats_kernel(const __grid_constant__ StatsArgs a) {
         sh.part[1][wid] = acc.s;
         sh.part[2][wid] = acc.u;
     }
-    __syncthreads();
+    sync();
     bool nan = false;
 #pragma unroll
     for (int w = 0; w < NW; ++w) nan |= sh.part[1][w] != sh.part[1][w];
@@ -563,30 +572,30 @@ lse_stats_kernel(const __grid_constant__ StatsArgs a) {
                 }
             }
         }
-        __syncthreads();
+        sync();
         scan = scan || sh.overflow != 0 || sh.founds > kFoundList;
         const int n = scan ? T : sh.founds;
         if (scan) {  // a part of the vectors per warp, in order
-            __syncthreads();
+            sync();
             const int64_t share = (k_end - k_begin + NW - 1) / NW;
             const int64_t k0 = k_begin + wid * share < k_end ? k_begin + wid * share : k_end;
             const int64_t k1 = k0 + share < k_end ? k0 + share : k_end;
             sh.found[tid] = scan_vectors<DT>(r, k0, k1, a.N, a.K, lane);
-            __syncthreads();
+            sync();
         }
         if (!CLUSTER) {
             const RowStats rs = sh.row;
-            rank_keys(sh.found, n, a.K, tid, T, [&](int place, uint64_t key) { put_top(a, row, place, key, rs); });
+            rank_keys<T == 32 ? 1 : 4>(sh.found, n, a.K, tid, T, [&](int place, uint64_t key) { put_top(a, row, place, key, rs); });
             return;
         }
         // A part hands on what it found, or the K largest of many.
         int count = n;
         const uint64_t* from = sh.found;
         if (n > kPartKeys) {
-            rank_keys(sh.found, n, a.K, tid, T, [&](int place, uint64_t key) { sh.own[place] = key; });
+            rank_keys<4>(sh.found, n, a.K, tid, T, [&](int place, uint64_t key) { sh.own[place] = key; });
             count = a.K;
             from = sh.own;
-            __syncthreads();
+            sync();
         }
         cluster_wait();
         if (tid < count) cluster_map(sh.keys, 0)[seg * kPartKeys + tid] = from[tid];
@@ -638,7 +647,7 @@ lse_stats_kernel(const __grid_constant__ StatsArgs a) {
         }
         __syncthreads();
         const RowStats rs = sh.row;
-        rank_keys(reached, sh.founds, a.K, tid, T, [&](int place, uint64_t key) { put_top(a, row, place, key, rs); });
+        rank_keys<4>(reached, sh.founds, a.K, tid, T, [&](int place, uint64_t key) { put_top(a, row, place, key, rs); });
     }
 }
 
@@ -829,8 +838,9 @@ lse_stats_backward_kernel(const StatsBackwardArgs a) {
 template <int DT, int T, bool CLUSTER>
 cudaError_t launch_stats_long(const StatsArgs& a, cudaStream_t stream) {
     const auto kernel = lse_stats_kernel<DT, T, CLUSTER>;
-    const dim3 grid(static_cast<unsigned>(a.B * a.cluster));
-    if (!CLUSTER) return launch_pdl(kernel, grid, dim3(T), stream, a);
+    const int64_t ctas = T == 32 ? (a.B + kUnitsPerCta - 1) / kUnitsPerCta : a.B * a.cluster;
+    const dim3 grid(static_cast<unsigned>(ctas));
+    if (!CLUSTER) return launch_pdl(kernel, grid, dim3(T == 32 ? 32 * kUnitsPerCta : T), stream, a);
     cudaLaunchAttribute attr[2] = {};
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -881,7 +891,6 @@ cudaError_t launch_stats(StatsArgs a, int sms, cudaStream_t stream) {
         int G = 32;
         if (vectors <= 16 * 8 && a.K <= 8) G = 16;
         if (vectors <= 8 * 8 && a.K <= 4) G = 8;
-        if (const char* e = getenv("LSE_G")) G = atoi(e);
         const int V = static_cast<int>((vectors + G - 1) / G);
         return G == 8 ? launch_stats_short<DT, 8>(a, V, sms, stream)
                : G == 16 ? launch_stats_short<DT, 16>(a, V, sms, stream)
@@ -892,13 +901,13 @@ cudaError_t launch_stats(StatsArgs a, int sms, cudaStream_t stream) {
     int T = 512;
     while (T > 128 && vectors < 2LL * kStatU * T) T /= 2;
     if (a.B >= 4LL * sms) T = 128;
+    // Rows of up to 1024 vectors by the thousand: a warp each.
+    if (vectors <= 1024 && a.B >= 16LL * sms) T = 32;
     int P = 1;
     if (a.B < sms) {
         while (P < kMaxCluster && a.B * P * 2 <= 2LL * sms && vectors >= 2LL * P * kStatU * 128) P *= 2;
         while (T > 128 && vectors < 1LL * P * kStatU * T) T /= 2;
     }
-    if (const char* e = getenv("LSE_T")) T = atoi(e);
-    if (const char* e = getenv("LSE_P")) P = atoi(e);
     if (P > 1 && T > 256) T = 256;
     a.cluster = P;
     const int64_t batches = ((vectors + P - 1) / P + kStatU * T - 1) / (kStatU * T);
@@ -907,6 +916,7 @@ cudaError_t launch_stats(StatsArgs a, int sms, cudaStream_t stream) {
         return T == 128 ? launch_stats_long<DT, 128, true>(a, stream) : launch_stats_long<DT, 256, true>(a, stream);
     }
     switch (T) {
+    case 32: return launch_stats_long<DT, 32, false>(a, stream);
     case 128: return launch_stats_long<DT, 128, false>(a, stream);
     case 256: return launch_stats_long<DT, 256, false>(a, stream);
     default: return launch_stats_long<DT, 512, false>(a, stream);
