@@ -54,6 +54,8 @@ struct StatsBackwardArgs {
     const float* grad_lse;
     void* dx;
     int64_t dx_row_stride;
+    int64_t seg_slots;  // vectors or elements of a segment
+    int64_t segments;   // per row
 };
 
 // Two floats -> packed 16-bit pair, nearest-even.
@@ -779,59 +781,218 @@ lse_stats_short_kernel(const __grid_constant__ StatsArgs a) {
     }
 }
 
-constexpr int kStatThreads = 256;
-
+// ---------------------------------------------------------------------------
+// Gradient.
+//
+//     dx_n = p_n (A - gH log p_n) + gl [n = t] + sum_k gt_k [n = i_k],
+//     A = g_lse - gl - sum_k gt_k - gH H,   log p_n = x_n - lse
+//
+// TX threads take a segment of a row, four vectors each at a time, every load
+// issued before the stores.  The few elements with a unit term are read before
+// anything is stored (dx may be x) and written once more, whole, at the end, so the
+// loop compares no columns.  Rows run from the last to the first: the forward pass
+// that comes before has left the last ones in L2.
+// ---------------------------------------------------------------------------
 template <int DT>
 __device__ __forceinline__ void put_elem(void* row, int64_t i, float v) {
-    if constexpr (DT == kF32) {
-        static_cast<float*>(row)[i] = v;
+    if constexpr (DT == kF32) static_cast<float*>(row)[i] = v;
+    else static_cast<unsigned short*>(row)[i] = static_cast<unsigned short>(pack2<DT>(v, 0.0f));
+}
+
+struct RowGrad {
+    float lse, A, gh;
+};
+
+// One pair of elements.  An element with p = 0 adds nothing: log p is bounded from
+// below, so that it stays 0 * finite.
+template <bool ENT>
+__device__ __forceinline__ uint64_t grad_pair(uint64_t x, const RowGrad& g) {
+    const uint64_t lp = f2_sub(x, f2_pack(g.lse, g.lse));
+    const uint64_t e = f2_ex2(f2_mul(lp, f2_pack(kLog2e, kLog2e)));
+    if constexpr (!ENT) {
+        return f2_mul(e, f2_pack(g.A, g.A));
     } else {
-        uint32_t r;
-        if constexpr (DT == kBF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(0.0f), "f"(v));
-        else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(0.0f), "f"(v));
-        static_cast<unsigned short*>(row)[i] = static_cast<unsigned short>(r);
+        float l0, l1;
+        f2_unpack(lp, l0, l1);
+        const uint64_t low = f2_pack(fmaxf(l0, kFarBelow), fmaxf(l1, kFarBelow));
+        return f2_mul(e, f2_fma(f2_pack(-g.gh, -g.gh), low, f2_pack(g.A, g.A)));
     }
 }
 
-// dx_n = p_n (c - gH (log p_n + H)) + gl [n = t] + sum_k gt_k [n = i_k],
-// c = g_lse - gl - sum_k gt_k.  A CTA per row.
-template <int DT>
-__global__ void __launch_bounds__(kStatThreads)
-lse_stats_backward_kernel(const StatsBackwardArgs a) {
+// The same for one element, with what is added to it.
+__device__ __forceinline__ float grad_elem(float x, const RowGrad& g, float unit) {
+    const float lp = x - g.lse;
+    const float e = ex2(lp * kLog2e);
+    return (g.gh != 0.0f ? e * fmaf(-g.gh, fmaxf(lp, kFarBelow), g.A) : e * g.A) + unit;
+}
+
+template <int DT, bool ENT>
+__device__ __forceinline__ uint4 grad_vector(uint4 v, const RowGrad& g) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o[4];
+    if constexpr (DT == kF32) {
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            float a, b;
+            f2_unpack(grad_pair<ENT>(f2_pack(__uint_as_float(w[i]), __uint_as_float(w[i + 1])), g), a, b);
+            o[i] = __float_as_uint(a);
+            o[i + 1] = __float_as_uint(b);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float a, b;
+            f2_unpack(grad_pair<ENT>(f2_pack(word_lo<DT>(w[i]), word_hi<DT>(w[i])), g), a, b);
+            o[i] = pack2<DT>(a, b);
+        }
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+constexpr int kGradU = 4;        // vectors (or elements) per thread and step
+constexpr int kGradCta = 256;    // threads of a CTA of one-warp units
+
+// Slots [k0, k1) of a row: the 16-byte vectors that cover it (VEC; x and dx rows at
+// the same offset from a boundary), the outer ones stored element by element, or
+// single elements.
+template <int DT, int TX, bool VEC, bool ENT>
+__device__ __forceinline__ void grad_slots(const char* xr, char* dr, int off, int64_t end, int64_t k0,
+                                           int64_t k1, int tid, const RowGrad& g) {
+    constexpr int EB = DType<DT>::bytes, EPV = 16 / EB;
+    for (int64_t k = k0 + tid; k < k1; k += kGradU * TX) {
+        if constexpr (VEC) {
+            const char* x0 = xr - off;
+            char* d0 = dr - off;
+            uint4 v[kGradU];
+#pragma unroll
+            for (int j = 0; j < kGradU; ++j)
+                if (k + j * TX < k1) v[j] = ldg_stream16(x0 + (k + j * TX) * 16);
+#pragma unroll
+            for (int j = 0; j < kGradU; ++j) {
+                const int64_t kk = k + j * TX;
+                if (kk >= k1) continue;
+                const uint4 o = grad_vector<DT, ENT>(v[j], g);
+                if ((kk > 0 || off == 0) && kk * 16 + 16 <= end) {
+                    *reinterpret_cast<uint4*>(d0 + kk * 16) = o;
+                } else {
+                    const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                    for (int i = 0; i < EPV; ++i) {
+                        const int64_t at = kk * 16 + i * EB;
+                        if (at < off || at >= end) continue;
+                        if constexpr (DT == kF32) *reinterpret_cast<uint32_t*>(d0 + at) = w[i];
+                        else *reinterpret_cast<unsigned short*>(d0 + at) = static_cast<unsigned short>((i & 1) ? w[i / 2] >> 16 : w[i / 2]);
+                    }
+                }
+            }
+        } else {
+            float v[kGradU];
+#pragma unroll
+            for (int j = 0; j < kGradU; ++j)
+                if (k + j * TX < k1) v[j] = load_elem<DT>(xr, k + j * TX);
+#pragma unroll
+            for (int j = 0; j < kGradU; ++j)
+                if (k + j * TX < k1) put_elem<DT>(dr, k + j * TX, grad_elem(v[j], g, 0.0f));
+        }
+    }
+}
+
+// Zeros for the same slots of a row that carries no gradient.
+template <int DT, int TX, bool VEC>
+__device__ __forceinline__ void zero_slots(char* dr, int off, int64_t end, int64_t k0, int64_t k1, int tid) {
+    constexpr int EB = DType<DT>::bytes;
+    for (int64_t k = k0 + tid; k < k1; k += TX) {
+        if constexpr (!VEC) {
+            put_elem<DT>(dr, k, 0.0f);
+        } else if ((k > 0 || off == 0) && k * 16 + 16 <= end) {
+            *reinterpret_cast<uint4*>(dr - off + k * 16) = make_uint4(0, 0, 0, 0);
+        } else {
+            for (int64_t at = k * 16; at < k * 16 + 16; at += EB)
+                if (at >= off && at < end) put_elem<DT>(dr, (at - off) / EB, 0.0f);
+        }
+    }
+}
+
+template <int DT, int TX, bool VEC>
+__global__ void __launch_bounds__(TX == 32 ? kGradCta : TX, TX == 32 ? 4 : 1024 / TX)
+lse_stats_backward_kernel(const __grid_constant__ StatsBackwardArgs a) {
+    constexpr int EB = DType<DT>::bytes, UNITS = TX == 32 ? kGradCta / 32 : 1;
+    const int tid = threadIdx.x % TX, lane = threadIdx.x & 31;
+    const auto sync = [] {
+        if (TX == 32) __syncwarp();
+        else __syncthreads();
+    };
     pdl_trigger();
     pdl_wait();
-    const int tid = threadIdx.x;
-    for (int64_t row = blockIdx.x; row < a.B; row += gridDim.x) {
-        const char* xr = static_cast<const char*>(a.x) + row * a.row_stride * DType<DT>::bytes;
-        char* dr = static_cast<char*>(a.dx) + row * a.dx_row_stride * DType<DT>::bytes;
-        const int64_t t = a.grad_logprob ? a.target[row] : -1;
-        const float gl = t >= 0 && t < a.N ? a.grad_logprob[row] : 0.0f;
-        const float gh = a.grad_entropy ? a.grad_entropy[row] : 0.0f;
-        const float gs = a.grad_lse ? a.grad_lse[row] : 0.0f;
-        float c = gs - gl;
-        bool any = gl != 0.0f || gh != 0.0f || gs != 0.0f;
-        for (int k = 0; k < a.K; ++k) {
-            const int64_t i = a.top_index[row * a.K + k];
-            const float g = a.grad_top[row * a.K + k];
-            if (i >= 0 && i < a.N && g != 0.0f) {
-                c -= g;
-                any = true;
-            }
+    const int64_t units = a.B * a.segments;
+    for (int64_t unit = static_cast<int64_t>(blockIdx.x) * UNITS + threadIdx.x / TX; unit < units;
+         unit += static_cast<int64_t>(gridDim.x) * UNITS) {
+        const int64_t row = a.B - 1 - unit / a.segments;
+        const int64_t seg = unit % a.segments;
+        const char* xr = static_cast<const char*>(a.x) + row * a.row_stride * EB;
+        char* dr = static_cast<char*>(a.dx) + row * a.dx_row_stride * EB;
+        const int off = VEC ? static_cast<int>(reinterpret_cast<uintptr_t>(xr) & 15u) : 0;
+        const int64_t end = off + a.N * EB;  // (VEC) bytes from the first vector
+        const int64_t slots = VEC ? (end + 15) >> 4 : a.N;
+        const int64_t k0 = seg * a.seg_slots;
+        const int64_t k1 = k0 + a.seg_slots < slots ? k0 + a.seg_slots : slots;
+        if (k0 >= k1) continue;
+        // The segment's columns.
+        const int64_t n0 = VEC ? (k0 == 0 ? 0 : (k0 * 16 - off) / EB) : k0;
+        const int64_t n1 = VEC ? (k1 == slots ? a.N : (k1 * 16 - off) / EB) : k1;
+
+        // The row's gradients (every warp for itself).
+        RowGrad g;
+        g.lse = __ldg(a.lse + row);
+        const int64_t t = a.grad_logprob ? __ldg(a.target + row) : -1;
+        const bool in_row = t >= 0 && t < a.N;
+        const float gl = in_row ? __ldg(a.grad_logprob + row) : 0.0f;
+        const float gs = a.grad_lse ? __ldg(a.grad_lse + row) : 0.0f;
+        g.gh = a.grad_entropy ? __ldg(a.grad_entropy + row) : 0.0f;
+        int64_t ti = -1;  // lane k: alternative k
+        float gt = 0.0f;
+        if (lane < a.K) {
+            ti = __ldg(a.top_index + row * a.K + lane);
+            if (ti < 0 || ti >= a.N) ti = -1;
+            else gt = __ldg(a.grad_top + row * a.K + lane);
         }
-        const float l = a.lse[row];
-        const float h = gh != 0.0f ? a.entropy[row] : 0.0f;
-        for (int64_t n = tid; n < a.N; n += kStatThreads) {
-            float d = 0.0f;
-            if (any) {
-                const float lp = load_elem<DT>(xr, n) - l;
-                const float p = ex2(lp * kLog2e);
-                d = p * (c - gh * (fmaxf(lp, kFarBelow) + h));
-                if (n == t) d += gl;
-                for (int k = 0; k < a.K; ++k)
-                    if (a.top_index[row * a.K + k] == n) d += a.grad_top[row * a.K + k];
-            }
-            put_elem<DT>(dr, n, d);
+        float sum = gt;
+        if (a.K > 0) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         }
+        const bool any = gl != 0.0f || gs != 0.0f || g.gh != 0.0f || __any_sync(0xffffffffu, gt != 0.0f);
+        if (!any) {
+            zero_slots<DT, TX, VEC>(dr, off, end, k0, k1, tid);
+            continue;  // (the same for the whole unit)
+        }
+        g.A = gs - gl - sum;
+        if (g.gh != 0.0f) g.A = fmaf(-g.gh, __ldg(a.entropy + row), g.A);
+
+        // The first warp keeps the elements with a unit term.
+        const bool first = tid < 32;
+        const bool mine = first && ti >= n0 && ti < n1;
+        float unit_term = 0.0f, x_mine = 0.0f, x_target = 0.0f;
+        bool target_alone = false;
+        if (first && a.K > 0) {
+            for (int k = 0; k < a.K; ++k) {
+                const int64_t ok = __shfl_sync(0xffffffffu, ti, k);
+                const float gk = __shfl_sync(0xffffffffu, gt, k);
+                if (ok == ti) unit_term += gk;
+            }
+            if (ti == t && in_row) unit_term += gl;
+            if (mine) x_mine = load_elem<DT>(xr, ti);
+        }
+        if (first && in_row && t >= n0 && t < n1) {
+            target_alone = !__any_sync(0xffffffffu, ti == t);
+            if (target_alone && lane == 0) x_target = load_elem<DT>(xr, t);
+        }
+        sync();
+        if (g.gh != 0.0f) grad_slots<DT, TX, VEC, true>(xr, dr, off, end, k0, k1, tid, g);
+        else grad_slots<DT, TX, VEC, false>(xr, dr, off, end, k0, k1, tid, g);
+        sync();
+        if (mine) put_elem<DT>(dr, ti, grad_elem(x_mine, g, unit_term));
+        if (target_alone && lane == 0) put_elem<DT>(dr, t, grad_elem(x_target, g, gl));
     }
 }
 
@@ -923,7 +1084,41 @@ cudaError_t launch_stats(StatsArgs a, int sms, cudaStream_t stream) {
     }
 }
 
-unsigned row_grid(int64_t B) { return static_cast<unsigned>(B < INT_MAX ? B : INT_MAX); }
+template <int DT, int TX, bool VEC>
+cudaError_t launch_stats_backward_tx(const StatsBackwardArgs& a, cudaStream_t stream) {
+    constexpr int64_t units_per_cta = TX == 32 ? kGradCta / 32 : 1;
+    const int64_t ctas = (a.B * a.segments + units_per_cta - 1) / units_per_cta;
+    return launch_pdl(lse_stats_backward_kernel<DT, TX, VEC>,
+                      dim3(static_cast<unsigned>(ctas < INT_MAX ? ctas : INT_MAX)), dim3(TX == 32 ? kGradCta : TX),
+                      stream, a);
+}
+
+// Vectors where each x row and its dx row sit at the same offset from a 16-byte
+// boundary, elements otherwise.  A warp per row of up to 256 slots, 128 threads up to
+// 1024, 256 beyond; longer rows in segments of up to 16 slots per thread, shorter
+// ones while the segments would not fill the GPU.
+template <int DT>
+cudaError_t launch_stats_backward(StatsBackwardArgs a, int sms, cudaStream_t stream) {
+    const int64_t eb = DType<DT>::bytes;
+    const uintptr_t xa = reinterpret_cast<uintptr_t>(a.x), da = reinterpret_cast<uintptr_t>(a.dx);
+    const bool vec = (xa - da) % 16 == 0 && ((a.row_stride - a.dx_row_stride) * eb) % 16 == 0;
+    const bool aligned = xa % 16 == 0 && (a.row_stride * eb) % 16 == 0;
+    const int64_t slots = vec ? (a.N * eb + 15) / 16 + (aligned ? 0 : 1) : a.N;  // at most
+    const int TX = slots <= 256 ? 32 : slots <= 1024 ? 128 : 256;
+    int64_t steps = 4;
+    while (TX > 32 && steps > 1 && a.B * ((slots + steps * kGradU * TX - 1) / (steps * kGradU * TX)) * TX < 1024LL * sms)
+        --steps;
+    a.seg_slots = TX == 32 ? slots : steps * kGradU * TX;
+    a.segments = (slots + a.seg_slots - 1) / a.seg_slots;
+    if (a.B > INT64_MAX / a.segments) return cudaErrorInvalidValue;
+    if (vec)
+        return TX == 32 ? launch_stats_backward_tx<DT, 32, true>(a, stream)
+               : TX == 128 ? launch_stats_backward_tx<DT, 128, true>(a, stream)
+                           : launch_stats_backward_tx<DT, 256, true>(a, stream);
+    return TX == 32 ? launch_stats_backward_tx<DT, 32, false>(a, stream)
+           : TX == 128 ? launch_stats_backward_tx<DT, 128, false>(a, stream)
+                       : launch_stats_backward_tx<DT, 256, false>(a, stream);
+}
 
 // The checks that the forward and the backward share beyond check_args.
 bool misaligned(const void* p, uintptr_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; }
@@ -1012,11 +1207,12 @@ lse_status lse_token_stats_backward(const void* x, lse_dtype dtype, int64_t B, i
     a.grad_lse = grad_lse;
     a.dx = dx;
     a.dx_row_stride = dx_row_stride;
-    const auto kernel = dtype == LSE_F32 ? lse_stats_backward_kernel<kF32>
-                        : dtype == LSE_BF16 ? lse_stats_backward_kernel<kBF16>
-                                            : lse_stats_backward_kernel<kF16>;
-    return cuda_status(launch_pdl(kernel, dim3(row_grid(B)), dim3(kStatThreads),
-                                  reinterpret_cast<cudaStream_t>(stream), a));
+    int sms = 0;
+    if ((st = device_sms(&sms)) != LSE_OK) return st;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return cuda_status(dtype == LSE_F32 ? launch_stats_backward<kF32>(a, sms, s)
+                       : dtype == LSE_BF16 ? launch_stats_backward<kBF16>(a, sms, s)
+                                           : launch_stats_backward<kF16>(a, sms, s));
 }
 
 }  // extern "C"
