@@ -4,12 +4,18 @@
 //     out[t, :]    = scale * table[ids[t], :]
 //     dtable[v, :] = scale * sum_{t : ids[t] = v} grad[t, :]
 //
-// The gradient sorts the tokens by id, stably, so that each table row's sum runs
-// over its tokens in their order: nothing is added through atomics, and equal
-// inputs give equal bits.
+// The gradient sorts the tokens by id, stably (least significant digit first), so
+// that each table row's sum runs over its tokens in their order.  The sorted tokens
+// are cut into tiles of equal length, whatever their ids, so a frequent token's rows
+// are summed by many CTAs at once: a run of one id inside a tile is summed and written
+// by it, a run that crosses tiles leaves one partial sum per tile, which a second
+// kernel adds up in order.  Nothing is added through floating-point atomics, and equal
+// inputs give equal bits.  Rows without a token are found in a bitmap and zeroed by
+// further CTAs of the summing kernel.
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 
 #include <cuda_runtime.h>
 
@@ -22,90 +28,474 @@ namespace {
 constexpr int kEmbedThreads = 256;
 
 template <int DT>
-__device__ __forceinline__ void put_elem(void* row, int64_t i, float v) {
-    if constexpr (DT == kF32) {
-        static_cast<float*>(row)[i] = v;
-    } else {
-        uint32_t r;
-        if constexpr (DT == kBF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(0.0f), "f"(v));
-        else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(0.0f), "f"(v));
-        static_cast<unsigned short*>(row)[i] = static_cast<unsigned short>(r);
-    }
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t r;
+    if constexpr (DT == kBF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kEmbedThreads)
-embed_kernel(const char* __restrict__ table, int64_t V, int64_t D, int64_t table_stride,
-             const int64_t* __restrict__ ids, int64_t T, float scale, char* __restrict__ out,
-             int64_t out_stride) {
-    pdl_trigger();
-    pdl_wait();
-    for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
-        const int64_t id = ids[t];
-        const bool in = id >= 0 && id < V;
-        for (int64_t d = threadIdx.x; d < D; d += kEmbedThreads)
-            put_elem<DT>(out + t * out_stride * DType<DT>::bytes, d,
-                         in ? load_elem<DT>(table + id * table_stride * DType<DT>::bytes, d) * scale
-                            : __int_as_float(0x7fc00000));
-    }
+__device__ __forceinline__ void put_elem(void* row, int64_t i, float v) {
+    if constexpr (DT == kF32) static_cast<float*>(row)[i] = v;
+    else static_cast<unsigned short*>(row)[i] = static_cast<unsigned short>(pack2<DT>(v, 0.0f));
 }
 
-// Sorted place of every token: the tokens with a lower id, or the same id and an
-// earlier place.  Tokens that add nothing sort last.
-__device__ __forceinline__ uint32_t sort_id(int64_t id, int64_t V, int64_t padding) {
-    return id >= 0 && id < V && id != padding ? static_cast<uint32_t>(id) : 0xffffffffu;
-}
-
-__global__ void __launch_bounds__(kEmbedThreads)
-rank_kernel(const int64_t* __restrict__ ids, int64_t T, int64_t V, int64_t padding,
-            uint32_t* __restrict__ sorted_id, uint32_t* __restrict__ sorted_at) {
-    pdl_trigger();
-    pdl_wait();
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kEmbedThreads + threadIdx.x; t < T;
-         t += static_cast<int64_t>(gridDim.x) * kEmbedThreads) {
-        const uint32_t mine = sort_id(ids[t], V, padding);
-        uint32_t place = 0;
-        for (int64_t j = 0; j < T; ++j) {
-            const uint32_t other = sort_id(__ldg(ids + j), V, padding);
-            place += other < mine || (other == mine && j < t);
+// The 4 or 8 elements of a 16-byte vector as f32 and back.
+template <int DT>
+__device__ __forceinline__ void unpack_vector(uint4 v, float (&x)[16 / DType<DT>::bytes]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (DT == kF32) {
+            x[i] = __uint_as_float(w[i]);
+        } else {
+            x[2 * i] = word_lo<DT>(w[i]);
+            x[2 * i + 1] = word_hi<DT>(w[i]);
         }
-        sorted_id[place] = mine;
-        sorted_at[place] = static_cast<uint32_t>(t);
+    }
+}
+template <int DT>
+__device__ __forceinline__ uint4 pack_vector(const float (&x)[16 / DType<DT>::bytes]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (DT == kF32) w[i] = __float_as_uint(x[i]);
+        else w[i] = pack2<DT>(x[2 * i], x[2 * i + 1]);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// ---------------------------------------------------------------------------
+// Lookup: a warp per token and segment of its row.
+// ---------------------------------------------------------------------------
+struct EmbedArgs {
+    const char* table;
+    int64_t V, D, table_stride;
+    const int64_t* ids;
+    int64_t T;
+    float scale;
+    char* out;
+    int64_t out_stride;
+    int64_t segments;  // per row, of 32 * U slots
+};
+
+// U slots per lane; a slot is a 16-byte vector (VEC: every row of both sides starts on
+// a 16-byte boundary and is a whole number of vectors) or an element.
+template <int DT, bool VEC, int U>
+__global__ void __launch_bounds__(kEmbedThreads)
+embed_kernel(const __grid_constant__ EmbedArgs a) {
+    constexpr int EB = DType<DT>::bytes, EPV = 16 / EB;
+    const int lane = threadIdx.x & 31;
+    const int64_t slots = VEC ? a.D / EPV : a.D;
+    pdl_trigger();
+    pdl_wait();
+    const int64_t units = a.T * a.segments;
+    for (int64_t unit = (static_cast<int64_t>(blockIdx.x) * kEmbedThreads + threadIdx.x) >> 5; unit < units;
+         unit += (static_cast<int64_t>(gridDim.x) * kEmbedThreads) >> 5) {
+        const int64_t t = unit / a.segments;
+        const int64_t k0 = (unit - t * a.segments) * (32 * U) + lane;
+        const int64_t id = __ldg(a.ids + t);
+        const bool in = id >= 0 && id < a.V;
+        const char* from = a.table + (in ? id : 0) * a.table_stride * EB;
+        char* to = a.out + t * a.out_stride * EB;
+        if constexpr (VEC) {
+            uint4 v[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (in && k0 + 32 * j < slots) v[j] = __ldg(reinterpret_cast<const uint4*>(from) + k0 + 32 * j);
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                if (k0 + 32 * j >= slots) continue;
+                float x[EPV];
+                if (in) unpack_vector<DT>(v[j], x);
+#pragma unroll
+                for (int i = 0; i < EPV; ++i) x[i] = in ? x[i] * a.scale : __int_as_float(0x7fc00000);
+                reinterpret_cast<uint4*>(to)[k0 + 32 * j] = pack_vector<DT>(x);
+            }
+        } else {
+            float v[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                v[j] = __int_as_float(0x7fc00000);
+                if (in && k0 + 32 * j < slots) v[j] = load_elem<DT>(from, k0 + 32 * j);
+            }
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (k0 + 32 * j < slots) put_elem<DT>(to, k0 + 32 * j, v[j] * a.scale);
+        }
     }
 }
 
-__device__ __forceinline__ int64_t lower_bound(const uint32_t* a, int64_t n, uint32_t v) {
-    int64_t lo = 0, hi = n;
+// ---------------------------------------------------------------------------
+// Sorting the tokens by id.  A block takes per_block tokens; a digit's counts per
+// block give every block its places, and a token's place follows from the tokens of
+// its digit before it: in earlier blocks, earlier warps of the block, earlier in the
+// warp.  The pass that moves the tokens also counts the next digit, for the blocks
+// that they arrive in.
+// ---------------------------------------------------------------------------
+constexpr int kSortThreads = 256;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortPer = 8;                            // tokens per thread and round
+constexpr int kSortRound = kSortThreads * kSortPer;    // tokens of a round
+constexpr int kSortMaxBits = 10;
+constexpr int kSortMaxBlocks = 256;
+
+struct SortArgs {
+    const int64_t* ids;
+    int T;
+    int64_t V, padding;
+    int block_shift;           // log2 of the tokens per block
+    int shift, bits;           // this pass's digit
+    int next_bits;             // 0: the last pass
+    const uint32_t* key_in;    // (passes after the first)
+    const uint32_t* at_in;
+    uint32_t* key_out;
+    uint32_t* at_out;
+    uint32_t* counts;          // [blocks][1 << bits]
+    uint32_t* next_counts;     // [blocks][1 << next_bits], zero before
+    uint32_t* bitmap;          // ids that occur
+};
+
+// Tokens that add nothing sort last.
+__device__ __forceinline__ uint32_t sort_key(int64_t id, int64_t V, int64_t padding) {
+    return static_cast<uint32_t>(id >= 0 && id < V && id != padding ? id : V);
+}
+
+// The first digit's counts; clears what later passes count into.
+__global__ void __launch_bounds__(kSortThreads)
+sort_count_kernel(const __grid_constant__ SortArgs a, uint32_t* clear, int64_t clear_words) {
+    __shared__ uint32_t count[1 << kSortMaxBits];
+    const int bins = 1 << a.bits;
+    pdl_trigger();
+    pdl_wait();
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kSortThreads + threadIdx.x; i < clear_words;
+         i += static_cast<int64_t>(gridDim.x) * kSortThreads)
+        clear[i] = 0;
+    for (int i = threadIdx.x; i < bins; i += kSortThreads) count[i] = 0;
+    __syncthreads();
+    const int64_t first = static_cast<int64_t>(blockIdx.x) << a.block_shift;
+    const int64_t past = first + (1LL << a.block_shift) < a.T ? first + (1LL << a.block_shift) : a.T;
+    for (int64_t i = first + threadIdx.x; i < past; i += kSortThreads)
+        atomicAdd(&count[sort_key(__ldg(a.ids + i), a.V, a.padding) & (bins - 1)], 1u);
+    __syncthreads();
+    for (int i = threadIdx.x; i < bins; i += kSortThreads)
+        a.counts[static_cast<int64_t>(blockIdx.x) * bins + i] = count[i];
+}
+
+template <bool FIRST>
+__global__ void __launch_bounds__(kSortThreads)
+sort_move_kernel(const __grid_constant__ SortArgs a) {
+    __shared__ uint32_t place[1 << kSortMaxBits];               // next place of each digit
+    __shared__ uint32_t by_warp[kSortWarps][1 << kSortMaxBits];
+    __shared__ uint32_t warp_sum[kSortWarps];
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const int bins = 1 << a.bits, mask = bins - 1;
+    pdl_trigger();
+    pdl_wait();
+
+    // place[d] = the tokens of lower digits, and of this digit in earlier blocks.
+    for (int d = tid; d < bins; d += kSortThreads) {
+        uint32_t before = 0, all = 0;
+        for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
+            const uint32_t c = a.counts[static_cast<int64_t>(b) * bins + d];
+            if (b < static_cast<int>(blockIdx.x)) before += c;
+            all += c;
+        }
+        place[d] = before;
+        by_warp[0][d] = all;
+    }
+    __syncthreads();
+    {
+        const int per = (bins + kSortThreads - 1) / kSortThreads;  // consecutive digits per thread
+        uint32_t mine = 0;
+        for (int i = 0; i < per; ++i)
+            if (tid * per + i < bins) mine += by_warp[0][tid * per + i];
+        uint32_t sum = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const uint32_t o = __shfl_up_sync(0xffffffffu, sum, off);
+            if (lane >= off) sum += o;
+        }
+        if (lane == 31) warp_sum[wid] = sum;
+        __syncthreads();
+        uint32_t run = sum - mine;
+        for (int w = 0; w < wid; ++w) run += warp_sum[w];
+        for (int i = 0; i < per; ++i)
+            if (tid * per + i < bins) {
+                place[tid * per + i] += run;
+                run += by_warp[0][tid * per + i];
+            }
+        __syncthreads();
+    }
+
+    const int64_t first = static_cast<int64_t>(blockIdx.x) << a.block_shift;
+    const int64_t past = first + (1LL << a.block_shift) < a.T ? first + (1LL << a.block_shift) : a.T;
+    for (int64_t start = first; start < past; start += kSortRound) {
+        for (int i = tid; i < kSortWarps * bins; i += kSortThreads) by_warp[i >> a.bits][i & mask] = 0;
+        __syncthreads();
+        uint32_t key[kSortPer], rank[kSortPer];
+        const int64_t at0 = start + wid * (32 * kSortPer) + lane;
+#pragma unroll
+        for (int j = 0; j < kSortPer; ++j) {
+            const int64_t i = at0 + 32 * j;
+            key[j] = 0;
+            if (i < past) key[j] = FIRST ? sort_key(__ldg(a.ids + i), a.V, a.padding) : a.key_in[i];
+        }
+#pragma unroll
+        for (int j = 0; j < kSortPer; ++j) {
+            const bool live = at0 + 32 * j < past;
+            const uint32_t d = live ? (key[j] >> a.shift) & mask : 0xffffffffu;
+            const uint32_t same = __match_any_sync(0xffffffffu, d);
+            uint32_t before = 0;
+            if (live) before = by_warp[wid][d];
+            __syncwarp();
+            if (live && lane == __ffs(same) - 1) by_warp[wid][d] = before + __popc(same);
+            __syncwarp();
+            rank[j] = before + __popc(same & ((1u << lane) - 1));
+        }
+        __syncthreads();
+        for (int d = tid; d < bins; d += kSortThreads) {
+            uint32_t run = place[d];
+#pragma unroll
+            for (int w = 0; w < kSortWarps; ++w) {
+                const uint32_t c = by_warp[w][d];
+                by_warp[w][d] = run;
+                run += c;
+            }
+            place[d] = run;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kSortPer; ++j) {
+            const int64_t i = at0 + 32 * j;
+            if (i >= past) continue;
+            const uint32_t to = by_warp[wid][(key[j] >> a.shift) & mask] + rank[j];
+            a.key_out[to] = key[j];
+            a.at_out[to] = FIRST ? static_cast<uint32_t>(i) : a.at_in[i];
+            if (a.next_bits > 0)
+                atomicAdd(&a.next_counts[((to >> a.block_shift) << a.next_bits) +
+                                         ((key[j] >> (a.shift + a.bits)) & ((1u << a.next_bits) - 1))], 1u);
+            if (FIRST && key[j] < a.V) atomicOr(&a.bitmap[key[j] >> 5], 1u << (key[j] & 31));
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Sums over the sorted tokens.
+// ---------------------------------------------------------------------------
+constexpr int kTile = 32;    // sorted tokens of a tile
+constexpr int kSumU = 8;     // rows of grad in flight per thread
+
+struct SumArgs {
+    const char* grad;
+    int64_t D, grad_stride;
+    const uint32_t* key;     // sorted ids; V for tokens that add nothing
+    const uint32_t* at;
+    int T;
+    int64_t V;
+    float scale;
+    char* dtable;
+    int64_t dtable_stride;
+    bool accumulate;
+    float* head;             // [tiles][D]: the sum of a tile's first run, when the run began before
+    float* tail;             // [tiles][D]: of its last run, when that begins here and goes on
+    int tiles;
+    int64_t slots;           // per row: 16-byte vectors or elements of grad
+    int64_t col_blocks;      // of blockDim.x slots
+    int64_t sum_ctas;        // CTAs before those that zero rows
+    const uint32_t* bitmap;  // null: no row has a token
+};
+
+template <int DT, bool VEC> struct Slot {
+    static constexpr int elems = VEC ? 16 / DType<DT>::bytes : 1;
+};
+
+// dtable's slot of row v: scale * sum, plus what was there.
+template <int DT, int OT, bool VEC>
+__device__ __forceinline__ void put_slot(const SumArgs& a, uint32_t v, int64_t slot, const float (&s)[Slot<DT, VEC>::elems]) {
+    constexpr int E = Slot<DT, VEC>::elems, OB = DType<OT>::bytes;
+    char* row = a.dtable + static_cast<int64_t>(v) * a.dtable_stride * OB;
+    float x[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[i] = s[i] * a.scale;
+    if constexpr (VEC) {
+        constexpr int OE = 16 / OB;  // elements per vector of dtable
+        uint4* to = reinterpret_cast<uint4*>(row + slot * E * OB);
+#pragma unroll
+        for (int q = 0; q < E / OE; ++q) {
+            float y[OE];
+            if (a.accumulate) unpack_vector<OT>(to[q], y);
+#pragma unroll
+            for (int i = 0; i < OE; ++i) y[i] = a.accumulate ? y[i] + x[q * OE + i] : x[q * OE + i];
+            to[q] = pack_vector<OT>(y);
+        }
+    } else {
+        if (a.accumulate) {
+            if constexpr (OT == kF32) x[0] += reinterpret_cast<const float*>(row)[slot];
+            else x[0] += load_elem<OT>(row, slot);
+        }
+        put_elem<OT>(row, slot, x[0]);
+    }
+}
+
+template <int DT, bool VEC>
+__device__ __forceinline__ void put_partial(float* to, const SumArgs& a, int tile, int64_t slot,
+                                            const float (&s)[Slot<DT, VEC>::elems]) {
+    constexpr int E = Slot<DT, VEC>::elems;
+    float* p = to + static_cast<int64_t>(tile) * a.D + slot * E;
+#pragma unroll
+    for (int i = 0; i < E; i += E >= 4 ? 4 : 1) {
+        if constexpr (E >= 4) *reinterpret_cast<float4*>(p + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+        else p[i] = s[i];
+    }
+}
+
+// blockDim = (slots of a column block, tiles of a CTA).
+template <int DT, int OT, bool VEC>
+__global__ void __launch_bounds__(kEmbedThreads, 4)
+embed_sum_kernel(const __grid_constant__ SumArgs a) {
+    constexpr int E = Slot<DT, VEC>::elems, EB = DType<DT>::bytes, OB = DType<OT>::bytes;
+    extern __shared__ uint32_t sm[];
+    const int tx = threadIdx.x, ty = threadIdx.y, TX = blockDim.x, TY = blockDim.y;
+    pdl_trigger();
+    pdl_wait();
+
+    if (blockIdx.x >= a.sum_ctas) {  // zero 32 rows' worth of rows without a token
+        const int64_t v0 = (static_cast<int64_t>(blockIdx.x) - a.sum_ctas) * 32;
+        const uint32_t present = a.bitmap ? a.bitmap[v0 >> 5] : 0u;
+        // Zeros need no unpacking: slots of 16 bytes of dtable, or its elements.
+        const int64_t slots = VEC ? a.D * OB / 16 : a.D;
+        const int threads = TX * TY;
+        for (int q = 0; q < 32; ++q) {
+            const int64_t v = v0 + q;
+            if (v >= a.V || ((present >> q) & 1u)) continue;
+            char* row = a.dtable + v * a.dtable_stride * OB;
+            for (int64_t k = ty * TX + tx; k < slots; k += threads) {
+                if constexpr (VEC) reinterpret_cast<uint4*>(row)[k] = make_uint4(0, 0, 0, 0);
+                else put_elem<OT>(row, k, 0.0f);
+            }
+        }
+        return;
+    }
+
+    const int64_t group = blockIdx.x / a.col_blocks;
+    const int64_t slot = (blockIdx.x - group * a.col_blocks) * TX + tx;
+    const int64_t tile0 = group * TY;
+    // Keys of the tiles with one neighbour on either side, and where the rows are.
+    uint32_t* key = sm + ty * (kTile + 2);
+    uint32_t* at = sm + TY * (kTile + 2) + ty * kTile;
+    const int64_t i0 = (tile0 + ty) * kTile;
+    for (int e = tx; e < kTile + 2; e += TX) {
+        const int64_t i = i0 + e - 1;
+        key[e] = i >= 0 && i < a.T ? a.key[i] : 0xffffffffu;  // (no id)
+        if (e < kTile) at[e] = i0 + e < a.T ? a.at[i0 + e] : 0u;
+    }
+    __syncthreads();
+    if (tile0 + ty >= a.tiles || slot >= a.slots) return;
+    const int tile = static_cast<int>(tile0 + ty);
+    const int n = a.T - i0 < kTile ? static_cast<int>(a.T - i0) : kTile;
+    const char* col = a.grad + slot * (E * EB);
+
+    float s[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) s[i] = 0.0f;
+    uint32_t run = key[1];
+    bool began_before = key[0] == run;
+    for (int e0 = 0; e0 < n; e0 += kSumU) {
+        float x[kSumU];
+        uint4 v[kSumU];
+#pragma unroll
+        for (int u = 0; u < kSumU; ++u) {
+            if (e0 + u >= n || key[e0 + u + 1] >= a.V) continue;
+            const char* p = col + static_cast<int64_t>(at[e0 + u]) * a.grad_stride * EB;
+            if constexpr (VEC) v[u] = ldg_stream16(p);
+            else x[u] = load_elem<DT>(p, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < kSumU; ++u) {
+            if (e0 + u >= n) break;
+            const uint32_t k = key[e0 + u + 1];
+            if (k != run) {
+                if (began_before) put_partial<DT, VEC>(a.head, a, tile, slot, s);
+                else if (run < a.V) put_slot<DT, OT, VEC>(a, run, slot, s);
+#pragma unroll
+                for (int i = 0; i < E; ++i) s[i] = 0.0f;
+                run = k;
+                began_before = false;
+            }
+            if (k >= a.V) break;  // (they sort last)
+            if constexpr (VEC) {
+                float y[E];
+                unpack_vector<DT>(v[u], y);
+#pragma unroll
+                for (int i = 0; i < E; ++i) s[i] += y[i];
+            } else {
+                s[0] += x[u];
+            }
+        }
+    }
+    if (run >= a.V) return;
+    if (began_before) put_partial<DT, VEC>(a.head, a, tile, slot, s);
+    else if (key[n + 1] == run) put_partial<DT, VEC>(a.tail, a, tile, slot, s);
+    else put_slot<DT, OT, VEC>(a, run, slot, s);
+}
+
+// Runs that cross tiles: the tile where the run begins adds the later tiles' sums to
+// its own.  TY groups of threads take equal parts of the tiles, then their sums are
+// added in order.
+template <int DT, int OT, bool VEC>
+__global__ void __launch_bounds__(kEmbedThreads)
+embed_join_kernel(const __grid_constant__ SumArgs a) {
+    constexpr int E = Slot<DT, VEC>::elems;
+    __shared__ float part[kEmbedThreads * E];
+    const int tx = threadIdx.x, ty = threadIdx.y, TX = blockDim.x, TY = blockDim.y;
+    pdl_trigger();
+    pdl_wait();
+    const int tile = static_cast<int>(blockIdx.x / a.col_blocks);
+    const int64_t slot = (blockIdx.x % a.col_blocks) * TX + tx;
+    const int64_t i0 = static_cast<int64_t>(tile) * kTile, i1 = i0 + kTile;
+    if (i1 >= a.T) return;  // (uniform, like the next two)
+    const uint32_t run = a.key[i1 - 1];
+    if (run >= a.V || a.key[i1] != run) return;
+    if (a.key[i0] == run && i0 > 0 && a.key[i0 - 1] == run) return;  // begins earlier
+    // The last tile whose first token is of this run.
+    int lo = tile + 1, hi = a.tiles - 1;
     while (lo < hi) {
-        const int64_t mid = (lo + hi) / 2;
-        if (a[mid] < v) lo = mid + 1;
-        else hi = mid;
+        const int mid = (lo + hi + 1) / 2;
+        if (a.key[static_cast<int64_t>(mid) * kTile] == run) lo = mid;
+        else hi = mid - 1;
     }
-    return lo;
-}
-
-template <int DT, int OT>
-__global__ void __launch_bounds__(kEmbedThreads)
-embed_backward_kernel(const char* __restrict__ grad, int64_t T, int64_t D, int64_t grad_stride,
-                      const uint32_t* __restrict__ sorted_id, const uint32_t* __restrict__ sorted_at,
-                      int64_t V, float scale, char* __restrict__ dtable, int64_t dtable_stride,
-                      bool accumulate) {
-    pdl_trigger();
-    pdl_wait();
-    for (int64_t v = blockIdx.x; v < V; v += gridDim.x) {
-        const int64_t i0 = lower_bound(sorted_id, T, static_cast<uint32_t>(v));
-        const int64_t i1 = lower_bound(sorted_id, T, static_cast<uint32_t>(v) + 1);
-        if (accumulate && i0 == i1) continue;
-        char* row = dtable + v * dtable_stride * DType<OT>::bytes;
-        for (int64_t d = threadIdx.x; d < D; d += kEmbedThreads) {
-            float s = 0.0f;
-            for (int64_t i = i0; i < i1; ++i)
-                s += load_elem<DT>(grad + static_cast<int64_t>(sorted_at[i]) * grad_stride * DType<DT>::bytes, d);
-            s *= scale;
-            if (accumulate) s += load_elem<OT>(row, d);
-            put_elem<OT>(row, d, s);
+    const int count = lo - tile;  // tiles tile + 1 .. lo
+    const int each = (count + TY - 1) / TY;
+    const int j0 = tile + 1 + ty * each;
+    const int j1 = j0 + each < lo + 1 ? j0 + each : lo + 1;
+    float s[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) s[i] = 0.0f;
+    if (slot < a.slots) {
+        if (ty == 0) {
+#pragma unroll
+            for (int i = 0; i < E; ++i) s[i] = a.tail[static_cast<int64_t>(tile) * a.D + slot * E + i];
+        }
+#pragma unroll 4
+        for (int j = j0; j < j1; ++j) {
+            const float* p = a.head + static_cast<int64_t>(j) * a.D + slot * E;
+#pragma unroll
+            for (int i = 0; i < E; ++i) s[i] += p[i];
         }
     }
+    const int t = ty * TX + tx;
+#pragma unroll
+    for (int i = 0; i < E; ++i) part[i * (TX * TY) + t] = s[i];
+    __syncthreads();
+    if (ty != 0 || slot >= a.slots) return;
+    for (int y = 1; y < TY; ++y) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) s[i] += part[i * (TX * TY) + y * TX + tx];
+    }
+    put_slot<DT, OT, VEC>(a, run, slot, s);
 }
 
 bool rows_ok(int64_t rows, int64_t D, int64_t stride, int64_t eb) {
@@ -119,6 +509,134 @@ bool valid_dtype(int dt) { return dt == LSE_F32 || dt == LSE_BF16 || dt == LSE_F
 bool misaligned(const void* p, uintptr_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; }
 
 unsigned capped(int64_t n, int64_t most) { return static_cast<unsigned>(n < 1 ? 1 : n < most ? n : most); }
+
+bool rows_aligned(const void* p, int64_t stride, int64_t eb) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (stride * eb) % 16 == 0;
+}
+
+template <int DT, bool VEC, int U>
+cudaError_t launch_embed_u(EmbedArgs a, cudaStream_t stream) {
+    const int64_t slots = VEC ? a.D / (16 / DType<DT>::bytes) : a.D;
+    a.segments = (slots + 32 * U - 1) / (32 * U);
+    const int64_t ctas = (a.T * a.segments * 32 + kEmbedThreads - 1) / kEmbedThreads;
+    return launch_pdl(embed_kernel<DT, VEC, U>, dim3(capped(ctas, INT_MAX)), dim3(kEmbedThreads), stream, a);
+}
+
+// One slot per lane for small calls, where latency counts; else as many loads in
+// flight as a warp's segment holds.
+template <int DT>
+cudaError_t launch_embed(const EmbedArgs& a, cudaStream_t stream) {
+    constexpr int eb = DType<DT>::bytes;
+    const bool vec = rows_aligned(a.table, a.table_stride, eb) && rows_aligned(a.out, a.out_stride, eb) &&
+                     (a.D * eb) % 16 == 0;
+    const int64_t slots = vec ? a.D * eb / 16 : a.D;
+    const bool small = a.T * slots <= 1 << 17;
+    if (vec) return small ? launch_embed_u<DT, true, 1>(a, stream) : launch_embed_u<DT, true, 4>(a, stream);
+    return small ? launch_embed_u<DT, false, 1>(a, stream) : launch_embed_u<DT, false, 8>(a, stream);
+}
+
+template <int DT, int OT, bool VEC>
+cudaError_t launch_sums(SumArgs a, cudaStream_t stream) {
+    a.slots = VEC ? a.D / Slot<DT, VEC>::elems : a.D;
+    int TX = 8;
+    while (TX < kEmbedThreads && TX < a.slots) TX *= 2;
+    const int TY = kEmbedThreads / TX;
+    a.col_blocks = (a.slots + TX - 1) / TX;
+    a.tiles = static_cast<int>((static_cast<int64_t>(a.T) + kTile - 1) / kTile);
+    a.sum_ctas = (a.tiles + TY - 1) / TY * a.col_blocks;
+    const int64_t ctas = a.sum_ctas + (a.accumulate ? 0 : (a.V + 31) / 32);
+    if (ctas > INT_MAX || a.tiles * a.col_blocks > INT_MAX) return cudaErrorInvalidValue;
+    cudaError_t e = cudaSuccess;
+    if (ctas > 0)
+        e = launch_pdl_smem(embed_sum_kernel<DT, OT, VEC>, dim3(static_cast<unsigned>(ctas)), dim3(TX, TY),
+                            sizeof(uint32_t) * TY * (2 * kTile + 2), stream, a);
+    if (e == cudaSuccess && a.tiles > 1)
+        e = launch_pdl(embed_join_kernel<DT, OT, VEC>, dim3(static_cast<unsigned>(a.tiles * a.col_blocks)),
+                       dim3(TX, TY), stream, a);
+    return e;
+}
+
+template <int DT>
+cudaError_t launch_sums_dt(const SumArgs& a, int out_dtype, cudaStream_t stream) {
+    const int64_t eb = DType<DT>::bytes, ob = out_dtype == LSE_F32 ? 4 : 2;
+    const bool vec = rows_aligned(a.grad, a.grad_stride, eb) && rows_aligned(a.dtable, a.dtable_stride, ob) &&
+                     (a.D * eb) % 16 == 0 && (a.D * ob) % 16 == 0;
+    if constexpr (DT != kF32) {
+        if (out_dtype != LSE_F32)
+            return vec ? launch_sums<DT, DT, true>(a, stream) : launch_sums<DT, DT, false>(a, stream);
+    }
+    return vec ? launch_sums<DT, kF32, true>(a, stream) : launch_sums<DT, kF32, false>(a, stream);
+}
+
+int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+lse_status embed_backward(SumArgs a, lse_dtype dtype, lse_dtype out_dtype, const int64_t* ids,
+                          int64_t padding, cudaStream_t stream) {
+    char* scratch = nullptr;
+    cudaError_t e = cudaSuccess;
+    if (a.T > 0) {
+        // Blocks of at least one round of tokens, at most kSortMaxBlocks of them.
+        SortArgs s;
+        std::memset(&s, 0, sizeof s);
+        s.ids = ids;
+        s.T = a.T;
+        s.V = a.V;
+        s.padding = padding;
+        s.block_shift = 11;
+        static_assert(kSortRound == 1 << 11, "a block holds whole rounds");
+        while ((static_cast<int64_t>(a.T) + (1LL << s.block_shift) - 1) >> s.block_shift > kSortMaxBlocks) ++s.block_shift;
+        const int blocks = static_cast<int>((static_cast<int64_t>(a.T) + (1LL << s.block_shift) - 1) >> s.block_shift);
+        int bits = 1;  // of keys 0 .. V
+        while (bits < 31 && (a.V >> bits) != 0) ++bits;
+        const int passes = (bits + kSortMaxBits - 1) / kSortMaxBits;
+        const int per = (bits + passes - 1) / passes;
+
+        const int64_t tiles = (static_cast<int64_t>(a.T) + kTile - 1) / kTile;
+        const int64_t list = round_up(static_cast<int64_t>(a.T) * 4, 256);
+        const int64_t counts = round_up((static_cast<int64_t>(blocks) << per) * 4, 256);
+        const int64_t bitmap = round_up((a.V + 31) / 32 * 4, 256);
+        const int64_t partial = round_up(tiles * a.D * 4, 256);
+        const lse_status st = take_scratch(reinterpret_cast<void**>(&scratch),
+                                           static_cast<size_t>(4 * list + passes * counts + bitmap + 2 * partial), stream);
+        if (st != LSE_OK) return st;
+        uint32_t* key[2] = {reinterpret_cast<uint32_t*>(scratch), reinterpret_cast<uint32_t*>(scratch + list)};
+        uint32_t* at[2] = {reinterpret_cast<uint32_t*>(scratch + 2 * list), reinterpret_cast<uint32_t*>(scratch + 3 * list)};
+        char* const count0 = scratch + 4 * list;
+        s.bitmap = reinterpret_cast<uint32_t*>(count0 + passes * counts);
+        a.head = reinterpret_cast<float*>(count0 + passes * counts + bitmap);
+        a.tail = reinterpret_cast<float*>(count0 + passes * counts + bitmap + partial);
+        a.bitmap = s.bitmap;
+
+        s.bits = per;
+        s.counts = reinterpret_cast<uint32_t*>(count0);
+        // (the later passes' counts and the bitmap lie behind the first pass's)
+        e = launch_pdl(sort_count_kernel, dim3(blocks), dim3(kSortThreads), stream, s,
+                       reinterpret_cast<uint32_t*>(count0 + counts), ((passes - 1) * counts + bitmap) / 4);
+        for (int p = 0; p < passes && e == cudaSuccess; ++p) {
+            s.shift = p * per;
+            s.next_bits = p + 1 < passes ? per : 0;
+            s.counts = reinterpret_cast<uint32_t*>(count0 + p * counts);
+            s.next_counts = reinterpret_cast<uint32_t*>(count0 + (p + 1) * counts);
+            s.key_in = key[(p + 1) & 1];
+            s.at_in = at[(p + 1) & 1];
+            s.key_out = key[p & 1];
+            s.at_out = at[p & 1];
+            e = p == 0 ? launch_pdl(sort_move_kernel<true>, dim3(blocks), dim3(kSortThreads), stream, s)
+                       : launch_pdl(sort_move_kernel<false>, dim3(blocks), dim3(kSortThreads), stream, s);
+        }
+        a.key = key[(passes - 1) & 1];
+        a.at = at[(passes - 1) & 1];
+    }
+    if (e == cudaSuccess)
+        e = dtype == LSE_F32 ? launch_sums_dt<kF32>(a, out_dtype, stream)
+            : dtype == LSE_BF16 ? launch_sums_dt<kBF16>(a, out_dtype, stream)
+                                : launch_sums_dt<kF16>(a, out_dtype, stream);
+    if (scratch) {
+        const cudaError_t ef = cudaFreeAsync(scratch, stream);
+        if (e == cudaSuccess) e = ef;
+    }
+    return cuda_status(e);
+}
 
 }  // namespace
 }  // namespace lse
@@ -136,12 +654,10 @@ lse_status lse_embedding(const void* table, lse_dtype dtype, int64_t V, int64_t 
     if (misaligned(table, eb) || misaligned(out, eb) || misaligned(ids, 8)) return LSE_ERR_INVALID_ARG;
     if (T == 0 || D == 0) return LSE_OK;
     if (ids == nullptr || out == nullptr || (V > 0 && table == nullptr)) return LSE_ERR_INVALID_ARG;
-    const auto kernel = dtype == LSE_F32 ? embed_kernel<kF32>
-                        : dtype == LSE_BF16 ? embed_kernel<kBF16> : embed_kernel<kF16>;
-    return cuda_status(launch_pdl(kernel, dim3(capped(T, INT_MAX)), dim3(kEmbedThreads),
-                                  reinterpret_cast<cudaStream_t>(stream),
-                                  static_cast<const char*>(table), V, D, table_stride, ids, T, scale,
-                                  static_cast<char*>(out), out_stride));
+    EmbedArgs a{static_cast<const char*>(table), V, D, table_stride, ids, T, scale, static_cast<char*>(out), out_stride, 1};
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return cuda_status(dtype == LSE_F32 ? launch_embed<kF32>(a, s)
+                       : dtype == LSE_BF16 ? launch_embed<kBF16>(a, s) : launch_embed<kF16>(a, s));
 }
 
 lse_status lse_embedding_backward(const void* grad, lse_dtype dtype, int64_t T, int64_t D,
@@ -156,26 +672,18 @@ lse_status lse_embedding_backward(const void* grad, lse_dtype dtype, int64_t T, 
     if (misaligned(grad, eb) || misaligned(dtable, ob) || misaligned(ids, 8)) return LSE_ERR_INVALID_ARG;
     if (V == 0 || D == 0) return LSE_OK;
     if (dtable == nullptr || (T > 0 && (grad == nullptr || ids == nullptr))) return LSE_ERR_INVALID_ARG;
-    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-    uint32_t* scratch = nullptr;
-    const lse_status st = take_scratch(reinterpret_cast<void**>(&scratch), sizeof(uint32_t) * 2 * (T + 1), stream);
-    if (st != LSE_OK) return st;
-    cudaError_t e = cudaSuccess;
-    if (T > 0)
-        e = launch_pdl(rank_kernel, dim3(capped((T + kEmbedThreads - 1) / kEmbedThreads, 65536)),
-                       dim3(kEmbedThreads), stream, ids, T, V, padding, scratch, scratch + T);
-    const auto kernel = dtype == LSE_F32 ? embed_backward_kernel<kF32, kF32>
-                        : dtype == LSE_BF16 ? (dtable_dtype == LSE_F32 ? embed_backward_kernel<kBF16, kF32>
-                                                                       : embed_backward_kernel<kBF16, kBF16>)
-                                            : (dtable_dtype == LSE_F32 ? embed_backward_kernel<kF16, kF32>
-                                                                       : embed_backward_kernel<kF16, kF16>);
-    if (e == cudaSuccess)
-        e = launch_pdl(kernel, dim3(capped(V, 1 << 20)), dim3(kEmbedThreads), stream,
-                       static_cast<const char*>(grad), T, D, grad_stride,
-                       static_cast<const uint32_t*>(scratch), static_cast<const uint32_t*>(scratch + T), V,
-                       scale, static_cast<char*>(dtable), dtable_stride, accumulate != 0);
-    const cudaError_t ef = cudaFreeAsync(scratch, stream);
-    return cuda_status(e == cudaSuccess ? ef : e);
+    SumArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.grad = static_cast<const char*>(grad);
+    a.D = D;
+    a.grad_stride = grad_stride;
+    a.T = static_cast<int>(T);
+    a.V = V;
+    a.scale = scale;
+    a.dtable = static_cast<char*>(dtable);
+    a.dtable_stride = dtable_stride;
+    a.accumulate = accumulate != 0;
+    return embed_backward(a, dtype, dtable_dtype, ids, padding, reinterpret_cast<cudaStream_t>(stream_));
 }
 
 }  // extern "C"
