@@ -128,6 +128,38 @@ embed_kernel(const __grid_constant__ EmbedArgs a) {
 }
 
 // ---------------------------------------------------------------------------
+// Zeroing table rows without a token, 32 rows (a word of the bitmap) per CTA.  These
+// CTAs ride along with kernels that leave the memory idle: the last sorting pass
+// (a few CTAs, bound by latency), the sums, the joins.
+// ---------------------------------------------------------------------------
+struct ZeroRows {
+    char* table;
+    int64_t row_bytes, stride_bytes, rows;
+    const uint32_t* bitmap;  // null: no row has a token
+    int64_t first;           // word of this launch's first CTA
+    int64_t words;           // CTAs of this launch
+    int unit;                // 16 (rows of whole, aligned 16-byte vectors), 4 or 2 bytes per store
+};
+
+__device__ __forceinline__ void zero_rows(const ZeroRows& z, int64_t cta, int tid, int threads) {
+    const int64_t word = z.first + cta;
+    const uint32_t present = z.bitmap ? z.bitmap[word] : 0u;
+    const int64_t units = z.row_bytes / z.unit;
+    for (int q = 0; q < 32; ++q) {
+        const int64_t v = word * 32 + q;
+        if (v >= z.rows) return;
+        if ((present >> q) & 1u) continue;
+        char* row = z.table + v * z.stride_bytes;
+        if (z.unit == 16)
+            for (int64_t k = tid; k < units; k += threads) __stcs(reinterpret_cast<uint4*>(row) + k, make_uint4(0, 0, 0, 0));
+        else if (z.unit == 4)
+            for (int64_t k = tid; k < units; k += threads) reinterpret_cast<uint32_t*>(row)[k] = 0u;
+        else
+            for (int64_t k = tid; k < units; k += threads) reinterpret_cast<unsigned short*>(row)[k] = 0;
+    }
+}
+
+// ---------------------------------------------------------------------------
 // Sorting the tokens by id.  A block takes per_block tokens; a digit's counts per
 // block give every block its places, and a token's place follows from the tokens of
 // its digit before it: in earlier blocks, earlier warps of the block, earlier in the
@@ -136,7 +168,7 @@ embed_kernel(const __grid_constant__ EmbedArgs a) {
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 256;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortPer = 8;                            // tokens per thread and round
+constexpr int kSortPer = 4;                            // tokens per thread and round
 constexpr int kSortRound = kSortThreads * kSortPer;    // tokens of a round
 constexpr int kSortMaxBits = 10;
 constexpr int kSortMaxBlocks = 256;
@@ -155,6 +187,8 @@ struct SortArgs {
     uint32_t* counts;          // [blocks][1 << bits]
     uint32_t* next_counts;     // [blocks][1 << next_bits], zero before
     uint32_t* bitmap;          // ids that occur
+    int blocks;                // sorting CTAs, before those that zero rows
+    ZeroRows zero;
 };
 
 // Tokens that add nothing sort last.
@@ -193,14 +227,24 @@ sort_move_kernel(const __grid_constant__ SortArgs a) {
     const int bins = 1 << a.bits, mask = bins - 1;
     pdl_trigger();
     pdl_wait();
+    if (static_cast<int>(blockIdx.x) >= a.blocks) {
+        if (!FIRST) zero_rows(a.zero, blockIdx.x - a.blocks, tid, kSortThreads);
+        return;
+    }
 
     // place[d] = the tokens of lower digits, and of this digit in earlier blocks.
     for (int d = tid; d < bins; d += kSortThreads) {
         uint32_t before = 0, all = 0;
-        for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
-            const uint32_t c = a.counts[static_cast<int64_t>(b) * bins + d];
-            if (b < static_cast<int>(blockIdx.x)) before += c;
-            all += c;
+        for (int b0 = 0; b0 < a.blocks; b0 += 16) {  // (16 loads in flight)
+            uint32_t c[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                c[i] = b0 + i < a.blocks ? a.counts[static_cast<int64_t>(b0 + i) * bins + d] : 0u;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                if (b0 + i < static_cast<int>(blockIdx.x)) before += c[i];
+                all += c[i];
+            }
         }
         place[d] = before;
         by_warp[0][d] = all;
@@ -234,13 +278,17 @@ sort_move_kernel(const __grid_constant__ SortArgs a) {
     for (int64_t start = first; start < past; start += kSortRound) {
         for (int i = tid; i < kSortWarps * bins; i += kSortThreads) by_warp[i >> a.bits][i & mask] = 0;
         __syncthreads();
-        uint32_t key[kSortPer], rank[kSortPer];
+        uint32_t key[kSortPer], from[kSortPer], rank[kSortPer];
         const int64_t at0 = start + wid * (32 * kSortPer) + lane;
 #pragma unroll
         for (int j = 0; j < kSortPer; ++j) {
             const int64_t i = at0 + 32 * j;
             key[j] = 0;
-            if (i < past) key[j] = FIRST ? sort_key(__ldg(a.ids + i), a.V, a.padding) : a.key_in[i];
+            from[j] = static_cast<uint32_t>(i);
+            if (i < past) {
+                key[j] = FIRST ? sort_key(__ldg(a.ids + i), a.V, a.padding) : a.key_in[i];
+                if (!FIRST) from[j] = a.at_in[i];
+            }
         }
 #pragma unroll
         for (int j = 0; j < kSortPer; ++j) {
@@ -272,7 +320,7 @@ sort_move_kernel(const __grid_constant__ SortArgs a) {
             if (i >= past) continue;
             const uint32_t to = by_warp[wid][(key[j] >> a.shift) & mask] + rank[j];
             a.key_out[to] = key[j];
-            a.at_out[to] = FIRST ? static_cast<uint32_t>(i) : a.at_in[i];
+            a.at_out[to] = from[j];
             if (a.next_bits > 0)
                 atomicAdd(&a.next_counts[((to >> a.block_shift) << a.next_bits) +
                                          ((key[j] >> (a.shift + a.bits)) & ((1u << a.next_bits) - 1))], 1u);
@@ -287,6 +335,9 @@ sort_move_kernel(const __grid_constant__ SortArgs a) {
 // ---------------------------------------------------------------------------
 constexpr int kTile = 32;    // sorted tokens of a tile
 constexpr int kSumU = 8;     // rows of grad in flight per thread
+// Bytes zeroed next to the last sorting pass and next to the joins (about 6 us each).
+constexpr int64_t kSortZeroBytes = 40 << 20;
+constexpr int64_t kJoinZeroBytes = 40 << 20;
 
 struct SumArgs {
     const char* grad;
@@ -305,7 +356,7 @@ struct SumArgs {
     int64_t slots;           // per row: 16-byte vectors or elements of grad
     int64_t col_blocks;      // of blockDim.x slots
     int64_t sum_ctas;        // CTAs before those that zero rows
-    const uint32_t* bitmap;  // null: no row has a token
+    ZeroRows zero;
 };
 
 template <int DT, bool VEC> struct Slot {
@@ -362,21 +413,8 @@ embed_sum_kernel(const __grid_constant__ SumArgs a) {
     pdl_trigger();
     pdl_wait();
 
-    if (blockIdx.x >= a.sum_ctas) {  // zero 32 rows' worth of rows without a token
-        const int64_t v0 = (static_cast<int64_t>(blockIdx.x) - a.sum_ctas) * 32;
-        const uint32_t present = a.bitmap ? a.bitmap[v0 >> 5] : 0u;
-        // Zeros need no unpacking: slots of 16 bytes of dtable, or its elements.
-        const int64_t slots = VEC ? a.D * OB / 16 : a.D;
-        const int threads = TX * TY;
-        for (int q = 0; q < 32; ++q) {
-            const int64_t v = v0 + q;
-            if (v >= a.V || ((present >> q) & 1u)) continue;
-            char* row = a.dtable + v * a.dtable_stride * OB;
-            for (int64_t k = ty * TX + tx; k < slots; k += threads) {
-                if constexpr (VEC) reinterpret_cast<uint4*>(row)[k] = make_uint4(0, 0, 0, 0);
-                else put_elem<OT>(row, k, 0.0f);
-            }
-        }
+    if (blockIdx.x >= a.sum_ctas) {
+        zero_rows(a.zero, blockIdx.x - a.sum_ctas, ty * TX + tx, TX * TY);
         return;
     }
 
@@ -453,6 +491,10 @@ embed_join_kernel(const __grid_constant__ SumArgs a) {
     const int tx = threadIdx.x, ty = threadIdx.y, TX = blockDim.x, TY = blockDim.y;
     pdl_trigger();
     pdl_wait();
+    if (blockIdx.x >= a.sum_ctas) {
+        zero_rows(a.zero, blockIdx.x - a.sum_ctas, ty * TX + tx, TX * TY);
+        return;
+    }
     const int tile = static_cast<int>(blockIdx.x / a.col_blocks);
     const int64_t slot = (blockIdx.x % a.col_blocks) * TX + tx;
     const int64_t i0 = static_cast<int64_t>(tile) * kTile, i1 = i0 + kTile;
@@ -479,7 +521,7 @@ embed_join_kernel(const __grid_constant__ SumArgs a) {
 #pragma unroll
             for (int i = 0; i < E; ++i) s[i] = a.tail[static_cast<int64_t>(tile) * a.D + slot * E + i];
         }
-#pragma unroll 4
+#pragma unroll 8
         for (int j = j0; j < j1; ++j) {
             const float* p = a.head + static_cast<int64_t>(j) * a.D + slot * E;
 #pragma unroll
@@ -538,22 +580,34 @@ cudaError_t launch_embed(const EmbedArgs& a, cudaStream_t stream) {
 template <int DT, int OT, bool VEC>
 cudaError_t launch_sums(SumArgs a, cudaStream_t stream) {
     a.slots = VEC ? a.D / Slot<DT, VEC>::elems : a.D;
+    a.tiles = static_cast<int>((static_cast<int64_t>(a.T) + kTile - 1) / kTile);
+    const bool join = a.tiles > 1;
+    // The rest of the words of rows to zero: a part for the joining kernel, if there is
+    // one, for which it would take about as long as its longest run.
+    ZeroRows rest = a.zero;
+    const int64_t row32 = a.zero.row_bytes * 32;
+    a.zero.words = join ? rest.words - (rest.words < kJoinZeroBytes / row32 ? rest.words : kJoinZeroBytes / row32) : rest.words;
     int TX = 8;
     while (TX < kEmbedThreads && TX < a.slots) TX *= 2;
     const int TY = kEmbedThreads / TX;
     a.col_blocks = (a.slots + TX - 1) / TX;
-    a.tiles = static_cast<int>((static_cast<int64_t>(a.T) + kTile - 1) / kTile);
     a.sum_ctas = (a.tiles + TY - 1) / TY * a.col_blocks;
-    const int64_t ctas = a.sum_ctas + (a.accumulate ? 0 : (a.V + 31) / 32);
-    if (ctas > INT_MAX || a.tiles * a.col_blocks > INT_MAX) return cudaErrorInvalidValue;
+    const int64_t ctas = a.sum_ctas + a.zero.words;
+    if (ctas > INT_MAX) return cudaErrorInvalidValue;
     cudaError_t e = cudaSuccess;
     if (ctas > 0)
         e = launch_pdl_smem(embed_sum_kernel<DT, OT, VEC>, dim3(static_cast<unsigned>(ctas)), dim3(TX, TY),
                             sizeof(uint32_t) * TY * (2 * kTile + 2), stream, a);
-    if (e == cudaSuccess && a.tiles > 1)
-        e = launch_pdl(embed_join_kernel<DT, OT, VEC>, dim3(static_cast<unsigned>(a.tiles * a.col_blocks)),
-                       dim3(TX, TY), stream, a);
-    return e;
+    if (e != cudaSuccess || !join) return e;
+    // Narrow column blocks, so that several groups of threads share a long run.
+    const int JX = TX < 32 ? TX : 32;
+    a.zero.first = rest.first + a.zero.words;
+    a.zero.words = rest.words - a.zero.words;
+    a.col_blocks = (a.slots + JX - 1) / JX;
+    a.sum_ctas = a.tiles * a.col_blocks;
+    if (a.sum_ctas + a.zero.words > INT_MAX) return cudaErrorInvalidValue;
+    return launch_pdl(embed_join_kernel<DT, OT, VEC>, dim3(static_cast<unsigned>(a.sum_ctas + a.zero.words)),
+                      dim3(JX, kEmbedThreads / JX), stream, a);
 }
 
 template <int DT>
@@ -574,6 +628,13 @@ lse_status embed_backward(SumArgs a, lse_dtype dtype, lse_dtype out_dtype, const
                           int64_t padding, cudaStream_t stream) {
     char* scratch = nullptr;
     cudaError_t e = cudaSuccess;
+    const int64_t ob = out_dtype == LSE_F32 ? 4 : 2;
+    a.zero.table = a.dtable;
+    a.zero.row_bytes = a.D * ob;
+    a.zero.stride_bytes = a.dtable_stride * ob;
+    a.zero.rows = a.V;
+    a.zero.words = a.accumulate ? 0 : (a.V + 31) / 32;
+    a.zero.unit = rows_aligned(a.dtable, a.dtable_stride, ob) && a.zero.row_bytes % 16 == 0 ? 16 : static_cast<int>(ob);
     if (a.T > 0) {
         // Blocks of at least one round of tokens, at most kSortMaxBlocks of them.
         SortArgs s;
@@ -582,8 +643,8 @@ lse_status embed_backward(SumArgs a, lse_dtype dtype, lse_dtype out_dtype, const
         s.T = a.T;
         s.V = a.V;
         s.padding = padding;
-        s.block_shift = 11;
-        static_assert(kSortRound == 1 << 11, "a block holds whole rounds");
+        s.block_shift = 10;
+        static_assert(kSortRound == 1 << 10, "a block holds whole rounds");
         while ((static_cast<int64_t>(a.T) + (1LL << s.block_shift) - 1) >> s.block_shift > kSortMaxBlocks) ++s.block_shift;
         const int blocks = static_cast<int>((static_cast<int64_t>(a.T) + (1LL << s.block_shift) - 1) >> s.block_shift);
         int bits = 1;  // of keys 0 .. V
@@ -605,7 +666,8 @@ lse_status embed_backward(SumArgs a, lse_dtype dtype, lse_dtype out_dtype, const
         s.bitmap = reinterpret_cast<uint32_t*>(count0 + passes * counts);
         a.head = reinterpret_cast<float*>(count0 + passes * counts + bitmap);
         a.tail = reinterpret_cast<float*>(count0 + passes * counts + bitmap + partial);
-        a.bitmap = s.bitmap;
+        a.zero.bitmap = s.bitmap;
+        s.blocks = blocks;
 
         s.bits = per;
         s.counts = reinterpret_cast<uint32_t*>(count0);
@@ -621,8 +683,19 @@ lse_status embed_backward(SumArgs a, lse_dtype dtype, lse_dtype out_dtype, const
             s.at_in = at[(p + 1) & 1];
             s.key_out = key[p & 1];
             s.at_out = at[p & 1];
-            e = p == 0 ? launch_pdl(sort_move_kernel<true>, dim3(blocks), dim3(kSortThreads), stream, s)
-                       : launch_pdl(sort_move_kernel<false>, dim3(blocks), dim3(kSortThreads), stream, s);
+            if (p == 0) {
+                e = launch_pdl(sort_move_kernel<true>, dim3(blocks), dim3(kSortThreads), stream, s);
+                continue;
+            }
+            if (p + 1 == passes) {  // the last pass zeroes the first rows
+                const int64_t words = kSortZeroBytes / (a.zero.row_bytes * 32);
+                s.zero = a.zero;
+                s.zero.words = words < a.zero.words ? words : a.zero.words;
+                a.zero.first = s.zero.words;
+                a.zero.words -= s.zero.words;
+            }
+            e = launch_pdl(sort_move_kernel<false>, dim3(static_cast<unsigned>(blocks + s.zero.words)),
+                           dim3(kSortThreads), stream, s);
         }
         a.key = key[(passes - 1) & 1];
         a.at = at[(passes - 1) & 1];

@@ -143,17 +143,33 @@ __device__ __forceinline__ double chunk_squares(const GradEntry& t, int64_t k0) 
     return bits == 0 ? 0.0 : squares_in_f64(t, k);
 }
 
-// The sum of a double over the CTA, in thread 0 (or, with a second use of `part`
-// ahead, in every thread after a barrier of the caller's).
+// The sum of a double over the CTA, in thread 0.  64-bit adds are few per clock on this
+// GPU, so only one warp takes the last steps.
 __device__ __forceinline__ double cta_sum(double s, double* part) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
     __syncthreads();
-    s = 0.0;
+    if (threadIdx.x < 32) {
+        s = threadIdx.x < kGradWarps ? part[threadIdx.x] : 0.0;
 #pragma unroll
-    for (int w = 0; w < kGradWarps; ++w) s += part[w];
+        for (int off = kGradWarps / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    }
     return s;
+}
+
+// sqrt(s) as f32: the mantissa's root in f32, the (even) exponent halved.  s is 0, or
+// at least 2^-298 (the smallest square), or infinite or NaN.
+__device__ __forceinline__ float root(double s) {
+    if (!(s > 0.0) || s > 1.0e300) return static_cast<float>(s);  // 0, NaN, inf
+    const int e = ((__double2hiint(s) >> 20) - 1023) & ~1;
+    const double two_e = __hiloint2double((1023 - e) << 20, 0);   // 2^-e
+    const float r = sqrtf(static_cast<float>(s * two_e));         // of [1, 4)
+    const int h = e / 2;                                          // -149 .. 498
+    // (in two factors: 2^h alone may be beyond f32)
+    const int h0 = h < -64 ? -64 : h > 64 ? 64 : h;
+    const int h1 = h - h0 > 127 ? 127 : h - h0;
+    return r * __int_as_float((127 + h0) << 23) * __int_as_float((127 + h1) << 23);
 }
 
 // partial[c] = the sum of CTA c's squares.
@@ -179,18 +195,25 @@ grad_square_kernel(const __grid_constant__ GradList<N> list, double* __restrict_
 }
 
 // The norm from n partial sums, the same in every thread of a CTA.
-__device__ __forceinline__ float norm_of(const double* partial, int64_t n, double* part) {
+struct NormShared {
+    double part[kGradWarps];
+    float norm;
+};
+__device__ __forceinline__ float norm_of(const double* partial, int64_t n, NormShared& sh) {
     double s = 0.0;
     for (int64_t i = threadIdx.x; i < n; i += kGradThreads) s += partial[i];
-    return static_cast<float>(sqrt(cta_sum(s, part)));
+    s = cta_sum(s, sh.part);
+    if (threadIdx.x == 0) sh.norm = root(s);
+    __syncthreads();
+    return sh.norm;
 }
 
 __global__ void __launch_bounds__(kGradThreads)
 grad_norm_kernel(const double* __restrict__ partial, int64_t n, float* __restrict__ norm) {
-    __shared__ double part[kGradWarps];
+    __shared__ NormShared sh;
     pdl_trigger();
     pdl_wait();
-    const float v = norm_of(partial, n, part);
+    const float v = norm_of(partial, n, sh);
     if (threadIdx.x == 0) norm[0] = v;
 }
 
@@ -241,7 +264,7 @@ __device__ __forceinline__ void chunk_scale(const GradEntry& t, int64_t k0, floa
                 }
             }
             if (vec && (kk > 0 || off == 0) && (kk + 1) * 16 <= end) {
-                *reinterpret_cast<uint4*>(o0 + kk * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+                __stcs(reinterpret_cast<uint4*>(o0 + kk * 16), make_uint4(o[0], o[1], o[2], o[3]));
             } else {
                 const int from = kk == 0 ? off : 0;
                 const int to = (kk + 1) * 16 > end ? static_cast<int>(end - kk * 16) : 16;
@@ -257,10 +280,10 @@ template <int N>
 __global__ void __launch_bounds__(kGradThreads, kGradCtas)
 grad_scale_kernel(const __grid_constant__ GradList<N> list, const double* __restrict__ partial, int64_t n,
                   float max_norm, float eps, float* __restrict__ norm) {
-    __shared__ double part[kGradWarps];
+    __shared__ NormShared sh;
     pdl_trigger();
     pdl_wait();
-    const float v = norm_of(partial, n, part);
+    const float v = norm_of(partial, n, sh);
     if (blockIdx.x == 0 && threadIdx.x == 0) norm[0] = v;
     const float c0 = max_norm / (v + eps);
     const float coef = c0 > 1.0f ? 1.0f : c0;  // NaN stays NaN
