@@ -128,25 +128,26 @@ embed_kernel(const __grid_constant__ EmbedArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Zeroing table rows without a token, 32 rows (a word of the bitmap) per CTA.  These
-// CTAs ride along with kernels that leave the memory idle: the last sorting pass
+// Zeroing table rows without a token, kZeroRows rows per CTA.  These CTAs ride along with kernels that leave the memory idle: the last sorting pass
 // (a few CTAs, bound by latency), the sums, the joins.
 // ---------------------------------------------------------------------------
+constexpr int kZeroRows = 8;
+
 struct ZeroRows {
     char* table;
     int64_t row_bytes, stride_bytes, rows;
     const uint32_t* bitmap;  // null: no row has a token
-    int64_t first;           // word of this launch's first CTA
-    int64_t words;           // CTAs of this launch
+    int64_t first;           // group of kZeroRows rows of this launch's first CTA
+    int64_t groups;          // CTAs of this launch
     int unit;                // 16 (rows of whole, aligned 16-byte vectors), 4 or 2 bytes per store
 };
 
 __device__ __forceinline__ void zero_rows(const ZeroRows& z, int64_t cta, int tid, int threads) {
-    const int64_t word = z.first + cta;
-    const uint32_t present = z.bitmap ? z.bitmap[word] : 0u;
+    const int64_t v0 = (z.first + cta) * kZeroRows;
+    const uint32_t present = z.bitmap ? z.bitmap[v0 >> 5] >> (v0 & 31) : 0u;
     const int64_t units = z.row_bytes / z.unit;
-    for (int q = 0; q < 32; ++q) {
-        const int64_t v = word * 32 + q;
+    for (int q = 0; q < kZeroRows; ++q) {
+        const int64_t v = v0 + q;
         if (v >= z.rows) return;
         if ((present >> q) & 1u) continue;
         char* row = z.table + v * z.stride_bytes;
@@ -203,8 +204,12 @@ sort_count_kernel(const __grid_constant__ SortArgs a, uint32_t* clear, int64_t c
     const int bins = 1 << a.bits;
     pdl_trigger();
     pdl_wait();
+    if (static_cast<int>(blockIdx.x) >= a.blocks) {
+        zero_rows(a.zero, blockIdx.x - a.blocks, threadIdx.x, kSortThreads);
+        return;
+    }
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kSortThreads + threadIdx.x; i < clear_words;
-         i += static_cast<int64_t>(gridDim.x) * kSortThreads)
+         i += static_cast<int64_t>(a.blocks) * kSortThreads)
         clear[i] = 0;
     for (int i = threadIdx.x; i < bins; i += kSortThreads) count[i] = 0;
     __syncthreads();
@@ -228,7 +233,7 @@ sort_move_kernel(const __grid_constant__ SortArgs a) {
     pdl_trigger();
     pdl_wait();
     if (static_cast<int>(blockIdx.x) >= a.blocks) {
-        if (!FIRST) zero_rows(a.zero, blockIdx.x - a.blocks, tid, kSortThreads);
+        zero_rows(a.zero, blockIdx.x - a.blocks, tid, kSortThreads);
         return;
     }
 
@@ -335,8 +340,10 @@ sort_move_kernel(const __grid_constant__ SortArgs a) {
 // ---------------------------------------------------------------------------
 constexpr int kTile = 32;    // sorted tokens of a tile
 constexpr int kSumU = 8;     // rows of grad in flight per thread
-// Bytes zeroed next to the last sorting pass and next to the joins (about 6 us each).
+// Bytes zeroed next to the sorting passes and next to the joins (about 6 us each).
+constexpr int64_t kCountZeroBytes = 8 << 20;
 constexpr int64_t kSortZeroBytes = 40 << 20;
+constexpr int64_t kJoinCtas = 608;  // four for each SM
 constexpr int64_t kJoinZeroBytes = 40 << 20;
 
 struct SumArgs {
@@ -350,6 +357,8 @@ struct SumArgs {
     char* dtable;
     int64_t dtable_stride;
     bool accumulate;
+    uint32_t* cross;         // tiles whose last run goes on, in any order
+    uint32_t* cross_count;
     float* head;             // [tiles][D]: the sum of a tile's first run, when the run began before
     float* tail;             // [tiles][D]: of its last run, when that begins here and goes on
     int tiles;
@@ -476,13 +485,33 @@ embed_sum_kernel(const __grid_constant__ SumArgs a) {
     }
     if (run >= a.V) return;
     if (began_before) put_partial<DT, VEC>(a.head, a, tile, slot, s);
-    else if (key[n + 1] == run) put_partial<DT, VEC>(a.tail, a, tile, slot, s);
+    else if (key[n + 1] == run) {
+        put_partial<DT, VEC>(a.tail, a, tile, slot, s);
+        if (slot == 0) a.cross[atomicAdd(a.cross_count, 1u)] = static_cast<uint32_t>(tile);
+    }
     else put_slot<DT, OT, VEC>(a, run, slot, s);
 }
 
-// Runs that cross tiles: the tile where the run begins adds the later tiles' sums to
-// its own.  TY groups of threads take equal parts of the tiles, then their sums are
-// added in order.
+template <int E>
+__device__ __forceinline__ void add_partial(float (&s)[E], const float* p) {
+    if constexpr (E >= 4) {
+#pragma unroll
+        for (int i = 0; i < E; i += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(p + i);
+            s[i] += v.x;
+            s[i + 1] += v.y;
+            s[i + 2] += v.z;
+            s[i + 3] += v.w;
+        }
+    } else {
+        s[0] += *p;
+    }
+}
+
+// Runs that cross tiles, listed by the tiles where they begin: the tile's own sum and
+// the later tiles'.  blockDim = (slots of a column block, groups): the groups take
+// equal parts of the tiles, then their sums are added in order.  The CTAs take
+// (run, column block) pairs in turn; further CTAs zero rows.
 template <int DT, int OT, bool VEC>
 __global__ void __launch_bounds__(kEmbedThreads)
 embed_join_kernel(const __grid_constant__ SumArgs a) {
@@ -495,49 +524,49 @@ embed_join_kernel(const __grid_constant__ SumArgs a) {
         zero_rows(a.zero, blockIdx.x - a.sum_ctas, ty * TX + tx, TX * TY);
         return;
     }
-    const int tile = static_cast<int>(blockIdx.x / a.col_blocks);
-    const int64_t slot = (blockIdx.x % a.col_blocks) * TX + tx;
-    const int64_t i0 = static_cast<int64_t>(tile) * kTile, i1 = i0 + kTile;
-    if (i1 >= a.T) return;  // (uniform, like the next two)
-    const uint32_t run = a.key[i1 - 1];
-    if (run >= a.V || a.key[i1] != run) return;
-    if (a.key[i0] == run && i0 > 0 && a.key[i0 - 1] == run) return;  // begins earlier
-    // The last tile whose first token is of this run.
-    int lo = tile + 1, hi = a.tiles - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (a.key[static_cast<int64_t>(mid) * kTile] == run) lo = mid;
-        else hi = mid - 1;
-    }
-    const int count = lo - tile;  // tiles tile + 1 .. lo
-    const int each = (count + TY - 1) / TY;
-    const int j0 = tile + 1 + ty * each;
-    const int j1 = j0 + each < lo + 1 ? j0 + each : lo + 1;
-    float s[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) s[i] = 0.0f;
-    if (slot < a.slots) {
-        if (ty == 0) {
-#pragma unroll
-            for (int i = 0; i < E; ++i) s[i] = a.tail[static_cast<int64_t>(tile) * a.D + slot * E + i];
-        }
-#pragma unroll 8
-        for (int j = j0; j < j1; ++j) {
-            const float* p = a.head + static_cast<int64_t>(j) * a.D + slot * E;
-#pragma unroll
-            for (int i = 0; i < E; ++i) s[i] += p[i];
-        }
-    }
     const int t = ty * TX + tx;
+    const int64_t units = static_cast<int64_t>(*a.cross_count) * a.col_blocks;
+    for (int64_t unit = blockIdx.x; unit < units; unit += a.sum_ctas) {
+        const int tile = static_cast<int>(a.cross[unit / a.col_blocks]);
+        const int64_t slot = unit % a.col_blocks * TX + tx;
+        const uint32_t run = a.key[static_cast<int64_t>(tile + 1) * kTile];
+        // The last tile whose first token is of this run: 32 tiles looked at in one go
+        // (most runs end in the next tile), then by halves.
+        const int look = tile + 2 + (t & 31);
+        const bool more = look < a.tiles && a.key[static_cast<int64_t>(look) * kTile] == run;
+        const uint32_t ends = ~__ballot_sync(0xffffffffu, more);
+        int lo = tile + 1 + (ends == 0 ? 32 : __ffs(ends) - 1);
+        if (ends == 0) {
+            int hi = a.tiles - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) / 2;
+                if (a.key[static_cast<int64_t>(mid) * kTile] == run) lo = mid;
+                else hi = mid - 1;
+            }
+        }
+        const int each = (lo - tile + TY - 1) / TY;  // of tiles tile + 1 .. lo
+        const int j0 = tile + 1 + ty * each;
+        const int j1 = j0 + each < lo + 1 ? j0 + each : lo + 1;
+        float s[E];
 #pragma unroll
-    for (int i = 0; i < E; ++i) part[i * (TX * TY) + t] = s[i];
-    __syncthreads();
-    if (ty != 0 || slot >= a.slots) return;
-    for (int y = 1; y < TY; ++y) {
+        for (int i = 0; i < E; ++i) s[i] = 0.0f;
+        if (slot < a.slots) {
+            if (ty == 0) add_partial<E>(s, a.tail + static_cast<int64_t>(tile) * a.D + slot * E);
+#pragma unroll 4
+            for (int j = j0; j < j1; ++j) add_partial<E>(s, a.head + static_cast<int64_t>(j) * a.D + slot * E);
+        }
 #pragma unroll
-        for (int i = 0; i < E; ++i) s[i] += part[i * (TX * TY) + y * TX + tx];
+        for (int i = 0; i < E; ++i) part[i * (TX * TY) + t] = s[i];
+        __syncthreads();
+        if (ty == 0 && slot < a.slots) {
+            for (int y = 1; y < TY && tile + 1 + y * each <= lo; ++y) {
+#pragma unroll
+                for (int i = 0; i < E; ++i) s[i] += part[i * (TX * TY) + y * TX + tx];
+            }
+            put_slot<DT, OT, VEC>(a, run, slot, s);
+        }
+        __syncthreads();
     }
-    put_slot<DT, OT, VEC>(a, run, slot, s);
 }
 
 bool rows_ok(int64_t rows, int64_t D, int64_t stride, int64_t eb) {
@@ -582,17 +611,17 @@ cudaError_t launch_sums(SumArgs a, cudaStream_t stream) {
     a.slots = VEC ? a.D / Slot<DT, VEC>::elems : a.D;
     a.tiles = static_cast<int>((static_cast<int64_t>(a.T) + kTile - 1) / kTile);
     const bool join = a.tiles > 1;
-    // The rest of the words of rows to zero: a part for the joining kernel, if there is
+    // The rest of the rows to zero: a part for the joining kernel, if there is
     // one, for which it would take about as long as its longest run.
     ZeroRows rest = a.zero;
-    const int64_t row32 = a.zero.row_bytes * 32;
-    a.zero.words = join ? rest.words - (rest.words < kJoinZeroBytes / row32 ? rest.words : kJoinZeroBytes / row32) : rest.words;
+    const int64_t late = kJoinZeroBytes / (a.zero.row_bytes * kZeroRows);
+    a.zero.groups = join ? rest.groups - (rest.groups < late ? rest.groups : late) : rest.groups;
     int TX = 8;
     while (TX < kEmbedThreads && TX < a.slots) TX *= 2;
     const int TY = kEmbedThreads / TX;
     a.col_blocks = (a.slots + TX - 1) / TX;
     a.sum_ctas = (a.tiles + TY - 1) / TY * a.col_blocks;
-    const int64_t ctas = a.sum_ctas + a.zero.words;
+    const int64_t ctas = a.sum_ctas + a.zero.groups;
     if (ctas > INT_MAX) return cudaErrorInvalidValue;
     cudaError_t e = cudaSuccess;
     if (ctas > 0)
@@ -601,12 +630,12 @@ cudaError_t launch_sums(SumArgs a, cudaStream_t stream) {
     if (e != cudaSuccess || !join) return e;
     // Narrow column blocks, so that several groups of threads share a long run.
     const int JX = TX < 32 ? TX : 32;
-    a.zero.first = rest.first + a.zero.words;
-    a.zero.words = rest.words - a.zero.words;
+    a.zero.first = rest.first + a.zero.groups;
+    a.zero.groups = rest.groups - a.zero.groups;
     a.col_blocks = (a.slots + JX - 1) / JX;
-    a.sum_ctas = a.tiles * a.col_blocks;
-    if (a.sum_ctas + a.zero.words > INT_MAX) return cudaErrorInvalidValue;
-    return launch_pdl(embed_join_kernel<DT, OT, VEC>, dim3(static_cast<unsigned>(a.sum_ctas + a.zero.words)),
+    a.sum_ctas = (a.tiles - 1) * a.col_blocks < kJoinCtas ? (a.tiles - 1) * a.col_blocks : kJoinCtas;
+    if (a.sum_ctas + a.zero.groups > INT_MAX) return cudaErrorInvalidValue;
+    return launch_pdl(embed_join_kernel<DT, OT, VEC>, dim3(static_cast<unsigned>(a.sum_ctas + a.zero.groups)),
                       dim3(JX, kEmbedThreads / JX), stream, a);
 }
 
@@ -624,6 +653,17 @@ cudaError_t launch_sums_dt(const SumArgs& a, int out_dtype, cudaStream_t stream)
 
 int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
+// The next groups of *from, as many as `bytes` cover, for a kernel to zero.
+ZeroRows take_zero_rows(ZeroRows* from, int64_t bytes, const uint32_t* bitmap) {
+    ZeroRows z = *from;
+    const int64_t groups = bytes / (z.row_bytes * kZeroRows);
+    z.groups = groups < z.groups ? groups : z.groups;
+    z.bitmap = bitmap;
+    from->first += z.groups;
+    from->groups -= z.groups;
+    return z;
+}
+
 lse_status embed_backward(SumArgs a, lse_dtype dtype, lse_dtype out_dtype, const int64_t* ids,
                           int64_t padding, cudaStream_t stream) {
     char* scratch = nullptr;
@@ -633,7 +673,7 @@ lse_status embed_backward(SumArgs a, lse_dtype dtype, lse_dtype out_dtype, const
     a.zero.row_bytes = a.D * ob;
     a.zero.stride_bytes = a.dtable_stride * ob;
     a.zero.rows = a.V;
-    a.zero.words = a.accumulate ? 0 : (a.V + 31) / 32;
+    a.zero.groups = a.accumulate ? 0 : (a.V + kZeroRows - 1) / kZeroRows;
     a.zero.unit = rows_aligned(a.dtable, a.dtable_stride, ob) && a.zero.row_bytes % 16 == 0 ? 16 : static_cast<int>(ob);
     if (a.T > 0) {
         // Blocks of at least one round of tokens, at most kSortMaxBlocks of them.
@@ -656,24 +696,32 @@ lse_status embed_backward(SumArgs a, lse_dtype dtype, lse_dtype out_dtype, const
         const int64_t list = round_up(static_cast<int64_t>(a.T) * 4, 256);
         const int64_t counts = round_up((static_cast<int64_t>(blocks) << per) * 4, 256);
         const int64_t bitmap = round_up((a.V + 31) / 32 * 4, 256);
+        const int64_t cross = round_up((tiles + 1) * 4, 256);
         const int64_t partial = round_up(tiles * a.D * 4, 256);
         const lse_status st = take_scratch(reinterpret_cast<void**>(&scratch),
-                                           static_cast<size_t>(4 * list + passes * counts + bitmap + 2 * partial), stream);
+                                           static_cast<size_t>(4 * list + passes * counts + bitmap + cross + 2 * partial), stream);
         if (st != LSE_OK) return st;
         uint32_t* key[2] = {reinterpret_cast<uint32_t*>(scratch), reinterpret_cast<uint32_t*>(scratch + list)};
         uint32_t* at[2] = {reinterpret_cast<uint32_t*>(scratch + 2 * list), reinterpret_cast<uint32_t*>(scratch + 3 * list)};
         char* const count0 = scratch + 4 * list;
         s.bitmap = reinterpret_cast<uint32_t*>(count0 + passes * counts);
-        a.head = reinterpret_cast<float*>(count0 + passes * counts + bitmap);
-        a.tail = reinterpret_cast<float*>(count0 + passes * counts + bitmap + partial);
+        char* const behind = count0 + passes * counts + bitmap;
+        a.cross_count = reinterpret_cast<uint32_t*>(behind);
+        a.cross = a.cross_count + 1;
+        a.head = reinterpret_cast<float*>(behind + cross);
+        a.tail = reinterpret_cast<float*>(behind + cross + partial);
         a.zero.bitmap = s.bitmap;
         s.blocks = blocks;
 
+        // Before the bitmap is known, rows are zeroed whether they have tokens or not:
+        // worth it while most have none.
+        const bool blind = 2 * static_cast<int64_t>(a.T) <= a.V;
         s.bits = per;
         s.counts = reinterpret_cast<uint32_t*>(count0);
-        // (the later passes' counts and the bitmap lie behind the first pass's)
-        e = launch_pdl(sort_count_kernel, dim3(blocks), dim3(kSortThreads), stream, s,
-                       reinterpret_cast<uint32_t*>(count0 + counts), ((passes - 1) * counts + bitmap) / 4);
+        s.zero = take_zero_rows(&a.zero, blind ? kCountZeroBytes : 0, nullptr);
+        // (behind the first pass's counts: the later passes', the bitmap, the list's length)
+        e = launch_pdl(sort_count_kernel, dim3(static_cast<unsigned>(blocks + s.zero.groups)), dim3(kSortThreads), stream,
+                       s, reinterpret_cast<uint32_t*>(count0 + counts), ((passes - 1) * counts + bitmap) / 4 + 1);
         for (int p = 0; p < passes && e == cudaSuccess; ++p) {
             s.shift = p * per;
             s.next_bits = p + 1 < passes ? per : 0;
@@ -683,19 +731,11 @@ lse_status embed_backward(SumArgs a, lse_dtype dtype, lse_dtype out_dtype, const
             s.at_in = at[(p + 1) & 1];
             s.key_out = key[p & 1];
             s.at_out = at[p & 1];
-            if (p == 0) {
-                e = launch_pdl(sort_move_kernel<true>, dim3(blocks), dim3(kSortThreads), stream, s);
-                continue;
-            }
-            if (p + 1 == passes) {  // the last pass zeroes the first rows
-                const int64_t words = kSortZeroBytes / (a.zero.row_bytes * 32);
-                s.zero = a.zero;
-                s.zero.words = words < a.zero.words ? words : a.zero.words;
-                a.zero.first = s.zero.words;
-                a.zero.words -= s.zero.words;
-            }
-            e = launch_pdl(sort_move_kernel<false>, dim3(static_cast<unsigned>(blocks + s.zero.words)),
-                           dim3(kSortThreads), stream, s);
+            s.zero = p == 0 ? take_zero_rows(&a.zero, blind ? kSortZeroBytes : 0, nullptr)
+                            : take_zero_rows(&a.zero, kSortZeroBytes, s.bitmap);
+            const dim3 grid(static_cast<unsigned>(blocks + s.zero.groups));
+            e = p == 0 ? launch_pdl(sort_move_kernel<true>, grid, dim3(kSortThreads), stream, s)
+                       : launch_pdl(sort_move_kernel<false>, grid, dim3(kSortThreads), stream, s);
         }
         a.key = key[(passes - 1) & 1];
         a.at = at[(passes - 1) & 1];
