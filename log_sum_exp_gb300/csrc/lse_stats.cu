@@ -267,6 +267,52 @@ __device__ __forceinline__ int64_t column_of(const Row& r, int64_t k, int i) {
 // everything masked with -inf) or a NaN are scanned once more in full.
 // ---------------------------------------------------------------------------
 
+// Packed 16-bit maxima; NaN lanes are ignored.  f32 maxima are kept as bf16, rounded
+// to nearest: rounding keeps the order, so what reaches a bound reaches the rounded
+// bound after it too.
+template <int DT>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    return DT == kF16 ? hmax2_f16(a, b) : hmax2_bf16(a, b);
+}
+template <int DT> __device__ __forceinline__ float half_lo(uint32_t w) { return word_lo<DT == kF16 ? kF16 : kBF16>(w); }
+template <int DT> __device__ __forceinline__ float half_hi(uint32_t w) { return word_hi<DT == kF16 ? kF16 : kBF16>(w); }
+template <int DT>
+__device__ __forceinline__ float round16(float x) {
+    return DT == kF32 ? word_lo<kBF16>(pack2<kBF16>(x, x)) : x;  // (16-bit elements are as they are)
+}
+
+// The maxima of the four pairs of neighbouring vectors of a batch of eight, and the
+// largest of all.
+template <int DT>
+__device__ __forceinline__ float batch_maxima(const uint32_t (&w)[32], uint2& maxima) {
+    if constexpr (DT == kF32) {
+        float c[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t* v = w + 8 * q;
+            c[q] = fmax3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
+            c[q] = fmax3(c[q], __uint_as_float(v[3]), __uint_as_float(v[4]));
+            c[q] = fmax3(c[q], __uint_as_float(v[5]), __uint_as_float(v[6]));
+            c[q] = fmaxf(c[q], __uint_as_float(v[7]));
+        }
+        maxima = make_uint2(pack2<kBF16>(c[0], c[1]), pack2<kBF16>(c[2], c[3]));
+        return fmax3(c[0], c[1], fmaxf(c[2], c[3]));
+    } else {
+        uint32_t c[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t* v = w + 8 * q;
+            c[q] = max2<DT>(max2<DT>(max2<DT>(v[0], v[1]), max2<DT>(v[2], v[3])),
+                            max2<DT>(max2<DT>(v[4], v[5]), max2<DT>(v[6], v[7])));
+        }
+        // Both halves of a pair of words at once.
+        maxima.x = max2<DT>(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[0], c[1], 0x7632));
+        maxima.y = max2<DT>(__byte_perm(c[2], c[3], 0x5410), __byte_perm(c[2], c[3], 0x7632));
+        const uint32_t m = max2<DT>(maxima.x, maxima.y);
+        return fmaxf(word_lo<DT>(m), word_hi<DT>(m));
+    }
+}
+
 // K-th largest of the G values of a group of G lanes (bitonic sort), K <= G.
 template <int G = 32>
 __device__ __forceinline__ float kth_largest(float v, int K, int lane) {
@@ -383,7 +429,9 @@ __device__ __forceinline__ V* cluster_map(V* p, uint32_t cta) {
 // Long rows: a CTA per row, or a cluster of CTAs that share one.
 // ---------------------------------------------------------------------------
 constexpr int kStatU = 8;         // vectors per thread and batch
-constexpr int kStatChunks = 16;   // chunk maxima kept per thread
+// A chunk is two vectors of a thread (and, in rows of more than kStatBatches batches,
+// the same two of 2^chunk_shift batches in a row); its maximum is kept in 16 bits.
+constexpr int kStatBatches = 16;
 constexpr int kChunkList = 64;    // chunks that a warp may read again
 constexpr int kMaxCluster = 16;
 constexpr int kUnitsPerCta = 8;   // one-warp rows per CTA
@@ -391,9 +439,9 @@ constexpr int kPartKeys = 48;     // keys that a part hands on as it found them
 
 template <int T, bool CLUSTER>
 struct StatsShared {
-    static constexpr int kFoundList = T == 32 ? 192 : 512;  // elements that may reach the bound
+    static constexpr int kFoundList = T == 32 ? 128 : 512;  // elements that may reach the bound
     float4 group_max4[8];
-    alignas(16) float chunk_max[kStatChunks * T];
+    alignas(16) uint2 chunk_max[kStatBatches * T];
     uint64_t found[kFoundList];
     uint64_t own[kMaxTopK];
     // In the cluster's first CTA: the parts' keys, how many, their accumulators, and
@@ -444,11 +492,12 @@ lse_stats_kernel(const __grid_constant__ StatsArgs a) {
     if (tid == 0) sh.founds = sh.overflow = 0;
     if (CLUSTER && tid < kMaxTopK) sh.own[tid] = 0;
 
-    // The row, in batches of U vectors per thread; a chunk is 2^chunk_shift of them.
+    // The row, in batches of U vectors per thread.
     StatAcc acc = stat_identity();
     {
         Shift shift = make_shift<DT>(acc.m);
-        float chunk_max = acc.m;
+        constexpr uint32_t low16 = DT == kF16 ? kNegInfF16x2 : kNegInfBF16x2;
+        uint2 chunk_max = make_uint2(low16, low16);
         int chunk = 0, in_chunk = 0;
         for (int64_t k = k_begin + tid; k - tid < k_end; k += U * T) {
             uint32_t w[4 * U];
@@ -468,16 +517,18 @@ lse_stats_kernel(const __grid_constant__ StatsArgs a) {
                     if (k + j * T == 0 || k + j * T == r.vectors - 1) mask_vector<DT>(r, k + j * T, &w[4 * j]);
                 }
             }
-            const float cm = words_max<DT, 4 * U>(w);
+            uint2 maxima;
+            const float cm = batch_maxima<DT>(w, maxima);
             if (cm > acc.m) {
                 acc = stat_shift<DT>(acc, cm);
                 shift = make_shift<DT>(cm);
             }
             stat_add_words<DT, 4 * U>(acc, shift, w);
-            chunk_max = fmaxf(chunk_max, cm);
+            chunk_max.x = max2<DT>(chunk_max.x, maxima.x);
+            chunk_max.y = max2<DT>(chunk_max.y, maxima.y);
             if (++in_chunk == 1 << a.chunk_shift) {
                 sh.chunk_max[chunk * T + tid] = chunk_max;
-                chunk_max = __int_as_float(kNegInfF32);
+                chunk_max = make_uint2(low16, low16);
                 in_chunk = 0;
                 ++chunk;
             }
@@ -519,45 +570,52 @@ lse_stats_kernel(const __grid_constant__ StatsArgs a) {
         const float bound = kth_largest_of(group_max, a.K, lane);
         bool scan = nan || bound == __int_as_float(kNegInfF32);  // NaN, or too few left
         if (!scan && warp_max >= bound) {
-            const int per_shift = 3 + a.chunk_shift;  // log2 of a chunk's vectors
-            const int chunks = static_cast<int>((k_end - k_begin + (static_cast<int64_t>(T) << per_shift) - 1) >> per_shift) / T;
-            int n = 0;
+            const int batches = static_cast<int>((k_end - k_begin + U * T - 1) / (U * T));
+            const int groups = (batches + (1 << a.chunk_shift) - 1) >> a.chunk_shift;
+            // The thread's chunks that reach the bound, a bit each; then one of them per
+            // lane and round goes to the warp's list.
+            uint64_t flags = 0;
+            const float bound16 = round16<DT>(bound);
 #pragma unroll 4
-            for (int c = 0; c < chunks; ++c) {
-                const bool in = sh.chunk_max[c * T + tid] >= bound;
-                const uint32_t who = __ballot_sync(0xffffffffu, in);
+            for (int c = 0; c < groups; ++c) {
+                const uint2 m = sh.chunk_max[c * T + tid];
+                const uint32_t f = (half_lo<DT>(m.x) >= bound16 ? 1u : 0u) | (half_hi<DT>(m.x) >= bound16 ? 2u : 0u) |
+                                   (half_lo<DT>(m.y) >= bound16 ? 4u : 0u) | (half_hi<DT>(m.y) >= bound16 ? 8u : 0u);
+                flags |= static_cast<uint64_t>(f) << (4 * c);
+            }
+            int n = 0;
+            for (uint32_t who; (who = __ballot_sync(0xffffffffu, flags != 0)) != 0; n += __popc(who)) {
+                if (flags == 0) continue;
+                const int c = __ffsll(static_cast<long long>(flags)) - 1;
+                flags &= flags - 1;
                 const int at = n + __popc(who & ((1u << lane) - 1));
-                if (in && at < kChunkList) sh.chunk[wid][at] = static_cast<int16_t>(c * 32 + lane);
-                n += __popc(who);
+                if (at < kChunkList) sh.chunk[wid][at] = static_cast<int16_t>(c * 32 + lane);
             }
             if (n > kChunkList) {
                 n = 0;
                 sh.overflow = 1;
             }
             __syncwarp();
-            const int items = n << per_shift;
-            // Two vectors of the chunks per lane and round.
-            for (int i0 = 0; i0 < items; i0 += 64) {
-                uint32_t w[8];
-                uint32_t col[2];  // of each vector's first element (wraps below the row's first)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int i = i0 + 32 * h + lane;
-                    const int c = i < items ? sh.chunk[wid][i >> per_shift] : 0;
-                    // (a part's vectors fit 32 bits: N does)
-                    const int k = ((c >> 5) << per_shift) * T + wid * 32 + (c & 31) + (i & ((1 << per_shift) - 1)) * T;
-                    load_vector<DT>(r, k_begin + k, i < items ? k_end : 0, &w[4 * h]);
-                    col[h] = static_cast<uint32_t>(column_of<DT>(r, k_begin + k, 0));
-                }
+            const int item_shift = 1 + a.chunk_shift;  // log2 of a chunk's vectors
+            const int items = n << item_shift;
+            // A vector of the chunks per lane and round.
+            for (int i0 = 0; i0 < items; i0 += 32) {
+                const int i = i0 + lane;
+                const int c = i < items ? sh.chunk[wid][i >> item_shift] : 0;
+                const int e0 = i & ((1 << item_shift) - 1);  // which of the chunk's vectors
+                // (a part's vectors fit 32 bits: N does)
+                const int batch = ((c >> 7) << a.chunk_shift) + (e0 >> 1);
+                const int k = (batch * U + ((c >> 5) & 3) * 2 + (e0 & 1)) * T + wid * 32 + (c & 31);
+                uint32_t w[4];
+                load_vector<DT>(r, k_begin + k, i < items ? k_end : 0, w);
+                const uint32_t col = static_cast<uint32_t>(column_of<DT>(r, k_begin + k, 0));  // (wraps before the row)
                 uint32_t mine = 0;
 #pragma unroll
-                for (int e = 0; e < 2 * EPV; ++e)
-                    mine |= (word_elem<DT>(&w[e / EPV * 4], e % EPV) >= bound ? 1u : 0u) << e;
-                const uint32_t inside = static_cast<uint32_t>(a.N) - EPV;
-                if (col[0] > inside || col[1] > inside) {  // the row's ends: elements outside it
+                for (int e = 0; e < EPV; ++e) mine |= (word_elem<DT>(w, e) >= bound ? 1u : 0u) << e;
+                if (col > static_cast<uint32_t>(a.N) - EPV) {  // the row's ends: elements outside it
 #pragma unroll
-                    for (int e = 0; e < 2 * EPV; ++e)
-                        if (col[e / EPV] + e % EPV >= a.N) mine &= ~(1u << e);
+                    for (int e = 0; e < EPV; ++e)
+                        if (col + e >= a.N) mine &= ~(1u << e);
                 }
                 const int total = __reduce_add_sync(0xffffffffu, __popc(mine));
                 if (total == 0) continue;
@@ -569,8 +627,7 @@ lse_stats_kernel(const __grid_constant__ StatsArgs a) {
                     const int e = __ffs(mine) - 1;
                     mine &= mine - 1;
                     const int place = at + __popc(who & ((1u << lane) - 1));
-                    if (place < kFoundList)
-                        sh.found[place] = topk_key(pick_elem<DT, 8>(w, e), (e < EPV ? col[0] : col[1] - EPV) + e);
+                    if (place < kFoundList) sh.found[place] = topk_key(pick_elem<DT, 4>(w, e), col + e);
                 }
             }
         }
@@ -631,7 +688,7 @@ lse_stats_kernel(const __grid_constant__ StatsArgs a) {
         }
         if (a.K == 0) return;
         // Of the parts' keys, those that reach the bound of the whole row.
-        static_assert(kMaxCluster * kPartKeys * 8 <= kStatChunks * 128 * 4 && kPartKeys % 16 == 0, "whole warps");
+        static_assert(kMaxCluster * kPartKeys <= kStatBatches * 128 && kPartKeys % 16 == 0, "whole warps");
         uint64_t* reached = reinterpret_cast<uint64_t*>(sh.chunk_max);  // (no longer needed)
         if (tid == 0) sh.founds = 0;
         const float bound = kth_largest_of(reinterpret_cast<const float*>(sh.cluster_max4), a.K, lane);
@@ -660,15 +717,51 @@ constexpr int kShortThreads = 256;
 constexpr int kShortWarps = kShortThreads / 32;
 constexpr int kShortFound = 192;  // elements of a warp's rows that may reach their bounds
 
+// Keys of short rows: f32 ones as elsewhere; a 16-bit element's fits 32 bits, its
+// ordered bits above the complement of its column (< 2^16).  No NaN comes here.
+template <int DT> struct ShortKey {
+    using type = uint32_t;
+    static __device__ __forceinline__ uint32_t make(const char* p, int column) {
+        uint32_t b = *reinterpret_cast<const unsigned short*>(p);
+        if (b == 0x8000u) b = 0;  // -0
+        return ((b ^ ((b & 0x8000u) ? 0xffffu : 0x8000u)) << 16) | (0xffffu - static_cast<uint32_t>(column));
+    }
+    static __device__ __forceinline__ float value(uint32_t k) {
+        const uint32_t o = k >> 16;
+        return word_lo<DT>(o ^ ((o & 0x8000u) ? 0x8000u : 0xffffu));
+    }
+    static __device__ __forceinline__ int64_t column(uint32_t k) { return 0xffff - static_cast<int>(k & 0xffffu); }
+};
+template <> struct ShortKey<kF32> {
+    using type = uint64_t;
+    static __device__ __forceinline__ uint64_t make(const char* p, int column) {
+        return topk_key(*reinterpret_cast<const float*>(p), static_cast<uint32_t>(column));
+    }
+    static __device__ __forceinline__ float value(uint64_t k) { return key_value(k); }
+    static __device__ __forceinline__ int64_t column(uint64_t k) { return key_column(k); }
+};
+
+template <bool WIDE> struct ShortBits {
+    using type = uint32_t;
+    static __device__ __forceinline__ int first(uint32_t b) { return __ffs(static_cast<int>(b)) - 1; }
+};
+template <> struct ShortBits<true> {
+    using type = uint64_t;
+    static __device__ __forceinline__ int first(uint64_t b) { return __ffsll(static_cast<long long>(b)) - 1; }
+};
+
 template <int DT, int G, int V>
 __global__ void __launch_bounds__(kShortThreads, V <= 4 ? 5 : V <= 6 ? 4 : 3)
 lse_stats_short_kernel(const __grid_constant__ StatsArgs a) {
     constexpr int EB = DType<DT>::bytes, EPV = 16 / EB, RPW = 32 / G;
-    constexpr int kCap = kShortFound / RPW;  // per row
-    __shared__ uint64_t found_all[kShortWarps][kShortFound];
+    constexpr int kCap = kShortFound / RPW - 4;  // per row (and room for empty keys after the last)
+    using Key = typename ShortKey<DT>::type;
+    __shared__ uint4 stage_all[kShortWarps][32 * V];  // the warp's vectors, to be picked from
+    __shared__ alignas(16) Key found_all[kShortWarps][kShortFound];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const int sub = lane & (G - 1), group = lane / G;
-    uint64_t* found = found_all[wid] + group * kCap;
+    uint4* const stage = stage_all[wid];
+    Key* const found = found_all[wid] + group * (kShortFound / RPW);
     pdl_trigger();
     pdl_wait();
     for (int64_t row0 = (static_cast<int64_t>(blockIdx.x) * kShortWarps + wid) * RPW; row0 < a.B;
@@ -730,40 +823,49 @@ lse_stats_short_kernel(const __grid_constant__ StatsArgs a) {
         bool scan = acc.s != acc.s || bound == __int_as_float(kNegInfF32);
         // Which of the lane's elements reach the bound, one bit each; then one of them
         // per lane and round goes to the row's list, in turn within the round.
-        uint64_t mine = 0;
+        using Bits = typename ShortBits<(V * EPV > 32)>::type;
+        Bits mine = 0;
 #pragma unroll
         for (int i = 0; i < V * EPV; ++i)
-            mine |= static_cast<uint64_t>(word_elem<DT>(&w[i / EPV * 4], i % EPV) >= bound) << i;
+            mine |= static_cast<Bits>(word_elem<DT>(&w[i / EPV * 4], i % EPV) >= bound ? 1 : 0) << i;
         if (scan || !live) mine = 0;
+#pragma unroll
+        for (int j = 0; j < V; ++j) stage[32 * j + lane] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
         int n = 0;
         const int column0 = (sub * 16 - off) / EB;
         const uint32_t group_bits = G == 32 ? 0xffffffffu : ((1u << (G & 31)) - 1) << (group * G);
         const uint32_t before = group_bits & ((1u << lane) - 1);
         for (uint32_t who; (who = __ballot_sync(0xffffffffu, mine != 0)) != 0;) {
             if (mine != 0) {
-                const int i = __ffsll(static_cast<long long>(mine)) - 1;
+                const int i = ShortBits<(V * EPV > 32)>::first(mine);
                 mine &= mine - 1;
                 const int at = n + __popc(who & before);
-                if (at < kCap) found[at] = static_cast<uint64_t>(column0 + (i / EPV) * (G * EPV) + i % EPV);
+                if (at < kCap)
+                    found[at] = ShortKey<DT>::make(reinterpret_cast<const char*>(stage + 32 * (i / EPV) + lane) + i % EPV * EB,
+                                                   column0 + (i / EPV) * (G * EPV) + i % EPV);
             }
             n += __popc(who & group_bits);
         }
         scan |= n > kCap;
-        __syncwarp();
-        if (!scan) {  // the values again, from L1
-            for (int i = sub; i < n; i += G) {
-                const int col = static_cast<int>(found[i]);
-                found[i] = topk_key(load_elem<DT>(rp, col), static_cast<uint32_t>(col));
-            }
-        }
+        if (!scan && sub < 4) found[n + sub] = 0;
         __syncwarp();
         if (!scan) {
+            constexpr int PER = 16 / sizeof(Key);  // keys per load
             for (int i = sub; i < n; i += G) {
-                const uint64_t key = found[i];
+                const Key key = found[i];
                 int rank = 0;
-#pragma unroll 4
-                for (int j = 0; j < n; ++j) rank += found[j] > key;
-                if (rank < a.K) put_top(a, row, rank, key, rs);
+                for (int j = 0; j < n; j += PER) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(found + j);
+                    if constexpr (PER == 4) {
+                        rank += (v.x > key) + (v.y > key) + (v.z > key) + (v.w > key);
+                    } else {
+                        rank += ((static_cast<uint64_t>(v.y) << 32 | v.x) > key) + ((static_cast<uint64_t>(v.w) << 32 | v.z) > key);
+                    }
+                }
+                if (rank < a.K) {
+                    a.top_index[row * a.K + rank] = ShortKey<DT>::column(key);
+                    a.top_logprob[row * a.K + rank] = stat_logprob(ShortKey<DT>::value(key), rs);
+                }
             }
         }
         // Rows that need the scan, by the whole warp in turn.
@@ -1059,28 +1161,26 @@ cudaError_t launch_stats(StatsArgs a, int sms, cudaStream_t stream) {
     }
     // Threads of a CTA: enough for one batch of the row each; at most 128 when rows
     // are plentiful, so that rows at their ends overlap with rows under way.
-    int T = 512;
+    int T = 256;
     while (T > 128 && vectors < 2LL * kStatU * T) T /= 2;
     if (a.B >= 4LL * sms) T = 128;
     // Rows of up to 1024 vectors by the thousand: a warp each.
-    if (vectors <= 1024 && a.B >= 16LL * sms) T = 32;
+    if (vectors <= 1024 && a.B >= 16LL * sms && a.K <= 24) T = 32;
     int P = 1;
     if (a.B < sms) {
         while (P < kMaxCluster && a.B * P * 2 <= 2LL * sms && vectors >= 2LL * P * kStatU * 128) P *= 2;
         while (T > 128 && vectors < 1LL * P * kStatU * T) T /= 2;
     }
-    if (P > 1 && T > 256) T = 256;
     a.cluster = P;
     const int64_t batches = ((vectors + P - 1) / P + kStatU * T - 1) / (kStatU * T);
-    while ((batches + (1LL << a.chunk_shift) - 1) >> a.chunk_shift > kStatChunks) ++a.chunk_shift;
+    while ((batches + (1LL << a.chunk_shift) - 1) >> a.chunk_shift > kStatBatches) ++a.chunk_shift;
     if (P > 1) {
         return T == 128 ? launch_stats_long<DT, 128, true>(a, stream) : launch_stats_long<DT, 256, true>(a, stream);
     }
     switch (T) {
     case 32: return launch_stats_long<DT, 32, false>(a, stream);
     case 128: return launch_stats_long<DT, 128, false>(a, stream);
-    case 256: return launch_stats_long<DT, 256, false>(a, stream);
-    default: return launch_stats_long<DT, 512, false>(a, stream);
+    default: return launch_stats_long<DT, 256, false>(a, stream);
     }
 }
 

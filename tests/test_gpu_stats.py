@@ -462,3 +462,14 @@ def test_refusals():
             call()
     with pytest.raises(TypeError):
         L.lse_token_stats(x.double())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("N,K", [(1500, 20), (2311, 8), (4000, 24), (4103, 1), (8191, 0), (5003, 32)])
+def test_special_rows_by_the_thousand(dtype, N, K):
+    """Many rows of middling length take a mapping of their own."""
+    x = special_rows(N, dtype, seed=N)
+    x = x.repeat(2600 // x.shape[0] + 1, 1)
+    t = torch.randint(0, N, (x.shape[0],), generator=torch.Generator().manual_seed(N))
+    xd = place(x, offset=1, row_stride=N + 3)
+    check(xd, x, t, K)
