@@ -281,34 +281,39 @@ __device__ __forceinline__ float round16(float x) {
     return DT == kF32 ? word_lo<kBF16>(pack2<kBF16>(x, x)) : x;  // (16-bit elements are as they are)
 }
 
-// The maxima of the four pairs of neighbouring vectors of a batch of eight, and the
-// largest of all.
-template <int DT>
-__device__ __forceinline__ float batch_maxima(const uint32_t (&w)[32], uint2& maxima) {
+// The maxima of the U / 2 pairs of neighbouring vectors of a batch, two per word, and
+// the largest of all.
+template <int DT, int U>
+__device__ __forceinline__ float batch_maxima(const uint32_t (&w)[4 * U], uint32_t (&maxima)[U / 4]) {
+    float all[U / 4];
+#pragma unroll
+    for (int h = 0; h < U / 4; ++h) {
+        const uint32_t* const v = w + 16 * h;  // two pairs
+        if constexpr (DT == kF32) {
+            float c[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                c[q] = fmax3(__uint_as_float(v[8 * q]), __uint_as_float(v[8 * q + 1]), __uint_as_float(v[8 * q + 2]));
+                c[q] = fmax3(c[q], __uint_as_float(v[8 * q + 3]), __uint_as_float(v[8 * q + 4]));
+                c[q] = fmax3(c[q], __uint_as_float(v[8 * q + 5]), __uint_as_float(v[8 * q + 6]));
+                c[q] = fmaxf(c[q], __uint_as_float(v[8 * q + 7]));
+            }
+            maxima[h] = pack2<kBF16>(c[0], c[1]);
+            all[h] = fmaxf(c[0], c[1]);
+        } else {
+            uint32_t c[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                c[q] = max2<DT>(max2<DT>(max2<DT>(v[8 * q], v[8 * q + 1]), max2<DT>(v[8 * q + 2], v[8 * q + 3])),
+                                max2<DT>(max2<DT>(v[8 * q + 4], v[8 * q + 5]), max2<DT>(v[8 * q + 6], v[8 * q + 7])));
+            // Both halves of the two words at once.
+            maxima[h] = max2<DT>(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[0], c[1], 0x7632));
+        }
+    }
     if constexpr (DT == kF32) {
-        float c[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const uint32_t* v = w + 8 * q;
-            c[q] = fmax3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
-            c[q] = fmax3(c[q], __uint_as_float(v[3]), __uint_as_float(v[4]));
-            c[q] = fmax3(c[q], __uint_as_float(v[5]), __uint_as_float(v[6]));
-            c[q] = fmaxf(c[q], __uint_as_float(v[7]));
-        }
-        maxima = make_uint2(pack2<kBF16>(c[0], c[1]), pack2<kBF16>(c[2], c[3]));
-        return fmax3(c[0], c[1], fmaxf(c[2], c[3]));
+        return U == 4 ? all[0] : fmaxf(all[0], all[U / 4 - 1]);
     } else {
-        uint32_t c[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const uint32_t* v = w + 8 * q;
-            c[q] = max2<DT>(max2<DT>(max2<DT>(v[0], v[1]), max2<DT>(v[2], v[3])),
-                            max2<DT>(max2<DT>(v[4], v[5]), max2<DT>(v[6], v[7])));
-        }
-        // Both halves of a pair of words at once.
-        maxima.x = max2<DT>(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[0], c[1], 0x7632));
-        maxima.y = max2<DT>(__byte_perm(c[2], c[3], 0x5410), __byte_perm(c[2], c[3], 0x7632));
-        const uint32_t m = max2<DT>(maxima.x, maxima.y);
+        const uint32_t m = U == 4 ? maxima[0] : max2<DT>(maxima[0], maxima[U / 4 - 1]);
         return fmaxf(word_lo<DT>(m), word_hi<DT>(m));
     }
 }
@@ -328,17 +333,21 @@ __device__ __forceinline__ float kth_largest(float v, int K, int lane) {
     return __shfl_sync(0xffffffffu, v, K - 1, G);
 }
 
-// The same for 32 values in shared memory (16-byte aligned): the smallest of those
-// that fewer than K exceed.
-__device__ __forceinline__ float kth_largest_of(const float* v32, int K, int lane) {
-    const float v = v32[lane];
-    int above = 0;
+// The same for M = 32 or 64 values in shared memory (16-byte aligned): the smallest of
+// those that fewer than K exceed.
+template <int M>
+__device__ __forceinline__ float kth_largest_of(const float* values, int K, int lane) {
+    const float v = values[lane], u = M > 32 ? values[lane + M - 32] : 0.0f;
+    int above_v = 0, above_u = 0;
 #pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-        const float4 o = *reinterpret_cast<const float4*>(v32 + j);
-        above += (o.x > v) + (o.y > v) + (o.z > v) + (o.w > v);
+    for (int j = 0; j < M; j += 4) {
+        const float4 o = *reinterpret_cast<const float4*>(values + j);
+        above_v += (o.x > v) + (o.y > v) + (o.z > v) + (o.w > v);
+        if (M > 32) above_u += (o.x > u) + (o.y > u) + (o.z > u) + (o.w > u);
     }
-    return order_value(__reduce_min_sync(0xffffffffu, above < K ? order_bits(v) : 0xffffffffu));
+    uint32_t least = above_v < K ? order_bits(v) : 0xffffffffu;
+    if (M > 32 && above_u < K) least = min(least, order_bits(u));
+    return order_value(__reduce_min_sync(0xffffffffu, least));
 }
 
 // Element e of W / 4 vectors held in registers, e not known at compile time.
@@ -428,10 +437,15 @@ __device__ __forceinline__ V* cluster_map(V* p, uint32_t cta) {
 // ---------------------------------------------------------------------------
 // Long rows: a CTA per row, or a cluster of CTAs that share one.
 // ---------------------------------------------------------------------------
-constexpr int kStatU = 8;         // vectors per thread and batch
-// A chunk is two vectors of a thread (and, in rows of more than kStatBatches batches,
-// the same two of 2^chunk_shift batches in a row); its maximum is kept in 16 bits.
-constexpr int kStatBatches = 16;
+// Vectors per thread and batch: eight; four in one-warp rows, which are short, so that
+// less of the last batch is empty.
+__host__ __device__ constexpr int stat_u(int T) { return T == 32 ? 4 : 8; }
+// A chunk is two vectors of a thread (and, in rows of more batches than maxima are kept
+// of, the same two of 2^chunk_shift batches in a row); its maximum is kept in 16 bits.
+__host__ __device__ constexpr int stat_batches(int T) { return 128 / stat_u(T); }
+// The bound is taken from the maxima of 32 groups of threads, or of 64 for larger K,
+// for which 32 would let many more elements through (K = 32: about 130 against 44).
+constexpr int kWideGroupsK = 24;
 constexpr int kChunkList = 64;    // chunks that a warp may read again
 constexpr int kMaxCluster = 16;
 constexpr int kUnitsPerCta = 8;   // one-warp rows per CTA
@@ -440,8 +454,8 @@ constexpr int kPartKeys = 48;     // keys that a part hands on as it found them
 template <int T, bool CLUSTER>
 struct StatsShared {
     static constexpr int kFoundList = T == 32 ? 128 : 512;  // elements that may reach the bound
-    float4 group_max4[8];
-    alignas(16) uint2 chunk_max[kStatBatches * T];
+    float4 group_max4[T > 32 ? 16 : 8];
+    alignas(16) uint32_t chunk_max[stat_u(T) / 4 * stat_batches(T) * T];
     uint64_t found[kFoundList];
     uint64_t own[kMaxTopK];
     // In the cluster's first CTA: the parts' keys, how many, their accumulators, and
@@ -457,12 +471,18 @@ struct StatsShared {
     int overflow;
 };
 
+template <int W>
+__device__ __forceinline__ void put_words(uint32_t* to, const uint32_t (&v)[W]) {
+    if constexpr (W == 2) *reinterpret_cast<uint2*>(to) = make_uint2(v[0], v[1]);
+    else *to = v[0];
+}
+
 // T threads per row: a CTA, or (32) one of the kUnitsPerCta warps of a CTA, which then
 // need no barrier and overlap one row's end with other rows' loads.
 template <int DT, int T, bool CLUSTER>
 __global__ void __launch_bounds__(T == 32 ? 32 * kUnitsPerCta : T, T == 32 ? 32 / kUnitsPerCta : 1024 / T)
 lse_stats_kernel(const __grid_constant__ StatsArgs a) {
-    constexpr int U = kStatU, NW = T / 32, EPV = 16 / DType<DT>::bytes, UNITS = T == 32 ? kUnitsPerCta : 1;
+    constexpr int U = stat_u(T), MW = U / 4, NW = T / 32, EPV = 16 / DType<DT>::bytes, UNITS = T == 32 ? kUnitsPerCta : 1;
     __shared__ StatsShared<T, CLUSTER> sh_units[UNITS];
     StatsShared<T, CLUSTER>& sh = sh_units[UNITS > 1 ? threadIdx.x / 32 : 0];
     constexpr int kFoundList = StatsShared<T, CLUSTER>::kFoundList;
@@ -497,7 +517,9 @@ lse_stats_kernel(const __grid_constant__ StatsArgs a) {
     {
         Shift shift = make_shift<DT>(acc.m);
         constexpr uint32_t low16 = DT == kF16 ? kNegInfF16x2 : kNegInfBF16x2;
-        uint2 chunk_max = make_uint2(low16, low16);
+        uint32_t chunk_max[MW];
+#pragma unroll
+        for (int h = 0; h < MW; ++h) chunk_max[h] = low16;
         int chunk = 0, in_chunk = 0;
         for (int64_t k = k_begin + tid; k - tid < k_end; k += U * T) {
             uint32_t w[4 * U];
@@ -517,28 +539,32 @@ lse_stats_kernel(const __grid_constant__ StatsArgs a) {
                     if (k + j * T == 0 || k + j * T == r.vectors - 1) mask_vector<DT>(r, k + j * T, &w[4 * j]);
                 }
             }
-            uint2 maxima;
-            const float cm = batch_maxima<DT>(w, maxima);
+            uint32_t maxima[MW];
+            const float cm = batch_maxima<DT, U>(w, maxima);
             if (cm > acc.m) {
                 acc = stat_shift<DT>(acc, cm);
                 shift = make_shift<DT>(cm);
             }
             stat_add_words<DT, 4 * U>(acc, shift, w);
-            chunk_max.x = max2<DT>(chunk_max.x, maxima.x);
-            chunk_max.y = max2<DT>(chunk_max.y, maxima.y);
+#pragma unroll
+            for (int h = 0; h < MW; ++h) chunk_max[h] = max2<DT>(chunk_max[h], maxima[h]);
             if (++in_chunk == 1 << a.chunk_shift) {
-                sh.chunk_max[chunk * T + tid] = chunk_max;
-                chunk_max = make_uint2(low16, low16);
+                put_words<MW>(sh.chunk_max + (chunk * T + tid) * MW, chunk_max);
+#pragma unroll
+                for (int h = 0; h < MW; ++h) chunk_max[h] = low16;
                 in_chunk = 0;
                 ++chunk;
             }
         }
-        if (in_chunk > 0) sh.chunk_max[chunk * T + tid] = chunk_max;
+        if (in_chunk > 0) put_words<MW>(sh.chunk_max + (chunk * T + tid) * MW, chunk_max);
     }
-    float warp_max = acc.m;  // on the way to it, the maximum of NW neighbouring threads
+    // The warp's maximum, and on the way to it those of `apart` neighbouring threads.
+    const bool wide = T > 32 && a.K > kWideGroupsK;
+    const int apart = wide ? NW / 2 : NW;
+    float warp_max = acc.m;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        if (off == NW && tid % NW == 0) group_max[tid / NW] = warp_max;  // (NW = 1: each lane's own)
+        if (off == apart && tid % apart == 0) group_max[tid / apart] = warp_max;
         warp_max = fmaxf(warp_max, __shfl_xor_sync(0xffffffffu, warp_max, off));
     }
     acc = stat_shift<DT>(acc, warp_max);
@@ -567,7 +593,8 @@ lse_stats_kernel(const __grid_constant__ StatsArgs a) {
     }
 
     if (a.K > 0) {
-        const float bound = kth_largest_of(group_max, a.K, lane);
+        const float bound = wide ? kth_largest_of<T == 32 ? 32 : 64>(group_max, a.K, lane)
+                                 : kth_largest_of<32>(group_max, a.K, lane);
         bool scan = nan || bound == __int_as_float(kNegInfF32);  // NaN, or too few left
         if (!scan && warp_max >= bound) {
             const int batches = static_cast<int>((k_end - k_begin + U * T - 1) / (U * T));
@@ -578,10 +605,13 @@ lse_stats_kernel(const __grid_constant__ StatsArgs a) {
             const float bound16 = round16<DT>(bound);
 #pragma unroll 4
             for (int c = 0; c < groups; ++c) {
-                const uint2 m = sh.chunk_max[c * T + tid];
-                const uint32_t f = (half_lo<DT>(m.x) >= bound16 ? 1u : 0u) | (half_hi<DT>(m.x) >= bound16 ? 2u : 0u) |
-                                   (half_lo<DT>(m.y) >= bound16 ? 4u : 0u) | (half_hi<DT>(m.y) >= bound16 ? 8u : 0u);
-                flags |= static_cast<uint64_t>(f) << (4 * c);
+                uint32_t f = 0;
+#pragma unroll
+                for (int h = 0; h < MW; ++h) {
+                    const uint32_t m = sh.chunk_max[(c * T + tid) * MW + h];
+                    f |= (half_lo<DT>(m) >= bound16 ? 1u : 0u) << (2 * h) | (half_hi<DT>(m) >= bound16 ? 2u : 0u) << (2 * h);
+                }
+                flags |= static_cast<uint64_t>(f) << (2 * MW * c);
             }
             int n = 0;
             for (uint32_t who; (who = __ballot_sync(0xffffffffu, flags != 0)) != 0; n += __popc(who)) {
@@ -604,8 +634,9 @@ lse_stats_kernel(const __grid_constant__ StatsArgs a) {
                 const int c = i < items ? sh.chunk[wid][i >> item_shift] : 0;
                 const int e0 = i & ((1 << item_shift) - 1);  // which of the chunk's vectors
                 // (a part's vectors fit 32 bits: N does)
-                const int batch = ((c >> 7) << a.chunk_shift) + (e0 >> 1);
-                const int k = (batch * U + ((c >> 5) & 3) * 2 + (e0 & 1)) * T + wid * 32 + (c & 31);
+                const int pair = (c >> 5) % (U / 2);
+                const int batch = ((c >> 5) / (U / 2) << a.chunk_shift) + (e0 >> 1);
+                const int k = (batch * U + pair * 2 + (e0 & 1)) * T + wid * 32 + (c & 31);
                 uint32_t w[4];
                 load_vector<DT>(r, k_begin + k, i < items ? k_end : 0, w);
                 const uint32_t col = static_cast<uint32_t>(column_of<DT>(r, k_begin + k, 0));  // (wraps before the row)
@@ -660,8 +691,9 @@ lse_stats_kernel(const __grid_constant__ StatsArgs a) {
         if (tid < count) cluster_map(sh.keys, 0)[seg * kPartKeys + tid] = from[tid];
         if (tid == 0) cluster_map(sh.key_count, 0)[seg] = count;
         if (tid >= T - 32 && lane < 32 / P) {  // its threads in 32 / P groups
-            float m = group_max[lane * P];
-            for (int i = 1; i < P; ++i) m = fmaxf(m, group_max[lane * P + i]);
+            const int per_group = wide ? 2 * P : P;
+            float m = group_max[lane * per_group];
+            for (int i = 1; i < per_group; ++i) m = fmaxf(m, group_max[lane * per_group + i]);
             reinterpret_cast<float*>(cluster_map(sh.cluster_max4, 0))[seg * (32 / P) + lane] = m;
         }
     } else if (CLUSTER) {
@@ -688,10 +720,10 @@ lse_stats_kernel(const __grid_constant__ StatsArgs a) {
         }
         if (a.K == 0) return;
         // Of the parts' keys, those that reach the bound of the whole row.
-        static_assert(kMaxCluster * kPartKeys <= kStatBatches * 128 && kPartKeys % 16 == 0, "whole warps");
+        static_assert(!CLUSTER || (kMaxCluster * kPartKeys * 2 <= sizeof(sh.chunk_max) / 4 && kPartKeys % 16 == 0), "whole warps");
         uint64_t* reached = reinterpret_cast<uint64_t*>(sh.chunk_max);  // (no longer needed)
         if (tid == 0) sh.founds = 0;
-        const float bound = kth_largest_of(reinterpret_cast<const float*>(sh.cluster_max4), a.K, lane);
+        const float bound = kth_largest_of<32>(reinterpret_cast<const float*>(sh.cluster_max4), a.K, lane);
         __syncthreads();
         for (int i = tid; i < P * kPartKeys; i += T) {
             const int part = i / kPartKeys;
@@ -1162,18 +1194,18 @@ cudaError_t launch_stats(StatsArgs a, int sms, cudaStream_t stream) {
     // Threads of a CTA: enough for one batch of the row each; at most 128 when rows
     // are plentiful, so that rows at their ends overlap with rows under way.
     int T = 256;
-    while (T > 128 && vectors < 2LL * kStatU * T) T /= 2;
+    while (T > 128 && vectors < 2LL * stat_u(T) * T) T /= 2;
     if (a.B >= 4LL * sms) T = 128;
     // Rows of up to 1024 vectors by the thousand: a warp each.
     if (vectors <= 1024 && a.B >= 16LL * sms && a.K <= 24) T = 32;
     int P = 1;
     if (a.B < sms) {
-        while (P < kMaxCluster && a.B * P * 2 <= 2LL * sms && vectors >= 2LL * P * kStatU * 128) P *= 2;
-        while (T > 128 && vectors < 1LL * P * kStatU * T) T /= 2;
+        while (P < kMaxCluster && a.B * P * 2 <= 2LL * sms && vectors >= 2LL * P * stat_u(128) * 128) P *= 2;
+        while (T > 128 && vectors < 1LL * P * stat_u(T) * T) T /= 2;
     }
     a.cluster = P;
-    const int64_t batches = ((vectors + P - 1) / P + kStatU * T - 1) / (kStatU * T);
-    while ((batches + (1LL << a.chunk_shift) - 1) >> a.chunk_shift > kStatBatches) ++a.chunk_shift;
+    const int64_t batches = ((vectors + P - 1) / P + stat_u(T) * T - 1) / (stat_u(T) * T);
+    while ((batches + (1LL << a.chunk_shift) - 1) >> a.chunk_shift > stat_batches(T)) ++a.chunk_shift;
     if (P > 1) {
         return T == 128 ? launch_stats_long<DT, 128, true>(a, stream) : launch_stats_long<DT, 256, true>(a, stream);
     }
