@@ -628,39 +628,53 @@ lse_stats_kernel(const __grid_constant__ StatsArgs a) {
             __syncwarp();
             const int item_shift = 1 + a.chunk_shift;  // log2 of a chunk's vectors
             const int items = n << item_shift;
-            // A vector of the chunks per lane and round.
-            for (int i0 = 0; i0 < items; i0 += 32) {
-                const int i = i0 + lane;
-                const int c = i < items ? sh.chunk[wid][i >> item_shift] : 0;
-                const int e0 = i & ((1 << item_shift) - 1);  // which of the chunk's vectors
-                // (a part's vectors fit 32 bits: N does)
-                const int pair = (c >> 5) % (U / 2);
-                const int batch = ((c >> 5) / (U / 2) << a.chunk_shift) + (e0 >> 1);
-                const int k = (batch * U + pair * 2 + (e0 & 1)) * T + wid * 32 + (c & 31);
-                uint32_t w[4];
-                load_vector<DT>(r, k_begin + k, i < items ? k_end : 0, w);
-                const uint32_t col = static_cast<uint32_t>(column_of<DT>(r, k_begin + k, 0));  // (wraps before the row)
+            // H vectors of the chunks per lane and round: two for one-warp rows, which read
+            // all of the row's chunks.
+            constexpr int H = T == 32 ? 2 : 1;
+            int found = 0;  // (one-warp rows count for themselves)
+            for (int i0 = 0; i0 < items; i0 += 32 * H) {
+                uint32_t w[4 * H], col[H];
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    const int i = i0 + 32 * h + lane;
+                    const int c = i < items ? sh.chunk[wid][i >> item_shift] : 0;
+                    const int e0 = i & ((1 << item_shift) - 1);  // which of the chunk's vectors
+                    // (a part's vectors fit 32 bits: N does)
+                    const int pair = (c >> 5) % (U / 2);
+                    const int batch = ((c >> 5) / (U / 2) << a.chunk_shift) + (e0 >> 1);
+                    const int k = (batch * U + pair * 2 + (e0 & 1)) * T + wid * 32 + (c & 31);
+                    load_vector<DT>(r, k_begin + k, i < items ? k_end : 0, &w[4 * h]);
+                    col[h] = static_cast<uint32_t>(column_of<DT>(r, k_begin + k, 0));  // (wraps before the row)
+                }
                 uint32_t mine = 0;
 #pragma unroll
-                for (int e = 0; e < EPV; ++e) mine |= (word_elem<DT>(w, e) >= bound ? 1u : 0u) << e;
-                if (col > static_cast<uint32_t>(a.N) - EPV) {  // the row's ends: elements outside it
+                for (int e = 0; e < H * EPV; ++e)
+                    mine |= (word_elem<DT>(&w[e / EPV * 4], e % EPV) >= bound ? 1u : 0u) << e;
 #pragma unroll
-                    for (int e = 0; e < EPV; ++e)
-                        if (col + e >= a.N) mine &= ~(1u << e);
+                for (int h = 0; h < H; ++h)
+                    if (col[h] > static_cast<uint32_t>(a.N) - EPV) {  // the row's ends: elements outside it
+#pragma unroll
+                        for (int e = 0; e < EPV; ++e)
+                            if (col[h] + e >= a.N) mine &= ~(1u << (h * EPV + e));
+                    }
+                int at = found;
+                if (T > 32) {
+                    const int total = __reduce_add_sync(0xffffffffu, __popc(mine));
+                    if (total == 0) continue;
+                    if (lane == 0) at = atomicAdd(&sh.founds, total);
+                    at = __shfl_sync(0xffffffffu, at, 0);
                 }
-                const int total = __reduce_add_sync(0xffffffffu, __popc(mine));
-                if (total == 0) continue;
-                int at = 0;
-                if (lane == 0) at = atomicAdd(&sh.founds, total);
-                at = __shfl_sync(0xffffffffu, at, 0);
                 for (uint32_t who; (who = __ballot_sync(0xffffffffu, mine != 0)) != 0; at += __popc(who)) {
                     if (mine == 0) continue;
                     const int e = __ffs(mine) - 1;
                     mine &= mine - 1;
                     const int place = at + __popc(who & ((1u << lane) - 1));
-                    if (place < kFoundList) sh.found[place] = topk_key(pick_elem<DT, 4>(w, e), col + e);
+                    const uint32_t column = (H == 1 || e < EPV ? col[0] : col[H - 1] - EPV) + e;
+                    if (place < kFoundList) sh.found[place] = topk_key(pick_elem<DT, 4 * H>(w, e), column);
                 }
+                if (T == 32) found = at;
             }
+            if (T == 32 && lane == 0) sh.founds = found;
         }
         sync();
         scan = scan || sh.overflow != 0 || sh.founds > kFoundList;
