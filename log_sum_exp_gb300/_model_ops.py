@@ -42,14 +42,22 @@ class _allocating:
             self.ctx.__exit__(*exc)
 
 
+def _at_home(torch, stream, device) -> bool:
+    """The call needs neither another current device nor another stream's memory."""
+    return stream is None and torch.cuda.current_device() == device.index
+
+
+def _elsewhere(call, args):
+    """``call(*args)``, whose last arguments are the stream and the device, with
+    that device current and new outputs belonging to that stream."""
+    with _on_device(args[-1]), _allocating(args[-2]):
+        return call(*args)
+
+
 def _need_vector(t, name, dtype, n, device):
     if t.dtype != dtype or t.device != device or t.numel() != n or not t.is_contiguous():
         kind = str(dtype).replace("torch.", "")
         raise ValueError(f"{name} must be a contiguous {kind} tensor of {n} elements on x's device")
-
-
-def _ptr(t):
-    return t.data_ptr() or None if t is not None else None
 
 
 # ---------------------------------------------------------------------------
@@ -77,11 +85,8 @@ def lse_token_stats(x, target=None, top_k=0, entropy=True, stream=None) -> Token
     device = x.device
     if target is not None:
         _need_vector(target, "target", torch.int64, B, device)
-    if stream is not None or torch.cuda.current_device() != device.index:
-        with _on_device(device), _allocating(stream):
-            out = _stats_call(torch, x, dt, B, N, row_stride, target, top_k, entropy, stream, device)
-    else:
-        out = _stats_call(torch, x, dt, B, N, row_stride, target, top_k, entropy, None, device)
+    args = (torch, x, dt, B, N, row_stride, target, top_k, entropy, stream, device)
+    out = _stats_call(*args) if _at_home(torch, stream, device) else _elsewhere(_stats_call, args)
     if x.dim() == 1:
         out = [None if t is None else t[0] for t in out]
     return TokenStats(*out)
@@ -89,18 +94,18 @@ def lse_token_stats(x, target=None, top_k=0, entropy=True, stream=None) -> Token
 
 def _stats_call(torch, x, dt, B, N, row_stride, target, top_k, entropy, stream, device):
     # One allocation per output: views of a shared one cost more host time.
-    empty, f32 = torch.empty, torch.float32
+    empty, like, f32 = torch.empty, torch.empty_like, torch.float32
     lse = empty(B, dtype=f32, device=device)
     logprob = ent = top_lp = top_i = p_t = p_logprob = p_ent = p_lp = p_i = None
     if target is not None:
-        logprob = empty(B, dtype=f32, device=device)
+        logprob = like(lse)
         p_t, p_logprob = target.data_ptr(), logprob.data_ptr()
     if entropy:
-        ent = empty(B, dtype=f32, device=device)
+        ent = like(lse)
         p_ent = ent.data_ptr()
     if top_k:
         top_lp = empty((B, top_k), dtype=f32, device=device)
-        top_i = empty((B, top_k), dtype=torch.int64, device=device)
+        top_i = like(top_lp, dtype=torch.int64)
         p_lp, p_i = top_lp.data_ptr(), top_i.data_ptr()
     _check(load().lse_token_stats(x.data_ptr(), dt, B, N, row_stride, p_t, top_k, p_logprob, p_ent,
                                   lse.data_ptr(), p_lp, p_i, _stream_handle(stream, device)),
@@ -119,7 +124,7 @@ def lse_token_stats_backward(x, stats: TokenStats, target=None, grad_logprob=Non
     torch = _torch()
     if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor")
-    dt = _dtype_name(x)
+    dt = DTYPES[_dtype_name(x)]
     B, N, row_stride = _rows(x)
     K = stats.top_index.shape[-1] if stats.top_index is not None else 0
     _need_vector(stats.lse, "stats.lse", torch.float32, B, x.device)
@@ -139,20 +144,31 @@ def lse_token_stats_backward(x, stats: TokenStats, target=None, grad_logprob=Non
         if stats.top_index is None:
             raise ValueError("grad_top needs stats.top_index")
         _need_vector(stats.top_index, "stats.top_index", torch.int64, B * K, x.device)
-    with _on_device(x.device):
-        if dx is None:
-            with _allocating(stream):
-                dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        if dx.shape != x.shape or dx.dtype != x.dtype or dx.device != x.device:
-            raise ValueError("dx must match x's shape, dtype and device")
+    if dx is not None and (dx.shape != x.shape or dx.dtype != x.dtype or dx.device != x.device):
+        raise ValueError("dx must match x's shape, dtype and device")
+    args = (torch, x, dt, B, N, row_stride, stats, target, K, grad_logprob, grad_entropy, grad_top,
+            grad_lse, dx, stream, x.device)
+    return _stats_backward_call(*args) if _at_home(torch, stream, x.device) \
+        else _elsewhere(_stats_backward_call, args)
+
+
+def _stats_backward_call(torch, x, dt, B, N, row_stride, stats, target, K, grad_logprob,
+                         grad_entropy, grad_top, grad_lse, dx, stream, device):
+    if dx is None:
+        dx = torch.empty_like(x, memory_format=torch.contiguous_format)
+        dx_stride = N
+    else:
         dx_stride = _rows(dx)[2]
-        _check(load().lse_token_stats_backward(
-            _ptr(x), DTYPES[dt], B, N, row_stride, _ptr(stats.lse),
-            _ptr(stats.entropy) if grad_entropy is not None else None,
-            _ptr(target) if grad_logprob is not None else None,
-            _ptr(stats.top_index) if grad_top is not None else None, K, _ptr(grad_logprob),
-            _ptr(grad_entropy), _ptr(grad_top), _ptr(grad_lse), _ptr(dx), dx_stride,
-            _stream_handle(stream, x.device) or None), "lse_token_stats_backward")
+    _check(load().lse_token_stats_backward(
+        x.data_ptr(), dt, B, N, row_stride, stats.lse.data_ptr(),
+        stats.entropy.data_ptr() if grad_entropy is not None else None,
+        target.data_ptr() if grad_logprob is not None else None,
+        stats.top_index.data_ptr() if grad_top is not None else None, K,
+        None if grad_logprob is None else grad_logprob.data_ptr(),
+        None if grad_entropy is None else grad_entropy.data_ptr(),
+        None if grad_top is None else grad_top.data_ptr(),
+        None if grad_lse is None else grad_lse.data_ptr(), dx.data_ptr(), dx_stride,
+        _stream_handle(stream, device)), "lse_token_stats_backward")
     return dx
 
 
@@ -284,15 +300,18 @@ class GradList:
         return len(self.grads)
 
 
-def _grad_call(grads, stream, name, *args):
+def _grad_call(torch, lst, name, args, stream, device):
+    norm = torch.empty((), dtype=torch.float32, device=device)
+    _check(getattr(load(), name)(lst._table, len(lst.grads), *args, norm.data_ptr(),
+                                 _stream_handle(stream, device)), name)
+    return norm
+
+
+def _on_list(grads, stream, name, *args):
     torch = _torch()
     lst = grads if isinstance(grads, GradList) else GradList(grads)
-    with _on_device(lst.device):
-        with _allocating(stream):
-            norm = torch.empty((), dtype=torch.float32, device=lst.device)
-        _check(getattr(load(), name)(lst._table, len(lst), *args, norm.data_ptr(),
-                                     _stream_handle(stream, lst.device) or None), name)
-    return norm
+    args = (torch, lst, name, args, stream, lst.device)
+    return _grad_call(*args) if _at_home(torch, stream, lst.device) else _elsewhere(_grad_call, args)
 
 
 def lse_grad_norm(grads, stream=None):
@@ -300,7 +319,7 @@ def lse_grad_norm(grads, stream=None):
 
     ``grads`` is a ``GradList`` or a sequence of tensors.  No host synchronisation.
     """
-    return _grad_call(grads, stream, "lse_grad_norm")
+    return _on_list(grads, stream, "lse_grad_norm")
 
 
 def lse_grad_clip(grads, max_norm, eps=1e-6, stream=None):
@@ -310,7 +329,7 @@ def lse_grad_clip(grads, max_norm, eps=1e-6, stream=None):
     ``grads`` is a ``GradList`` (its ``out`` tensors receive the result where it
     has them) or a sequence of tensors, clipped in place.  No host synchronisation.
     """
-    return _grad_call(grads, stream, "lse_grad_clip", float(max_norm), float(eps))
+    return _on_list(grads, stream, "lse_grad_clip", max_norm, eps)
 
 
 # ---------------------------------------------------------------------------
@@ -344,21 +363,26 @@ def lse_embedding(table, ids, scale=1.0, out=None, stream=None):
     torch = _torch()
     if not table.is_cuda:
         raise ValueError("table must be a CUDA tensor")
-    dt = _dtype_name(table)
+    dt = DTYPES[_dtype_name(table)]
     V, D, stride = _matrix(table, "table")
-    T = _ids(ids, table.device)
-    with _on_device(table.device):
-        given = out is not None
-        if not given:
-            with _allocating(stream):
-                out = torch.empty((T, D), dtype=table.dtype, device=table.device)
-        if tuple(out.shape) != (T, D) or out.dtype != table.dtype or out.device != table.device:
-            raise ValueError("out must be a [T, D] tensor of the table's dtype and device")
+    device = table.device
+    T = _ids(ids, device)
+    if out is not None and (tuple(out.shape) != (T, D) or out.dtype != table.dtype
+                            or out.device != device):
+        raise ValueError("out must be a [T, D] tensor of the table's dtype and device")
+    args = (torch, table, dt, V, D, stride, ids, T, scale, out, stream, device)
+    return _embed_call(*args) if _at_home(torch, stream, device) else _elsewhere(_embed_call, args)
+
+
+def _embed_call(torch, table, dt, V, D, stride, ids, T, scale, out, stream, device):
+    if out is None:
+        out, out_stride = torch.empty((*ids.shape, D), dtype=table.dtype, device=device), D
+    else:
         out_stride = _matrix(out, "out")[2]
-        _check(load().lse_embedding(_ptr(table), DTYPES[dt], V, D, stride, _ptr(ids), T,
-                                    float(scale), _ptr(out), out_stride,
-                                    _stream_handle(stream, table.device) or None), "lse_embedding")
-    return out if given else out.reshape(tuple(ids.shape) + (D,))
+    _check(load().lse_embedding(table.data_ptr(), dt, V, D, stride, ids.data_ptr(), T, scale,
+                                out.data_ptr(), out_stride, _stream_handle(stream, device)),
+           "lse_embedding")
+    return out
 
 
 def lse_embedding_backward(grad, ids, rows, scale=1.0, padding=-1, dtable=None, accumulate=False,
@@ -374,25 +398,31 @@ def lse_embedding_backward(grad, ids, rows, scale=1.0, padding=-1, dtable=None, 
     torch = _torch()
     if not grad.is_cuda:
         raise ValueError("grad must be a CUDA tensor")
-    dt = _dtype_name(grad)
+    dt = DTYPES[_dtype_name(grad)]
     T, D, stride = _matrix(grad, "grad")
     if _ids(ids, grad.device) != T:
         raise ValueError("ids must hold one id for each row of grad")
     if accumulate and dtable is None:
         raise ValueError("accumulate needs dtable")
-    with _on_device(grad.device):
-        if dtable is None:
-            with _allocating(stream):
-                dtable = torch.empty((rows, D), dtype=grad.dtype, device=grad.device)
-        if tuple(dtable.shape) != (rows, D) or dtable.device != grad.device \
-                or dtable.dtype not in (grad.dtype, torch.float32):
-            raise ValueError("dtable must be a [rows, D] tensor of grad's dtype or float32")
-        dstride = _matrix(dtable, "dtable")[2]
-        _check(load().lse_embedding_backward(_ptr(grad), DTYPES[dt], T, D, stride, _ptr(ids), rows,
-                                             float(scale), padding, _ptr(dtable),
-                                             DTYPES[_dtype_name(dtable)], dstride, int(accumulate),
-                                             _stream_handle(stream, grad.device) or None),
-               "lse_embedding_backward")
+    device = grad.device
+    if dtable is not None and (tuple(dtable.shape) != (rows, D) or dtable.device != device
+                               or dtable.dtype not in (grad.dtype, torch.float32)):
+        raise ValueError("dtable must be a [rows, D] tensor of grad's dtype or float32")
+    args = (torch, grad, dt, T, D, stride, ids, rows, scale, padding, dtable, accumulate, stream,
+            device)
+    return _embed_backward_call(*args) if _at_home(torch, stream, device) \
+        else _elsewhere(_embed_backward_call, args)
+
+
+def _embed_backward_call(torch, grad, dt, T, D, stride, ids, rows, scale, padding, dtable,
+                         accumulate, stream, device):
+    if dtable is None:
+        dtable = torch.empty((rows, D), dtype=grad.dtype, device=device)
+    _check(load().lse_embedding_backward(grad.data_ptr(), dt, T, D, stride, ids.data_ptr(), rows,
+                                         scale, padding, dtable.data_ptr(),
+                                         DTYPES[_dtype_name(dtable)],
+                                         _matrix(dtable, "dtable")[2], 1 if accumulate else 0,
+                                         _stream_handle(stream, device)), "lse_embedding_backward")
     return dtable
 
 

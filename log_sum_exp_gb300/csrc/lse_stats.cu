@@ -13,6 +13,7 @@
 // a sum of two non-negative terms, so nothing cancels.  (m, s, u) is kept online:
 // raising the maximum by d (in units of z) turns u into (u + d s) 2^-d and s into
 // s 2^-d.
+#include <atomic>
 #include <climits>
 #include <cstdint>
 
@@ -1163,8 +1164,16 @@ cudaError_t launch_stats_long(const StatsArgs& a, cudaStream_t stream) {
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     cudaError_t e = cudaSuccess;
-    if (a.cluster > 8)
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (a.cluster > 8) {  // more than the portable size: allowed once per device
+        static std::atomic<uint64_t> allowed{0};
+        int dev = 0;
+        e = cudaGetDevice(&dev);
+        const uint64_t bit = 1ull << (dev & 63);
+        if (e == cudaSuccess && (allowed.load() & bit) == 0) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e == cudaSuccess) allowed.fetch_or(bit);
+        }
+    }
     if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kernel, a);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
