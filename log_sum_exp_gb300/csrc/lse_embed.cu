@@ -136,6 +136,7 @@ constexpr int kZeroRows = 8;
 struct ZeroRows {
     char* table;
     int64_t row_bytes, stride_bytes, rows;
+    int64_t units;           // stores of a row
     const uint32_t* bitmap;  // null: no row has a token
     int64_t first;           // group of kZeroRows rows of this launch's first CTA
     int64_t groups;          // CTAs of this launch
@@ -145,7 +146,7 @@ struct ZeroRows {
 __device__ __forceinline__ void zero_rows(const ZeroRows& z, int64_t cta, int tid, int threads) {
     const int64_t v0 = (z.first + cta) * kZeroRows;
     const uint32_t present = z.bitmap ? z.bitmap[v0 >> 5] >> (v0 & 31) : 0u;
-    const int64_t units = z.row_bytes / z.unit;
+    const int64_t units = z.units;
     for (int q = 0; q < kZeroRows; ++q) {
         const int64_t v = v0 + q;
         if (v >= z.rows) return;
@@ -339,6 +340,7 @@ sort_move_kernel(const __grid_constant__ SortArgs a) {
 // Sums over the sorted tokens.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 32;    // sorted tokens of a tile
+constexpr int kLongRun = 7;  // further tiles of a run that counts as long
 constexpr int kSumU = 8;     // rows of grad in flight per thread
 // Bytes zeroed next to the sorting passes and next to the joins (about 6 us each).
 constexpr int64_t kCountZeroBytes = 8 << 20;
@@ -357,8 +359,8 @@ struct SumArgs {
     char* dtable;
     int64_t dtable_stride;
     bool accumulate;
-    uint32_t* cross;         // tiles whose last run goes on, in any order
-    uint32_t* cross_count;
+    uint32_t* cross;         // [tiles]: those whose last run goes on, in any order
+    uint32_t* cross_count;   // of long runs, and of others
     float* head;             // [tiles][D]: the sum of a tile's first run, when the run began before
     float* tail;             // [tiles][D]: of its last run, when that begins here and goes on
     int tiles;
@@ -487,7 +489,11 @@ embed_sum_kernel(const __grid_constant__ SumArgs a) {
     if (began_before) put_partial<DT, VEC>(a.head, a, tile, slot, s);
     else if (key[n + 1] == run) {
         put_partial<DT, VEC>(a.tail, a, tile, slot, s);
-        if (slot == 0) a.cross[atomicAdd(a.cross_count, 1u)] = static_cast<uint32_t>(tile);
+        if (slot == 0) {  // long runs from the list's front, others from its back
+            const int64_t far = i0 + (kLongRun + 1) * kTile;
+            if (far < a.T && a.key[far] == run) a.cross[atomicAdd(a.cross_count, 1u)] = static_cast<uint32_t>(tile);
+            else a.cross[a.tiles - 1 - static_cast<int>(atomicAdd(a.cross_count + 1, 1u))] = static_cast<uint32_t>(tile);
+        }
     }
     else put_slot<DT, OT, VEC>(a, run, slot, s);
 }
@@ -508,10 +514,20 @@ __device__ __forceinline__ void add_partial(float (&s)[E], const float* p) {
     }
 }
 
+// The sum of a run that begins in `tile` and goes on up to tile `last`, as far as
+// tiles first .. past - 1 (of the later ones) go; with `tail`, the tile's own.
+template <int E>
+__device__ __forceinline__ void add_run(float (&s)[E], const SumArgs& a, int64_t slot, int tile, bool tail, int first, int past) {
+    if (tail) add_partial<E>(s, a.tail + static_cast<int64_t>(tile) * a.D + slot * E);
+#pragma unroll 4
+    for (int j = first; j < past; ++j) add_partial<E>(s, a.head + static_cast<int64_t>(j) * a.D + slot * E);
+}
+
 // Runs that cross tiles, listed by the tiles where they begin: the tile's own sum and
-// the later tiles'.  blockDim = (slots of a column block, groups): the groups take
-// equal parts of the tiles, then their sums are added in order.  The CTAs take
-// (run, column block) pairs in turn; further CTAs zero rows.
+// the later tiles', in order.  blockDim = (slots of a narrow column block, groups).  For
+// a long run the groups take equal parts of the tiles of one narrow block, then their
+// sums are added in order; for others each group has a narrow block of its own.  The
+// CTAs take (run, column block) pairs in turn; further CTAs zero rows.
 template <int DT, int OT, bool VEC>
 __global__ void __launch_bounds__(kEmbedThreads)
 embed_join_kernel(const __grid_constant__ SumArgs a) {
@@ -525,13 +541,18 @@ embed_join_kernel(const __grid_constant__ SumArgs a) {
         return;
     }
     const int t = ty * TX + tx;
-    const int64_t units = static_cast<int64_t>(*a.cross_count) * a.col_blocks;
+    const int64_t wide_blocks = (a.col_blocks + TY - 1) / TY;
+    const int64_t longs = static_cast<int64_t>(a.cross_count[0]) * a.col_blocks;
+    const int64_t units = longs + static_cast<int64_t>(a.cross_count[1]) * wide_blocks;
     for (int64_t unit = blockIdx.x; unit < units; unit += a.sum_ctas) {
-        const int tile = static_cast<int>(a.cross[unit / a.col_blocks]);
-        const int64_t slot = unit % a.col_blocks * TX + tx;
+        const bool is_long = unit < longs;
+        const int64_t q = is_long ? unit / a.col_blocks : (unit - longs) / wide_blocks;
+        const int64_t block = is_long ? unit - q * a.col_blocks : (unit - longs - q * wide_blocks) * TY + ty;
+        const int tile = static_cast<int>(a.cross[is_long ? q : a.tiles - 1 - q]);
+        const int64_t slot = block * TX + tx;
         const uint32_t run = a.key[static_cast<int64_t>(tile + 1) * kTile];
-        // The last tile whose first token is of this run: 32 tiles looked at in one go
-        // (most runs end in the next tile), then by halves.
+        // The last tile whose first token is of this run: 32 tiles looked at in one go,
+        // then by halves.
         const int look = tile + 2 + (t & 31);
         const bool more = look < a.tiles && a.key[static_cast<int64_t>(look) * kTile] == run;
         const uint32_t ends = ~__ballot_sync(0xffffffffu, more);
@@ -544,17 +565,20 @@ embed_join_kernel(const __grid_constant__ SumArgs a) {
                 else hi = mid - 1;
             }
         }
-        const int each = (lo - tile + TY - 1) / TY;  // of tiles tile + 1 .. lo
-        const int j0 = tile + 1 + ty * each;
-        const int j1 = j0 + each < lo + 1 ? j0 + each : lo + 1;
         float s[E];
 #pragma unroll
         for (int i = 0; i < E; ++i) s[i] = 0.0f;
-        if (slot < a.slots) {
-            if (ty == 0) add_partial<E>(s, a.tail + static_cast<int64_t>(tile) * a.D + slot * E);
-#pragma unroll 4
-            for (int j = j0; j < j1; ++j) add_partial<E>(s, a.head + static_cast<int64_t>(j) * a.D + slot * E);
+        if (!is_long) {
+            if (slot < a.slots) {
+                add_run<E>(s, a, slot, tile, true, tile + 1, lo + 1);
+                put_slot<DT, OT, VEC>(a, run, slot, s);
+            }
+            continue;
         }
+        const int each = (lo - tile + TY - 1) / TY;  // of tiles tile + 1 .. lo
+        const int j0 = tile + 1 + ty * each;
+        const int j1 = j0 + each < lo + 1 ? j0 + each : lo + 1;
+        if (slot < a.slots) add_run<E>(s, a, slot, tile, ty == 0, j0, j1);
 #pragma unroll
         for (int i = 0; i < E; ++i) part[i * (TX * TY) + t] = s[i];
         __syncthreads();
@@ -675,6 +699,7 @@ lse_status embed_backward(SumArgs a, lse_dtype dtype, lse_dtype out_dtype, const
     a.zero.rows = a.V;
     a.zero.groups = a.accumulate ? 0 : (a.V + kZeroRows - 1) / kZeroRows;
     a.zero.unit = rows_aligned(a.dtable, a.dtable_stride, ob) && a.zero.row_bytes % 16 == 0 ? 16 : static_cast<int>(ob);
+    a.zero.units = a.zero.row_bytes / a.zero.unit;
     if (a.T > 0) {
         // Blocks of at least one round of tokens, at most kSortMaxBlocks of them.
         SortArgs s;
@@ -696,7 +721,7 @@ lse_status embed_backward(SumArgs a, lse_dtype dtype, lse_dtype out_dtype, const
         const int64_t list = round_up(static_cast<int64_t>(a.T) * 4, 256);
         const int64_t counts = round_up((static_cast<int64_t>(blocks) << per) * 4, 256);
         const int64_t bitmap = round_up((a.V + 31) / 32 * 4, 256);
-        const int64_t cross = round_up((tiles + 1) * 4, 256);
+        const int64_t cross = round_up((tiles + 2) * 4, 256);
         const int64_t partial = round_up(tiles * a.D * 4, 256);
         const lse_status st = take_scratch(reinterpret_cast<void**>(&scratch),
                                            static_cast<size_t>(4 * list + passes * counts + bitmap + cross + 2 * partial), stream);
@@ -707,7 +732,7 @@ lse_status embed_backward(SumArgs a, lse_dtype dtype, lse_dtype out_dtype, const
         s.bitmap = reinterpret_cast<uint32_t*>(count0 + passes * counts);
         char* const behind = count0 + passes * counts + bitmap;
         a.cross_count = reinterpret_cast<uint32_t*>(behind);
-        a.cross = a.cross_count + 1;
+        a.cross = a.cross_count + 2;
         a.head = reinterpret_cast<float*>(behind + cross);
         a.tail = reinterpret_cast<float*>(behind + cross + partial);
         a.zero.bitmap = s.bitmap;
@@ -719,9 +744,9 @@ lse_status embed_backward(SumArgs a, lse_dtype dtype, lse_dtype out_dtype, const
         s.bits = per;
         s.counts = reinterpret_cast<uint32_t*>(count0);
         s.zero = take_zero_rows(&a.zero, blind ? kCountZeroBytes : 0, nullptr);
-        // (behind the first pass's counts: the later passes', the bitmap, the list's length)
+        // (behind the first pass's counts: the later passes', the bitmap, the list's lengths)
         e = launch_pdl(sort_count_kernel, dim3(static_cast<unsigned>(blocks + s.zero.groups)), dim3(kSortThreads), stream,
-                       s, reinterpret_cast<uint32_t*>(count0 + counts), ((passes - 1) * counts + bitmap) / 4 + 1);
+                       s, reinterpret_cast<uint32_t*>(count0 + counts), ((passes - 1) * counts + bitmap) / 4 + 2);
         for (int p = 0; p < passes && e == cudaSuccess; ++p) {
             s.shift = p * per;
             s.next_bits = p + 1 < passes ? per : 0;
