@@ -411,8 +411,10 @@ LSE_API lse_status lse_forward_split_static(const void *x, lse_dtype dtype, int6
  * Entries beyond the row (top_k > N) hold index -1 and log-probability -inf.
  * Among equal values -0 equals +0; a NaN ranks above every number.  entropy is
  * NaN for a row that is no distribution: one that holds a NaN or +inf, or
- * nothing but -inf (or N == 0).  Log-probabilities follow IEEE arithmetic on
- * x - lse, so they are NaN in a row of only -inf.
+ * nothing but -inf (or N == 0); there log-probabilities follow IEEE arithmetic
+ * on x - lse (NaN in a row of only -inf).  In every other row they are computed
+ * as (x - max) - log sum exp(x - max), which keeps its digits when all logits
+ * are large.
  * Results do not depend on scheduling: equal inputs give equal bits.
  */
 LSE_API lse_status lse_token_stats(const void *x, lse_dtype dtype, int64_t B, int64_t N,
