@@ -7,9 +7,9 @@
 // A tensor is the 16-byte vectors that cover it (elements outside it count as 0 and
 // are not written), in chunks of kChunk vectors, numbered through the list.  CTA c of
 // G takes a contiguous range of chunks, so it looks its tensors up once and then
-// walks; the clipping pass walks the same ranges backwards, because what was read
-// last is what L2 still holds.  The list travels as a kernel parameter: a call copies
-// nothing to the device and can be captured.
+// walks.  (Walking the ranges backwards when clipping, to meet what L2 still holds,
+// measured the same: 388 us for 400 M bf16 elements either way.)  The list travels as a
+// kernel parameter: a call copies nothing to the device and can be captured.
 //
 // A thread squares and adds up to 64 elements in f32 (four sums, so at most 16
 // squares in a row), then goes on in 64 bits.  Squares of f32 and bf16 gradients can
@@ -264,7 +264,7 @@ __device__ __forceinline__ void chunk_scale(const GradEntry& t, int64_t k0, floa
                 }
             }
             if (vec && (kk > 0 || off == 0) && (kk + 1) * 16 <= end) {
-                __stcs(reinterpret_cast<uint4*>(o0 + kk * 16), make_uint4(o[0], o[1], o[2], o[3]));
+                *reinterpret_cast<uint4*>(o0 + kk * 16) = make_uint4(o[0], o[1], o[2], o[3]);
             } else {
                 const int from = kk == 0 ? off : 0;
                 const int to = (kk + 1) * 16 > end ? static_cast<int>(end - kk * 16) : 16;
@@ -287,12 +287,11 @@ grad_scale_kernel(const __grid_constant__ GradList<N> list, const double* __rest
     if (blockIdx.x == 0 && threadIdx.x == 0) norm[0] = v;
     const float c0 = max_norm / (v + eps);
     const float coef = c0 > 1.0f ? 1.0f : c0;  // NaN stays NaN
-    int first, c;
-    chunk_range(list, &first, &c);
-    if (first >= c) return;
-    int i = tensor_of(list, c - 1);
-    for (--c; c >= first; --c) {
-        while (list.t[i].first_chunk > c) --i;
+    int c, last;
+    chunk_range(list, &c, &last);
+    int i = tensor_of(list, c);
+    for (; c < last; ++c) {
+        while (i + 1 < list.count && list.t[i + 1].first_chunk <= c) ++i;
         const GradEntry& t = list.t[i];
         if (coef == 1.0f && t.out == t.data) continue;
         const int64_t k0 = (c - t.first_chunk) * kChunk;

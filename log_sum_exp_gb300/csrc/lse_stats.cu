@@ -939,8 +939,7 @@ lse_stats_short_kernel(const __grid_constant__ StatsArgs a) {
 // TX threads take a segment of a row, four vectors each at a time, every load
 // issued before the stores.  The few elements with a unit term are read before
 // anything is stored (dx may be x) and written once more, whole, at the end, so the
-// loop compares no columns.  Rows run from the last to the first: the forward pass
-// that comes before has left the last ones in L2.
+// loop compares no columns.
 // ---------------------------------------------------------------------------
 template <int DT>
 __device__ __forceinline__ void put_elem(void* row, int64_t i, float v) {
@@ -1076,8 +1075,8 @@ lse_stats_backward_kernel(const __grid_constant__ StatsBackwardArgs a) {
     const int64_t units = a.B * a.segments;
     for (int64_t unit = static_cast<int64_t>(blockIdx.x) * UNITS + threadIdx.x / TX; unit < units;
          unit += static_cast<int64_t>(gridDim.x) * UNITS) {
-        const int64_t row = a.B - 1 - unit / a.segments;
-        const int64_t seg = unit % a.segments;
+        const int64_t row = unit / a.segments;
+        const int64_t seg = unit - row * a.segments;
         const char* xr = static_cast<const char*>(a.x) + row * a.row_stride * EB;
         char* dr = static_cast<char*>(a.dx) + row * a.dx_row_stride * EB;
         const int off = VEC ? static_cast<int>(reinterpret_cast<uintptr_t>(xr) & 15u) : 0;
