@@ -16,6 +16,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include <cuda_runtime.h>
 
@@ -66,6 +67,37 @@ __device__ __forceinline__ uint4 pack_vector(const float (&x)[16 / DType<DT>::by
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// A slot is what a thread moves at a time: SB = 16 bytes where every row of both sides
+// starts on a 16-byte boundary and is a whole number of vectors, 4 bytes where two
+// 16-bit elements can go together, or an element.  Small slots make up with more of
+// them in flight.
+template <int DT, int SB> struct Slot {
+    static constexpr int elems = SB / DType<DT>::bytes;
+    static constexpr int in_flight = SB == 16 ? 8 : SB == 4 ? 16 : 24;
+    using Raw = typename std::conditional<SB == 16, uint4, uint32_t>::type;
+    static __device__ __forceinline__ Raw load(const char* p) {
+        if constexpr (SB == 16) return ldg_stream16(p);
+        else if constexpr (SB == 4) return __ldg(reinterpret_cast<const uint32_t*>(p));
+        else return __ldg(reinterpret_cast<const unsigned short*>(p));
+    }
+    static __device__ __forceinline__ void unpack(Raw r, float (&x)[elems]) {
+        if constexpr (SB == 16) {
+            unpack_vector<DT>(r, x);
+        } else if constexpr (DT == kF32) {
+            x[0] = __uint_as_float(r);
+        } else {
+            x[0] = word_lo<DT>(r);
+            if constexpr (SB == 4) x[1] = word_hi<DT>(r);
+        }
+    }
+    static __device__ __forceinline__ void store(char* p, const float (&x)[elems]) {
+        if constexpr (SB == 16) *reinterpret_cast<uint4*>(p) = pack_vector<DT>(x);
+        else if constexpr (DT == kF32) *reinterpret_cast<float*>(p) = x[0];
+        else if constexpr (SB == 4) *reinterpret_cast<uint32_t*>(p) = pack2<DT>(x[0], x[1]);
+        else *reinterpret_cast<unsigned short*>(p) = static_cast<unsigned short>(pack2<DT>(x[0], 0.0f));
+    }
+};
+
 // ---------------------------------------------------------------------------
 // Lookup: a warp per token and segment of its row.
 // ---------------------------------------------------------------------------
@@ -80,14 +112,14 @@ struct EmbedArgs {
     int64_t segments;  // per row, of 32 * U slots
 };
 
-// U slots per lane; a slot is a 16-byte vector (VEC: every row of both sides starts on
-// a 16-byte boundary and is a whole number of vectors) or an element.
-template <int DT, bool VEC, int U>
+// U slots per lane.
+template <int DT, int SB, int U>
 __global__ void __launch_bounds__(kEmbedThreads)
 embed_kernel(const __grid_constant__ EmbedArgs a) {
-    constexpr int EB = DType<DT>::bytes, EPV = 16 / EB;
+    using S = Slot<DT, SB>;
+    constexpr int EB = DType<DT>::bytes;
     const int lane = threadIdx.x & 31;
-    const int64_t slots = VEC ? a.D / EPV : a.D;
+    const int64_t slots = a.D / S::elems;
     pdl_trigger();
     pdl_wait();
     const int64_t units = a.T * a.segments;
@@ -99,30 +131,18 @@ embed_kernel(const __grid_constant__ EmbedArgs a) {
         const bool in = id >= 0 && id < a.V;
         const char* from = a.table + (in ? id : 0) * a.table_stride * EB;
         char* to = a.out + t * a.out_stride * EB;
-        if constexpr (VEC) {
-            uint4 v[U];
+        typename S::Raw v[U];
 #pragma unroll
-            for (int j = 0; j < U; ++j)
-                if (in && k0 + 32 * j < slots) v[j] = __ldg(reinterpret_cast<const uint4*>(from) + k0 + 32 * j);
+        for (int j = 0; j < U; ++j)
+            if (in && k0 + 32 * j < slots) v[j] = S::load(from + (k0 + 32 * j) * SB);
 #pragma unroll
-            for (int j = 0; j < U; ++j) {
-                if (k0 + 32 * j >= slots) continue;
-                float x[EPV];
-                if (in) unpack_vector<DT>(v[j], x);
+        for (int j = 0; j < U; ++j) {
+            if (k0 + 32 * j >= slots) continue;
+            float x[S::elems];
+            if (in) S::unpack(v[j], x);
 #pragma unroll
-                for (int i = 0; i < EPV; ++i) x[i] = in ? x[i] * a.scale : __int_as_float(0x7fc00000);
-                reinterpret_cast<uint4*>(to)[k0 + 32 * j] = pack_vector<DT>(x);
-            }
-        } else {
-            float v[U];
-#pragma unroll
-            for (int j = 0; j < U; ++j) {
-                v[j] = __int_as_float(0x7fc00000);
-                if (in && k0 + 32 * j < slots) v[j] = load_elem<DT>(from, k0 + 32 * j);
-            }
-#pragma unroll
-            for (int j = 0; j < U; ++j)
-                if (k0 + 32 * j < slots) put_elem<DT>(to, k0 + 32 * j, v[j] * a.scale);
+            for (int i = 0; i < S::elems; ++i) x[i] = in ? x[i] * a.scale : __int_as_float(0x7fc00000);
+            S::store(to + (k0 + 32 * j) * SB, x);
         }
     }
 }
@@ -136,28 +156,40 @@ constexpr int kZeroRows = 8;
 struct ZeroRows {
     char* table;
     int64_t row_bytes, stride_bytes, rows;
-    int64_t units;           // stores of a row
     const uint32_t* bitmap;  // null: no row has a token
     int64_t first;           // group of kZeroRows rows of this launch's first CTA
     int64_t groups;          // CTAs of this launch
-    int unit;                // 16 (rows of whole, aligned 16-byte vectors), 4 or 2 bytes per store
+    int64_t vectors;         // of a row, where all rows are whole, aligned 16-byte vectors; else 0
+    int eb;                  // bytes of an element, 4 or 2
 };
+
+__device__ __forceinline__ void put_zero(char* p, int eb) {
+    if (eb == 4) *reinterpret_cast<uint32_t*>(p) = 0u;
+    else *reinterpret_cast<unsigned short*>(p) = 0;
+}
 
 __device__ __forceinline__ void zero_rows(const ZeroRows& z, int64_t cta, int tid, int threads) {
     const int64_t v0 = (z.first + cta) * kZeroRows;
     const uint32_t present = z.bitmap ? z.bitmap[v0 >> 5] >> (v0 & 31) : 0u;
-    const int64_t units = z.units;
     for (int q = 0; q < kZeroRows; ++q) {
         const int64_t v = v0 + q;
         if (v >= z.rows) return;
         if ((present >> q) & 1u) continue;
         char* row = z.table + v * z.stride_bytes;
-        if (z.unit == 16)
-            for (int64_t k = tid; k < units; k += threads) __stcs(reinterpret_cast<uint4*>(row) + k, make_uint4(0, 0, 0, 0));
-        else if (z.unit == 4)
-            for (int64_t k = tid; k < units; k += threads) reinterpret_cast<uint32_t*>(row)[k] = 0u;
-        else
-            for (int64_t k = tid; k < units; k += threads) reinterpret_cast<unsigned short*>(row)[k] = 0;
+        if (z.vectors > 0) {
+            for (int64_t k = tid; k < z.vectors; k += threads) __stcs(reinterpret_cast<uint4*>(row) + k, make_uint4(0, 0, 0, 0));
+            continue;
+        }
+        // Elements up to a 16-byte boundary, vectors, elements.
+        int64_t head = (16 - static_cast<int64_t>(reinterpret_cast<uintptr_t>(row) & 15u)) & 15;
+        if (head > z.row_bytes) head = z.row_bytes;
+        const int64_t vectors = (z.row_bytes - head) >> 4;
+        const int64_t tail = z.row_bytes - head - vectors * 16;
+        for (int64_t k = tid; k < vectors; k += threads) __stcs(reinterpret_cast<uint4*>(row + head) + k, make_uint4(0, 0, 0, 0));
+        if (head + tail == 0) continue;
+        const int64_t b = static_cast<int64_t>(tid) * z.eb;  // one element per thread at either end
+        if (b < head) put_zero(row + b, z.eb);
+        if (b < tail) put_zero(row + head + vectors * 16 + b, z.eb);
     }
 }
 
@@ -330,7 +362,12 @@ sort_move_kernel(const __grid_constant__ SortArgs a) {
             if (a.next_bits > 0)
                 atomicAdd(&a.next_counts[((to >> a.block_shift) << a.next_bits) +
                                          ((key[j] >> (a.shift + a.bits)) & ((1u << a.next_bits) - 1))], 1u);
-            if (FIRST && key[j] < a.V) atomicOr(&a.bitmap[key[j] >> 5], 1u << (key[j] & 31));
+            if (FIRST && key[j] < a.V) {
+                // (looked at first: the bits of frequent ids share few words)
+                uint32_t* const word = &a.bitmap[key[j] >> 5];
+                const uint32_t bit = 1u << (key[j] & 31);
+                if ((__ldcg(word) & bit) == 0) atomicOr(word, bit);
+            }
         }
         __syncthreads();
     }
@@ -339,12 +376,12 @@ sort_move_kernel(const __grid_constant__ SortArgs a) {
 // ---------------------------------------------------------------------------
 // Sums over the sorted tokens.
 // ---------------------------------------------------------------------------
-constexpr int kTile = 32;    // sorted tokens of a tile
 constexpr int kLongRun = 7;  // further tiles of a run that counts as long
-constexpr int kSumU = 8;     // rows of grad in flight per thread
-// Bytes zeroed next to the sorting passes and next to the joins (about 6 us each).
-constexpr int64_t kCountZeroBytes = 8 << 20;
-constexpr int64_t kSortZeroBytes = 40 << 20;
+// Bytes zeroed next to the counting, to each sorting pass and to the joins: about what
+// the memory takes while these wait for their own few loads (32768 tokens, 2048 columns:
+// 136 us with 4, 24 and 24 MB, 130 with 8, 40 and 40, 127 with these).
+constexpr int64_t kCountZeroBytes = 16 << 20;
+constexpr int64_t kSortZeroBytes = 56 << 20;
 constexpr int64_t kJoinCtas = 608;  // four for each SM
 constexpr int64_t kJoinZeroBytes = 40 << 20;
 
@@ -363,6 +400,7 @@ struct SumArgs {
     uint32_t* cross_count;   // of long runs, and of others
     float* head;             // [tiles][D]: the sum of a tile's first run, when the run began before
     float* tail;             // [tiles][D]: of its last run, when that begins here and goes on
+    int tile_len;            // sorted tokens of a tile
     int tiles;
     int64_t slots;           // per row: 16-byte vectors or elements of grad
     int64_t col_blocks;      // of blockDim.x slots
@@ -370,55 +408,61 @@ struct SumArgs {
     ZeroRows zero;
 };
 
-template <int DT, bool VEC> struct Slot {
-    static constexpr int elems = VEC ? 16 / DType<DT>::bytes : 1;
+// A slot's sums.
+template <int E> struct Sums {
+    float v[E];
 };
 
 // dtable's slot of row v: scale * sum, plus what was there.
-template <int DT, int OT, bool VEC>
-__device__ __forceinline__ void put_slot(const SumArgs& a, uint32_t v, int64_t slot, const float (&s)[Slot<DT, VEC>::elems]) {
-    constexpr int E = Slot<DT, VEC>::elems, OB = DType<OT>::bytes;
-    char* row = a.dtable + static_cast<int64_t>(v) * a.dtable_stride * OB;
-    float x[E];
+template <int DT, int OT, int SB>
+__device__ __forceinline__ void put_slot(const SumArgs& a, uint32_t v, int64_t slot, const Sums<Slot<DT, SB>::elems>& s) {
+    constexpr int E = Slot<DT, SB>::elems, OB = DType<OT>::bytes;
+    // dtable's share of the slot in pieces of at most 16 bytes, of the same alignment.
+    constexpr int PB = OT == DT ? SB : (SB == 16 ? 16 : 4), PE = PB / OB;
+    using P = Slot<OT, PB>;
+    char* to = a.dtable + static_cast<int64_t>(v) * a.dtable_stride * OB + slot * (E * OB);
 #pragma unroll
-    for (int i = 0; i < E; ++i) x[i] = s[i] * a.scale;
-    if constexpr (VEC) {
-        constexpr int OE = 16 / OB;  // elements per vector of dtable
-        uint4* to = reinterpret_cast<uint4*>(row + slot * E * OB);
-#pragma unroll
-        for (int q = 0; q < E / OE; ++q) {
-            float y[OE];
-            if (a.accumulate) unpack_vector<OT>(to[q], y);
-#pragma unroll
-            for (int i = 0; i < OE; ++i) y[i] = a.accumulate ? y[i] + x[q * OE + i] : x[q * OE + i];
-            to[q] = pack_vector<OT>(y);
-        }
-    } else {
+    for (int q = 0; q < E / PE; ++q, to += PB) {
+        float x[PE];
         if (a.accumulate) {
-            if constexpr (OT == kF32) x[0] += reinterpret_cast<const float*>(row)[slot];
-            else x[0] += load_elem<OT>(row, slot);
+            typename P::Raw old;  // (a plain load: the row is written here)
+            if constexpr (PB == 2) old = *reinterpret_cast<const unsigned short*>(to);
+            else old = *reinterpret_cast<const typename P::Raw*>(to);
+            P::unpack(old, x);
         }
-        put_elem<OT>(row, slot, x[0]);
+#pragma unroll
+        for (int i = 0; i < PE; ++i) x[i] = a.accumulate ? fmaf(s.v[q * PE + i], a.scale, x[i]) : s.v[q * PE + i] * a.scale;
+        P::store(to, x);
     }
 }
 
-template <int DT, bool VEC>
-__device__ __forceinline__ void put_partial(float* to, const SumArgs& a, int tile, int64_t slot,
-                                            const float (&s)[Slot<DT, VEC>::elems]) {
-    constexpr int E = Slot<DT, VEC>::elems;
+template <int E>
+__device__ __forceinline__ void put_partial(float* to, const SumArgs& a, int tile, int64_t slot, const Sums<E>& s) {
     float* p = to + static_cast<int64_t>(tile) * a.D + slot * E;
 #pragma unroll
     for (int i = 0; i < E; i += E >= 4 ? 4 : 1) {
-        if constexpr (E >= 4) *reinterpret_cast<float4*>(p + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
-        else p[i] = s[i];
+        if constexpr (E >= 4) *reinterpret_cast<float4*>(p + i) = make_float4(s.v[i], s.v[i + 1], s.v[i + 2], s.v[i + 3]);
+        else p[i] = s.v[i];
     }
 }
 
+// The end of a run in a tile.  (Inlined at every step of the unrolled sum: as a called
+// function it measured 160 against 140 us for 32768 tokens of 2048 columns.)
+template <int DT, int OT, int SB>
+__device__ __forceinline__ void end_run(const SumArgs& a, uint32_t run, bool began_before, bool goes_on, int tile,
+                                     int64_t slot, Sums<Slot<DT, SB>::elems> s) {
+    if (run >= a.V) return;
+    if (began_before) put_partial(a.head, a, tile, slot, s);
+    else if (goes_on) put_partial(a.tail, a, tile, slot, s);
+    else put_slot<DT, OT, SB>(a, run, slot, s);
+}
+
 // blockDim = (slots of a column block, tiles of a CTA).
-template <int DT, int OT, bool VEC>
+template <int DT, int OT, int SB>
 __global__ void __launch_bounds__(kEmbedThreads, 4)
 embed_sum_kernel(const __grid_constant__ SumArgs a) {
-    constexpr int E = Slot<DT, VEC>::elems, EB = DType<DT>::bytes, OB = DType<OT>::bytes;
+    using S = Slot<DT, SB>;
+    constexpr int E = S::elems, U = S::in_flight;
     extern __shared__ uint32_t sm[];
     const int tx = threadIdx.x, ty = threadIdx.y, TX = blockDim.x, TY = blockDim.y;
     pdl_trigger();
@@ -433,91 +477,82 @@ embed_sum_kernel(const __grid_constant__ SumArgs a) {
     const int64_t slot = (blockIdx.x - group * a.col_blocks) * TX + tx;
     const int64_t tile0 = group * TY;
     // Keys of the tiles with one neighbour on either side, and where the rows are.
-    uint32_t* key = sm + ty * (kTile + 2);
-    uint32_t* at = sm + TY * (kTile + 2) + ty * kTile;
-    const int64_t i0 = (tile0 + ty) * kTile;
-    for (int e = tx; e < kTile + 2; e += TX) {
+    const int len = a.tile_len;
+    uint32_t* key = sm + ty * (len + 2);
+    uint32_t* at = sm + TY * (len + 2) + ty * len;
+    const int64_t i0 = (tile0 + ty) * len;
+    for (int e = tx; e < len + 2; e += TX) {
         const int64_t i = i0 + e - 1;
         key[e] = i >= 0 && i < a.T ? a.key[i] : 0xffffffffu;  // (no id)
-        if (e < kTile) at[e] = i0 + e < a.T ? a.at[i0 + e] : 0u;
+        if (e < len) at[e] = i0 + e < a.T ? a.at[i0 + e] : 0u;
     }
     __syncthreads();
     if (tile0 + ty >= a.tiles || slot >= a.slots) return;
     const int tile = static_cast<int>(tile0 + ty);
-    const int n = a.T - i0 < kTile ? static_cast<int>(a.T - i0) : kTile;
-    const char* col = a.grad + slot * (E * EB);
+    const int n = a.T - i0 < len ? static_cast<int>(a.T - i0) : len;
+    const char* col = a.grad + slot * SB;
+    const int64_t row_bytes = a.grad_stride * DType<DT>::bytes;
 
-    float s[E];
+    Sums<E> s;
 #pragma unroll
-    for (int i = 0; i < E; ++i) s[i] = 0.0f;
+    for (int i = 0; i < E; ++i) s.v[i] = 0.0f;
     uint32_t run = key[1];
     bool began_before = key[0] == run;
-    for (int e0 = 0; e0 < n; e0 += kSumU) {
-        float x[kSumU];
-        uint4 v[kSumU];
+    for (int e0 = 0; e0 < n; e0 += U) {
+        typename S::Raw v[U];
 #pragma unroll
-        for (int u = 0; u < kSumU; ++u) {
+        for (int u = 0; u < U; ++u) {
             if (e0 + u >= n || key[e0 + u + 1] >= a.V) continue;
-            const char* p = col + static_cast<int64_t>(at[e0 + u]) * a.grad_stride * EB;
-            if constexpr (VEC) v[u] = ldg_stream16(p);
-            else x[u] = load_elem<DT>(p, 0);
+            v[u] = S::load(col + static_cast<int64_t>(at[e0 + u]) * row_bytes);
         }
 #pragma unroll
-        for (int u = 0; u < kSumU; ++u) {
+        for (int u = 0; u < U; ++u) {
             if (e0 + u >= n) break;
             const uint32_t k = key[e0 + u + 1];
             if (k != run) {
-                if (began_before) put_partial<DT, VEC>(a.head, a, tile, slot, s);
-                else if (run < a.V) put_slot<DT, OT, VEC>(a, run, slot, s);
+                end_run<DT, OT, SB>(a, run, began_before, false, tile, slot, s);
 #pragma unroll
-                for (int i = 0; i < E; ++i) s[i] = 0.0f;
+                for (int i = 0; i < E; ++i) s.v[i] = 0.0f;
                 run = k;
                 began_before = false;
             }
             if (k >= a.V) break;  // (they sort last)
-            if constexpr (VEC) {
-                float y[E];
-                unpack_vector<DT>(v[u], y);
+            float y[E];
+            S::unpack(v[u], y);
 #pragma unroll
-                for (int i = 0; i < E; ++i) s[i] += y[i];
-            } else {
-                s[0] += x[u];
-            }
+            for (int i = 0; i < E; ++i) s.v[i] += y[i];
         }
     }
-    if (run >= a.V) return;
-    if (began_before) put_partial<DT, VEC>(a.head, a, tile, slot, s);
-    else if (key[n + 1] == run) {
-        put_partial<DT, VEC>(a.tail, a, tile, slot, s);
-        if (slot == 0) {  // long runs from the list's front, others from its back
-            const int64_t far = i0 + (kLongRun + 1) * kTile;
-            if (far < a.T && a.key[far] == run) a.cross[atomicAdd(a.cross_count, 1u)] = static_cast<uint32_t>(tile);
-            else a.cross[a.tiles - 1 - static_cast<int>(atomicAdd(a.cross_count + 1, 1u))] = static_cast<uint32_t>(tile);
-        }
+    const bool goes_on = !began_before && run < a.V && key[n + 1] == run;
+    end_run<DT, OT, SB>(a, run, began_before, goes_on, tile, slot, s);
+    if (goes_on && slot == 0) {  // long runs from the list's front, others from its back
+        const int64_t far = i0 + (kLongRun + 1) * len;
+        if (far < a.T && a.key[far] == run) a.cross[atomicAdd(a.cross_count, 1u)] = static_cast<uint32_t>(tile);
+        else a.cross[a.tiles - 1 - static_cast<int>(atomicAdd(a.cross_count + 1, 1u))] = static_cast<uint32_t>(tile);
     }
-    else put_slot<DT, OT, VEC>(a, run, slot, s);
 }
 
 template <int E>
-__device__ __forceinline__ void add_partial(float (&s)[E], const float* p) {
+__device__ __forceinline__ void add_partial(Sums<E>& s, const float* p) {
     if constexpr (E >= 4) {
 #pragma unroll
         for (int i = 0; i < E; i += 4) {
             const float4 v = *reinterpret_cast<const float4*>(p + i);
-            s[i] += v.x;
-            s[i + 1] += v.y;
-            s[i + 2] += v.z;
-            s[i + 3] += v.w;
+            s.v[i] += v.x;
+            s.v[i + 1] += v.y;
+            s.v[i + 2] += v.z;
+            s.v[i + 3] += v.w;
         }
     } else {
-        s[0] += *p;
+#pragma unroll
+        for (int i = 0; i < E; ++i) s.v[i] += p[i];
     }
 }
 
 // The sum of a run that begins in `tile` and goes on up to tile `last`, as far as
 // tiles first .. past - 1 (of the later ones) go; with `tail`, the tile's own.
 template <int E>
-__device__ __forceinline__ void add_run(float (&s)[E], const SumArgs& a, int64_t slot, int tile, bool tail, int first, int past) {
+__device__ __forceinline__ void add_run(Sums<E>& s, const SumArgs& a, int64_t slot, int tile, bool tail, int first, int past) {
     if (tail) add_partial<E>(s, a.tail + static_cast<int64_t>(tile) * a.D + slot * E);
 #pragma unroll 4
     for (int j = first; j < past; ++j) add_partial<E>(s, a.head + static_cast<int64_t>(j) * a.D + slot * E);
@@ -528,10 +563,10 @@ __device__ __forceinline__ void add_run(float (&s)[E], const SumArgs& a, int64_t
 // a long run the groups take equal parts of the tiles of one narrow block, then their
 // sums are added in order; for others each group has a narrow block of its own.  The
 // CTAs take (run, column block) pairs in turn; further CTAs zero rows.
-template <int DT, int OT, bool VEC>
+template <int DT, int OT, int SB>
 __global__ void __launch_bounds__(kEmbedThreads)
 embed_join_kernel(const __grid_constant__ SumArgs a) {
-    constexpr int E = Slot<DT, VEC>::elems;
+    constexpr int E = Slot<DT, SB>::elems;
     __shared__ float part[kEmbedThreads * E];
     const int tx = threadIdx.x, ty = threadIdx.y, TX = blockDim.x, TY = blockDim.y;
     pdl_trigger();
@@ -550,28 +585,28 @@ embed_join_kernel(const __grid_constant__ SumArgs a) {
         const int64_t block = is_long ? unit - q * a.col_blocks : (unit - longs - q * wide_blocks) * TY + ty;
         const int tile = static_cast<int>(a.cross[is_long ? q : a.tiles - 1 - q]);
         const int64_t slot = block * TX + tx;
-        const uint32_t run = a.key[static_cast<int64_t>(tile + 1) * kTile];
+        const uint32_t run = a.key[static_cast<int64_t>(tile + 1) * a.tile_len];
         // The last tile whose first token is of this run: 32 tiles looked at in one go,
         // then by halves.
         const int look = tile + 2 + (t & 31);
-        const bool more = look < a.tiles && a.key[static_cast<int64_t>(look) * kTile] == run;
+        const bool more = look < a.tiles && a.key[static_cast<int64_t>(look) * a.tile_len] == run;
         const uint32_t ends = ~__ballot_sync(0xffffffffu, more);
         int lo = tile + 1 + (ends == 0 ? 32 : __ffs(ends) - 1);
         if (ends == 0) {
             int hi = a.tiles - 1;
             while (lo < hi) {
                 const int mid = (lo + hi + 1) / 2;
-                if (a.key[static_cast<int64_t>(mid) * kTile] == run) lo = mid;
+                if (a.key[static_cast<int64_t>(mid) * a.tile_len] == run) lo = mid;
                 else hi = mid - 1;
             }
         }
-        float s[E];
+        Sums<E> s;
 #pragma unroll
-        for (int i = 0; i < E; ++i) s[i] = 0.0f;
+        for (int i = 0; i < E; ++i) s.v[i] = 0.0f;
         if (!is_long) {
             if (slot < a.slots) {
                 add_run<E>(s, a, slot, tile, true, tile + 1, lo + 1);
-                put_slot<DT, OT, VEC>(a, run, slot, s);
+                put_slot<DT, OT, SB>(a, run, slot, s);
             }
             continue;
         }
@@ -580,14 +615,14 @@ embed_join_kernel(const __grid_constant__ SumArgs a) {
         const int j1 = j0 + each < lo + 1 ? j0 + each : lo + 1;
         if (slot < a.slots) add_run<E>(s, a, slot, tile, ty == 0, j0, j1);
 #pragma unroll
-        for (int i = 0; i < E; ++i) part[i * (TX * TY) + t] = s[i];
+        for (int i = 0; i < E; ++i) part[i * (TX * TY) + t] = s.v[i];
         __syncthreads();
         if (ty == 0 && slot < a.slots) {
             for (int y = 1; y < TY && tile + 1 + y * each <= lo; ++y) {
 #pragma unroll
-                for (int i = 0; i < E; ++i) s[i] += part[i * (TX * TY) + y * TX + tx];
+                for (int i = 0; i < E; ++i) s.v[i] += part[i * (TX * TY) + y * TX + tx];
             }
-            put_slot<DT, OT, VEC>(a, run, slot, s);
+            put_slot<DT, OT, SB>(a, run, slot, s);
         }
         __syncthreads();
     }
@@ -605,35 +640,44 @@ bool misaligned(const void* p, uintptr_t bytes) { return reinterpret_cast<uintpt
 
 unsigned capped(int64_t n, int64_t most) { return static_cast<unsigned>(n < 1 ? 1 : n < most ? n : most); }
 
-bool rows_aligned(const void* p, int64_t stride, int64_t eb) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (stride * eb) % 16 == 0;
+// The slot that rows of D elements on both sides allow.
+template <int DT>
+int slot_bytes(const void* p, int64_t stride, const void* q, int64_t stride_q, int64_t eb_q, int64_t D) {
+    constexpr int64_t eb = DType<DT>::bytes;
+    const auto fits = [&](int64_t sb) {
+        return reinterpret_cast<uintptr_t>(p) % sb == 0 && stride * eb % sb == 0 && D * eb % sb == 0 &&
+               reinterpret_cast<uintptr_t>(q) % sb == 0 && stride_q * eb_q % sb == 0;
+    };
+    return fits(16) ? 16 : fits(4) ? 4 : static_cast<int>(eb);
 }
 
-template <int DT, bool VEC, int U>
+template <int DT, int SB, int U>
 cudaError_t launch_embed_u(EmbedArgs a, cudaStream_t stream) {
-    const int64_t slots = VEC ? a.D / (16 / DType<DT>::bytes) : a.D;
+    const int64_t slots = a.D / Slot<DT, SB>::elems;
     a.segments = (slots + 32 * U - 1) / (32 * U);
     const int64_t ctas = (a.T * a.segments * 32 + kEmbedThreads - 1) / kEmbedThreads;
-    return launch_pdl(embed_kernel<DT, VEC, U>, dim3(capped(ctas, INT_MAX)), dim3(kEmbedThreads), stream, a);
+    return launch_pdl(embed_kernel<DT, SB, U>, dim3(capped(ctas, INT_MAX)), dim3(kEmbedThreads), stream, a);
 }
 
-// One slot per lane for small calls, where latency counts; else as many loads in
-// flight as a warp's segment holds.
+// One slot per lane for small calls, where latency counts; else about 64 bytes of each
+// row in flight per lane.
+template <int DT, int SB>
+cudaError_t launch_embed_sb(const EmbedArgs& a, cudaStream_t stream) {
+    const bool small = a.T * (a.D / Slot<DT, SB>::elems) <= 1 << 17;
+    return small ? launch_embed_u<DT, SB, 1>(a, stream) : launch_embed_u<DT, SB, SB == 16 ? 4 : 16>(a, stream);
+}
+
 template <int DT>
 cudaError_t launch_embed(const EmbedArgs& a, cudaStream_t stream) {
-    constexpr int eb = DType<DT>::bytes;
-    const bool vec = rows_aligned(a.table, a.table_stride, eb) && rows_aligned(a.out, a.out_stride, eb) &&
-                     (a.D * eb) % 16 == 0;
-    const int64_t slots = vec ? a.D * eb / 16 : a.D;
-    const bool small = a.T * slots <= 1 << 17;
-    if (vec) return small ? launch_embed_u<DT, true, 1>(a, stream) : launch_embed_u<DT, true, 4>(a, stream);
-    return small ? launch_embed_u<DT, false, 1>(a, stream) : launch_embed_u<DT, false, 8>(a, stream);
+    const int sb = slot_bytes<DT>(a.table, a.table_stride, a.out, a.out_stride, DType<DT>::bytes, a.D);
+    if (sb == 16) return launch_embed_sb<DT, 16>(a, stream);
+    if (DT == kF32 || sb == 4) return launch_embed_sb<DT, 4>(a, stream);
+    return launch_embed_sb<DT, DType<DT>::bytes>(a, stream);
 }
 
-template <int DT, int OT, bool VEC>
+template <int DT, int OT, int SB>
 cudaError_t launch_sums(SumArgs a, cudaStream_t stream) {
-    a.slots = VEC ? a.D / Slot<DT, VEC>::elems : a.D;
-    a.tiles = static_cast<int>((static_cast<int64_t>(a.T) + kTile - 1) / kTile);
+    a.slots = a.D / Slot<DT, SB>::elems;
     const bool join = a.tiles > 1;
     // The rest of the rows to zero: a part for the joining kernel, if there is
     // one, for which it would take about as long as its longest run.
@@ -649,8 +693,8 @@ cudaError_t launch_sums(SumArgs a, cudaStream_t stream) {
     if (ctas > INT_MAX) return cudaErrorInvalidValue;
     cudaError_t e = cudaSuccess;
     if (ctas > 0)
-        e = launch_pdl_smem(embed_sum_kernel<DT, OT, VEC>, dim3(static_cast<unsigned>(ctas)), dim3(TX, TY),
-                            sizeof(uint32_t) * TY * (2 * kTile + 2), stream, a);
+        e = launch_pdl_smem(embed_sum_kernel<DT, OT, SB>, dim3(static_cast<unsigned>(ctas)), dim3(TX, TY),
+                            sizeof(uint32_t) * TY * (2 * a.tile_len + 2), stream, a);
     if (e != cudaSuccess || !join) return e;
     // Narrow column blocks, so that several groups of threads share a long run.
     const int JX = TX < 32 ? TX : 32;
@@ -659,20 +703,22 @@ cudaError_t launch_sums(SumArgs a, cudaStream_t stream) {
     a.col_blocks = (a.slots + JX - 1) / JX;
     a.sum_ctas = (a.tiles - 1) * a.col_blocks < kJoinCtas ? (a.tiles - 1) * a.col_blocks : kJoinCtas;
     if (a.sum_ctas + a.zero.groups > INT_MAX) return cudaErrorInvalidValue;
-    return launch_pdl(embed_join_kernel<DT, OT, VEC>, dim3(static_cast<unsigned>(a.sum_ctas + a.zero.groups)),
+    return launch_pdl(embed_join_kernel<DT, OT, SB>, dim3(static_cast<unsigned>(a.sum_ctas + a.zero.groups)),
                       dim3(JX, kEmbedThreads / JX), stream, a);
+}
+
+template <int DT, int OT>
+cudaError_t launch_sums_slot(const SumArgs& a, cudaStream_t stream) {
+    const int sb = slot_bytes<DT>(a.grad, a.grad_stride, a.dtable, a.dtable_stride, DType<OT>::bytes, a.D);
+    if (sb == 16) return launch_sums<DT, OT, 16>(a, stream);
+    if (DT == kF32 || sb == 4) return launch_sums<DT, OT, 4>(a, stream);
+    return launch_sums<DT, OT, DType<DT>::bytes>(a, stream);
 }
 
 template <int DT>
 cudaError_t launch_sums_dt(const SumArgs& a, int out_dtype, cudaStream_t stream) {
-    const int64_t eb = DType<DT>::bytes, ob = out_dtype == LSE_F32 ? 4 : 2;
-    const bool vec = rows_aligned(a.grad, a.grad_stride, eb) && rows_aligned(a.dtable, a.dtable_stride, ob) &&
-                     (a.D * eb) % 16 == 0 && (a.D * ob) % 16 == 0;
-    if constexpr (DT != kF32) {
-        if (out_dtype != LSE_F32)
-            return vec ? launch_sums<DT, DT, true>(a, stream) : launch_sums<DT, DT, false>(a, stream);
-    }
-    return vec ? launch_sums<DT, kF32, true>(a, stream) : launch_sums<DT, kF32, false>(a, stream);
+    if (DT == kF32 || out_dtype == LSE_F32) return launch_sums_slot<DT, kF32>(a, stream);
+    return launch_sums_slot<DT, DT>(a, stream);
 }
 
 int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
@@ -698,8 +744,9 @@ lse_status embed_backward(SumArgs a, lse_dtype dtype, lse_dtype out_dtype, const
     a.zero.stride_bytes = a.dtable_stride * ob;
     a.zero.rows = a.V;
     a.zero.groups = a.accumulate ? 0 : (a.V + kZeroRows - 1) / kZeroRows;
-    a.zero.unit = rows_aligned(a.dtable, a.dtable_stride, ob) && a.zero.row_bytes % 16 == 0 ? 16 : static_cast<int>(ob);
-    a.zero.units = a.zero.row_bytes / a.zero.unit;
+    a.zero.eb = static_cast<int>(ob);
+    const bool whole = reinterpret_cast<uintptr_t>(a.dtable) % 16 == 0 && a.zero.stride_bytes % 16 == 0 && a.zero.row_bytes % 16 == 0;
+    a.zero.vectors = whole ? a.zero.row_bytes / 16 : 0;
     if (a.T > 0) {
         // Blocks of at least one round of tokens, at most kSortMaxBlocks of them.
         SortArgs s;
@@ -717,7 +764,11 @@ lse_status embed_backward(SumArgs a, lse_dtype dtype, lse_dtype out_dtype, const
         const int passes = (bits + kSortMaxBits - 1) / kSortMaxBits;
         const int per = (bits + passes - 1) / passes;
 
-        const int64_t tiles = (static_cast<int64_t>(a.T) + kTile - 1) / kTile;
+        // Longer tiles leave fewer partial sums, shorter ones more CTAs: 64 tokens measured
+        // 127 against 130 us with 32 for 32768 tokens of 2048 columns.
+        a.tile_len = a.T >= 1 << 15 ? 64 : a.T >= 1 << 11 ? 32 : 16;
+        const int64_t tiles = (static_cast<int64_t>(a.T) + a.tile_len - 1) / a.tile_len;
+        a.tiles = static_cast<int>(tiles);
         const int64_t list = round_up(static_cast<int64_t>(a.T) * 4, 256);
         const int64_t counts = round_up((static_cast<int64_t>(blocks) << per) * 4, 256);
         const int64_t bitmap = round_up((a.V + 31) / 32 * 4, 256);
