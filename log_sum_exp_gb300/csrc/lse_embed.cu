@@ -789,12 +789,11 @@ lse_status embed_backward(SumArgs a, lse_dtype dtype, lse_dtype out_dtype, const
         a.zero.bitmap = s.bitmap;
         s.blocks = blocks;
 
-        // Before the bitmap is known, rows are zeroed whether they have tokens or not:
-        // worth it while most have none.
-        const bool blind = 2 * static_cast<int64_t>(a.T) <= a.V;
+        // Before the bitmap is known, rows are zeroed whether they have tokens or not: the
+        // memory would be idle.
         s.bits = per;
         s.counts = reinterpret_cast<uint32_t*>(count0);
-        s.zero = take_zero_rows(&a.zero, blind ? kCountZeroBytes : 0, nullptr);
+        s.zero = take_zero_rows(&a.zero, kCountZeroBytes, nullptr);
         // (behind the first pass's counts: the later passes', the bitmap, the list's lengths)
         e = launch_pdl(sort_count_kernel, dim3(static_cast<unsigned>(blocks + s.zero.groups)), dim3(kSortThreads), stream,
                        s, reinterpret_cast<uint32_t*>(count0 + counts), ((passes - 1) * counts + bitmap) / 4 + 2);
@@ -807,7 +806,7 @@ lse_status embed_backward(SumArgs a, lse_dtype dtype, lse_dtype out_dtype, const
             s.at_in = at[(p + 1) & 1];
             s.key_out = key[p & 1];
             s.at_out = at[p & 1];
-            s.zero = p == 0 ? take_zero_rows(&a.zero, blind ? kSortZeroBytes : 0, nullptr)
+            s.zero = p == 0 ? take_zero_rows(&a.zero, kSortZeroBytes, nullptr)
                             : take_zero_rows(&a.zero, kSortZeroBytes, s.bitmap);
             const dim3 grid(static_cast<unsigned>(blocks + s.zero.groups));
             e = p == 0 ? launch_pdl(sort_move_kernel<true>, grid, dim3(kSortThreads), stream, s)
