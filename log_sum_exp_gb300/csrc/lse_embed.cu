@@ -363,10 +363,11 @@ sort_move_kernel(const __grid_constant__ SortArgs a) {
                 atomicAdd(&a.next_counts[((to >> a.block_shift) << a.next_bits) +
                                          ((key[j] >> (a.shift + a.bits)) & ((1u << a.next_bits) - 1))], 1u);
             if (FIRST && key[j] < a.V) {
-                // (looked at first: the bits of frequent ids share few words)
+                // (looked at first, in L1: the bits of frequent ids share few words; a stale
+                // look costs one more atomic)
                 uint32_t* const word = &a.bitmap[key[j] >> 5];
                 const uint32_t bit = 1u << (key[j] & 31);
-                if ((__ldcg(word) & bit) == 0) atomicOr(word, bit);
+                if ((__ldca(word) & bit) == 0) atomicOr(word, bit);
             }
         }
         __syncthreads();
@@ -408,9 +409,32 @@ struct SumArgs {
     ZeroRows zero;
 };
 
-// A slot's sums.
+// A slot's sums, and the same while they are added up (two at a time, packed FP32).
 template <int E> struct Sums {
     float v[E];
+};
+template <int E> struct Total {
+    uint64_t pair[E / 2];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) pair[i] = 0ull;
+    }
+    __device__ __forceinline__ void add(const float (&y)[E]) {
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) pair[i] = f2_add(pair[i], f2_pack(y[2 * i], y[2 * i + 1]));
+    }
+    __device__ __forceinline__ Sums<E> sums() const {
+        Sums<E> s;
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) f2_unpack(pair[i], s.v[2 * i], s.v[2 * i + 1]);
+        return s;
+    }
+};
+template <> struct Total<1> {
+    float v;
+    __device__ __forceinline__ void clear() { v = 0.0f; }
+    __device__ __forceinline__ void add(const float (&y)[1]) { v += y[0]; }
+    __device__ __forceinline__ Sums<1> sums() const { return Sums<1>{{v}}; }
 };
 
 // dtable's slot of row v: scale * sum, plus what was there.
@@ -451,7 +475,6 @@ __device__ __forceinline__ void put_partial(float* to, const SumArgs& a, int til
 template <int DT, int OT, int SB>
 __device__ __forceinline__ void end_run(const SumArgs& a, uint32_t run, bool began_before, bool goes_on, int tile,
                                      int64_t slot, Sums<Slot<DT, SB>::elems> s) {
-    if (run >= a.V) return;
     if (began_before) put_partial(a.head, a, tile, slot, s);
     else if (goes_on) put_partial(a.tail, a, tile, slot, s);
     else put_slot<DT, OT, SB>(a, run, slot, s);
@@ -489,42 +512,39 @@ embed_sum_kernel(const __grid_constant__ SumArgs a) {
     __syncthreads();
     if (tile0 + ty >= a.tiles || slot >= a.slots) return;
     const int tile = static_cast<int>(tile0 + ty);
-    const int n = a.T - i0 < len ? static_cast<int>(a.T - i0) : len;
     const char* col = a.grad + slot * SB;
     const int64_t row_bytes = a.grad_stride * DType<DT>::bytes;
 
-    Sums<E> s;
-#pragma unroll
-    for (int i = 0; i < E; ++i) s.v[i] = 0.0f;
+    // (tokens that add nothing sort last)
+    int n = a.T - i0 < len ? static_cast<int>(a.T - i0) : len;
+    while (n > 0 && key[n] >= a.V) --n;
+    if (n == 0) return;
+    Total<E> s;
+    s.clear();
     uint32_t run = key[1];
     bool began_before = key[0] == run;
     for (int e0 = 0; e0 < n; e0 += U) {
         typename S::Raw v[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (e0 + u >= n || key[e0 + u + 1] >= a.V) continue;
-            v[u] = S::load(col + static_cast<int64_t>(at[e0 + u]) * row_bytes);
-        }
+        for (int u = 0; u < U; ++u)
+            if (e0 + u < n) v[u] = S::load(col + static_cast<int64_t>(at[e0 + u]) * row_bytes);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (e0 + u >= n) break;
             const uint32_t k = key[e0 + u + 1];
             if (k != run) {
-                end_run<DT, OT, SB>(a, run, began_before, false, tile, slot, s);
-#pragma unroll
-                for (int i = 0; i < E; ++i) s.v[i] = 0.0f;
+                end_run<DT, OT, SB>(a, run, began_before, false, tile, slot, s.sums());
+                s.clear();
                 run = k;
                 began_before = false;
             }
-            if (k >= a.V) break;  // (they sort last)
             float y[E];
             S::unpack(v[u], y);
-#pragma unroll
-            for (int i = 0; i < E; ++i) s.v[i] += y[i];
+            s.add(y);
         }
     }
-    const bool goes_on = !began_before && run < a.V && key[n + 1] == run;
-    end_run<DT, OT, SB>(a, run, began_before, goes_on, tile, slot, s);
+    const bool goes_on = !began_before && key[n + 1] == run;
+    end_run<DT, OT, SB>(a, run, began_before, goes_on, tile, slot, s.sums());
     if (goes_on && slot == 0) {  // long runs from the list's front, others from its back
         const int64_t far = i0 + (kLongRun + 1) * len;
         if (far < a.T && a.key[far] == run) a.cross[atomicAdd(a.cross_count, 1u)] = static_cast<uint32_t>(tile);
