@@ -195,6 +195,7 @@ def _token_stats_function(torch):
             return tuple(s)
 
         @staticmethod
+        @torch.autograd.function.once_differentiable
         def backward(ctx, g_lp, g_ent, g_lse, g_top, _):
             x, target, ent, lse, top_index = ctx.saved_tensors
             g = [None if t is None else t.to(torch.float32).contiguous()
@@ -292,7 +293,8 @@ class GradList:
             for p in {g.data_ptr(), o.data_ptr() if o is not None else g.data_ptr()}:
                 if g.numel() and p in seen:
                     raise ValueError("a tensor stands in the list twice")
-                seen.add(p)
+                if g.numel():
+                    seen.add(p)
             self._table[i] = LseTensor(g.data_ptr() or None, o.data_ptr() or None if o is not None else None,
                                        g.numel(), dt)
 
@@ -435,6 +437,7 @@ def _embedding_function(torch):
             return lse_embedding(table, ids, scale, stream=stream)
 
         @staticmethod
+        @torch.autograd.function.once_differentiable
         def backward(ctx, g):
             (ids,) = ctx.saved_tensors
             (V, D), scale, padding, stream = ctx.args

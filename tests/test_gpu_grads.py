@@ -173,6 +173,11 @@ def test_beyond_32_bits():
     assert (t[-5:] == 0.25).all() and (t[(1 << 31) - 3:(1 << 31) + 3] == 0.25).all() and t[0] == 0.25
 
 
+def test_empty_views_next_to_their_tensor():
+    t = torch.randn(1000, device="cuda")
+    check_norm(L.lse_grad_norm([t[:0], t, t[:0]]), [t])
+
+
 def test_refusals():
     a = torch.zeros(4, device="cuda")
     for call in [lambda: L.lse_grad_norm([]), lambda: L.lse_grad_norm([a.cpu()]),

@@ -433,6 +433,14 @@ def test_autograd():
     assert torch.isfinite(x2.grad).all()
 
 
+def test_second_derivatives_are_refused():
+    x = torch.randn((3, 40), device="cuda", requires_grad=True)
+    s = L.token_stats(x)
+    (g,) = torch.autograd.grad(s.entropy.sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()
+
+
 def test_refusals():
     x = torch.zeros((4, 10), device="cuda")
     t = torch.zeros(4, dtype=torch.int64, device="cuda")
