@@ -999,24 +999,23 @@ cudaError_t launch_stats(StatsArgs a, int sms, cudaStream_t stream) {
         return a.K <= 24 ? launch_stats_short<DT, 32, 1>(a, vectors, sms, stream)
                          : launch_stats_short<DT, 32, 2>(a, vectors, sms, stream);
     }
-    // Threads of a CTA: enough for one batch of the row each; at most 128 when rows
-    // are plentiful, so that rows at their ends overlap with rows under way.
+    // Threads of a CTA: 256 while rows are few (10 rows of 16384 bf16: 4.8 us against 5.8
+    // with 128); otherwise 128, so that rows at their ends overlap with more rows under way
+    // (400 rows of 8192 f32: 7.0 against 7.3), but for long rows 256 up to 4 rows per SM.
     int T = 256;
-    while (T > 128 && vectors < 2LL * stat_u(T) * T) T /= 2;
-    if (a.B >= 4LL * sms) T = 128;
+    if (a.B >= 4LL * sms || (a.B > 2LL * sms && vectors < 2LL * stat_u(T) * T)) T = 128;
     // Rows of up to 1024 vectors by the thousand: a warp each.
     if (vectors <= 1024 && a.B >= 16LL * sms && a.K <= 24) T = 32;
     // Few rows: a cluster of 256-thread CTAs per row, as many as leave each three quarters
-    // of a batch and together fill two thirds of the GPU (128256 bf16, K = 20: one row
+    // of a batch and together are resident at once (128256 bf16, K = 20: one row
     // 6.4 us with 8 CTAs, 7.4 with 4, 6.6 with 16; 96 rows of 100003 f32 16.8 with 4, 18.8
     // alone); two CTAs do not pay for the cluster's barriers (19.6).
     int P = 1;
     if (a.B < sms) {
         while (2 * P <= kMaxCluster && vectors >= 2LL * P * (stat_u(256) * 256 * 3 / 4) &&
-               a.B * (2 * P) * 256 * 3 <= 2LL * 1024 * sms)
+               a.B * (2 * P) * 256 <= 1024LL * sms)
             P *= 2;
         if (P < 4) P = 1;
-        else T = 256;
     }
     a.cluster = P;
     const int64_t batches = ((vectors + P - 1) / P + stat_u(T) * T - 1) / (stat_u(T) * T);
