@@ -126,29 +126,31 @@ def lse_token_stats_backward(x, stats: TokenStats, target=None, grad_logprob=Non
         raise ValueError("x must be a CUDA tensor")
     dt = DTYPES[_dtype_name(x)]
     B, N, row_stride = _rows(x)
+    device, f32, i64 = x.device, torch.float32, torch.int64
     K = stats.top_index.shape[-1] if stats.top_index is not None else 0
-    _need_vector(stats.lse, "stats.lse", torch.float32, B, x.device)
-    for name, g, n in (("grad_logprob", grad_logprob, B), ("grad_entropy", grad_entropy, B),
-                       ("grad_top", grad_top, B * K), ("grad_lse", grad_lse, B)):
-        if g is not None:
-            _need_vector(g, name, torch.float32, n, x.device)
+    _need_vector(stats.lse, "stats.lse", f32, B, device)
     if grad_logprob is not None:
         if target is None:
             raise ValueError("grad_logprob needs target")
-        _need_vector(target, "target", torch.int64, B, x.device)
+        _need_vector(grad_logprob, "grad_logprob", f32, B, device)
+        _need_vector(target, "target", i64, B, device)
     if grad_entropy is not None:
         if stats.entropy is None:
             raise ValueError("grad_entropy needs stats.entropy")
-        _need_vector(stats.entropy, "stats.entropy", torch.float32, B, x.device)
+        _need_vector(grad_entropy, "grad_entropy", f32, B, device)
+        _need_vector(stats.entropy, "stats.entropy", f32, B, device)
     if grad_top is not None:
         if stats.top_index is None:
             raise ValueError("grad_top needs stats.top_index")
-        _need_vector(stats.top_index, "stats.top_index", torch.int64, B * K, x.device)
-    if dx is not None and (dx.shape != x.shape or dx.dtype != x.dtype or dx.device != x.device):
+        _need_vector(grad_top, "grad_top", f32, B * K, device)
+        _need_vector(stats.top_index, "stats.top_index", i64, B * K, device)
+    if grad_lse is not None:
+        _need_vector(grad_lse, "grad_lse", f32, B, device)
+    if dx is not None and (dx.shape != x.shape or dx.dtype != x.dtype or dx.device != device):
         raise ValueError("dx must match x's shape, dtype and device")
     args = (torch, x, dt, B, N, row_stride, stats, target, K, grad_logprob, grad_entropy, grad_top,
-            grad_lse, dx, stream, x.device)
-    return _stats_backward_call(*args) if _at_home(torch, stream, x.device) \
+            grad_lse, dx, stream, device)
+    return _stats_backward_call(*args) if _at_home(torch, stream, device) \
         else _elsewhere(_stats_backward_call, args)
 
 
