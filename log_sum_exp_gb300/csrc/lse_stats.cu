@@ -98,7 +98,7 @@ __device__ __forceinline__ uint4 grad_vector(uint4 v, const RowGrad& g) {
 }
 
 constexpr int kGradU = 4;        // vectors (or elements) per thread and step
-constexpr int kGradCta = 256;    // threads of a CTA of one-warp units
+constexpr int kGradCta = 256;    // threads of a CTA whose rows take a warp or less
 
 // Slots [k0, k1) of a row: the 16-byte vectors that cover it (VEC; x and dx rows at
 // the same offset from a boundary), the outer ones stored element by element, or
@@ -162,12 +162,14 @@ __device__ __forceinline__ void zero_slots(char* dr, int off, int64_t end, int64
 }
 
 template <int DT, int TX, bool VEC>
-__global__ void __launch_bounds__(TX == 32 ? kGradCta : TX, TX == 32 ? 4 : 1024 / TX)
+__global__ void __launch_bounds__(TX <= 32 ? kGradCta : TX, TX <= 32 ? 4 : 1024 / TX)
 lse_stats_backward_kernel(const __grid_constant__ StatsBackwardArgs a) {
-    constexpr int EB = DType<DT>::bytes, UNITS = TX == 32 ? kGradCta / 32 : 1;
-    const int tid = threadIdx.x % TX, lane = threadIdx.x & 31;
-    const auto sync = [] {
-        if (TX == 32) __syncwarp();
+    constexpr int EB = DType<DT>::bytes, UNITS = TX <= 32 ? kGradCta / TX : 1;
+    constexpr int W = TX < 32 ? TX : 32;  // lanes that share a row's gradients
+    const int tid = threadIdx.x % TX, lane = threadIdx.x & (W - 1);
+    const uint32_t group = W == 32 ? 0xffffffffu : ((1u << (W & 31)) - 1) << (threadIdx.x & 31 & ~(W - 1));
+    const auto sync = [group] {
+        if (TX <= 32) __syncwarp(group);
         else __syncthreads();
     };
     pdl_trigger();
@@ -189,33 +191,38 @@ lse_stats_backward_kernel(const __grid_constant__ StatsBackwardArgs a) {
         const int64_t n0 = VEC ? (k0 == 0 ? 0 : (k0 * 16 - off) / EB) : k0;
         const int64_t n1 = VEC ? (k1 == slots ? a.N : (k1 * 16 - off) / EB) : k1;
 
-        // The row's gradients (every warp for itself).
+        // The row's gradients (every group of W lanes for itself; K <= W), all loaded at once.
         RowGrad g;
         g.lse = __ldg(a.lse + row);
         const int64_t t = a.grad_logprob ? __ldg(a.target + row) : -1;
-        const bool in_row = t >= 0 && t < a.N;
-        const float gl = in_row ? __ldg(a.grad_logprob + row) : 0.0f;
+        float gl = a.grad_logprob ? __ldg(a.grad_logprob + row) : 0.0f;
         const float gs = a.grad_lse ? __ldg(a.grad_lse + row) : 0.0f;
         g.gh = a.grad_entropy ? __ldg(a.grad_entropy + row) : 0.0f;
+        const float h = a.grad_entropy ? __ldg(a.entropy + row) : 0.0f;
         int64_t ti = -1;  // lane k: alternative k
         float gt = 0.0f;
         if (lane < a.K) {
             ti = __ldg(a.top_index + row * a.K + lane);
-            if (ti < 0 || ti >= a.N) ti = -1;
-            else gt = __ldg(a.grad_top + row * a.K + lane);
+            gt = __ldg(a.grad_top + row * a.K + lane);
+        }
+        const bool in_row = t >= 0 && t < a.N;
+        if (!in_row) gl = 0.0f;
+        if (ti < 0 || ti >= a.N) {
+            ti = -1;
+            gt = 0.0f;
         }
         float sum = gt;
         if (a.K > 0) {
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            for (int o = W / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(group, sum, o, W);
         }
-        const bool any = gl != 0.0f || gs != 0.0f || g.gh != 0.0f || __any_sync(0xffffffffu, gt != 0.0f);
+        const bool any = gl != 0.0f || gs != 0.0f || g.gh != 0.0f || __any_sync(group, gt != 0.0f);
         if (!any) {
             zero_slots<DT, TX, VEC>(dr, off, end, k0, k1, tid);
             continue;  // (the same for the whole unit)
         }
         g.A = gs - gl - sum;
-        if (g.gh != 0.0f) g.A = fmaf(-g.gh, __ldg(a.entropy + row), g.A);
+        if (g.gh != 0.0f) g.A = fmaf(-g.gh, h, g.A);
 
         // The first warp keeps the elements with a unit term.
         const bool first = tid < 32;
@@ -224,15 +231,15 @@ lse_stats_backward_kernel(const __grid_constant__ StatsBackwardArgs a) {
         bool target_alone = false;
         if (first && a.K > 0) {
             for (int k = 0; k < a.K; ++k) {
-                const int64_t ok = __shfl_sync(0xffffffffu, ti, k);
-                const float gk = __shfl_sync(0xffffffffu, gt, k);
+                const int64_t ok = __shfl_sync(group, ti, k, W);
+                const float gk = __shfl_sync(group, gt, k, W);
                 if (ok == ti) unit_term += gk;
             }
             if (ti == t && in_row) unit_term += gl;
             if (mine) x_mine = load_elem<DT>(xr, ti);
         }
         if (first && in_row && t >= n0 && t < n1) {
-            target_alone = !__any_sync(0xffffffffu, ti == t);
+            target_alone = !__any_sync(group, ti == t);
             if (target_alone && lane == 0) x_target = load_elem<DT>(xr, t);
         }
         sync();
@@ -244,19 +251,20 @@ lse_stats_backward_kernel(const __grid_constant__ StatsBackwardArgs a) {
     }
 }
 
-template <int DT, int TX, bool VEC>
-cudaError_t launch_stats_backward_tx(const StatsBackwardArgs& a, cudaStream_t stream) {
-    constexpr int64_t units_per_cta = TX == 32 ? kGradCta / 32 : 1;
+template <int DT, int TX>
+cudaError_t launch_stats_backward_tx(const StatsBackwardArgs& a, bool vec, cudaStream_t stream) {
+    constexpr int64_t units_per_cta = TX <= 32 ? kGradCta / TX : 1;
     const int64_t ctas = (a.B * a.segments + units_per_cta - 1) / units_per_cta;
-    return launch_pdl(lse_stats_backward_kernel<DT, TX, VEC>,
-                      dim3(static_cast<unsigned>(ctas < INT_MAX ? ctas : INT_MAX)), dim3(TX == 32 ? kGradCta : TX),
-                      stream, a);
+    const dim3 grid(static_cast<unsigned>(ctas < INT_MAX ? ctas : INT_MAX)), block(TX <= 32 ? kGradCta : TX);
+    return vec ? launch_pdl(lse_stats_backward_kernel<DT, TX, true>, grid, block, stream, a)
+               : launch_pdl(lse_stats_backward_kernel<DT, TX, false>, grid, block, stream, a);
 }
 
 // Vectors where each x row and its dx row sit at the same offset from a 16-byte
-// boundary, elements otherwise.  A warp per row of up to 256 slots, 128 threads up to
-// 1024, 256 beyond; longer rows in segments of up to 16 slots per thread, shorter
-// ones while the segments would not fill the GPU.
+// boundary, elements otherwise.  8, 16 or 32 lanes per row of up to 64, 128 or 256 slots
+// (and no more alternatives than lanes), 128 threads up to 1024, 256 beyond; longer rows
+// in segments of up to 16 slots per thread, shorter ones while the segments would not
+// fill the GPU.
 template <int DT>
 cudaError_t launch_stats_backward(StatsBackwardArgs a, int sms, cudaStream_t stream) {
     const int64_t eb = DType<DT>::bytes;
@@ -264,20 +272,20 @@ cudaError_t launch_stats_backward(StatsBackwardArgs a, int sms, cudaStream_t str
     const bool vec = (xa - da) % 16 == 0 && ((a.row_stride - a.dx_row_stride) * eb) % 16 == 0;
     const bool aligned = xa % 16 == 0 && (a.row_stride * eb) % 16 == 0;
     const int64_t slots = vec ? (a.N * eb + 15) / 16 + (aligned ? 0 : 1) : a.N;  // at most
-    const int TX = slots <= 256 ? 32 : slots <= 1024 ? 128 : 256;
+    const int TX = slots <= 64 && a.K <= 8 ? 8 : slots <= 128 && a.K <= 16 ? 16 : slots <= 256 ? 32 : slots <= 1024 ? 128 : 256;
     int64_t steps = 4;
     while (TX > 32 && steps > 1 && a.B * ((slots + steps * kGradU * TX - 1) / (steps * kGradU * TX)) * TX < 1024LL * sms)
         --steps;
-    a.seg_slots = TX == 32 ? slots : steps * kGradU * TX;
+    a.seg_slots = TX <= 32 ? slots : steps * kGradU * TX;
     a.segments = (slots + a.seg_slots - 1) / a.seg_slots;
     if (a.B > INT64_MAX / a.segments) return cudaErrorInvalidValue;
-    if (vec)
-        return TX == 32 ? launch_stats_backward_tx<DT, 32, true>(a, stream)
-               : TX == 128 ? launch_stats_backward_tx<DT, 128, true>(a, stream)
-                           : launch_stats_backward_tx<DT, 256, true>(a, stream);
-    return TX == 32 ? launch_stats_backward_tx<DT, 32, false>(a, stream)
-           : TX == 128 ? launch_stats_backward_tx<DT, 128, false>(a, stream)
-                       : launch_stats_backward_tx<DT, 256, false>(a, stream);
+    switch (TX) {
+    case 8: return launch_stats_backward_tx<DT, 8>(a, vec, stream);
+    case 16: return launch_stats_backward_tx<DT, 16>(a, vec, stream);
+    case 32: return launch_stats_backward_tx<DT, 32>(a, vec, stream);
+    case 128: return launch_stats_backward_tx<DT, 128>(a, vec, stream);
+    default: return launch_stats_backward_tx<DT, 256>(a, vec, stream);
+    }
 }
 
 // The checks that the forward and the backward share beyond check_args.

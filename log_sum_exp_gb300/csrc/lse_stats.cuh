@@ -242,6 +242,14 @@ __device__ __forceinline__ float round16(float x) {
     return DT == kF32 ? word_lo<kBF16>(pack2<kBF16>(x, x)) : x;  // (16-bit elements are as they are)
 }
 
+// A value that no f32 maximum kept as bf16 v lies below (16-bit ones are as they are).
+template <int DT>
+__device__ __forceinline__ float step_down(float v) {
+    if (DT != kF32 || !(fabsf(v) <= 3.4e38f)) return DT == kF32 && v > 0.0f ? 3.3e38f : v;
+    const float d = v - fmaxf(fabsf(v) * 0x1.0p-8f, 0x1.0p-126f);
+    return d;
+}
+
 // The maxima of the U / 2 pairs of neighbouring vectors of a batch, two per word, and
 // the largest of all.
 template <int DT, int U>
@@ -426,7 +434,7 @@ constexpr int kPartKeys = 48;     // keys that a part hands on as it found them
 template <int T, bool CLUSTER>
 struct StatsShared {
     static constexpr int kFoundList = T == 32 ? 128 : 512;  // elements that may reach the bound
-    float4 group_max4[T > 32 ? 16 : 8];
+    float4 group_max4[16];
     alignas(16) uint32_t chunk_max[stat_u(T) / 4 * stat_batches(T) * T];
     uint64_t found[kFoundList];
     uint64_t own[kMaxTopK];
@@ -531,13 +539,23 @@ lse_stats_kernel(const __grid_constant__ StatsArgs a) {
         if (in_chunk > 0) put_words<MW>(sh.chunk_max + (chunk * T + tid) * MW, chunk_max);
     }
     // The warp's maximum, and on the way to it those of `apart` neighbouring threads.
-    const bool wide = T > 32 && a.K > kWideGroupsK;
-    const int apart = wide ? NW / 2 : NW;
+    const bool wide = a.K > kWideGroupsK;
+    const int apart = wide && T > 32 ? NW / 2 : NW;
     float warp_max = acc.m;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         if (off == apart && tid % apart == 0) group_max[tid / apart] = warp_max;
         warp_max = fmaxf(warp_max, __shfl_xor_sync(0xffffffffu, warp_max, off));
+    }
+    if (T == 32 && wide) {
+        // Two groups per lane, from its chunks' maxima (two to a word).  f32 ones have been
+        // rounded to bf16, maybe up: one step down is a bound for sure.
+        const int64_t batches = (k_end - k_begin + U * T - 1) / (U * T);
+        const int groups = static_cast<int>((batches + (1 << a.chunk_shift) - 1) >> a.chunk_shift);
+        uint32_t both = DT == kF16 ? kNegInfF16x2 : kNegInfBF16x2;
+        for (int c = 0; c < groups; ++c) both = max2<DT>(both, sh.chunk_max[(c * T + tid) * MW]);
+        group_max[lane] = step_down<DT>(half_lo<DT>(both));
+        group_max[lane + 32] = step_down<DT>(half_hi<DT>(both));
     }
     acc = stat_shift<DT>(acc, warp_max);
 #pragma unroll
@@ -565,7 +583,7 @@ lse_stats_kernel(const __grid_constant__ StatsArgs a) {
     }
 
     if (a.K > 0) {
-        const float bound = wide ? kth_largest_of<T == 32 ? 32 : 64>(group_max, a.K, lane)
+        const float bound = wide ? kth_largest_of<64>(group_max, a.K, lane)
                                  : kth_largest_of<32>(group_max, a.K, lane);
         bool scan = nan || bound == __int_as_float(kNegInfF32);  // NaN, or too few left
         if (!scan && warp_max >= bound) {
@@ -830,18 +848,13 @@ lse_stats_short_kernel(const __grid_constant__ StatsArgs a) {
         float m;
         if constexpr (M == 1) {
             m = part_max[0] = words_max<DT, 4 * V>(w);
-        } else {  // the lane's first and last vectors
-            constexpr int H = (V + 1) / 2;
-            uint32_t first[4 * H];
+        } else {  // the halves of the lane's words
+            uint32_t half[2 * V];
 #pragma unroll
-            for (int i = 0; i < 4 * H; ++i) first[i] = w[i];
-            part_max[0] = words_max<DT, 4 * H>(first);
-            part_max[1] = __int_as_float(kNegInfF32);
-            if constexpr (V > 1) {
-                uint32_t last[4 * (V - H)];
+            for (int q = 0; q < 2; ++q) {
 #pragma unroll
-                for (int i = 0; i < 4 * (V - H); ++i) last[i] = w[4 * H + i];
-                part_max[1] = words_max<DT, 4 * (V - H)>(last);
+                for (int i = 0; i < 2 * V; ++i) half[i] = w[2 * V * q + i];
+                part_max[q] = words_max<DT, 2 * V>(half);
             }
             m = fmaxf(part_max[0], part_max[1]);
         }
@@ -1005,7 +1018,7 @@ cudaError_t launch_stats(StatsArgs a, int sms, cudaStream_t stream) {
     int T = 256;
     if (a.B >= 4LL * sms || (a.B > 2LL * sms && vectors < 2LL * stat_u(T) * T)) T = 128;
     // Rows of up to 1024 vectors by the thousand: a warp each.
-    if (vectors <= 1024 && a.B >= 16LL * sms && a.K <= 24) T = 32;
+    if (vectors <= 1024 && a.B >= 16LL * sms) T = 32;
     // Few rows: a cluster of 256-thread CTAs per row, as many as leave each three quarters
     // of a batch and together are resident at once (128256 bf16, K = 20: one row
     // 6.4 us with 8 CTAs, 7.4 with 4, 6.6 with 16; 96 rows of 100003 f32 16.8 with 4, 18.8
