@@ -36,7 +36,7 @@ struct StatsBackwardArgs {
 //     dx_n = p_n (A - gH log p_n) + gl [n = t] + sum_k gt_k [n = i_k],
 //     A = g_lse - gl - sum_k gt_k - gH H,   log p_n = x_n - lse
 //
-// TX threads take a segment of a row, four vectors each at a time, every load
+// TX threads take a segment of a row, two or four vectors each at a time, every load
 // issued before the stores.  The few elements with a unit term are read before
 // anything is stored (dx may be x) and written once more, whole, at the end, so the
 // loop compares no columns.
@@ -97,7 +97,8 @@ __device__ __forceinline__ uint4 grad_vector(uint4 v, const RowGrad& g) {
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-constexpr int kGradU = 4;        // vectors (or elements) per thread and step
+// Vectors (or elements) per thread and step.
+__host__ __device__ constexpr int grad_u(int TX) { return TX < 32 ? 2 : 4; }
 constexpr int kGradCta = 256;    // threads of a CTA whose rows take a warp or less
 
 // Slots [k0, k1) of a row: the 16-byte vectors that cover it (VEC; x and dx rows at
@@ -107,16 +108,17 @@ template <int DT, int TX, bool VEC, bool ENT>
 __device__ __forceinline__ void grad_slots(const char* xr, char* dr, int off, int64_t end, int64_t k0,
                                            int64_t k1, int tid, const RowGrad& g) {
     constexpr int EB = DType<DT>::bytes, EPV = 16 / EB;
-    for (int64_t k = k0 + tid; k < k1; k += kGradU * TX) {
+    constexpr int U = grad_u(TX);
+    for (int64_t k = k0 + tid; k < k1; k += U * TX) {
         if constexpr (VEC) {
             const char* x0 = xr - off;
             char* d0 = dr - off;
-            uint4 v[kGradU];
+            uint4 v[U];
 #pragma unroll
-            for (int j = 0; j < kGradU; ++j)
+            for (int j = 0; j < U; ++j)
                 if (k + j * TX < k1) v[j] = ldg_stream16(x0 + (k + j * TX) * 16);
 #pragma unroll
-            for (int j = 0; j < kGradU; ++j) {
+            for (int j = 0; j < U; ++j) {
                 const int64_t kk = k + j * TX;
                 if (kk >= k1) continue;
                 const uint4 o = grad_vector<DT, ENT>(v[j], g);
@@ -134,12 +136,12 @@ __device__ __forceinline__ void grad_slots(const char* xr, char* dr, int off, in
                 }
             }
         } else {
-            float v[kGradU];
+            float v[U];
 #pragma unroll
-            for (int j = 0; j < kGradU; ++j)
+            for (int j = 0; j < U; ++j)
                 if (k + j * TX < k1) v[j] = load_elem<DT>(xr, k + j * TX);
 #pragma unroll
-            for (int j = 0; j < kGradU; ++j)
+            for (int j = 0; j < U; ++j)
                 if (k + j * TX < k1) put_elem<DT>(dr, k + j * TX, grad_elem(v[j], g, 0.0f));
         }
     }
@@ -162,7 +164,7 @@ __device__ __forceinline__ void zero_slots(char* dr, int off, int64_t end, int64
 }
 
 template <int DT, int TX, bool VEC>
-__global__ void __launch_bounds__(TX <= 32 ? kGradCta : TX, TX <= 32 ? 4 : 1024 / TX)
+__global__ void __launch_bounds__(TX <= 32 ? kGradCta : TX, TX < 32 ? 5 : TX == 32 ? 4 : 1024 / TX)
 lse_stats_backward_kernel(const __grid_constant__ StatsBackwardArgs a) {
     constexpr int EB = DType<DT>::bytes, UNITS = TX <= 32 ? kGradCta / TX : 1;
     constexpr int W = TX < 32 ? TX : 32;  // lanes that share a row's gradients
@@ -261,9 +263,13 @@ cudaError_t launch_stats_backward_tx(const StatsBackwardArgs& a, bool vec, cudaS
 }
 
 // Vectors where each x row and its dx row sit at the same offset from a 16-byte
-// boundary, elements otherwise.  8, 16 or 32 lanes per row of up to 64, 128 or 256 slots
-// (and no more alternatives than lanes), 128 threads up to 1024, 256 beyond; longer rows
-// in segments of up to 16 slots per thread, shorter ones while the segments would not
+// boundary, elements otherwise.  8, 16 or 32 lanes per row of up to 64, 256 or 512 slots
+// (and no more alternatives than lanes), which waste fewer lanes and keep more rows in
+// flight (us; 468750 bf16 rows of 256: 8 lanes 112, 32 lanes about 330; 80000 bf16 rows
+// of 1500: 16 lanes 105, 32 lanes 108; 39986 bf16 rows of 3001: 32 lanes 93, 128 threads
+// 119; 5000 bf16 rows of 6000: 32 lanes 27, 128 threads 22.6); 128 threads up to 1024
+// slots, 256 beyond.  Few rows of more than 256 slots take 128 threads too.  Longer rows
+// go in segments of up to 16 slots per thread, shorter ones while the segments would not
 // fill the GPU.
 template <int DT>
 cudaError_t launch_stats_backward(StatsBackwardArgs a, int sms, cudaStream_t stream) {
@@ -272,11 +278,15 @@ cudaError_t launch_stats_backward(StatsBackwardArgs a, int sms, cudaStream_t str
     const bool vec = (xa - da) % 16 == 0 && ((a.row_stride - a.dx_row_stride) * eb) % 16 == 0;
     const bool aligned = xa % 16 == 0 && (a.row_stride * eb) % 16 == 0;
     const int64_t slots = vec ? (a.N * eb + 15) / 16 + (aligned ? 0 : 1) : a.N;  // at most
-    const int TX = slots <= 64 && a.K <= 8 ? 8 : slots <= 128 && a.K <= 16 ? 16 : slots <= 256 ? 32 : slots <= 1024 ? 128 : 256;
+    const int TX = slots <= 64 && a.K <= 8                   ? 8
+                   : slots <= 256 && a.K <= 16               ? 16
+                   : slots <= (a.B >= 8LL * sms ? 512 : 256) ? 32
+                   : slots <= 1024                           ? 128
+                                                             : 256;
     int64_t steps = 4;
-    while (TX > 32 && steps > 1 && a.B * ((slots + steps * kGradU * TX - 1) / (steps * kGradU * TX)) * TX < 1024LL * sms)
+    while (TX > 32 && steps > 1 && a.B * ((slots + steps * grad_u(TX) * TX - 1) / (steps * grad_u(TX) * TX)) * TX < 1024LL * sms)
         --steps;
-    a.seg_slots = TX <= 32 ? slots : steps * kGradU * TX;
+    a.seg_slots = TX <= 32 ? slots : steps * grad_u(TX) * TX;
     a.segments = (slots + a.seg_slots - 1) / a.seg_slots;
     if (a.B > INT64_MAX / a.segments) return cudaErrorInvalidValue;
     switch (TX) {

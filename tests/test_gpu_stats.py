@@ -481,3 +481,38 @@ def test_special_rows_by_the_thousand(dtype, N, K):
     t = torch.randint(0, N, (x.shape[0],), generator=torch.Generator().manual_seed(N))
     xd = place(x, offset=1, row_stride=N + 3)
     check(xd, x, t, K)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("N,K", [(1500, 32), (2311, 25), (4000, 31), (4100, 28), (8190, 32)])
+def test_many_alternatives_by_the_thousand(dtype, N, K):
+    """For K > 24 their bound comes from the kept 16-bit maxima: ties, masks, values that
+    round up (to infinity too) and one column that holds nearly all of the row."""
+    x = special_rows(N, dtype, seed=N)
+    g = torch.Generator().manual_seed(N + K)
+    more = torch.randn((8, N), generator=g)
+    more[0] = torch.finfo(torch.float32).max * (1 - 2.0 ** -12 * torch.rand(N, generator=g)) if dtype == "f32" else 60000.0
+    more[1] = 1.0 + 2.0 ** -9 * torch.rand(N, generator=g)     # one bf16 value, many f32 ones
+    more[2] = -1.0 - 2.0 ** -9 * torch.rand(N, generator=g)
+    more[3, :N - K] = -float("inf")                             # K left
+    more[4, :N - K + 1] = -float("inf")                         # one too few
+    more[5] = torch.arange(N) * 2.0 ** -6                       # the largest all at the end
+    more[6] = -torch.arange(N) * 2.0 ** -6
+    more[7] = torch.randint(0, 40, (N,), generator=g).float()
+    x = torch.cat([x, more.to(DT[dtype])])
+    x = x.repeat(2600 // x.shape[0] + 1, 1)
+    t = torch.randint(0, N, (x.shape[0],), generator=torch.Generator().manual_seed(N))
+    check(place(x, offset=2, row_stride=N + 1), x, t, K)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("N", [1, 63, 64, 65, 250, 257, 511, 1020, 1030, 2047, 4100])
+def test_gradient_of_many_short_rows(dtype, N):
+    """A few lanes per row, each row's gradients among them alone."""
+    x, t = rows(1300, N, dtype, seed=N)
+    t[::7] = -100
+    for i, K in enumerate((0, 7, 8, 9, 16, 17)):
+        lay = dict(offset=i % 4, row_stride=N + (0, 1, 8)[i % 3])
+        xd = place(x, **lay)
+        dx = (None, xd, place(torch.zeros_like(x)))[i % 3]
+        run_gradient(xd, x, t, min(K, N), dtype, dx=dx, seed=i)
