@@ -54,6 +54,19 @@ def _elsewhere(call, args):
         return call(*args)
 
 
+def _ordered(torch, stream, device, call):
+    """``call()``, a gradient on the forward's ``stream`` (None: the current one),
+    between what autograd has put on the current stream and what it puts there next."""
+    if stream is None:
+        return call()
+    here = torch.cuda.current_stream(device)
+    stream.wait_stream(here)
+    d = call()
+    here.wait_stream(stream)
+    d.record_stream(here)
+    return d
+
+
 def _need_vector(t, name, dtype, n, device):
     if t.dtype != dtype or t.device != device or t.numel() != n or not t.is_contiguous():
         kind = str(dtype).replace("torch.", "")
@@ -205,7 +218,9 @@ def _token_stats_function(torch):
             if all(t is None for t in g):
                 return None, None, None, None
             s = TokenStats(None, ent, lse, None, top_index)
-            return lse_token_stats_backward(x, s, target, *g, stream=ctx.stream), None, None, None
+            dx = _ordered(torch, ctx.stream, x.device,
+                          lambda: lse_token_stats_backward(x, s, target, *g, stream=ctx.stream))
+            return dx, None, None, None
 
     return TokenStatsFunction
 
@@ -261,7 +276,8 @@ class GradList:
     ``lse_grad_clip``, laid out once and used for many steps.
 
     The tensors may differ in shape and in type (float32, bfloat16, float16) but
-    share a device, and each fills its memory without gaps (any dimension order).
+    share a device but no memory, and each fills its own without gaps (any dimension
+    order).
     ``out`` (optional) gives the tensors that ``lse_grad_clip`` writes, with the
     shapes, strides and types of ``grads``; without it gradients are clipped in
     place.  The list holds its tensors alive and refers to their memory as it was
@@ -279,7 +295,7 @@ class GradList:
         if self.device.type != "cuda":
             raise ValueError("gradients must be CUDA tensors")
         self._table = (LseTensor * len(self.grads))()
-        seen = set()
+        spans = []
         for i, g in enumerate(self.grads):
             dt = DTYPES[_dtype_name(g)]
             if g.device != self.device:
@@ -292,13 +308,17 @@ class GradList:
                 if o.dtype != g.dtype or o.device != self.device or o.shape != g.shape \
                         or (o.stride() != g.stride() and not (o.is_contiguous() and g.is_contiguous())):
                     raise ValueError("out must match the gradients' types, shapes and strides")
-            for p in {g.data_ptr(), o.data_ptr() if o is not None else g.data_ptr()}:
-                if g.numel() and p in seen:
-                    raise ValueError("a tensor stands in the list twice")
-                if g.numel():
-                    seen.add(p)
+            if g.numel():
+                nbytes = g.numel() * g.element_size()
+                spans.append((g.data_ptr(), nbytes))
+                if o is not None and o.data_ptr() != g.data_ptr():
+                    spans.append((o.data_ptr(), nbytes))
             self._table[i] = LseTensor(g.data_ptr() or None, o.data_ptr() or None if o is not None else None,
                                        g.numel(), dt)
+
+        spans.sort()
+        if any(p + n > q for (p, n), (q, _) in zip(spans, spans[1:])):
+            raise ValueError("tensors of the list share memory")
 
     def __len__(self):
         return len(self.grads)
@@ -443,8 +463,10 @@ def _embedding_function(torch):
         def backward(ctx, g):
             (ids,) = ctx.saved_tensors
             (V, D), scale, padding, stream = ctx.args
-            d = lse_embedding_backward(g.contiguous().reshape(-1, D), ids.reshape(-1), V, scale,
-                                       padding, stream=stream)
+            g = g.contiguous().reshape(-1, D)
+            d = _ordered(torch, stream, g.device,
+                         lambda: lse_embedding_backward(g, ids.reshape(-1), V, scale, padding,
+                                                        stream=stream))
             return d, None, None, None, None
 
     return EmbeddingFunction

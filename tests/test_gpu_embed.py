@@ -211,3 +211,23 @@ def test_refusals():
             call()
     with pytest.raises(TypeError):
         L.lse_embedding(t.double(), ids)
+
+
+def test_gradient_on_the_forward_stream():
+    st = torch.cuda.Stream()
+    table = torch.randn(9000, 256, device="cuda")
+    ids = torch.randint(0, 9000, (20000,), device="cuda")
+    w = torch.randn(20000, 256, device="cuda")
+    want = []
+    for stream in (None, st):
+        leaf = table.clone().requires_grad_()
+        if stream is not None:
+            st.wait_stream(torch.cuda.current_stream())
+        out = L.embedding(ids, leaf, scale=0.5, stream=stream)
+        torch.cuda.current_stream().wait_stream(st)
+        big = torch.randn(4096, 4096, device="cuda")
+        for _ in range(8):  # the incoming gradient is late
+            big = big @ big / 64
+        (out * w * (1 + 0 * big[0, 0].nan_to_num(0.0, 0.0, 0.0))).sum().backward()
+        want.append(leaf.grad * 2)
+    assert torch.equal(want[0], want[1])

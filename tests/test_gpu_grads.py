@@ -195,3 +195,13 @@ def test_refusals():
             L.lse_grad_clip([a], bad)
     with pytest.raises(L.LseError):
         L.lse_grad_clip([a], 1.0, eps=-1.0)
+
+
+def test_lists_that_share_memory_are_refused():
+    buf = torch.zeros(1000, device="cuda")
+    with pytest.raises(ValueError, match="share memory"):
+        L.GradList([buf[:600], buf[599:]])
+    with pytest.raises(ValueError, match="share memory"):
+        L.GradList([buf[:300], buf[300:600]], [buf[600:900], buf[200:500]])
+    L.GradList([buf[:600], buf[600:], buf[:0]])
+    L.GradList([buf[:300], buf[300:600]], [buf[:300], buf[600:900]])

@@ -516,3 +516,25 @@ def test_gradient_of_many_short_rows(dtype, N):
         xd = place(x, **lay)
         dx = (None, xd, place(torch.zeros_like(x)))[i % 3]
         run_gradient(xd, x, t, min(K, N), dtype, dx=dx, seed=i)
+
+
+def test_gradient_on_the_forward_stream():
+    """autograd's own work runs on the current stream; the gradient kernel on the one that
+    the forward was given, after the incoming gradients and before their use."""
+    st = torch.cuda.Stream()
+    x, t = rows(4000, 4096, "f32", 11)
+    xd, td = x.cuda(), t.cuda()
+    w = torch.randn(4000, device="cuda")
+    want = []
+    for stream in (None, st):
+        leaf = xd.clone().requires_grad_()
+        st.wait_stream(torch.cuda.current_stream())
+        s = L.token_stats(leaf, td, 4, stream=stream)
+        torch.cuda.current_stream().wait_stream(st)
+        big = torch.randn(4096, 4096, device="cuda")
+        for _ in range(8):  # the incoming gradient is late
+            big = big @ big / 64
+        y = (s.logprob + s.entropy) * (w + 0 * big[:4000, 0].nan_to_num(0.0, 0.0, 0.0))
+        y.sum().backward()
+        want.append(leaf.grad * 2)
+    assert torch.equal(want[0], want[1])
