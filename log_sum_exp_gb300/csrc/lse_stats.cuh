@@ -1020,15 +1020,17 @@ cudaError_t launch_stats(StatsArgs a, int sms, cudaStream_t stream) {
     // Rows of up to 1024 vectors by the thousand: a warp each.
     if (vectors <= 1024 && a.B >= 16LL * sms) T = 32;
     // Few rows: a cluster of 256-thread CTAs per row, as many as leave each three quarters
-    // of a batch and together are resident at once (128256 bf16, K = 20: one row
-    // 6.4 us with 8 CTAs, 7.4 with 4, 6.6 with 16; 96 rows of 100003 f32 16.8 with 4, 18.8
-    // alone); two CTAs do not pay for the cluster's barriers (19.6).
+    // of a batch and are all resident at once -- in 15 of 16 SMs: some take no clusters
+    // (us; 128256 bf16, K = 20, one row: 6.4 with 8 CTAs, 7.4 with 4, 6.6 with 16; 200003
+    // f32: 60 rows 13.6 with 8, 16.8 with 4; 76 rows 19.4 and 17.7; 144 rows 23.6 with 4,
+    // 149 rows 30.3).  Two CTAs pay for the cluster's barriers only in long rows that are
+    // about as many as SMs (170 of 128256 bf16, K = 20: 18.3 against 22.4).
     int P = 1;
-    if (a.B < sms) {
+    if (a.B * 4 <= 5LL * sms) {
         while (2 * P <= kMaxCluster && vectors >= 2LL * P * (stat_u(256) * 256 * 3 / 4) &&
-               a.B * (2 * P) * 256 <= 1024LL * sms)
+               (P == 1 || a.B * (2 * P) * 256 <= 1024LL * sms * 15 / 16))
             P *= 2;
-        if (P < 4) P = 1;
+        if (P == 2 && vectors < 8192) P = 1;
     }
     a.cluster = P;
     const int64_t batches = ((vectors + P - 1) / P + stat_u(T) * T - 1) / (stat_u(T) * T);

@@ -538,3 +538,12 @@ def test_gradient_on_the_forward_stream():
         y.sum().backward()
         want.append(leaf.grad * 2)
     assert torch.equal(want[0], want[1])
+
+
+@pytest.mark.parametrize("dtype,N,K", [("f32", 33001, 32), ("bf16", 66000, 20), ("f16", 65539, 0)])
+def test_about_as_many_long_rows_as_processors(dtype, N, K):
+    """Long rows of which each takes two blocks."""
+    x = special_rows(N, dtype, seed=N)
+    x = x.repeat(150 // x.shape[0] + 1, 1)[:150]
+    t = torch.randint(0, N, (150,), generator=torch.Generator().manual_seed(N))
+    check(place(x, offset=1, row_stride=N + 1), x, t, K)
