@@ -148,19 +148,22 @@ embed_kernel(const __grid_constant__ EmbedArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Zeroing table rows without a token, kZeroRows rows per CTA.  These CTAs ride along with kernels that leave the memory idle: the last sorting pass
-// (a few CTAs, bound by latency), the sums, the joins.
+// Zeroing table rows without a token.  These CTAs ride along with kernels that leave the
+// memory idle: the sorting passes (a few CTAs, bound by latency), the sums, the joins.
+// The whole CTA takes row after row where a row gives each thread a vector at least
+// (gradient of 32768 tokens in 128256 rows of 4 KB: 119 us, 125 with a warp per row);
+// a warp takes a shorter one (20000 tokens in 300000 rows of 200 bytes: 53 against 220,
+// 65536 tokens in 50000 rows of 1800 bytes: 89 against 104).
 // ---------------------------------------------------------------------------
-constexpr int kZeroRows = 8;
-
 struct ZeroRows {
     char* table;
     int64_t row_bytes, stride_bytes, rows;
     const uint32_t* bitmap;  // null: no row has a token
-    int64_t first;           // group of kZeroRows rows of this launch's first CTA
+    int64_t first;           // group of rows of this launch's first CTA
     int64_t groups;          // CTAs of this launch
-    int64_t vectors;         // of a row, where all rows are whole, aligned 16-byte vectors; else 0
+    int group_rows;          // 8, 16 or 32 (rows of one word of the bitmap)
     int eb;                  // bytes of an element, 4 or 2
+    int64_t vectors;         // of a long row, if all rows are whole, aligned 16-byte vectors; else 0
 };
 
 __device__ __forceinline__ void put_zero(char* p, int eb) {
@@ -169,25 +172,32 @@ __device__ __forceinline__ void put_zero(char* p, int eb) {
 }
 
 __device__ __forceinline__ void zero_rows(const ZeroRows& z, int64_t cta, int tid, int threads) {
-    const int64_t v0 = (z.first + cta) * kZeroRows;
+    const int64_t v0 = (z.first + cta) * z.group_rows;
     const uint32_t present = z.bitmap ? z.bitmap[v0 >> 5] >> (v0 & 31) : 0u;
-    for (int q = 0; q < kZeroRows; ++q) {
+    if (z.vectors > 0) {
+        for (int q = 0; q < z.group_rows; ++q) {
+            if (v0 + q >= z.rows) return;
+            if ((present >> q) & 1u) continue;
+            uint4* row = reinterpret_cast<uint4*>(z.table + (v0 + q) * z.stride_bytes);
+            for (int64_t k = tid; k < z.vectors; k += threads) __stcs(row + k, make_uint4(0, 0, 0, 0));
+        }
+        return;
+    }
+    const int lane = tid & 31;
+    for (int q = tid >> 5; q < z.group_rows; q += threads >> 5) {
         const int64_t v = v0 + q;
         if (v >= z.rows) return;
         if ((present >> q) & 1u) continue;
         char* row = z.table + v * z.stride_bytes;
-        if (z.vectors > 0) {
-            for (int64_t k = tid; k < z.vectors; k += threads) __stcs(reinterpret_cast<uint4*>(row) + k, make_uint4(0, 0, 0, 0));
-            continue;
-        }
         // Elements up to a 16-byte boundary, vectors, elements.
         int64_t head = (16 - static_cast<int64_t>(reinterpret_cast<uintptr_t>(row) & 15u)) & 15;
         if (head > z.row_bytes) head = z.row_bytes;
         const int64_t vectors = (z.row_bytes - head) >> 4;
         const int64_t tail = z.row_bytes - head - vectors * 16;
-        for (int64_t k = tid; k < vectors; k += threads) __stcs(reinterpret_cast<uint4*>(row + head) + k, make_uint4(0, 0, 0, 0));
+#pragma unroll 4
+        for (int64_t k = lane; k < vectors; k += 32) __stcs(reinterpret_cast<uint4*>(row + head) + k, make_uint4(0, 0, 0, 0));
         if (head + tail == 0) continue;
-        const int64_t b = static_cast<int64_t>(tid) * z.eb;  // one element per thread at either end
+        const int64_t b = static_cast<int64_t>(lane) * z.eb;  // one element per lane at either end
         if (b < head) put_zero(row + b, z.eb);
         if (b < tail) put_zero(row + head + vectors * 16 + b, z.eb);
     }
@@ -481,12 +491,15 @@ __device__ __forceinline__ void end_run(const SumArgs& a, uint32_t run, bool beg
 }
 
 // blockDim = (slots of a column block, tiles of a CTA).
+// A tile's tokens in whole batches of U.
+__host__ __device__ constexpr int sum_padded(int len, int U) { return (len + U - 1) / U * U; }
+
 template <int DT, int OT, int SB>
 __global__ void __launch_bounds__(kEmbedThreads, 4)
 embed_sum_kernel(const __grid_constant__ SumArgs a) {
     using S = Slot<DT, SB>;
     constexpr int E = S::elems, U = S::in_flight;
-    extern __shared__ uint32_t sm[];
+    extern __shared__ uint4 sm[];
     const int tx = threadIdx.x, ty = threadIdx.y, TX = blockDim.x, TY = blockDim.y;
     pdl_trigger();
     pdl_wait();
@@ -499,21 +512,29 @@ embed_sum_kernel(const __grid_constant__ SumArgs a) {
     const int64_t group = blockIdx.x / a.col_blocks;
     const int64_t slot = (blockIdx.x - group * a.col_blocks) * TX + tx;
     const int64_t tile0 = group * TY;
-    // Keys of the tiles with one neighbour on either side, and where the rows are.
-    const int len = a.tile_len;
-    uint32_t* key = sm + ty * (len + 2);
-    uint32_t* at = sm + TY * (len + 2) + ty * len;
+    // Of each tile: its keys with one neighbour on either side, where the rows of grad are,
+    // and (a byte each) whether a token's key differs from the one before it.  In whole
+    // batches of U: what is past the tile is a row that may be read.
+    const int len = a.tile_len, padded = sum_padded(len, U);
+    uint64_t* const from = reinterpret_cast<uint64_t*>(sm) + ty * padded;
+    unsigned char* const starts = reinterpret_cast<unsigned char*>(reinterpret_cast<uint64_t*>(sm) + TY * padded) + ty * padded;
+    uint32_t* const key = reinterpret_cast<uint32_t*>(reinterpret_cast<unsigned char*>(sm) + TY * padded * 9) + ty * (len + 2);
     const int64_t i0 = (tile0 + ty) * len;
+    const uint64_t row_bytes = static_cast<uint64_t>(a.grad_stride) * DType<DT>::bytes;
+    for (int e = tx; e < padded; e += TX) {
+        const int64_t i = i0 + e;
+        const bool in = e < len && i < a.T;
+        from[e] = in ? a.at[i] * row_bytes : 0ull;
+        starts[e] = in && e > 0 && a.key[i] != a.key[i - 1] ? 1 : 0;
+    }
     for (int e = tx; e < len + 2; e += TX) {
         const int64_t i = i0 + e - 1;
         key[e] = i >= 0 && i < a.T ? a.key[i] : 0xffffffffu;  // (no id)
-        if (e < len) at[e] = i0 + e < a.T ? a.at[i0 + e] : 0u;
     }
     __syncthreads();
     if (tile0 + ty >= a.tiles || slot >= a.slots) return;
     const int tile = static_cast<int>(tile0 + ty);
     const char* col = a.grad + slot * SB;
-    const int64_t row_bytes = a.grad_stride * DType<DT>::bytes;
 
     // (tokens that add nothing sort last)
     int n = a.T - i0 < len ? static_cast<int>(a.T - i0) : len;
@@ -526,16 +547,26 @@ embed_sum_kernel(const __grid_constant__ SumArgs a) {
     for (int e0 = 0; e0 < n; e0 += U) {
         typename S::Raw v[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (e0 + u < n) v[u] = S::load(col + static_cast<int64_t>(at[e0 + u]) * row_bytes);
+        for (int u = 0; u < U; ++u) v[u] = S::load(col + from[e0 + u]);
+        uint64_t start[U / 8], any = 0;
+#pragma unroll
+        for (int q = 0; q < U / 8; ++q) any |= start[q] = *reinterpret_cast<const uint64_t*>(starts + e0 + 8 * q);
+        if (any == 0 && e0 + U <= n) {  // one run all through
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float y[E];
+                S::unpack(v[u], y);
+                s.add(y);
+            }
+            continue;
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (e0 + u >= n) break;
-            const uint32_t k = key[e0 + u + 1];
-            if (k != run) {
+            if ((start[u / 8] >> (8 * (u % 8))) & 0xffu) {
                 end_run<DT, OT, SB>(a, run, began_before, false, tile, slot, s.sums());
                 s.clear();
-                run = k;
+                run = key[e0 + u + 1];
                 began_before = false;
             }
             float y[E];
@@ -702,7 +733,7 @@ cudaError_t launch_sums(SumArgs a, cudaStream_t stream) {
     // The rest of the rows to zero: a part for the joining kernel, if there is
     // one, for which it would take about as long as its longest run.
     ZeroRows rest = a.zero;
-    const int64_t late = kJoinZeroBytes / (a.zero.row_bytes * kZeroRows);
+    const int64_t late = kJoinZeroBytes / (a.zero.row_bytes * a.zero.group_rows);
     a.zero.groups = join ? rest.groups - (rest.groups < late ? rest.groups : late) : rest.groups;
     int TX = 8;
     while (TX < kEmbedThreads && TX < a.slots) TX *= 2;
@@ -714,7 +745,7 @@ cudaError_t launch_sums(SumArgs a, cudaStream_t stream) {
     cudaError_t e = cudaSuccess;
     if (ctas > 0)
         e = launch_pdl_smem(embed_sum_kernel<DT, OT, SB>, dim3(static_cast<unsigned>(ctas)), dim3(TX, TY),
-                            sizeof(uint32_t) * TY * (2 * a.tile_len + 2), stream, a);
+                            TY * (9 * sum_padded(a.tile_len, Slot<DT, SB>::in_flight) + 4 * (a.tile_len + 2)), stream, a);
     if (e != cudaSuccess || !join) return e;
     // Narrow column blocks, so that several groups of threads share a long run.
     const int JX = TX < 32 ? TX : 32;
@@ -746,7 +777,7 @@ int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 // The next groups of *from, as many as `bytes` cover, for a kernel to zero.
 ZeroRows take_zero_rows(ZeroRows* from, int64_t bytes, const uint32_t* bitmap) {
     ZeroRows z = *from;
-    const int64_t groups = bytes / (z.row_bytes * kZeroRows);
+    const int64_t groups = bytes / (z.row_bytes * z.group_rows);
     z.groups = groups < z.groups ? groups : z.groups;
     z.bitmap = bitmap;
     from->first += z.groups;
@@ -763,10 +794,12 @@ lse_status embed_backward(SumArgs a, lse_dtype dtype, lse_dtype out_dtype, const
     a.zero.row_bytes = a.D * ob;
     a.zero.stride_bytes = a.dtable_stride * ob;
     a.zero.rows = a.V;
-    a.zero.groups = a.accumulate ? 0 : (a.V + kZeroRows - 1) / kZeroRows;
-    a.zero.eb = static_cast<int>(ob);
+    // (about 16 KB per CTA, or 32 rows: shorter ones would leave the CTA's launch to pay for)
+    a.zero.group_rows = a.zero.row_bytes >= 2048 ? 8 : a.zero.row_bytes >= 1024 ? 16 : 32;
+    a.zero.groups = a.accumulate ? 0 : (a.V + a.zero.group_rows - 1) / a.zero.group_rows;
     const bool whole = reinterpret_cast<uintptr_t>(a.dtable) % 16 == 0 && a.zero.stride_bytes % 16 == 0 && a.zero.row_bytes % 16 == 0;
-    a.zero.vectors = whole ? a.zero.row_bytes / 16 : 0;
+    a.zero.vectors = whole && a.zero.row_bytes >= 16 * kEmbedThreads ? a.zero.row_bytes / 16 : 0;
+    a.zero.eb = static_cast<int>(ob);
     if (a.T > 0) {
         // Blocks of at least one round of tokens, at most kSortMaxBlocks of them.
         SortArgs s;
