@@ -112,7 +112,9 @@ struct EmbedArgs {
     int64_t segments;  // per row, of 32 * U slots
 };
 
-// U slots per lane.
+// U slots per lane.  Bound by the rows' bytes when they are many: 20000 rows of 1001 f32 (no
+// 16-byte alignment, so 4-byte slots, 16 in flight) in 20.8 us, 7.7 TB/s with what repeats
+// coming from L2; 64 rows of 2048 bf16 in 2.3 us, a launch and two dependent loads.
 template <int DT, int SB, int U>
 __global__ void __launch_bounds__(kEmbedThreads)
 embed_kernel(const __grid_constant__ EmbedArgs a) {
@@ -208,7 +210,9 @@ __device__ __forceinline__ void zero_rows(const ZeroRows& z, int64_t cta, int ti
 // block give every block its places, and a token's place follows from the tokens of
 // its digit before it: in earlier blocks, earlier warps of the block, earlier in the
 // warp.  The pass that moves the tokens also counts the next digit, for the blocks
-// that they arrive in.
+// that they arrive in.  Latency (counts, barriers, a trip to memory
+// each way), so rows are zeroed meanwhile: 32768 tokens, two digits, and 16, 56 and 56 MB
+// of zeros take 6, 16 and 12 us.
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 256;
 constexpr int kSortWarps = kSortThreads / 32;
@@ -491,6 +495,12 @@ __device__ __forceinline__ void end_run(const SumArgs& a, uint32_t run, bool beg
 }
 
 // blockDim = (slots of a column block, tiles of a CTA).
+//
+// Bound by memory: 32768 tokens of 2048 bf16 read, their rows written and what is
+// left of 128256 zeroed in 69 us, 6.5 TB/s.  A thread owns a column slot of a tile and walks down
+// its tokens, U rows in flight; whether a token starts a run is found out once per tile
+// and not by every thread, and a batch without a start is added without looking (122 to
+// 119 us for the whole gradient).  A second batch in flight meanwhile spills (123).
 // A tile's tokens in whole batches of U.
 __host__ __device__ constexpr int sum_padded(int len, int U) { return (len + U - 1) / U * U; }
 
@@ -613,7 +623,9 @@ __device__ __forceinline__ void add_run(Sums<E>& s, const SumArgs& a, int64_t sl
 // the later tiles', in order.  blockDim = (slots of a narrow column block, groups).  For
 // a long run the groups take equal parts of the tiles of one narrow block, then their
 // sums are added in order; for others each group has a narrow block of its own.  The
-// CTAs take (run, column block) pairs in turn; further CTAs zero rows.
+// CTAs take (run, column block) pairs in turn; further CTAs zero rows.  Latency: 8 us
+// for 32768 tokens (a look at the keys, the longest run's partial sums), next to 40 MB of
+// zeros.
 template <int DT, int OT, int SB>
 __global__ void __launch_bounds__(kEmbedThreads)
 embed_join_kernel(const __grid_constant__ SumArgs a) {

@@ -173,6 +173,11 @@ __device__ __forceinline__ float root(double s) {
 }
 
 // partial[c] = the sum of CTA c's squares.
+//
+// Bound by its one read: 400 M bf16 in 119 us, 6.7 TB/s.  Eight 16-byte loads per thread
+// and four CTAs per SM keep 128 KB per SM in flight; half an instruction per element
+// (packed FMA) leaves two thirds of the issue rate unused.  The 64-bit adds, which this
+// GPU has few of, are one per thread and chunk of 32 to 64 elements.
 template <int N>
 __global__ void __launch_bounds__(kGradThreads, kGradCtas)
 grad_square_kernel(const __grid_constant__ GradList<N> list, double* __restrict__ partial) {
@@ -274,6 +279,10 @@ __device__ __forceinline__ void chunk_scale(const GradEntry& t, int64_t k0, floa
     }
 }
 
+// Bound by one read and one write: 400 M bf16 in 258 us, 6.2 TB/s (the copy rate measured
+// on this GPU is 6.8).  Four loads per thread are in flight: eight spill (453 us), two
+// measured 393 us for norm and clipping together against 388.
+//
 // out = g c for the list's tensors; every CTA forms the norm from the n partial sums
 // itself (a few KB from L2), which costs less than one more launch.
 template <int N>

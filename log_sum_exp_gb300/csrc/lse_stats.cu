@@ -163,6 +163,10 @@ __device__ __forceinline__ void zero_slots(char* dr, int off, int64_t end, int64
     }
 }
 
+// Bound by one read of x and one write of dx: 4096 rows of 32000 bf16 in 72 us, 7.3 TB/s
+// (a part of it in L2); 599 of 200003 f32 in 147, 6.5.  Short rows pay for their own gradients, loaded
+// in a chain of two trips before the first store (468750 rows of 256 bf16: 112 us, 4.3
+// TB/s), which is why several of them share a warp.
 template <int DT, int TX, bool VEC>
 __global__ void __launch_bounds__(TX <= 32 ? kGradCta : TX, TX < 32 ? 5 : TX == 32 ? 4 : 1024 / TX)
 lse_stats_backward_kernel(const __grid_constant__ StatsBackwardArgs a) {
