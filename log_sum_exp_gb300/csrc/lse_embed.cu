@@ -388,6 +388,56 @@ sort_move_kernel(const __grid_constant__ SortArgs a) {
     }
 }
 
+// Up to kRankMaxTokens tokens: each one's place is the number of smaller keys, and of
+// equal ones before it, counted by eight lanes over all keys in shared memory (T^2 / 8
+// steps, on all SMs at once).  One launch instead of three (whole gradient, us against
+// those of the sorting passes: 4 tokens in 32000 rows of 1024 bf16 12.4 and 16.5; 300 in
+// 20000 of 512 13.2 and 21.8; 4000 24.5 and 28.3; 6000 30.1 and 29.2).
+constexpr int kRankMaxTokens = 4096;
+constexpr int kRankLanes = 8;
+constexpr int kRankTokens = kSortThreads / kRankLanes;  // of a CTA
+
+__global__ void __launch_bounds__(kSortThreads)
+sort_rank_kernel(const __grid_constant__ SortArgs a, uint32_t* cross_count) {
+    __shared__ uint4 keys4[kRankMaxTokens / 4];
+    const int tid = threadIdx.x;
+    pdl_trigger();
+    pdl_wait();
+    if (static_cast<int>(blockIdx.x) >= a.blocks) {
+        zero_rows(a.zero, blockIdx.x - a.blocks, tid, kSortThreads);
+        return;
+    }
+    uint32_t* const keys = reinterpret_cast<uint32_t*>(keys4);
+    if (blockIdx.x == 0 && tid < 2) cross_count[tid] = 0;
+    const int padded = (a.T + kRankTokens - 1) / kRankTokens * kRankTokens;
+#pragma unroll 8
+    for (int i = tid; i < padded; i += kSortThreads)
+        keys[i] = i < a.T ? sort_key(__ldg(a.ids + i), a.V, a.padding) : 0xffffffffu;  // (below no key)
+    __syncthreads();
+    const int t0 = blockIdx.x * kRankTokens, lane = tid % kRankLanes;
+    const int i = t0 + tid / kRankLanes;
+    const uint32_t key = keys[i];
+    uint32_t place = 0;
+    // Before the CTA's tokens equal keys count, after them they do not; among them by number.
+#pragma unroll 4
+    for (int j = lane; j < t0 / 4; j += kRankLanes) {
+        const uint4 k = keys4[j];
+        place += (k.x <= key) + (k.y <= key) + (k.z <= key) + (k.w <= key);
+    }
+#pragma unroll 4
+    for (int j = t0 / 4 + lane; j < padded / 4; j += kRankLanes) {
+        const uint4 k = keys4[j];
+        place += (k.x < key) + (k.y < key) + (k.z < key) + (k.w < key);
+    }
+    for (int j = t0 + lane; j < i; j += kRankLanes) place += keys[j] == key;
+#pragma unroll
+    for (int off = 1; off < kRankLanes; off <<= 1) place += __shfl_xor_sync(0xffffffffu, place, off);
+    if (lane == 0 && i < a.T) {
+        a.key_out[place] = key;
+        a.at_out[place] = static_cast<uint32_t>(i);
+    }
+}
+
 // ---------------------------------------------------------------------------
 // Sums over the sorted tokens.
 // ---------------------------------------------------------------------------
@@ -397,6 +447,9 @@ constexpr int kLongRun = 7;  // further tiles of a run that counts as long
 // 136 us with 4, 24 and 24 MB, 130 with 8, 40 and 40, 127 with these).
 constexpr int64_t kCountZeroBytes = 16 << 20;
 constexpr int64_t kSortZeroBytes = 56 << 20;
+// The ranking kernel zeroes all rows alone, without the overlap with the joins: it is
+// taken while there are no more bytes than the sorting passes would zero.
+constexpr int64_t kRankZeroBytes = kCountZeroBytes + 2 * kSortZeroBytes;
 constexpr int64_t kJoinCtas = 608;  // four for each SM
 constexpr int64_t kJoinZeroBytes = 40 << 20;
 
@@ -826,8 +879,9 @@ lse_status embed_backward(SumArgs a, lse_dtype dtype, lse_dtype out_dtype, const
         const int blocks = static_cast<int>((static_cast<int64_t>(a.T) + (1LL << s.block_shift) - 1) >> s.block_shift);
         int bits = 1;  // of keys 0 .. V
         while (bits < 31 && (a.V >> bits) != 0) ++bits;
-        const int passes = (bits + kSortMaxBits - 1) / kSortMaxBits;
-        const int per = (bits + passes - 1) / passes;
+        const bool ranked = a.T <= kRankMaxTokens && a.zero.groups * a.zero.group_rows * a.zero.row_bytes <= kRankZeroBytes;
+        const int passes = ranked ? 0 : (bits + kSortMaxBits - 1) / kSortMaxBits;
+        const int per = ranked ? 0 : (bits + passes - 1) / passes;
 
         // Longer tiles leave fewer partial sums, shorter ones more CTAs: 64 tokens measured
         // 127 against 130 us with 32 for 32768 tokens of 2048 columns.
@@ -836,7 +890,7 @@ lse_status embed_backward(SumArgs a, lse_dtype dtype, lse_dtype out_dtype, const
         a.tiles = static_cast<int>(tiles);
         const int64_t list = round_up(static_cast<int64_t>(a.T) * 4, 256);
         const int64_t counts = round_up((static_cast<int64_t>(blocks) << per) * 4, 256);
-        const int64_t bitmap = round_up((a.V + 31) / 32 * 4, 256);
+        const int64_t bitmap = ranked ? 0 : round_up((a.V + 31) / 32 * 4, 256);
         const int64_t cross = round_up((tiles + 2) * 4, 256);
         const int64_t partial = round_up(tiles * a.D * 4, 256);
         const lse_status st = take_scratch(reinterpret_cast<void**>(&scratch),
@@ -854,31 +908,40 @@ lse_status embed_backward(SumArgs a, lse_dtype dtype, lse_dtype out_dtype, const
         a.zero.bitmap = s.bitmap;
         s.blocks = blocks;
 
-        // Before the bitmap is known, rows are zeroed whether they have tokens or not: the
-        // memory would be idle.
-        s.bits = per;
-        s.counts = reinterpret_cast<uint32_t*>(count0);
-        s.zero = take_zero_rows(&a.zero, kCountZeroBytes, nullptr);
-        // (behind the first pass's counts: the later passes', the bitmap, the list's lengths)
-        e = launch_pdl(sort_count_kernel, dim3(static_cast<unsigned>(blocks + s.zero.groups)), dim3(kSortThreads), stream,
-                       s, reinterpret_cast<uint32_t*>(count0 + counts), ((passes - 1) * counts + bitmap) / 4 + 2);
-        for (int p = 0; p < passes && e == cudaSuccess; ++p) {
-            s.shift = p * per;
-            s.next_bits = p + 1 < passes ? per : 0;
-            s.counts = reinterpret_cast<uint32_t*>(count0 + p * counts);
-            s.next_counts = reinterpret_cast<uint32_t*>(count0 + (p + 1) * counts);
-            s.key_in = key[(p + 1) & 1];
-            s.at_in = at[(p + 1) & 1];
-            s.key_out = key[p & 1];
-            s.at_out = at[p & 1];
-            s.zero = p == 0 ? take_zero_rows(&a.zero, kSortZeroBytes, nullptr)
-                            : take_zero_rows(&a.zero, kSortZeroBytes, s.bitmap);
-            const dim3 grid(static_cast<unsigned>(blocks + s.zero.groups));
-            e = p == 0 ? launch_pdl(sort_move_kernel<true>, grid, dim3(kSortThreads), stream, s)
-                       : launch_pdl(sort_move_kernel<false>, grid, dim3(kSortThreads), stream, s);
+        if (ranked) {
+            s.key_out = key[0];
+            s.at_out = at[0];
+            s.blocks = (a.T + kRankTokens - 1) / kRankTokens;
+            s.zero = take_zero_rows(&a.zero, INT64_MAX, nullptr);
+            e = launch_pdl(sort_rank_kernel, dim3(static_cast<unsigned>(s.blocks + s.zero.groups)), dim3(kSortThreads),
+                           stream, s, a.cross_count);
+        } else {
+            // Before the bitmap is known, rows are zeroed whether they have tokens or not: the
+            // memory would be idle.
+            s.bits = per;
+            s.counts = reinterpret_cast<uint32_t*>(count0);
+            s.zero = take_zero_rows(&a.zero, kCountZeroBytes, nullptr);
+            // (behind the first pass's counts: the later passes', the bitmap, the list's lengths)
+            e = launch_pdl(sort_count_kernel, dim3(static_cast<unsigned>(blocks + s.zero.groups)), dim3(kSortThreads), stream,
+                           s, reinterpret_cast<uint32_t*>(count0 + counts), ((passes - 1) * counts + bitmap) / 4 + 2);
+            for (int p = 0; p < passes && e == cudaSuccess; ++p) {
+                s.shift = p * per;
+                s.next_bits = p + 1 < passes ? per : 0;
+                s.counts = reinterpret_cast<uint32_t*>(count0 + p * counts);
+                s.next_counts = reinterpret_cast<uint32_t*>(count0 + (p + 1) * counts);
+                s.key_in = key[(p + 1) & 1];
+                s.at_in = at[(p + 1) & 1];
+                s.key_out = key[p & 1];
+                s.at_out = at[p & 1];
+                s.zero = p == 0 ? take_zero_rows(&a.zero, kSortZeroBytes, nullptr)
+                                : take_zero_rows(&a.zero, kSortZeroBytes, s.bitmap);
+                const dim3 grid(static_cast<unsigned>(blocks + s.zero.groups));
+                e = p == 0 ? launch_pdl(sort_move_kernel<true>, grid, dim3(kSortThreads), stream, s)
+                           : launch_pdl(sort_move_kernel<false>, grid, dim3(kSortThreads), stream, s);
+            }
         }
-        a.key = key[(passes - 1) & 1];
-        a.at = at[(passes - 1) & 1];
+        a.key = key[ranked ? 0 : (passes - 1) & 1];
+        a.at = at[ranked ? 0 : (passes - 1) & 1];
     }
     if (e == cudaSuccess)
         e = dtype == LSE_F32 ? launch_sums_dt<kF32>(a, out_dtype, stream)

@@ -231,3 +231,22 @@ def test_gradient_on_the_forward_stream():
         (out * w * (1 + 0 * big[0, 0].nan_to_num(0.0, 0.0, 0.0))).sum().backward()
         want.append(leaf.grad * 2)
     assert torch.equal(want[0], want[1])
+
+
+@pytest.mark.parametrize("T", [1, 2, 31, 32, 33, 255, 257, 1000, 4095, 4096, 4097, 8193])
+@pytest.mark.parametrize("V,D", [(1, 40), (7, 33), (300, 64), (20011, 96)])
+def test_gradient_of_few_tokens(T, V, D):
+    """Up to 4096 tokens are put in order by counting, more by sorting: the same sums."""
+    g = torch.Generator().manual_seed(T * 31 + V)
+    ids = torch.randint(-1, V + 1, (T,), generator=g)
+    ids[::3] = ids[0].clamp(0, V - 1)  # a frequent one
+    grad = torch.randint(-8, 9, (T, D), generator=g).float()  # sums without rounding
+    want = torch.zeros(V, D)
+    ok = (ids >= 0) & (ids < V) & (ids != 2)
+    want.index_add_(0, ids[ok], grad[ok])
+    got = L.lse_embedding_backward(grad.cuda(), ids.cuda(), V, padding=2)
+    assert torch.equal(got.cpu(), want)
+    held = torch.randint(-8, 9, (V, D), generator=g).float()
+    dt = held.cuda()
+    L.lse_embedding_backward(grad.cuda(), ids.cuda(), V, padding=2, dtable=dt, accumulate=True)
+    assert torch.equal(dt.cpu(), held + want)
