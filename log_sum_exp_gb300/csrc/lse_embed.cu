@@ -99,7 +99,7 @@ template <int DT, int SB> struct Slot {
 };
 
 // ---------------------------------------------------------------------------
-// Lookup: a warp per token and segment of its row.
+// Lookup: a warp, or a part of one, per token and segment of its row.
 // ---------------------------------------------------------------------------
 struct EmbedArgs {
     const char* table;
@@ -109,26 +109,28 @@ struct EmbedArgs {
     float scale;
     char* out;
     int64_t out_stride;
-    int64_t segments;  // per row, of 32 * U slots
+    int64_t segments;  // per row, of G * U slots
 };
 
-// U slots per lane.  Bound by the rows' bytes when they are many: 20000 rows of 1001 f32 (no
+// G lanes per row, U slots per lane.  Bound by the rows' bytes when they are many: 20000 rows of 1001 f32 (no
 // 16-byte alignment, so 4-byte slots, 16 in flight) in 20.8 us, 7.7 TB/s with what repeats
 // coming from L2; 64 rows of 2048 bf16 in 2.3 us, a launch and two dependent loads.
-template <int DT, int SB, int U>
+// Few lanes for a short row keep more rows in flight: 65536 rows of 64 bf16 in 3.9 us,
+// 14.6 with a warp each.
+template <int DT, int SB, int U, int G>
 __global__ void __launch_bounds__(kEmbedThreads)
 embed_kernel(const __grid_constant__ EmbedArgs a) {
     using S = Slot<DT, SB>;
     constexpr int EB = DType<DT>::bytes;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & (G - 1);
     const int64_t slots = a.D / S::elems;
     pdl_trigger();
     pdl_wait();
     const int64_t units = a.T * a.segments;
-    for (int64_t unit = (static_cast<int64_t>(blockIdx.x) * kEmbedThreads + threadIdx.x) >> 5; unit < units;
-         unit += (static_cast<int64_t>(gridDim.x) * kEmbedThreads) >> 5) {
+    for (int64_t unit = (static_cast<int64_t>(blockIdx.x) * kEmbedThreads + threadIdx.x) / G; unit < units;
+         unit += static_cast<int64_t>(gridDim.x) * (kEmbedThreads / G)) {
         const int64_t t = unit / a.segments;
-        const int64_t k0 = (unit - t * a.segments) * (32 * U) + lane;
+        const int64_t k0 = (unit - t * a.segments) * (G * U) + lane;
         const int64_t id = __ldg(a.ids + t);
         const bool in = id >= 0 && id < a.V;
         const char* from = a.table + (in ? id : 0) * a.table_stride * EB;
@@ -136,15 +138,15 @@ embed_kernel(const __grid_constant__ EmbedArgs a) {
         typename S::Raw v[U];
 #pragma unroll
         for (int j = 0; j < U; ++j)
-            if (in && k0 + 32 * j < slots) v[j] = S::load(from + (k0 + 32 * j) * SB);
+            if (in && k0 + G * j < slots) v[j] = S::load(from + (k0 + G * j) * SB);
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-            if (k0 + 32 * j >= slots) continue;
+            if (k0 + G * j >= slots) continue;
             float x[S::elems];
             if (in) S::unpack(v[j], x);
 #pragma unroll
             for (int i = 0; i < S::elems; ++i) x[i] = in ? x[i] * a.scale : __int_as_float(0x7fc00000);
-            S::store(to + (k0 + 32 * j) * SB, x);
+            S::store(to + (k0 + G * j) * SB, x);
         }
     }
 }
@@ -767,12 +769,23 @@ int slot_bytes(const void* p, int64_t stride, const void* q, int64_t stride_q, i
     return fits(16) ? 16 : fits(4) ? 4 : static_cast<int>(eb);
 }
 
-template <int DT, int SB, int U>
-cudaError_t launch_embed_u(EmbedArgs a, cudaStream_t stream) {
+template <int DT, int SB, int U, int G>
+cudaError_t launch_embed_g(EmbedArgs a, cudaStream_t stream) {
     const int64_t slots = a.D / Slot<DT, SB>::elems;
-    a.segments = (slots + 32 * U - 1) / (32 * U);
-    const int64_t ctas = (a.T * a.segments * 32 + kEmbedThreads - 1) / kEmbedThreads;
-    return launch_pdl(embed_kernel<DT, SB, U>, dim3(capped(ctas, INT_MAX)), dim3(kEmbedThreads), stream, a);
+    a.segments = (slots + G * U - 1) / (G * U);
+    const int64_t rows = kEmbedThreads / G;
+    const int64_t ctas = (a.T * a.segments + rows - 1) / rows;
+    return launch_pdl(embed_kernel<DT, SB, U, G>, dim3(capped(ctas, INT_MAX)), dim3(kEmbedThreads), stream, a);
+}
+
+// The fewest lanes (4 to 32) that hold a row.
+template <int DT, int SB, int U>
+cudaError_t launch_embed_u(const EmbedArgs& a, cudaStream_t stream) {
+    const int64_t slots = a.D / Slot<DT, SB>::elems;
+    return slots <= 4 * U    ? launch_embed_g<DT, SB, U, 4>(a, stream)
+           : slots <= 8 * U  ? launch_embed_g<DT, SB, U, 8>(a, stream)
+           : slots <= 16 * U ? launch_embed_g<DT, SB, U, 16>(a, stream)
+                             : launch_embed_g<DT, SB, U, 32>(a, stream);
 }
 
 // One slot per lane for small calls, where latency counts; else about 64 bytes of each
