@@ -454,6 +454,7 @@ constexpr int64_t kSortZeroBytes = 56 << 20;
 constexpr int64_t kRankZeroBytes = kCountZeroBytes + 2 * kSortZeroBytes;
 constexpr int64_t kJoinCtas = 608;  // four for each SM
 constexpr int64_t kJoinZeroBytes = 40 << 20;
+constexpr int64_t kSumCtas = 256;
 
 struct SumArgs {
     const char* grad;
@@ -836,9 +837,14 @@ cudaError_t launch_sums(SumArgs a, cudaStream_t stream) {
                       dim3(JX, kEmbedThreads / JX), stream, a);
 }
 
+template <int DT>
+int sum_slot_bytes(const SumArgs& a, int64_t ob) {
+    return slot_bytes<DT>(a.grad, a.grad_stride, a.dtable, a.dtable_stride, ob, a.D);
+}
+
 template <int DT, int OT>
 cudaError_t launch_sums_slot(const SumArgs& a, cudaStream_t stream) {
-    const int sb = slot_bytes<DT>(a.grad, a.grad_stride, a.dtable, a.dtable_stride, DType<OT>::bytes, a.D);
+    const int sb = sum_slot_bytes<DT>(a, DType<OT>::bytes);
     if (sb == 16) return launch_sums<DT, OT, 16>(a, stream);
     if (DT == kF32 || sb == 4) return launch_sums<DT, OT, 4>(a, stream);
     return launch_sums<DT, OT, DType<DT>::bytes>(a, stream);
@@ -896,9 +902,14 @@ lse_status embed_backward(SumArgs a, lse_dtype dtype, lse_dtype out_dtype, const
         const int passes = ranked ? 0 : (bits + kSortMaxBits - 1) / kSortMaxBits;
         const int per = ranked ? 0 : (bits + passes - 1) / passes;
 
-        // Longer tiles leave fewer partial sums, shorter ones more CTAs: 64 tokens measured
-        // 127 against 130 us with 32 for 32768 tokens of 2048 columns.
-        a.tile_len = a.T >= 1 << 15 ? 64 : a.T >= 1 << 11 ? 32 : 16;
+        // Longer tiles leave fewer partial sums, shorter ones more CTAs: the longest of 64
+        // that leaves kSumCtas of them (bf16, us, with tiles of 8, 16, 32, 64: 300 tokens of
+        // 512 columns 10.9, 12.6, 15.8, 21.6; 8192 of 1024 36.9, 33.1, 35.9, 41.9; 65536 of
+        // 896 99, 83, 77, 76; 32768 of 2048 145, 129, 121, 118).
+        const int sb = dtype == LSE_F32 ? sum_slot_bytes<kF32>(a, ob) : dtype == LSE_BF16 ? sum_slot_bytes<kBF16>(a, ob) : sum_slot_bytes<kF16>(a, ob);
+        const int64_t slots = a.D * (dtype == LSE_F32 ? 4 : 2) / sb;
+        a.tile_len = 64;
+        while (a.tile_len > (sb == 16 ? 8 : 16) && a.T * slots < kSumCtas * kEmbedThreads * a.tile_len) a.tile_len /= 2;
         const int64_t tiles = (static_cast<int64_t>(a.T) + a.tile_len - 1) / a.tile_len;
         a.tiles = static_cast<int>(tiles);
         const int64_t list = round_up(static_cast<int64_t>(a.T) * 4, 256);
