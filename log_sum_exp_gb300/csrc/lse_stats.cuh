@@ -439,11 +439,11 @@ struct StatsShared {
     uint64_t found[kFoundList];
     uint64_t own[kMaxTopK];
     // In the cluster's first CTA: the parts' keys, how many, their accumulators, and
-    // the maxima of 32 groups of threads of the whole cluster.
+    // the maxima of 32 or 64 groups of threads of the whole cluster.
     uint64_t keys[CLUSTER ? kMaxCluster * kPartKeys : 1];
     int key_count[CLUSTER ? kMaxCluster : 1];
     float acc[3][CLUSTER ? kMaxCluster : 1];
-    float4 cluster_max4[CLUSTER ? 8 : 1];
+    float4 cluster_max4[CLUSTER ? 16 : 1];
     float part[3][T / 32];
     RowStats row;
     int16_t chunk[T / 32][kChunkList];
@@ -703,11 +703,11 @@ lse_stats_kernel(const __grid_constant__ StatsArgs a) {
         cluster_wait();
         if (tid < count) cluster_map(sh.keys, 0)[seg * kPartKeys + tid] = from[tid];
         if (tid == 0) cluster_map(sh.key_count, 0)[seg] = count;
-        if (tid >= T - 32 && lane < 32 / P) {  // its threads in 32 / P groups
-            const int per_group = wide ? 2 * P : P;
-            float m = group_max[lane * per_group];
-            for (int i = 1; i < per_group; ++i) m = fmaxf(m, group_max[lane * per_group + i]);
-            reinterpret_cast<float*>(cluster_map(sh.cluster_max4, 0))[seg * (32 / P) + lane] = m;
+        const int groups_here = (wide ? 64 : 32) / P;  // of its threads
+        if (tid >= T - 32 && lane < groups_here) {
+            float m = group_max[lane * P];
+            for (int i = 1; i < P; ++i) m = fmaxf(m, group_max[lane * P + i]);
+            reinterpret_cast<float*>(cluster_map(sh.cluster_max4, 0))[seg * groups_here + lane] = m;
         }
     } else if (CLUSTER) {
         cluster_wait();
@@ -736,7 +736,8 @@ lse_stats_kernel(const __grid_constant__ StatsArgs a) {
         static_assert(!CLUSTER || (kMaxCluster * kPartKeys * 2 <= sizeof(sh.chunk_max) / 4 && kPartKeys % 16 == 0), "whole warps");
         uint64_t* reached = reinterpret_cast<uint64_t*>(sh.chunk_max);  // (no longer needed)
         if (tid == 0) sh.founds = 0;
-        const float bound = kth_largest_of<32>(reinterpret_cast<const float*>(sh.cluster_max4), a.K, lane);
+        const float* const cluster_max = reinterpret_cast<const float*>(sh.cluster_max4);
+        const float bound = wide ? kth_largest_of<64>(cluster_max, a.K, lane) : kth_largest_of<32>(cluster_max, a.K, lane);
         __syncthreads();
         for (int i = tid; i < P * kPartKeys; i += T) {
             const int part = i / kPartKeys;
@@ -1040,11 +1041,13 @@ cudaError_t launch_stats(StatsArgs a, int sms, cudaStream_t stream) {
     // (us; 128256 bf16, K = 20, one row: 6.4 with 8 CTAs, 7.4 with 4, 6.6 with 16; 200003
     // f32: 60 rows 13.6 with 8, 16.8 with 4; 76 rows 19.4 and 17.7; 144 rows 23.6 with 4,
     // 149 rows 30.3).  Two CTAs pay for the cluster's barriers only in long rows that are
-    // about as many as SMs (170 of 128256 bf16, K = 20: 18.3 against 22.4).
+    // about as many as SMs (170 of 128256 bf16, K = 20: 18.3 against 22.4), sixteen with
+    // alternatives only while each has an SM to itself (200000 f16, K = 20: 8 rows 7.7
+    // against 8.7 with 8, 30 rows 13.5 and 12.4; K = 0, 30 rows 7.2 and 8.6).
     int P = 1;
     if (a.B * 4 <= 5LL * sms) {
         while (2 * P <= kMaxCluster && vectors >= 2LL * P * (stat_u(256) * 256 * 3 / 4) &&
-               (P == 1 || a.B * (2 * P) * 256 <= 1024LL * sms * 15 / 16))
+               (P == 1 || a.B * (2 * P) * 256 <= 1024LL * sms * 15 / 16) && (P < 8 || a.K == 0 || a.B * (2 * P) <= sms))
             P *= 2;
         if (P == 2 && vectors < 8192) P = 1;
     }
