@@ -423,6 +423,18 @@ LSE_API lse_status lse_token_stats(const void *x, lse_dtype dtype, int64_t B, in
                                    float *top_logprob, int64_t *top_index, lse_stream_t stream);
 
 /*
+ * lse_token_stats_pair -- lse_token_stats, and in lse_low (B floats, or NULL)
+ * what rounding took from lse_out: lse_out + lse_low is the row's maximum plus
+ * log sum exp(x - max), a sum of two floats, before it was rounded to one (0
+ * where lse is infinite or NaN).  For lse_token_stats_backward_pair.
+ */
+LSE_API lse_status lse_token_stats_pair(const void *x, lse_dtype dtype, int64_t B, int64_t N,
+                                        int64_t row_stride, const int64_t *target, int64_t top_k,
+                                        float *logprob, float *entropy, float *lse_out,
+                                        float *lse_low, float *top_logprob, int64_t *top_index,
+                                        lse_stream_t stream);
+
+/*
  * lse_token_stats_backward -- the gradient of lse_token_stats' outputs:
  *
  *     dx_n = p_n (g_lse - g_lp - sum_k g_top_k - g_H (log p_n + H))
@@ -441,11 +453,25 @@ LSE_API lse_status lse_token_stats(const void *x, lse_dtype dtype, int64_t B, in
  * alternative whose index does, is dropped.  A row whose gradients are all zero
  * or dropped gets zeros whatever it holds (it is not read); other rows follow
  * IEEE arithmetic on the formula.
+ * lse alone gives every p_n of a row the same relative error of up to
+ * 2^-24 |lse| (1e-3 at 16384; all of log N next to the lowest f32): rows of
+ * large logits need lse_token_stats_backward_pair.
  */
 LSE_API lse_status lse_token_stats_backward(
     const void *x, lse_dtype dtype, int64_t B, int64_t N, int64_t row_stride, const float *lse,
     const float *entropy, const int64_t *target, const int64_t *top_index, int64_t top_k,
     const float *grad_logprob, const float *grad_entropy, const float *grad_top,
+    const float *grad_lse, void *dx, int64_t dx_row_stride, lse_stream_t stream);
+
+/*
+ * lse_token_stats_backward_pair -- the same with log p_n = (x_n - lse) - lse_low,
+ * lse and lse_low from lse_token_stats_pair (NULL: zeros): p and log p keep their
+ * digits however large the logits are.
+ */
+LSE_API lse_status lse_token_stats_backward_pair(
+    const void *x, lse_dtype dtype, int64_t B, int64_t N, int64_t row_stride, const float *lse,
+    const float *lse_low, const float *entropy, const int64_t *target, const int64_t *top_index,
+    int64_t top_k, const float *grad_logprob, const float *grad_entropy, const float *grad_top,
     const float *grad_lse, void *dx, int64_t dx_row_stride, lse_stream_t stream);
 
 /* One tensor of a gradient list: numel contiguous elements. */

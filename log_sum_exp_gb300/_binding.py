@@ -26,7 +26,8 @@ ABI_FUNCTIONS = ["lse_forward", "lse_plan_query", "lse_forward_plan", "lse_forwa
                  "lse_backward", "lse_forward_strided", "lse_backward_strided",
                  "lse_trim_memory", "lse_wait_timeouts", "lse_set_wait_limit", "lse_status_string",
                  "lse_last_cuda_error", "lse_forward_split_static",
-                 "lse_token_stats", "lse_token_stats_backward", "lse_grad_norm", "lse_grad_clip",
+                 "lse_token_stats", "lse_token_stats_pair", "lse_token_stats_backward",
+                 "lse_token_stats_backward_pair", "lse_grad_norm", "lse_grad_clip",
                  "lse_embedding", "lse_embedding_backward"]
 
 
@@ -120,9 +121,14 @@ def load() -> ctypes.CDLL:
         f32 = ctypes.c_float
         lib.lse_token_stats.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, vp, vp, vp, vp, vp]
         lib.lse_token_stats.restype = i32
+        lib.lse_token_stats_pair.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp]
+        lib.lse_token_stats_pair.restype = i32
         lib.lse_token_stats_backward.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp, i64, vp,
                                                  vp, vp, vp, vp, i64, vp]
         lib.lse_token_stats_backward.restype = i32
+        lib.lse_token_stats_backward_pair.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, i64,
+                                                      vp, vp, vp, vp, vp, i64, vp]
+        lib.lse_token_stats_backward_pair.restype = i32
         lib.lse_grad_norm.argtypes = [vp, i64, vp, vp]
         lib.lse_grad_norm.restype = i32
         lib.lse_grad_clip.argtypes = [vp, i64, f32, f32, vp, vp]

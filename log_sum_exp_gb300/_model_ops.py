@@ -16,13 +16,36 @@ from ._binding import (DTYPES, LseTensor, _check, _dtype_name, _on_device, _rows
 MAX_TOP_K = 32
 
 
-class TokenStats(NamedTuple):
-    """What ``lse_token_stats`` returns; absent parts are None."""
+class _TokenStats(NamedTuple):
     logprob: Optional[object]
     entropy: Optional[object]
     lse: object
     top_logprob: Optional[object]
     top_index: Optional[object]
+
+
+class TokenStats(_TokenStats):
+    """What ``lse_token_stats`` returns; absent parts are None.
+
+    The attribute ``lse_low`` (not one of the tuple's elements) is what rounding to
+    float32 took from ``lse``; the gradient uses both.  A tuple that was put together
+    by hand has None there, and its gradient's probabilities are as good as ``lse``
+    alone: a relative error of up to 2^-24 |lse|.
+    """
+
+    lse_low = None
+
+    def _replace(self, **parts):
+        new = super()._replace(**parts)
+        if "lse" not in parts:
+            new.lse_low = self.lse_low
+        return new
+
+
+def _token_stats(parts, lse_low):
+    s = TokenStats(*parts)
+    s.lse_low = lse_low
+    return s
 
 
 class _allocating:
@@ -102,13 +125,14 @@ def lse_token_stats(x, target=None, top_k=0, entropy=True, stream=None) -> Token
     out = _stats_call(*args) if _at_home(torch, stream, device) else _elsewhere(_stats_call, args)
     if x.dim() == 1:
         out = [None if t is None else t[0] for t in out]
-    return TokenStats(*out)
+    return _token_stats(out[:5], out[5])
 
 
 def _stats_call(torch, x, dt, B, N, row_stride, target, top_k, entropy, stream, device):
     # One allocation per output: views of a shared one cost more host time.
     empty, like, f32 = torch.empty, torch.empty_like, torch.float32
     lse = empty(B, dtype=f32, device=device)
+    low = like(lse)
     logprob = ent = top_lp = top_i = p_t = p_logprob = p_ent = p_lp = p_i = None
     if target is not None:
         logprob = like(lse)
@@ -120,10 +144,10 @@ def _stats_call(torch, x, dt, B, N, row_stride, target, top_k, entropy, stream, 
         top_lp = empty((B, top_k), dtype=f32, device=device)
         top_i = like(top_lp, dtype=torch.int64)
         p_lp, p_i = top_lp.data_ptr(), top_i.data_ptr()
-    _check(load().lse_token_stats(x.data_ptr(), dt, B, N, row_stride, p_t, top_k, p_logprob, p_ent,
-                                  lse.data_ptr(), p_lp, p_i, _stream_handle(stream, device)),
-           "lse_token_stats")
-    return logprob, ent, lse, top_lp, top_i
+    _check(load().lse_token_stats_pair(x.data_ptr(), dt, B, N, row_stride, p_t, top_k, p_logprob,
+                                       p_ent, lse.data_ptr(), low.data_ptr(), p_lp, p_i,
+                                       _stream_handle(stream, device)), "lse_token_stats")
+    return logprob, ent, lse, top_lp, top_i, low
 
 
 def lse_token_stats_backward(x, stats: TokenStats, target=None, grad_logprob=None,
@@ -142,6 +166,8 @@ def lse_token_stats_backward(x, stats: TokenStats, target=None, grad_logprob=Non
     device, f32, i64 = x.device, torch.float32, torch.int64
     K = stats.top_index.shape[-1] if stats.top_index is not None else 0
     _need_vector(stats.lse, "stats.lse", f32, B, device)
+    if stats.lse_low is not None:
+        _need_vector(stats.lse_low, "stats.lse_low", f32, B, device)
     if grad_logprob is not None:
         if target is None:
             raise ValueError("grad_logprob needs target")
@@ -174,8 +200,9 @@ def _stats_backward_call(torch, x, dt, B, N, row_stride, stats, target, K, grad_
         dx_stride = N
     else:
         dx_stride = _rows(dx)[2]
-    _check(load().lse_token_stats_backward(
+    _check(load().lse_token_stats_backward_pair(
         x.data_ptr(), dt, B, N, row_stride, stats.lse.data_ptr(),
+        None if stats.lse_low is None else stats.lse_low.data_ptr(),
         stats.entropy.data_ptr() if grad_entropy is not None else None,
         target.data_ptr() if grad_logprob is not None else None,
         stats.top_index.data_ptr() if grad_top is not None else None, K,
@@ -202,22 +229,21 @@ def _token_stats_function(torch):
         @staticmethod
         def forward(ctx, x, target, top_k, stream):
             s = lse_token_stats(x, target, top_k, stream=stream)
-            ctx.save_for_backward(x, target, s.entropy, s.lse, s.top_index)
+            ctx.save_for_backward(x, target, s.entropy, s.lse, s.top_index, s.lse_low)
             ctx.stream = stream
             ctx.set_materialize_grads(False)
-            if s.top_index is not None:
-                ctx.mark_non_differentiable(s.top_index)
-            return tuple(s)
+            ctx.mark_non_differentiable(*(t for t in (s.top_index, s.lse_low) if t is not None))
+            return (*s, s.lse_low)
 
         @staticmethod
         @torch.autograd.function.once_differentiable
-        def backward(ctx, g_lp, g_ent, g_lse, g_top, _):
-            x, target, ent, lse, top_index = ctx.saved_tensors
+        def backward(ctx, g_lp, g_ent, g_lse, g_top, *_):
+            x, target, ent, lse, top_index, lse_low = ctx.saved_tensors
             g = [None if t is None else t.to(torch.float32).contiguous()
                  for t in (g_lp, g_ent, g_top, g_lse)]
             if all(t is None for t in g):
                 return None, None, None, None
-            s = TokenStats(None, ent, lse, None, top_index)
+            s = _token_stats((None, ent, lse, None, top_index), lse_low)
             dx = _ordered(torch, ctx.stream, x.device,
                           lambda: lse_token_stats_backward(x, s, target, *g, stream=ctx.stream))
             return dx, None, None, None
@@ -247,13 +273,13 @@ def token_stats(x, target=None, top_k=0, stream=None) -> TokenStats:
         target = target.contiguous().reshape(rows)
     x2 = x.reshape(rows, N)
     if torch.is_grad_enabled() and x.requires_grad:
-        s = TokenStats(*_function("token_stats", _token_stats_function).apply(x2, target, top_k,
-                                                                              stream))
+        *s, low = _function("token_stats", _token_stats_function).apply(x2, target, top_k, stream)
     else:
         s = lse_token_stats(x2, target, top_k, stream=stream)
+        low = s.lse_low
     vectors = [None if t is None else t.reshape(lead) for t in s[:3]]
     tops = [None if t is None else t.reshape(tuple(lead) + (top_k,)) for t in s[3:]]
-    return TokenStats(*vectors, *tops)
+    return _token_stats(vectors + tops, low.reshape(lead))
 
 
 # ---------------------------------------------------------------------------

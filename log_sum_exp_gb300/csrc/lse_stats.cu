@@ -16,6 +16,7 @@ struct StatsBackwardArgs {
     const void* x;
     int64_t B, N, row_stride;
     const float* lse;
+    const float* lse_low;  // may be null (zero)
     const float* entropy;
     const int64_t* target;
     const int64_t* top_index;
@@ -34,7 +35,12 @@ struct StatsBackwardArgs {
 // Gradient.
 //
 //     dx_n = p_n (A - gH log p_n) + gl [n = t] + sum_k gt_k [n = i_k],
-//     A = g_lse - gl - sum_k gt_k - gH H,   log p_n = x_n - lse
+//     A = g_lse - gl - sum_k gt_k - gH H,   log p_n = (x_n - lse) - lse_low
+//
+// lse + lse_low is the row value before it was rounded: at an lse of 30000 the rounding
+// alone is 1e-3 of every p, and next to the type's lowest value all of log N.  x - lse is
+// exact near the maximum, and lse_low enters through the FMA that forms the exponent, so
+// both cost no more instructions than lse alone.
 //
 // TX threads take a segment of a row, two or four vectors each at a time, every load
 // issued before the stores.  The few elements with a unit term are read before
@@ -47,16 +53,17 @@ __device__ __forceinline__ void put_elem(void* row, int64_t i, float v) {
     else static_cast<unsigned short*>(row)[i] = static_cast<unsigned short>(pack2<DT>(v, 0.0f));
 }
 
+// (in octaves: low = -lse_low log2 e, gh = gH ln 2)
 struct RowGrad {
-    float lse, A, gh;
+    float lse, low, A, gh;
 };
 
 // One pair of elements.  An element with p = 0 adds nothing: log p is bounded from
 // below, so that it stays 0 * finite.
 template <bool ENT>
 __device__ __forceinline__ uint64_t grad_pair(uint64_t x, const RowGrad& g) {
-    const uint64_t lp = f2_sub(x, f2_pack(g.lse, g.lse));
-    const uint64_t e = f2_ex2(f2_mul(lp, f2_pack(kLog2e, kLog2e)));
+    const uint64_t lp = f2_fma(f2_sub(x, f2_pack(g.lse, g.lse)), f2_pack(kLog2e, kLog2e), f2_pack(g.low, g.low));
+    const uint64_t e = f2_ex2(lp);
     if constexpr (!ENT) {
         return f2_mul(e, f2_pack(g.A, g.A));
     } else {
@@ -69,8 +76,8 @@ __device__ __forceinline__ uint64_t grad_pair(uint64_t x, const RowGrad& g) {
 
 // The same for one element, with what is added to it.
 __device__ __forceinline__ float grad_elem(float x, const RowGrad& g, float unit) {
-    const float lp = x - g.lse;
-    const float e = ex2(lp * kLog2e);
+    const float lp = fmaf(x - g.lse, kLog2e, g.low);
+    const float e = ex2(lp);
     return (g.gh != 0.0f ? e * fmaf(-g.gh, fmaxf(lp, kFarBelow), g.A) : e * g.A) + unit;
 }
 
@@ -200,6 +207,7 @@ lse_stats_backward_kernel(const __grid_constant__ StatsBackwardArgs a) {
         // The row's gradients (every group of W lanes for itself; K <= W), all loaded at once.
         RowGrad g;
         g.lse = __ldg(a.lse + row);
+        g.low = a.lse_low ? -kLog2e * __ldg(a.lse_low + row) : 0.0f;
         const int64_t t = a.grad_logprob ? __ldg(a.target + row) : -1;
         float gl = a.grad_logprob ? __ldg(a.grad_logprob + row) : 0.0f;
         const float gs = a.grad_lse ? __ldg(a.grad_lse + row) : 0.0f;
@@ -229,6 +237,7 @@ lse_stats_backward_kernel(const __grid_constant__ StatsBackwardArgs a) {
         }
         g.A = gs - gl - sum;
         if (g.gh != 0.0f) g.A = fmaf(-g.gh, h, g.A);
+        g.gh *= kLn2;
 
         // The first warp keeps the elements with a unit term.
         const bool first = tid < 32;
@@ -316,18 +325,26 @@ lse_status lse_token_stats(const void* x, lse_dtype dtype, int64_t B, int64_t N,
                            const int64_t* target, int64_t top_k, float* logprob, float* entropy,
                            float* lse_out, float* top_logprob, int64_t* top_index,
                            lse_stream_t stream) {
+    return lse_token_stats_pair(x, dtype, B, N, row_stride, target, top_k, logprob, entropy, lse_out, nullptr,
+                                top_logprob, top_index, stream);
+}
+
+lse_status lse_token_stats_pair(const void* x, lse_dtype dtype, int64_t B, int64_t N, int64_t row_stride,
+                                const int64_t* target, int64_t top_k, float* logprob, float* entropy,
+                                float* lse_out, float* lse_low, float* top_logprob, int64_t* top_index,
+                                lse_stream_t stream) {
     const void* stand_in = reinterpret_cast<const void*>(static_cast<uintptr_t>(256));
     lse_status st = check_args(x, dtype, B, N, row_stride, stand_in);
     if (st != LSE_OK) return st;
     if (top_k < 0 || top_k > LSE_MAX_TOP_K) return LSE_ERR_INVALID_ARG;
     if (top_k > 0 && N > INT32_MAX) return LSE_ERR_INVALID_ARG;
     if (misaligned(target, 8) || misaligned(top_index, 8) || misaligned(logprob, 4) ||
-        misaligned(entropy, 4) || misaligned(lse_out, 4) || misaligned(top_logprob, 4))
+        misaligned(entropy, 4) || misaligned(lse_out, 4) || misaligned(lse_low, 4) || misaligned(top_logprob, 4))
         return LSE_ERR_INVALID_ARG;
     if (B == 0) return LSE_OK;
     if ((logprob != nullptr) != (target != nullptr)) return LSE_ERR_INVALID_ARG;
     if (top_k > 0 && (top_logprob == nullptr || top_index == nullptr)) return LSE_ERR_INVALID_ARG;
-    if (!logprob && !entropy && !lse_out && top_k == 0) return LSE_ERR_INVALID_ARG;
+    if (!logprob && !entropy && !lse_out && !lse_low && top_k == 0) return LSE_ERR_INVALID_ARG;
     StatsArgs a;
     a.x = x;
     a.B = B;
@@ -338,6 +355,7 @@ lse_status lse_token_stats(const void* x, lse_dtype dtype, int64_t B, int64_t N,
     a.logprob = logprob;
     a.entropy = entropy;
     a.lse = lse_out;
+    a.lse_low = lse_low;
     a.top_logprob = top_logprob;
     a.top_index = top_index;
     int sms = 0;
@@ -354,6 +372,17 @@ lse_status lse_token_stats_backward(const void* x, lse_dtype dtype, int64_t B, i
                                     const float* grad_logprob, const float* grad_entropy,
                                     const float* grad_top, const float* grad_lse, void* dx,
                                     int64_t dx_row_stride, lse_stream_t stream) {
+    return lse_token_stats_backward_pair(x, dtype, B, N, row_stride, lse_in, nullptr, entropy, target, top_index, top_k,
+                                         grad_logprob, grad_entropy, grad_top, grad_lse, dx, dx_row_stride, stream);
+}
+
+lse_status lse_token_stats_backward_pair(const void* x, lse_dtype dtype, int64_t B, int64_t N,
+                                         int64_t row_stride, const float* lse_in, const float* lse_low,
+                                         const float* entropy, const int64_t* target,
+                                         const int64_t* top_index, int64_t top_k,
+                                         const float* grad_logprob, const float* grad_entropy,
+                                         const float* grad_top, const float* grad_lse, void* dx,
+                                         int64_t dx_row_stride, lse_stream_t stream) {
     const void* stand_in = reinterpret_cast<const void*>(static_cast<uintptr_t>(256));
     lse_status st = check_args(x, dtype, B, N, row_stride, stand_in);
     if (st != LSE_OK) return st;
@@ -365,7 +394,7 @@ lse_status lse_token_stats_backward(const void* x, lse_dtype dtype, int64_t B, i
         __builtin_mul_overflow(extent, static_cast<int64_t>(eb), &extent))
         return LSE_ERR_INVALID_ARG;
     if (misaligned(dx, eb) || misaligned(target, 8) || misaligned(top_index, 8) ||
-        misaligned(lse_in, 4) || misaligned(entropy, 4) || misaligned(grad_logprob, 4) ||
+        misaligned(lse_in, 4) || misaligned(lse_low, 4) || misaligned(entropy, 4) || misaligned(grad_logprob, 4) ||
         misaligned(grad_entropy, 4) || misaligned(grad_top, 4) || misaligned(grad_lse, 4))
         return LSE_ERR_INVALID_ARG;
     if (B == 0 || N == 0) return LSE_OK;
@@ -379,6 +408,7 @@ lse_status lse_token_stats_backward(const void* x, lse_dtype dtype, int64_t B, i
     a.N = N;
     a.row_stride = row_stride;
     a.lse = lse_in;
+    a.lse_low = lse_low;
     a.entropy = entropy;
     a.target = target;
     a.top_index = top_index;

@@ -377,9 +377,18 @@ __device__ __forceinline__ uint64_t scan_vectors(const Row& r, int64_t k0, int64
     return best;
 }
 
+// What is lost when lse = max + log sum exp(x - max) is rounded to f32, exactly (the
+// error of a sum is a float): the gradient takes x - lse from both.
+__device__ __forceinline__ float lse_rest(const RowStats& r) {
+    if (r.logs != r.logs) return 0.0f;  // no distribution: lse is infinite or NaN
+    const float b = __fsub_rn(r.lse, r.m);
+    return __fadd_rn(__fsub_rn(r.m, __fsub_rn(r.lse, b)), __fsub_rn(r.logs, b));
+}
+
 // Writes of one row's results.
 __device__ __forceinline__ void put_row(const StatsArgs& a, int64_t row, const StatAcc& acc, const RowStats& r, float xt) {
     if (a.lse) a.lse[row] = r.lse;
+    if (a.lse_low) a.lse_low[row] = lse_rest(r);
     if (a.entropy) a.entropy[row] = stat_entropy(acc, r);
     if (a.logprob) a.logprob[row] = stat_logprob(xt, r);
 }

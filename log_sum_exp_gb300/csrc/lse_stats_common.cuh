@@ -18,6 +18,7 @@ struct StatsArgs {
     float* logprob;      // each output may be null
     float* entropy;
     float* lse;
+    float* lse_low;      // what rounding took from lse
     float* top_logprob;  // [B, K]
     int64_t* top_index;
     int cluster;         // CTAs that share a row
