@@ -248,7 +248,7 @@ __device__ __forceinline__ void chunk_scale(const GradEntry& t, int64_t k0, floa
         uint4 v[kScaleU];
 #pragma unroll
         for (int j = 0; j < kScaleU; ++j)
-            if (k + j * kGradThreads < vectors) v[j] = ldg_stream16(a0 + (k + j * kGradThreads) * 16);
+            if (k + j * kGradThreads < vectors) v[j] = ld_stream16(a0 + (k + j * kGradThreads) * 16);
 #pragma unroll
         for (int j = 0; j < kScaleU; ++j) {
             const int64_t kk = k + j * kGradThreads;
@@ -282,6 +282,9 @@ __device__ __forceinline__ void chunk_scale(const GradEntry& t, int64_t k0, floa
 // Bound by one read and one write: 400 M bf16 in 258 us, 6.2 TB/s (the copy rate measured
 // on this GPU is 6.8).  Four loads per thread are in flight: eight spill (453 us), two
 // measured 393 us for norm and clipping together against 388.
+//
+// `out` may be the tensor itself, and neighbouring tensors share vectors, so nothing here is
+// read through the read-only path.
 //
 // out = g c for the list's tensors; every CTA forms the norm from the n partial sums
 // itself (a few KB from L2), which costs less than one more launch.

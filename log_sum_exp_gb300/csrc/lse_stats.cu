@@ -44,8 +44,9 @@ struct StatsBackwardArgs {
 //
 // TX threads take a segment of a row, two or four vectors each at a time, every load
 // issued before the stores.  The few elements with a unit term are read before
-// anything is stored (dx may be x) and written once more, whole, at the end, so the
-// loop compares no columns.
+// anything is stored and written once more, whole, at the end, so the loop compares no
+// columns.  dx may be x, so x is not read through the read-only path: what is loaded
+// before a store must not be loaded again after it.
 // ---------------------------------------------------------------------------
 template <int DT>
 __device__ __forceinline__ void put_elem(void* row, int64_t i, float v) {
@@ -123,7 +124,7 @@ __device__ __forceinline__ void grad_slots(const char* xr, char* dr, int off, in
             uint4 v[U];
 #pragma unroll
             for (int j = 0; j < U; ++j)
-                if (k + j * TX < k1) v[j] = ldg_stream16(x0 + (k + j * TX) * 16);
+                if (k + j * TX < k1) v[j] = ld_stream16(x0 + (k + j * TX) * 16);
 #pragma unroll
             for (int j = 0; j < U; ++j) {
                 const int64_t kk = k + j * TX;
@@ -146,7 +147,7 @@ __device__ __forceinline__ void grad_slots(const char* xr, char* dr, int off, in
             float v[U];
 #pragma unroll
             for (int j = 0; j < U; ++j)
-                if (k + j * TX < k1) v[j] = load_elem<DT>(xr, k + j * TX);
+                if (k + j * TX < k1) v[j] = load_own_elem<DT>(xr, k + j * TX);
 #pragma unroll
             for (int j = 0; j < U; ++j)
                 if (k + j * TX < k1) put_elem<DT>(dr, k + j * TX, grad_elem(v[j], g, 0.0f));
@@ -251,11 +252,11 @@ lse_stats_backward_kernel(const __grid_constant__ StatsBackwardArgs a) {
                 if (ok == ti) unit_term += gk;
             }
             if (ti == t && in_row) unit_term += gl;
-            if (mine) x_mine = load_elem<DT>(xr, ti);
+            if (mine) x_mine = load_own_elem<DT>(xr, ti);
         }
         if (first && in_row && t >= n0 && t < n1) {
             target_alone = !__any_sync(group, ti == t);
-            if (target_alone && lane == 0) x_target = load_elem<DT>(xr, t);
+            if (target_alone && lane == 0) x_target = load_own_elem<DT>(xr, t);
         }
         sync();
         if (g.gh != 0.0f) grad_slots<DT, TX, VEC, true>(xr, dr, off, end, k0, k1, tid, g);
