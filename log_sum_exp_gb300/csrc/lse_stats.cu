@@ -2,6 +2,7 @@
 // (sm_103a).  The statistics' own kernels are in lse_stats.cuh.
 #include <climits>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_runtime.h>
 
@@ -108,16 +109,19 @@ __device__ __forceinline__ uint4 grad_vector(uint4 v, const RowGrad& g) {
 // Vectors (or elements) per thread and step.
 __host__ __device__ constexpr int grad_u(int TX) { return TX < 32 ? 2 : 4; }
 constexpr int kGradCta = 256;    // threads of a CTA whose rows take a warp or less
+// Positions in a row: rows that take a warp or less have at most 512 slots.
+template <int TX> using GradIndex = typename std::conditional<(TX <= 32), int, int64_t>::type;
 
 // Slots [k0, k1) of a row: the 16-byte vectors that cover it (VEC; x and dx rows at
 // the same offset from a boundary), the outer ones stored element by element, or
 // single elements.
 template <int DT, int TX, bool VEC, bool ENT>
-__device__ __forceinline__ void grad_slots(const char* xr, char* dr, int off, int64_t end, int64_t k0,
-                                           int64_t k1, int tid, const RowGrad& g) {
+__device__ __forceinline__ void grad_slots(const char* xr, char* dr, int off, GradIndex<TX> end, GradIndex<TX> k0,
+                                           GradIndex<TX> k1, int tid, const RowGrad& g) {
+    using I = GradIndex<TX>;
     constexpr int EB = DType<DT>::bytes, EPV = 16 / EB;
     constexpr int U = grad_u(TX);
-    for (int64_t k = k0 + tid; k < k1; k += U * TX) {
+    for (I k = k0 + tid; k < k1; k += U * TX) {
         if constexpr (VEC) {
             const char* x0 = xr - off;
             char* d0 = dr - off;
@@ -127,7 +131,7 @@ __device__ __forceinline__ void grad_slots(const char* xr, char* dr, int off, in
                 if (k + j * TX < k1) v[j] = ld_stream16(x0 + (k + j * TX) * 16);
 #pragma unroll
             for (int j = 0; j < U; ++j) {
-                const int64_t kk = k + j * TX;
+                const I kk = k + j * TX;
                 if (kk >= k1) continue;
                 const uint4 o = grad_vector<DT, ENT>(v[j], g);
                 if ((kk > 0 || off == 0) && kk * 16 + 16 <= end) {
@@ -136,7 +140,7 @@ __device__ __forceinline__ void grad_slots(const char* xr, char* dr, int off, in
                     const uint32_t w[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
                     for (int i = 0; i < EPV; ++i) {
-                        const int64_t at = kk * 16 + i * EB;
+                        const I at = kk * 16 + i * EB;
                         if (at < off || at >= end) continue;
                         if constexpr (DT == kF32) *reinterpret_cast<uint32_t*>(d0 + at) = w[i];
                         else *reinterpret_cast<unsigned short*>(d0 + at) = static_cast<unsigned short>((i & 1) ? w[i / 2] >> 16 : w[i / 2]);
@@ -157,15 +161,16 @@ __device__ __forceinline__ void grad_slots(const char* xr, char* dr, int off, in
 
 // Zeros for the same slots of a row that carries no gradient.
 template <int DT, int TX, bool VEC>
-__device__ __forceinline__ void zero_slots(char* dr, int off, int64_t end, int64_t k0, int64_t k1, int tid) {
+__device__ __forceinline__ void zero_slots(char* dr, int off, GradIndex<TX> end, GradIndex<TX> k0, GradIndex<TX> k1, int tid) {
+    using I = GradIndex<TX>;
     constexpr int EB = DType<DT>::bytes;
-    for (int64_t k = k0 + tid; k < k1; k += TX) {
+    for (I k = k0 + tid; k < k1; k += TX) {
         if constexpr (!VEC) {
             put_elem<DT>(dr, k, 0.0f);
         } else if ((k > 0 || off == 0) && k * 16 + 16 <= end) {
             *reinterpret_cast<uint4*>(dr - off + k * 16) = make_uint4(0, 0, 0, 0);
         } else {
-            for (int64_t at = k * 16; at < k * 16 + 16; at += EB)
+            for (I at = k * 16; at < k * 16 + 16; at += EB)
                 if (at >= off && at < end) put_elem<DT>(dr, (at - off) / EB, 0.0f);
         }
     }
@@ -173,11 +178,14 @@ __device__ __forceinline__ void zero_slots(char* dr, int off, int64_t end, int64
 
 // Bound by one read of x and one write of dx: 4096 rows of 32000 bf16 in 72 us, 7.3 TB/s
 // (a part of it in L2); 599 of 200003 f32 in 147, 6.5.  Short rows pay for their own gradients, loaded
-// in a chain of two trips before the first store (468750 rows of 256 bf16: 112 us, 4.3
-// TB/s), which is why several of them share a warp.
+// in a chain of two trips before the first store (468750 rows of 256 bf16: 103 us, 4.6
+// TB/s), which is why several of them share a warp; with 64-bit positions in the row these
+// mappings spilled about 110 bytes and took 10 % longer (at most 28 now, none in f32's 8
+// and 16 lanes).
 template <int DT, int TX, bool VEC>
 __global__ void __launch_bounds__(TX <= 32 ? kGradCta : TX, TX < 32 ? 5 : TX == 32 ? 4 : 1024 / TX)
 lse_stats_backward_kernel(const __grid_constant__ StatsBackwardArgs a) {
+    using I = GradIndex<TX>;
     constexpr int EB = DType<DT>::bytes, UNITS = TX <= 32 ? kGradCta / TX : 1;
     constexpr int W = TX < 32 ? TX : 32;  // lanes that share a row's gradients
     const int tid = threadIdx.x % TX, lane = threadIdx.x & (W - 1);
@@ -191,41 +199,42 @@ lse_stats_backward_kernel(const __grid_constant__ StatsBackwardArgs a) {
     const int64_t units = a.B * a.segments;
     for (int64_t unit = static_cast<int64_t>(blockIdx.x) * UNITS + threadIdx.x / TX; unit < units;
          unit += static_cast<int64_t>(gridDim.x) * UNITS) {
-        const int64_t row = unit / a.segments;
-        const int64_t seg = unit - row * a.segments;
+        const int64_t row = TX <= 32 ? unit : unit / a.segments;  // (a row of up to a warp is one segment)
+        const int64_t seg = TX <= 32 ? 0 : unit - row * a.segments;
         const char* xr = static_cast<const char*>(a.x) + row * a.row_stride * EB;
         char* dr = static_cast<char*>(a.dx) + row * a.dx_row_stride * EB;
         const int off = VEC ? static_cast<int>(reinterpret_cast<uintptr_t>(xr) & 15u) : 0;
-        const int64_t end = off + a.N * EB;  // (VEC) bytes from the first vector
-        const int64_t slots = VEC ? (end + 15) >> 4 : a.N;
-        const int64_t k0 = seg * a.seg_slots;
-        const int64_t k1 = k0 + a.seg_slots < slots ? k0 + a.seg_slots : slots;
+        const I N = static_cast<I>(a.N);
+        const I end = off + N * EB;  // (VEC) bytes from the first vector
+        const I slots = VEC ? (end + 15) >> 4 : N;
+        const I seg_slots = static_cast<I>(a.seg_slots);
+        const I k0 = static_cast<I>(seg) * seg_slots;
+        const I k1 = TX <= 32 || k0 + seg_slots >= slots ? slots : k0 + seg_slots;
         if (k0 >= k1) continue;
         // The segment's columns.
-        const int64_t n0 = VEC ? (k0 == 0 ? 0 : (k0 * 16 - off) / EB) : k0;
-        const int64_t n1 = VEC ? (k1 == slots ? a.N : (k1 * 16 - off) / EB) : k1;
+        const I n0 = VEC ? (k0 == 0 ? 0 : (k0 * 16 - off) / EB) : k0;
+        const I n1 = VEC ? (k1 == slots ? N : (k1 * 16 - off) / EB) : k1;
 
         // The row's gradients (every group of W lanes for itself; K <= W), all loaded at once.
         RowGrad g;
         g.lse = __ldg(a.lse + row);
         g.low = a.lse_low ? -kLog2e * __ldg(a.lse_low + row) : 0.0f;
-        const int64_t t = a.grad_logprob ? __ldg(a.target + row) : -1;
+        const int64_t given = a.grad_logprob ? __ldg(a.target + row) : -1;
         float gl = a.grad_logprob ? __ldg(a.grad_logprob + row) : 0.0f;
         const float gs = a.grad_lse ? __ldg(a.grad_lse + row) : 0.0f;
         g.gh = a.grad_entropy ? __ldg(a.grad_entropy + row) : 0.0f;
         const float h = a.grad_entropy ? __ldg(a.entropy + row) : 0.0f;
-        int64_t ti = -1;  // lane k: alternative k
+        I ti = -1;  // lane k: alternative k
         float gt = 0.0f;
         if (lane < a.K) {
-            ti = __ldg(a.top_index + row * a.K + lane);
-            gt = __ldg(a.grad_top + row * a.K + lane);
+            const int64_t column = __ldg(a.top_index + row * a.K + lane);
+            const bool in = column >= 0 && column < a.N;
+            ti = in ? static_cast<I>(column) : -1;
+            gt = in ? __ldg(a.grad_top + row * a.K + lane) : 0.0f;
         }
-        const bool in_row = t >= 0 && t < a.N;
+        const bool in_row = given >= 0 && given < a.N;
+        const I t = in_row ? static_cast<I>(given) : -1;
         if (!in_row) gl = 0.0f;
-        if (ti < 0 || ti >= a.N) {
-            ti = -1;
-            gt = 0.0f;
-        }
         float sum = gt;
         if (a.K > 0) {
 #pragma unroll
@@ -247,7 +256,7 @@ lse_stats_backward_kernel(const __grid_constant__ StatsBackwardArgs a) {
         bool target_alone = false;
         if (first && a.K > 0) {
             for (int k = 0; k < a.K; ++k) {
-                const int64_t ok = __shfl_sync(group, ti, k, W);
+                const I ok = __shfl_sync(group, ti, k, W);
                 const float gk = __shfl_sync(group, gt, k, W);
                 if (ok == ti) unit_term += gk;
             }
@@ -279,9 +288,9 @@ cudaError_t launch_stats_backward_tx(const StatsBackwardArgs& a, bool vec, cudaS
 // Vectors where each x row and its dx row sit at the same offset from a 16-byte
 // boundary, elements otherwise.  8, 16 or 32 lanes per row of up to 64, 256 or 512 slots
 // (and no more alternatives than lanes), which waste fewer lanes and keep more rows in
-// flight (us; 468750 bf16 rows of 256: 8 lanes 112, 32 lanes about 330; 80000 bf16 rows
-// of 1500: 16 lanes 105, 32 lanes 108; 39986 bf16 rows of 3001: 32 lanes 93, 128 threads
-// 119; 5000 bf16 rows of 6000: 32 lanes 27, 128 threads 22.6); 128 threads up to 1024
+// flight (us; 468750 bf16 rows of 256: 8 lanes 103, 16 136, 32 266; 80000 bf16 rows of
+// 1500: 16 lanes 98, 32 lanes 100; 39986 bf16 rows of 3001: 16 lanes 100, 32 88, 128
+// threads 121; 5000 bf16 rows of 6000: 32 lanes 27, 128 threads 22.4); 128 threads up to 1024
 // slots, 256 beyond.  Few rows of more than 256 slots take 128 threads too.  Longer rows
 // go in segments of up to 16 slots per thread, shorter ones while the segments would not
 // fill the GPU.
