@@ -255,7 +255,7 @@ def token_stats(x, target=None, top_k=0, stream=None) -> TokenStats:
     """``lse_token_stats`` over the last dimension of contiguous CUDA logits of any
     shape [..., N], differentiable with respect to x.
 
-    ``target`` has x's leading shape.  ``logprob``, ``entropy``, ``lse`` and
+    ``target`` has x's leading shape, in any strides.  ``logprob``, ``entropy``, ``lse`` and
     ``top_logprob`` carry gradients.
     """
     torch = _torch()
@@ -270,7 +270,10 @@ def token_stats(x, target=None, top_k=0, stream=None) -> TokenStats:
     if target is not None:
         if target.shape != lead:
             raise ValueError("target must have x's shape without the last dimension")
-        target = target.contiguous().reshape(rows)
+        if not target.is_contiguous():  # the copy belongs to the stream that reads it
+            with _on_device(x.device), _allocating(stream):
+                target = target.contiguous()
+        target = target.reshape(rows)
     x2 = x.reshape(rows, N)
     if torch.is_grad_enabled() and x.requires_grad:
         *s, low = _function("token_stats", _token_stats_function).apply(x2, target, top_k, stream)
