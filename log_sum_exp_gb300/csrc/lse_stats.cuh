@@ -11,7 +11,7 @@
 //
 //     ln 2 * ( log2 s + u / s ),   s = sum 2^z,   u = sum 2^z (-z),
 //
-// a sum of two non-negative terms, so nothing cancels.  (m, s, u) is kept online:
+// a sum of two non-negative terms.  (m, s, u) is kept online:
 // raising the maximum by d (in units of z) turns u into (u + d s) 2^-d and s into
 // s 2^-d.
 #pragma once
@@ -33,7 +33,10 @@ namespace {
 
 // The exponentials' argument is z = x log2 e - c, c = fl(mu log2 e), by one FMA, so
 // every term carries the factor 2^r, r = mu log2 e - c, which the logarithm takes
-// out again; the entropy does not change with it.  Beyond |mu| = 2^24 (r would
+// out again; the entropy does not change with it but for rounding, as r enters log2 s
+// and u / s with opposite signs.  In a row with nearly all of p on one token that is all
+// there is, so what must not be negative (H, log sum exp(x - max)) ends at 0.  Beyond
+// |mu| = 2^24 (r would
 // exceed an octave), and for f16 where mu is next to the lowest value, z is
 // (x - mu) log2 e in two steps and r is 0.
 struct Shift {
@@ -96,14 +99,16 @@ __device__ __forceinline__ RowStats row_stats(StatAcc a) {
     if (a.s != a.s) return r;  // NaN in the row
     r.lse = a.m;               // +inf in it, or nothing but -inf
     if (!(fabsf(a.m) < __int_as_float(0x7f800000))) return r;
-    r.logs = kLn2 * (lg2(a.s) - shift_residue<DT>(a.m));
+    r.logs = fmaxf(kLn2 * (lg2(a.s) - shift_residue<DT>(a.m)), 0.0f);
     r.lse = a.m + r.logs;
     return r;
 }
 
 // NaN for a row that is no distribution.
 __device__ __forceinline__ float stat_entropy(StatAcc a, const RowStats& r) {
-    return r.logs != r.logs ? r.logs : kLn2 * (lg2(a.s) + a.u / a.s);
+    if (r.logs != r.logs) return r.logs;
+    const float h = kLn2 * (lg2(a.s) + a.u / a.s);
+    return h <= 0.0f ? 0.0f : h;
 }
 
 // x - lse as (x - max) - log sum exp(x - max): next to a large maximum lse itself
