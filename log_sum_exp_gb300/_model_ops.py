@@ -224,6 +224,13 @@ def _function(name, build):
     return _FUNCTIONS[name]
 
 
+def _needs_function(torch, t) -> bool:
+    """The result must know about t: t takes a gradient, or carries a forward-mode
+    tangent, which the autograd function refuses and a plain call would drop."""
+    return (torch.is_grad_enabled() and t.requires_grad) \
+        or torch.autograd.forward_ad.unpack_dual(t).tangent is not None
+
+
 def _token_stats_function(torch):
     class TokenStatsFunction(torch.autograd.Function):
         @staticmethod
@@ -255,8 +262,9 @@ def token_stats(x, target=None, top_k=0, stream=None) -> TokenStats:
     """``lse_token_stats`` over the last dimension of contiguous CUDA logits of any
     shape [..., N], differentiable with respect to x.
 
-    ``target`` has x's leading shape, in any strides.  ``logprob``, ``entropy``, ``lse`` and
-    ``top_logprob`` carry gradients.
+    ``target`` has x's leading shape, in any strides.  ``logprob``, ``entropy``,
+    ``lse`` and ``top_logprob`` carry gradients; forward-mode and second derivatives
+    are refused.
     """
     torch = _torch()
     if not x.is_cuda:
@@ -275,7 +283,7 @@ def token_stats(x, target=None, top_k=0, stream=None) -> TokenStats:
                 target = target.contiguous()
         target = target.reshape(rows)
     x2 = x.reshape(rows, N)
-    if torch.is_grad_enabled() and x.requires_grad:
+    if _needs_function(torch, x):
         *s, low = _function("token_stats", _token_stats_function).apply(x2, target, top_k, stream)
     else:
         s = lse_token_stats(x2, target, top_k, stream=stream)
@@ -503,8 +511,9 @@ def _embedding_function(torch):
 
 def embedding(ids, table, scale=1.0, padding=-1, stream=None):
     """``lse_embedding`` with int64 ids of any shape, differentiable with respect
-    to the table; tokens with id ``padding`` give it no gradient."""
+    to the table; tokens with id ``padding`` give it no gradient.  Forward-mode and
+    second derivatives are refused."""
     torch = _torch()
-    if torch.is_grad_enabled() and table.requires_grad:
+    if _needs_function(torch, table):
         return _function("embedding", _embedding_function).apply(table, ids, scale, padding, stream)
     return lse_embedding(table, ids, scale, stream=stream)
