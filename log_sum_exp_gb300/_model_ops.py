@@ -317,8 +317,12 @@ class GradList:
     order).
     ``out`` (optional) gives the tensors that ``lse_grad_clip`` writes, with the
     shapes, strides and types of ``grads``; without it gradients are clipped in
-    place.  The list holds its tensors alive and refers to their memory as it was
-    when the list was made: make a new one when gradients are reallocated.
+    place.  The list refers to the tensors' memory as it was when the list was made,
+    and keeps that memory alive, also where a tensor has been given other memory since
+    (``t.data = ...``).  It does not notice that: make a new list when gradients are
+    reallocated, as ``zero_grad(set_to_none=True)`` has them in every step.  Making one
+    takes about 1.3 us of host time per tensor (0.18 ms for 148), and so does every call
+    that is given plain tensors instead of a list.
     """
 
     def __init__(self, grads, out=None):
@@ -328,6 +332,7 @@ class GradList:
             raise ValueError("out must hold one tensor for each gradient")
         if not self.grads:
             raise ValueError("an empty list of gradients")
+        self._memory = [t.untyped_storage() for t in self.grads + (self.out or ())]
         self.device = self.grads[0].device
         if self.device.type != "cuda":
             raise ValueError("gradients must be CUDA tensors")
@@ -339,19 +344,19 @@ class GradList:
                 raise ValueError("gradients must share one device")
             if not _is_dense(g):
                 raise ValueError("a gradient must fill its memory without gaps")
-            o = None
+            p, n, to = g.data_ptr(), g.numel(), None
             if self.out is not None:
                 o = self.out[i]
+                to = o.data_ptr()
                 if o.dtype != g.dtype or o.device != self.device or o.shape != g.shape \
                         or (o.stride() != g.stride() and not (o.is_contiguous() and g.is_contiguous())):
                     raise ValueError("out must match the gradients' types, shapes and strides")
-            if g.numel():
-                nbytes = g.numel() * g.element_size()
-                spans.append((g.data_ptr(), nbytes))
-                if o is not None and o.data_ptr() != g.data_ptr():
-                    spans.append((o.data_ptr(), nbytes))
-            self._table[i] = LseTensor(g.data_ptr() or None, o.data_ptr() or None if o is not None else None,
-                                       g.numel(), dt)
+            if n:
+                nbytes = n * (2 if dt else 4)
+                spans.append((p, nbytes))
+                if to is not None and to != p:
+                    spans.append((to, nbytes))
+            self._table[i] = LseTensor(p or None, to or None, n, dt)
 
         spans.sort()
         if any(p + n > q for (p, n), (q, _) in zip(spans, spans[1:])):
