@@ -414,8 +414,11 @@ LSE_API lse_status lse_forward_split_static(const void *x, lse_dtype dtype, int6
  * nothing but -inf (or N == 0); there log-probabilities follow IEEE arithmetic
  * on x - lse (NaN in a row of only -inf).  In every other row they are computed
  * as (x - max) - log sum exp(x - max), which keeps its digits when all logits
- * are large.
- * Results do not depend on scheduling: equal inputs give equal bits.
+ * are large.  No entropy is negative and no log-probability of a finite row
+ * positive.
+ * Results do not depend on scheduling: a repeated call gives equal bits.  The
+ * order of the sums follows B, N, top_k, the element type, the alignment of
+ * the rows and the GPU's number of SMs.
  */
 LSE_API lse_status lse_token_stats(const void *x, lse_dtype dtype, int64_t B, int64_t N,
                                    int64_t row_stride, const int64_t *target, int64_t top_k,
@@ -490,7 +493,10 @@ typedef struct {
  * Squares are summed without overflow or underflow over the whole f32 range
  * (the result is +inf only where the norm itself exceeds it, or a gradient is
  * infinite); a NaN gradient gives NaN.  No elements give 0.  The summation
- * order is fixed by the sizes alone.  Takes a few KB of stream-ordered scratch.
+ * order follows the sizes, types and order of the tensors, their offsets from
+ * 16-byte boundaries and the GPU's number of SMs, so a repeated call gives
+ * equal bits and the same values elsewhere may differ in the last one.  Takes a
+ * few KB of stream-ordered scratch.
  */
 LSE_API lse_status lse_grad_norm(const lse_tensor *tensors, int64_t count, float *norm,
                                  lse_stream_t stream);
@@ -528,9 +534,11 @@ LSE_API lse_status lse_embedding(const void *table, lse_dtype dtype, int64_t V, 
  *     dtable[v, :] = scale * sum over t with ids[t] = v of grad[t, :]
  *
  * (plus the dtable[v, :] that was there, when accumulate is nonzero).  Tokens
- * are sorted by id and summed in f32 in an order that the sizes and ids alone
- * fix (so equal inputs give equal bits), and rounded once.  Rows without a
- * token are zeroed, or left as they are with accumulate.
+ * are sorted by id and summed in f32, in their order within tiles and tile by
+ * tile, without floating-point atomics, and rounded once: a repeated call gives
+ * equal bits.  The tiles follow T, D, the ids, and the alignment and strides of
+ * grad and dtable.  Rows without a token are zeroed, or left as they are with
+ * accumulate.
  *   padding      tokens with this id add nothing (-1: none is left out);
  *                neither do ids outside [0, V).
  *   dtable       V rows of D elements of dtable_dtype, which is dtype or

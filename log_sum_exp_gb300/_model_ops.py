@@ -459,7 +459,8 @@ def lse_embedding_backward(grad, ids, rows, scale=1.0, padding=-1, dtable=None, 
     Ids equal to ``padding`` or outside [0, V) add nothing.  ``dtable``
     (optional) is [V, D] of grad's dtype or float32; with ``accumulate`` the
     gradient is added to what it holds, and rows without a token stay untouched.
-    The sums run in f32 in the tokens' order.
+    The sums run in f32 over tiles of the tokens in their order, then over the tiles;
+    a repeated call gives equal bits.
     """
     torch = _torch()
     if not grad.is_cuda:

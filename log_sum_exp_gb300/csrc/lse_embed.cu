@@ -9,9 +9,11 @@
 // are cut into tiles of equal length, whatever their ids, so a frequent token's rows
 // are summed by many CTAs at once: a run of one id inside a tile is summed and written
 // by it, a run that crosses tiles leaves one partial sum per tile, which a second
-// kernel adds up in order.  Nothing is added through floating-point atomics, and equal
-// inputs give equal bits.  Rows without a token are found in a bitmap and zeroed by
-// further CTAs of the summing kernel.
+// kernel adds up in order.  Nothing is added through floating-point atomics: a repeated
+// call gives equal bits (tile lengths follow the sizes and the alignment).  Up to a few
+// thousand tokens are put in order by counting instead.  Rows are zeroed by further CTAs
+// of all these kernels: of the sort's first ones (and of the counting) whether they have
+// tokens or not, later by a bitmap of the ids that occur.
 #include <climits>
 #include <cmath>
 #include <cstdint>
