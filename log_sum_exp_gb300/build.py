@@ -17,7 +17,7 @@ SOURCES = ["lse_api.cu", "lse_kernels_f32.cu", "lse_kernels_bf16.cu", "lse_kerne
            "lse_strided.cu", "lse_rowtile.cu", "lse_noalloc.cu", "lse_ex16_f32.cu",
            "lse_ex16_bf16.cu", "lse_ex16_f16.cu", "lse_stats.cu", "lse_stats_f32.cu", "lse_stats_bf16.cu",
            "lse_stats_f16.cu", "lse_grads.cu", "lse_embed.cu"]
-HEADERS = ["lse_device.cuh", "lse_edges.cuh", "lse_kernels.cuh", "lse_internal.h", "lse_topk.cuh",
+HEADERS = ["lse_device.cuh", "lse_edges.cuh", "lse_kernels.cuh", "lse_internal.h", "lse_elem.cuh", "lse_topk.cuh",
            "lse_stats.cuh", "lse_stats_common.cuh"]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -106,8 +106,6 @@ cudaError_t scratch_alloc(const DeviceInfo& info, void** p, size_t bytes, cudaSt
     return cudaMallocFromPoolAsync(p, bytes, info.pool, stream);
 }
 
-bool valid_dtype(int dt) { return dt == LSE_F32 || dt == LSE_BF16 || dt == LSE_F16; }
-
 int pow2_ceil(int64_t v) {
     int p = 1;
     while (p < v) p <<= 1;

@@ -147,26 +147,6 @@ template <> __device__ __forceinline__ float load_elem<kF16>(const void* row, in
     return __half2float(__ushort_as_half(h));
 }
 
-// The same two loads for what the kernel itself may write (an output that is the input):
-// the read-only path above is for memory that nothing writes while the kernel runs.
-__device__ __forceinline__ uint4 ld_stream16(const void* p) {
-    uint4 r;
-    asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                 : "l"(p)
-                 : "memory");
-    return r;
-}
-template <int DT> __device__ __forceinline__ float load_own_elem(const void* row, int64_t i) {
-    if constexpr (DT == kF32) {
-        return static_cast<const float*>(row)[i];
-    } else {
-        const unsigned short h = static_cast<const unsigned short*>(row)[i];
-        if constexpr (DT == kBF16) return __uint_as_float(static_cast<uint32_t>(h) << 16);
-        else return __half2float(__ushort_as_half(h));
-    }
-}
-
 // Low / high element of a 32-bit word holding one f32 or two 16-bit elements.
 template <int DT> __device__ __forceinline__ float word_lo(uint32_t w);
 template <int DT> __device__ __forceinline__ float word_hi(uint32_t w);

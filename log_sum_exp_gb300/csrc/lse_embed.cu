@@ -23,26 +23,13 @@
 #include <cuda_runtime.h>
 
 #include "lse_device.cuh"
+#include "lse_elem.cuh"
 #include "lse_internal.h"
 
 namespace lse {
 namespace {
 
 constexpr int kEmbedThreads = 256;
-
-template <int DT>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    uint32_t r;
-    if constexpr (DT == kBF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-template <int DT>
-__device__ __forceinline__ void put_elem(void* row, int64_t i, float v) {
-    if constexpr (DT == kF32) static_cast<float*>(row)[i] = v;
-    else static_cast<unsigned short*>(row)[i] = static_cast<unsigned short>(pack2<DT>(v, 0.0f));
-}
 
 // The 4 or 8 elements of a 16-byte vector as f32 and back.
 template <int DT>
@@ -755,9 +742,6 @@ bool rows_ok(int64_t rows, int64_t D, int64_t stride, int64_t eb) {
     if (rows > 0 && __builtin_mul_overflow(rows - 1, stride, &extent)) return false;
     return !__builtin_add_overflow(extent, D, &extent) && !__builtin_mul_overflow(extent, eb, &extent);
 }
-
-bool valid_dtype(int dt) { return dt == LSE_F32 || dt == LSE_BF16 || dt == LSE_F16; }
-bool misaligned(const void* p, uintptr_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; }
 
 unsigned capped(int64_t n, int64_t most) { return static_cast<unsigned>(n < 1 ? 1 : n < most ? n : most); }
 

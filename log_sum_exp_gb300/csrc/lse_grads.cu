@@ -24,6 +24,7 @@
 
 #include "lse_device.cuh"
 #include "lse_edges.cuh"
+#include "lse_elem.cuh"
 #include "lse_internal.h"
 
 namespace lse {
@@ -264,8 +265,7 @@ __device__ __forceinline__ void chunk_scale(const GradEntry& t, int64_t k0, floa
                     o[i + 1] = __float_as_uint(y);
                 } else {
                     f2_unpack(f2_mul(f2_pack(word_lo<DT>(w[i]), word_hi<DT>(w[i])), c2), x, y);
-                    if constexpr (DT == kBF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[i]) : "f"(y), "f"(x));
-                    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[i]) : "f"(y), "f"(x));
+                    o[i] = pack2<DT>(x, y);
                 }
             }
             if (vec && (kk > 0 || off == 0) && (kk + 1) * 16 <= end) {

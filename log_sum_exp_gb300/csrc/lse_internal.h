@@ -197,6 +197,9 @@ inline lse_status cuda_status(cudaError_t e) {
     record_cuda_error(e);
     return LSE_ERR_CUDA;
 }
+// Checks of arguments.
+inline bool valid_dtype(int dt) { return dt == LSE_F32 || dt == LSE_BF16 || dt == LSE_F16; }
+inline bool misaligned(const void* p, uintptr_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; }
 // SMs of the current device.
 lse_status device_sms(int* sms);
 // Stream-ordered scratch of the current device from the library pool (the

@@ -321,9 +321,6 @@ cudaError_t launch_stats_backward(StatsBackwardArgs a, int sms, cudaStream_t str
     }
 }
 
-// The checks that the forward and the backward share beyond check_args.
-bool misaligned(const void* p, uintptr_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; }
-
 }  // namespace
 }  // namespace lse
 

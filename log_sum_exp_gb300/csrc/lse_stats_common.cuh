@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include "lse_device.cuh"
+#include "lse_elem.cuh"
 
 namespace lse {
 
@@ -28,15 +29,6 @@ struct StatsArgs {
 cudaError_t launch_token_stats_f32(const StatsArgs& a, int sms, cudaStream_t s);
 cudaError_t launch_token_stats_bf16(const StatsArgs& a, int sms, cudaStream_t s);
 cudaError_t launch_token_stats_f16(const StatsArgs& a, int sms, cudaStream_t s);
-
-// Two floats -> packed 16-bit pair, nearest-even.
-template <int DT>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    uint32_t r;
-    if constexpr (DT == kBF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 
 // Below this many octaves of the maximum an exponential is 0 in f32.
 constexpr float kFarBelow = -16384.0f;
