@@ -435,13 +435,14 @@ sort_rank_kernel(const __grid_constant__ SortArgs a, uint32_t* cross_count) {
 constexpr int kLongRun = 7;  // further tiles of a run that counts as long
 // Bytes zeroed next to the counting, to each sorting pass and to the joins: about what
 // the memory takes while these wait for their own few loads (32768 tokens, 2048 columns:
-// 136 us with 4, 24 and 24 MB, 130 with 8, 40 and 40, 127 with these).
+// 136 us with 4, 24 and 24 MB, 130 with 8, 40 and 40, 127 with these).  Measured at that
+// size alone; the waits of other sizes are longer or shorter, and the bytes do not follow.
 constexpr int64_t kCountZeroBytes = 16 << 20;
 constexpr int64_t kSortZeroBytes = 56 << 20;
 // The ranking kernel zeroes all rows alone, without the overlap with the joins: it is
 // taken while there are no more bytes than the sorting passes would zero.
 constexpr int64_t kRankZeroBytes = kCountZeroBytes + 2 * kSortZeroBytes;
-constexpr int64_t kJoinCtas = 608;  // four for each SM
+constexpr int64_t kJoinCtas = 608;  // four for each of the 152 SMs
 constexpr int64_t kJoinZeroBytes = 40 << 20;
 constexpr int64_t kSumCtas = 256;
 
@@ -545,7 +546,9 @@ __device__ __forceinline__ void end_run(const SumArgs& a, uint32_t run, bool beg
 // left of 128256 zeroed in 69 us, 6.5 TB/s.  A thread owns a column slot of a tile and walks down
 // its tokens, U rows in flight; whether a token starts a run is found out once per tile
 // and not by every thread, and a batch without a start is added without looking (122 to
-// 119 us for the whole gradient).  A second batch in flight meanwhile spills (123).
+// 119 us for the whole gradient).  A second batch in flight meanwhile spills in the loop
+// (123); as it is 16-bit rows spill 56 bytes, at the ends of runs (0.8 % of the
+// instructions executed are to local memory).
 // A tile's tokens in whole batches of U.
 __host__ __device__ constexpr int sum_padded(int len, int U) { return (len + U - 1) / U * U; }
 

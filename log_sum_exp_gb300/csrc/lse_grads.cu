@@ -8,7 +8,8 @@
 // are not written), in chunks of kChunk vectors, numbered through the list.  CTA c of
 // G takes a contiguous range of chunks, so it looks its tensors up once and then
 // walks.  (Walking the ranges backwards when clipping, to meet what L2 still holds,
-// measured the same: 388 us for 400 M bf16 elements either way.)  The list travels as a
+// measured the same: 388 us for 400 M bf16 elements either way, before the loads were
+// ordinary ones; 386 now.)  The list travels as a
 // kernel parameter: a call copies nothing to the device and can be captured.
 //
 // A thread squares and adds up to 64 elements in f32 (four sums, so at most 16
@@ -243,7 +244,8 @@ __device__ __forceinline__ void chunk_scale(const GradEntry& t, int64_t k0, floa
     const int64_t end = off + t.numel * EB;
     const int64_t vectors = (end + 15) >> 4;
     const uint64_t c2 = f2_pack(coef, coef);
-    // (four vectors at a time: eight would spill at 64 registers)
+    // (four vectors at a time: eight would spill in the loop at 64 registers; four spill 48
+    // bytes in the parts for a tensor's ends, none of it executed for whole vectors)
 #pragma unroll 1
     for (int64_t k = k0 + threadIdx.x; k < k0 + kChunk && k < vectors; k += kScaleU * kGradThreads) {
         uint4 v[kScaleU];
@@ -280,7 +282,7 @@ __device__ __forceinline__ void chunk_scale(const GradEntry& t, int64_t k0, floa
 }
 
 // Bound by one read and one write: 400 M bf16 in 258 us, 6.2 TB/s (the copy rate measured
-// on this GPU is 6.8).  Four loads per thread are in flight: eight spill (453 us), two
+// on this GPU is 6.8).  Four loads per thread are in flight: eight spill in the loop (453 us), two
 // measured 393 us for norm and clipping together against 388.
 //
 // `out` may be the tensor itself, and neighbouring tensors share vectors, so nothing here is
