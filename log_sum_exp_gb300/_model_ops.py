@@ -154,7 +154,8 @@ def lse_token_stats_backward(x, stats: TokenStats, target=None, grad_logprob=Non
                              grad_entropy=None, grad_top=None, grad_lse=None, dx=None, stream=None):
     """The gradient of ``lse_token_stats`` with respect to x.
 
-    ``stats`` is the forward's result; gradients left out count as zeros.
+    ``stats`` is the forward's result, or any object with its attributes (``lse_low``
+    may be missing); gradients left out count as zeros.
     ``dx`` (optional) has x's dtype and shape and may be x itself.  A row whose
     gradients are all zero gets zeros, whatever it holds.
     """
@@ -166,8 +167,9 @@ def lse_token_stats_backward(x, stats: TokenStats, target=None, grad_logprob=Non
     device, f32, i64 = x.device, torch.float32, torch.int64
     K = stats.top_index.shape[-1] if stats.top_index is not None else 0
     _need_vector(stats.lse, "stats.lse", f32, B, device)
-    if stats.lse_low is not None:
-        _need_vector(stats.lse_low, "stats.lse_low", f32, B, device)
+    low = getattr(stats, "lse_low", None)
+    if low is not None:
+        _need_vector(low, "stats.lse_low", f32, B, device)
     if grad_logprob is not None:
         if target is None:
             raise ValueError("grad_logprob needs target")
@@ -187,13 +189,13 @@ def lse_token_stats_backward(x, stats: TokenStats, target=None, grad_logprob=Non
         _need_vector(grad_lse, "grad_lse", f32, B, device)
     if dx is not None and (dx.shape != x.shape or dx.dtype != x.dtype or dx.device != device):
         raise ValueError("dx must match x's shape, dtype and device")
-    args = (torch, x, dt, B, N, row_stride, stats, target, K, grad_logprob, grad_entropy, grad_top,
-            grad_lse, dx, stream, device)
+    args = (torch, x, dt, B, N, row_stride, stats, low, target, K, grad_logprob, grad_entropy,
+            grad_top, grad_lse, dx, stream, device)
     return _stats_backward_call(*args) if _at_home(torch, stream, device) \
         else _elsewhere(_stats_backward_call, args)
 
 
-def _stats_backward_call(torch, x, dt, B, N, row_stride, stats, target, K, grad_logprob,
+def _stats_backward_call(torch, x, dt, B, N, row_stride, stats, low, target, K, grad_logprob,
                          grad_entropy, grad_top, grad_lse, dx, stream, device):
     if dx is None:
         dx = torch.empty_like(x, memory_format=torch.contiguous_format)
@@ -202,7 +204,7 @@ def _stats_backward_call(torch, x, dt, B, N, row_stride, stats, target, K, grad_
         dx_stride = _rows(dx)[2]
     _check(load().lse_token_stats_backward_pair(
         x.data_ptr(), dt, B, N, row_stride, stats.lse.data_ptr(),
-        None if stats.lse_low is None else stats.lse_low.data_ptr(),
+        None if low is None else low.data_ptr(),
         stats.entropy.data_ptr() if grad_entropy is not None else None,
         target.data_ptr() if grad_logprob is not None else None,
         stats.top_index.data_ptr() if grad_top is not None else None, K,
