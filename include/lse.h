@@ -508,9 +508,10 @@ LSE_API lse_status lse_grad_norm(const lse_tensor *tensors, int64_t count, float
  *
  * computed in f32 and rounded to nearest-even on store.  max_norm >= 0 and
  * eps >= 0.  Tensors clipped in place are not written when c = 1; those with an
- * `out` of their own are copied then.  An infinite norm gives c = 0 and a NaN
- * norm c = NaN, so infinite and NaN gradients become NaN.  Distinct tensors
- * and outs must not overlap.
+ * `out` of their own are copied then.  A norm of 0 gives c = 1, whatever
+ * max_norm and eps are.  An infinite norm gives c = 0 (NaN with an infinite
+ * max_norm) and a NaN norm c = NaN, so infinite and NaN gradients become NaN.
+ * Distinct tensors and outs must not overlap.
  */
 LSE_API lse_status lse_grad_clip(const lse_tensor *tensors, int64_t count, float max_norm,
                                  float eps, float *norm, lse_stream_t stream);

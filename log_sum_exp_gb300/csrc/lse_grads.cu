@@ -300,7 +300,7 @@ grad_scale_kernel(const __grid_constant__ GradList<N> list, const double* __rest
     const float v = norm_of(partial, n, sh);
     if (blockIdx.x == 0 && threadIdx.x == 0) norm[0] = v;
     const float c0 = max_norm / (v + eps);
-    const float coef = c0 > 1.0f ? 1.0f : c0;  // NaN stays NaN
+    const float coef = c0 > 1.0f || v == 0.0f ? 1.0f : c0;  // NaN stays NaN, but zeros have nothing to clip (0 / 0)
     int c, last;
     chunk_range(list, &c, &last);
     int i = tensor_of(list, c);
