@@ -552,6 +552,167 @@ LSE_API lse_status lse_embedding_backward(const void *grad, lse_dtype dtype, int
                                           lse_dtype dtable_dtype, int64_t dtable_stride,
                                           int accumulate, lse_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Operators between a model's last block and its next token: the end of a block
+ * (norm, gate, residual scale, sum, norm), projections by matrices held in 4
+ * bits, and drawing tokens.  Conventions, status codes and streams as above.
+ * ------------------------------------------------------------------------ */
+
+/* How a block's output is gated. */
+typedef enum {
+    LSE_GATE_NONE = 0,
+    LSE_GATE_CHANNEL = 1, /* one value for every column, of the weights' type */
+    LSE_GATE_ELEMENT = 2  /* one for every element, of the rows' type         */
+} lse_gate;
+
+/*
+ * lse_residual_norm -- for every row t < T of D <= 16384 columns:
+ *
+ *     a[t] = y[t] post_rstd[t] post_weight       post_rstd = (mean y^2 + eps)^-1/2
+ *     h[t] = x[t] + scale gate a[t]
+ *     out[t] = h[t] rstd[t] weight               rstd = (mean h^2 + eps)^-1/2
+ *
+ * with a = y where post_weight is NULL, and gate = 1 for LSE_GATE_NONE.  Computed
+ * in f32 and rounded to nearest-even on store, out from h before its rounding.
+ *   x, y, h, out   rows of D elements of `dtype`, `*_stride` elements apart
+ *                (>= D).  y NULL: out is the norm of x alone (then gate_kind is
+ *                LSE_GATE_NONE and post_weight, h and post_rstd are NULL).  h may
+ *                be NULL.  h may be x itself and out may be y itself (same
+ *                stride); other overlaps are undefined.
+ *   gate         NULL, D values, or T rows gate_stride apart.
+ *   weight, post_weight   D values of weight_dtype, which is dtype or LSE_F32.
+ *   rstd, post_rstd       T floats each, or NULL: for lse_residual_norm_backward.
+ * T <= INT32_MAX; eps >= 0; scale finite.  NaN and infinities follow IEEE
+ * arithmetic on the formulas, row by row.  A sum of squares beyond the f32 range
+ * is infinite, so a row with magnitudes near 1e19 gives zeros.
+ */
+LSE_API lse_status lse_residual_norm(const void *x, lse_dtype dtype, int64_t T, int64_t D,
+                                     int64_t x_stride, const void *y, int64_t y_stride,
+                                     const void *gate, lse_gate gate_kind, int64_t gate_stride,
+                                     const void *post_weight, const void *weight,
+                                     lse_dtype weight_dtype, float scale, float eps, void *h,
+                                     int64_t h_stride, void *out, int64_t out_stride, float *rstd,
+                                     float *post_rstd, lse_stream_t stream);
+
+/*
+ * lse_residual_norm_backward -- the gradient of lse_residual_norm's h and out.
+ *   grad_out     what arrives at out; grad_h what arrives at h (NULL: zeros).
+ *   rstd, post_rstd   the forward's (post_rstd only with post_weight).
+ *   dx, dy       rows of dtype; dgate: D values of weight_dtype for
+ *                LSE_GATE_CHANNEL, T rows of dtype for LSE_GATE_ELEMENT.
+ *   dweight, dpost_weight   D values of weight_dtype: sums over all rows.
+ * Each output may be NULL (not wanted); none may overlap an input.  Sums over rows
+ * are taken in f32, row after row within a CTA and CTA by CTA, and rounded once; a
+ * repeated call gives equal bits (the rows of a CTA follow T, D, the alignment of
+ * the rows and the GPU's number of SMs).  T == 0 gives zeros there.  Takes
+ * stream-ordered scratch when a sum over rows is asked for.
+ */
+LSE_API lse_status lse_residual_norm_backward(
+    const void *grad_out, int64_t grad_out_stride, const void *grad_h, int64_t grad_h_stride,
+    const void *x, lse_dtype dtype, int64_t T, int64_t D, int64_t x_stride, const void *y,
+    int64_t y_stride, const void *gate, lse_gate gate_kind, int64_t gate_stride,
+    const void *post_weight, const void *weight, lse_dtype weight_dtype, float scale,
+    const float *rstd, const float *post_rstd, void *dx, int64_t dx_stride, void *dy,
+    int64_t dy_stride, void *dgate, int64_t dgate_stride, void *dpost_weight, void *dweight,
+    lse_stream_t stream);
+
+/*
+ * A matrix of N rows and K columns held in 4 bits: whole numbers q of -8 .. 7 and a
+ * scale for each group of 32, 64 or 128 columns, standing for q * scale.
+ *   codes        N rows of ceil(K / 128) * 64 bytes, on a 16-byte boundary.  Byte
+ *                16 c + 4 w (c, w < 4) of a 64-byte block starts the little-endian
+ *                word of its columns 32 w + 8 c .. + 7; bits 4 i .. of a word hold
+ *                q + 8 of its column 2 i, bits 16 + 4 i .. that of column 2 i + 1.
+ *                Columns from K on hold 8 (q = 0).
+ *   scales       ceil(K / group) values per row, rows scale_stride apart.
+ * K < 2^31 - 128.
+ */
+
+/*
+ * lse_quantize4 -- scales[n, g] = max |w| / 7 over the group, rounded to w's type,
+ * and q = w / scale rounded to the nearest whole number, halves to even (cut off at
+ * -8 and 7; a scale of 0 gives q = 0).  A group that holds a NaN or an infinity gets
+ * the scale NaN and q = 0, so it reads back as NaN.
+ *   w            N rows of K elements of `dtype`, w_stride apart; scales of dtype.
+ */
+LSE_API lse_status lse_quantize4(const void *w, lse_dtype dtype, int64_t N, int64_t K,
+                                 int64_t w_stride, int64_t group, void *codes, void *scales,
+                                 int64_t scale_stride, lse_stream_t stream);
+
+/* lse_pack4 -- the codes of given whole numbers (int8, rows values_stride apart; cut
+ * off at -8 and 7). */
+LSE_API lse_status lse_pack4(const signed char *values, int64_t N, int64_t K,
+                             int64_t values_stride, void *codes, lse_stream_t stream);
+
+/* lse_dequantize4 -- out[n, k] = q * scale, rounded to nearest-even to the scales'
+ * type `dtype`; rows of out lie out_stride (>= K) elements apart. */
+LSE_API lse_status lse_dequantize4(const void *codes, const void *scales, lse_dtype dtype,
+                                   int64_t scale_stride, int64_t N, int64_t K, int64_t group,
+                                   void *out, int64_t out_stride, lse_stream_t stream);
+
+/*
+ * lse_linear4 -- out[t, n] = sum_k x[t, k] q[n, k] scale[n, k / group], for T tokens.
+ * Products of a group are summed in f32 with the exact q, times the scale, and summed
+ * over the groups in f32; the result is rounded once.
+ *   x            T rows of K elements of `dtype`, x_stride apart (f32 tokens count with
+ *                all their bits).
+ *   scales       of scale_dtype, whatever dtype is.
+ *   out          T rows of N elements of out_dtype, which is dtype or LSE_F32,
+ *                out_stride apart (>= N).
+ * Made for few tokens: they are taken 32 at a time, and each time the codes are read.
+ * T <= 524280.  The order of the sums follows T, N, K, dtype, group and the GPU's
+ * number of SMs; a repeated call gives equal bits.
+ */
+LSE_API lse_status lse_linear4(const void *x, lse_dtype dtype, int64_t T, int64_t K,
+                               int64_t x_stride, const void *codes, const void *scales,
+                               lse_dtype scale_dtype, int64_t scale_stride, int64_t N,
+                               int64_t group, void *out, lse_dtype out_dtype,
+                               int64_t out_stride, lse_stream_t stream);
+
+/* Settings of lse_sample: each a device pointer to one value per row, or NULL and a
+ * value for all rows. */
+typedef struct {
+    const float *temperature_rows;
+    const int64_t *top_k_rows;
+    const float *top_p_rows;
+    const float *min_p_rows;
+    int64_t top_k;     /* 0 (or N and more): off                                  */
+    float temperature; /* 0 .. 1e20; below 1e-20 the largest element is drawn     */
+    float top_p;       /* 1 and more: off                                         */
+    float min_p;       /* 0: off                                                  */
+} lse_sampling;
+
+/*
+ * lse_sample -- a token for every row of logits from a given uniform number.  With the
+ * columns of row b in the order (x descending, column ascending; -0 equals +0), m the
+ * row's largest element and w_n = exp((x_n - m) / temperature):
+ *
+ *     kept    the first top_k columns; of these, those before which the sum of w is
+ *             less than top_p times the sum of w over all of these (always the first);
+ *             of these, those with x_n - m >= temperature log(min(min_p, 1))
+ *     token   the first column n at which the sum of w over the kept columns up to n
+ *             (in column order) is more than u[b] times the sum over all kept ones
+ *     logprob (x_token - m) / temperature - log of the sum of w over the kept columns
+ *
+ *   u            B numbers of [0, 1).  One below 0 or NaN counts as 0, one of 1 or more
+ *                draws the last kept column.
+ *   settings     HOST struct, read during the call.
+ *   token        B int64.  logprob: B floats, or NULL.
+ * Sums are taken in whole numbers of 2^-44 (rows of more than 2^18 columns: as many bits
+ * fewer as N takes more), each w off by at most about 2^-30 of itself, so results do not
+ * depend on the order of sums: a repeated call gives equal bits, and the token is that of
+ * exact arithmetic unless a border of it lies within about 1e-9 of u.  A column whose w is
+ * below 2^-45 is not drawn.  Temperature 0 draws the first of the largest elements with
+ * logprob 0, whatever the other settings are.
+ * A row that is no distribution (it holds a NaN or +inf, or nothing but -inf, or N == 0),
+ * or whose own temperature is outside 0 .. 1e20 or whose top_p or min_p is NaN, gets the
+ * token -1 and logprob NaN; a top_k below 0 is off.  For values given for all rows those
+ * are refused.  B <= INT32_MAX, N < INT32_MAX - 64.
+ */
+LSE_API lse_status lse_sample(const void *x, lse_dtype dtype, int64_t B, int64_t N,
+                              int64_t row_stride, const float *u, const lse_sampling *settings,
+                              int64_t *token, float *logprob, lse_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -12,6 +12,7 @@ from ._binding import (  # noqa: F401
     PATHS,
     LseError,
     LsePlan,
+    LseSampling,
     LseTensor,
     library_path,
     load,
@@ -50,4 +51,17 @@ from ._model_ops import (  # noqa: F401
     lse_token_stats,
     lse_token_stats_backward,
     token_stats,
+)
+from ._block_ops import (  # noqa: F401
+    ResidualNorm,
+    ResidualNormGrads,
+    Sample,
+    Weights4,
+    lse_dequantize4,
+    lse_linear4,
+    lse_quantize4,
+    lse_residual_norm,
+    lse_residual_norm_backward,
+    lse_sample,
+    residual_norm,
 )

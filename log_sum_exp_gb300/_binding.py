@@ -28,7 +28,9 @@ ABI_FUNCTIONS = ["lse_forward", "lse_plan_query", "lse_forward_plan", "lse_forwa
                  "lse_last_cuda_error", "lse_forward_split_static",
                  "lse_token_stats", "lse_token_stats_pair", "lse_token_stats_backward",
                  "lse_token_stats_backward_pair", "lse_grad_norm", "lse_grad_clip",
-                 "lse_embedding", "lse_embedding_backward"]
+                 "lse_embedding", "lse_embedding_backward",
+                 "lse_residual_norm", "lse_residual_norm_backward", "lse_quantize4", "lse_pack4",
+                 "lse_dequantize4", "lse_linear4", "lse_sample"]
 
 
 class LsePlan(ctypes.Structure):
@@ -59,6 +61,20 @@ class LseTensor(ctypes.Structure):
         ("out", ctypes.c_void_p),
         ("numel", ctypes.c_int64),
         ("dtype", ctypes.c_int32),
+    ]
+
+
+class LseSampling(ctypes.Structure):
+    """Mirror of ``lse_sampling``."""
+    _fields_ = [
+        ("temperature_rows", ctypes.c_void_p),
+        ("top_k_rows", ctypes.c_void_p),
+        ("top_p_rows", ctypes.c_void_p),
+        ("min_p_rows", ctypes.c_void_p),
+        ("top_k", ctypes.c_int64),
+        ("temperature", ctypes.c_float),
+        ("top_p", ctypes.c_float),
+        ("min_p", ctypes.c_float),
     ]
 
 
@@ -138,6 +154,23 @@ def load() -> ctypes.CDLL:
         lib.lse_embedding_backward.argtypes = [vp, i32, i64, i64, i64, vp, i64, f32, i64, vp, i32,
                                                i64, i32, vp]
         lib.lse_embedding_backward.restype = i32
+        lib.lse_residual_norm.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i32, i64, vp, vp, i32,
+                                          f32, f32, vp, i64, vp, i64, vp, vp, vp]
+        lib.lse_residual_norm.restype = i32
+        lib.lse_residual_norm_backward.argtypes = [vp, i64, vp, i64, vp, i32, i64, i64, i64, vp, i64,
+                                                   vp, i32, i64, vp, vp, i32, f32, vp, vp, vp, i64,
+                                                   vp, i64, vp, i64, vp, vp, vp]
+        lib.lse_residual_norm_backward.restype = i32
+        lib.lse_quantize4.argtypes = [vp, i32, i64, i64, i64, i64, vp, vp, i64, vp]
+        lib.lse_quantize4.restype = i32
+        lib.lse_pack4.argtypes = [vp, i64, i64, i64, vp, vp]
+        lib.lse_pack4.restype = i32
+        lib.lse_dequantize4.argtypes = [vp, vp, i32, i64, i64, i64, i64, vp, i64, vp]
+        lib.lse_dequantize4.restype = i32
+        lib.lse_linear4.argtypes = [vp, i32, i64, i64, i64, vp, vp, i32, i64, i64, i64, vp, i32, i64, vp]
+        lib.lse_linear4.restype = i32
+        lib.lse_sample.argtypes = [vp, i32, i64, i64, i64, vp, ctypes.POINTER(LseSampling), vp, vp, vp]
+        lib.lse_sample.restype = i32
         lib.lse_wait_timeouts.argtypes = [ctypes.POINTER(ctypes.c_ulonglong)]
         lib.lse_wait_timeouts.restype = i32
         lib.lse_set_wait_limit.argtypes = [ctypes.c_uint32]

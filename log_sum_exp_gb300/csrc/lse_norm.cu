@@ -1,0 +1,805 @@
+// lse_norm.cu -- the end of a block: norm of its output, gate, residual scale, the sum with
+// the residual stream and the norm of the sum, and their gradient (sm_103a).
+//
+//     r1 = (mean y^2 + eps)^-1/2     a = y r1 w1     (w1 absent: a = y)
+//     h  = x + s g a                 r2 = (mean h^2 + eps)^-1/2     out = h r2 w
+//
+// Bound by memory: x and y are read once, h and out written once, and a row stays in
+// registers between its two sums, which depend on each other.  The sums are taken apart
+// although sum h^2 could be written in sums that do not need r1: where x and s g a cancel,
+// those lose all their digits.
+//
+// Gradient, with G what arrives at h from both sides:
+//
+//     n = w dout     G = dh + r2 n - h r2^3/D sum(n h)     dx = G
+//     e = s g w1 G   dy = r1 e - y r1^3/D sum(e y)         dgate = s a G
+//     dw = sum over rows of dout h r2                      dw1 = the same of s g G y r1
+//
+// sum(e y) needs G, which needs sum(n h); with q = s g w1 y it is sum q (dh + r2 n) -
+// r2^3/D sum(n h) sum(q h), so one reduction per row carries all three sums.
+// CTAs walk over rows and keep the sums over rows for the columns of each thread in
+// registers; a second kernel adds the CTAs' parts in their order, so a repeated call gives
+// equal bits.  For a gate of one value per column, dw1 = g S and dgate = w1 S share the sum
+// S = sum s G y r1.
+#include <cmath>
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "lse_device.cuh"
+#include "lse_elem.cuh"
+#include "lse_internal.h"
+
+namespace lse {
+namespace {
+
+enum Gate : int { kNoGate = LSE_GATE_NONE, kChannelGate = LSE_GATE_CHANNEL, kElementGate = LSE_GATE_ELEMENT };
+
+constexpr int kNormMaxColumns = 16384;
+
+struct NormArgs {
+    int64_t T;
+    int D;
+    const char* x;
+    const char* y;     // may be null: h = x
+    const char* gate;  // null, a row of columns, or T rows
+    const char* post;  // null: no norm of y
+    const char* weight;
+    int64_t x_bytes, y_bytes, gate_bytes;  // between rows
+    bool weights_f32;  // weight, post and a channel gate (else of the rows' type)
+    bool weights_vec;  // they start on 16-byte boundaries
+    int gate_kind;
+    float scale, eps, inv_d;
+    // forward
+    char* h;  // null: not wanted
+    char* out;
+    int64_t h_bytes, out_bytes;
+    float* rstd;       // may be null
+    float* post_rstd;  // may be null
+    // gradient
+    const char* dout;
+    const char* dh;  // may be null: zeros
+    int64_t dout_bytes, dh_bytes;
+    const float* rstd_in;
+    const float* post_rstd_in;
+    char* dx;     // each may be null
+    char* dy;
+    char* dgate;  // of an element gate
+    int64_t dx_bytes, dy_bytes, dgate_bytes;
+    float* part;  // [2, parts, D]; null: no sums over rows are wanted
+    int parts;
+};
+
+// ---------------------------------------------------------------------------
+// A thread's share of a row: V slots of 16 bytes.  VEC: the aligned vectors that cover the
+// row, which lies `off` bytes behind a boundary in every array; else single elements, the
+// lanes of a group next to each other.  Elements outside the row are zeros.
+// ---------------------------------------------------------------------------
+template <int DT> struct Slot {
+    static constexpr int EB = DType<DT>::bytes, E = 16 / EB;
+    uint32_t w[4];
+};
+
+template <int DT> __device__ __forceinline__ void slot_floats(const Slot<DT>& s, float (&f)[Slot<DT>::E]) {
+    if constexpr (DT == kF32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(s.w[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = word_lo<DT>(s.w[i]);
+            f[2 * i + 1] = word_hi<DT>(s.w[i]);
+        }
+    }
+}
+
+template <int DT> __device__ __forceinline__ Slot<DT> slot_of(const float (&f)[Slot<DT>::E]) {
+    Slot<DT> s;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (DT == kF32) s.w[i] = __float_as_uint(f[i]);
+        else s.w[i] = pack2<DT>(f[2 * i], f[2 * i + 1]);
+    }
+    return s;
+}
+
+// Columns of slot j of thread t: element i is column c + i * step.
+template <int DT, int TX, bool VEC> struct Columns {
+    int c, step;
+    bool whole;  // VEC: no element lies outside the row
+    bool any;
+    __device__ __forceinline__ Columns(int j, int t, int off_e, int D) {
+        constexpr int E = Slot<DT>::E;
+        if constexpr (VEC) {
+            c = (j * TX + t) * E - off_e;
+            step = 1;
+            whole = c >= 0 && c + E <= D;
+            any = c < D;
+        } else {
+            c = j * E * TX + t;
+            step = TX;
+            whole = false;
+            any = c < D;
+        }
+    }
+};
+
+template <int DT, class C> __device__ __forceinline__ Slot<DT> load_slot(const char* row, const C& at, int D) {
+    constexpr int E = Slot<DT>::E, EB = Slot<DT>::EB;
+    Slot<DT> s;
+    if (at.whole) {
+        const uint4 v = ld_stream16(row + static_cast<int64_t>(at.c) * EB);
+        s.w[0] = v.x, s.w[1] = v.y, s.w[2] = v.z, s.w[3] = v.w;
+        return s;
+    }
+    s.w[0] = s.w[1] = s.w[2] = s.w[3] = 0;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        const int c = at.c + i * at.step;
+        if (c < 0 || c >= D) continue;
+        if constexpr (DT == kF32) s.w[i] = reinterpret_cast<const uint32_t*>(row)[c];
+        else s.w[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const unsigned short*>(row)[c]) << (i % 2 * 16);
+    }
+    return s;
+}
+
+template <int DT, class C> __device__ __forceinline__ void store_slot(char* row, const C& at, int D, const Slot<DT>& s) {
+    constexpr int E = Slot<DT>::E, EB = Slot<DT>::EB;
+    if (at.whole) {
+        *reinterpret_cast<uint4*>(row + static_cast<int64_t>(at.c) * EB) = make_uint4(s.w[0], s.w[1], s.w[2], s.w[3]);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        const int c = at.c + i * at.step;
+        if (c < 0 || c >= D) continue;
+        if constexpr (DT == kF32) reinterpret_cast<uint32_t*>(row)[c] = s.w[i];
+        else reinterpret_cast<unsigned short*>(row)[c] = static_cast<unsigned short>(s.w[i / 2] >> (i % 2 * 16));
+    }
+}
+
+// The same columns of a vector of weights (1 outside the row: it meets zeros only).
+template <int DT, class C>
+__device__ __forceinline__ void load_weights(const char* p, const C& at, int D, const NormArgs& a,
+                                             float (&f)[Slot<DT>::E]) {
+    constexpr int E = Slot<DT>::E;
+    if (at.whole && a.weights_vec) {
+        if (DT == kF32 || a.weights_f32) {
+            const char* q = p + static_cast<int64_t>(at.c) * 4;
+            if ((at.c & 3) == 0) {
+#pragma unroll
+                for (int i = 0; i < E; i += 4) {
+                    const float4 v = __ldg(reinterpret_cast<const float4*>(q + i * 4));
+                    f[i] = v.x, f[i + 1] = v.y, f[i + 2] = v.z, f[i + 3] = v.w;
+                }
+                return;
+            }
+        } else if ((at.c & 7) == 0) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(p + static_cast<int64_t>(at.c) * 2));
+            Slot<DT> s;
+            s.w[0] = v.x, s.w[1] = v.y, s.w[2] = v.z, s.w[3] = v.w;
+            slot_floats<DT>(s, f);
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        const int c = at.c + i * at.step;
+        f[i] = 1.0f;
+        if (c < 0 || c >= D) continue;
+        f[i] = (DT == kF32 || a.weights_f32) ? __ldg(reinterpret_cast<const float*>(p) + c) : load_elem<DT>(p, c);
+    }
+}
+
+// Sums of N values over the TX threads of a row, in every one of them.  `buf` holds one
+// value per warp; two calls in turn take different ones, so one barrier each suffices.
+template <int TX, int N> __device__ __forceinline__ void row_sums(float (&v)[N], float (*buf)[32]) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+#pragma unroll
+        for (int o = (TX < 32 ? TX : 32) / 2; o > 0; o >>= 1) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
+    }
+    if constexpr (TX > 32) {
+        constexpr int W = TX / 32;
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = warp / W * W;
+        if (lane == 0) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) buf[n][warp] = v[n];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            float s = lane < W ? buf[n][first + lane] : 0.0f;
+#pragma unroll
+            for (int o = W / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            v[n] = __shfl_sync(0xffffffffu, s, 0);
+        }
+    }
+}
+
+template <int TX> __host__ __device__ constexpr int norm_threads() { return TX < 128 ? 128 : TX; }
+
+// s * gate * (post weight) of a slot: what y (times r1) is multiplied by.
+template <int DT, class C>
+__device__ __forceinline__ void block_factors(const NormArgs& a, const C& at, const char* gate_row, float (&f)[Slot<DT>::E]) {
+    constexpr int E = Slot<DT>::E;
+#pragma unroll
+    for (int i = 0; i < E; ++i) f[i] = a.scale;
+    if (a.post) {
+        float w[E];
+        load_weights<DT>(a.post, at, a.D, a, w);
+#pragma unroll
+        for (int i = 0; i < E; ++i) f[i] *= w[i];
+    }
+    if (a.gate_kind != kNoGate) {
+        float g[E];
+        if (a.gate_kind == kChannelGate) load_weights<DT>(a.gate, at, a.D, a, g);
+        else slot_floats<DT>(load_slot<DT>(gate_row, at, a.D), g);
+#pragma unroll
+        for (int i = 0; i < E; ++i) f[i] *= g[i];
+    }
+}
+
+// TX threads per row, V slots per thread.
+template <int DT, int TX, int V, bool VEC>
+__global__ void __launch_bounds__(norm_threads<TX>()) norm_kernel(NormArgs a) {
+    constexpr int E = Slot<DT>::E, EB = Slot<DT>::EB;
+    __shared__ float buf[2][1][32];
+    pdl_trigger();
+    pdl_wait();
+    const int t = threadIdx.x % TX;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * (norm_threads<TX>() / TX) + threadIdx.x / TX;
+    const bool live = row < a.T;
+    const int D = live ? a.D : 0;
+    const char* xr = a.x + row * a.x_bytes;
+    const char* yr = a.y ? a.y + row * a.y_bytes : nullptr;
+    const char* gr = a.gate_kind == kElementGate ? a.gate + row * a.gate_bytes : nullptr;
+    const int off_e = VEC ? static_cast<int>(reinterpret_cast<uintptr_t>(xr) & 15) / EB : 0;
+
+    Slot<DT> x[V], y[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const Columns<DT, TX, VEC> at(j, t, off_e, D);
+        x[j].w[0] = x[j].w[1] = x[j].w[2] = x[j].w[3] = 0;
+        y[j] = x[j];
+        if (!at.any) continue;
+        x[j] = load_slot<DT>(xr, at, D);
+        if (yr) y[j] = load_slot<DT>(yr, at, D);
+    }
+    float r1 = 1.0f;
+    if (a.post) {
+        float s[1] = {0.0f};
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            float f[E];
+            slot_floats<DT>(y[j], f);
+#pragma unroll
+            for (int i = 0; i < E; ++i) s[0] = fmaf(f[i], f[i], s[0]);
+        }
+        row_sums<TX, 1>(s, buf[0]);
+        r1 = 1.0f / sqrtf(fmaf(s[0], a.inv_d, a.eps));
+        if (a.post_rstd && live && t == 0) a.post_rstd[row] = r1;
+    }
+    float h[V][E];
+    float s[1] = {0.0f};
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const Columns<DT, TX, VEC> at(j, t, off_e, D);
+        slot_floats<DT>(x[j], h[j]);
+        if (yr && at.any) {
+            float f[E], q[E];
+            slot_floats<DT>(y[j], f);
+            block_factors<DT>(a, at, gr, q);
+#pragma unroll
+            for (int i = 0; i < E; ++i) h[j][i] = fmaf(f[i] * r1, q[i], h[j][i]);
+        }
+        if (a.h && at.any) store_slot<DT>(a.h + row * a.h_bytes, at, D, slot_of<DT>(h[j]));
+#pragma unroll
+        for (int i = 0; i < E; ++i) s[0] = fmaf(h[j][i], h[j][i], s[0]);
+    }
+    row_sums<TX, 1>(s, buf[1]);
+    const float r2 = 1.0f / sqrtf(fmaf(s[0], a.inv_d, a.eps));
+    if (a.rstd && live && t == 0) a.rstd[row] = r2;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const Columns<DT, TX, VEC> at(j, t, off_e, D);
+        if (!at.any) continue;
+        float w[E];
+        load_weights<DT>(a.weight, at, D, a, w);
+#pragma unroll
+        for (int i = 0; i < E; ++i) h[j][i] = h[j][i] * r2 * w[i];
+        store_slot<DT>(a.out + row * a.out_bytes, at, D, slot_of<DT>(h[j]));
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Gradient.  The grid is a multiple of 8, so all rows of a group lie at the same offset
+// from a 16-byte boundary and a thread's slots are the same columns in each.
+// ---------------------------------------------------------------------------
+// What a slot adds to a row's sums: h, the gradient that arrives at it before the norm's
+// sum is taken off, and q = s g w1 y.
+template <int DT> struct GradSlot {
+    float h[Slot<DT>::E], gh[Slot<DT>::E], q[Slot<DT>::E];
+    Slot<DT> y;
+};
+struct GradRow {
+    const char *x, *y, *gate, *dout, *dh;
+    float r1, r2;
+};
+
+template <int DT, class C>
+__device__ __forceinline__ void grad_slot(const NormArgs& a, const GradRow& r, const C& at, int D, GradSlot<DT>& g,
+                                          float (&n)[Slot<DT>::E], float (*sw)[Slot<DT>::E]) {
+    constexpr int E = Slot<DT>::E;
+    Slot<DT> x, dn, dh;
+    x.w[0] = x.w[1] = x.w[2] = x.w[3] = 0;
+    g.y = dn = dh = x;
+    float w[E], f[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) g.q[i] = w[i] = 0.0f;
+    if (at.any) {
+        x = load_slot<DT>(r.x, at, D);
+        if (r.y) g.y = load_slot<DT>(r.y, at, D);
+        dn = load_slot<DT>(r.dout, at, D);
+        if (r.dh) dh = load_slot<DT>(r.dh, at, D);
+        load_weights<DT>(a.weight, at, D, a, w);
+        if (r.y) block_factors<DT>(a, at, r.gate, g.q);
+    }
+    slot_floats<DT>(x, g.h);
+    slot_floats<DT>(dn, n);
+    slot_floats<DT>(dh, g.gh);
+    slot_floats<DT>(g.y, f);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        g.q[i] *= f[i];
+        g.h[i] = fmaf(g.q[i], r.r1, g.h[i]);
+        if (sw) (*sw)[i] = fmaf(n[i] * r.r2, g.h[i], (*sw)[i]);
+        n[i] *= w[i];
+        g.gh[i] = fmaf(n[i], r.r2, g.gh[i]);
+    }
+}
+
+// One slot per thread stays in registers between the row's sums and its gradients; more
+// (rows of more than 16 KB) are loaded again, from L2: with the sums over rows they would
+// take more registers than an SM has.
+template <int DT, int TX, int V, bool VEC>
+__global__ void __launch_bounds__(norm_threads<TX>()) norm_backward_kernel(NormArgs a) {
+    constexpr int E = Slot<DT>::E, EB = Slot<DT>::EB, G = norm_threads<TX>() / TX;
+    constexpr int kShared = G > 1 ? TX * V * E : 1;
+    __shared__ float buf[2][3][32];
+    __shared__ float sums[2][kShared];
+    pdl_trigger();
+    pdl_wait();
+    const int t = threadIdx.x % TX, group = threadIdx.x / TX;
+    float sw[V][E], sp[V][E];  // sums over rows: of dw, and of dw1 or what it shares with dgate
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+        for (int i = 0; i < E; ++i) sw[j][i] = sp[j][i] = 0.0f;
+    int off_e = 0;
+    int turn = 0;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * G + group;
+    if (VEC && first < a.T)
+        off_e = static_cast<int>(reinterpret_cast<uintptr_t>(a.x + first * a.x_bytes) & 15) / EB;
+    for (int64_t base = static_cast<int64_t>(blockIdx.x) * G; base < a.T; base += static_cast<int64_t>(gridDim.x) * G, turn ^= 1) {
+        const int64_t row = base + group;
+        const bool live = row < a.T;
+        const int D = live ? a.D : 0;
+        GradRow r;
+        r.x = a.x + row * a.x_bytes;
+        r.y = a.y ? a.y + row * a.y_bytes : nullptr;
+        r.gate = a.gate_kind == kElementGate ? a.gate + row * a.gate_bytes : nullptr;
+        r.dout = a.dout + row * a.dout_bytes;
+        r.dh = a.dh ? a.dh + row * a.dh_bytes : nullptr;
+        r.r1 = live && a.post ? a.post_rstd_in[row] : 1.0f;
+        r.r2 = live ? a.rstd_in[row] : 0.0f;
+        GradSlot<DT> g;
+        float s[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const Columns<DT, TX, VEC> at(j, t, off_e, D);
+            float n[E];
+            grad_slot<DT>(a, r, at, D, g, n, &sw[j]);
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                s[0] = fmaf(n[i], g.h[i], s[0]);
+                s[1] = fmaf(g.q[i], g.gh[i], s[1]);
+                s[2] = fmaf(g.q[i], g.h[i], s[2]);
+            }
+        }
+        row_sums<TX, 3>(s, buf[turn]);
+        const float k2 = r.r2 * r.r2 * r.r2 * a.inv_d * s[0];
+        const float k1 = a.post ? r.r1 * r.r1 * r.r1 * a.inv_d * (s[1] - k2 * s[2]) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const Columns<DT, TX, VEC> at(j, t, off_e, D);
+            if (!at.any) continue;
+            float f[E], e[E], o[E];
+            if constexpr (V > 1) grad_slot<DT>(a, r, at, D, g, f, nullptr);
+            slot_floats<DT>(g.y, f);
+#pragma unroll
+            for (int i = 0; i < E; ++i) g.gh[i] = fmaf(-g.h[i], k2, g.gh[i]);  // G
+            if (a.dx) store_slot<DT>(a.dx + row * a.dx_bytes, at, D, slot_of<DT>(g.gh));
+            if (!r.y) continue;
+            if (a.dy) {
+                block_factors<DT>(a, at, r.gate, e);
+#pragma unroll
+                for (int i = 0; i < E; ++i) o[i] = fmaf(e[i] * g.gh[i], r.r1, -f[i] * k1);
+                store_slot<DT>(a.dy + row * a.dy_bytes, at, D, slot_of<DT>(o));
+            }
+            // s r1 y G: the sum that dw1 and the gate of a column share
+#pragma unroll
+            for (int i = 0; i < E; ++i) e[i] = g.gh[i] * f[i] * r.r1 * a.scale;
+            if (a.gate_kind == kElementGate) {
+                if (a.dgate) {
+                    if (a.post) load_weights<DT>(a.post, at, D, a, o);
+#pragma unroll
+                    for (int i = 0; i < E; ++i) o[i] = a.post ? e[i] * o[i] : e[i];
+                    store_slot<DT>(a.dgate + row * a.dgate_bytes, at, D, slot_of<DT>(o));
+                }
+                slot_floats<DT>(load_slot<DT>(r.gate, at, D), o);
+#pragma unroll
+                for (int i = 0; i < E; ++i) e[i] *= o[i];
+            }
+#pragma unroll
+            for (int i = 0; i < E; ++i) sp[j][i] += e[i];
+        }
+    }
+    if (!a.part) return;
+    // The CTA's part: the groups' sums one after the other.
+    const int64_t stride = static_cast<int64_t>(a.parts) * a.D;
+    float* pw = a.part + static_cast<int64_t>(blockIdx.x) * a.D;
+    if constexpr (G > 1) {
+        for (int i = threadIdx.x; i < kShared; i += norm_threads<TX>()) sums[0][i] = sums[1][i] = 0.0f;
+        for (int g = 0; g < G; ++g) {
+            __syncthreads();
+            if (g != group) continue;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const Columns<DT, TX, VEC> at(j, t, off_e, a.D);
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    const int c = at.c + i * at.step;
+                    if (c < 0 || c >= a.D) continue;
+                    sums[0][c] += sw[j][i];
+                    sums[1][c] += sp[j][i];
+                }
+            }
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < a.D; c += norm_threads<TX>()) {
+            pw[c] = sums[0][c];
+            pw[stride + c] = sums[1][c];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const Columns<DT, TX, VEC> at(j, t, off_e, a.D);
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const int c = at.c + i * at.step;
+                if (c < 0 || c >= a.D) continue;
+                pw[c] = sw[j][i];
+                pw[stride + c] = sp[j][i];
+            }
+        }
+    }
+}
+
+// Sums the parts of 32 columns: eight warps take the parts in turn, then their sums in order.
+constexpr int kFinishWarps = 8;
+struct NormFinishArgs {
+    const float* part;  // [2, parts, D]
+    int parts, D;
+    const void* post;  // factors of the second sum
+    const void* gate;
+    bool weights_f32;
+    void* dweight;  // each may be null
+    void* dpost;
+    void* dgate;
+};
+
+template <int DT> __device__ __forceinline__ float weight_at(const void* p, bool f32, int c) {
+    return f32 ? __ldg(static_cast<const float*>(p) + c) : load_elem<DT>(p, c);
+}
+template <int DT> __device__ __forceinline__ void put_weight(void* p, bool f32, int c, float v) {
+    if (DT == kF32 || f32) static_cast<float*>(p)[c] = v;
+    else static_cast<unsigned short*>(p)[c] = static_cast<unsigned short>(pack2<DT == kF32 ? kBF16 : DT>(v, 0.0f));
+}
+
+template <int DT>
+__global__ void __launch_bounds__(32 * kFinishWarps) norm_finish_kernel(NormFinishArgs a) {
+    __shared__ float sums[2][kFinishWarps][32];
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + lane;
+    float s0 = 0.0f, s1 = 0.0f;
+    if (c < a.D) {
+        const float* p = a.part + c;
+        const int64_t stride = static_cast<int64_t>(a.parts) * a.D;
+#pragma unroll 4
+        for (int i = warp; i < a.parts; i += kFinishWarps) {
+            s0 += p[static_cast<int64_t>(i) * a.D];
+            s1 += p[static_cast<int64_t>(i) * a.D + stride];
+        }
+    }
+    sums[0][warp][lane] = s0;
+    sums[1][warp][lane] = s1;
+    __syncthreads();
+    if (warp != 0 || c >= a.D) return;
+    s0 = s1 = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kFinishWarps; ++w) {
+        s0 += sums[0][w][lane];
+        s1 += sums[1][w][lane];
+    }
+    const bool f32 = DT == kF32 || a.weights_f32;
+    if (a.dweight) put_weight<DT>(a.dweight, f32, c, s0);
+    if (a.dpost) put_weight<DT>(a.dpost, f32, c, a.gate ? s1 * weight_at<DT>(a.gate, f32, c) : s1);
+    if (a.dgate) put_weight<DT>(a.dgate, f32, c, a.post ? s1 * weight_at<DT>(a.post, f32, c) : s1);
+}
+
+// ---------------------------------------------------------------------------
+// Launches
+// ---------------------------------------------------------------------------
+int64_t slots_of(int D, int EB, bool vec, bool aligned) {
+    const int64_t s = (static_cast<int64_t>(D) * EB + 15) / 16;
+    return s + (vec && !aligned ? 1 : 0);
+}
+
+template <int DT, bool VEC>
+cudaError_t launch_norm(const NormArgs& a, int64_t slots, cudaStream_t s) {
+    const auto go = [&](auto kernel, int tx) {
+        const int threads = tx < 128 ? 128 : tx;
+        const int64_t grid = (a.T + threads / tx - 1) / (threads / tx);
+        return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(threads), s, a);
+    };
+    if (slots <= 16) return go(norm_kernel<DT, 8, 2, VEC>, 8);
+    if (slots <= 64) return go(norm_kernel<DT, 32, 2, VEC>, 32);
+    if (slots <= 128) return go(norm_kernel<DT, 32, 4, VEC>, 32);
+    if (slots <= 256) return go(norm_kernel<DT, 128, 2, VEC>, 128);
+    if (slots <= 512) return go(norm_kernel<DT, 256, 2, VEC>, 256);
+    if (slots <= 1024) return go(norm_kernel<DT, 512, 2, VEC>, 512);
+    if (slots <= 2048) return go(norm_kernel<DT, 1024, 2, VEC>, 1024);
+    if constexpr (DT != kF32) {
+        return go(norm_kernel<DT, 1024, 3, VEC>, 1024);
+    } else {
+        if (slots <= 4096) return go(norm_kernel<DT, 1024, 4, VEC>, 1024);
+        return go(norm_kernel<DT, 1024, 5, VEC>, 1024);
+    }
+}
+
+// Rows that a CTA of the gradient takes at a time, and CTAs that are resident on an SM.
+struct BackwardPlan {
+    int tx, v, rows, grid;
+};
+BackwardPlan plan_norm_backward(int64_t T, int64_t slots, int sms) {
+    BackwardPlan p;
+    p.v = 1;
+    if (slots <= 8) p.tx = 8;
+    else if (slots <= 32) p.tx = 32;
+    else if (slots <= 64) p.tx = 64;
+    else if (slots <= 128) p.tx = 128;
+    else if (slots <= 256) p.tx = 256;
+    else if (slots <= 512) p.tx = 512;
+    else p.tx = 1024, p.v = slots <= 1024 ? 1 : slots <= 2048 ? 2 : 5;
+    const int threads = p.tx < 128 ? 128 : p.tx;
+    p.rows = threads / p.tx;
+    const int64_t resident = static_cast<int64_t>(sms) * (threads <= 128 ? 6 : threads == 256 ? 3 : threads == 512 ? 2 : 1) / 8 * 8;
+    int64_t grid = (T + p.rows - 1) / p.rows;
+    if (grid > resident) grid = resident;
+    p.grid = static_cast<int>((grid + 7) / 8 * 8);
+    return p;
+}
+
+template <int DT, bool VEC>
+cudaError_t launch_norm_backward(const NormArgs& a, const BackwardPlan& p, cudaStream_t s) {
+    const auto go = [&](auto kernel, int threads) {
+        return launch_pdl(kernel, dim3(static_cast<unsigned>(p.grid)), dim3(threads), s, a);
+    };
+    switch (p.tx) {
+    case 8: return go(norm_backward_kernel<DT, 8, 1, VEC>, 128);
+    case 32: return go(norm_backward_kernel<DT, 32, 1, VEC>, 128);
+    case 64: return go(norm_backward_kernel<DT, 64, 1, VEC>, 128);
+    case 128: return go(norm_backward_kernel<DT, 128, 1, VEC>, 128);
+    case 256: return go(norm_backward_kernel<DT, 256, 1, VEC>, 256);
+    case 512: return go(norm_backward_kernel<DT, 512, 1, VEC>, 512);
+    default:
+        return p.v == 1 ? go(norm_backward_kernel<DT, 1024, 1, VEC>, 1024)
+               : p.v == 2 ? go(norm_backward_kernel<DT, 1024, 2, VEC>, 1024)
+                          : go(norm_backward_kernel<DT, 1024, 5, VEC>, 1024);
+    }
+}
+
+// Rows of one array: pointer, distance and alignment.  Checked here so that every array of
+// a call is refused for the same reasons.
+struct Rows {
+    const void* p;
+    int64_t stride;
+    bool wanted;
+};
+
+// All rows start at the same offset from a 16-byte boundary, row by row.
+bool same_offsets(const Rows* rows, int n, int EB) {
+    for (int i = 1; i < n; ++i) {
+        if (!rows[i].p) continue;
+        if ((reinterpret_cast<uintptr_t>(rows[i].p) - reinterpret_cast<uintptr_t>(rows[0].p)) % 16 != 0) return false;
+        if ((rows[i].stride - rows[0].stride) * EB % 16 != 0) return false;
+    }
+    return true;
+}
+
+lse_status check_norm(int dtype, int64_t T, int64_t D, const Rows* rows, int n, int gate_kind, const void* gate,
+                      const void* weight, const void* post, int weight_dtype, float scale, float eps) {
+    if (!valid_dtype(dtype) || !valid_dtype(weight_dtype)) return LSE_ERR_UNSUPPORTED_DTYPE;
+    if (weight_dtype != dtype && weight_dtype != LSE_F32) return LSE_ERR_UNSUPPORTED_DTYPE;
+    if (T < 0 || D < 0 || D > kNormMaxColumns || T > INT32_MAX) return LSE_ERR_INVALID_ARG;
+    if (!(eps >= 0.0f) || !(fabsf(scale) <= 3.4e38f)) return LSE_ERR_INVALID_ARG;
+    if (gate_kind != kNoGate && gate_kind != kChannelGate && gate_kind != kElementGate) return LSE_ERR_INVALID_ARG;
+    const int eb = dtype == LSE_F32 ? 4 : 2, wb = weight_dtype == LSE_F32 ? 4 : 2;
+    for (int i = 0; i < n; ++i) {
+        if (!rows[i].p) {
+            if (rows[i].wanted && T > 0 && D > 0) return LSE_ERR_INVALID_ARG;
+            continue;
+        }
+        int64_t extent = 0;
+        if (rows[i].stride < D || misaligned(rows[i].p, eb) || __builtin_mul_overflow(T, rows[i].stride, &extent) ||
+            __builtin_mul_overflow(extent, static_cast<int64_t>(eb), &extent))
+            return LSE_ERR_INVALID_ARG;
+    }
+    if (misaligned(weight, wb) || misaligned(post, wb) || (gate_kind == kChannelGate && misaligned(gate, wb))) return LSE_ERR_INVALID_ARG;
+    if (T > 0 && D > 0 && (!weight || (gate_kind != kNoGate && !gate))) return LSE_ERR_INVALID_ARG;
+    return LSE_OK;
+}
+
+void set_common(NormArgs* a, int dtype, int64_t T, int64_t D, const void* x, int64_t x_stride, const void* y,
+                int64_t y_stride, int gate_kind, const void* gate, int64_t gate_stride, const void* post,
+                const void* weight, int weight_dtype, float scale) {
+    const int64_t eb = dtype == LSE_F32 ? 4 : 2;
+    a->T = T;
+    a->D = static_cast<int>(D);
+    a->x = static_cast<const char*>(x);
+    a->y = static_cast<const char*>(y);
+    a->x_bytes = x_stride * eb;
+    a->y_bytes = y_stride * eb;
+    a->gate_kind = gate_kind;
+    a->gate = static_cast<const char*>(gate);
+    a->gate_bytes = gate_stride * eb;
+    a->post = static_cast<const char*>(post);
+    a->weight = static_cast<const char*>(weight);
+    a->weights_f32 = weight_dtype == LSE_F32;
+    a->weights_vec = !misaligned(weight, 16) && !misaligned(post, 16) && (gate_kind != kChannelGate || !misaligned(gate, 16));
+    a->scale = scale;
+    a->inv_d = static_cast<float>(1.0 / static_cast<double>(D));
+}
+
+template <class F> cudaError_t by_type(int dtype, bool vec, F&& f) {
+    switch (dtype) {
+    case LSE_F32: return vec ? f(IntConst<kF32>{}, IntConst<1>{}) : f(IntConst<kF32>{}, IntConst<0>{});
+    case LSE_BF16: return vec ? f(IntConst<kBF16>{}, IntConst<1>{}) : f(IntConst<kBF16>{}, IntConst<0>{});
+    default: return vec ? f(IntConst<kF16>{}, IntConst<1>{}) : f(IntConst<kF16>{}, IntConst<0>{});
+    }
+}
+
+bool on_boundaries(const Rows& r, int eb) { return !misaligned(r.p, 16) && r.stride * eb % 16 == 0; }
+
+}  // namespace
+}  // namespace lse
+
+using namespace lse;
+
+extern "C" {
+
+lse_status lse_residual_norm(const void* x, lse_dtype dtype, int64_t T, int64_t D, int64_t x_stride, const void* y,
+                             int64_t y_stride, const void* gate, lse_gate gate_kind, int64_t gate_stride,
+                             const void* post_weight, const void* weight, lse_dtype weight_dtype, float scale,
+                             float eps, void* h, int64_t h_stride, void* out, int64_t out_stride, float* rstd,
+                             float* post_rstd, lse_stream_t stream) {
+    if (!y && T > 0 && D > 0) {  // nothing to add: h is x
+        if (gate_kind != LSE_GATE_NONE || post_weight || h || post_rstd) return LSE_ERR_INVALID_ARG;
+    }
+    const Rows rows[] = {{x, x_stride, true}, {y, y_stride, false}, {h, h_stride, false}, {out, out_stride, true},
+                         {gate_kind == LSE_GATE_ELEMENT ? gate : nullptr, gate_stride, false}};
+    const lse_status st = check_norm(dtype, T, D, rows, 5, gate_kind, gate, weight, post_weight, weight_dtype, scale, eps);
+    if (st != LSE_OK) return st;
+    if (misaligned(rstd, 4) || misaligned(post_rstd, 4)) return LSE_ERR_INVALID_ARG;
+    if (T == 0 || D == 0) return LSE_OK;
+    const int eb = dtype == LSE_F32 ? 4 : 2;
+    NormArgs a = {};
+    set_common(&a, dtype, T, D, x, x_stride, y, y_stride, gate_kind, gate, gate_stride, post_weight, weight, weight_dtype, scale);
+    a.eps = eps;
+    a.h = static_cast<char*>(h);
+    a.h_bytes = h_stride * eb;
+    a.out = static_cast<char*>(out);
+    a.out_bytes = out_stride * eb;
+    a.rstd = rstd;
+    a.post_rstd = post_rstd;
+    const bool vec = same_offsets(rows, 5, eb);
+    const int64_t slots = slots_of(a.D, eb, vec, on_boundaries(rows[0], eb));
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return cuda_status(by_type(dtype, vec, [&](auto dt, auto v) {
+        return launch_norm<decltype(dt)::value, decltype(v)::value != 0>(a, slots, s);
+    }));
+}
+
+lse_status lse_residual_norm_backward(const void* grad_out, int64_t grad_out_stride, const void* grad_h,
+                                      int64_t grad_h_stride, const void* x, lse_dtype dtype, int64_t T, int64_t D,
+                                      int64_t x_stride, const void* y, int64_t y_stride, const void* gate,
+                                      lse_gate gate_kind, int64_t gate_stride, const void* post_weight,
+                                      const void* weight, lse_dtype weight_dtype, float scale, const float* rstd,
+                                      const float* post_rstd, void* dx, int64_t dx_stride, void* dy, int64_t dy_stride,
+                                      void* dgate, int64_t dgate_stride, void* dpost_weight, void* dweight,
+                                      lse_stream_t stream) {
+    if (!y && T > 0 && D > 0 && (gate_kind != LSE_GATE_NONE || post_weight || dy)) return LSE_ERR_INVALID_ARG;
+    if ((dgate && gate_kind == LSE_GATE_NONE) || (dpost_weight && !post_weight)) return LSE_ERR_INVALID_ARG;
+    const bool by_element = gate_kind == LSE_GATE_ELEMENT;
+    const Rows rows[] = {{x, x_stride, true}, {y, y_stride, false}, {grad_out, grad_out_stride, true},
+                         {grad_h, grad_h_stride, false}, {by_element ? gate : nullptr, gate_stride, false},
+                         {dx, dx_stride, false}, {dy, dy_stride, false}, {by_element ? dgate : nullptr, dgate_stride, false}};
+    lse_status st = check_norm(dtype, T, D, rows, 8, gate_kind, gate, weight, post_weight, weight_dtype, scale, 0.0f);
+    if (st != LSE_OK) return st;
+    const uintptr_t wb = weight_dtype == LSE_F32 ? 4 : 2;
+    if (misaligned(rstd, 4) || misaligned(post_rstd, 4) || misaligned(dweight, wb) || misaligned(dpost_weight, wb) ||
+        (!by_element && misaligned(dgate, wb)))
+        return LSE_ERR_INVALID_ARG;
+    if (D == 0) return LSE_OK;
+    if (T > 0 && (!rstd || (post_weight && !post_rstd))) return LSE_ERR_INVALID_ARG;
+    const int eb = dtype == LSE_F32 ? 4 : 2;
+    NormArgs a = {};
+    set_common(&a, dtype, T, D, x, x_stride, y, y_stride, gate_kind, gate, gate_stride, post_weight, weight, weight_dtype, scale);
+    a.dout = static_cast<const char*>(grad_out);
+    a.dout_bytes = grad_out_stride * eb;
+    a.dh = static_cast<const char*>(grad_h);
+    a.dh_bytes = grad_h_stride * eb;
+    a.rstd_in = rstd;
+    a.post_rstd_in = post_rstd;
+    a.dx = static_cast<char*>(dx);
+    a.dx_bytes = dx_stride * eb;
+    a.dy = static_cast<char*>(dy);
+    a.dy_bytes = dy_stride * eb;
+    a.dgate = by_element ? static_cast<char*>(dgate) : nullptr;
+    a.dgate_bytes = dgate_stride * eb;
+    void* const dgate_columns = by_element ? nullptr : dgate;
+    const bool sums = dweight || dpost_weight || dgate_columns;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    void* scratch = nullptr;
+    cudaError_t e = cudaSuccess;
+    if (T > 0) {
+        int sms = 0;
+        if ((st = device_sms(&sms)) != LSE_OK) return st;
+        const bool vec = same_offsets(rows, 8, eb);
+        const BackwardPlan p = plan_norm_backward(T, slots_of(a.D, eb, vec, on_boundaries(rows[0], eb)), sms);
+        if (sums) {
+            st = take_scratch(&scratch, static_cast<size_t>(p.grid) * a.D * 2 * sizeof(float), s);
+            if (st != LSE_OK) return st;
+            a.part = static_cast<float*>(scratch);
+            a.parts = p.grid;
+        }
+        e = by_type(dtype, vec, [&](auto dt, auto v) {
+            return launch_norm_backward<decltype(dt)::value, decltype(v)::value != 0>(a, p, s);
+        });
+    }
+    if (sums && e == cudaSuccess) {
+        NormFinishArgs f;
+        f.part = a.part;
+        f.parts = a.parts;
+        f.D = a.D;
+        f.post = post_weight;
+        f.gate = gate_kind == LSE_GATE_CHANNEL ? gate : nullptr;
+        f.weights_f32 = a.weights_f32;
+        f.dweight = dweight;
+        f.dpost = dpost_weight;
+        f.dgate = dgate_columns;
+        e = by_type(dtype, true, [&](auto dt, auto) {
+            return launch_pdl(norm_finish_kernel<decltype(dt)::value>, dim3((a.D + 31) / 32), dim3(32 * kFinishWarps), s, f);
+        });
+    }
+    if (scratch) {
+        const cudaError_t freed = cudaFreeAsync(scratch, s);
+        if (e == cudaSuccess) e = freed;
+    }
+    return cuda_status(e);
+}
+
+}  // extern "C"
