@@ -12,23 +12,28 @@
 // complement of the column) is at least a threshold key.
 //
 // Precision.  A token changes where a sum passes a border, and a row has N borders, so sums
-// in 32 bits would give another token than the formula in one row of a few hundred.  Weights
-// are therefore whole numbers of 2^-S (S about 44): 2^z with z the distance to the maximum
-// in octaves, taken apart as 2^(k/64) 2^r with the remainder r formed without rounding the
-// product and a cubic for 2^r - 1; off by at most about 2^-30 of itself.  Sums of whole numbers do not
-// depend on their order.  That takes about 25 instructions, twice what the memory's rate leaves
-// for a bf16 element, so the pass over a whole row computes weights with ex2 instead, off by at
-// most kFastError of each (2^-22 of the instruction, whose argument carries its own rounding
-// error along, and the sums' roundings), and keeps a sum for every chunk of a few
-// thousand columns.  Where the drawn number lies further than that from both borders of its
-// token the result stands; else the row's sums are taken again exactly.
+// in 32 bits would give another token than the formula in one row of a few hundred.  Exact
+// weights are therefore whole numbers of 2^-S (S about 44): 2^z with z the distance to the
+// maximum in octaves, taken apart as 2^(k/64) 2^r with the remainder r formed without rounding
+// the product and a cubic for 2^r - 1; off by at most about 2^-30 of itself.  Sums of whole
+// numbers do not depend on their order.  That takes about 40 instructions, four times what the
+// memory's rate leaves for a bf16 element, so passes over a row use fast weights, of ex2 with the
+// rounding error of its argument carried along.  (ex2.approx is off by at most 1.45e-7, measured
+// over every f32 in [-32, 0); two sums that are compared may be off by twice that and by
+// the roundings of their additions, fast_error() in all.)  Where a comparison is closer than that,
+// about one row in twenty of 128256 columns, the row is done again with exact weights.
 //
 // Threshold.  Every lane's maximum in every chunk is kept in shared memory.  They bound the
 // threshold from below (the k-th largest of them is at most the k-th largest element; the same
 // for sums), and later passes read only the vectors of lanes and chunks that reach the bound:
-// few for peaked rows.  What they find is put in order in shared memory; more than the list
-// holds (flat rows) is first narrowed down by histograms of counts and masses over the
-// bits of the ordered values.
+// few for peaked rows.  Where what they find fits a list in shared memory, the list is put in
+// order and cut, put in column order and drawn from, and the row is not read again.  Otherwise
+// (flat rows) a histogram of counts over the values brackets the threshold, since within a bin all
+// weights are within a few percent of each other; the bracket's elements go to the list, what
+// lies above is summed, and one more pass sums what is kept by chunks.
+//
+// Rows of up to 256 vectors take a warp each and stay in registers; sums are f32 there, and a
+// row in which one of them lies too close to a border to tell is done by the warp as above.
 #pragma once
 
 #include <climits>
@@ -44,10 +49,13 @@
 namespace lse {
 namespace {
 
-constexpr int kBatch = 8;                // vectors of a lane in flight
-constexpr int kBins = 512;
-constexpr int kList = 256;
-constexpr float kFastError = 6e-7f;
+constexpr int kBatch = 4;    // vectors of a lane in flight
+constexpr int kChunk = 128;  // vectors of a chunk, at least
+// Histogram bins and list entries of a row's threads.
+template <int TX> __host__ __device__ constexpr int bins_log2() { return TX == 32 ? 7 : 10; }
+template <int TX> __host__ __device__ constexpr int list_size() { return TX == 32 ? 64 : 2048; }
+// The part of a sum that two fast sums may be off by when they are compared.
+__device__ __forceinline__ uint64_t fast_error(uint64_t total) { return (total >> 22) + (total >> 23) + 1; }  // 3.6e-7
 constexpr float kInf = __builtin_inff();
 
 // 2^(j / 64) in units of 2^-30, rounded to nearest.
@@ -60,6 +68,28 @@ __constant__ uint32_t kPowers[64] = {
     1655936265u, 1673968228u, 1692196547u, 1710623359u, 1729250827u, 1748081133u, 1767116489u, 1786359126u,
     1805811301u, 1825475297u, 1845353420u, 1865448001u, 1885761398u, 1906295993u, 1927054196u, 1948038440u,
     1969251188u, 1990694927u, 2012372174u, 2034285470u, 2056437387u, 2078830522u, 2101467502u, 2124350982u,
+};
+
+// 2^(j / 32) as the sum of two floats.
+__constant__ float kHigh[32] = {
+    0x1.0000000000000p+0f, 0x1.059b0e0000000p+0f, 0x1.0b55860000000p+0f, 0x1.11301e0000000p+0f,
+    0x1.172b840000000p+0f, 0x1.1d48740000000p+0f, 0x1.2387a60000000p+0f, 0x1.29e9e00000000p+0f,
+    0x1.306fe00000000p+0f, 0x1.371a740000000p+0f, 0x1.3dea640000000p+0f, 0x1.44e0860000000p+0f,
+    0x1.4bfdae0000000p+0f, 0x1.5342b60000000p+0f, 0x1.5ab07e0000000p+0f, 0x1.6247ec0000000p+0f,
+    0x1.6a09e60000000p+0f, 0x1.71f75e0000000p+0f, 0x1.7a11480000000p+0f, 0x1.82589a0000000p+0f,
+    0x1.8ace540000000p+0f, 0x1.93737c0000000p+0f, 0x1.9c49180000000p+0f, 0x1.a5503c0000000p+0f,
+    0x1.ae89fa0000000p+0f, 0x1.b7f7700000000p+0f, 0x1.c199be0000000p+0f, 0x1.cb720e0000000p+0f,
+    0x1.d5818e0000000p+0f, 0x1.dfc9740000000p+0f, 0x1.ea4afa0000000p+0f, 0x1.f507660000000p+0f,
+};
+__constant__ float kLow[32] = {
+    0x0.0p+0f, -0x1.9d4f520000000p-25f, 0x1.9f31220000000p-25f, -0x1.fdb4960000000p-25f,
+    -0x1.c157420000000p-27f, -0x1.d2e8ca0000000p-25f, 0x1.ceac480000000p-25f, -0x1.5c04240000000p-25f,
+    0x1.4636e20000000p-25f, -0x1.18aac60000000p-25f, 0x1.8246840000000p-25f, 0x1.8624b40000000p-30f,
+    -0x1.593abc0000000p-25f, -0x1.2c56100000000p-25f, -0x1.5bd5ec0000000p-27f, -0x1.f8b5500000000p-25f,
+    0x1.9fcef40000000p-26f, 0x1.1d8bee0000000p-25f, -0x1.829fd00000000p-25f, -0x1.accc7c0000000p-26f,
+    0x1.15506e0000000p-27f, -0x1.e647440000000p-25f, 0x1.51f8480000000p-27f, -0x1.b83b540000000p-25f,
+    -0x1.a94b140000000p-26f, -0x1.a094380000000p-25f, -0x1.3d56b20000000p-27f, -0x1.8837cc0000000p-27f,
+    -0x1.822dbc0000000p-27f, -0x1.908c940000000p-25f, 0x1.52486c0000000p-27f, -0x1.246eb00000000p-26f,
 };
 
 template <int TX> __device__ __forceinline__ void row_sync() {
@@ -84,13 +114,16 @@ __device__ __forceinline__ uint64_t part_of(uint64_t t, float f, bool* whole) {
     return q;
 }
 
-// What a row's kernel shares between its threads.
+// What a row's threads share.
 template <int TX> struct SampleShared {
-    static constexpr int W = TX / 32;
-    uint32_t powers[64];
-    uint32_t count[kBins], mass[kBins];
-    uint64_t list[kList];
-    uint64_t weights[kList];
+    static constexpr int W = TX / 32, kBins = 1 << bins_log2<TX>(), kList = list_size<TX>();
+    uint32_t bins[kBins];
+    uint64_t list[kList];      // keys
+    static constexpr int kPart = TX == 32 ? 64 : 1024;  // of the list, put in order
+    union {
+        uint64_t work[kBins + kPart];                     // sums of weights by bins, and a bin's keys
+        unsigned short entries[4 * (kBins + kPart)];      // lanes and chunks that reach a bound
+    };
     uint64_t warp64[W + 1];
     float warpf[W];
     uint64_t r64[4];
@@ -99,22 +132,27 @@ template <int TX> struct SampleShared {
 
 template <int DT, int TX> struct Sampler {
     static constexpr int W = TX / 32, EB = DType<DT>::bytes, E = 16 / EB;
+    static constexpr int kBins = SampleShared<TX>::kBins, kList = SampleShared<TX>::kList, kPart = SampleShared<TX>::kPart;
     SampleShared<TX>& sh;
+    const uint32_t* powers;  // kPowers in shared memory
     // the row
     const char* base;  // the 16-byte boundary at or before its first element
     int off, end;      // its first and last bytes (end: in the last vector, from its start)
     int slots;         // vectors that cover it
     int N;
-    int per_warp, chunk, chunks_per_warp, chunks;  // vectors of a warp's range, of a chunk; chunks
+    int chunk, chunks_per_warp, chunks;  // vectors of a chunk; chunks of a warp (one after the other), in all
     // per chunk
     float* maxima;     // [chunks, 32]
     uint64_t* sums;    // [chunks + 1]: sums, then sums before
+    uint64_t* added;   // [chunks], in the place of the first pass's sums
     // weights
     float m, ch, cl;   // maximum; log2 e / T in two floats
+    float far;         // the distance from which weights are 0
     int S;             // fractional bits of a weight
-    int lane, warp;
+    int lane, warp, tid;  // in the row's group of threads
 
-    __device__ __forceinline__ Sampler(SampleShared<TX>& s) : sh(s), lane(threadIdx.x & 31), warp(threadIdx.x >> 5) {}
+    __device__ __forceinline__ Sampler(SampleShared<TX>& s)
+        : sh(s), lane(threadIdx.x & 31), warp(TX == 32 ? 0 : threadIdx.x >> 5), tid(TX == 32 ? lane : threadIdx.x) {}
 
     // -----------------------------------------------------------------------
     // Elements
@@ -122,23 +160,22 @@ template <int DT, int TX> struct Sampler {
     __device__ __forceinline__ void load(int slot, uint32_t (&w)[4]) const {
         const uint4 v = ldg_stream16(base + static_cast<int64_t>(slot) * 16);
         w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    }
+    // Elements outside the row to -inf.  Apart from load(): a use of the words next to each load
+    // would keep the next load waiting for it.
+    __device__ __forceinline__ void mask(int slot, uint32_t (&w)[4]) const {
         if ((slot == 0 && off != 0) || slot == slots - 1)
             mask_words<DT>(w, 0, slot == 0 ? off : 0, slot == slots - 1 ? end : 16);
     }
+    // Whether any of the vectors [a, b) holds elements outside the row.
+    __device__ __forceinline__ bool has_edge(int a, int b) const { return (a == 0 && off != 0) || b >= slots; }
     __device__ __forceinline__ int column(int slot, int e) const { return slot * E + e - off / EB; }
-    __device__ __forceinline__ int chunk_begin(int c) const {
-        const int w = c / chunks_per_warp;
-        return w * per_warp + (c - w * chunks_per_warp) * chunk;
-    }
-    __device__ __forceinline__ int chunk_end(int c) const {
-        const int w = c / chunks_per_warp;
-        return min(min(chunk_begin(c) + chunk, (w + 1) * per_warp), slots);
-    }
+    __device__ __forceinline__ int chunk_begin(int c) const { return c * chunk; }
+    __device__ __forceinline__ int chunk_end(int c) const { return min(c * chunk + chunk, slots); }
 
-    // The weight of an element, a whole number of 2^-S.
-    __device__ __forceinline__ uint64_t weight(float x) const {
-        const float d = x - m;
-        if (!(d * ch >= -static_cast<float>(S + 1))) return 0;
+    // 2^((x - m) log2 e / T) for x <= m and distances d ch of less than 2^15 octaves, as
+    // p 2^(e - 30).
+    __device__ __forceinline__ void power(float x, float d, uint32_t* p, int* e) const {
         const float a = d + m, b = d - a, dl = (x - a) + (-m - b);  // x - m = d + dl
         const float kf = fmaf(d, ch * 64.0f, 12582912.0f);
         const int k = __float_as_int(kf) - 0x4b400000;
@@ -146,39 +183,116 @@ template <int DT, int TX> struct Sampler {
         r = fmaf(d, cl, r);
         r = fmaf(dl, ch, r);
         const float q = r * fmaf(r, fmaf(r, 0.0555041087f, 0.240226507f), 0.693147181f);
-        const uint32_t t = sh.powers[k & 63];
-        const uint32_t p = t + __float2int_rn(static_cast<float>(t) * q);
-        const int s = S - 30 + (k >> 6);
+        const uint32_t t = powers[k & 63];
+        *p = t + __float2int_rn(static_cast<float>(t) * q);
+        *e = k >> 6;
+    }
+    // The weight of an element, a whole number of 2^-S (0 from S + 2 octaves on).
+    __device__ __forceinline__ uint64_t weight(float x) const {
+        const float d = x - m;
+        uint32_t p;
+        int e;
+        power(d > far ? x : m + far, fmaxf(d, far), &p, &e);
+        const int s = S - 30 + e;
         return s >= 0 ? static_cast<uint64_t>(p) << s : (static_cast<uint64_t>(p) + (1ull << (-s - 1))) >> -s;
     }
-    // 2^((x - m) log2 e / T) for x <= m.
     __device__ __forceinline__ double factor(float x) const {
         const float d = x - m;
         if (!(d * ch >= -900.0f)) return 0.0;
-        const float a = d + m, b = d - a, dl = (x - a) + (-m - b);
-        const float kf = fmaf(d, ch * 64.0f, 12582912.0f);
-        const int k = __float_as_int(kf) - 0x4b400000;
-        float r = fmaf(d, ch, (kf - 12582912.0f) * -0.015625f);
-        r = fmaf(d, cl, r);
-        r = fmaf(dl, ch, r);
-        const float q = r * fmaf(r, fmaf(r, 0.0555041087f, 0.240226507f), 0.693147181f);
-        const uint32_t t = sh.powers[k & 63];
-        const uint32_t p = t + __float2int_rn(static_cast<float>(t) * q);
-        return static_cast<double>(p) * __hiloint2double((1023 - 30 + (k >> 6)) << 20, 0);
+        uint32_t p;
+        int e;
+        power(x, d, &p, &e);
+        return static_cast<double>(p) * __hiloint2double((1023 - 30 + e) << 20, 0);
     }
 
-    // f(x, column) for a lane's elements of a chunk, where the lane has one of at least `lo`.
-    template <class F> __device__ __forceinline__ void each(int c, uint32_t lo, F&& f) const {
-        if (order_bits(maxima[c * 32 + lane]) < lo) return;
-        const int stop = chunk_end(c);
-        for (int s = chunk_begin(c) + lane; s < stop; s += 32) {
-            uint32_t w[4];
-            load(s, w);
+    // f(words, vector, mask of its elements) for the elements of at least `low`, by the lanes'
+    // maxima: the lanes and chunks that reach it are listed and their vectors handed out to all
+    // threads, a warp's lanes in step.  false: they are more than the list holds (f has not been
+    // called).
+    template <class F> __device__ __forceinline__ bool sparse(float low, F&& f) {
+        constexpr uint32_t kEntries = 4 * (kBins + kPart);
+        row_sync<TX>();
+        if (tid == 0) sh.r32[2] = 0;
+        row_sync<TX>();
+        for (int i0 = 0; i0 < chunks * 32; i0 += 16 * TX) {
+            uint32_t mask = 0;
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float x = word_elem<DT>(w, e);
-                if (order_bits(x) >= lo) f(x, column(s, e));
+            for (int j = 0; j < 16; ++j) {
+                const int i = i0 + j * TX + tid;
+                if (i < chunks * 32 && !(maxima[i] < low)) mask |= 1u << j;
             }
+            uint32_t at = places(&sh.r32[2], __popc(mask));
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (mask >> j & 1) {
+                    if (at < kEntries) sh.entries[at] = static_cast<unsigned short>(i0 + j * TX + tid);
+                    ++at;
+                }
+        }
+        row_sync<TX>();
+        const uint32_t n = sh.r32[2];
+        if (n > kEntries) return false;
+        const uint32_t vectors = chunk / 32;  // a power of two
+        const int shift = __ffs(vectors) - 1;
+        for (uint32_t t0 = 0; t0 < n * vectors; t0 += TX) {  // (all lanes in step)
+            const uint32_t t = t0 + tid;
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) w[q] = neg_inf_word<DT>();
+            int s = -1;
+            if (t < n * vectors) {
+                const int i = sh.entries[t >> shift], c = i >> 5;
+                s = chunk_begin(c) + (i & 31) + 32 * static_cast<int>(t & (vectors - 1));
+                if (s < chunk_end(c)) load(s, w), mask(s, w);
+                else s = -1;
+            }
+            uint32_t mask = 0;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (s >= 0 && !(word_elem<DT>(w, e) < low) && static_cast<unsigned>(column(s, e)) < static_cast<unsigned>(N)) mask |= 1u << e;
+            f(w, s, mask);
+        }
+        row_sync<TX>();
+        return true;
+    }
+    // The first of `n` places of this lane behind a shared counter: one addition per warp (one
+    // per element made every thread wait 26 ns for each).
+    __device__ __forceinline__ uint32_t places(uint32_t* counter, uint32_t n) const {
+        uint32_t s = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t b = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += b;
+        }
+        uint32_t first = 0;
+        if (lane == 31 && s != 0) first = atomicAdd(counter, s);
+        return __shfl_sync(0xffffffffu, first, 31) + s - n;
+    }
+    // f(words, first vector) for every batch of the row's chunks, the words of lanes whose
+    // maximum is below `low` as -inf; done(c) after a chunk.
+    template <class F, class G> __device__ __forceinline__ void dense(float low, F&& f, G&& done) {
+        for (int i = 0; i < chunks_per_warp; ++i) {
+            const int c = warp * chunks_per_warp + i, stop = chunk_end(c);
+            const bool some = !(maxima[c * 32 + lane] < low);
+            if (__any_sync(0xffffffffu, some)) {
+                for (int s0 = chunk_begin(c) + lane; s0 - lane < stop; s0 += 32 * kBatch) {
+                    uint32_t w[kBatch][4];
+#pragma unroll
+                    for (int j = 0; j < kBatch; ++j) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) w[j][q] = neg_inf_word<DT>();
+                        if (some && s0 + 32 * j < stop) load(s0 + 32 * j, w[j]);
+                    }
+                    if (has_edge(s0 - lane, s0 - lane + 32 * kBatch)) {
+#pragma unroll
+                        for (int j = 0; j < kBatch; ++j)
+                            if (some && s0 + 32 * j < stop) mask(s0 + 32 * j, w[j]);
+                    }
+                    f(w, s0);
+                }
+            }
+            __syncwarp();
+            done(c);
         }
     }
     static __device__ __forceinline__ uint64_t key(float x, int col) {
@@ -257,48 +371,126 @@ template <int DT, int TX> struct Sampler {
         row_sync<TX>();
         return sums[chunks];
     }
-    // The sums of f(x, column) over the chunks, elements below `lo` counting 0.
-    template <class F> __device__ __forceinline__ uint64_t sum_chunks(uint32_t lo, F&& f) {
+    // The counts over the chunks of the elements that keep(x, column) names, all of them at
+    // least `low`.
+    template <class F> __device__ __noinline__ uint64_t count_chunks(float low, F keep) {
         row_sync<TX>();
-        for (int i = 0; i < chunks_per_warp; ++i) {
-            const int c = warp * chunks_per_warp + i;
-            uint64_t s = 0;
-            each(c, lo, [&](float x, int col) { s += f(x, col); });
-            __syncwarp();
+        uint64_t s = 0;
+        dense(low, [&](const uint32_t (&w)[kBatch][4], int s0) {
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+                for (int e = 0; e < E; ++e) s += keep(word_elem<DT>(w[j], e), column(s0 + 32 * j, e)) ? 1 : 0;
+        }, [&](int c) {
             s = warp_sum(s);
             if (lane == 0) sums[c] = s;
-        }
+            s = 0;
+        });
         return scan_chunks();
+    }
+    // The exact weights of a pair, added to sums of pairs (hi + lo): as power(), in f32 pairs, with
+    // the table's entries in the lanes of the warp (all of which take part): 2^z = (high + low)
+    // 2^r 2^e.  -inf adds nothing that counts (2^-60).
+    __device__ __forceinline__ void add_exact_pair(uint64_t& hi, uint64_t& lo, uint64_t x, float high, float low, float dmin) const {
+        const uint64_t m2 = f2_pack(m, m), ch2 = f2_pack(ch, ch), cl2 = f2_pack(cl, cl);
+        uint64_t d = f2_sub(x, m2);
+        const uint64_t a = f2_add(d, m2), b = f2_sub(d, a);
+        uint64_t dl = f2_add(f2_sub(x, a), f2_sub(f2_pack(-m, -m), b));  // x - m = d + dl
+        float d0, d1, l0, l1;
+        f2_unpack(d, d0, d1);
+        f2_unpack(dl, l0, l1);
+        dl = f2_pack(d0 > dmin ? l0 : 0.0f, d1 > dmin ? l1 : 0.0f);
+        d = f2_pack(fmaxf(d0, dmin), fmaxf(d1, dmin));
+        const float magic = 12582912.0f;
+        const uint64_t kf = f2_fma(d, f2_pack(ch * 32.0f, ch * 32.0f), f2_pack(magic, magic));
+        const uint64_t nf = f2_sub(kf, f2_pack(magic, magic));
+        uint64_t r = f2_fma(d, ch2, f2_mul(nf, f2_pack(-0.03125f, -0.03125f)));
+        r = f2_fma(d, cl2, r);
+        r = f2_fma(dl, ch2, r);
+        uint64_t q = f2_fma(r, f2_pack(0.00961812911f, 0.00961812911f), f2_pack(0.0555041087f, 0.0555041087f));
+        q = f2_fma(r, q, f2_pack(0.240226507f, 0.240226507f));
+        q = f2_fma(r, q, f2_pack(0.693147181f, 0.693147181f));
+        q = f2_mul(r, q);
+        float k0, k1;
+        f2_unpack(kf, k0, k1);
+        const int i0 = __float_as_int(k0) - 0x4b400000, i1 = __float_as_int(k1) - 0x4b400000;
+        const uint64_t t = f2_pack(__shfl_sync(0xffffffffu, high, i0 & 31), __shfl_sync(0xffffffffu, high, i1 & 31));
+        const uint64_t u = f2_pack(__shfl_sync(0xffffffffu, low, i0 & 31), __shfl_sync(0xffffffffu, low, i1 & 31));
+        const uint64_t e = f2_pack(__int_as_float((127 + (i0 >> 5)) << 23), __int_as_float((127 + (i1 >> 5)) << 23));
+        const uint64_t v = f2_mul(t, e);
+        const uint64_t n = f2_add(hi, v), aa = f2_sub(n, v), bb = f2_sub(n, aa);  // hi + v = n + what it loses
+        lo = f2_add(lo, f2_add(f2_sub(hi, aa), f2_sub(v, bb)));
+        lo = f2_add(lo, f2_mul(f2_fma(t, q, u), e));
+        hi = n;
+    }
+    // The exact sums over the chunks of the weights of the elements that keep(x, column) names,
+    // all of them at least `low`.
+    template <class F> __device__ __noinline__ uint64_t exact_chunks(float low, F keep) {
+        row_sync<TX>();
+        const float high = kHigh[lane], rest = kLow[lane], dmin = -60.0f / ch;
+        uint64_t hi = 0, lo = 0;
+        dense(low, [&](const uint32_t (&w)[kBatch][4], int s0) {
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e) {
+                    float x0, x1;
+                    f2_unpack(pair_of(w[j], e), x0, x1);
+                    x0 = keep(x0, column(s0 + 32 * j, 2 * e)) ? x0 : -kInf;
+                    x1 = keep(x1, column(s0 + 32 * j, 2 * e + 1)) ? x1 : -kInf;
+                    add_exact_pair(hi, lo, f2_pack(x0, x1), high, rest, dmin);
+                }
+        }, [&](int c) {
+            const uint64_t s = exact_sum(hi, lo);
+            if (lane == 0) sums[c] = s;
+            hi = lo = 0;
+        });
+        return scan_chunks();
+    }
+    // The warp's sum of pairs of sums, as a weight.
+    __device__ __forceinline__ uint64_t exact_sum(uint64_t hi, uint64_t lo) const {
+        float h0, h1, l0, l1;
+        f2_unpack(hi, h0, h1);
+        f2_unpack(lo, l0, l1);
+        const double v = (static_cast<double>(h0) + static_cast<double>(h1)) + (static_cast<double>(l0) + static_cast<double>(l1));
+        return warp_sum(__double2ull_rn(v * __hiloint2double((1023 + S) << 20, 0)));
     }
     // The first column at which the running sum of f passes `target`; sums are scanned.
     // Sets the sums before it and with it; false if there is none in the chunk that the
     // chunks' sums name (they may be approximate).
     template <class F>
-    __device__ __forceinline__ bool locate(uint64_t target, F&& f, int* col, float* value, uint64_t* before, uint64_t* with) {
-        if (threadIdx.x == 0) sh.r32[1] = 0;
+    __device__ __forceinline__ bool locate(uint64_t target, bool clamp, F&& f, int* col, float* value, uint64_t* before, uint64_t* with) {
+        if (tid == 0) sh.r32[1] = 0;
         row_sync<TX>();
-        for (int c = threadIdx.x; c < chunks; c += TX)
+        for (int c = tid; c < chunks; c += TX)
             if (sums[c] <= target && target < sums[c + 1]) sh.r32[0] = c, sh.r32[1] = 1;
         row_sync<TX>();
         const bool any = sh.r32[1] != 0;
         const int c = sh.r32[0];
         row_sync<TX>();
-        if (threadIdx.x == 0) sh.r32[1] = 0;
+        if (tid == 0) sh.r32[1] = 0;
         if (!any) {
             row_sync<TX>();
             return false;
         }
         const int b = chunk_begin(c), n = chunk_end(c) - b;
-        const int per = (n + TX - 1) / TX, s0 = b + threadIdx.x * per, s1 = min(s0 + per, b + n);
+        const int per = (n + TX - 1) / TX, s0 = b + tid * per, s1 = min(s0 + per, b + n);
         uint64_t own = 0;
         for (int s = s0; s < s1; ++s) {
             uint32_t w[4];
             load(s, w);
+            mask(s, w);
 #pragma unroll
             for (int e = 0; e < E; ++e) own += f(word_elem<DT>(w, e), column(s, e));
         }
         const uint64_t first = row_before(own);
-        const uint64_t rest = target - sums[c];
+        // (Chunks' sums are good to about 2^-32; what is left of the target beyond the chunk's
+        // own sum by that is its last element's.)
+        uint64_t rest = target - sums[c];
+        if (clamp) {
+            const uint64_t all = row_sum(own);
+            if (rest >= all && all > 0) rest = all - 1;
+        }
         row_sync<TX>();
         if (first <= rest && rest < first + own) {
             uint64_t run = first;
@@ -306,6 +498,7 @@ template <int DT, int TX> struct Sampler {
             for (int s = s0; s < s1 && !found; ++s) {
                 uint32_t w[4];
                 load(s, w);
+                mask(s, w);
                 for (int e = 0; e < E && !found; ++e) {
                     const float x = word_elem<DT>(w, e);
                     const uint64_t v = f(x, column(s, e));
@@ -332,359 +525,821 @@ template <int DT, int TX> struct Sampler {
     }
 
     // -----------------------------------------------------------------------
-    // Pass over the row: maxima, and sums of fast weights relative to a shift of the warp's
+    // Pass over the row: maxima, and sums of fast weights relative to a shift of the chunk's
+    // (chunks are the same whatever the number of threads, and so are a row's sums in any batch)
     // -----------------------------------------------------------------------
-    __device__ __forceinline__ float batch_sum(const uint32_t (&w)[4 * kBatch], float mu, float dmin) const {
-        uint64_t acc[4] = {0, 0, 0, 0};
+    // The fast weight of a pair, added to a sum of pairs.
+    __device__ __forceinline__ uint64_t add_pair(uint64_t acc, uint64_t x, float mu, float dmin) const {
         const uint64_t mu2 = f2_pack(mu, mu), ch2 = f2_pack(ch, ch), nch2 = f2_pack(-ch, -ch), ncl2 = f2_pack(-cl, -cl);
         const uint64_t nln2 = f2_pack(-kLn2, -kLn2), one2 = f2_pack(1.0f, 1.0f);
-#pragma unroll
-        for (int i = 0; i < 4 * kBatch; ++i) {
-            uint64_t x;
-            if constexpr (DT == kF32) {
-                if (i & 1) continue;
-                x = f2_pack(__uint_as_float(w[i]), __uint_as_float(w[i + 1]));
-            } else {
-                x = f2_pack(word_lo<DT>(w[i]), word_hi<DT>(w[i]));
-            }
-            uint64_t d = f2_sub(x, mu2);
-            uint64_t dl = 0;
-            float d0, d1;
-            if constexpr (DT == kF32) {  // what the difference of two f32 loses
-                const uint64_t a = f2_add(d, mu2), b = f2_sub(d, a);
-                dl = f2_add(f2_sub(x, a), f2_sub(f2_pack(-mu, -mu), b));
-                float l0, l1;
-                f2_unpack(d, d0, d1);
-                f2_unpack(dl, l0, l1);
-                dl = f2_pack(d0 > dmin ? l0 : 0.0f, d1 > dmin ? l1 : 0.0f);
-            } else {
-                f2_unpack(d, d0, d1);
-            }
-            // A weight of 2^-200 is 0; an infinite distance would give inf - inf below.  (A NaN stays.)
-            asm("max.NaN.f32 %0, %0, %1;" : "+f"(d0) : "f"(dmin));
-            asm("max.NaN.f32 %0, %0, %1;" : "+f"(d1) : "f"(dmin));
-            d = f2_pack(d0, d1);
-            const uint64_t t = f2_mul(d, ch2);
-            uint64_t e = f2_fma(d, nch2, t);  // minus what the product lost
-            e = f2_fma(d, ncl2, e);
-            if constexpr (DT == kF32) e = f2_fma(dl, nch2, e);
-            const int at = DT == kF32 ? (i >> 1) & 3 : i & 3;
-            acc[at] = f2_fma(f2_ex2(t), f2_fma(e, nln2, one2), acc[at]);
+        uint64_t d = f2_sub(x, mu2);
+        uint64_t dl = 0;
+        float d0, d1;
+        f2_unpack(d, d0, d1);
+        if constexpr (DT == kF32) {  // what the difference of two f32 loses
+            const uint64_t a = f2_add(d, mu2), b = f2_sub(d, a);
+            dl = f2_add(f2_sub(x, a), f2_sub(f2_pack(-mu, -mu), b));
+            float l0, l1;
+            f2_unpack(dl, l0, l1);
+            dl = f2_pack(d0 > dmin ? l0 : 0.0f, d1 > dmin ? l1 : 0.0f);
         }
+        // A weight of 2^-200 is 0; an infinite distance would give inf - inf below.  (A NaN stays.)
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(d0) : "f"(dmin));
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(d1) : "f"(dmin));
+        d = f2_pack(d0, d1);
+        const uint64_t t = f2_mul(d, ch2);
+        uint64_t e = f2_fma(d, nch2, t);  // minus what the product lost
+        e = f2_fma(d, ncl2, e);
+        if constexpr (DT == kF32) e = f2_fma(dl, nch2, e);
+        return f2_fma(f2_ex2(t), f2_fma(e, nln2, one2), acc);
+    }
+    __device__ __forceinline__ static uint64_t pair_of(const uint32_t (&w)[4], int i) {  // i < E / 2
+        if constexpr (DT == kF32) return f2_pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        else return f2_pack(word_lo<DT>(w[i]), word_hi<DT>(w[i]));
+    }
+    __device__ __forceinline__ float batch_sum(const uint32_t (&w)[kBatch][4], float mu, float dmin) const {
+        uint64_t acc[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) acc[(j * E / 2 + i) & 3] = add_pair(acc[(j * E / 2 + i) & 3], pair_of(w[j], i), mu, dmin);
         float a, b;
         f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), a, b);
         return a + b;
     }
+    // hi + lo + v without loss.
+    __device__ __forceinline__ static void add_exact(float& hi, float& lo, float v) {
+        const float n = hi + v, a = n - v, b = n - a;
+        lo += (hi - a) + (v - b);
+        hi = n;
+    }
 
     // Leaves (sum, shift) of every chunk in `fast`; returns the lane's maximum.
     __device__ __forceinline__ float first_pass(float2* fast, bool with_sums) {
-        float top = -kInf, mu = 0.0f, lim = -kInf;
+        float top = -kInf;
         const float dmin = -200.0f / ch;
-        for (int i = 0; i < chunks_per_warp; ++i) {
-            const int c = warp * chunks_per_warp + i;
-            const int stop = chunk_end(c);
-            float cm = -kInf, hi = 0.0f, lo = 0.0f;
-            for (int s0 = chunk_begin(c); s0 < stop; s0 += 32 * kBatch) {
-                uint32_t w[4 * kBatch];
+        const int batches = chunk / (32 * kBatch);  // of a chunk
+        const int first = chunk_begin(warp * chunks_per_warp);
+        const int stop = min(first + chunks_per_warp * chunk, slots);
+        float cm = -kInf, hi = 0.0f, lo = 0.0f, mu = 0.0f, lim = -kInf;
+        int c = warp * chunks_per_warp, left = batches;
+        const int all = chunks_per_warp * batches;
+        for (int i = 0; i < all; i += 2) {
+            uint32_t v[2][kBatch][4];  // two batches in flight
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int j = 0; j < kBatch; ++j) {
-                    const int s = s0 + lane + 32 * j;
-                    uint32_t v[4];
+                    const int s = first + (i + h) * (32 * kBatch) + lane + 32 * j;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) v[q] = neg_inf_word<DT>();
-                    if (s < stop) load(s, v);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) w[4 * j + q] = v[q];
+                    for (int q = 0; q < 4; ++q) v[h][j][q] = neg_inf_word<DT>();
+                    if (s < stop) load(s, v[h][j]);
                 }
-                const float bm = words_max<DT, 4 * kBatch>(w);
-                cm = fmaxf(cm, bm);
-                if (!with_sums) {
-                    // NaN: a product with 0 and a sum keep it
-                    float z = 0.0f;
+            const int at = first + i * (32 * kBatch);
+            if (has_edge(at, at + 64 * kBatch)) {
 #pragma unroll
-                    for (int q = 0; q < 4 * kBatch; ++q) {
-                        if constexpr (DT == kF32) z = __uint_as_float(w[q]) != __uint_as_float(w[q]) ? kInf - kInf : z;
-                        else z = (word_lo<DT>(w[q]) != word_lo<DT>(w[q]) || word_hi<DT>(w[q]) != word_hi<DT>(w[q])) ? kInf - kInf : z;
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < kBatch; ++j) {
+                        const int s = at + h * (32 * kBatch) + lane + 32 * j;
+                        if (s < stop) mask(s, v[h][j]);
                     }
-                    hi += z;
-                    continue;
-                }
-                if (__any_sync(0xffffffffu, bm > lim)) {  // the warp's shift goes up
-                    float wm = bm;
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, o));
-                    if (wm < kInf) {
-                        if (hi != 0.0f) {  // sums relative to the old one (rare: a step of 64 octaves)
-                            Sampler t = *this;
-                            t.m = wm;
-                            const double v = (static_cast<double>(hi) + static_cast<double>(lo)) * t.factor(mu);
-                            hi = static_cast<float>(v);
-                            lo = static_cast<float>(v - static_cast<double>(hi));
-                        }
-                        mu = wm;
-                        lim = mu + 64.0f / ch;
-                        if (!(lim > mu)) lim = mu;
-                    }
-                }
-                const float v = batch_sum(w, mu, dmin);
-                const float n = hi + v, a = n - v, b = n - a;  // hi + lo + v without loss
-                lo += (hi - a) + (v - b);
-                hi = n;
             }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (i + h >= all) continue;
+                const auto& w = v[h];
+                float bm = words_max<DT, 4>(w[0]);
+#pragma unroll
+                for (int j = 1; j < kBatch; ++j) bm = fmaxf(bm, words_max<DT, 4>(w[j]));
+                cm = fmaxf(cm, bm);
+                if (!with_sums) {  // maxima ignore NaN: leave one in the sum
+                    bool nan = false;
+#pragma unroll
+                    for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+                        for (int e = 0; e < E; ++e) nan |= word_elem<DT>(w[j], e) != word_elem<DT>(w[j], e);
+                    if (nan) hi = kInf - kInf;
+                } else {
+                    if (__any_sync(0xffffffffu, bm > lim)) {  // the shift goes up
+                        float wm = bm;
+#pragma unroll
+                        for (int o = 16; o > 0; o >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, o));
+                        if (wm < kInf) {
+                            if (hi != 0.0f) {  // sums relative to the old one (rare: a step of 64 octaves)
+                                Sampler t = *this;
+                                t.m = wm;
+                                const double sum = (static_cast<double>(hi) + static_cast<double>(lo)) * t.factor(mu);
+                                hi = static_cast<float>(sum);
+                                lo = static_cast<float>(sum - static_cast<double>(hi));
+                            }
+                            mu = wm;
+                            lim = mu + 64.0f / ch;
+                            if (!(lim > mu)) lim = mu;
+                        }
+                    }
+                    add_exact(hi, lo, batch_sum(w, mu, dmin));
+                }
+                if (--left == 0) {  // the chunk is complete
+                    float s = hi + lo;
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                    maxima[c * 32 + lane] = cm;
+                    if (lane == 0) fast[c] = make_float2(s, mu);
+                    top = fmaxf(top, cm);
+                    cm = -kInf, hi = lo = mu = 0.0f, lim = -kInf;
+                    left = batches;
+                    ++c;
+                }
+            }
+        }
+        return top;
+    }
+    // The sums over the chunks of the fast weights of the elements that keep(x, column) names,
+    // all of them at least `low`; the rest counts as -inf, so that no lane waits for another.
+    template <class F> __device__ __forceinline__ uint64_t fast_chunks(float low, F&& keep) {
+        row_sync<TX>();
+        const float dmin = -200.0f / ch;
+        float hi = 0.0f, lo = 0.0f;
+        dense(low, [&](const uint32_t (&w)[kBatch][4], int s0) {
+            uint64_t acc[2] = {0, 0};
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e) {
+                    float x0, x1;
+                    f2_unpack(pair_of(w[j], e), x0, x1);
+                    x0 = keep(x0, column(s0 + 32 * j, 2 * e)) ? x0 : -kInf;
+                    x1 = keep(x1, column(s0 + 32 * j, 2 * e + 1)) ? x1 : -kInf;
+                    acc[e & 1] = add_pair(acc[e & 1], f2_pack(x0, x1), m, dmin);
+                }
+            float a, b;
+            f2_unpack(f2_add(acc[0], acc[1]), a, b);
+            add_exact(hi, lo, a + b);
+        }, [&](int c) {
             float s = hi + lo;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            maxima[c * 32 + lane] = cm;
-            if (lane == 0) fast[c] = make_float2(s, mu);
-            top = fmaxf(top, cm);
-        }
-        return top;
+            if (lane == 0) sums[c] = __double2ull_rn(static_cast<double>(s) * __hiloint2double((1023 + S) << 20, 0));
+            hi = lo = 0.0f;
+        });
+        return scan_chunks();
     }
 
     // -----------------------------------------------------------------------
     // Threshold keys
     // -----------------------------------------------------------------------
-    // Histogram of the elements in [lo, hi] (ordered bits) that `source` gives: counts and
-    // masses in units of 2^hs weights.
     __device__ __forceinline__ void clear_bins() {
         row_sync<TX>();
-        for (int i = threadIdx.x; i < kBins; i += TX) sh.count[i] = sh.mass[i] = 0;
+        for (int i = tid; i < kBins; i += TX) sh.bins[i] = 0;
         row_sync<TX>();
     }
-    static __device__ __forceinline__ int bin_shift(uint32_t lo, uint32_t hi) {
-        const uint32_t span = hi - lo;
-        return span < kBins ? 0 : 32 - __clz(span) - 9;  // (span >> shift) < 512
-    }
-    // From the top: the first bin at which the sum of v (+ one for every element, `over`)
-    // reaches `need`, and the sum before it; kBins if none does.
-    __device__ __forceinline__ int find_bin(const uint32_t* v, bool over, uint64_t need, uint64_t* before) {
+    // Bins of the values from hi down to lo: equal parts of their distance where that is
+    // finite, else of the ordered bits.  A larger value never has a larger bin; what lies
+    // below lo is in the last one.  (Bits alone would put all values within a factor of two
+    // into two bins, whose counters every thread would wait for.)
+    struct Bins {
+        float hi, scale;
+        uint32_t ohi;
+        int shift;
+        bool linear;
+        __device__ __forceinline__ Bins(uint32_t lo, uint32_t top) {
+            ohi = top;
+            hi = order_value(top);
+            const float span = hi - order_value(lo);
+            scale = kBins * 0.9999f / span;
+            linear = span > 0.0f && scale > 0.0f && scale < 1e30f && span < 1e30f;
+            const uint32_t bits = top - lo;
+            shift = bits < kBins ? 0 : 32 - __clz(bits) - bins_log2<TX>();
+        }
+        // The value at which bin b begins (for `more` above 0: at which the one before ends), moved
+        // down by `more` bins where bins are rounded.
+        __device__ __forceinline__ float edge(int b, float more) const {
+            if (linear) return hi - (static_cast<float>(b) + more) / scale;
+            const int64_t o = static_cast<int64_t>(ohi) - (static_cast<int64_t>(b) << shift) + (more > 0.0f ? 1 : 0);
+            // (ordered bits below those of -inf and above those of the largest value are no numbers)
+            return o <= 0x007fffff ? -kInf : order_value(static_cast<uint32_t>(min(o, static_cast<int64_t>(0xff7fffffu))));
+        }
+        __device__ __forceinline__ int of(float x) const {
+            if (linear) return static_cast<int>(fminf(fmaxf(hi - x, 0.0f) * scale, static_cast<float>(kBins - 1)));
+            return min((ohi - order_bits(x)) >> shift, static_cast<uint32_t>(kBins - 1));
+        }
+    };
+    // From the top: the first bin at which the sum of the bins reaches `need`, and the sum
+    // before it; kBins if none does.
+    __device__ __forceinline__ int find_bin(uint64_t need, uint64_t* before) {
+        constexpr int P = kBins > TX ? kBins / TX : 1;
         row_sync<TX>();
-        if (warp == 0) {
-            constexpr int P = kBins / 32;
-            const int b0 = lane * P;
-            uint64_t own = 0;
-            for (int i = 0; i < P; ++i) own += v[b0 + i] + (over ? sh.count[b0 + i] : 0u);
-            uint64_t s = own;
+        if (tid == 0) sh.r32[0] = kBins;
+        uint64_t own = 0;
+        if (tid * P < kBins) {
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint64_t p = shfl_up64(s, o);
-                if (lane >= o) s += p;
-            }
-            uint64_t run = s - own;
-            if (lane == 0) sh.r32[0] = kBins, sh.r64[0] = 0;
-            __syncwarp();
-            if (run < need && need <= s) {
-                int at = b0;
-                for (int i = 0; i < P; ++i) {
-                    const uint64_t n = run + v[b0 + i] + (over ? sh.count[b0 + i] : 0u);
-                    if (n >= need) {
-                        at = b0 + i;
-                        break;
-                    }
-                    run = n;
+            for (int i = 0; i < P; ++i) own += sh.bins[tid * P + i];
+        }
+        uint64_t run = row_before(own);
+        row_sync<TX>();
+        if (run < need && need <= run + own) {
+            for (int i = 0; i < P; ++i) {
+                const uint64_t n = run + sh.bins[tid * P + i];
+                if (n >= need) {
+                    sh.r32[0] = tid * P + i;
+                    sh.r64[0] = run;
+                    break;
                 }
-                sh.r32[0] = at;
-                sh.r64[0] = run;
+                run = n;
             }
-            if (lane == 31 && need > s) sh.r64[0] = s;
         }
         row_sync<TX>();
         const int at = sh.r32[0];
-        if (before) *before = sh.r64[0];
+        *before = sh.r64[0];
         row_sync<TX>();
         return at;
     }
-
-    // The threshold key of the shortest prefix (of the elements with keys >= base) whose count
-    // or sum of weights reaches `need` (>= 1), given to within `err`; `base_key` where all of
-    // them do not.  `total`: the sum of all weights.  *sure is false where err left it open.
-    __device__ uint64_t select(bool by_mass, uint64_t need, uint64_t total, uint64_t err, uint64_t base_key, bool* sure) {
-        *sure = true;
-        const uint32_t top = order_bits(m);
-        uint32_t lo = static_cast<uint32_t>(base_key >> 32), hi = top;
-        if (by_mass) {  // lighter elements weigh nothing
-            const float x = m - (S + 2) / ch;
-            if (x > -kInf) lo = max(lo, order_bits(x));
-        }
-        lo = min(lo, hi);
-        const uint32_t floor = lo;
-        const int hs0 = max(0, 33 - __clzll(static_cast<long long>(total)));  // total in 31 bits
-        // A bound from the lanes' maxima: they are elements, so as many of them, or as much,
-        // as is needed is enough.
-        bool bounded = false;
-        {
-            uint32_t mlo = lo, mhi = hi;
-            uint64_t left = by_mass ? ((need + err) >> hs0) + 1 : need;
-            for (int round = 0; round < 4; ++round) {
-                const int shift = bin_shift(mlo, mhi);
-                clear_bins();
-                for (int i = threadIdx.x; i < chunks * 32; i += TX) {
-                    const float x = maxima[i];
-                    const uint32_t o = order_bits(x);
-                    if (o < mlo || o > mhi) continue;
-                    const int b = (mhi - o) >> shift;
-                    if (by_mass) atomicAdd(&sh.mass[b], static_cast<uint32_t>(min(weight(x) >> hs0, static_cast<uint64_t>(left))));
-                    else atomicAdd(&sh.count[b], 1u);
-                }
-                uint64_t before;
-                const int b = find_bin(by_mass ? sh.mass : sh.count, false, left, &before);
-                if (b == kBins) break;  // (round 0 only: later ones narrow a bin that reaches)
-                const uint32_t bin_hi = mhi - (static_cast<uint32_t>(b) << shift);
-                const uint32_t width = (1u << shift) - 1;
-                mhi = bin_hi;
-                mlo = bin_hi - mlo > width ? bin_hi - width : mlo;
-                lo = mlo;
-                bounded = true;
-                left -= before;
-                const uint32_t in_bin = sh.count[b];
-                row_sync<TX>();
-                if (shift == 0 || (!by_mass && in_bin <= 4)) break;
-            }
-        }
-        uint64_t above = 0;      // count or weights of the elements with keys >= base above hi
-        uint64_t left = need, range_most = total + err;
-        for (int round = 0; round < 64; ++round) {  // (every histogram narrows the range: a few rounds)
-            if (bounded || round > 0) {
-                // Elements in the range to the list; what lies above it is summed.
-                if (threadIdx.x == 0) sh.r32[3] = 0;
-                row_sync<TX>();
-                uint64_t own = 0;
-                for (int i = 0; i < chunks_per_warp; ++i)
-                    each(warp * chunks_per_warp + i, lo, [&](float x, int col) {
-                        const uint64_t k = key(x, col);
-                        if (k < base_key) return;
-                        if (static_cast<uint32_t>(k >> 32) > hi) {
-                            own += by_mass ? weight(x) : 1;
-                        } else {
-                            const uint32_t at = atomicAdd(&sh.r32[3], 1u);
-                            if (at < kList) sh.list[at] = k;
-                        }
-                    });
-                __syncwarp();
-                above = row_sum(own);
-                row_sync<TX>();
-                const uint32_t n = sh.r32[3];
-                if (above >= need) {  // (only where err is wrong)
-                    *sure = err == 0;
-                    return (static_cast<uint64_t>(hi) + 1) << 32;
-                }
-                left = need - above;
-                if (n <= (TX == 32 ? 64 : kList)) {
-                    // Ranks by counting, then the running sum in that order.
-                    for (uint32_t i = threadIdx.x; i < n; i += TX) {
-                        const uint64_t k = sh.list[i];
-                        uint64_t w = 0;
-                        for (uint32_t j = 0; j < n; ++j) {
-                            const uint64_t o = sh.list[j];
-                            if (o >= k) w += by_mass ? weight(order_value(static_cast<uint32_t>(o >> 32))) : 1;
-                        }
-                        sh.weights[i] = w;  // of the prefix that ends here
-                    }
-                    if (threadIdx.x == 0) sh.r64[2] = 0, sh.r32[0] = 1;
-                    row_sync<TX>();
-                    for (uint32_t i = threadIdx.x; i < n; i += TX) {
-                        const uint64_t k = sh.list[i], w = sh.weights[i];
-                        const uint64_t one = by_mass ? weight(order_value(static_cast<uint32_t>(k >> 32))) : 1;
-                        if (w >= left && w - one < left) {
-                            sh.r64[2] = k;
-                            const uint64_t over = above + w - need, under = need - (above + w - one);
-                            if (err && (over <= err || under <= err)) sh.r32[0] = 0;
-                        }
-                    }
-                    row_sync<TX>();
-                    const uint64_t k = sh.r64[2];
-                    const bool ok = sh.r32[0] != 0;
-                    row_sync<TX>();
-                    if (k == 0) {
-                        *sure = err == 0;
-                        return base_key;
-                    }
-                    *sure = ok;
-                    return k;
-                }
-                if (lo == hi) {  // equal values: a count of columns
-                    if (err) {
-                        *sure = false;
-                        return base_key;
-                    }
-                    const float x = order_value(lo);
-                    const uint64_t one = by_mass ? weight(x) : 1;
-                    uint64_t count = one ? (left + one - 1) / one : 1;
-                    const uint32_t o = lo;
-                    const auto same = [&](float v, int col) -> uint64_t { return order_bits(v) == o && key(v, col) >= base_key; };
-                    const uint64_t all = sum_chunks(o, same);
-                    if (count > all) count = all;
-                    int col = 0;
-                    float value;
-                    uint64_t b, w;
-                    locate(count - 1, same, &col, &value, &b, &w);
-                    return (static_cast<uint64_t>(o) << 32) | (0xffffffffu - static_cast<uint32_t>(col));
-                }
-                if (err && round >= 3) {
-                    *sure = false;
-                    return base_key;
-                }
-            }
-            // Narrow the range: to the bins in which the sum can reach what is left.
-            const int shift = bin_shift(lo, hi);
-            const int hs = by_mass ? max(0, 33 - __clzll(static_cast<long long>(range_most))) : 0;  // in 31 bits
+    // Elements below this weigh nothing.
+    __device__ __forceinline__ uint32_t weightless() const {
+        const float x = m - (S + 2) / ch;
+        return x > -kInf ? min(order_bits(x), order_bits(m)) : 0;
+    }
+    // Elements below this all together weigh less than `rest`: N times such a weight is less.
+    __device__ __forceinline__ uint32_t light(uint64_t rest) const {
+        if (rest == 0) return weightless();
+        const float z = __log2f(static_cast<float>(rest) / static_cast<float>(N)) - static_cast<float>(S) - 0.01f;
+        const float x = m + z / ch;  // (z < 0; rounded below by the hundredth and by a step of m)
+        const uint32_t o = order_bits(x - 4e-7f * fabsf(m));
+        return x > -kInf && z < 0.0f ? max(weightless(), min(o, order_bits(m))) : weightless();
+    }
+    // Raises *lo to a value that the threshold cannot lie below, from the lanes' maxima: they
+    // are elements, so as many of them, or as much of their weights, as is needed is enough.
+    // false: they do not reach (lo is left).
+    __device__ __forceinline__ bool bound(bool by_mass, uint64_t need, uint64_t total, uint32_t* lo) {
+        const int hs = max(0, 33 - __clzll(static_cast<long long>(total)));  // total in 31 bits
+        uint32_t mlo = max(*lo, weightless()), mhi = order_bits(m);
+        uint64_t left = by_mass ? (need >> hs) + 1 : need;
+        bool reached = false;
+        for (int round = 0; round < 4; ++round) {
+            const Bins bins(mlo, mhi);
+            const float low = order_value(mlo), top = order_value(mhi);
             clear_bins();
-            for (int i = 0; i < chunks_per_warp; ++i)
-                each(warp * chunks_per_warp + i, lo, [&](float x, int col) {
-                    const uint64_t k = key(x, col);
-                    const uint32_t o = static_cast<uint32_t>(k >> 32);
-                    if (k < base_key || o > hi) return;
-                    const int b = (hi - o) >> shift;
-                    atomicAdd(&sh.count[b], 1u);
-                    if (by_mass) atomicAdd(&sh.mass[b], static_cast<uint32_t>(weight(x) >> hs));
-                });
-            int b0, b1;
-            uint64_t before0 = 0, before1 = 0;
-            if (by_mass) {
-                const uint64_t low = left > err ? left - err : 1;
-                const uint64_t need_low = max(static_cast<uint64_t>(1), low >> hs), need_high = ((left + err) >> hs) + 1;
-                b0 = find_bin(sh.mass, true, need_low, &before0);
-                b1 = find_bin(sh.mass, false, need_high, &before1);
-                if (b0 == kBins) {
-                    *sure = err == 0;
-                    return base_key;
-                }
-                if (b1 == kBins) b1 = kBins - 1;
-            } else {
-                b0 = b1 = find_bin(sh.count, false, left, &before0);
-                if (b0 == kBins) return base_key;
+            for (int i = tid; i < chunks * 32; i += TX) {
+                const float x = maxima[i];
+                if (x < low || x > top) continue;  // (low may be no number: then nothing is below it)
+                if (by_mass) atomicAdd(&sh.bins[bins.of(x)], static_cast<uint32_t>(weight(x) >> hs));
+                else atomicAdd(&sh.bins[bins.of(x)], 1u);
             }
-            // An upper bound on the mass of the new range sets the next histogram's units.
-            if (by_mass) {
-                uint64_t mass = 0;
-                for (int b = b0; b <= b1; ++b) mass += static_cast<uint64_t>(sh.mass[b]) + sh.count[b];
-                range_most = mass << hs;
-                row_sync<TX>();
+            uint64_t before;
+            const int b = find_bin(left, &before);
+            if (b == kBins) {
+                // Counts may need elements that weigh nothing.
+                if (reached || by_mass || mlo <= *lo) break;
+                mlo = *lo;
+                continue;
             }
-            const uint32_t old_hi = hi;
-            hi = old_hi - (static_cast<uint32_t>(b0) << shift);
-            const uint64_t reach = (static_cast<uint64_t>(b1) + 1) << shift;
-            const uint32_t new_lo = reach > old_hi - lo ? lo : old_hi - static_cast<uint32_t>(reach) + 1;
-            if (new_lo == lo && hi == old_hi && err) {
-                *sure = false;
-                return base_key;
+            const bool enough = by_mass ? round >= 1 : sh.bins[b] * 4ull <= need + 32;
+            row_sync<TX>();
+            // The bin's ends, moved out by a hundredth of its width.
+            const uint32_t a = max(mlo, b == kBins - 1 ? 0u : order_bits(bins.edge(b + 1, 0.01f)));
+            const uint32_t z = min(mhi, order_bits(bins.edge(b, -0.01f)));
+            if (a == mlo && z == mhi) {
+                *lo = a;
+                return true;
             }
-            lo = max(new_lo, floor);
+            // Elements above z were counted; those between the bin's end and z are counted again.
+            mlo = a;
+            mhi = z;
+            reached = true;
+            *lo = mlo;
+            if (enough || mlo >= mhi) break;
+            // (what was counted above z: at most `before`)
+            uint64_t over = 0;
+            const float zv = order_value(z);
+            for (int i = tid; i < chunks * 32; i += TX)
+                if (maxima[i] > zv) over += by_mass ? weight(maxima[i]) >> hs : 1;
+            over = row_sum(over);
+            left = (by_mass ? (need >> hs) + 1 : need) - min(over, by_mass ? need >> hs : need - 1);
         }
+        return reached;
+    }
+    // All elements of at least `lo` to the list; returns how many there are, also where they
+    // are more than it holds.
+    __device__ __forceinline__ uint32_t gather(uint32_t lo) {
+        if (tid == 0) sh.r32[3] = 0;
+        const bool done = sparse(order_value(lo), [&](const uint32_t (&w)[4], int s, uint32_t mask) {
+            uint32_t at = places(&sh.r32[3], __popc(mask));
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (mask >> e & 1) {
+                    if (at < kList) sh.list[at] = key(word_elem<DT>(w, e), column(s, e));
+                    ++at;
+                }
+        });
+        const uint32_t n = sh.r32[3];
+        row_sync<TX>();
+        return done ? n : 0xffffffffu;
+    }
+    // The first n entries in descending order (bitonic; exchanges over less than 64 entries stay
+    // within a warp).
+    __device__ __forceinline__ void sort_list(uint64_t* v, uint32_t n) {
+        uint32_t size = 2;
+        while (size < n) size <<= 1;
+        for (uint32_t i = n + tid; i < size; i += TX) v[i] = 0;
+        row_sync<TX>();
+        for (uint32_t k = 2; k <= size; k <<= 1) {
+            for (uint32_t j = k >> 1; j > 0; j >>= 1) {
+                for (uint32_t t = tid; t < size / 2; t += TX) {
+                    const uint32_t a = 2 * t - (t & (j - 1)), b = a + j;
+                    const uint64_t x = v[a], y = v[b];
+                    if ((x < y) == ((a & k) == 0)) v[a] = y, v[b] = x;
+                }
+                if (j >= 64 || (j == 1 && k >= 64)) row_sync<TX>();
+                else __syncwarp();
+            }
+        }
+        row_sync<TX>();
+    }
+    // In keys v[0 .. n) in order: the first at which `before` and the running sum (of ones or
+    // weights) reach `need`, and the sums before and with it.  false: they do not.
+    __device__ __forceinline__ bool reach(const uint64_t* v, uint32_t n, bool by_mass, uint64_t before, uint64_t need, uint64_t* at,
+                                          uint64_t* under, uint64_t* with) {
+        const uint32_t per = (n + TX - 1) / TX, b = min(tid * per, n), e = min(b + per, n);
+        const auto one = [&](uint32_t i) -> uint64_t { return by_mass ? weight(order_value(static_cast<uint32_t>(v[i] >> 32))) : 1; };
+        uint64_t own = 0;
+        for (uint32_t i = b; i < e; ++i) own += one(i);
+        if (tid == 0) sh.r32[0] = 0;
+        uint64_t run = before + row_before(own);
+        row_sync<TX>();
+        if (run < need && need <= run + own) {
+            for (uint32_t i = b; i < e; ++i) {
+                const uint64_t w = one(i);
+                if (need <= run + w) {
+                    sh.r32[0] = 1;
+                    sh.r64[0] = v[i];
+                    sh.r64[1] = run;
+                    sh.r64[2] = run + w;
+                    break;
+                }
+                run += w;
+            }
+        }
+        row_sync<TX>();
+        const bool ok = sh.r32[0] != 0;
+        *at = sh.r64[0];
+        *under = sh.r64[1];
+        *with = sh.r64[2];
+        row_sync<TX>();
+        return ok;
+    }
+    // The same for the first n entries of the list with keys >= base, in whatever order they are:
+    // sums by bins of their values, and the keys of the bin that reaches put in order.
+    __device__ __noinline__ bool list_cut(bool by_mass, uint32_t n, uint64_t base_key, uint64_t before, uint64_t need, uint64_t* at,
+                                          uint64_t* under, uint64_t* with) {
+        uint64_t* const part = sh.work + kBins;
+        if (n > 32) {
+            uint32_t a = 0xffffffffu;
+            for (uint32_t i = tid; i < n; i += TX)
+                if (sh.list[i] >= base_key) a = min(a, static_cast<uint32_t>(sh.list[i] >> 32));
+            a = __reduce_min_sync(0xffffffffu, a);
+            if (tid == 0) sh.r32[1] = 0xffffffffu, sh.r32[2] = 0;
+            row_sync<TX>();
+            if (lane == 0) atomicMin(&sh.r32[1], a);
+            for (int i = tid; i < kBins; i += TX) sh.work[i] = 0;
+            row_sync<TX>();
+            const uint32_t top = order_bits(m);
+            const Bins bins(min(sh.r32[1], top), top);
+            for (uint32_t i = tid; i < n; i += TX) {
+                const uint64_t k = sh.list[i];
+                const float x = order_value(static_cast<uint32_t>(k >> 32));
+                if (k >= base_key) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.work[bins.of(x)]), by_mass ? weight(x) : 1ull);
+            }
+            row_sync<TX>();
+            constexpr int P = kBins > TX ? kBins / TX : 1;
+            uint64_t own = 0;
+            if (tid * P < kBins) {
+#pragma unroll
+                for (int i = 0; i < P; ++i) own += sh.work[tid * P + i];
+            }
+            if (tid == 0) sh.r32[0] = kBins;
+            uint64_t run = before + row_before(own);
+            row_sync<TX>();
+            if (run < need && need <= run + own) {
+                for (int i = 0; i < P; ++i) {
+                    const uint64_t w = sh.work[tid * P + i];
+                    if (need <= run + w) {
+                        sh.r32[0] = tid * P + i;
+                        sh.r64[0] = run;
+                        break;
+                    }
+                    run += w;
+                }
+            }
+            row_sync<TX>();
+            const int bin = sh.r32[0];
+            const uint64_t above = sh.r64[0];
+            if (bin == kBins) {
+                row_sync<TX>();
+                return false;
+            }
+            for (uint32_t i0 = 0; i0 < n; i0 += TX) {
+                const uint32_t i = i0 + tid;
+                const bool in = i < n && sh.list[i] >= base_key && bins.of(list_value(i)) == bin;
+                const uint32_t to = places(&sh.r32[2], in ? 1 : 0);
+                if (in && to < kPart) part[to] = sh.list[i];
+            }
+            row_sync<TX>();
+            const uint32_t c = sh.r32[2];
+            row_sync<TX>();
+            if (c <= kPart) {
+                sort_list(part, c);
+                return reach(part, c, by_mass, above, need, at, under, with);
+            }
+        }
+        sort_list(sh.list, n);  // few, or nearly all of one value
+        uint32_t kept = 0;      // (keys below base come last)
+        for (uint32_t i = tid; i < n; i += TX) kept += sh.list[i] >= base_key;
+        kept = static_cast<uint32_t>(row_sum(kept));
+        return reach(sh.list, kept, by_mass, before, need, at, under, with);
+    }
+    __device__ __forceinline__ float list_value(uint32_t i) const { return order_value(static_cast<uint32_t>(sh.list[i] >> 32)); }
+    // The sum of the weights of the list's entries with keys >= base.
+    __device__ __forceinline__ uint64_t list_sum(uint32_t n, uint64_t base_key) {
+        uint64_t s = 0;
+        for (uint32_t i = tid; i < n; i += TX) s += sh.list[i] >= base_key ? weight(list_value(i)) : 0;
+        return row_sum(s);
+    }
+    // Adds the same by chunks: to sums of chunks that have not been scanned.
+    __device__ __forceinline__ void list_chunks(uint32_t n, uint64_t base_key) {
+        for (uint32_t i = tid; i < n; i += TX) {
+            const uint64_t k = sh.list[i];
+            if (k < base_key) continue;
+            const int col = static_cast<int>(0xffffffffu - static_cast<uint32_t>(k));
+            atomicAdd(reinterpret_cast<unsigned long long*>(&sums[(col + off / EB) / E / chunk]), weight(list_value(i)));
+        }
+    }
+
+    // A range of values that a threshold lies in, and how many elements reach its lower end.
+    struct Range {
+        float lo, hi;
+        uint64_t through;
+    };
+    // The range that holds the threshold of top-p, from a sample: one vector in `every` of a lane.
+    // What lies below the threshold has a known sum, `rest`, made of many light elements, so the
+    // sample's light elements give its place to within a few percent of that, whatever a few heavy
+    // elements hold; split() shows whether the threshold is in the range.
+    __device__ __noinline__ bool guess(uint64_t rest, bool part_of_row, uint32_t lo_bits, Range* out) {
+        constexpr int P = kBins > TX ? kBins / TX : 1;
+        const uint32_t hi_bits = order_bits(m);
+        const Bins bins(lo_bits, hi_bits);
+        const float low = order_value(lo_bits);
+        clear_bins();
+        // every fourth vector, and of every `step`-th chunk: about 2^15 elements
+        int step = 1;
+        while (chunks / (2 * step) * 32 * E >= (1 << 15)) step *= 2;
+        float light = 0.0f;  // the sample's weights below lo
+        for (int c = warp * step; c < chunks; c += W * step) {
+            const int s = chunk_begin(c) + lane;
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) w[q] = neg_inf_word<DT>();
+            if (s < chunk_end(c)) load(s, w), mask(s, w);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float x = word_elem<DT>(w, e);
+                if (x >= low) atomicAdd(&sh.bins[bins.of(x)], 1u);
+                else if (!part_of_row) light += ex2((x - m) * ch);
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) light += __shfl_xor_sync(0xffffffffu, light, o);
+        if (lane == 0) sh.warpf[warp] = light;
+        row_sync<TX>();
+        light = 0.0f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) light += sh.warpf[i];
+        // From the bottom: estimates of the sums below each bin, and of their variance.
+        const float scale = static_cast<float>(chunk / 32 * step);
+        const float want = static_cast<float>(rest) * __int_as_float((127 - S) << 23);
+        float own = 0.0f, var = 0.0f;
+        float mid[P];
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int b = kBins - 1 - (tid * P + i);
+            mid[i] = 0.0f;
+            if (b >= 0) mid[i] = ex2((fminf(bins.edge(b, 0.5f), m) - m) * ch);
+            const float c = b >= 0 ? static_cast<float>(sh.bins[b]) : 0.0f;
+            own += c * mid[i];
+            var += c * mid[i] * mid[i];
+        }
+        float s = own, v = var;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float p = __shfl_up_sync(0xffffffffu, s, o), q = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) s += p, v += q;
+        }
+        row_sync<TX>();
+        if (lane == 31) sh.work[warp] = static_cast<uint64_t>(__float_as_uint(s)) << 32 | __float_as_uint(v);
+        if (tid == 0) sh.r32[0] = 0xffffffffu, sh.r32[1] = 0xffffffffu;
+        row_sync<TX>();
+        float run = s - own + light, spread = v - var;
+        for (int i = 0; i < warp; ++i) {
+            run += __uint_as_float(static_cast<uint32_t>(sh.work[i] >> 32));
+            spread += __uint_as_float(static_cast<uint32_t>(sh.work[i]));
+        }
+        // Four deviations (a sum of independent draws, one in `scale` elements) and a little for
+        // the bins' widths.  The first bin from below whose upper end may reach, and the first
+        // whose lower end certainly has passed.
+        uint32_t first = 0xffffffffu, last = 0xffffffffu;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int b = kBins - 1 - (tid * P + i);
+            if (b < 0) continue;
+            const float c = static_cast<float>(sh.bins[b]);
+            run += c * mid[i];
+            spread += c * mid[i] * mid[i];
+            const float est = run * scale, off = 4.0f * scale * sqrtf(spread + mid[i] * mid[i]) + 0.003f * est;
+            if (est + off >= want) first = min(first, static_cast<uint32_t>(tid * P + i));
+            if (est - off >= want) last = min(last, static_cast<uint32_t>(tid * P + i));
+        }
+        first = __reduce_min_sync(0xffffffffu, first);
+        last = __reduce_min_sync(0xffffffffu, last);
+        if (lane == 0) atomicMin(&sh.r32[0], first), atomicMin(&sh.r32[1], last);
+        row_sync<TX>();
+        first = sh.r32[0];
+        last = sh.r32[1];
+        row_sync<TX>();
+        if (first == 0xffffffffu) return false;
+        const int b1 = kBins - 1 - static_cast<int>(first);  // the lower bin of the range
+        const int b0 = last == 0xffffffffu ? 0 : kBins - 1 - static_cast<int>(last);
+        out->lo = b1 == kBins - 1 ? low : bins.edge(b1 + 1, 0.01f);
+        out->hi = b0 == 0 ? m : fminf(m, bins.edge(b0, -0.01f));
+        return out->lo <= out->hi;
+    }
+    // Counts the elements with keys >= base from lo to hi and brackets the threshold at which
+    // their count, or the sum of their weights, reaches `left` (to within err).  false: they do
+    // not reach.  `guide`: where the bins end.
+    __device__ __noinline__ bool bracket(bool by_mass, uint64_t left, uint64_t err, uint64_t base_key, uint32_t lo, uint32_t guide,
+                                         uint32_t hi, Range* out) {
+        constexpr int P = kBins > TX ? kBins / TX : 1;
+        const Bins bins(guide, hi);
+        const float low = order_value(lo), top = order_value(hi);
+        clear_bins();
+        dense(low, [&](const uint32_t (&w)[kBatch][4], int s0) {
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const float x = word_elem<DT>(w[j], e);
+                    const int b = bins.of(x);
+                    const bool in = !(x < low) && x <= top && (base_key == 0 || key(x, column(s0 + 32 * j, e)) >= base_key) &&
+                                    static_cast<unsigned>(column(s0 + 32 * j, e)) < static_cast<unsigned>(N);
+                    if (in) atomicAdd(&sh.bins[b], 1u);
+                }
+        }, [](int) {});
+        int b0, b1;
+        if (!by_mass) {
+            uint64_t before;
+            b0 = b1 = find_bin(left, &before);
+            out->through = b0 < kBins ? before + sh.bins[b0] : 0;
+            row_sync<TX>();
+        } else {
+            // A bin's weights lie between those of its ends (moved out by a hundredth of its
+            // width, far more than the roundings of a bin's number); the last bin has no lower end.
+            row_sync<TX>();
+            if (tid == 0) sh.r32[0] = kBins, sh.r32[1] = kBins;
+            uint64_t up = 0, down = 0, n = 0;
+            uint64_t ups[P], downs[P];
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const int b = tid * P + i;
+                ups[i] = downs[i] = 0;
+                if (b < kBins) {
+                    const uint64_t c = sh.bins[b];
+                    const float x1 = fminf(bins.edge(b, -0.01f), m), x0 = b == kBins - 1 ? -kInf : fminf(bins.edge(b + 1, 0.01f), m);
+                    ups[i] = c * weight(x1);
+                    downs[i] = c * weight(x0);
+                    n += c;
+                }
+                up += ups[i];
+                down += downs[i];
+            }
+            uint64_t u = row_before(up), d = row_before(down), before = row_before(n);
+            const uint64_t small = left > err ? left - err : 1, large = left + err;
+            row_sync<TX>();
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const int b = tid * P + i;
+                if (b >= kBins) continue;
+                before += sh.bins[b];
+                if (u < small && small <= u + ups[i]) sh.r32[0] = b;
+                if (d < large && large <= d + downs[i]) sh.r32[1] = b, sh.r64[0] = before;
+                if (b == kBins - 1) sh.r64[1] = before;
+                u += ups[i];
+                d += downs[i];
+            }
+            row_sync<TX>();
+            b0 = sh.r32[0];
+            out->through = sh.r32[1] < kBins ? sh.r64[0] : sh.r64[1];
+            b1 = min(sh.r32[1], static_cast<uint32_t>(kBins - 1));
+            row_sync<TX>();
+        }
+        if (b0 >= kBins) return false;
+        out->hi = fminf(top, b0 == 0 ? top : bins.edge(b0, -0.01f));
+        const float edge = b1 == kBins - 1 ? low : bins.edge(b1 + 1, 0.01f);
+        out->lo = edge > low ? edge : low;  // (low may be no number)
+        return true;
+    }
+    // Sums what lies above a range by chunks (left in `added`, not scanned), and puts the range's
+    // elements to the list; returns the sum of all chunks and, in *n, how many elements are in the range.
+    template <bool EXACT, bool MASS>
+    __device__ __noinline__ uint64_t split(Range at, uint32_t* n, uint32_t* least, uint32_t* most) {
+        row_sync<TX>();
+        if (tid == 0) sh.r32[3] = 0, sh.r32[0] = 0xffffffffu, sh.r32[1] = 0;
+        row_sync<TX>();
+        uint32_t a = 0xffffffffu, z = 0;
+        const float dmin = -200.0f / ch;
+        float hi = 0.0f, lo = 0.0f;
+        uint64_t exact = 0, ehi = 0, elo = 0;
+        const float high = kHigh[lane], rest = kLow[lane], far60 = -60.0f / ch;
+        const bool beyond = !(at.lo > -kInf);  // elements outside the row are -inf
+        dense(at.lo, [&](const uint32_t (&w)[kBatch][4], int s0) {
+            uint64_t acc[2] = {0, 0};
+            uint32_t mask = 0;  // of the range's elements, at most 32
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const float x = word_elem<DT>(w[j], e);
+                    if (!(x < at.lo) && x <= at.hi) mask |= 1u << (j * E + e);
+                    if constexpr (!MASS) exact += x > at.hi ? 1 : 0;
+                }
+            if constexpr (MASS && EXACT) {
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+                    for (int e = 0; e < E / 2; ++e) {
+                        float x0, x1;
+                        f2_unpack(pair_of(w[j], e), x0, x1);
+                        add_exact_pair(ehi, elo, f2_pack(x0 > at.hi ? x0 : -kInf, x1 > at.hi ? x1 : -kInf), high, rest, far60);
+                    }
+            }
+            if constexpr (!EXACT) {
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+                    for (int e = 0; e < E / 2; ++e) {
+                        float x0, x1;
+                        f2_unpack(pair_of(w[j], e), x0, x1);
+                        acc[e & 1] = add_pair(acc[e & 1], f2_pack(x0 > at.hi ? x0 : -kInf, x1 > at.hi ? x1 : -kInf), m, dmin);
+                    }
+                float p, q;
+                f2_unpack(f2_add(acc[0], acc[1]), p, q);
+                add_exact(hi, lo, p + q);
+            }
+            if (beyond) {
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        if (static_cast<unsigned>(column(s0 + 32 * j, e)) >= static_cast<unsigned>(N)) mask &= ~(1u << (j * E + e));
+            }
+            if (__any_sync(0xffffffffu, mask != 0)) {
+                uint32_t to = places(&sh.r32[3], __popc(mask));
+                while (mask) {  // (few: read again, so that no register is indexed)
+                    const int i = __ffs(mask) - 1;
+                    mask &= mask - 1;
+                    const int col = column(s0 + 32 * (i / E), i % E);
+                    const uint64_t k = key(load_elem<DT>(base + off, col), col);
+                    a = min(a, static_cast<uint32_t>(k >> 32));
+                    z = max(z, static_cast<uint32_t>(k >> 32));
+                    if (to < kList) sh.list[to] = k;
+                    ++to;
+                }
+                __syncwarp();
+            }
+        }, [&](int c) {
+            if constexpr (EXACT) {
+                const uint64_t v = MASS ? exact_sum(ehi, elo) : warp_sum(exact);
+                if (lane == 0) sums[c] = added[c] = v;
+                exact = ehi = elo = 0;
+            } else {
+                float s = hi + lo;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                if (lane == 0) sums[c] = added[c] = __double2ull_rn(static_cast<double>(s) * __hiloint2double((1023 + S) << 20, 0));
+                hi = lo = 0.0f;
+            }
+        });
+        const uint64_t sum = scan_chunks();
+        a = __reduce_min_sync(0xffffffffu, a);
+        z = __reduce_max_sync(0xffffffffu, z);
+        if (lane == 0) atomicMin(&sh.r32[0], a), atomicMax(&sh.r32[1], z);
+        row_sync<TX>();
+        *n = sh.r32[3];
+        *least = sh.r32[0];
+        *most = sh.r32[1];
+        row_sync<TX>();
+        return sum;
+    }
+    // The threshold key of the shortest prefix (of the elements with keys >= base) whose count
+    // or sum of weights reaches `need` (>= 1), given to within `err` (0: exact weights are used
+    // throughout); `base_key` where all of them do not.  It lies above lo (ordered bits).
+    // *sure is false where err left it open; *listed: the threshold is in the list of *listed
+    // entries, and what lies above those is summed in `added` (0: it is not).
+    __device__ __noinline__ uint64_t select(bool by_mass, uint64_t need, uint64_t total, uint64_t err, uint64_t base_key, uint32_t lo,
+                                            uint32_t guide, bool* sure, uint32_t* listed) {
+        uint64_t left = need;
+        uint32_t hi = order_bits(m);
+        const uint32_t lowest = lo, first_guide = guide;
+        bool tentative = false;
         *sure = err == 0;
+        *listed = 0;
+        for (int round = 0; round < 40; ++round) {  // (every histogram narrows the range: a few rounds)
+            Range at;
+            const bool sampled = round == 0 && by_mass && total > need && chunks >= 16 && guess(total - need, base_key != 0, lo, &at);
+            if (!sampled && !bracket(by_mass, left, err, base_key, lo, guide, hi, &at)) {
+                if (!tentative) return base_key;
+                tentative = false;  // the sample was wrong
+                lo = lowest, guide = first_guide, hi = order_bits(m), left = need;
+                continue;
+            }
+            uint32_t n, least, most;
+            const uint64_t above = !by_mass ? split<true, false>(at, &n, &least, &most)
+                                   : err ? split<false, true>(at, &n, &least, &most) : split<true, true>(at, &n, &least, &most);
+            uint64_t k, under, with;
+            if (above < need && n <= kList && list_cut(by_mass, n, base_key, above, need, &k, &under, &with)) {
+                *sure = err == 0 || (with - need > err && need - under > err);
+                *listed = by_mass ? n : 0;
+                return k;
+            }
+            if (sampled) {
+                if (above >= need || n <= kList) continue;  // not in the range: histograms find it
+                tentative = true;
+                left = need - above;
+                lo = guide = least;
+                hi = most;
+                continue;
+            }
+            tentative = false;
+            if (n <= kList || above >= need) return base_key;  // (only where err is wrong, or all of them do not reach)
+            left = need - above;
+            if (err && (least == most || (least == lo && most == hi))) return base_key;  // not sure
+            if (least == most) {  // equal values: a count of columns
+                const uint64_t one = by_mass ? weight(order_value(least)) : 1;
+                uint64_t count = one ? (left + one - 1) / one : 1;
+                const auto same = [=](float v, int col) -> uint64_t {
+                    return order_bits(v) == least && static_cast<unsigned>(col) < static_cast<unsigned>(N) && key(v, col) >= base_key;
+                };
+                const uint64_t all = count_chunks(order_value(least), same);
+                if (all == 0) return base_key;
+                if (count > all) count = all;
+                int col = 0;
+                float value;
+                uint64_t b, w;
+                locate(count - 1, false, same, &col, &value, &b, &w);
+                return (static_cast<uint64_t>(least) << 32) | (0xffffffffu - static_cast<uint32_t>(col));
+            }
+            lo = guide = least;
+            hi = most;
+        }
         return base_key;
     }
 };
 
-template <int DT, int TX> __global__ void __launch_bounds__(TX) sample_kernel(SampleArgs a) {
+// A row's settings.
+struct RowSettings {
+    float temperature, top_p, min_p, u;
+    int64_t top_k;
+    float ch, cl;  // log2 e / T in two floats
+    bool greedy, use_k, use_p, use_min, valid;
+    __device__ __forceinline__ RowSettings(const SampleArgs& a, int64_t row) {
+        temperature = a.temperature ? a.temperature[row] : a.temperature_all;
+        top_k = a.top_k ? a.top_k[row] : a.top_k_all;
+        top_p = a.top_p ? a.top_p[row] : a.top_p_all;
+        min_p = a.min_p ? a.min_p[row] : a.min_p_all;
+        u = a.u[row];
+        greedy = temperature < kSampleGreedy;
+        use_k = top_k > 0 && top_k < a.N && !greedy;
+        use_p = top_p < 1.0f && !greedy;
+        use_min = min_p > 0.0f && !greedy;
+        valid = temperature >= 0.0f && temperature <= kSampleHottest && top_p == top_p && min_p == min_p;
+        // the quotient of the first 24 bits, and what the remainder and the next bits add
+        const float t = greedy ? 1.0f : temperature;
+        ch = __fdiv_rn(kLog2e, t);
+        cl = __fdiv_rn(fmaf(-ch, t, kLog2e) + 1.92596299e-8f, t);
+    }
+};
+
+__device__ __forceinline__ void put_token(const SampleArgs& a, int64_t row, int64_t token, float logprob) {
+    a.token[row] = token;
+    if (a.logprob) a.logprob[row] = logprob;
+}
+
+// One row by the TX threads of its group.  `dynamic`: chunks + 1 sums, chunks pairs, and the
+// lanes' maxima.
+template <int DT, int TX>
+__device__ void sample_row(SampleShared<TX>& sh, const uint32_t* powers, unsigned char* dynamic, const SampleArgs& a, int64_t row) {
     using R = Sampler<DT, TX>;
-    __shared__ SampleShared<TX> sh;
-    extern __shared__ __align__(16) unsigned char dynamic[];
-    pdl_trigger();
-    pdl_wait();
-    for (int i = threadIdx.x; i < 64; i += TX) sh.powers[i] = kPowers[i];
-    const int64_t row = blockIdx.x;
+    const RowSettings g(a, row);
     R r(sh);
+    r.powers = powers;
     r.N = static_cast<int>(a.N);
     const char* x0 = static_cast<const char*>(a.x) + row * a.row_stride * R::EB;
     r.off = static_cast<int>(reinterpret_cast<uintptr_t>(x0) & 15);
@@ -695,33 +1350,23 @@ template <int DT, int TX> __global__ void __launch_bounds__(TX) sample_kernel(Sa
     r.chunk = a.chunk;
     r.chunks_per_warp = a.chunks_per_warp;
     r.chunks = R::W * a.chunks_per_warp;
-    r.per_warp = a.per_warp;
     r.sums = reinterpret_cast<uint64_t*>(dynamic);
     float2* fast = reinterpret_cast<float2*>(r.sums + r.chunks + 1);
+    r.added = reinterpret_cast<uint64_t*>(fast);
     r.maxima = reinterpret_cast<float*>(fast + r.chunks);
-
-    const float temperature = a.temperature ? a.temperature[row] : a.temperature_all;
-    const int64_t top_k = a.top_k ? a.top_k[row] : a.top_k_all;
-    const float top_p = a.top_p ? a.top_p[row] : a.top_p_all;
-    const float min_p = a.min_p ? a.min_p[row] : a.min_p_all;
-    const float u = a.u[row];
-    const bool greedy = temperature < kSampleGreedy;
-    const bool use_k = top_k > 0 && top_k < a.N && !greedy, use_p = top_p < 1.0f && !greedy, use_min = min_p > 0.0f && !greedy;
-    {   // log2 e / T: the quotient of its first 24 bits, and what the remainder and the next bits add
-        const float t = greedy ? 1.0f : temperature;
-        r.ch = __fdiv_rn(kLog2e, t);
-        r.cl = __fdiv_rn(fmaf(-r.ch, t, kLog2e) + 1.92596299e-8f, t);
-    }
+    r.ch = g.ch;
+    r.cl = g.cl;
     r.S = a.bits;
+    r.far = -static_cast<float>(a.bits + 3) / g.ch;
     row_sync<TX>();
     // A greedy row needs no sums, nor does one whose top_k cuts the rest off before any sum.
-    const bool with_sums = !(greedy || use_k);
+    const bool with_sums = !(g.greedy || g.use_k);
     r.m = r.row_max(r.first_pass(fast, with_sums));
     row_sync<TX>();
     // Chunks' sums relative to the maximum, in whole numbers.
-    bool bad = !(temperature >= 0.0f && temperature <= kSampleHottest) || top_p != top_p || min_p != min_p || !(fabsf(r.m) < kInf);
+    const bool bad = !g.valid || !(fabsf(r.m) < kInf);
     int nan = 0;
-    for (int c = threadIdx.x; c < r.chunks; c += TX) {
+    for (int c = r.tid; c < r.chunks; c += TX) {
         const float2 f = fast[c];
         nan |= f.x != f.x;
         if (with_sums) {
@@ -732,117 +1377,559 @@ template <int DT, int TX> __global__ void __launch_bounds__(TX) sample_kernel(Sa
     if constexpr (TX == 32) nan = __any_sync(0xffffffffu, nan);
     else nan = __syncthreads_or(nan);
     if (bad || nan) {
-        if (threadIdx.x == 0) {
-            a.token[row] = -1;
-            if (a.logprob) a.logprob[row] = __int_as_float(0x7fc00000);
-        }
+        if (r.tid == 0) put_token(a, row, -1, __int_as_float(0x7fc00000));
         return;
     }
     const uint32_t top = order_bits(r.m);
-    if (greedy) {
-        if (threadIdx.x == 0) sh.r32[0] = 0xffffffffu;
+    if (g.greedy) {
+        if (r.tid == 0) sh.r32[0] = 0xffffffffu;
         row_sync<TX>();
-        for (int i = 0; i < r.chunks_per_warp; ++i)
-            r.each(r.warp * r.chunks_per_warp + i, top, [&](float, int col) { atomicMin(&sh.r32[0], static_cast<uint32_t>(col)); });
+        uint32_t best = 0xffffffffu;
+        const auto lower = [&](const uint32_t (&w)[4], int s, uint32_t) {
+            for (int e = R::E - 1; e >= 0; --e)
+                if (s >= 0 && word_elem<DT>(w, e) == r.m) best = min(best, static_cast<uint32_t>(r.column(s, e)));
+        };
+        if (!r.sparse(r.m, lower))  // the maximum nearly everywhere
+            r.dense(r.m, [&](const uint32_t (&w)[kBatch][4], int s0) {
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) lower(w[j], s0 + 32 * j, 0);
+            }, [](int) {});
+        best = __reduce_min_sync(0xffffffffu, best);
+        if (r.lane == 0) atomicMin(&sh.r32[0], best);
         row_sync<TX>();
-        if (threadIdx.x == 0) {
-            a.token[row] = sh.r32[0];
-            if (a.logprob) a.logprob[row] = 0.0f;
-        }
+        if (r.tid == 0) put_token(a, row, sh.r32[0], 0.0f);
         return;
     }
+    // The maximum is kept and weighs 1: log(1 + rest) keeps the digits of a small rest.
+    const auto finish = [&](int64_t token, float x, uint64_t total) {
+        const uint64_t one = 1ull << r.S, rest = total > one ? total - one : 0;
+        put_token(a, row, token, (x - r.m) / g.temperature - log1pf(static_cast<float>(rest) * __int_as_float((127 - r.S) << 23)));
+    };
+    const auto drawn = [&](uint64_t total) -> uint64_t {
+        bool whole;
+        return g.u >= 1.0f ? total - 1 : part_of(total, g.u, &whole);
+    };
+    const auto mass_needed = [&](uint64_t total) -> uint64_t {
+        bool whole;
+        const uint64_t n = part_of(total, g.top_p, &whole);
+        return !whole || n == 0 ? n + 1 : n;
+    };
     const auto all_weights = [&](float x, int) -> uint64_t { return r.weight(x); };
     uint64_t total = 0, err = 0;
-    bool have_sums = false;  // exact ones of what is kept
     if (with_sums) {
         total = r.scan_chunks();
-        err = (total >> 21) + (total >> 23) + 1;  // kFastError of it
+        err = fast_error(total);
+    }
+    uint32_t floor_bits = 0;  // of min_p
+    if (g.use_min) {
+        // x - m >= T log(min_p) in 64 bits, as a comparison of x in 32.
+        if (r.tid == 0) {
+            const double v = static_cast<double>(r.m) + static_cast<double>(g.temperature) * log(static_cast<double>(fminf(g.min_p, 1.0f)));
+            sh.r32[0] = min(order_bits(__double2float_ru(v)), top);
+        }
+        row_sync<TX>();
+        floor_bits = sh.r32[0];
+        row_sync<TX>();
     }
     uint64_t threshold = 0;
-    if (use_k) {
-        bool sure;
-        threshold = r.select(false, static_cast<uint64_t>(top_k), 0, 0, 0, &sure);
-    }
-    if (use_p) {
-        if (use_k) {
-            const uint64_t t = threshold;
-            total = r.sum_chunks(static_cast<uint32_t>(t >> 32), [&](float x, int col) -> uint64_t { return R::key(x, col) >= t ? r.weight(x) : 0; });
-            err = 0;
+    bool exact = false;   // sums are
+    uint32_t listed = 0;  // entries of the list, if what is kept is those and what `added` sums
+    if (g.use_k || g.use_p || g.use_min) {
+        // Everything that can be kept in a list, if it fits.  lo: a bound that all of it reaches.
+        const uint64_t need = g.use_k ? static_cast<uint64_t>(g.top_k) : g.use_p ? mass_needed(total) : 0;
+        const bool by_mass = !g.use_k;
+        uint32_t lo = 0, guide = 0, n = 0;
+        bool fits;
+        if (need) {
+            if (by_mass) lo = r.light(total > need + 2 * err ? total - need - 2 * err : 0);
+            guide = lo;
+            fits = r.bound(by_mass, need + (by_mass ? err : 0), total, &lo);
+            if (fits) guide = lo;
+            else if (!by_mass) r.bound(false, r.chunks * 24, 0, &guide);  // where three quarters of the maxima lie above
+        } else {
+            fits = true;
         }
-        for (;;) {
-            bool whole;
-            uint64_t need = part_of(total, top_p, &whole);
-            if (!whole || need == 0) ++need;
+        if (g.use_min && by_mass && floor_bits >= lo) lo = guide = floor_bits, fits = true;
+        if (a.N <= R::kList) fits = true;
+        if (fits) {
+            n = r.gather(lo);
+            fits = n <= R::kList;
+        }
+        if (!fits && need && !by_mass && need <= R::kList) {
+            typename R::Range at;
+            if (r.bracket(false, need, 0, 0, lo, guide, top, &at) && at.through <= R::kList) {
+                n = r.gather(order_bits(at.lo));
+                fits = n <= R::kList;
+            }
+        }
+        if (fits) {
+            uint64_t cut = 0, under, with;
+            if (g.use_k) r.list_cut(false, n, 0, 0, static_cast<uint64_t>(g.top_k), &cut, &under, &with);
+            if (g.use_p) {
+                const uint64_t base = cut;
+                for (;;) {
+                    const uint64_t mass = mass_needed(g.use_k ? r.list_sum(n, base) : total), e = g.use_k ? 0 : err;
+                    uint64_t k;
+                    const bool found = r.list_cut(true, n, base, 0, mass, &k, &under, &with);
+                    if (found) cut = k;
+                    // (Not reached: the cut lies below what min_p keeps.)
+                    if (e == 0 || (found ? with - mass > e && mass - under > e : g.use_min)) break;
+                    total = r.exact_chunks(-kInf, [](float, int) -> bool { return true; });  // too close to tell
+                    err = 0;
+                }
+            }
+            threshold = max(cut, static_cast<uint64_t>(floor_bits) << 32);
+            row_sync<TX>();
+            for (int c = r.tid; c < r.chunks; c += TX) r.sums[c] = 0;
+            row_sync<TX>();
+            r.list_chunks(n, threshold);
+            total = r.scan_chunks();
+            const auto kept = [&](float v, int c) -> uint64_t { return R::key(v, c) >= threshold ? r.weight(v) : 0; };
+            int col;
+            float x;
+            uint64_t before;
+            r.locate(drawn(total), false, kept, &col, &x, &before, &with);
+            if (r.tid == 0) finish(col, x, total);
+            return;
+        }
+        if (g.use_k) {
             bool sure;
-            const uint64_t t = r.select(true, need, total, err, threshold, &sure);
-            if (sure) {
-                threshold = t > threshold ? t : threshold;
-                break;
+            threshold = r.select(false, static_cast<uint64_t>(g.top_k), 0, 0, 0, lo, guide, &sure, &listed);
+        }
+        if (g.use_p) {
+            const uint64_t base = threshold;
+            if (g.use_k) {
+                total = r.exact_chunks(order_value(static_cast<uint32_t>(base >> 32)), [&](float x, int col) -> bool { return R::key(x, col) >= base; });
+                err = 0;
             }
-            total = r.sum_chunks(0, all_weights);
-            err = 0;
-        }
-    }
-    if (use_min) {
-        // x - m >= T log(min_p) in 64 bits, as a comparison of x in 32.
-        if (threadIdx.x == 0) {
-            const double v = static_cast<double>(r.m) + static_cast<double>(temperature) * log(static_cast<double>(fminf(min_p, 1.0f)));
-            sh.r32[0] = order_bits(__double2float_ru(v));
-        }
-        row_sync<TX>();
-        const uint64_t t = static_cast<uint64_t>(sh.r32[0]) << 32;
-        row_sync<TX>();
-        threshold = t > threshold ? t : threshold;
-    }
-    const auto kept = [&](float x, int col) -> uint64_t { return R::key(x, col) >= threshold ? r.weight(x) : 0; };
-    const bool cut = threshold != 0;
-    for (;;) {
-        if (cut || have_sums) {
-            total = r.sum_chunks(static_cast<uint32_t>(threshold >> 32), kept);
-            err = 0;
-        }
-        bool whole;
-        uint64_t target = u >= 1.0f ? total - 1 : part_of(total, u, &whole);
-        int col = 0;
-        float x = 0.0f;
-        uint64_t before = 0, with = 0;
-        const bool found = r.locate(target, kept, &col, &x, &before, &with);
-        if (err && (!found || target - before < err || with - target <= err)) {
-            have_sums = true;  // too close to tell
-            continue;
-        }
-        if (threadIdx.x == 0) {
-            a.token[row] = found ? col : -1;
-            if (a.logprob) {
-                // The maximum is kept and weighs 1: log(1 + rest) keeps the digits of a small rest.
-                const uint64_t rest = total - min(total, 1ull << r.S);
-                a.logprob[row] = (x - r.m) / temperature - log1pf(static_cast<float>(rest) * __int_as_float((127 - r.S) << 23));
+            for (;;) {
+                bool sure;
+                const uint64_t mass = mass_needed(total);
+                const uint32_t from = max(static_cast<uint32_t>(base >> 32), r.light(total > mass + 2 * err ? total - mass - 2 * err : 0));
+                const uint64_t t = r.select(true, mass, total, err, base, from, from, &sure, &listed);
+                if (sure || err == 0) {
+                    threshold = max(threshold, t);
+                    exact = err == 0;
+                    break;
+                }
+                total = r.exact_chunks(-kInf, [](float, int) -> bool { return true; });  // too close to tell
+                err = 0;
             }
         }
-        return;
+        const uint64_t t = static_cast<uint64_t>(floor_bits) << 32;
+        if (t > threshold) threshold = t, listed = 0;
     }
+    int col = 0;
+    float x = 0.0f;
+    uint64_t before = 0, with = 0;
+    if (threshold == 0) {  // nothing is cut off
+        if (!with_sums) total = r.exact_chunks(-kInf, [](float, int) -> bool { return true; });
+        for (;;) {
+            const uint64_t target = drawn(total);
+            const bool found = r.locate(target, err == 0, all_weights, &col, &x, &before, &with);
+            if (err == 0 || (found && target - before > err && with - target > err)) break;
+            total = r.exact_chunks(-kInf, [](float, int) -> bool { return true; });  // too close to tell
+            err = 0;
+        }
+    } else {
+        const uint32_t bits = static_cast<uint32_t>(threshold >> 32);
+        const float low = order_value(bits);
+        const uint32_t place = static_cast<uint32_t>(threshold);
+        const int last = place == 0 ? INT_MAX : static_cast<int>(0xffffffffu - place);  // column, at the value `low`
+        const auto kept = [&](float v, int c) -> uint64_t { return R::key(v, c) >= threshold ? r.weight(v) : 0; };
+        if (listed) {
+            row_sync<TX>();
+            for (int c = r.tid; c < r.chunks; c += TX) r.sums[c] = r.added[c];
+            row_sync<TX>();
+            r.list_chunks(listed, threshold);
+            total = r.scan_chunks();
+            err = exact ? 0 : fast_error(total);
+        } else {
+            total = r.fast_chunks(low, [&](float v, int c) -> bool { return v > low || (v == low && c <= last); });
+            err = fast_error(total);
+        }
+        const uint64_t target = drawn(total);
+        const bool found = r.locate(target, err == 0, kept, &col, &x, &before, &with);
+        if (err && (!found || target - before <= err || with - target <= err)) {  // too close to tell
+            total = r.exact_chunks(low, [&](float v, int c) -> bool { return v > low || (v == low && c <= last); });
+            r.locate(drawn(total), true, kept, &col, &x, &before, &with);
+        }
+    }
+    if (r.tid == 0) finish(col, x, total);
+}
+
+template <int TX> __host__ __device__ constexpr int sample_ctas() { return TX == 128 ? 8 : TX == 256 ? 4 : 1; }
+template <int DT, int TX> __global__ void __launch_bounds__(TX, sample_ctas<TX>()) sample_kernel(SampleArgs a) {
+    __shared__ SampleShared<TX> sh;
+    __shared__ uint32_t powers[64];
+    extern __shared__ __align__(16) unsigned char dynamic[];
+    pdl_trigger();
+    pdl_wait();
+    for (int i = threadIdx.x; i < 64; i += TX) powers[i] = kPowers[i];
+    sample_row<DT, TX>(sh, powers, dynamic, a, blockIdx.x);
+}
+
+// Vectors of a chunk, by the row's length alone: whole batches, and as many chunks as 32 KB
+// of maxima hold.
+void plan_chunks(SampleArgs* a, int EB, int W) {
+    const int64_t slots = (a->N * EB + 15) / 16 + 1;  // one more for rows off a boundary
+    int64_t chunk = kChunk;
+    while ((slots + chunk - 1) / chunk > 256) chunk *= 2;
+    a->chunk = static_cast<int>(chunk);
+    a->chunks_per_warp = static_cast<int>(((slots + chunk - 1) / chunk + W - 1) / W);
+}
+__host__ __device__ constexpr size_t chunk_bytes(int chunks) {
+    return (chunks + 1) * sizeof(uint64_t) + chunks * (sizeof(float2) + 32 * sizeof(float));
 }
 
 template <int DT, int TX> cudaError_t launch_sample_rows(SampleArgs a, cudaStream_t s) {
-    constexpr int W = TX / 32, EB = DType<DT>::bytes;
-    // Vectors of a row, one more for rows off a boundary; whole batches, and as many chunks
-    // as 32 KB of maxima hold.
-    const int64_t slots = (a.N * EB + 15) / 16 + 1;
-    int64_t per = (slots + W - 1) / W;
-    per = (per + 31) / 32 * 32;
-    int64_t chunk = 32 * kBatch;
-    while ((per + chunk - 1) / chunk * W > 256) chunk *= 2;
-    a.per_warp = static_cast<int>(per);
-    a.chunk = static_cast<int>(chunk);
-    a.chunks_per_warp = static_cast<int>((per + chunk - 1) / chunk);
-    const int chunks = a.chunks_per_warp * W;
-    const size_t smem = (chunks + 1) * sizeof(uint64_t) + chunks * (sizeof(float2) + 32 * sizeof(float));
+    plan_chunks(&a, DType<DT>::bytes, TX / 32);
+    const size_t smem = chunk_bytes(a.chunks_per_warp * (TX / 32));
     auto kernel = sample_kernel<DT, TX>;
-    if (smem > 30 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
-    }
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
     return launch_pdl_smem(kernel, dim3(static_cast<unsigned>(a.B)), dim3(TX), smem, s, a);
+}
+
+// ---------------------------------------------------------------------------
+// Rows of up to 256 vectors: a warp each, V vectors per lane in registers, sums in f32.
+// ---------------------------------------------------------------------------
+constexpr int kShortWarps = 4;
+constexpr int kShortBins = 1 << bins_log2<32>();
+
+template <int DT> struct ShortShared {
+    SampleShared<32> row;
+    uint64_t dynamic[(chunk_bytes(2) + 7) / 8];
+    uint64_t keys[32];
+};
+
+template <int DT, int V> struct ShortRow {
+    static constexpr int EB = DType<DT>::bytes, E = 16 / EB, M = V * E;
+    uint32_t raw[V][4];
+    float w[M];  // weights; element j of the lane: vector j / E of its V, lanes next to each other
+    int col0, lane;
+    float m, ch, cl;
+    __device__ __forceinline__ float x(int j) const { return word_elem<DT>(raw[j / E], j % E); }
+    __device__ __forceinline__ int column(int j) const { return (j / E * 32 + lane) * E + j % E - col0; }
+    __device__ __forceinline__ float weight(float v) const {
+        const float d = v - m, t = d * ch, e = fmaf(d, cl, fmaf(d, ch, -t));  // e: what t lost (NaN for -inf)
+        return t > -126.0f ? fmaf(ex2(t), e * kLn2, ex2(t)) : 0.0f;
+    }
+    // The part of a sum that a comparison of two may be off by: twice the 1.45e-7 of ex2, the
+    // rounding of x - m (2^-24 of |z|, at most 8 octaves where the mass is), and chains of
+    // M + 10 additions.
+    static constexpr float kError = 8e-7f + (M + 10) * 6e-8f;
+    __device__ __forceinline__ float sum() const {
+        float s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < M; ++j) s += w[j];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        return s;
+    }
+    // Cuts off what lies behind the shortest prefix (of the elements with a positive weight, or
+    // of all for a count) that reaches `need`; false where f32 sums cannot tell.
+    __device__ __forceinline__ bool cut(bool by_mass, float need, float total, float err, uint64_t* keys, uint32_t* bins) {
+        uint32_t ohi = order_bits(m), olo;
+        {
+            float low = kInf;
+#pragma unroll
+            for (int j = 0; j < M; ++j)
+                if (by_mass ? w[j] > 0.0f : column(j) >= 0) low = fminf(low, x(j));
+            olo = __reduce_min_sync(0xffffffffu, order_bits(low));
+            olo = olo > 0 ? olo - 1 : 0;
+        }
+        float above = 0.0f;
+        // First a histogram of counts: over the values from the largest down to where the rest is
+        // lighter than what lies behind the threshold, or to the smallest of the lanes' maxima
+        // (of which there are 32), and as far again.
+        float low = m;
+        if (by_mass) {
+            const float z = __log2f(fmaxf(total - need, 1e-7f * total) / static_cast<float>(32 * M)) - 0.01f;
+            low = m + z / ch;
+        } else {
+            float top = x(0);
+#pragma unroll
+            for (int j = 1; j < M; ++j) top = fmaxf(top, x(j));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fminf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            low = need <= 32.0f ? top : m - 2.0f * (m - top);
+        }
+        const float scale = kShortBins * 0.9999f / (m - low);
+        // (Of 12 elements or fewer a lane, bisection takes fewer instructions for sums.)
+        if ((!by_mass || M > 12) && scale > 0.0f && scale < 1e30f && m - low < 1e30f) {
+            constexpr int P = kShortBins / 32;
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < P; ++i) bins[lane * P + i] = 0;
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < M; ++j)
+                if (x(j) >= low && (!by_mass || w[j] > 0.0f)) atomicAdd(&bins[static_cast<int>((m - x(j)) * scale)], 1u);
+            __syncwarp();
+            // By the weights of a bin's ends where they count.
+            float up = 0.0f, down = 0.0f, ups[P], downs[P];
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const int b = lane * P + i;
+                const float c = static_cast<float>(bins[b]);
+                ups[i] = downs[i] = c;
+                if (by_mass) {
+                    ups[i] *= weight(fminf(m, m - (static_cast<float>(b) - 0.01f) / scale));
+                    downs[i] *= weight(m - (static_cast<float>(b) + 1.01f) / scale);
+                }
+                up += ups[i];
+                down += downs[i];
+            }
+            float su = up, sd = down;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float p = __shfl_up_sync(0xffffffffu, su, o), q = __shfl_up_sync(0xffffffffu, sd, o);
+                if (lane >= o) su += p, sd += q;
+            }
+            su -= up;
+            sd -= down;
+            int b0 = INT_MAX, b1 = INT_MAX;
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                su += ups[i];
+                sd += downs[i];
+                if (su >= need - err && b0 == INT_MAX) b0 = lane * P + i;
+                if (sd >= need + err && b1 == INT_MAX) b1 = lane * P + i;
+            }
+            b0 = __reduce_min_sync(0xffffffffu, b0);
+            b1 = __reduce_min_sync(0xffffffffu, b1);
+            if (b0 != INT_MAX && b1 != INT_MAX) {
+                const float hi = b0 == 0 ? m : fminf(m, m - (static_cast<float>(b0) - 0.01f) / scale);
+                const float lo = m - (static_cast<float>(b1) + 1.01f) / scale;
+                float s = 0.0f;
+#pragma unroll
+                for (int j = 0; j < M; ++j) s += x(j) > hi ? (by_mass ? w[j] : 1.0f) : 0.0f;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                above = s;
+                ohi = order_bits(hi);
+                olo = max(olo, order_bits(lo));
+            }
+        }
+        // Bisection to at most 32 elements in (lo, hi] that hold the last kept one: values for
+        // sums, whose relevant elements lie within a few octaves; bits of ordered values for counts.
+        bool settled = false;
+        for (int step = 0; step < 64 && !settled; ++step) {
+            const float lo = order_value(olo), hi = order_value(ohi);
+            uint32_t inside = 0;
+#pragma unroll
+            for (int j = 0; j < M; ++j) inside += (!(x(j) <= lo) && x(j) <= hi && (!by_mass || w[j] > 0.0f)) ? 1u : 0u;
+            inside = __reduce_add_sync(0xffffffffu, inside);
+            if (inside <= 32) {
+                settled = true;
+                break;
+            }
+            if (ohi - olo < 2) return false;  // more than 32 equal values
+            uint32_t mid = olo + (ohi - olo) / 2;
+            if (by_mass) {
+                const uint32_t v = order_bits(0.5f * lo + 0.5f * hi);
+                if (v > olo && v < ohi) mid = v;
+            }
+            const float pivot = order_value(mid);
+            float s = 0.0f;
+#pragma unroll
+            for (int j = 0; j < M; ++j) s += x(j) > pivot ? (by_mass ? w[j] : 1.0f) : 0.0f;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            if (by_mass && fabsf(s - need) <= err) return false;
+            if (s >= need) olo = mid;
+            else ohi = mid, above = s;
+        }
+        if (!settled) return false;
+        // One element per lane, in order.
+        const float lo = order_value(olo), hi = order_value(ohi);
+        uint32_t at = 0;
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < M; ++j) {
+            const bool in = !(x(j) <= lo) && x(j) <= hi && (!by_mass || w[j] > 0.0f) && column(j) >= 0;
+            const uint32_t b = __ballot_sync(0xffffffffu, in);
+            if (in) keys[at + __popc(b & ((1u << lane) - 1u))] = topk_key(x(j), static_cast<uint32_t>(column(j)));
+            at += __popc(b);
+        }
+        __syncwarp();
+        const uint64_t key = list_sort(lane < static_cast<int>(at) ? keys[lane] : 0, lane);
+        const bool real = lane < static_cast<int>(at);
+        float s = !real ? 0.0f : by_mass ? weight(key_value(key)) : 1.0f;
+        const float own = s;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float b = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += b;
+        }
+        s += above;
+        const uint32_t reach = __ballot_sync(0xffffffffu, real && s >= need);
+        if (reach == 0) return false;
+        const int last = __ffs(reach) - 1;
+        const float over = __shfl_sync(0xffffffffu, s - need, last), under = __shfl_sync(0xffffffffu, need - (s - own), last);
+        if (by_mass && (over <= err || under <= err)) return false;
+        const uint64_t threshold = __shfl_sync(0xffffffffu, key, last);
+        const float tx = key_value(threshold);
+        const int tc = static_cast<int>(key_column(threshold));
+#pragma unroll
+        for (int j = 0; j < M; ++j)
+            if (!(x(j) > tx || (x(j) == tx && column(j) <= tc))) w[j] = 0.0f;
+        return true;
+    }
+};
+
+// false: the row is left to sample_row.
+template <int DT, int V> __device__ __forceinline__ bool sample_short(const SampleArgs& a, int64_t row, int lane, uint64_t* keys, uint32_t* bins) {
+    using R = ShortRow<DT, V>;
+    constexpr int E = R::E, M = R::M;
+    const RowSettings g(a, row);
+    const char* x0 = static_cast<const char*>(a.x) + row * a.row_stride * R::EB;
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(x0) & 15);
+    const char* base = x0 - off;
+    const int end = off + static_cast<int>(a.N) * R::EB, slots = a.N == 0 ? 0 : (end + 15) / 16;
+    R r;
+    r.lane = lane;
+    r.col0 = off / R::EB;
+    r.ch = g.ch;
+    r.cl = g.cl;
+    auto& w = r.raw;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int s = v * 32 + lane;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[v][i] = neg_inf_word<DT>();
+        if (s < slots) {
+            const uint4 q = ldg_stream16(base + s * 16);
+            w[v][0] = q.x, w[v][1] = q.y, w[v][2] = q.z, w[v][3] = q.w;
+            if (s == 0 || s == slots - 1) mask_words<DT>(w[v], s * 16, off, end);
+        }
+    }
+    float m = -kInf;
+    bool nan = false;
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+        nan |= r.x(j) != r.x(j);
+        m = fmaxf(m, r.x(j));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    r.m = m;
+    if (!g.valid || !(fabsf(m) < kInf) || __any_sync(0xffffffffu, nan)) {
+        if (lane == 0) put_token(a, row, -1, __int_as_float(0x7fc00000));
+        return true;
+    }
+    if (g.greedy) {
+        int c = INT_MAX;
+#pragma unroll
+        for (int j = 0; j < M; ++j)
+            if (r.x(j) == m) c = min(c, r.column(j));
+        c = __reduce_min_sync(0xffffffffu, c);
+        if (lane == 0) put_token(a, row, c, 0.0f);
+        return true;
+    }
+#pragma unroll
+    for (int j = 0; j < M; ++j) r.w[j] = r.weight(r.x(j));
+    if (g.use_k && !r.cut(false, static_cast<float>(g.top_k), 0.0f, 0.0f, keys, bins)) return false;
+    float total = r.sum();
+    if (g.use_p) {
+        if (!r.cut(true, g.top_p * total, total, R::kError * total, keys, bins)) return false;
+        total = r.sum();
+    }
+    if (g.use_min) {
+        // In octaves; the border is good to 2^-21 of the distance and of the logarithm.
+        const float z = __log2f(fminf(g.min_p, 1.0f));
+        bool open = false;
+        const float near = 4e-6f * (1.0f - z);
+#pragma unroll
+        for (int j = 0; j < M; ++j) {
+            const float t = (r.x(j) - m) * r.ch;
+            open |= fabsf(t - z) <= near && t != 0.0f;
+            if (t < z) r.w[j] = 0.0f;
+        }
+        if (__any_sync(0xffffffffu, open)) return false;
+        total = r.sum();
+    }
+    // The vector, the lane and the element at which the running sum passes the target.
+    const float err = R::kError * total;
+    float target = fminf(fmaxf(g.u, 0.0f), 1.0f) * total;  // (fmaxf: NaN counts as 0)
+    float before = 0.0f, run = 0.0f;
+    float mine[E];
+    int at = -1;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        float s = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) s += r.w[v * E + e];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (at < 0 && target < run + s) {
+            at = v;
+            before = run;
+#pragma unroll
+            for (int e = 0; e < E; ++e) mine[e] = r.w[v * E + e];
+        }
+        run += s;
+    }
+    if (at < 0) return false;
+    float s = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) s += mine[e];
+    const float own = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float b = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += b;
+    }
+    s += before;
+    const uint32_t reach = __ballot_sync(0xffffffffu, target < s);
+    if (reach == 0) return false;
+    const int who = __ffs(reach) - 1;
+    run = s - own;
+    int e_at = -1;
+    float lower = 0.0f, upper = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const float n = run + mine[e];
+        if (e_at < 0 && target < n) e_at = e, lower = run, upper = n;
+        run = n;
+    }
+    e_at = __shfl_sync(0xffffffffu, e_at, who);
+    lower = __shfl_sync(0xffffffffu, lower, who);
+    upper = __shfl_sync(0xffffffffu, upper, who);
+    if (e_at < 0 || target - lower <= err || upper - target <= err) return false;
+    if (lane == who) {
+        const int c = (at * 32 + lane) * E + e_at - r.col0;
+        // x from its weight's own element: the registers are indexed by constants only
+        float v = 0.0f;
+#pragma unroll
+        for (int j = 0; j < M; ++j)
+            if (j == at * E + e_at) v = r.x(j);
+        put_token(a, row, c, (v - m) / g.temperature - log1pf(fmaxf(total - 1.0f, 0.0f)));
+    }
+    return true;
+}
+
+template <int DT, int V> __global__ void __launch_bounds__(32 * kShortWarps, V <= 4 ? 6 : 3) sample_short_kernel(SampleArgs a) {
+    __shared__ ShortShared<DT> sh[kShortWarps];
+    __shared__ uint32_t powers[64];
+    pdl_trigger();
+    pdl_wait();
+    for (int i = threadIdx.x; i < 64; i += 32 * kShortWarps) powers[i] = kPowers[i];
+    __syncthreads();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kShortWarps + warp;
+    if (row >= a.B) return;
+    if (sample_short<DT, V>(a, row, lane, sh[warp].keys, sh[warp].row.bins)) return;
+    sample_row<DT, 32>(sh[warp].row, powers, reinterpret_cast<unsigned char*>(sh[warp].dynamic), a, row);
+}
+
+template <int DT, int V> cudaError_t launch_sample_short(SampleArgs a, cudaStream_t s) {
+    plan_chunks(&a, DType<DT>::bytes, 1);
+    return launch_pdl(sample_short_kernel<DT, V>, dim3(static_cast<unsigned>((a.B + kShortWarps - 1) / kShortWarps)),
+                      dim3(32 * kShortWarps), s, a);
 }
 
 template <int DT> cudaError_t launch_sample(SampleArgs a, int sms, cudaStream_t s) {
@@ -850,10 +1937,14 @@ template <int DT> cudaError_t launch_sample(SampleArgs a, int sms, cudaStream_t 
     a.bits = 62;
     for (int64_t n = a.N; n > 1; n = (n + 1) / 2) --a.bits;
     if (a.bits > 44) a.bits = 44;
-    if (slots <= 256) return launch_sample_rows<DT, 32>(a, s);
+    if (slots <= 32) return launch_sample_short<DT, 1>(a, s);
+    if (slots <= 64) return launch_sample_short<DT, 2>(a, s);
+    if (slots <= 96) return launch_sample_short<DT, 3>(a, s);
+    if (slots <= 128) return launch_sample_short<DT, 4>(a, s);
+    if (slots <= 256) return launch_sample_short<DT, 8>(a, s);
     if (slots <= 2048) return launch_sample_rows<DT, 128>(a, s);
-    if (a.B >= 4 * sms || slots <= 8192) return launch_sample_rows<DT, 256>(a, s);
-    return launch_sample_rows<DT, 1024>(a, s);
+    if (a.B >= 4 * sms || slots <= 4096) return launch_sample_rows<DT, 256>(a, s);
+    return launch_sample_rows<DT, 512>(a, s);
 }
 
 }  // namespace

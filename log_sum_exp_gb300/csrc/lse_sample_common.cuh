@@ -24,7 +24,7 @@ struct SampleArgs {
     int64_t* token;
     float* logprob;  // may be null
     int bits;        // fractional bits of a weight: N of them sum to less than 2^63
-    int per_warp, chunk, chunks_per_warp;  // vectors, vectors, chunks
+    int chunk, chunks_per_warp;  // vectors of a chunk, chunks of a warp
 };
 
 cudaError_t launch_sample_f32(const SampleArgs& a, int sms, cudaStream_t s);
