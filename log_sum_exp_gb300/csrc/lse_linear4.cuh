@@ -1,0 +1,381 @@
+// lse_linear4.cuh -- products of a few tokens with a matrix held in 4 bits (sm_103a).
+//
+//     y[t, n] = sum_g s[n, g] sum_{k in g} x[t, k] q[n, k]
+//
+// Bound by reading the codes: half a byte per weight leaves about three
+// instructions per weight and lane at the memory's rate, so the weights do not go through
+// scalar arithmetic.  A pair of nibbles becomes a pair of 16-bit floats, exactly q, by an or
+// with the bits of 1024 (bf16: 128) and a subtraction, and mma.sync multiplies 16 rows x 16
+// columns with 8 tokens, summing in f32.  The scale multiplies a group's f32 sum, so nothing
+// but the result is rounded to 16 bits.  f32 tokens are cut into three bf16 parts (8 + 8 + 8
+// bits, exact) that are three more columns of the product.  tcgen05 would need the
+// weights' floats in shared memory, four times the codes' bytes through it and back, to win
+// a product that takes less than a tenth of the time here; the tokens are few.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "lse_device.cuh"
+#include "lse_elem.cuh"
+#include "lse_internal.h"
+#include "lse_linear4_common.cuh"
+
+namespace lse {
+namespace {
+
+template <bool F16> __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    if constexpr (F16) asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// The eight values of a word as four pairs of columns.
+template <bool F16> __device__ __forceinline__ void word_pairs(uint32_t w, uint32_t (&p)[4]) {
+    if constexpr (F16) {
+        // 1024 + q + 8 has its last bit at 1; in the second nibble the code counts 16 times,
+        // and (1024 + 16 (q + 8)) / 16 - 72 = q without a shift.
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            const uint32_t v = i ? w >> 8 : w;
+            p[i] = sub2<true>((v & 0x000f000fu) | 0x64006400u, 0x64086408u);
+            asm("fma.rn.f16x2 %0, %1, %2, %3;"
+                : "=r"(p[i + 1])
+                : "r"((v & 0x00f000f0u) | 0x64006400u), "r"(0x2c002c00u), "r"(0xd480d480u));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = sub2<false>((w >> (4 * i) & 0x000f000fu) | 0x43004300u, 0x43084308u);
+    }
+}
+
+// c += a (16 x 16) b (16 x 8)
+template <bool F16>
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    if constexpr (F16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The part of x that a chunk needs, as 16-bit floats: PL planes of `tokens` rows.
+template <int DT>
+__device__ __forceinline__ void stage_tokens(const LinearArgs& a, int64_t t0, int b0, int nb, unsigned char* smem) {
+    const int cols = nb * kBlock, k0 = b0 * kBlock;
+    const int plane = a.tokens * a.row_bytes;
+    const int per_row = cols / 8;
+    for (int i = threadIdx.x; i < a.tokens * per_row; i += blockDim.x) {
+        const int t = i / per_row, v = i - t * per_row;
+        const int k = k0 + v * 8;
+        unsigned char* to = smem + t * a.row_bytes + v * 16;
+        const char* row = static_cast<const char*>(a.x) + (t0 + t) * a.x_stride * DType<DT>::bytes;
+        const bool live = t0 + t < a.T;
+        if constexpr (DT == kF32) {
+            float f[8];
+            load8<kF32>(row, k, live ? a.K : 0, a.x_vec, f);
+            uint32_t h[4], m[4], l[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                uint32_t part[3][2];
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    // Cut off, not rounded, so that no part overflows; nothing is left of an
+                    // infinity or a NaN.
+                    float r = f[2 * e + s];
+                    const bool finite = fabsf(r) <= 3.4028235e38f;
+#pragma unroll
+                    for (int q = 0; q < 3; ++q) {
+                        const uint32_t top = __float_as_uint(r) & 0xffff0000u;
+                        part[q][s] = (q == 0 && r != r) ? 0x7fc00000u : top;
+                        r = finite ? r - __uint_as_float(top) : 0.0f;
+                    }
+                }
+                h[e] = part[0][0] >> 16 | part[0][1];
+                m[e] = part[1][0] >> 16 | part[1][1];
+                l[e] = part[2][0] >> 16 | part[2][1];
+            }
+            *reinterpret_cast<uint4*>(to) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(to + plane) = make_uint4(m[0], m[1], m[2], m[3]);
+            *reinterpret_cast<uint4*>(to + 2 * plane) = make_uint4(l[0], l[1], l[2], l[3]);
+        } else {
+            uint4 v4 = make_uint4(0, 0, 0, 0);
+            if (live && a.x_vec && k + 8 <= a.K) {
+                v4 = __ldg(reinterpret_cast<const uint4*>(row + static_cast<int64_t>(k) * 2));
+            } else if (live) {
+                const unsigned short* r = reinterpret_cast<const unsigned short*>(row);
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[e] = (k + 2 * e < a.K ? __ldg(r + k + 2 * e) : 0u) |
+                           (k + 2 * e + 1 < a.K ? static_cast<uint32_t>(__ldg(r + k + 2 * e + 1)) << 16 : 0u);
+                v4 = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            *reinterpret_cast<uint4*>(to) = v4;
+        }
+    }
+}
+
+// A block's codes and scales of a warp's rows, as loaded: nothing is made of them before the
+// loads behind them are under way.  The 2 NS scales of a pair of rows are spread over the four
+// lanes that share it.
+template <int RT, int NS> struct Loaded {
+    static constexpr int kScales = NS == 4 ? 2 : 1;
+    uint4 q[RT][2];
+    uint32_t s[RT][kScales];
+};
+template <bool S32> __device__ __forceinline__ float scale_of(uint32_t bits, int dtype) {
+    if constexpr (S32) return __uint_as_float(bits);
+    else return dtype == kBF16 ? __uint_as_float(bits << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
+}
+
+// Tokens by groups of 8 (NT), groups of columns in a block (NS), tiles of 16 rows per warp (RT),
+// blocks of codes in flight per warp (D), scales of 32 bits.  a.ks warps share the columns of a
+// tile: block b of a chunk belongs to warp b % ks.  MW: warps of a CTA at most.
+template <int DT, int NT, int NS, int RT, int D, bool S32, int MW>
+__global__ void __launch_bounds__(32 * MW, MW == 8 ? 3 : 1) linear4_kernel(LinearArgs a) {
+    constexpr bool F16 = DT == kF16;
+    constexpr int PL = DT == kF32 ? 3 : 1;
+    extern __shared__ __align__(16) unsigned char smem[];
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+    const int KS = a.ks, ks = warp % KS, together = (blockDim.x >> 5) / KS;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.y) * 8 * NT;
+    const int plane = a.tokens * a.row_bytes;
+    float* red = reinterpret_cast<float*>(smem + PL * plane);
+
+    Loaded<RT, NS> ring[D];
+    // Where this lane's codes and scales of the tile begin.  Rows behind the last are computed from
+    // it and not stored.
+    const uint4* codes[RT][2];
+    const char* scales[RT][Loaded<RT, NS>::kScales];
+    constexpr int SB = S32 ? 4 : 2;
+    const int group0 = NS == 4 ? c : NS == 2 ? (c & 1) : 0;  // of a block: the group whose scale this lane loads
+    const auto aim = [&](int64_t tile) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t row = (tile * RT + r) * 16 + h * 8 + g;
+                codes[r][h] = a.codes + (row < a.N ? row : a.N - 1) * a.blocks * 4 + c;
+            }
+#pragma unroll
+            for (int i = 0; i < Loaded<RT, NS>::kScales; ++i) {
+                const int h = NS == 4 ? i : NS == 2 ? c >> 1 : c & 1;
+                const int64_t row = (tile * RT + r) * 16 + h * 8 + g;
+                scales[r][i] = static_cast<const char*>(a.scales) + (row < a.N ? row : a.N - 1) * a.scale_stride * SB;
+            }
+        }
+    };
+    const auto fetch = [&](Loaded<RT, NS>& to, int block) {
+        // (Groups behind the last meet codes of 0: any scale of the row that is there does.)
+        const int grp = min(block * NS + group0, a.groups - 1);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) to.q[r][h] = ldg_stream16(codes[r][h] + block * 4);
+#pragma unroll
+            for (int i = 0; i < Loaded<RT, NS>::kScales; ++i) {
+                if constexpr (S32) to.s[r][i] = __ldg(reinterpret_cast<const uint32_t*>(scales[r][i]) + grp);
+                else to.s[r][i] = __ldg(reinterpret_cast<const unsigned short*>(scales[r][i]) + grp);
+            }
+        }
+    };
+    float acc[RT][NT][4];
+    const auto multiply = [&](const Loaded<RT, NS>& from, int at) {  // at: the block in the chunk
+        float part[RT][NT][4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            if (w % (4 / NS) == 0) {
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) part[r][n][i] = 0.0f;
+            }
+            uint32_t p[RT][2][4];
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint4 v = from.q[r][h];
+                    word_pairs<F16>(w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w, p[r][h]);
+                }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                for (int l = 0; l < PL; ++l) {
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (n * 8 + g < a.tokens)
+                        x = *reinterpret_cast<const uint4*>(smem + l * plane + (n * 8 + g) * a.row_bytes + at * (kBlock * 2) +
+                                                            w * 64 + c * 16);
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        mma<F16>(part[r][n], p[r][0][0], p[r][1][0], p[r][0][1], p[r][1][1], x.x, x.y);
+                        mma<F16>(part[r][n], p[r][0][2], p[r][1][2], p[r][0][3], p[r][1][3], x.z, x.w);
+                    }
+                }
+            }
+            if (w % (4 / NS) == 4 / NS - 1) {
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    // From the lane that loaded it: group i of the block, rows g and g + 8.
+                    const int i = w / (4 / NS), lane0 = lane & ~3;
+                    const uint32_t b0 = __shfl_sync(0xffffffffu, from.s[r][0], lane0 + (NS == 1 ? 0 : i));
+                    const uint32_t b1 = __shfl_sync(0xffffffffu, from.s[r][NS == 4 ? 1 : 0], lane0 + (NS == 4 ? i : NS == 2 ? 2 + i : 1));
+                    const float s0 = scale_of<S32>(b0, a.scale_dtype), s1 = scale_of<S32>(b1, a.scale_dtype);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) acc[r][n][j] = fmaf(j < 2 ? s0 : s1, part[r][n][j], acc[r][n][j]);
+                }
+            }
+        }
+    };
+    // The first D blocks of a warp in the chunk at b0.
+    const auto refill = [&](int64_t tile, int b0) {
+        if (tile >= a.tiles) return;
+        if (b0 == 0) aim(tile);
+        const int nb = min(a.chunk_blocks, a.blocks - b0);
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+            if (ks + d * KS < nb) fetch(ring[d], b0 + ks + d * KS);
+    };
+    bool staged = false;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * together;
+    int64_t tile = static_cast<int64_t>(blockIdx.x) * together + warp / KS;
+    refill(tile, 0);
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * together; first < a.tiles; first += step, tile += step) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[r][n][i] = 0.0f;
+        for (int b0 = 0; b0 < a.blocks; b0 += a.chunk_blocks) {
+            const int nb = min(a.chunk_blocks, a.blocks - b0);
+            if (!staged || a.chunk_blocks < a.blocks) {
+                __syncthreads();
+                stage_tokens<DT>(a, t0, b0, nb, smem);
+                __syncthreads();
+                staged = true;
+            }
+            if (tile < a.tiles) {
+                for (int b = ks; b < nb; b += D * KS) {
+#pragma unroll
+                    for (int d = 0; d < D; ++d) {
+                        const int at = b + d * KS;
+                        if (at >= nb) continue;
+                        multiply(ring[d], at);
+                        if (at + D * KS < nb) fetch(ring[d], b0 + at + D * KS);
+                    }
+                }
+            }
+            // What comes next is under way before this tile's sums are put together.
+            if (b0 + a.chunk_blocks < a.blocks) refill(tile, b0 + a.chunk_blocks);
+            else refill(tile + step, 0);
+        }
+        if (KS > 1) {  // the warps' sums in their order
+            __syncthreads();
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    *reinterpret_cast<float4*>(red + (((warp * RT + r) * NT + n) * 32 + lane) * 4) =
+                        make_float4(acc[r][n][0], acc[r][n][1], acc[r][n][2], acc[r][n][3]);
+            __syncthreads();
+            if (ks == 0) {
+                for (int k = 1; k < KS; ++k)
+#pragma unroll
+                    for (int r = 0; r < RT; ++r)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const float4 v = *reinterpret_cast<const float4*>(red + ((((warp + k) * RT + r) * NT + n) * 32 + lane) * 4);
+                            acc[r][n][0] += v.x;
+                            acc[r][n][1] += v.y;
+                            acc[r][n][2] += v.z;
+                            acc[r][n][3] += v.w;
+                        }
+            }
+        }
+        if (ks != 0 || tile >= a.tiles) continue;
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t t = t0 + n * 8 + c * 2 + (i & 1), at = (tile * RT + r) * 16 + (i / 2) * 8 + g;
+                    if (t >= a.T || at >= a.N) continue;
+                    const int64_t o = t * a.out_stride + at;
+                    if (DT == kF32 || a.out_f32) static_cast<float*>(a.out)[o] = acc[r][n][i];
+                    else static_cast<unsigned short*>(a.out)[o] = static_cast<unsigned short>(pack2<DT == kF32 ? kBF16 : DT>(acc[r][n][i], 0.0f));
+                }
+    }
+}
+
+constexpr int kLinearSmem = 220 * 1024;  // of the 227 KB that a CTA may have
+
+template <int DT, int NT, int NS, bool S32> cudaError_t launch_linear(LinearArgs a, int sms, cudaStream_t s) {
+    constexpr int PL = DT == kF32 ? 3 : 1;
+    // Two tiles per warp halve the reads of x from shared memory for each weight; with four
+    // groups of tokens their sums would take more registers than there are.
+    constexpr int RT = NT * PL == 2 || NT * PL == 3 ? 2 : 1;
+
+    a.tokens = static_cast<int>(a.T < 8 * NT ? a.T : 8 * NT);
+    a.tiles = (a.N + 16 * RT - 1) / (16 * RT);
+    const int64_t row = static_cast<int64_t>(a.blocks) * kBlock * 2 + 64;
+    // Three CTAs of 8 warps per SM; x that leaves room for one only: 16 warps in it.
+    const bool wide = NT > 1 || PL * a.tokens * row > 64 * 1024;
+    const int warps = wide ? 16 : 8;
+    auto kernel = linear4_kernel<DT, NT, NS, RT, RT == 2 ? 2 : 3, S32, 16>;
+    if constexpr (NT == 1) {
+        if (!wide) kernel = linear4_kernel<DT, NT, NS, RT, RT == 2 ? 2 : 4, S32, 8>;
+    }
+    // About 24 warps per SM read at the same time; where rows are too few for that, several share
+    // a tile's columns.
+    int ks = 1;
+    while (ks < warps && a.tiles * ks < static_cast<int64_t>(sms) * 24 && 2 * ks <= a.blocks) ks *= 2;
+    a.ks = ks;
+    const int red = ks > 1 ? static_cast<int>(sizeof(float)) * warps * RT * NT * 128 : 0;
+    int most = ((kLinearSmem - red) / (PL * a.tokens) - 64) / (kBlock * 2);
+    if (most > a.blocks) most = a.blocks;
+    a.chunk_blocks = most < 1 ? 1 : most;
+    a.row_bytes = a.chunk_blocks * kBlock * 2 + 64;
+    const size_t smem = static_cast<size_t>(PL) * a.tokens * a.row_bytes + red;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+    }
+    const int64_t groups = (a.tiles + warps / ks - 1) / (warps / ks);
+    // CTAs go on with further tiles, so that x is brought in once; small x may be brought in
+    // more often.
+    const int64_t fit = static_cast<int64_t>(227 * 1024 / (smem + 1024)), threads = warps == 16 ? 1 : 4;
+    int64_t grid = static_cast<int64_t>(sms) * (fit < threads ? fit : threads);
+    if (grid > groups) grid = groups;
+    const int64_t gy = (a.T + 8 * NT - 1) / (8 * NT);
+    return launch_pdl_smem(kernel, dim3(static_cast<unsigned>(grid), static_cast<unsigned>(gy)), dim3(32 * warps), smem, s, a);
+}
+
+template <int DT, int NT, int NS> cudaError_t launch_linear_scales(const LinearArgs& a, int sms, cudaStream_t s) {
+    return a.scale_dtype == kF32 ? launch_linear<DT, NT, NS, true>(a, sms, s) : launch_linear<DT, NT, NS, false>(a, sms, s);
+}
+template <int DT, int NT> cudaError_t launch_linear_groups(const LinearArgs& a, int sms, cudaStream_t s) {
+    return a.group == 128 ? launch_linear_scales<DT, NT, 1>(a, sms, s)
+           : a.group == 64 ? launch_linear_scales<DT, NT, 2>(a, sms, s) : launch_linear_scales<DT, NT, 4>(a, sms, s);
+}
+template <int DT> cudaError_t launch_linear_tokens(const LinearArgs& a, int sms, cudaStream_t s) {
+    if (a.T <= 8) return launch_linear_groups<DT, 1>(a, sms, s);
+    if (a.T <= 16) return launch_linear_groups<DT, 2>(a, sms, s);
+    return launch_linear_groups<DT, 4>(a, sms, s);
+}
+
+}  // namespace
+}  // namespace lse
