@@ -39,7 +39,7 @@ __device__ __forceinline__ uint32_t pack_word(const int (&c)[8]) {
 struct FormArgs {
     const void* in;  // matrix, or int8 values
     int64_t N, K, in_stride;
-    int group;
+    int group_log2;
     uint32_t* codes;
     void* scales;
     int64_t scale_stride;
@@ -49,7 +49,8 @@ struct FormArgs {
 };
 
 constexpr int kFormThreads = 256;
-constexpr int kFormWords = 2;  // words of a lane in flight
+constexpr int kFormWords = 4;  // words of a lane in flight
+constexpr int kWarpColumns = 256;  // of 32 words
 
 __device__ __forceinline__ float max_nan(float a, float b) {
     float d;
@@ -57,65 +58,130 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return d;
 }
 
-// w / s to the nearest whole number, halves to even, without a division: the quotient by
-// the reciprocal is off by less than 1e-5 for |w / s| <= 12, so only one next to a half needs
-// the remainder w - q s, which is exact (both terms are multiples of the smaller one's last
-// bit, and it is no larger than s).
-__device__ __forceinline__ int nearest(float w, float s, float inv) {
-    const float t = w * inv;
-    float q = rintf(t);
-    if (fabsf(t - q) > 0.499f) {
-        const float r = fmaf(-q, s, w), h = 0.5f * s;
+// w / s to the nearest whole number, halves to even, with the remainder of a first guess, which
+// is exact (both terms are multiples of the smaller one's last bit, and it is no larger than s).
+__device__ __noinline__ uint32_t nearest_codes(const float (&f)[8], float s) {
+    const float up = s < 0x1p-60f ? 0x1p64f : 1.0f;  // the reciprocal of a small scale overflows
+    const float su = s * up, inv = __fdiv_rn(1.0f, su);
+    int c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float w = f[i] * up;
+        float q = rintf(fminf(fmaxf(w * inv, -16.0f), 16.0f));
+        const float r = fmaf(-q, su, w), h = 0.5f * su;
         if (fabsf(r) > h || (fabsf(r) == h && (static_cast<int>(q) & 1))) q += copysignf(1.0f, r);
+        c[i] = static_cast<int>(fminf(fmaxf(q, -8.0f), 7.0f)) + 8;
     }
-    return static_cast<int>(fminf(fmaxf(q, -8.0f), 7.0f));
+    return pack_word(c);
 }
 
-// A warp takes 32 words of a row kFormWords times over; the lanes of a group find its largest
-// magnitude with shuffles.
+// Rows off a 16-byte boundary pass through shared memory, so that a warp's accesses to them are
+// next to each other: `columns` elements from column k on to or from 32 lanes of eight.
+template <int DT> __device__ __forceinline__ void load_row_part(const void* row, int64_t k, int64_t K, bool vec, float* stage, float (&f)[8]) {
+    const int lane = threadIdx.x & 31;
+    if (vec) {
+        load8<DT>(row, k + lane * 8, K, true, f);
+        return;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t at = k + i * 32 + lane;
+        stage[i * 32 + lane] = at < K ? load_elem<DT>(row, at) : 0.0f;
+    }
+    __syncwarp();
+    const float4 a = *reinterpret_cast<const float4*>(stage + lane * 8), b = *reinterpret_cast<const float4*>(stage + lane * 8 + 4);
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+}
+template <int DT> __device__ __forceinline__ void store_row_part(void* row, int64_t k, int64_t K, bool vec, float* stage, const float (&f)[8]) {
+    const int lane = threadIdx.x & 31;
+    if (vec && k + lane * 8 + 8 <= K) {
+        char* p = static_cast<char*>(row) + (k + lane * 8) * DType<DT>::bytes;
+        if constexpr (DT == kF32) {
+            *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+            *reinterpret_cast<float4*>(p + 16) = make_float4(f[4], f[5], f[6], f[7]);
+        } else {
+            *reinterpret_cast<uint4*>(p) = make_uint4(pack2<DT>(f[0], f[1]), pack2<DT>(f[2], f[3]), pack2<DT>(f[4], f[5]), pack2<DT>(f[6], f[7]));
+        }
+        return;
+    }
+    const auto put = [&](int64_t at, float v) {
+        if (at >= K) return;
+        if constexpr (DT == kF32) static_cast<float*>(row)[at] = v;
+        else static_cast<unsigned short*>(row)[at] = static_cast<unsigned short>(pack2<DT>(v, 0.0f));
+    };
+    if (vec) {  // the row's end
+#pragma unroll
+        for (int i = 0; i < 8; ++i) put(k + lane * 8 + i, f[i]);
+        return;
+    }
+    __syncwarp();
+    *reinterpret_cast<float4*>(stage + lane * 8) = make_float4(f[0], f[1], f[2], f[3]);
+    *reinterpret_cast<float4*>(stage + lane * 8 + 4) = make_float4(f[4], f[5], f[6], f[7]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) put(k + i * 32 + lane, stage[i * 32 + lane]);
+}
+
+// A warp takes 256 columns of a row kFormWords times over; the lanes of a group find its largest
+// magnitude with shuffles.  Per element and lane about ten instructions, which is what the
+// memory's rate leaves for 16-bit weights: a quotient is rounded by adding it to a number whose
+// last bit counts 1 (its low bits are then the code), and only words with a quotient within 4e-6 of
+// a half, where the reciprocal's error could matter, and those of scales below the type's normal
+// range, whose rounding may leave quotients beyond 7, are done again with exact remainders.
 template <int DT> __global__ void __launch_bounds__(kFormThreads) quantize4_kernel(FormArgs a) {
+    __shared__ __align__(16) float stage[kFormThreads / 32][kWarpColumns];
     pdl_trigger();
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t words = blocks_of(a.K) * kBlockWords;
-    const int64_t per_row = (words + 32 * kFormWords - 1) / (32 * kFormWords);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int words = static_cast<int>(blocks_of(a.K) * kBlockWords);
+    const int per_row = (words + 32 * kFormWords - 1) / (32 * kFormWords);
     const int64_t units = a.N * per_row;
-    const int64_t groups = (a.K + a.group - 1) / a.group;
-    for (int64_t u = (static_cast<int64_t>(blockIdx.x) * kFormThreads + threadIdx.x) >> 5; u < units;
+    const int groups = static_cast<int>((a.K + (1 << a.group_log2) - 1) >> a.group_log2);
+    const int span = 1 << (a.group_log2 - 3);  // lanes of a group
+    constexpr float least = DT == kF16 ? 0x1p-14f : 0x1p-100f;
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * (kFormThreads / 32) + warp; u < units;
          u += static_cast<int64_t>(gridDim.x) * (kFormThreads / 32)) {
-        const int64_t n = u / per_row, j0 = (u - n * per_row) * 32 * kFormWords + lane;
+        const int64_t n = u / per_row;
+        const int j0 = static_cast<int>(u - n * per_row) * 32 * kFormWords + lane;
         const char* row = static_cast<const char*>(a.in) + n * a.in_stride * DType<DT>::bytes;
         float f[kFormWords][8];
 #pragma unroll
-        for (int v = 0; v < kFormWords; ++v) load8<DT>(row, (j0 + 32 * v) * 8, a.K, a.vec, f[v]);
+        for (int v = 0; v < kFormWords; ++v)
+            load_row_part<DT>(row, static_cast<int64_t>(j0 - lane + 32 * v) * 8, a.K, a.vec, stage[warp], f[v]);
 #pragma unroll
         for (int v = 0; v < kFormWords; ++v) {
-            const int64_t j = j0 + 32 * v;
-            float m = 0.0f;
+            const int j = j0 + 32 * v;
+            float m = fabsf(f[v][0]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(f[v][i]));
-            for (int o = a.group / 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+            for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(f[v][i]));
+            for (int o = span / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
             // A group with a NaN or an infinity has no scale: it reads back as NaN.
             float s = m <= 3.4028235e38f ? __fdiv_rn(m, 7.0f) : __int_as_float(0x7fffffff);
             if constexpr (DT != kF32) s = word_lo<DT>(pack2<DT>(s, 0.0f));
-            const int64_t k = j * 8;
-            if (k % a.group == 0 && k / a.group < groups) {
-                const int64_t at = n * a.scale_stride + k / a.group;
+            const int grp = j >> (a.group_log2 - 3);
+            if ((j & (span - 1)) == 0 && grp < groups) {
+                const int64_t at = n * a.scale_stride + grp;
                 if constexpr (DT == kF32) static_cast<float*>(a.scales)[at] = s;
                 else static_cast<unsigned short*>(a.scales)[at] = static_cast<unsigned short>(pack2<DT>(s, 0.0f));
             }
             if (j >= words) continue;
-            int c[8];
+            uint32_t w = 0x88888888u;
             if (s > 0.0f) {
-                const float up = s < 0x1p-60f ? 0x1p64f : 1.0f;  // the reciprocal of a small scale overflows
-                const float su = s * up, inv = __fdiv_rn(1.0f, su);
+                const float inv = __fdividef(1.0f, s), magic = 12582920.0f;  // 1.5 2^23 + 8
+                float far = 0.0f;
+                w = 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) c[i] = nearest(f[v][i] * up, su, inv) + 8;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) c[i] = 8;
+                for (int i = 0; i < 8; i += 2) {
+                    const float t0 = f[v][i] * inv, t1 = f[v][i + 1] * inv;
+                    const float k0 = t0 + magic, k1 = t1 + magic;
+                    far = fmaxf(far, fmaxf(fabsf(t0 - (k0 - magic)), fabsf(t1 - (k1 - magic))));
+                    const uint32_t p = __byte_perm(__float_as_uint(k0), __float_as_uint(k1), 0x5410);
+                    w |= (p & 0x000f000fu) << (2 * i);
+                }
+                if (far > 0.499996f || s < least) w = nearest_codes(f[v], s);
             }
-            a.codes[n * words + word_bytes(j) / 4] = pack_word(c);
+            a.codes[n * words + word_bytes(j) / 4] = w;
         }
     }
 }
@@ -140,52 +206,41 @@ __global__ void __launch_bounds__(kFormThreads) pack4_kernel(FormArgs a) {
 }
 
 template <int DT> __global__ void __launch_bounds__(kFormThreads) dequantize4_kernel(FormArgs a) {
-    constexpr int EB = DType<DT>::bytes;
+    __shared__ __align__(16) float stage[kFormThreads / 32][kWarpColumns];
     pdl_trigger();
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t words = blocks_of(a.K) * kBlockWords;
-    const int64_t per_row = (words + 32 * kFormWords - 1) / (32 * kFormWords);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int words = static_cast<int>(blocks_of(a.K) * kBlockWords);
+    const int per_row = (words + 32 * kFormWords - 1) / (32 * kFormWords);
     const int64_t units = a.N * per_row;
-    for (int64_t u = (static_cast<int64_t>(blockIdx.x) * kFormThreads + threadIdx.x) >> 5; u < units;
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * (kFormThreads / 32) + warp; u < units;
          u += static_cast<int64_t>(gridDim.x) * (kFormThreads / 32)) {
-        const int64_t n = u / per_row, j0 = (u - n * per_row) * 32 * kFormWords + lane;
-        char* row = static_cast<char*>(a.out) + n * a.out_stride * EB;
+        const int64_t n = u / per_row;
+        const int j0 = static_cast<int>(u - n * per_row) * 32 * kFormWords + lane;
+        char* row = static_cast<char*>(a.out) + n * a.out_stride * DType<DT>::bytes;
         uint32_t w[kFormWords];
         float s[kFormWords];
 #pragma unroll
         for (int v = 0; v < kFormWords; ++v) {
-            const int64_t j = j0 + 32 * v, k = j * 8;
+            const int j = j0 + 32 * v;
             w[v] = 0;
             s[v] = 0.0f;
-            if (k >= a.K) continue;
+            if (static_cast<int64_t>(j) * 8 >= a.K) continue;
             w[v] = __ldg(a.codes + n * words + word_bytes(j) / 4);
-            s[v] = load_elem<DT>(a.scales, n * a.scale_stride + k / a.group);
+            s[v] = load_elem<DT>(a.scales, n * a.scale_stride + (j >> (a.group_log2 - 3)));
         }
 #pragma unroll
         for (int v = 0; v < kFormWords; ++v) {
-            const int64_t k = (j0 + 32 * v) * 8;
+            const int64_t k = static_cast<int64_t>(j0 - lane + 32 * v) * 8;  // of the warp
             if (k >= a.K) continue;
             float f[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                f[i] = static_cast<float>(static_cast<int>(w[v] >> (i / 2 * 4 + (i % 2) * 16) & 15) - 8) * s[v];
-            if (a.vec && k + 8 <= a.K) {
-                if constexpr (DT == kF32) {
-                    *reinterpret_cast<float4*>(row + k * 4) = make_float4(f[0], f[1], f[2], f[3]);
-                    *reinterpret_cast<float4*>(row + k * 4 + 16) = make_float4(f[4], f[5], f[6], f[7]);
-                } else {
-                    *reinterpret_cast<uint4*>(row + k * 2) = make_uint4(pack2<DT>(f[0], f[1]), pack2<DT>(f[2], f[3]),
-                                                                        pack2<DT>(f[4], f[5]), pack2<DT>(f[6], f[7]));
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (k + i >= a.K) continue;
-                    if constexpr (DT == kF32) reinterpret_cast<float*>(row)[k + i] = f[i];
-                    else reinterpret_cast<unsigned short*>(row)[k + i] = static_cast<unsigned short>(pack2<DT>(f[i], 0.0f));
-                }
+            for (int i = 0; i < 8; ++i) {
+                // 2^23 + q + 8, less 2^23 + 8
+                const uint32_t c = w[v] >> (i / 2 * 4 + (i % 2) * 16) & 15u;
+                f[i] = (__uint_as_float(c | 0x4b000000u) - 8388616.0f) * s[v];
             }
+            store_row_part<DT>(row, k, a.K, a.vec, stage[warp], f);
         }
     }
 }
@@ -230,7 +285,7 @@ FormArgs form_args(int64_t N, int64_t K, int64_t group, const void* codes, const
     FormArgs a = {};
     a.N = N;
     a.K = K;
-    a.group = static_cast<int>(group);
+    a.group_log2 = group == 32 ? 5 : group == 64 ? 6 : 7;
     a.codes = static_cast<uint32_t*>(const_cast<void*>(codes));
     a.scales = const_cast<void*>(scales);
     a.scale_stride = scale_stride;

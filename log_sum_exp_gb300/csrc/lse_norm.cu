@@ -320,41 +320,77 @@ __global__ void __launch_bounds__(norm_threads<TX>()) norm_kernel(NormArgs a) {
 // sum is taken off, and q = s g w1 y.
 template <int DT> struct GradSlot {
     float h[Slot<DT>::E], gh[Slot<DT>::E], q[Slot<DT>::E];
-    Slot<DT> y;
+    Slot<DT> y, gate;
 };
 struct GradRow {
     const char *x, *y, *gate, *dout, *dh;
     float r1, r2;
 };
 
+// The arrays' words of a slot.
+template <int DT> struct GradWords {
+    Slot<DT> x, y, dn, dh, gate;
+};
+// What columns are multiplied by, row after row: weight, and scale times post weight times a gate
+// of one value per column.
+template <int DT> struct GradColumns {
+    float w[Slot<DT>::E], c[Slot<DT>::E];
+};
 template <int DT, class C>
-__device__ __forceinline__ void grad_slot(const NormArgs& a, const GradRow& r, const C& at, int D, GradSlot<DT>& g,
+__device__ __forceinline__ void load_columns(const NormArgs& a, const C& at, int D, GradColumns<DT>& k) {
+    constexpr int E = Slot<DT>::E;
+    float f[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) k.w[i] = 0.0f, k.c[i] = a.scale;
+    if (!at.any) return;
+    load_weights<DT>(a.weight, at, D, a, k.w);
+    if (a.post) {
+        load_weights<DT>(a.post, at, D, a, f);
+#pragma unroll
+        for (int i = 0; i < E; ++i) k.c[i] *= f[i];
+    }
+    if (a.gate_kind == kChannelGate) {
+        load_weights<DT>(a.gate, at, D, a, f);
+#pragma unroll
+        for (int i = 0; i < E; ++i) k.c[i] *= f[i];
+    }
+}
+template <int DT, class C>
+__device__ __forceinline__ void load_words(const GradRow& r, const C& at, int D, GradWords<DT>& w) {
+    w.x.w[0] = w.x.w[1] = w.x.w[2] = w.x.w[3] = 0;
+    w.y = w.dn = w.dh = w.gate = w.x;
+    if (!at.any) return;
+    w.x = load_slot<DT>(r.x, at, D);
+    if (r.y) w.y = load_slot<DT>(r.y, at, D);
+    w.dn = load_slot<DT>(r.dout, at, D);
+    if (r.dh) w.dh = load_slot<DT>(r.dh, at, D);
+    if (r.gate) w.gate = load_slot<DT>(r.gate, at, D);
+}
+
+template <int DT>
+__device__ __forceinline__ void grad_slot(const GradRow& r, const GradWords<DT>& words, const GradColumns<DT>& k, GradSlot<DT>& g,
                                           float (&n)[Slot<DT>::E], float (*sw)[Slot<DT>::E]) {
     constexpr int E = Slot<DT>::E;
-    Slot<DT> x, dn, dh;
-    x.w[0] = x.w[1] = x.w[2] = x.w[3] = 0;
-    g.y = dn = dh = x;
-    float w[E], f[E];
+    float f[E];
+    g.y = words.y;
+    g.gate = words.gate;
+    slot_floats<DT>(words.x, g.h);
+    slot_floats<DT>(words.dn, n);
+    slot_floats<DT>(words.dh, g.gh);
+    slot_floats<DT>(words.y, f);
+    if (r.gate) {
+        slot_floats<DT>(words.gate, g.q);
 #pragma unroll
-    for (int i = 0; i < E; ++i) g.q[i] = w[i] = 0.0f;
-    if (at.any) {
-        x = load_slot<DT>(r.x, at, D);
-        if (r.y) g.y = load_slot<DT>(r.y, at, D);
-        dn = load_slot<DT>(r.dout, at, D);
-        if (r.dh) dh = load_slot<DT>(r.dh, at, D);
-        load_weights<DT>(a.weight, at, D, a, w);
-        if (r.y) block_factors<DT>(a, at, r.gate, g.q);
+        for (int i = 0; i < E; ++i) g.q[i] *= k.c[i] * f[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) g.q[i] = k.c[i] * f[i];
     }
-    slot_floats<DT>(x, g.h);
-    slot_floats<DT>(dn, n);
-    slot_floats<DT>(dh, g.gh);
-    slot_floats<DT>(g.y, f);
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-        g.q[i] *= f[i];
         g.h[i] = fmaf(g.q[i], r.r1, g.h[i]);
         if (sw) (*sw)[i] = fmaf(n[i] * r.r2, g.h[i], (*sw)[i]);
-        n[i] *= w[i];
+        n[i] *= k.w[i];
         g.gh[i] = fmaf(n[i], r.r2, g.gh[i]);
     }
 }
@@ -381,31 +417,54 @@ __global__ void __launch_bounds__(norm_threads<TX>()) norm_backward_kernel(NormA
     const int64_t first = static_cast<int64_t>(blockIdx.x) * G + group;
     if (VEC && first < a.T)
         off_e = static_cast<int>(reinterpret_cast<uintptr_t>(a.x + first * a.x_bytes) & 15) / EB;
-    for (int64_t base = static_cast<int64_t>(blockIdx.x) * G; base < a.T; base += static_cast<int64_t>(gridDim.x) * G, turn ^= 1) {
-        const int64_t row = base + group;
+    const auto row_at = [&](int64_t row, GradRow* r) {
         const bool live = row < a.T;
-        const int D = live ? a.D : 0;
-        GradRow r;
-        r.x = a.x + row * a.x_bytes;
-        r.y = a.y ? a.y + row * a.y_bytes : nullptr;
-        r.gate = a.gate_kind == kElementGate ? a.gate + row * a.gate_bytes : nullptr;
-        r.dout = a.dout + row * a.dout_bytes;
-        r.dh = a.dh ? a.dh + row * a.dh_bytes : nullptr;
-        r.r1 = live && a.post ? a.post_rstd_in[row] : 1.0f;
-        r.r2 = live ? a.rstd_in[row] : 0.0f;
+        r->x = a.x + row * a.x_bytes;
+        r->y = a.y ? a.y + row * a.y_bytes : nullptr;
+        r->gate = a.gate_kind == kElementGate ? a.gate + row * a.gate_bytes : nullptr;
+        r->dout = a.dout + row * a.dout_bytes;
+        r->dh = a.dh ? a.dh + row * a.dh_bytes : nullptr;
+        r->r1 = live && a.post ? a.post_rstd_in[row] : 1.0f;
+        r->r2 = live ? a.rstd_in[row] : 0.0f;
+        return live ? a.D : 0;
+    };
+    const int64_t step = static_cast<int64_t>(gridDim.x) * G;
+    // With one slot per thread the next row is loaded while this one's sums are put together.
+    GradRow r;
+    GradWords<DT> words;
+    GradColumns<DT> columns;
+    int D = 0;
+    if constexpr (V == 1) {
+        load_columns<DT>(a, Columns<DT, TX, VEC>(0, t, off_e, a.D), a.D, columns);
+        D = row_at(first, &r);
+        load_words<DT>(r, Columns<DT, TX, VEC>(0, t, off_e, D), D, words);
+    }
+    for (int64_t base = static_cast<int64_t>(blockIdx.x) * G; base < a.T; base += step, turn ^= 1) {
+        const int64_t row = base + group;
+        if constexpr (V > 1) D = row_at(row, &r);
         GradSlot<DT> g;
         float s[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const Columns<DT, TX, VEC> at(j, t, off_e, D);
             float n[E];
-            grad_slot<DT>(a, r, at, D, g, n, &sw[j]);
+            if constexpr (V > 1) {
+                load_words<DT>(r, at, D, words);
+                load_columns<DT>(a, at, D, columns);
+            }
+            grad_slot<DT>(r, words, columns, g, n, &sw[j]);
 #pragma unroll
             for (int i = 0; i < E; ++i) {
                 s[0] = fmaf(n[i], g.h[i], s[0]);
                 s[1] = fmaf(g.q[i], g.gh[i], s[1]);
                 s[2] = fmaf(g.q[i], g.h[i], s[2]);
             }
+        }
+        GradRow next;
+        int next_D = 0;
+        if constexpr (V == 1) {
+            next_D = row_at(row + step, &next);
+            if (row + step - group < a.T) load_words<DT>(next, Columns<DT, TX, VEC>(0, t, off_e, next_D), next_D, words);
         }
         row_sums<TX, 3>(s, buf[turn]);
         const float k2 = r.r2 * r.r2 * r.r2 * a.inv_d * s[0];
@@ -415,34 +474,40 @@ __global__ void __launch_bounds__(norm_threads<TX>()) norm_backward_kernel(NormA
             const Columns<DT, TX, VEC> at(j, t, off_e, D);
             if (!at.any) continue;
             float f[E], e[E], o[E];
-            if constexpr (V > 1) grad_slot<DT>(a, r, at, D, g, f, nullptr);
+            if constexpr (V > 1) {
+                load_words<DT>(r, at, D, words);
+                load_columns<DT>(a, at, D, columns);
+                grad_slot<DT>(r, words, columns, g, f, nullptr);
+            }
             slot_floats<DT>(g.y, f);
 #pragma unroll
             for (int i = 0; i < E; ++i) g.gh[i] = fmaf(-g.h[i], k2, g.gh[i]);  // G
             if (a.dx) store_slot<DT>(a.dx + row * a.dx_bytes, at, D, slot_of<DT>(g.gh));
             if (!r.y) continue;
+            if (r.gate) slot_floats<DT>(g.gate, e);
             if (a.dy) {
-                block_factors<DT>(a, at, r.gate, e);
 #pragma unroll
-                for (int i = 0; i < E; ++i) o[i] = fmaf(e[i] * g.gh[i], r.r1, -f[i] * k1);
+                for (int i = 0; i < E; ++i) o[i] = fmaf((r.gate ? columns.c[i] * e[i] : columns.c[i]) * g.gh[i], r.r1, -f[i] * k1);
                 store_slot<DT>(a.dy + row * a.dy_bytes, at, D, slot_of<DT>(o));
             }
-            // s r1 y G: the sum that dw1 and the gate of a column share
+            // r1 y G: the sum that dw1 and the gate of a column share, but for the scale
 #pragma unroll
-            for (int i = 0; i < E; ++i) e[i] = g.gh[i] * f[i] * r.r1 * a.scale;
-            if (a.gate_kind == kElementGate) {
+            for (int i = 0; i < E; ++i) f[i] *= g.gh[i] * r.r1;
+            if (r.gate) {
                 if (a.dgate) {
-                    if (a.post) load_weights<DT>(a.post, at, D, a, o);
 #pragma unroll
-                    for (int i = 0; i < E; ++i) o[i] = a.post ? e[i] * o[i] : e[i];
+                    for (int i = 0; i < E; ++i) o[i] = f[i] * columns.c[i];
                     store_slot<DT>(a.dgate + row * a.dgate_bytes, at, D, slot_of<DT>(o));
                 }
-                slot_floats<DT>(load_slot<DT>(r.gate, at, D), o);
 #pragma unroll
-                for (int i = 0; i < E; ++i) e[i] *= o[i];
+                for (int i = 0; i < E; ++i) f[i] *= e[i];
             }
 #pragma unroll
-            for (int i = 0; i < E; ++i) sp[j][i] += e[i];
+            for (int i = 0; i < E; ++i) sp[j][i] += f[i];
+        }
+        if constexpr (V == 1) {
+            r = next;
+            D = next_D;
         }
     }
     if (!a.part) return;
@@ -486,14 +551,15 @@ __global__ void __launch_bounds__(norm_threads<TX>()) norm_backward_kernel(NormA
     }
 }
 
-// Sums the parts of 32 columns: eight warps take the parts in turn, then their sums in order.
-constexpr int kFinishWarps = 8;
+// Sums the parts of 32 columns: the warps take the parts in turn, then their sums in order.
+constexpr int kFinishWarps = 32;
 struct NormFinishArgs {
     const float* part;  // [2, parts, D]
     int parts, D;
     const void* post;  // factors of the second sum
     const void* gate;
     bool weights_f32;
+    float scale;  // of the second sum
     void* dweight;  // each may be null
     void* dpost;
     void* dgate;
@@ -518,7 +584,7 @@ __global__ void __launch_bounds__(32 * kFinishWarps) norm_finish_kernel(NormFini
     if (c < a.D) {
         const float* p = a.part + c;
         const int64_t stride = static_cast<int64_t>(a.parts) * a.D;
-#pragma unroll 4
+#pragma unroll 10
         for (int i = warp; i < a.parts; i += kFinishWarps) {
             s0 += p[static_cast<int64_t>(i) * a.D];
             s1 += p[static_cast<int64_t>(i) * a.D + stride];
@@ -534,6 +600,7 @@ __global__ void __launch_bounds__(32 * kFinishWarps) norm_finish_kernel(NormFini
         s0 += sums[0][w][lane];
         s1 += sums[1][w][lane];
     }
+    s1 *= a.scale;
     const bool f32 = DT == kF32 || a.weights_f32;
     if (a.dweight) put_weight<DT>(a.dweight, f32, c, s0);
     if (a.dpost) put_weight<DT>(a.dpost, f32, c, a.gate ? s1 * weight_at<DT>(a.gate, f32, c) : s1);
@@ -549,7 +616,7 @@ int64_t slots_of(int D, int EB, bool vec, bool aligned) {
 }
 
 template <int DT, bool VEC>
-cudaError_t launch_norm(const NormArgs& a, int64_t slots, cudaStream_t s) {
+cudaError_t launch_norm(const NormArgs& a, int64_t slots, bool few, cudaStream_t s) {
     const auto go = [&](auto kernel, int tx) {
         const int threads = tx < 128 ? 128 : tx;
         const int64_t grid = (a.T + threads / tx - 1) / (threads / tx);
@@ -559,8 +626,10 @@ cudaError_t launch_norm(const NormArgs& a, int64_t slots, cudaStream_t s) {
     if (slots <= 64) return go(norm_kernel<DT, 32, 2, VEC>, 32);
     if (slots <= 128) return go(norm_kernel<DT, 32, 4, VEC>, 32);
     if (slots <= 256) return go(norm_kernel<DT, 128, 2, VEC>, 128);
-    if (slots <= 512) return go(norm_kernel<DT, 256, 2, VEC>, 256);
-    if (slots <= 1024) return go(norm_kernel<DT, 512, 2, VEC>, 512);
+    // Rows by the thousand: four slots per thread wait less at the rows' sums (16384 x 4096 bf16 97
+    // us, two slots 107, one 154).  A few: one slot answers sooner (300 x 4096 4.3 us, 5.3, 7.1).
+    if (slots <= 512) return few ? go(norm_kernel<DT, 512, 1, VEC>, 512) : go(norm_kernel<DT, 128, 4, VEC>, 128);
+    if (slots <= 1024) return few ? go(norm_kernel<DT, 512, 2, VEC>, 512) : go(norm_kernel<DT, 256, 4, VEC>, 256);
     if (slots <= 2048) return go(norm_kernel<DT, 1024, 2, VEC>, 1024);
     if constexpr (DT != kF32) {
         return go(norm_kernel<DT, 1024, 3, VEC>, 1024);
@@ -718,8 +787,11 @@ lse_status lse_residual_norm(const void* x, lse_dtype dtype, int64_t T, int64_t 
     const bool vec = same_offsets(rows, 5, eb);
     const int64_t slots = slots_of(a.D, eb, vec, on_boundaries(rows[0], eb));
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    int sms = 0;
+    lse_status found = device_sms(&sms);
+    if (found != LSE_OK) return found;
     return cuda_status(by_type(dtype, vec, [&](auto dt, auto v) {
-        return launch_norm<decltype(dt)::value, decltype(v)::value != 0>(a, slots, s);
+        return launch_norm<decltype(dt)::value, decltype(v)::value != 0>(a, slots, T <= 4 * sms, s);
     }));
 }
 
@@ -788,6 +860,7 @@ lse_status lse_residual_norm_backward(const void* grad_out, int64_t grad_out_str
         f.post = post_weight;
         f.gate = gate_kind == LSE_GATE_CHANNEL ? gate : nullptr;
         f.weights_f32 = a.weights_f32;
+        f.scale = scale;
         f.dweight = dweight;
         f.dpost = dpost_weight;
         f.dgate = dgate_columns;
