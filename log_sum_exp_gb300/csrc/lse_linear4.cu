@@ -60,7 +60,9 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 
 // w / s to the nearest whole number, halves to even, with the remainder of a first guess, which
 // is exact (both terms are multiples of the smaller one's last bit, and it is no larger than s).
-__device__ __noinline__ uint32_t nearest_codes(const float (&f)[8], float s) {
+// (By value: through a pointer the words would live in memory.)
+__device__ __noinline__ uint32_t nearest_codes(float4 fa, float4 fb, float s) {
+    const float f[8] = {fa.x, fa.y, fa.z, fa.w, fb.x, fb.y, fb.z, fb.w};
     const float up = s < 0x1p-60f ? 0x1p64f : 1.0f;  // the reciprocal of a small scale overflows
     const float su = s * up, inv = __fdiv_rn(1.0f, su);
     int c[8];
@@ -126,9 +128,12 @@ template <int DT> __device__ __forceinline__ void store_row_part(void* row, int6
 // A warp takes 256 columns of a row kFormWords times over; the lanes of a group find its largest
 // magnitude with shuffles.  Per element and lane about ten instructions, which is what the
 // memory's rate leaves for 16-bit weights: a quotient is rounded by adding it to a number whose
-// last bit counts 1 (its low bits are then the code), and only words with a quotient within 4e-6 of
-// a half, where the reciprocal's error could matter, and those of scales below the type's normal
-// range, whose rounding may leave quotients beyond 7, are done again with exact remainders.
+// last bit counts 1 (its low bits are then the code).  Quotients of 16-bit numbers are often exact
+// halves, and 2^-13 away from one otherwise (2 w - (2 k + 1) s is a multiple of half the last bit of
+// an 11-bit s): one correction by the remainder brings them to 2^-22 and exact halves out exactly.
+// Of f32, words with a quotient within 4e-6 of a half, where the reciprocal's error could matter, are
+// done again with exact remainders, and so are those of scales below the type's normal range, whose
+// rounding may leave quotients beyond 7.
 template <int DT> __global__ void __launch_bounds__(kFormThreads) quantize4_kernel(FormArgs a) {
     __shared__ __align__(16) float stage[kFormThreads / 32][kWarpColumns];
     pdl_trigger();
@@ -173,13 +178,18 @@ template <int DT> __global__ void __launch_bounds__(kFormThreads) quantize4_kern
                 w = 0;
 #pragma unroll
                 for (int i = 0; i < 8; i += 2) {
-                    const float t0 = f[v][i] * inv, t1 = f[v][i + 1] * inv;
+                    float t0 = f[v][i] * inv, t1 = f[v][i + 1] * inv;
+                    if constexpr (DT != kF32) {
+                        t0 = fmaf(fmaf(-t0, s, f[v][i]), inv, t0);
+                        t1 = fmaf(fmaf(-t1, s, f[v][i + 1]), inv, t1);
+                    }
                     const float k0 = t0 + magic, k1 = t1 + magic;
-                    far = fmaxf(far, fmaxf(fabsf(t0 - (k0 - magic)), fabsf(t1 - (k1 - magic))));
+                    if constexpr (DT == kF32) far = fmaxf(far, fmaxf(fabsf(t0 - (k0 - magic)), fabsf(t1 - (k1 - magic))));
                     const uint32_t p = __byte_perm(__float_as_uint(k0), __float_as_uint(k1), 0x5410);
                     w |= (p & 0x000f000fu) << (2 * i);
                 }
-                if (far > 0.499996f || s < least) w = nearest_codes(f[v], s);
+                if (far > 0.499996f || s < least) 
+                    w = nearest_codes(make_float4(f[v][0], f[v][1], f[v][2], f[v][3]), make_float4(f[v][4], f[v][5], f[v][6], f[v][7]), s);
             }
             a.codes[n * words + word_bytes(j) / 4] = w;
         }

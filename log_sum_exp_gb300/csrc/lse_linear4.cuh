@@ -148,7 +148,18 @@ __global__ void __launch_bounds__(32 * MW, MW == 8 ? 3 : 1) linear4_kernel(Linea
     const int KS = a.ks, ks = warp % KS, together = (blockDim.x >> 5) / KS;
     const int64_t t0 = static_cast<int64_t>(blockIdx.y) * 8 * NT;
     const int plane = a.tokens * a.row_bytes;
-    float* red = reinterpret_cast<float*>(smem + PL * plane);
+    // Behind x a row of zeros for the tokens that are not there, then the warps' sums.
+    unsigned char* zeros = smem + PL * plane;
+    float* red = reinterpret_cast<float*>(zeros + a.row_bytes);
+    for (int i = threadIdx.x * 16; i < a.row_bytes; i += blockDim.x * 16) *reinterpret_cast<uint4*>(zeros + i) = make_uint4(0, 0, 0, 0);
+    const unsigned char* mine[NT];  // where this lane's columns of its tokens are
+    int next_plane[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const bool there = n * 8 + g < a.tokens;
+        mine[n] = (there ? smem + (n * 8 + g) * a.row_bytes : zeros) + c * 16;
+        next_plane[n] = there ? plane : 0;
+    }
 
     Loaded<RT, NS> ring[D];
     // Where this lane's codes and scales of the tile begin.  Rows behind the last are computed from
@@ -212,10 +223,7 @@ __global__ void __launch_bounds__(32 * MW, MW == 8 ? 3 : 1) linear4_kernel(Linea
             for (int n = 0; n < NT; ++n) {
 #pragma unroll
                 for (int l = 0; l < PL; ++l) {
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (n * 8 + g < a.tokens)
-                        x = *reinterpret_cast<const uint4*>(smem + l * plane + (n * 8 + g) * a.row_bytes + at * (kBlock * 2) +
-                                                            w * 64 + c * 16);
+                    const uint4 x = *reinterpret_cast<const uint4*>(mine[n] + l * next_plane[n] + at * (kBlock * 2) + w * 64);
 #pragma unroll
                     for (int r = 0; r < RT; ++r) {
                         mma<F16>(part[r][n], p[r][0][0], p[r][1][0], p[r][0][1], p[r][1][1], x.x, x.y);
@@ -321,6 +329,188 @@ __global__ void __launch_bounds__(32 * MW, MW == 8 ? 3 : 1) linear4_kernel(Linea
     }
 }
 
+// ---------------------------------------------------------------------------
+// Up to four f32 tokens: scalar arithmetic in f32, no matrix instructions (which would need three
+// parts of each number: 3 tokens of 50257 x 1001 took 27 us with them and take 19, one of 50257 x 1024
+// 19 and 12; of 16-bit tokens matrix instructions are faster, 39 us against 53 for one of 128256 x
+// 2048 bf16).  A warp takes rows
+// whole, 1024 columns at a time: a lane's 16 bytes hold 32 codes, and a row's 512 bytes lie next
+// to each other.  A code becomes an f32 by an or alone: left where it is in its word, p bits up
+// (p <= 16), it is 2^23 + 2^p (q + 8), and taking 2^23 + 8 2^p off leaves 2^p q exactly, which meets
+// an x that was multiplied by 2^-p in shared memory.  Of the eight codes of a word five need no
+// shift and three share one.  With packed FP32 that is 1.1 logic, 0.5 add and 0.5 multiply-add
+// instructions per weight and token.
+// ---------------------------------------------------------------------------
+// Rows of a warp at a time, and CTAs that an SM holds: by the registers that codes, scales, x
+// and sums take.
+__host__ __device__ constexpr int few_rows(int tokens, int ns) { return tokens == 1 && ns < 4 ? 4 : 2; }
+__host__ __device__ constexpr int few_ctas(int tokens) { return tokens <= 2 ? 3 : 2; }
+constexpr int kFewWarps = 8;
+constexpr int kFewColumns = 1024;
+constexpr int kFewTokens = 4;
+
+// Bits by which the code of column e of a word lies above bit 0, after the shift of its half.
+__host__ __device__ constexpr int code_shift(int e) { return e == 1 ? 16 : e % 2 == 0 ? 2 * e : 2 * e + 2; }
+
+// x of the call, permuted: [chunk][word][half][token][lane][4 columns], each column times 2^-shift.
+template <int DT, int NTOK> __device__ __forceinline__ void stage_few(const LinearArgs& a, int chunks, float* smem) {
+    for (int i = threadIdx.x; i < chunks * 8 * NTOK * 32; i += blockDim.x) {
+        const int lane = i & 31, t = i / 32 % NTOK, h = i / (32 * NTOK) % 2, w = i / (64 * NTOK) % 4, chunk = i / (256 * NTOK);
+        const int k = chunk * kFewColumns + (lane >> 2) * kBlock + 32 * w + 8 * (lane & 3) + 4 * h;
+        const char* row = static_cast<const char*>(a.x) + static_cast<int64_t>(t) * a.x_stride * DType<DT>::bytes;
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float down = __int_as_float((127 - (h == 0 ? code_shift(e) : code_shift(e + 4))) << 23);
+            v[e] = k + e < a.K ? load_elem<DT>(row, k + e) * down : 0.0f;
+        }
+        *reinterpret_cast<float4*>(smem + i * 4) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+}
+
+template <int DT, int NTOK, int NS, bool S32>
+__global__ void __launch_bounds__(32 * kFewWarps, few_ctas(NTOK)) linear4_few_kernel(LinearArgs a, int chunks) {
+    constexpr int SB = S32 ? 4 : 2, R = few_rows(NTOK, NS);
+    extern __shared__ __align__(16) unsigned char smem_bytes[];
+    const float* smem = reinterpret_cast<const float*>(smem_bytes);
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kFewWarps * R;
+    int64_t row0 = (static_cast<int64_t>(blockIdx.x) * kFewWarps + warp) * R;
+
+    uint4 q[R];
+    uint32_t s[R][NS];
+    // Codes of the rows from `row` on in a chunk: 8 (q = 0) behind the matrix's last column or row.
+    const auto fetch = [&](int64_t row, int chunk) {
+        const int block = chunk * (kFewColumns / kBlock) + (lane >> 2);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            q[r] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+#pragma unroll
+            for (int i = 0; i < NS; ++i) s[r][i] = 0;
+            if (row + r < a.N && block < a.blocks) {
+                q[r] = ldg_stream16(a.codes + ((row + r) * a.blocks + block) * 4 + (lane & 3));
+                const char* p = static_cast<const char*>(a.scales) + (row + r) * a.scale_stride * SB;
+#pragma unroll
+                for (int i = 0; i < NS; ++i) {
+                    const int grp = min(block * NS + i, a.groups - 1);  // (one behind the last meets q = 0)
+                    if constexpr (S32) s[r][i] = __ldg(reinterpret_cast<const uint32_t*>(p) + grp);
+                    else s[r][i] = __ldg(reinterpret_cast<const unsigned short*>(p) + grp);
+                }
+            }
+        }
+    };
+    fetch(row0, 0);
+    stage_few<DT, NTOK>(a, chunks, reinterpret_cast<float*>(smem_bytes));
+    __syncthreads();
+    for (; row0 < a.N; row0 += step) {
+        float acc[R][NTOK];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int t = 0; t < NTOK; ++t) acc[r][t] = 0.0f;
+        for (int chunk = 0; chunk < chunks; ++chunk) {
+            uint4 qq[R];
+            float sc[R][NS];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                qq[r] = q[r];
+#pragma unroll
+                for (int i = 0; i < NS; ++i) sc[r][i] = scale_of<S32>(s[r][i], a.scale_dtype);
+            }
+            // The next codes are under way while these are multiplied.
+            if (chunk + 1 < chunks) fetch(row0, chunk + 1);
+            else fetch(row0 + step, 0);
+            uint64_t part[R][NTOK];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                if (w % (4 / NS) == 0) {
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int t = 0; t < NTOK; ++t) part[r][t] = 0;
+                }
+                uint64_t x[NTOK][4];  // pairs of columns
+#pragma unroll
+                for (int t = 0; t < NTOK; ++t)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float4 v = *reinterpret_cast<const float4*>(smem + ((((chunk * 4 + w) * 2 + h) * NTOK + t) * 32 + lane) * 4);
+                        x[t][2 * h] = f2_pack(v.x, v.y);
+                        x[t][2 * h + 1] = f2_pack(v.z, v.w);
+                    }
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const uint32_t v = w == 0 ? qq[r].x : w == 1 ? qq[r].y : w == 2 ? qq[r].z : qq[r].w;
+                    const uint32_t up = v >> 12;  // columns 3, 5, 7
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        const int p0 = code_shift(e), p1 = code_shift(e + 1);
+                        const uint32_t b0 = (v & (15u << p0)) | 0x4b000000u;
+                        const uint32_t b1 = ((e == 0 ? v : up) & (15u << p1)) | 0x4b000000u;
+                        const uint64_t c = f2_sub(f2_pack(__uint_as_float(b0), __uint_as_float(b1)),
+                                                  f2_pack(8388608.0f + static_cast<float>(8 << p0), 8388608.0f + static_cast<float>(8 << p1)));
+#pragma unroll
+                        for (int t = 0; t < NTOK; ++t) part[r][t] = f2_fma(c, x[t][e / 2], part[r][t]);
+                    }
+                }
+                if (w % (4 / NS) == 4 / NS - 1) {
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int t = 0; t < NTOK; ++t) {
+                            float lo, hi;
+                            f2_unpack(part[r][t], lo, hi);
+                            acc[r][t] = fmaf(sc[r][w / (4 / NS)], lo + hi, acc[r][t]);
+                        }
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int t = 0; t < NTOK; ++t) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) acc[r][t] += __shfl_xor_sync(0xffffffffu, acc[r][t], o);
+            }
+        // Lane r * NTOK + t writes the sum of row r and token t.
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int t = 0; t < NTOK; ++t)
+                if (lane == t * R + r && row0 + r < a.N) {
+                    const int64_t o = t * a.out_stride + row0 + r;
+                    if (DT == kF32 || a.out_f32) static_cast<float*>(a.out)[o] = acc[r][t];
+                    else static_cast<unsigned short*>(a.out)[o] = static_cast<unsigned short>(pack2<DT == kF32 ? kBF16 : DT>(acc[r][t], 0.0f));
+                }
+    }
+}
+
+// x in shared memory as f32, with room for three CTAs per SM.
+inline bool few_fits(const LinearArgs& a) {
+    const int64_t chunks = (a.blocks + kFewColumns / kBlock - 1) / (kFewColumns / kBlock);
+    return a.T <= kFewTokens && a.blocks > 0 && chunks * kFewColumns * 4 * a.T <= 72 * 1024;
+}
+template <int DT, int NTOK, int NS, bool S32> cudaError_t launch_few(const LinearArgs& a, int sms, cudaStream_t s) {
+    auto kernel = linear4_few_kernel<DT, NTOK, NS, S32>;
+    const int chunks = (a.blocks + kFewColumns / kBlock - 1) / (kFewColumns / kBlock);
+    const size_t smem = static_cast<size_t>(chunks) * kFewColumns * 4 * NTOK;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+    }
+    int64_t grid = (a.N + kFewWarps * few_rows(NTOK, NS) - 1) / (kFewWarps * few_rows(NTOK, NS));
+    if (grid > few_ctas(NTOK) * sms) grid = few_ctas(NTOK) * sms;
+    return launch_pdl_smem(kernel, dim3(static_cast<unsigned>(grid)), dim3(32 * kFewWarps), smem, s, a, chunks);
+}
+template <int DT, int NTOK> cudaError_t launch_few_groups(const LinearArgs& a, int sms, cudaStream_t s) {
+    const bool f32 = a.scale_dtype == kF32;
+    if (a.group == 128) return f32 ? launch_few<DT, NTOK, 1, true>(a, sms, s) : launch_few<DT, NTOK, 1, false>(a, sms, s);
+    if (a.group == 64) return f32 ? launch_few<DT, NTOK, 2, true>(a, sms, s) : launch_few<DT, NTOK, 2, false>(a, sms, s);
+    return f32 ? launch_few<DT, NTOK, 4, true>(a, sms, s) : launch_few<DT, NTOK, 4, false>(a, sms, s);
+}
+
 constexpr int kLinearSmem = 220 * 1024;  // of the 227 KB that a CTA may have
 
 template <int DT, int NT, int NS, bool S32> cudaError_t launch_linear(LinearArgs a, int sms, cudaStream_t s) {
@@ -345,11 +535,11 @@ template <int DT, int NT, int NS, bool S32> cudaError_t launch_linear(LinearArgs
     while (ks < warps && a.tiles * ks < static_cast<int64_t>(sms) * 24 && 2 * ks <= a.blocks) ks *= 2;
     a.ks = ks;
     const int red = ks > 1 ? static_cast<int>(sizeof(float)) * warps * RT * NT * 128 : 0;
-    int most = ((kLinearSmem - red) / (PL * a.tokens) - 64) / (kBlock * 2);
+    int most = ((kLinearSmem - red) / (PL * a.tokens + 1) - 64) / (kBlock * 2);
     if (most > a.blocks) most = a.blocks;
     a.chunk_blocks = most < 1 ? 1 : most;
     a.row_bytes = a.chunk_blocks * kBlock * 2 + 64;
-    const size_t smem = static_cast<size_t>(PL) * a.tokens * a.row_bytes + red;
+    const size_t smem = static_cast<size_t>(PL * a.tokens + 1) * a.row_bytes + red;
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return e;
@@ -372,6 +562,16 @@ template <int DT, int NT> cudaError_t launch_linear_groups(const LinearArgs& a, 
            : a.group == 64 ? launch_linear_scales<DT, NT, 2>(a, sms, s) : launch_linear_scales<DT, NT, 4>(a, sms, s);
 }
 template <int DT> cudaError_t launch_linear_tokens(const LinearArgs& a, int sms, cudaStream_t s) {
+    if constexpr (DT == kF32) {
+        if (few_fits(a)) {
+            switch (a.T) {
+            case 1: return launch_few_groups<DT, 1>(a, sms, s);
+            case 2: return launch_few_groups<DT, 2>(a, sms, s);
+            case 3: return launch_few_groups<DT, 3>(a, sms, s);
+            default: return launch_few_groups<DT, 4>(a, sms, s);
+            }
+        }
+    }
     if (a.T <= 8) return launch_linear_groups<DT, 1>(a, sms, s);
     if (a.T <= 16) return launch_linear_groups<DT, 2>(a, sms, s);
     return launch_linear_groups<DT, 4>(a, sms, s);

@@ -71,10 +71,13 @@ struct NormArgs {
 };
 
 // ---------------------------------------------------------------------------
-// A thread's share of a row: V slots of 16 bytes.  VEC: the aligned vectors that cover the
-// row, which lies `off` bytes behind a boundary in every array; else single elements, the
-// lanes of a group next to each other.  Elements outside the row are zeros.
+// A thread's share of a row: V slots of 16 bytes.  kWhole: rows and weights on 16-byte
+// boundaries and of whole vectors, so that nothing is checked but the row's end; kCover: the
+// aligned vectors that cover the row, which lies `off` bytes behind a boundary in every array;
+// kSingle: single elements, the lanes of a group next to each other.  Elements outside the row
+// are zeros.
 // ---------------------------------------------------------------------------
+enum Mode : int { kSingle = 0, kCover = 1, kWhole = 2 };
 template <int DT> struct Slot {
     static constexpr int EB = DType<DT>::bytes, E = 16 / EB;
     uint32_t w[4];
@@ -104,13 +107,18 @@ template <int DT> __device__ __forceinline__ Slot<DT> slot_of(const float (&f)[S
 }
 
 // Columns of slot j of thread t: element i is column c + i * step.
-template <int DT, int TX, bool VEC> struct Columns {
+template <int DT, int TX, int MODE> struct Columns {
+    static constexpr bool kAlways = MODE == kWhole;
     int c, step;
-    bool whole;  // VEC: no element lies outside the row
+    bool whole;  // no element lies outside the row
     bool any;
     __device__ __forceinline__ Columns(int j, int t, int off_e, int D) {
         constexpr int E = Slot<DT>::E;
-        if constexpr (VEC) {
+        if constexpr (MODE == kWhole) {
+            c = (j * TX + t) * E;
+            step = 1;
+            whole = any = c < D;
+        } else if constexpr (MODE == kCover) {
             c = (j * TX + t) * E - off_e;
             step = 1;
             whole = c >= 0 && c + E <= D;
@@ -133,6 +141,7 @@ template <int DT, class C> __device__ __forceinline__ Slot<DT> load_slot(const c
         return s;
     }
     s.w[0] = s.w[1] = s.w[2] = s.w[3] = 0;
+    if constexpr (C::kAlways) return s;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
         const int c = at.c + i * at.step;
@@ -149,6 +158,7 @@ template <int DT, class C> __device__ __forceinline__ void store_slot(char* row,
         *reinterpret_cast<uint4*>(row + static_cast<int64_t>(at.c) * EB) = make_uint4(s.w[0], s.w[1], s.w[2], s.w[3]);
         return;
     }
+    if constexpr (C::kAlways) return;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
         const int c = at.c + i * at.step;
@@ -163,10 +173,10 @@ template <int DT, class C>
 __device__ __forceinline__ void load_weights(const char* p, const C& at, int D, const NormArgs& a,
                                              float (&f)[Slot<DT>::E]) {
     constexpr int E = Slot<DT>::E;
-    if (at.whole && a.weights_vec) {
+    if (C::kAlways || (at.whole && a.weights_vec)) {
         if (DT == kF32 || a.weights_f32) {
             const char* q = p + static_cast<int64_t>(at.c) * 4;
-            if ((at.c & 3) == 0) {
+            if (C::kAlways || (at.c & 3) == 0) {
 #pragma unroll
                 for (int i = 0; i < E; i += 4) {
                     const float4 v = __ldg(reinterpret_cast<const float4*>(q + i * 4));
@@ -174,7 +184,7 @@ __device__ __forceinline__ void load_weights(const char* p, const C& at, int D, 
                 }
                 return;
             }
-        } else if ((at.c & 7) == 0) {
+        } else if (C::kAlways || (at.c & 7) == 0) {
             const uint4 v = __ldg(reinterpret_cast<const uint4*>(p + static_cast<int64_t>(at.c) * 2));
             Slot<DT> s;
             s.w[0] = v.x, s.w[1] = v.y, s.w[2] = v.z, s.w[3] = v.w;
@@ -241,7 +251,7 @@ __device__ __forceinline__ void block_factors(const NormArgs& a, const C& at, co
 }
 
 // TX threads per row, V slots per thread.
-template <int DT, int TX, int V, bool VEC>
+template <int DT, int TX, int V, int MODE>
 __global__ void __launch_bounds__(norm_threads<TX>()) norm_kernel(NormArgs a) {
     constexpr int E = Slot<DT>::E, EB = Slot<DT>::EB;
     __shared__ float buf[2][1][32];
@@ -254,12 +264,12 @@ __global__ void __launch_bounds__(norm_threads<TX>()) norm_kernel(NormArgs a) {
     const char* xr = a.x + row * a.x_bytes;
     const char* yr = a.y ? a.y + row * a.y_bytes : nullptr;
     const char* gr = a.gate_kind == kElementGate ? a.gate + row * a.gate_bytes : nullptr;
-    const int off_e = VEC ? static_cast<int>(reinterpret_cast<uintptr_t>(xr) & 15) / EB : 0;
+    const int off_e = MODE == kCover ? static_cast<int>(reinterpret_cast<uintptr_t>(xr) & 15) / EB : 0;
 
     Slot<DT> x[V], y[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const Columns<DT, TX, VEC> at(j, t, off_e, D);
+        const Columns<DT, TX, MODE> at(j, t, off_e, D);
         x[j].w[0] = x[j].w[1] = x[j].w[2] = x[j].w[3] = 0;
         y[j] = x[j];
         if (!at.any) continue;
@@ -284,7 +294,7 @@ __global__ void __launch_bounds__(norm_threads<TX>()) norm_kernel(NormArgs a) {
     float s[1] = {0.0f};
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const Columns<DT, TX, VEC> at(j, t, off_e, D);
+        const Columns<DT, TX, MODE> at(j, t, off_e, D);
         slot_floats<DT>(x[j], h[j]);
         if (yr && at.any) {
             float f[E], q[E];
@@ -302,7 +312,7 @@ __global__ void __launch_bounds__(norm_threads<TX>()) norm_kernel(NormArgs a) {
     if (a.rstd && live && t == 0) a.rstd[row] = r2;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const Columns<DT, TX, VEC> at(j, t, off_e, D);
+        const Columns<DT, TX, MODE> at(j, t, off_e, D);
         if (!at.any) continue;
         float w[E];
         load_weights<DT>(a.weight, at, D, a, w);
@@ -395,12 +405,19 @@ __device__ __forceinline__ void grad_slot(const GradRow& r, const GradWords<DT>&
     }
 }
 
+// CTAs of the gradient that an SM holds: a slot of 16-bit elements takes about 120 registers
+// (8 columns' sums, factors and terms), one of f32 about 64.
+__host__ __device__ constexpr int backward_ctas(int threads, bool f32) {
+    return threads == 128 ? (f32 ? 6 : 4) : threads == 256 ? (f32 ? 3 : 2) : threads == 512 && f32 ? 2 : 1;
+}
+
 // One slot per thread stays in registers between the row's sums and its gradients; more
 // (rows of more than 16 KB) are loaded again, from L2: with the sums over rows they would
 // take more registers than an SM has.
-template <int DT, int TX, int V, bool VEC>
-__global__ void __launch_bounds__(norm_threads<TX>()) norm_backward_kernel(NormArgs a) {
+template <int DT, int TX, int V, int MODE>
+__global__ void __launch_bounds__(norm_threads<TX>(), backward_ctas(norm_threads<TX>(), DT == kF32)) norm_backward_kernel(NormArgs a) {
     constexpr int E = Slot<DT>::E, EB = Slot<DT>::EB, G = norm_threads<TX>() / TX;
+    constexpr bool kAhead = V == 1 && TX < 1024;  // (1024 threads have 64 registers each)
     constexpr int kShared = G > 1 ? TX * V * E : 1;
     __shared__ float buf[2][3][32];
     __shared__ float sums[2][kShared];
@@ -415,7 +432,7 @@ __global__ void __launch_bounds__(norm_threads<TX>()) norm_backward_kernel(NormA
     int off_e = 0;
     int turn = 0;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * G + group;
-    if (VEC && first < a.T)
+    if (MODE == kCover && first < a.T)
         off_e = static_cast<int>(reinterpret_cast<uintptr_t>(a.x + first * a.x_bytes) & 15) / EB;
     const auto row_at = [&](int64_t row, GradRow* r) {
         const bool live = row < a.T;
@@ -429,26 +446,26 @@ __global__ void __launch_bounds__(norm_threads<TX>()) norm_backward_kernel(NormA
         return live ? a.D : 0;
     };
     const int64_t step = static_cast<int64_t>(gridDim.x) * G;
-    // With one slot per thread the next row is loaded while this one's sums are put together.
+    // With one slot per thread (of 512 at most) the next row is loaded while this one's sums are put together.
     GradRow r;
     GradWords<DT> words;
     GradColumns<DT> columns;
     int D = 0;
-    if constexpr (V == 1) {
-        load_columns<DT>(a, Columns<DT, TX, VEC>(0, t, off_e, a.D), a.D, columns);
+    if constexpr (kAhead) {
+        load_columns<DT>(a, Columns<DT, TX, MODE>(0, t, off_e, a.D), a.D, columns);
         D = row_at(first, &r);
-        load_words<DT>(r, Columns<DT, TX, VEC>(0, t, off_e, D), D, words);
+        load_words<DT>(r, Columns<DT, TX, MODE>(0, t, off_e, D), D, words);
     }
     for (int64_t base = static_cast<int64_t>(blockIdx.x) * G; base < a.T; base += step, turn ^= 1) {
         const int64_t row = base + group;
-        if constexpr (V > 1) D = row_at(row, &r);
+        if constexpr (!kAhead) D = row_at(row, &r);
         GradSlot<DT> g;
         float s[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const Columns<DT, TX, VEC> at(j, t, off_e, D);
+            const Columns<DT, TX, MODE> at(j, t, off_e, D);
             float n[E];
-            if constexpr (V > 1) {
+            if constexpr (!kAhead) {
                 load_words<DT>(r, at, D, words);
                 load_columns<DT>(a, at, D, columns);
             }
@@ -462,22 +479,24 @@ __global__ void __launch_bounds__(norm_threads<TX>()) norm_backward_kernel(NormA
         }
         GradRow next;
         int next_D = 0;
-        if constexpr (V == 1) {
+        if constexpr (kAhead) {
             next_D = row_at(row + step, &next);
-            if (row + step - group < a.T) load_words<DT>(next, Columns<DT, TX, VEC>(0, t, off_e, next_D), next_D, words);
+            if (row + step - group < a.T) load_words<DT>(next, Columns<DT, TX, MODE>(0, t, off_e, next_D), next_D, words);
         }
         row_sums<TX, 3>(s, buf[turn]);
         const float k2 = r.r2 * r.r2 * r.r2 * a.inv_d * s[0];
         const float k1 = a.post ? r.r1 * r.r1 * r.r1 * a.inv_d * (s[1] - k2 * s[2]) : 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const Columns<DT, TX, VEC> at(j, t, off_e, D);
+            const Columns<DT, TX, MODE> at(j, t, off_e, D);
             if (!at.any) continue;
             float f[E], e[E], o[E];
             if constexpr (V > 1) {
                 load_words<DT>(r, at, D, words);
                 load_columns<DT>(a, at, D, columns);
                 grad_slot<DT>(r, words, columns, g, f, nullptr);
+            } else if constexpr (!kAhead) {
+                load_columns<DT>(a, at, D, columns);
             }
             slot_floats<DT>(g.y, f);
 #pragma unroll
@@ -505,7 +524,7 @@ __global__ void __launch_bounds__(norm_threads<TX>()) norm_backward_kernel(NormA
 #pragma unroll
             for (int i = 0; i < E; ++i) sp[j][i] += f[i];
         }
-        if constexpr (V == 1) {
+        if constexpr (kAhead) {
             r = next;
             D = next_D;
         }
@@ -521,7 +540,7 @@ __global__ void __launch_bounds__(norm_threads<TX>()) norm_backward_kernel(NormA
             if (g != group) continue;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const Columns<DT, TX, VEC> at(j, t, off_e, a.D);
+                const Columns<DT, TX, MODE> at(j, t, off_e, a.D);
 #pragma unroll
                 for (int i = 0; i < E; ++i) {
                     const int c = at.c + i * at.step;
@@ -539,7 +558,7 @@ __global__ void __launch_bounds__(norm_threads<TX>()) norm_backward_kernel(NormA
     } else {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const Columns<DT, TX, VEC> at(j, t, off_e, a.D);
+            const Columns<DT, TX, MODE> at(j, t, off_e, a.D);
 #pragma unroll
             for (int i = 0; i < E; ++i) {
                 const int c = at.c + i * at.step;
@@ -615,35 +634,35 @@ int64_t slots_of(int D, int EB, bool vec, bool aligned) {
     return s + (vec && !aligned ? 1 : 0);
 }
 
-template <int DT, bool VEC>
+template <int DT, int MODE>
 cudaError_t launch_norm(const NormArgs& a, int64_t slots, bool few, cudaStream_t s) {
     const auto go = [&](auto kernel, int tx) {
         const int threads = tx < 128 ? 128 : tx;
         const int64_t grid = (a.T + threads / tx - 1) / (threads / tx);
         return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(threads), s, a);
     };
-    if (slots <= 16) return go(norm_kernel<DT, 8, 2, VEC>, 8);
-    if (slots <= 64) return go(norm_kernel<DT, 32, 2, VEC>, 32);
-    if (slots <= 128) return go(norm_kernel<DT, 32, 4, VEC>, 32);
-    if (slots <= 256) return go(norm_kernel<DT, 128, 2, VEC>, 128);
+    if (slots <= 16) return go(norm_kernel<DT, 8, 2, MODE>, 8);
+    if (slots <= 64) return go(norm_kernel<DT, 32, 2, MODE>, 32);
+    if (slots <= 128) return go(norm_kernel<DT, 32, 4, MODE>, 32);
+    if (slots <= 256) return go(norm_kernel<DT, 128, 2, MODE>, 128);
     // Rows by the thousand: four slots per thread wait less at the rows' sums (16384 x 4096 bf16 97
     // us, two slots 107, one 154).  A few: one slot answers sooner (300 x 4096 4.3 us, 5.3, 7.1).
-    if (slots <= 512) return few ? go(norm_kernel<DT, 512, 1, VEC>, 512) : go(norm_kernel<DT, 128, 4, VEC>, 128);
-    if (slots <= 1024) return few ? go(norm_kernel<DT, 512, 2, VEC>, 512) : go(norm_kernel<DT, 256, 4, VEC>, 256);
-    if (slots <= 2048) return go(norm_kernel<DT, 1024, 2, VEC>, 1024);
+    if (slots <= 512) return few ? go(norm_kernel<DT, 512, 1, MODE>, 512) : go(norm_kernel<DT, 128, 4, MODE>, 128);
+    if (slots <= 1024) return few ? go(norm_kernel<DT, 512, 2, MODE>, 512) : go(norm_kernel<DT, 256, 4, MODE>, 256);
+    if (slots <= 2048) return go(norm_kernel<DT, 1024, 2, MODE>, 1024);
     if constexpr (DT != kF32) {
-        return go(norm_kernel<DT, 1024, 3, VEC>, 1024);
+        return go(norm_kernel<DT, 1024, 3, MODE>, 1024);
     } else {
-        if (slots <= 4096) return go(norm_kernel<DT, 1024, 4, VEC>, 1024);
-        return go(norm_kernel<DT, 1024, 5, VEC>, 1024);
+        if (slots <= 4096) return go(norm_kernel<DT, 1024, 4, MODE>, 1024);
+        return go(norm_kernel<DT, 1024, 5, MODE>, 1024);
     }
 }
 
-// Rows that a CTA of the gradient takes at a time, and CTAs that are resident on an SM.
+// Rows that a CTA of the gradient takes at a time, and the CTAs.
 struct BackwardPlan {
     int tx, v, rows, grid;
 };
-BackwardPlan plan_norm_backward(int64_t T, int64_t slots, int sms) {
+BackwardPlan plan_norm_backward(int64_t T, int64_t slots, bool f32, int sms) {
     BackwardPlan p;
     p.v = 1;
     if (slots <= 8) p.tx = 8;
@@ -655,29 +674,29 @@ BackwardPlan plan_norm_backward(int64_t T, int64_t slots, int sms) {
     else p.tx = 1024, p.v = slots <= 1024 ? 1 : slots <= 2048 ? 2 : 5;
     const int threads = p.tx < 128 ? 128 : p.tx;
     p.rows = threads / p.tx;
-    const int64_t resident = static_cast<int64_t>(sms) * (threads <= 128 ? 6 : threads == 256 ? 3 : threads == 512 ? 2 : 1) / 8 * 8;
+    const int64_t resident = static_cast<int64_t>(sms) * backward_ctas(threads, f32) / 8 * 8;
     int64_t grid = (T + p.rows - 1) / p.rows;
     if (grid > resident) grid = resident;
     p.grid = static_cast<int>((grid + 7) / 8 * 8);
     return p;
 }
 
-template <int DT, bool VEC>
+template <int DT, int MODE>
 cudaError_t launch_norm_backward(const NormArgs& a, const BackwardPlan& p, cudaStream_t s) {
     const auto go = [&](auto kernel, int threads) {
         return launch_pdl(kernel, dim3(static_cast<unsigned>(p.grid)), dim3(threads), s, a);
     };
     switch (p.tx) {
-    case 8: return go(norm_backward_kernel<DT, 8, 1, VEC>, 128);
-    case 32: return go(norm_backward_kernel<DT, 32, 1, VEC>, 128);
-    case 64: return go(norm_backward_kernel<DT, 64, 1, VEC>, 128);
-    case 128: return go(norm_backward_kernel<DT, 128, 1, VEC>, 128);
-    case 256: return go(norm_backward_kernel<DT, 256, 1, VEC>, 256);
-    case 512: return go(norm_backward_kernel<DT, 512, 1, VEC>, 512);
+    case 8: return go(norm_backward_kernel<DT, 8, 1, MODE>, 128);
+    case 32: return go(norm_backward_kernel<DT, 32, 1, MODE>, 128);
+    case 64: return go(norm_backward_kernel<DT, 64, 1, MODE>, 128);
+    case 128: return go(norm_backward_kernel<DT, 128, 1, MODE>, 128);
+    case 256: return go(norm_backward_kernel<DT, 256, 1, MODE>, 256);
+    case 512: return go(norm_backward_kernel<DT, 512, 1, MODE>, 512);
     default:
-        return p.v == 1 ? go(norm_backward_kernel<DT, 1024, 1, VEC>, 1024)
-               : p.v == 2 ? go(norm_backward_kernel<DT, 1024, 2, VEC>, 1024)
-                          : go(norm_backward_kernel<DT, 1024, 5, VEC>, 1024);
+        return p.v == 1 ? go(norm_backward_kernel<DT, 1024, 1, MODE>, 1024)
+               : p.v == 2 ? go(norm_backward_kernel<DT, 1024, 2, MODE>, 1024)
+                          : go(norm_backward_kernel<DT, 1024, 5, MODE>, 1024);
     }
 }
 
@@ -743,15 +762,24 @@ void set_common(NormArgs* a, int dtype, int64_t T, int64_t D, const void* x, int
     a->inv_d = static_cast<float>(1.0 / static_cast<double>(D));
 }
 
-template <class F> cudaError_t by_type(int dtype, bool vec, F&& f) {
+template <int DT, class F> cudaError_t by_mode(int mode, F&& f) {
+    return mode == kWhole ? f(IntConst<DT>{}, IntConst<kWhole>{})
+           : mode == kCover ? f(IntConst<DT>{}, IntConst<kCover>{}) : f(IntConst<DT>{}, IntConst<kSingle>{});
+}
+template <class F> cudaError_t by_type(int dtype, int mode, F&& f) {
     switch (dtype) {
-    case LSE_F32: return vec ? f(IntConst<kF32>{}, IntConst<1>{}) : f(IntConst<kF32>{}, IntConst<0>{});
-    case LSE_BF16: return vec ? f(IntConst<kBF16>{}, IntConst<1>{}) : f(IntConst<kBF16>{}, IntConst<0>{});
-    default: return vec ? f(IntConst<kF16>{}, IntConst<1>{}) : f(IntConst<kF16>{}, IntConst<0>{});
+    case LSE_F32: return by_mode<kF32>(mode, f);
+    case LSE_BF16: return by_mode<kBF16>(mode, f);
+    default: return by_mode<kF16>(mode, f);
     }
 }
 
 bool on_boundaries(const Rows& r, int eb) { return !misaligned(r.p, 16) && r.stride * eb % 16 == 0; }
+
+int mode_of(const Rows* rows, int n, int eb, const NormArgs& a) {
+    if (!same_offsets(rows, n, eb)) return kSingle;
+    return on_boundaries(rows[0], eb) && a.D * eb % 16 == 0 && a.weights_vec ? kWhole : kCover;
+}
 
 }  // namespace
 }  // namespace lse
@@ -784,14 +812,14 @@ lse_status lse_residual_norm(const void* x, lse_dtype dtype, int64_t T, int64_t 
     a.out_bytes = out_stride * eb;
     a.rstd = rstd;
     a.post_rstd = post_rstd;
-    const bool vec = same_offsets(rows, 5, eb);
-    const int64_t slots = slots_of(a.D, eb, vec, on_boundaries(rows[0], eb));
+    const int mode = mode_of(rows, 5, eb, a);
+    const int64_t slots = slots_of(a.D, eb, mode != kSingle, on_boundaries(rows[0], eb));
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     int sms = 0;
     lse_status found = device_sms(&sms);
     if (found != LSE_OK) return found;
-    return cuda_status(by_type(dtype, vec, [&](auto dt, auto v) {
-        return launch_norm<decltype(dt)::value, decltype(v)::value != 0>(a, slots, T <= 4 * sms, s);
+    return cuda_status(by_type(dtype, mode, [&](auto dt, auto v) {
+        return launch_norm<decltype(dt)::value, decltype(v)::value>(a, slots, T <= 4 * sms, s);
     }));
 }
 
@@ -840,16 +868,16 @@ lse_status lse_residual_norm_backward(const void* grad_out, int64_t grad_out_str
     if (T > 0) {
         int sms = 0;
         if ((st = device_sms(&sms)) != LSE_OK) return st;
-        const bool vec = same_offsets(rows, 8, eb);
-        const BackwardPlan p = plan_norm_backward(T, slots_of(a.D, eb, vec, on_boundaries(rows[0], eb)), sms);
+        const int mode = mode_of(rows, 8, eb, a);
+        const BackwardPlan p = plan_norm_backward(T, slots_of(a.D, eb, mode != kSingle, on_boundaries(rows[0], eb)), dtype == LSE_F32, sms);
         if (sums) {
             st = take_scratch(&scratch, static_cast<size_t>(p.grid) * a.D * 2 * sizeof(float), s);
             if (st != LSE_OK) return st;
             a.part = static_cast<float*>(scratch);
             a.parts = p.grid;
         }
-        e = by_type(dtype, vec, [&](auto dt, auto v) {
-            return launch_norm_backward<decltype(dt)::value, decltype(v)::value != 0>(a, p, s);
+        e = by_type(dtype, mode, [&](auto dt, auto v) {
+            return launch_norm_backward<decltype(dt)::value, decltype(v)::value>(a, p, s);
         });
     }
     if (sums && e == cudaSuccess) {
@@ -864,7 +892,7 @@ lse_status lse_residual_norm_backward(const void* grad_out, int64_t grad_out_str
         f.dweight = dweight;
         f.dpost = dpost_weight;
         f.dgate = dgate_columns;
-        e = by_type(dtype, true, [&](auto dt, auto) {
+        e = by_type(dtype, kSingle, [&](auto dt, auto) {
             return launch_pdl(norm_finish_kernel<decltype(dt)::value>, dim3((a.D + 31) / 32), dim3(32 * kFinishWarps), s, f);
         });
     }
