@@ -13,7 +13,8 @@ tokens, rewards those that follow a hidden rule, and then
                          their gradient with respect to the logits
     lse_grad_clip        the global norm of both gradients, clipped in place
 
-At the end one token is decoded with its top alternatives (lse_token_stats).
+At the end one token is decoded with its top alternatives (lse_token_stats), and a few more
+are drawn with the output matrix held in 4 bits (lse_linear4, lse_sample).
 """
 from __future__ import annotations
 
@@ -93,6 +94,20 @@ def train(steps: int = 40, vocab: int = 2003, width: int = 256, batch: int = 409
     return model, rewards
 
 
+def decode(model: TokenModel, token: int, steps: int, seed: int = 0):
+    """Tokens drawn one after the other, the output matrix held in 4 bits (lse_quantize4,
+    lse_linear4, lse_sample)."""
+    head = L.lse_quantize4(model.params[1].detach(), group=64)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    ids, out = torch.tensor([token], device="cuda"), []
+    for _ in range(steps):
+        rows = L.lse_embedding(model.params[0].detach(), ids, scale=model.scale)
+        logits = L.lse_linear4(rows, head, out_dtype=torch.float32)
+        ids = L.lse_sample(logits, torch.rand(1, generator=g, device="cuda"), temperature=0.7, top_k=20).token
+        out.append(int(ids))
+    return out
+
+
 def main() -> None:
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--steps", type=int, default=40)
@@ -106,6 +121,7 @@ def main() -> None:
     top = ", ".join(f"{int(i)} ({math.exp(float(lp)):.2f})"
                     for i, lp in zip(s.top_index[0], s.top_logprob[0]))
     print(f"after token 5 (rule: {(7 * 5 + 3) % 16}): {top}")
+    print("drawn from there with a 4-bit output matrix:", decode(model, 5, 8))
 
 
 if __name__ == "__main__":

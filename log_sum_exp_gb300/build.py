@@ -17,12 +17,12 @@ SOURCES = ["lse_api.cu", "lse_kernels_f32.cu", "lse_kernels_bf16.cu", "lse_kerne
            "lse_strided.cu", "lse_rowtile.cu", "lse_noalloc.cu", "lse_ex16_f32.cu",
            "lse_ex16_bf16.cu", "lse_ex16_f16.cu", "lse_stats.cu", "lse_stats_f32.cu", "lse_stats_bf16.cu",
            "lse_stats_f16.cu", "lse_grads.cu", "lse_embed.cu",
-           "lse_norm.cu", "lse_linear4.cu", "lse_linear4_f32.cu", "lse_linear4_bf16.cu", "lse_linear4_f16.cu",
+           "lse_norm.cu", "lse_norm_f32.cu", "lse_norm_bf16.cu", "lse_norm_f16.cu", "lse_linear4.cu", "lse_linear4_f32.cu", "lse_linear4_bf16.cu", "lse_linear4_f16.cu",
            "lse_sample.cu", "lse_sample_f32.cu", "lse_sample_bf16.cu",
            "lse_sample_f16.cu"]
 HEADERS = ["lse_device.cuh", "lse_edges.cuh", "lse_kernels.cuh", "lse_internal.h", "lse_elem.cuh", "lse_topk.cuh",
            "lse_stats.cuh", "lse_stats_common.cuh", "lse_sample.cuh", "lse_sample_common.cuh",
-           "lse_linear4.cuh", "lse_linear4_common.cuh"]
+           "lse_linear4.cuh", "lse_linear4_common.cuh", "lse_norm.cuh", "lse_norm_common.cuh"]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",

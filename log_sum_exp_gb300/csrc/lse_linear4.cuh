@@ -329,6 +329,10 @@ __global__ void __launch_bounds__(32 * MW, MW == 8 ? 3 : 1) linear4_kernel(Linea
     }
 }
 
+// Dynamic shared memory of a CTA at most, the same in every call: calls of other threads do not
+// lower it in between.
+constexpr int kMostDynamic = 227 * 1024;
+
 // ---------------------------------------------------------------------------
 // Up to four f32 tokens: scalar arithmetic in f32, no matrix instructions (which would need three
 // parts of each number: 3 tokens of 50257 x 1001 took 27 us with them and take 19, one of 50257 x 1024
@@ -497,7 +501,7 @@ template <int DT, int NTOK, int NS, bool S32> cudaError_t launch_few(const Linea
     const int chunks = (a.blocks + kFewColumns / kBlock - 1) / (kFewColumns / kBlock);
     const size_t smem = static_cast<size_t>(chunks) * kFewColumns * 4 * NTOK;
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostDynamic);
         if (e != cudaSuccess) return e;
     }
     int64_t grid = (a.N + kFewWarps * few_rows(NTOK, NS) - 1) / (kFewWarps * few_rows(NTOK, NS));
@@ -541,7 +545,7 @@ template <int DT, int NT, int NS, bool S32> cudaError_t launch_linear(LinearArgs
     a.row_bytes = a.chunk_blocks * kBlock * 2 + 64;
     const size_t smem = static_cast<size_t>(PL * a.tokens + 1) * a.row_bytes + red;
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostDynamic);
         if (e != cudaSuccess) return e;
     }
     const int64_t groups = (a.tiles + warps / ks - 1) / (warps / ks);

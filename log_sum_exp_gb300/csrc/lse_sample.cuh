@@ -1582,13 +1582,14 @@ __host__ __device__ constexpr size_t chunk_bytes(int chunks) {
     return (chunks + 1) * sizeof(uint64_t) + chunks * (sizeof(float2) + 32 * sizeof(float));
 }
 
+constexpr int kMostDynamic = 64 * 1024;  // chunk_bytes(256 + 16) is 43 KB
+
 template <int DT, int TX> cudaError_t launch_sample_rows(SampleArgs a, cudaStream_t s) {
     plan_chunks(&a, DType<DT>::bytes, TX / 32);
     const size_t smem = chunk_bytes(a.chunks_per_warp * (TX / 32));
     auto kernel = sample_kernel<DT, TX>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    // (The same value in every call: calls of other threads do not lower it in between.)
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostDynamic);
     if (e != cudaSuccess) return e;
     return launch_pdl_smem(kernel, dim3(static_cast<unsigned>(a.B)), dim3(TX), smem, s, a);
 }
