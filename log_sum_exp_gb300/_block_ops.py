@@ -60,28 +60,30 @@ class ResidualNormGrads(NamedTuple):
 
 
 def _norm_operands(x, y, weight, post_weight, gate):
-    """Checks; (T, D, x's stride, y's stride, gate's kind and stride, weights' type)."""
+    """Checks; (T, D, x's type and stride, y's stride, gate's kind and stride, weights' type)."""
     torch = _torch()
     if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor")
-    _dtype_name(x)
+    dt = DTYPES[_dtype_name(x)]
     T, D, stride = _matrix(x, "x")
+    device, wdtype = x.device, weight.dtype
     if y is None and (post_weight is not None or gate is not None):
         raise ValueError("post_weight and gate need y")
     y_stride = D if y is None else _same_rows(y, "y", x)
-    if weight.dtype not in (x.dtype, torch.float32):
+    wdt = dt if wdtype == x.dtype else 0
+    if not wdt and wdtype != torch.float32:
         raise ValueError("weight must have x's dtype or float32")
-    _need_vector(weight, "weight", weight.dtype, D, x.device)
+    _need_vector(weight, "weight", wdtype, D, device)
     if post_weight is not None:
-        _need_vector(post_weight, "post_weight", weight.dtype, D, x.device)
+        _need_vector(post_weight, "post_weight", wdtype, D, device)
     kind, gate_stride = "none", D
     if gate is not None and gate.dim() == 1:
         kind = "channel"
-        _need_vector(gate, "gate", weight.dtype, D, x.device)
+        _need_vector(gate, "gate", wdtype, D, device)
     elif gate is not None:
         kind = "element"
         gate_stride = _same_rows(gate, "gate", x)
-    return T, D, stride, y_stride, GATES[kind], gate_stride, DTYPES[_dtype_name(weight)]
+    return T, D, dt, stride, y_stride, GATES[kind], gate_stride, wdt
 
 
 def lse_residual_norm(x, y, weight, post_weight=None, gate=None, scale=1.0, eps=1e-6, h=None, out=None,
@@ -103,26 +105,24 @@ def lse_residual_norm(x, y, weight, post_weight=None, gate=None, scale=1.0, eps=
     T, D, *rest = _norm_operands(x, y, weight, post_weight, gate)
     if y is None and h is not None:
         raise ValueError("without y there is no h to write")
-    for t, name in ((h, "h"), (out, "out")):
-        if t is not None:
-            _same_rows(t, name, x)
-    return _call(_norm_call, (torch, x, y, weight, post_weight, gate, scale, eps, h, out, T, D, *rest,
-                              stream, x.device))
+    h_stride = D if h is None else _same_rows(h, "h", x)
+    out_stride = D if out is None else _same_rows(out, "out", x)
+    return _call(_norm_call, (torch, x, y, weight, post_weight, gate, scale, eps, h, h_stride, out, out_stride, T, D,
+                              *rest, stream, x.device))
 
 
-def _norm_call(torch, x, y, weight, post_weight, gate, scale, eps, h, out, T, D, x_stride, y_stride, kind,
-               gate_stride, wdt, stream, device):
+def _norm_call(torch, x, y, weight, post_weight, gate, scale, eps, h, h_stride, out, out_stride, T, D, dt, x_stride,
+               y_stride, kind, gate_stride, wdt, stream, device):
     if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        out = torch.empty((T, D), dtype=x.dtype, device=device)
     if y is not None and h is None:
-        h = torch.empty_like(x, memory_format=torch.contiguous_format)
+        h = torch.empty((T, D), dtype=x.dtype, device=device)
     rstd = torch.empty(T, dtype=torch.float32, device=device)
     post_rstd = torch.empty_like(rstd) if post_weight is not None else None
     _check(load().lse_residual_norm(
-        x.data_ptr(), DTYPES[_dtype_name(x)], T, D, x_stride, _pointer(y), y_stride, _pointer(gate), kind,
-        gate_stride, _pointer(post_weight), weight.data_ptr(), wdt, scale, eps, _pointer(h),
-        D if h is None else _matrix(h, "h")[2], out.data_ptr(), _matrix(out, "out")[2], rstd.data_ptr(),
-        _pointer(post_rstd), _stream_handle(stream, device)), "lse_residual_norm")
+        x.data_ptr(), dt, T, D, x_stride, _pointer(y), y_stride, _pointer(gate), kind, gate_stride,
+        _pointer(post_weight), weight.data_ptr(), wdt, scale, eps, _pointer(h), h_stride, out.data_ptr(), out_stride,
+        rstd.data_ptr(), _pointer(post_rstd), _stream_handle(stream, device)), "lse_residual_norm")
     return ResidualNorm(x if y is None else h, out, rstd, post_rstd)
 
 
@@ -130,7 +130,8 @@ def lse_residual_norm_backward(grad_out, grad_h, x, y, stats: ResidualNorm, weig
                                scale=1.0, weights=True, stream=None) -> ResidualNormGrads:
     """The gradients of ``lse_residual_norm`` from those of ``out`` and ``h`` (``grad_h``
     None: zeros).  ``stats`` is the forward's result (``rstd`` and ``post_rstd`` of it
-    are used); x, y, the weights, gate and scale are the forward's.  ``weights`` False
+    are used); x, y, the weights, gate and scale are the forward's (with the values that they
+    had before it: not an x that it wrote ``h`` over).  ``weights`` False
     leaves out the sums over rows (of weight, post_weight and a [D] gate).  A repeated
     call gives equal bits.
     """
@@ -149,7 +150,7 @@ def lse_residual_norm_backward(grad_out, grad_h, x, y, stats: ResidualNorm, weig
 
 
 def _norm_backward_call(torch, grad_out, go_stride, grad_h, gh_stride, x, y, stats, weight, post_weight, gate, scale,
-                        weights, T, D, x_stride, y_stride, kind, gate_stride, wdt, stream, device):
+                        weights, T, D, dt, x_stride, y_stride, kind, gate_stride, wdt, stream, device):
     def like(t, wanted=True):
         return None if t is None or not wanted else torch.empty_like(t, memory_format=torch.contiguous_format)
 
@@ -157,9 +158,8 @@ def _norm_backward_call(torch, grad_out, go_stride, grad_h, gh_stride, x, y, sta
     dw, dpost = like(weight, weights), like(post_weight, weights)
     dgate = like(gate, weights or kind == GATES["element"])
     _check(load().lse_residual_norm_backward(
-        grad_out.data_ptr(), go_stride, _pointer(grad_h), gh_stride, x.data_ptr(), DTYPES[_dtype_name(x)], T, D,
-        x_stride, _pointer(y), y_stride, _pointer(gate), kind, gate_stride, _pointer(post_weight),
-        weight.data_ptr(), wdt, scale, stats.rstd.data_ptr(),
+        grad_out.data_ptr(), go_stride, _pointer(grad_h), gh_stride, x.data_ptr(), dt, T, D, x_stride, _pointer(y),
+        y_stride, _pointer(gate), kind, gate_stride, _pointer(post_weight), weight.data_ptr(), wdt, scale, stats.rstd.data_ptr(),
         _pointer(stats.post_rstd) if post_weight is not None else None, dx.data_ptr(), D, _pointer(dy), D,
         _pointer(dgate), D, _pointer(dpost), _pointer(dw), _stream_handle(stream, device)),
         "lse_residual_norm_backward")

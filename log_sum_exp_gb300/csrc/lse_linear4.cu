@@ -176,15 +176,22 @@ template <int DT> __global__ void __launch_bounds__(kFormThreads) quantize4_kern
                 const float inv = __fdividef(1.0f, s), magic = 12582920.0f;  // 1.5 2^23 + 8
                 float far = 0.0f;
                 w = 0;
+                const uint64_t inv2 = f2_pack(inv, inv), minus_s2 = f2_pack(-s, -s), magic2 = f2_pack(magic, magic);
 #pragma unroll
                 for (int i = 0; i < 8; i += 2) {
-                    float t0 = f[v][i] * inv, t1 = f[v][i + 1] * inv;
+                    const uint64_t x = f2_pack(f[v][i], f[v][i + 1]);
+                    uint64_t t = f2_mul(x, inv2);
                     if constexpr (DT != kF32) {
-                        t0 = fmaf(fmaf(-t0, s, f[v][i]), inv, t0);
-                        t1 = fmaf(fmaf(-t1, s, f[v][i + 1]), inv, t1);
+                        t = f2_fma(f2_fma(t, minus_s2, x), inv2, t);
                     }
-                    const float k0 = t0 + magic, k1 = t1 + magic;
-                    if constexpr (DT == kF32) far = fmaxf(far, fmaxf(fabsf(t0 - (k0 - magic)), fabsf(t1 - (k1 - magic))));
+                    const uint64_t k = f2_add(t, magic2);
+                    float k0, k1;
+                    f2_unpack(k, k0, k1);
+                    if constexpr (DT == kF32) {
+                        float d0, d1;
+                        f2_unpack(f2_sub(t, f2_sub(k, magic2)), d0, d1);
+                        far = fmaxf(far, fmaxf(fabsf(d0), fabsf(d1)));
+                    }
                     const uint32_t p = __byte_perm(__float_as_uint(k0), __float_as_uint(k1), 0x5410);
                     w |= (p & 0x000f000fu) << (2 * i);
                 }

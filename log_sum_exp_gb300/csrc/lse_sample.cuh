@@ -18,10 +18,14 @@
 // the product and a cubic for 2^r - 1; off by at most about 2^-30 of itself.  Sums of whole
 // numbers do not depend on their order.  That takes about 40 instructions, four times what the
 // memory's rate leaves for a bf16 element, so passes over a row use fast weights, of ex2 with the
-// rounding error of its argument carried along.  (ex2.approx is off by at most 1.45e-7, measured
-// over every f32 in [-32, 0); two sums that are compared may be off by twice that and by
-// the roundings of their additions, fast_error() in all.)  Where a comparison is closer than that,
-// about one row in twenty of 128256 columns, the row is done again with exact weights.
+// rounding error of its argument carried along.  What is compared is always a part of a sum with
+// u (or top_p) times the whole, and their difference is off by 1 - u times the sum of w e over the
+// part, less u times that over the rest, with e a weight's relative error.  An error that all
+// weights share cancels; where e lies within h of its middle the difference is off by at most
+// 2 u (1 - u) h of the whole, h / 2.  ex2.approx gave e from -1.44e-7 to 1.05e-7 over every f32 in
+// [-32, 0), so that is 6.3e-8; the additions' roundings are independent of each other and far
+// smaller.  fast_error() is twice that.  Where a comparison is closer, about one row of 128256
+// columns in fifty, the row is done again with exact weights.
 //
 // Threshold.  Every lane's maximum in every chunk is kept in shared memory.  They bound the
 // threshold from below (the k-th largest of them is at most the k-th largest element; the same
@@ -54,8 +58,8 @@ constexpr int kChunk = 128;  // vectors of a chunk, at least
 // Histogram bins and list entries of a row's threads.
 template <int TX> __host__ __device__ constexpr int bins_log2() { return TX == 32 ? 7 : 10; }
 template <int TX> __host__ __device__ constexpr int list_size() { return TX == 32 ? 64 : 2048; }
-// The part of a sum that two fast sums may be off by when they are compared.
-__device__ __forceinline__ uint64_t fast_error(uint64_t total) { return (total >> 22) + (total >> 23) + 1; }  // 3.6e-7
+// What a comparison of a part of a fast sum with a share of the whole may be off by.
+__device__ __forceinline__ uint64_t fast_error(uint64_t total) { return (total >> 23) + 1; }  // 1.2e-7
 constexpr float kInf = __builtin_inff();
 
 // 2^(j / 64) in units of 2^-30, rounded to nearest.
@@ -1714,35 +1718,48 @@ template <int DT, int V> struct ShortRow {
                 ohi = order_bits(hi);
                 olo = max(olo, order_bits(lo));
             }
+        } else if (by_mass && low < m) {
+            olo = max(olo, order_bits(low));
         }
         // Bisection to at most 32 elements in (lo, hi] that hold the last kept one: values for
         // sums, whose relevant elements lie within a few octaves; bits of ordered values for counts.
-        bool settled = false;
-        for (int step = 0; step < 64 && !settled; ++step) {
-            const float lo = order_value(olo), hi = order_value(ohi);
-            uint32_t inside = 0;
+        const auto beyond = [&](float v) -> int {  // elements above v
+            int c = 0;
 #pragma unroll
-            for (int j = 0; j < M; ++j) inside += (!(x(j) <= lo) && x(j) <= hi && (!by_mass || w[j] > 0.0f)) ? 1u : 0u;
-            inside = __reduce_add_sync(0xffffffffu, inside);
-            if (inside <= 32) {
-                settled = true;
-                break;
-            }
+            for (int j = 0; j < M; ++j) c += !(x(j) <= v) ? 1 : 0;
+            return __reduce_add_sync(0xffffffffu, c);
+        };
+        int from_lo = beyond(order_value(olo)), from_hi = beyond(order_value(ohi));
+        bool settled = from_lo - from_hi <= 32;
+        for (int step = 0; step < 64 && !settled; ++step) {
             if (ohi - olo < 2) return false;  // more than 32 equal values
             uint32_t mid = olo + (ohi - olo) / 2;
             if (by_mass) {
-                const uint32_t v = order_bits(0.5f * lo + 0.5f * hi);
+                const uint32_t v = order_bits(0.5f * order_value(olo) + 0.5f * order_value(ohi));
                 if (v > olo && v < ohi) mid = v;
             }
             const float pivot = order_value(mid);
             float s = 0.0f;
+            int c = 0;
 #pragma unroll
-            for (int j = 0; j < M; ++j) s += x(j) > pivot ? (by_mass ? w[j] : 1.0f) : 0.0f;
+            for (int j = 0; j < M; ++j)
+                if (x(j) > pivot) s += by_mass ? w[j] : 1.0f, ++c;
+            if (by_mass) {
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            }
+            c = __reduce_add_sync(0xffffffffu, c);
+            if (!by_mass) s = static_cast<float>(c);
             if (by_mass && fabsf(s - need) <= err) return false;
-            if (s >= need) olo = mid;
-            else ohi = mid, above = s;
+            if (s >= need) {
+                olo = mid;
+                from_lo = c;
+            } else {
+                ohi = mid;
+                above = s;
+                from_hi = c;
+            }
+            settled = from_lo - from_hi <= 32;
         }
         if (!settled) return false;
         // One element per lane, in order.
@@ -1751,7 +1768,7 @@ template <int DT, int V> struct ShortRow {
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < M; ++j) {
-            const bool in = !(x(j) <= lo) && x(j) <= hi && (!by_mass || w[j] > 0.0f) && column(j) >= 0;
+            const bool in = !(x(j) <= lo) && x(j) <= hi && (by_mass ? w[j] > 0.0f : column(j) >= 0);
             const uint32_t b = __ballot_sync(0xffffffffu, in);
             if (in) keys[at + __popc(b & ((1u << lane) - 1u))] = topk_key(x(j), static_cast<uint32_t>(column(j)));
             at += __popc(b);
