@@ -698,11 +698,12 @@ typedef struct {
  *                draws the last kept column.
  *   settings     HOST struct, read during the call.
  *   token        B int64.  logprob: B floats, or NULL.
- * Sums are taken in whole numbers of 2^-44 (rows of more than 2^18 columns: as many bits
- * fewer as N takes more), each w off by at most about 2^-30 of itself, so results do not
- * depend on the order of sums: a repeated call gives equal bits, and the token is that of
- * exact arithmetic unless a border of it lies within about 1e-9 of u.  A column whose w is
- * below 2^-45 is not drawn.  Temperature 0 draws the first of the largest elements with
+ * Where f32 sums decide a comparison by more than their error they are used; otherwise
+ * sums of weights that are off by at most about 2^-30 of themselves and held to 2^-44 (rows
+ * of more than 2^18 columns: as many bits fewer as N takes more).  So the token is that of
+ * exact arithmetic unless a border of it lies within about 1e-9 of u (or a cut's of top_p),
+ * and a repeated call gives equal bits.  logprob is good to a few f32 roundings of its two
+ * terms.  A column whose w is below 2^-45 is not drawn.  Temperature 0 draws the first of the largest elements with
  * logprob 0, whatever the other settings are.
  * A row that is no distribution (it holds a NaN or +inf, or nothing but -inf, or N == 0),
  * or whose own temperature is outside 0 .. 1e20 or whose top_p or min_p is NaN, gets the

@@ -2,15 +2,21 @@
 //
 //     y[t, n] = sum_g s[n, g] sum_{k in g} x[t, k] q[n, k]
 //
-// Bound by reading the codes: half a byte per weight leaves about three
-// instructions per weight and lane at the memory's rate, so the weights do not go through
-// scalar arithmetic.  A pair of nibbles becomes a pair of 16-bit floats, exactly q, by an or
-// with the bits of 1024 (bf16: 128) and a subtraction, and mma.sync multiplies 16 rows x 16
-// columns with 8 tokens, summing in f32.  The scale multiplies a group's f32 sum, so nothing
-// but the result is rounded to 16 bits.  f32 tokens are cut into three bf16 parts (8 + 8 + 8
-// bits, exact) that are three more columns of the product.  tcgen05 would need the
-// weights' floats in shared memory, four times the codes' bytes through it and back, to win
-// a product that takes less than a tenth of the time here; the tokens are few.
+// Bound by reading the codes, and here by instructions: half a byte per weight leaves about two
+// and a half per weight and lane at the memory's rate.  So the weights do not go through scalar
+// arithmetic.  A pair of nibbles becomes a pair of 16-bit floats, exactly q, by an or with the
+// bits of 1024 (bf16: 128) and a subtraction, and mma.sync multiplies 16 rows x 16 columns with 8
+// tokens, summing in f32.  The scale multiplies a group's f32 sum, so nothing but the result is
+// rounded to 16 bits.  f32 tokens are cut into three bf16 parts (8 + 8 + 8 bits, exact) that are
+// three more columns of the product.
+//
+// Measured: one bf16 token x 128256 x 2048 39 us, 3.4 TB/s (the same loads without the products 26
+// us); 16 f16 tokens x 32000 x 4096 34 us.  The matrix pipe is busy for 14 % and 21 % of that, the
+// logic pipe for 50 % and 34 %: making floats of codes is what counts, so a matrix instruction
+// of a higher rate (tcgen05, which would also take the floats through shared memory or tensor
+// memory) has little to win before that does.  Deeper prefetching (6 blocks instead of 4: 41 us) and two
+// tiles per warp (46 us) were slower for one token; more warps sharing a tile's columns, which
+// adds barriers, too (53 us).
 #pragma once
 
 #include <cstdint>

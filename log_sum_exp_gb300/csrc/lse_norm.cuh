@@ -21,6 +21,12 @@
 // registers; a second kernel adds the CTAs' parts in their order, so a repeated call gives
 // equal bits.  For a gate of one value per column, dw1 = g S and dgate = w1 S share the sum
 // S = sum s G y r1.
+//
+// Measured: 16384 x 4096 bf16 with post norm and a gate per column 86 us (6.2 TB/s), gradient 159
+// us (5.1 TB/s); 5000 x 1001 f32 with a gate per element 18 us (5.6 TB/s) and 33 us (4.8 TB/s).  The
+// gradient holds 8 columns' sums, factors and terms of 16-bit rows in 116 to 128 registers, so an SM
+// has 512 threads of it: loading the next row during a row's sums took it from 313 to 272 us, the
+// columns' factors in registers to 204, rows without edge checks to 159.
 #pragma once
 
 #include <cstdint>
