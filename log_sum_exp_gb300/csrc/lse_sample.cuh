@@ -472,36 +472,51 @@ template <int DT, int TX> struct Sampler {
     // chunks' sums name (they may be approximate).
     template <class F>
     __device__ __forceinline__ bool locate(uint64_t target, bool clamp, F&& f, int* col, float* value, uint64_t* before, uint64_t* with) {
-        if (tid == 0) sh.r32[1] = 0;
-        row_sync<TX>();
-        for (int c = tid; c < chunks; c += TX)
-            if (sums[c] <= target && target < sums[c + 1]) sh.r32[0] = c, sh.r32[1] = 1;
-        row_sync<TX>();
-        const bool any = sh.r32[1] != 0;
-        const int c = sh.r32[0];
-        row_sync<TX>();
-        if (tid == 0) sh.r32[1] = 0;
-        if (!any) {
+        int c, s0, s1;
+        uint64_t own, first, rest;
+        bool back = false;
+        // (One round, unless `clamp` meets chunks of nothing but elements below 2^-45 of the largest:
+        // each alone weighs nothing, while their exact sum may.  The next chunk that weighs takes
+        // their place, or the one before if there is none behind.)
+        for (int round = 0;; ++round) {
+            if (tid == 0) sh.r32[1] = 0;
             row_sync<TX>();
-            return false;
-        }
-        const int b = chunk_begin(c), n = chunk_end(c) - b;
-        const int per = (n + TX - 1) / TX, s0 = b + tid * per, s1 = min(s0 + per, b + n);
-        uint64_t own = 0;
-        for (int s = s0; s < s1; ++s) {
-            uint32_t w[4];
-            load(s, w);
-            mask(s, w);
+            for (int i = tid; i < chunks; i += TX)
+                if (sums[i] <= target && target < sums[i + 1]) sh.r32[0] = i, sh.r32[1] = 1;
+            row_sync<TX>();
+            const bool any = sh.r32[1] != 0;
+            c = sh.r32[0];
+            row_sync<TX>();
+            if (tid == 0) sh.r32[1] = 0;
+            if (!any) {
+                row_sync<TX>();
+                return false;
+            }
+            const int b = chunk_begin(c), n = chunk_end(c) - b;
+            const int per = (n + TX - 1) / TX;
+            s0 = b + tid * per;
+            s1 = min(s0 + per, b + n);
+            own = 0;
+            for (int s = s0; s < s1; ++s) {
+                uint32_t w[4];
+                load(s, w);
+                mask(s, w);
 #pragma unroll
-            for (int e = 0; e < E; ++e) own += f(word_elem<DT>(w, e), column(s, e));
-        }
-        const uint64_t first = row_before(own);
-        // (Chunks' sums are good to about 2^-32; what is left of the target beyond the chunk's
-        // own sum by that is its last element's.)
-        uint64_t rest = target - sums[c];
-        if (clamp) {
+                for (int e = 0; e < E; ++e) own += f(word_elem<DT>(w, e), column(s, e));
+            }
+            first = row_before(own);
+            // (Chunks' sums are good to about 2^-32; what is left of the target beyond the chunk's
+            // own sum by that is its last element's.)
+            rest = target - sums[c];
+            if (!clamp) break;
             const uint64_t all = row_sum(own);
-            if (rest >= all && all > 0) rest = all - 1;
+            if (all > 0) {
+                if (back || rest >= all) rest = all - 1;
+                break;
+            }
+            if (!back && sums[c + 1] >= sums[chunks]) back = true;
+            if (round > 2 * chunks || (back && sums[c] == 0)) break;
+            target = back ? sums[c] - 1 : sums[c + 1];
         }
         row_sync<TX>();
         if (first <= rest && rest < first + own) {
@@ -1263,11 +1278,15 @@ template <int DT, int TX> struct Sampler {
         bool tentative = false;
         *sure = err == 0;
         *listed = 0;
-        for (int round = 0; round < 40; ++round) {  // (every histogram narrows the range: a few rounds)
+        // (Each round leaves half of the ordered bits of its range or a quarter of its length: a few
+        // rounds as a rule, and less than 128 from any range.)
+        for (int round = 0; round < 128; ++round) {
             Range at;
             const bool sampled = round == 0 && by_mass && total > need && chunks >= 16 && guess(total - need, base_key != 0, lo, &at);
             if (!sampled && !bracket(by_mass, left, err, base_key, lo, guide, hi, &at)) {
-                if (!tentative) return base_key;
+                // (Exact sums and the weights of single elements differ by 2^-30, so that a range can
+                // fall short of what it has to reach by that: all of it is kept then.)
+                if (!tentative) return err == 0 && by_mass ? max(base_key, static_cast<uint64_t>(lo) << 32) : base_key;
                 tentative = false;  // the sample was wrong
                 lo = lowest, guide = first_guide, hi = order_bits(m), left = need;
                 continue;
@@ -1289,10 +1308,42 @@ template <int DT, int TX> struct Sampler {
                 hi = most;
                 continue;
             }
-            tentative = false;
-            if (n <= kList || above >= need) return base_key;  // (only where err is wrong, or all of them do not reach)
-            left = need - above;
-            if (err && (least == most || (least == lo && most == hi))) return base_key;  // not sure
+            if (tentative && (n <= kList || above >= need)) {  // the sample was wrong
+                tentative = false;
+                lo = lowest, guide = first_guide, hi = order_bits(m), left = need;
+                continue;
+            }
+            if (n <= kList || above >= need) {
+                if (err || !by_mass) return base_key;  // (err is too small, or all of them do not reach)
+                // Off by the 2^-30 again: the range's first element, or all of it.
+                if (n <= kList) {
+                    const uint64_t in = list_sum(n, base_key);
+                    if (in == 0) return max(base_key, (static_cast<uint64_t>(order_bits(at.hi)) + 1) << 32);
+                    const uint64_t reached = min(max(need, above + 1), above + in);
+                    if (!list_cut(true, n, base_key, above, reached, &k, &under, &with)) return base_key;
+                    *listed = n;
+                    return k;
+                }
+            }
+            left = need > above ? need - above : 1;
+            const float was = order_value(hi) - order_value(lo), now = order_value(most) - order_value(least);
+            const bool poor = most - least > (hi - lo) / 2 && !(was < kInf && now <= 0.25f * was);
+            if (err && (least == most || poor)) return base_key;  // not sure
+            if (by_mass && poor && least < most) {
+                // Heavy equal values: the widths of bins leave more open than lies between the sums.
+                const uint32_t mid = least + (most - least) / 2;
+                const float pivot = order_value(mid);
+                const uint64_t half = exact_chunks(pivot, [=](float v, int) -> bool { return v > pivot; });
+                if (half >= need) {
+                    lo = guide = mid + 1;
+                    hi = most;
+                } else {
+                    lo = guide = least;
+                    hi = mid;
+                    left = need - half;
+                }
+                continue;
+            }
             if (least == most) {  // equal values: a count of columns
                 const uint64_t one = by_mass ? weight(order_value(least)) : 1;
                 uint64_t count = one ? (left + one - 1) / one : 1;
@@ -1300,6 +1351,11 @@ template <int DT, int TX> struct Sampler {
                     return order_bits(v) == least && static_cast<unsigned>(col) < static_cast<unsigned>(N) && key(v, col) >= base_key;
                 };
                 const uint64_t all = count_chunks(order_value(least), same);
+                if (count > all && tentative) {  // the sample was wrong
+                    tentative = false;
+                    lo = lowest, guide = first_guide, hi = order_bits(m), left = need;
+                    continue;
+                }
                 if (all == 0) return base_key;
                 if (count > all) count = all;
                 int col = 0;
@@ -1483,7 +1539,7 @@ __device__ void sample_row(SampleShared<TX>& sh, const uint32_t* powers, unsigne
                     const uint64_t mass = mass_needed(g.use_k ? r.list_sum(n, base) : total), e = g.use_k ? 0 : err;
                     uint64_t k;
                     const bool found = r.list_cut(true, n, base, 0, mass, &k, &under, &with);
-                    if (found) cut = k;
+                    cut = found ? k : max(cut, static_cast<uint64_t>(lo) << 32);
                     // (Not reached: the cut lies below what min_p keeps.)
                     if (e == 0 || (found ? with - mass > e && mass - under > e : g.use_min)) break;
                     total = r.exact_chunks(-kInf, [](float, int) -> bool { return true; });  // too close to tell
@@ -1535,7 +1591,10 @@ __device__ void sample_row(SampleShared<TX>& sh, const uint32_t* powers, unsigne
     float x = 0.0f;
     uint64_t before = 0, with = 0;
     if (threshold == 0) {  // nothing is cut off
-        if (!with_sums) total = r.exact_chunks(-kInf, [](float, int) -> bool { return true; });
+        if (!with_sums || g.use_p) {  // (the sums of chunks are not there, or select() has used their place)
+            total = r.exact_chunks(-kInf, [](float, int) -> bool { return true; });
+            err = 0;
+        }
         for (;;) {
             const uint64_t target = drawn(total);
             const bool found = r.locate(target, err == 0, all_weights, &col, &x, &before, &with);
@@ -1634,10 +1693,13 @@ template <int DT, int V> struct ShortRow {
     // rounding of x - m (2^-24 of |z|, at most 8 octaves where the mass is), and chains of
     // M + 10 additions.
     static constexpr float kError = 8e-7f + (M + 10) * 6e-8f;
+    // By halves: the largest weight passes through log M roundings instead of M.
+    template <int A, int L> __device__ __forceinline__ float part() const {
+        if constexpr (L == 1) return w[A];
+        else return part<A, L / 2>() + part<A + L / 2, L - L / 2>();
+    }
     __device__ __forceinline__ float sum() const {
-        float s = 0.0f;
-#pragma unroll
-        for (int j = 0; j < M; ++j) s += w[j];
+        float s = part<0, M>();
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         return s;

@@ -195,6 +195,56 @@ def test_equal_values(N):
         check(x, u, **s)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("N", [64, 230, 628, 1653, 4096, 8669, 21247, 70001])
+def test_few_distinct_values(dtype, N):
+    """Cuts that fall into runs of equal values, close to the run's end: more elements than any
+    list, and sums that differ by less than the bins of a histogram are wide."""
+    B = 10
+    g = torch.Generator().manual_seed(N)
+    x = torch.empty((B, N))
+    for b, values in enumerate([2, 3, 5, 40]):
+        x[b] = torch.randint(0, values, (N,), generator=g) * 3.0
+    x[4] = torch.randint(0, 3, (N,), generator=g) * 0.01
+    x[5], x[6], x[7], x[8] = -20.0, -20.0, 100.0, 0.0
+    x[5, N // 3], x[6, N // 2], x[6, 7], x[7, 9] = 0.5, -2.4375, -2.375, 50.0
+    x[8, N // 4: N // 4 + 40] = 3.0
+    x[9] = torch.where(torch.rand(N, generator=g) < 0.6, -math.inf, x[1])
+    x = x.to(DT[dtype]).cuda()
+    u = torch.rand(B, generator=g).cuda()
+    for s in (dict(top_p=0.95), dict(top_p=0.99, temperature=1.3), dict(top_p=0.999999), dict(top_p=0.95, min_p=1e-4),
+              dict(top_k=N - 1, top_p=0.95), dict(top_k=3, top_p=0.999999), dict(top_p=0.7)):
+        check(x, u, **s)
+
+
+@pytest.mark.parametrize("N,k", [(125, 124), (700, 600), (5000, 3000)])
+def test_nearly_equal_weights(N, k):
+    """At a temperature of 1e10 half of an even count of tokens is a border to 1e-9: one more or not."""
+    x, u = logits(6, N, "f16", N)
+    got = L.lse_sample(x, u, temperature=1e10, top_k=k, top_p=0.5)
+    assert (got.token >= 0).all()
+    kept = torch.exp(-got.logprob.double())
+    assert ((kept - k / 2 > -1e-2 * k / 2 / 50) & (kept - k / 2 < 1 + 1e-2 * k / 2 / 50)).all(), kept
+    for b in range(6):
+        order = torch.sort(x[b].double(), descending=True, stable=True).indices
+        assert int(got.token[b]) in order[: k // 2 + 1].tolist()
+
+
+@pytest.mark.parametrize("N", [300, 5000, 70000])
+def test_numbers_of_zero_and_light_columns(N):
+    """u = 0 draws the first column that weighs 2^-45 or more, behind many that weigh less."""
+    x = torch.full((3, N), -31.5, device="cuda")  # 2^-45.4
+    x[0, N - 1] = 0.0
+    x[1, N // 2] = -10.0
+    x[1, N - 1] = 0.0
+    x[2, 0] = 0.0
+    u = torch.tensor([0.0, 0.0, 1.0 - 2.0 ** -24], device="cuda")
+    for s in (dict(), dict(temperature=0.9), dict(top_k=N - 1)):
+        got = L.lse_sample(x, u, **s)
+        assert got.token.tolist() == [N - 1, N // 2, 0], got.token
+        assert (got.logprob <= 0).all()
+
+
 def test_numbers_outside_the_unit_interval():
     x, _ = logits(6, 500, "f32", 2)
     u = torch.tensor([-1.0, math.nan, 1.0, 2.0, math.inf, 0.0], device="cuda")
