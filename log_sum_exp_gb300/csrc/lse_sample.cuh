@@ -34,12 +34,14 @@
 // order and cut, put in column order and drawn from, and the row is not read again.  Otherwise
 // (flat rows) a histogram of counts over the values brackets the threshold, since within a bin all
 // weights are within a few percent of each other; the bracket's elements go to the list, what
-// lies above is summed, and one more pass sums what is kept by chunks.
+// lies above is summed, and one more pass sums what is kept by chunks.  A range that a histogram hardly
+// narrows (a run of equal values so heavy that the widths of bins hide where the sum passes) is
+// bisected, a pass for each half.
 //
-// Measured (us): 2048 x 128256 bf16, nothing cut off 218 (2.4 TB/s; the pass alone, without weights,
+// Measured (us): 2048 x 128256 bf16, nothing cut off 216 (2.4 TB/s; the pass alone, without weights,
 // 126, bound by loads at 42 % of the warps), top_k 50 and top_p 0.95 275, top_p 0.9 of rows from peaked
 // to flat 2750 (instructions: three to four passes of 10 to 15 per element); one such row 15, 26 and
-// 69; 65536 x 261 f32 top_p 0.9 168 (1960 instructions per row).  Counters of several
+// 69; 65536 x 261 f32 top_p 0.9 174 (1960 instructions per row).  Counters of several
 // threads are the slowest part: 26 ns for each addition with a result to one of them, so places in a
 // list are handed out per warp; histograms by the bits of f32, which have two bins for all
 // values within a factor of two, took 11 ms where bins linear in the value take 3.
