@@ -604,7 +604,9 @@ LSE_API lse_status lse_residual_norm(const void *x, lse_dtype dtype, int64_t T, 
  * Each output may be NULL (not wanted); none may overlap an input.  Sums over rows
  * are taken in f32, row after row within a CTA and CTA by CTA, and rounded once; a
  * repeated call gives equal bits (the rows of a CTA follow T, D, the alignment of
- * the rows and the GPU's number of SMs).  T == 0 gives zeros there.  Takes
+ * the rows and the GPU's number of SMs).  T == 0 gives zeros there.  Computed from
+ * the normalised rows h rstd and y post_rstd, so rows of any magnitude for which the
+ * forward's sums of squares are f32 numbers keep all terms.  Takes
  * stream-ordered scratch when a sum over rows is asked for.
  */
 LSE_API lse_status lse_residual_norm_backward(

@@ -9,18 +9,20 @@
 // although sum h^2 could be written in sums that do not need r1: where x and s g a cancel,
 // those lose all their digits.
 //
-// Gradient, with G what arrives at h from both sides:
+// Gradient, with G what arrives at h from both sides and the normalised rows u = h r2, v = y r1:
 //
-//     n = w dout     G = dh + r2 n - h r2^3/D sum(n h)     dx = G
-//     e = s g w1 G   dy = r1 e - y r1^3/D sum(e y)         dgate = s a G
-//     dw = sum over rows of dout h r2                      dw1 = the same of s g G y r1
+//     n = w dout     G = dh + r2 n - u r2/D sum(n u)       dx = G
+//     e = s g w1 G   dy = r1 (e - v/D sum(e v))            dgate = s w1 v G  (w1 absent: s y G)
+//     dw = sum over rows of dout u                         dw1 = the same of s g v G
 //
-// sum(e y) needs G, which needs sum(n h); with q = s g w1 y it is sum q (dh + r2 n) -
-// r2^3/D sum(n h) sum(q h), so one reduction per row carries all three sums.
+// sum(e v) needs G, which needs sum(n u); with q = s g w1 v it is sum q (dh + r2 n) -
+// r2/D sum(n u) sum(q u), so one reduction per row carries all three sums.  The normalised rows
+// are of magnitude 1 whatever the rows are; powers of r1 and r2 would leave the f32 range long
+// before any result does (r2^3 / D is 0 for rows of an rms of 1e14).
 // CTAs walk over rows and keep the sums over rows for the columns of each thread in
 // registers; a second kernel adds the CTAs' parts in their order, so a repeated call gives
 // equal bits.  For a gate of one value per column, dw1 = g S and dgate = w1 S share the sum
-// S = sum s G y r1.
+// S = sum s G v.
 //
 // Measured: 16384 x 4096 bf16 with post norm and a gate per column 86 us (6.2 TB/s), gradient 159
 // us (5.1 TB/s); 5000 x 1001 f32 with a gate per element 18 us (5.6 TB/s) and 33 us (4.8 TB/s).  The
@@ -298,10 +300,10 @@ __global__ void __launch_bounds__(norm_threads<TX>()) norm_kernel(NormArgs a) {
 // Gradient.  The grid is a multiple of 8, so all rows of a group lie at the same offset
 // from a 16-byte boundary and a thread's slots are the same columns in each.
 // ---------------------------------------------------------------------------
-// What a slot adds to a row's sums: h, the gradient that arrives at it before the norm's
-// sum is taken off, and q = s g w1 y.
+// What a slot adds to a row's sums: u = h r2, the gradient that arrives at h before the norm's
+// sum is taken off, and q = s g w1 v.
 template <int DT> struct GradSlot {
-    float h[Slot<DT>::E], gh[Slot<DT>::E], q[Slot<DT>::E];
+    float u[Slot<DT>::E], gh[Slot<DT>::E], q[Slot<DT>::E];
     Slot<DT> y, gate;
 };
 struct GradRow {
@@ -356,22 +358,23 @@ __device__ __forceinline__ void grad_slot(const GradRow& r, const GradWords<DT>&
     float f[E];
     g.y = words.y;
     g.gate = words.gate;
-    slot_floats<DT>(words.x, g.h);
+    slot_floats<DT>(words.x, g.u);
     slot_floats<DT>(words.dn, n);
     slot_floats<DT>(words.dh, g.gh);
     slot_floats<DT>(words.y, f);
     if (r.gate) {
         slot_floats<DT>(words.gate, g.q);
 #pragma unroll
-        for (int i = 0; i < E; ++i) g.q[i] *= k.c[i] * f[i];
+        for (int i = 0; i < E; ++i) g.q[i] *= k.c[i];
     } else {
 #pragma unroll
-        for (int i = 0; i < E; ++i) g.q[i] = k.c[i] * f[i];
+        for (int i = 0; i < E; ++i) g.q[i] = k.c[i];
     }
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-        g.h[i] = fmaf(g.q[i], r.r1, g.h[i]);
-        if (sw) (*sw)[i] = fmaf(n[i] * r.r2, g.h[i], (*sw)[i]);
+        g.q[i] *= f[i] * r.r1;
+        g.u[i] = (g.u[i] + g.q[i]) * r.r2;
+        if (sw) (*sw)[i] = fmaf(n[i], g.u[i], (*sw)[i]);
         n[i] *= k.w[i];
         g.gh[i] = fmaf(n[i], r.r2, g.gh[i]);
     }
@@ -438,9 +441,9 @@ __global__ void __launch_bounds__(norm_threads<TX>(), backward_ctas(norm_threads
             grad_slot<DT>(r, words, columns, g, n, &sw[j]);
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                s[0] = fmaf(n[i], g.h[i], s[0]);
+                s[0] = fmaf(n[i], g.u[i], s[0]);
                 s[1] = fmaf(g.q[i], g.gh[i], s[1]);
-                s[2] = fmaf(g.q[i], g.h[i], s[2]);
+                s[2] = fmaf(g.q[i], g.u[i], s[2]);
             }
         }
         GradRow next;
@@ -450,8 +453,8 @@ __global__ void __launch_bounds__(norm_threads<TX>(), backward_ctas(norm_threads
             if (row + step - group < a.T) load_words<DT>(next, Columns<DT, TX, MODE>(0, t, off_e, next_D), next_D, words);
         }
         row_sums<TX, 3>(s, buf[turn]);
-        const float k2 = r.r2 * r.r2 * r.r2 * a.inv_d * s[0];
-        const float k1 = a.post ? r.r1 * r.r1 * r.r1 * a.inv_d * (s[1] - k2 * s[2]) : 0.0f;
+        const float k2 = s[0] * a.inv_d * r.r2;
+        const float k1 = a.post ? (s[1] - k2 * s[2]) * a.inv_d : 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const Columns<DT, TX, MODE> at(j, t, off_e, D);
@@ -466,18 +469,20 @@ __global__ void __launch_bounds__(norm_threads<TX>(), backward_ctas(norm_threads
             }
             slot_floats<DT>(g.y, f);
 #pragma unroll
-            for (int i = 0; i < E; ++i) g.gh[i] = fmaf(-g.h[i], k2, g.gh[i]);  // G
+            for (int i = 0; i < E; ++i) g.gh[i] = fmaf(-g.u[i], k2, g.gh[i]);  // G
             if (a.dx) store_slot<DT>(a.dx + row * a.dx_bytes, at, D, slot_of<DT>(g.gh));
             if (!r.y) continue;
             if (r.gate) slot_floats<DT>(g.gate, e);
+#pragma unroll
+            for (int i = 0; i < E; ++i) f[i] *= r.r1;  // v
             if (a.dy) {
 #pragma unroll
-                for (int i = 0; i < E; ++i) o[i] = fmaf((r.gate ? columns.c[i] * e[i] : columns.c[i]) * g.gh[i], r.r1, -f[i] * k1);
+                for (int i = 0; i < E; ++i) o[i] = fmaf(r.gate ? columns.c[i] * e[i] : columns.c[i], g.gh[i], -f[i] * k1) * r.r1;
                 store_slot<DT>(a.dy + row * a.dy_bytes, at, D, slot_of<DT>(o));
             }
-            // r1 y G: the sum that dw1 and the gate of a column share, but for the scale
+            // v G: the sum that dw1 and the gate of a column share, but for the scale
 #pragma unroll
-            for (int i = 0; i < E; ++i) f[i] *= g.gh[i] * r.r1;
+            for (int i = 0; i < E; ++i) f[i] *= g.gh[i];
             if (r.gate) {
                 if (a.dgate) {
 #pragma unroll
