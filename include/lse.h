@@ -581,7 +581,8 @@ typedef enum {
  *                stride); other overlaps are undefined.
  *   gate         NULL, D values, or T rows gate_stride apart.
  *   weight, post_weight   D values of weight_dtype, which is dtype or LSE_F32.
- *   rstd, post_rstd       T floats each, or NULL: for lse_residual_norm_backward.
+ *   rstd, post_rstd       T floats each, or NULL: for lse_residual_norm_backward.  With D == 0
+ *                nothing is written there.
  * T <= INT32_MAX; eps >= 0; scale finite.  NaN and infinities follow IEEE
  * arithmetic on the formulas, row by row.  A sum of squares beyond the f32 range
  * is infinite, so a row with magnitudes near 1e19 gives zeros.

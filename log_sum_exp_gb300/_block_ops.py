@@ -10,6 +10,7 @@ caller's part.
 from __future__ import annotations
 
 import ctypes
+import math
 from typing import NamedTuple, Optional
 
 from ._binding import (DTYPES, LseSampling, _check, _dtype_name, _on_device, _rows, _stream_handle,
@@ -99,7 +100,7 @@ def lse_residual_norm(x, y, weight, post_weight=None, gate=None, scale=1.0, eps=
     x's dtype or both of float32; ``gate`` is [D] of the weights' dtype or [T, D] of
     x's.  ``y`` None: ``out`` is the norm of x and ``h`` is x.  ``h`` and ``out`` may be
     given; ``h`` may be x itself and ``out`` may be y itself.  ``rstd`` and
-    ``post_rstd`` (float32 [T]) are for the gradient.
+    ``post_rstd`` (float32 [T]) are for the gradient (NaN for rows of no columns).
     """
     torch = _torch()
     T, D, *rest = _norm_operands(x, y, weight, post_weight, gate)
@@ -119,6 +120,10 @@ def _norm_call(torch, x, y, weight, post_weight, gate, scale, eps, h, h_stride, 
         h = torch.empty((T, D), dtype=x.dtype, device=device)
     rstd = torch.empty(T, dtype=torch.float32, device=device)
     post_rstd = torch.empty_like(rstd) if post_weight is not None else None
+    if D == 0:  # the mean of nothing; the C call does no work then
+        rstd.fill_(math.nan)
+        if post_rstd is not None:
+            post_rstd.fill_(math.nan)
     _check(load().lse_residual_norm(
         x.data_ptr(), dt, T, D, x_stride, _pointer(y), y_stride, _pointer(gate), kind, gate_stride,
         _pointer(post_weight), weight.data_ptr(), wdt, scale, eps, _pointer(h), h_stride, out.data_ptr(), out_stride,
