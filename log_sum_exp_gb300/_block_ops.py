@@ -288,7 +288,8 @@ class Weights4:
 
     @classmethod
     def from_values(cls, values, scales, group=128, stream=None):
-        """From whole numbers (int8 [N, K], cut off at -8 and 7) and given scales."""
+        """From whole numbers (int8 [N, K], cut off at -8 and 7) and given scales; both are
+        copied."""
         torch = _torch()
         if not values.is_cuda or values.dtype != torch.int8:
             raise ValueError("values must be a CUDA int8 tensor")
@@ -298,7 +299,7 @@ class Weights4:
 
 def _pack_call(torch, cls, values, scales, group, N, K, stride, stream, device):
     codes = torch.empty((N, -(-K // 128) * 64), dtype=torch.uint8, device=device)
-    w = cls(codes, scales.contiguous(), (N, K), group)
+    w = cls(codes, scales.clone(memory_format=torch.contiguous_format), (N, K), group)
     _check(load().lse_pack4(values.data_ptr(), N, K, stride, codes.data_ptr(), _stream_handle(stream, device)),
            "lse_pack4")
     return w
