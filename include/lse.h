@@ -656,7 +656,9 @@ LSE_API lse_status lse_dequantize4(const void *codes, const void *scales, lse_dt
 /*
  * lse_linear4 -- out[t, n] = sum_k x[t, k] q[n, k] scale[n, k / group], for T tokens.
  * Products of a group are summed in f32 with the exact q, times the scale, and summed
- * over the groups in f32; the result is rounded once.
+ * over the groups in f32; the result is rounded once.  A scale that is infinite or NaN
+ * follows from that: an infinite one gives an infinity of the sum's sign, or NaN for a
+ * sum of 0.
  *   x            T rows of K elements of `dtype`, x_stride apart (f32 tokens count with
  *                all their bits).
  *   scales       of scale_dtype, whatever dtype is.

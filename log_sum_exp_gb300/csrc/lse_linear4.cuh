@@ -191,7 +191,6 @@ __global__ void __launch_bounds__(32 * MW, MW == 8 ? 3 : 1) linear4_kernel(Linea
         }
     };
     const auto fetch = [&](Loaded<RT, NS>& to, int block) {
-        // (Groups behind the last meet codes of 0: any scale of the row that is there does.)
         const int grp = min(block * NS + group0, a.groups - 1);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
@@ -205,7 +204,10 @@ __global__ void __launch_bounds__(32 * MW, MW == 8 ? 3 : 1) linear4_kernel(Linea
         }
     };
     float acc[RT][NT][4];
-    const auto multiply = [&](const Loaded<RT, NS>& from, int at) {  // at: the block in the chunk
+    const auto multiply = [&](const Loaded<RT, NS>& from, int b0, int at) {  // at: the block in the chunk
+        // Groups behind the last meet codes of 0: with a scale of 0, since 0 times one that is there
+        // need not be 0.
+        const bool there = NS == 1 || (b0 + at) * NS + group0 < a.groups;
         float part[RT][NT][4];
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
@@ -242,8 +244,8 @@ __global__ void __launch_bounds__(32 * MW, MW == 8 ? 3 : 1) linear4_kernel(Linea
                 for (int r = 0; r < RT; ++r) {
                     // From the lane that loaded it: group i of the block, rows g and g + 8.
                     const int i = w / (4 / NS), lane0 = lane & ~3;
-                    const uint32_t b0 = __shfl_sync(0xffffffffu, from.s[r][0], lane0 + (NS == 1 ? 0 : i));
-                    const uint32_t b1 = __shfl_sync(0xffffffffu, from.s[r][NS == 4 ? 1 : 0], lane0 + (NS == 4 ? i : NS == 2 ? 2 + i : 1));
+                    const uint32_t b0 = __shfl_sync(0xffffffffu, there ? from.s[r][0] : 0u, lane0 + (NS == 1 ? 0 : i));
+                    const uint32_t b1 = __shfl_sync(0xffffffffu, there ? from.s[r][NS == 4 ? 1 : 0] : 0u, lane0 + (NS == 4 ? i : NS == 2 ? 2 + i : 1));
                     const float s0 = scale_of<S32>(b0, a.scale_dtype), s1 = scale_of<S32>(b1, a.scale_dtype);
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
@@ -287,7 +289,7 @@ __global__ void __launch_bounds__(32 * MW, MW == 8 ? 3 : 1) linear4_kernel(Linea
                     for (int d = 0; d < D; ++d) {
                         const int at = b + d * KS;
                         if (at >= nb) continue;
-                        multiply(ring[d], at);
+                        multiply(ring[d], b0, at);
                         if (at + D * KS < nb) fetch(ring[d], b0 + at + D * KS);
                     }
                 }
@@ -378,6 +380,44 @@ template <int DT, int NTOK> __device__ __forceinline__ void stage_few(const Line
     }
 }
 
+// Products of a warp's rows with each group's sum put together before it meets its scale, for rows
+// with a scale that is no finite number: there the sum of scaled parts need not be the scaled sum
+// (an infinite scale makes a NaN of a part that is 0, or of two parts of different signs).
+template <int DT, int NTOK, int R, bool S32> __device__ __noinline__ void odd_rows(LinearArgs a, int64_t row0) {
+    const int lane = threadIdx.x & 31;
+    for (int64_t row = row0; row < row0 + R && row < a.N; ++row) {
+        const char* const scales = static_cast<const char*>(a.scales) + row * a.scale_stride * (S32 ? 4 : 2);
+        const uint32_t* const codes = reinterpret_cast<const uint32_t*>(a.codes) + row * a.blocks * kBlockWords;
+        const auto scale = [&](int g) {
+            return scale_of<S32>(S32 ? __ldg(reinterpret_cast<const uint32_t*>(scales) + g)
+                                     : __ldg(reinterpret_cast<const unsigned short*>(scales) + g), a.scale_dtype);
+        };
+        bool finite = true;
+        for (int g = lane; g < a.groups; g += 32) finite &= fabsf(scale(g)) <= 3.4028235e38f;
+        if (__all_sync(0xffffffffu, finite)) continue;
+        for (int t = 0; t < NTOK; ++t) {
+            const char* const x = static_cast<const char*>(a.x) + t * a.x_stride * DType<DT>::bytes;
+            float sum = 0.0f;
+            for (int g = 0; g < a.groups; ++g) {
+                float part = 0.0f;
+                for (int k = g * a.group + lane; k < min((g + 1) * a.group, a.K); k += 32) {
+                    const int j = k >> 3 & 15, e = k & 7;
+                    const uint32_t w = __ldg(codes + (k >> 7) * kBlockWords + (j & 3) * 4 + (j >> 2));
+                    part = fmaf(static_cast<float>(static_cast<int>(w >> (e / 2 * 4 + e % 2 * 16) & 15u) - 8), load_elem<DT>(x, k), part);
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+                sum = fmaf(scale(g), part, sum);
+            }
+            if (lane == 0) {
+                const int64_t o = t * a.out_stride + row;
+                if (DT == kF32 || a.out_f32) static_cast<float*>(a.out)[o] = sum;
+                else static_cast<unsigned short*>(a.out)[o] = static_cast<unsigned short>(pack2<DT == kF32 ? kBF16 : DT>(sum, 0.0f));
+            }
+        }
+    }
+}
+
 template <int DT, int NTOK, int NS, bool S32>
 __global__ void __launch_bounds__(32 * kFewWarps, few_ctas(NTOK)) linear4_few_kernel(LinearArgs a, int chunks) {
     constexpr int SB = S32 ? 4 : 2, R = few_rows(NTOK, NS);
@@ -404,7 +444,8 @@ __global__ void __launch_bounds__(32 * kFewWarps, few_ctas(NTOK)) linear4_few_ke
                 const char* p = static_cast<const char*>(a.scales) + (row + r) * a.scale_stride * SB;
 #pragma unroll
                 for (int i = 0; i < NS; ++i) {
-                    const int grp = min(block * NS + i, a.groups - 1);  // (one behind the last meets q = 0)
+                    const int grp = block * NS + i;  // (one behind the last: a scale of 0)
+                    if (NS > 1 && grp >= a.groups) continue;
                     if constexpr (S32) s[r][i] = __ldg(reinterpret_cast<const uint32_t*>(p) + grp);
                     else s[r][i] = __ldg(reinterpret_cast<const unsigned short*>(p) + grp);
                 }
@@ -484,7 +525,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, few_ctas(NTOK)) linear4_few_ke
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) acc[r][t] += __shfl_xor_sync(0xffffffffu, acc[r][t], o);
             }
-        // Lane r * NTOK + t writes the sum of row r and token t.
+        // Lane t * R + r writes the sum of row r and token t.
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -494,6 +535,15 @@ __global__ void __launch_bounds__(32 * kFewWarps, few_ctas(NTOK)) linear4_few_ke
                     if (DT == kF32 || a.out_f32) static_cast<float*>(a.out)[o] = acc[r][t];
                     else static_cast<unsigned short*>(a.out)[o] = static_cast<unsigned short>(pack2<DT == kF32 ? kBF16 : DT>(acc[r][t], 0.0f));
                 }
+        float odd = 0.0f;  // NaN where a sum is no finite number (the same in all lanes)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int t = 0; t < NTOK; ++t) odd = fmaf(acc[r][t], 0.0f, odd);
+        if (odd != 0.0f) {
+            __syncwarp();
+            odd_rows<DT, NTOK, R, S32>(a, row0);
+        }
     }
 }
 
