@@ -8,7 +8,8 @@
 // bits of 1024 (bf16: 128) and a subtraction, and mma.sync multiplies 16 rows x 16 columns with 8
 // tokens, summing in f32.  The scale multiplies a group's f32 sum, so nothing but the result is
 // rounded to 16 bits.  f32 tokens are cut into three bf16 parts (8 + 8 + 8 bits, exact) that are
-// three more columns of the product.
+// three more columns of the product.  Numbers of which bf16's range would cut bits off (below
+// 2^-110) take a slower way, times 2^64 in columns of their own.
 //
 // Measured: one bf16 token x 128256 x 2048 39 us, 3.4 TB/s (the same loads without the products 26
 // us); 16 f16 tokens x 32000 x 4096 34 us.  The matrix pipe is busy for 14 % and 21 % of that, the
@@ -70,9 +71,17 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The part of x that a chunk needs, as 16-bit floats: PL planes of `tokens` rows.
-template <int DT>
-__device__ __forceinline__ void stage_tokens(const LinearArgs& a, int64_t t0, int b0, int nb, unsigned char* smem) {
+// An f32 from this magnitude on is three bf16 exactly: its last bit counts 2^-126 or more, bf16's
+// smallest normal number.  Where one of a chunk's numbers is not (below 2^-110 the last bits of it
+// lie below bf16's smallest), all that are smaller than this are cut into parts times 2^64.
+constexpr float kSmallToken = 0x1p-103f;
+enum Taken : int { kAllTokens, kLargeTokens, kSmallTokens };  // (the others as 0; small ones times 2^64)
+
+// The part of x that a chunk needs, as 16-bit floats: PL planes of `tokens` rows.  Whether there
+// are f32 among it that lose bits when cut as they are.
+template <int DT, int TAKEN = kAllTokens>
+__device__ __forceinline__ bool stage_tokens(const LinearArgs& a, int64_t t0, int b0, int nb, unsigned char* smem) {
+    uint32_t last = 0;  // the last parts as f32
     const int cols = nb * kBlock, k0 = b0 * kBlock;
     const int plane = a.tokens * a.row_bytes;
     const int per_row = cols / 8;
@@ -94,10 +103,13 @@ __device__ __forceinline__ void stage_tokens(const LinearArgs& a, int64_t t0, in
                     // Cut off, not rounded, so that no part overflows; nothing is left of an
                     // infinity or a NaN.
                     float r = f[2 * e + s];
+                    if constexpr (TAKEN == kLargeTokens) r = fabsf(r) < kSmallToken ? 0.0f : r;
+                    if constexpr (TAKEN == kSmallTokens) r = fabsf(r) < kSmallToken ? r * 0x1p64f : 0.0f;
                     const bool finite = fabsf(r) <= 3.4028235e38f;
 #pragma unroll
                     for (int q = 0; q < 3; ++q) {
                         const uint32_t top = __float_as_uint(r) & 0xffff0000u;
+                        if (q == 2) last |= __float_as_uint(r);
                         part[q][s] = (q == 0 && r != r) ? 0x7fc00000u : top;
                         r = finite ? r - __uint_as_float(top) : 0.0f;
                     }
@@ -125,6 +137,7 @@ __device__ __forceinline__ void stage_tokens(const LinearArgs& a, int64_t t0, in
             *reinterpret_cast<uint4*>(to) = v4;
         }
     }
+    return (last & 0xffffu) != 0;
 }
 
 // A block's codes and scales of a warp's rows, as loaded: nothing is made of them before the
@@ -142,14 +155,15 @@ template <bool S32> __device__ __forceinline__ float scale_of(uint32_t bits, int
 
 // Tokens by groups of 8 (NT), groups of columns in a block (NS), tiles of 16 rows per warp (RT),
 // blocks of codes in flight per warp (D), scales of 32 bits.  a.ks warps share the columns of a
-// tile: block b of a chunk belongs to warp b % ks.  MW: warps of a CTA at most.
-template <int DT, int NT, int NS, int RT, int D, bool S32, int MW>
-__global__ void __launch_bounds__(32 * MW, MW == 8 ? 3 : 1) linear4_kernel(LinearArgs a) {
+// tile: block b of a chunk belongs to warp b % ks.
+// A CTA's tiles from `first` on.  SMALL: chunks of half as many blocks, and behind their x the small
+// numbers of it, so that both meet in a group's sum.  Else it stops at f32 tokens that need that,
+// and returns where (-1: it came to the end).
+template <int DT, int NT, int NS, int RT, int D, bool S32, bool SMALL>
+__device__ __forceinline__ int64_t linear4_tiles(const LinearArgs& a, unsigned char* smem, int64_t first) {
     constexpr bool F16 = DT == kF16;
     constexpr int PL = DT == kF32 ? 3 : 1;
-    extern __shared__ __align__(16) unsigned char smem[];
-    pdl_trigger();
-    pdl_wait();
+    const int chunk = SMALL ? a.chunk_blocks / 2 : a.chunk_blocks;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     const int KS = a.ks, ks = warp % KS, together = (blockDim.x >> 5) / KS;
     const int64_t t0 = static_cast<int64_t>(blockIdx.y) * 8 * NT;
@@ -208,7 +222,7 @@ __global__ void __launch_bounds__(32 * MW, MW == 8 ? 3 : 1) linear4_kernel(Linea
         // Groups behind the last meet codes of 0: with a scale of 0, since 0 times one that is there
         // need not be 0.
         const bool there = NS == 1 || (b0 + at) * NS + group0 < a.groups;
-        float part[RT][NT][4];
+        float part[RT][NT][4], part_small[SMALL ? RT : 1][SMALL ? NT : 1][4];
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
             if (w % (4 / NS) == 0) {
@@ -217,7 +231,10 @@ __global__ void __launch_bounds__(32 * MW, MW == 8 ? 3 : 1) linear4_kernel(Linea
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) part[r][n][i] = 0.0f;
+                        for (int i = 0; i < 4; ++i) {
+                            part[r][n][i] = 0.0f;
+                            if constexpr (SMALL) part_small[r][n][i] = 0.0f;
+                        }
             }
             uint32_t p[RT][2][4];
 #pragma unroll
@@ -237,6 +254,14 @@ __global__ void __launch_bounds__(32 * MW, MW == 8 ? 3 : 1) linear4_kernel(Linea
                         mma<F16>(part[r][n], p[r][0][0], p[r][1][0], p[r][0][1], p[r][1][1], x.x, x.y);
                         mma<F16>(part[r][n], p[r][0][2], p[r][1][2], p[r][0][3], p[r][1][3], x.z, x.w);
                     }
+                    if constexpr (SMALL) {
+                        const uint4 y = *reinterpret_cast<const uint4*>(mine[n] + l * next_plane[n] + (chunk + at) * (kBlock * 2) + w * 64);
+#pragma unroll
+                        for (int r = 0; r < RT; ++r) {
+                            mma<F16>(part_small[r][n], p[r][0][0], p[r][1][0], p[r][0][1], p[r][1][1], y.x, y.y);
+                            mma<F16>(part_small[r][n], p[r][0][2], p[r][1][2], p[r][0][3], p[r][1][3], y.z, y.w);
+                        }
+                    }
                 }
             }
             if (w % (4 / NS) == 4 / NS - 1) {
@@ -250,7 +275,10 @@ __global__ void __launch_bounds__(32 * MW, MW == 8 ? 3 : 1) linear4_kernel(Linea
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) acc[r][n][j] = fmaf(j < 2 ? s0 : s1, part[r][n][j], acc[r][n][j]);
+                        for (int j = 0; j < 4; ++j) {
+                            if constexpr (SMALL) part[r][n][j] = fmaf(part_small[r][n][j], 0x1p-64f, part[r][n][j]);
+                            acc[r][n][j] = fmaf(j < 2 ? s0 : s1, part[r][n][j], acc[r][n][j]);
+                        }
                 }
             }
         }
@@ -259,28 +287,36 @@ __global__ void __launch_bounds__(32 * MW, MW == 8 ? 3 : 1) linear4_kernel(Linea
     const auto refill = [&](int64_t tile, int b0) {
         if (tile >= a.tiles) return;
         if (b0 == 0) aim(tile);
-        const int nb = min(a.chunk_blocks, a.blocks - b0);
+        const int nb = min(chunk, a.blocks - b0);
 #pragma unroll
         for (int d = 0; d < D; ++d)
             if (ks + d * KS < nb) fetch(ring[d], b0 + ks + d * KS);
     };
     bool staged = false;
     const int64_t step = static_cast<int64_t>(gridDim.x) * together;
-    int64_t tile = static_cast<int64_t>(blockIdx.x) * together + warp / KS;
+    int64_t tile = first + warp / KS;
     refill(tile, 0);
-    for (int64_t first = static_cast<int64_t>(blockIdx.x) * together; first < a.tiles; first += step, tile += step) {
+    for (; first < a.tiles; first += step, tile += step) {
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[r][n][i] = 0.0f;
-        for (int b0 = 0; b0 < a.blocks; b0 += a.chunk_blocks) {
-            const int nb = min(a.chunk_blocks, a.blocks - b0);
-            if (!staged || a.chunk_blocks < a.blocks) {
+        for (int b0 = 0; b0 < a.blocks; b0 += chunk) {
+            const int nb = min(chunk, a.blocks - b0);
+            if (!staged || chunk < a.blocks) {
                 __syncthreads();
-                stage_tokens<DT>(a, t0, b0, nb, smem);
-                __syncthreads();
+                if constexpr (SMALL) {
+                    stage_tokens<DT, kLargeTokens>(a, t0, b0, nb, smem);
+                    stage_tokens<DT, kSmallTokens>(a, t0, b0, nb, smem + chunk * (kBlock * 2));
+                    __syncthreads();
+                } else if constexpr (DT == kF32) {
+                    if (__syncthreads_or(stage_tokens<DT>(a, t0, b0, nb, smem))) return first;
+                } else {
+                    stage_tokens<DT>(a, t0, b0, nb, smem);
+                    __syncthreads();
+                }
                 staged = true;
             }
             if (tile < a.tiles) {
@@ -295,7 +331,7 @@ __global__ void __launch_bounds__(32 * MW, MW == 8 ? 3 : 1) linear4_kernel(Linea
                 }
             }
             // What comes next is under way before this tile's sums are put together.
-            if (b0 + a.chunk_blocks < a.blocks) refill(tile, b0 + a.chunk_blocks);
+            if (b0 + chunk < a.blocks) refill(tile, b0 + chunk);
             else refill(tile + step, 0);
         }
         if (KS > 1) {  // the warps' sums in their order
@@ -335,6 +371,26 @@ __global__ void __launch_bounds__(32 * MW, MW == 8 ? 3 : 1) linear4_kernel(Linea
                     else static_cast<unsigned short*>(a.out)[o] = static_cast<unsigned short>(pack2<DT == kF32 ? kBF16 : DT>(acc[r][n][i], 0.0f));
                 }
     }
+    return -1;
+}
+
+// (Not inlined: its registers are not the usual path's.)
+template <int DT, int NT, int NS, int RT, bool S32>
+__device__ __noinline__ void linear4_small_tiles(LinearArgs a, unsigned char* smem, int64_t first) {
+    linear4_tiles<DT, NT, NS, RT, 1, S32, true>(a, smem, first);
+}
+
+// MW: warps of a CTA at most.
+template <int DT, int NT, int NS, int RT, int D, bool S32, int MW>
+__global__ void __launch_bounds__(32 * MW, MW == 8 ? 3 : 1) linear4_kernel(LinearArgs a) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    pdl_trigger();
+    pdl_wait();
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * ((blockDim.x >> 5) / a.ks);
+    const int64_t left = linear4_tiles<DT, NT, NS, RT, D, S32, false>(a, smem, first);
+    if constexpr (DT == kF32) {
+        if (left >= 0) linear4_small_tiles<DT, NT, NS, RT, S32>(a, smem, left);
+    }
 }
 
 // Dynamic shared memory of a CTA at most, the same in every call: calls of other threads do not
@@ -349,8 +405,9 @@ constexpr int kMostDynamic = 227 * 1024;
 // whole, 1024 columns at a time: a lane's 16 bytes hold 32 codes, and a row's 512 bytes lie next
 // to each other.  A code becomes an f32 by an or alone: left where it is in its word, p bits up
 // (p <= 16), it is 2^23 + 2^p (q + 8), and taking 2^23 + 8 2^p off leaves 2^p q exactly, which meets
-// an x that was multiplied by 2^-p in shared memory.  Of the eight codes of a word five need no
-// shift and three share one.  With packed FP32 that is 1.1 logic, 0.5 add and 0.5 multiply-add
+// an x that was multiplied by 2^-p in shared memory.  (Where x has numbers that lose bits by that,
+// a multiply-add by 2^-p leaves q and meets x as it is: 58 us instead of 50 for one token of 128256 x
+// 2048.)  Of the eight codes of a word five need no shift and three share one.  With packed FP32 that is 1.1 logic, 0.5 add and 0.5 multiply-add
 // instructions per weight and token.
 // ---------------------------------------------------------------------------
 // Rows of a warp at a time, and CTAs that an SM holds: by the registers that codes, scales, x
@@ -364,8 +421,11 @@ constexpr int kFewTokens = 4;
 // Bits by which the code of column e of a word lies above bit 0, after the shift of its half.
 __host__ __device__ constexpr int code_shift(int e) { return e == 1 ? 16 : e % 2 == 0 ? 2 * e : 2 * e + 2; }
 
-// x of the call, permuted: [chunk][word][half][token][lane][4 columns], each column times 2^-shift.
-template <int DT, int NTOK> __device__ __forceinline__ void stage_few(const LinearArgs& a, int chunks, float* smem) {
+// x of the call, permuted: [chunk][word][half][token][lane][4 columns], each column times 2^-shift
+// unless SMALL.  Whether there are numbers that lose bits by that.
+constexpr float kSmallFew = 0x1p-110f;  // 2^-126 times the largest shift
+template <int DT, int NTOK, bool SMALL> __device__ __forceinline__ bool stage_few(const LinearArgs& a, int chunks, float* smem) {
+    bool small = false;
     for (int i = threadIdx.x; i < chunks * 8 * NTOK * 32; i += blockDim.x) {
         const int lane = i & 31, t = i / 32 % NTOK, h = i / (32 * NTOK) % 2, w = i / (64 * NTOK) % 4, chunk = i / (256 * NTOK);
         const int k = chunk * kFewColumns + (lane >> 2) * kBlock + 32 * w + 8 * (lane & 3) + 4 * h;
@@ -373,11 +433,14 @@ template <int DT, int NTOK> __device__ __forceinline__ void stage_few(const Line
         float v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float down = __int_as_float((127 - (h == 0 ? code_shift(e) : code_shift(e + 4))) << 23);
-            v[e] = k + e < a.K ? load_elem<DT>(row, k + e) * down : 0.0f;
+            const float down = __int_as_float((127 - (SMALL ? 0 : h == 0 ? code_shift(e) : code_shift(e + 4))) << 23);
+            v[e] = k + e < a.K ? load_elem<DT>(row, k + e) : 0.0f;
+            if constexpr (!SMALL) small |= fabsf(v[e]) < kSmallFew && v[e] != 0.0f;
+            v[e] *= down;
         }
         *reinterpret_cast<float4*>(smem + i * 4) = make_float4(v[0], v[1], v[2], v[3]);
     }
+    return small;
 }
 
 // Products of a warp's rows with each group's sum put together before it meets its scale, for rows
@@ -418,13 +481,10 @@ template <int DT, int NTOK, int R, bool S32> __device__ __noinline__ void odd_ro
     }
 }
 
-template <int DT, int NTOK, int NS, bool S32>
-__global__ void __launch_bounds__(32 * kFewWarps, few_ctas(NTOK)) linear4_few_kernel(LinearArgs a, int chunks) {
+// All rows of a warp; false where x has numbers that need SMALL (nothing is written then).
+template <int DT, int NTOK, int NS, bool S32, bool SMALL>
+__device__ __forceinline__ bool few_tokens(const LinearArgs& a, int chunks, float* smem) {
     constexpr int SB = S32 ? 4 : 2, R = few_rows(NTOK, NS);
-    extern __shared__ __align__(16) unsigned char smem_bytes[];
-    const float* smem = reinterpret_cast<const float*>(smem_bytes);
-    pdl_trigger();
-    pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t step = static_cast<int64_t>(gridDim.x) * kFewWarps * R;
     int64_t row0 = (static_cast<int64_t>(blockIdx.x) * kFewWarps + warp) * R;
@@ -453,8 +513,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, few_ctas(NTOK)) linear4_few_ke
         }
     };
     fetch(row0, 0);
-    stage_few<DT, NTOK>(a, chunks, reinterpret_cast<float*>(smem_bytes));
-    __syncthreads();
+    if (__syncthreads_or(stage_few<DT, NTOK, SMALL>(a, chunks, smem))) return false;
     for (; row0 < a.N; row0 += step) {
         float acc[R][NTOK];
 #pragma unroll
@@ -500,8 +559,14 @@ __global__ void __launch_bounds__(32 * kFewWarps, few_ctas(NTOK)) linear4_few_ke
                         const int p0 = code_shift(e), p1 = code_shift(e + 1);
                         const uint32_t b0 = (v & (15u << p0)) | 0x4b000000u;
                         const uint32_t b1 = ((e == 0 ? v : up) & (15u << p1)) | 0x4b000000u;
-                        const uint64_t c = f2_sub(f2_pack(__uint_as_float(b0), __uint_as_float(b1)),
-                                                  f2_pack(8388608.0f + static_cast<float>(8 << p0), 8388608.0f + static_cast<float>(8 << p1)));
+                        const uint64_t raised = f2_pack(__uint_as_float(b0), __uint_as_float(b1));
+                        uint64_t c;
+                        if constexpr (SMALL) {
+                            const float d0 = 1.0f / static_cast<float>(1 << p0), d1 = 1.0f / static_cast<float>(1 << p1);
+                            c = f2_fma(raised, f2_pack(d0, d1), f2_pack(-8388608.0f * d0 - 8.0f, -8388608.0f * d1 - 8.0f));
+                        } else {
+                            c = f2_sub(raised, f2_pack(8388608.0f + static_cast<float>(8 << p0), 8388608.0f + static_cast<float>(8 << p1)));
+                        }
 #pragma unroll
                         for (int t = 0; t < NTOK; ++t) part[r][t] = f2_fma(c, x[t][e / 2], part[r][t]);
                     }
@@ -545,6 +610,22 @@ __global__ void __launch_bounds__(32 * kFewWarps, few_ctas(NTOK)) linear4_few_ke
             odd_rows<DT, NTOK, R, S32>(a, row0);
         }
     }
+    return true;
+}
+
+// (Not inlined: its registers are not the usual path's.)
+template <int DT, int NTOK, int NS, bool S32>
+__device__ __noinline__ void few_small_tokens(LinearArgs a, int chunks, float* smem) {
+    few_tokens<DT, NTOK, NS, S32, true>(a, chunks, smem);
+}
+
+template <int DT, int NTOK, int NS, bool S32>
+__global__ void __launch_bounds__(32 * kFewWarps, few_ctas(NTOK)) linear4_few_kernel(LinearArgs a, int chunks) {
+    extern __shared__ __align__(16) unsigned char smem_bytes[];
+    float* const smem = reinterpret_cast<float*>(smem_bytes);
+    pdl_trigger();
+    pdl_wait();
+    if (!few_tokens<DT, NTOK, NS, S32, false>(a, chunks, smem)) few_small_tokens<DT, NTOK, NS, S32>(a, chunks, smem);
 }
 
 // x in shared memory as f32, with room for three CTAs per SM.
@@ -597,7 +678,9 @@ template <int DT, int NT, int NS, bool S32> cudaError_t launch_linear(LinearArgs
     const int red = ks > 1 ? static_cast<int>(sizeof(float)) * warps * RT * NT * 128 : 0;
     int most = ((kLinearSmem - red) / (PL * a.tokens + 1) - 64) / (kBlock * 2);
     if (most > a.blocks) most = a.blocks;
-    a.chunk_blocks = most < 1 ? 1 : most;
+    // (of f32 two at least: a block and its small numbers)
+    const int least = DT == kF32 ? 2 : 1;
+    a.chunk_blocks = most < least ? least : most;
     a.row_bytes = a.chunk_blocks * kBlock * 2 + 64;
     const size_t smem = static_cast<size_t>(PL * a.tokens + 1) * a.row_bytes + red;
     if (smem > 48 * 1024) {
