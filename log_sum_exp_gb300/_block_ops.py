@@ -407,7 +407,8 @@ def lse_sample(x, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stream=None
 
     ``token`` is int64 [B], ``logprob`` float32 [B]: the log-probability with which the
     token was drawn (0 at temperature 0).  A row that is no distribution (a NaN, +inf,
-    nothing but -inf), or whose own settings are NaN or out of range, gives -1 and NaN.
+    nothing but -inf), or whose own temperature, top_p or min_p is NaN or out of range, gives
+    -1 and NaN; a row's own top_k below 0 is off.
     1-D input drops the row dimension.
     """
     torch = _torch()

@@ -1389,7 +1389,7 @@ struct RowSettings {
         use_k = top_k > 0 && top_k < a.N && !greedy;
         use_p = top_p < 1.0f && !greedy;
         use_min = min_p > 0.0f && !greedy;
-        valid = temperature >= 0.0f && temperature <= kSampleHottest && top_p == top_p && min_p == min_p;
+        valid = temperature >= 0.0f && temperature <= kSampleHottest && top_p >= 0.0f && min_p >= 0.0f;  // (NaN: none)
         // the quotient of the first 24 bits, and what the remainder and the next bits add
         const float t = greedy ? 1.0f : temperature;
         ch = __fdiv_rn(kLog2e, t);
