@@ -708,7 +708,7 @@ typedef struct {
  * of more than 2^18 columns: as many bits fewer as N takes more).  So the token is that of
  * exact arithmetic unless a border of it lies within about 1e-9 of u (or a cut's of top_p),
  * and a repeated call gives equal bits.  logprob is good to a few f32 roundings of its two
- * terms.  A column whose w is below 2^-45 is not drawn.  Temperature 0 draws the first of the largest elements with
+ * terms (log(1 + r), r the weights but for the largest), and to 2^-35.  A column whose w is below 2^-45 is not drawn.  Temperature 0 draws the first of the largest elements with
  * logprob 0, whatever the other settings are.
  * A row that is no distribution (it holds a NaN or +inf, or nothing but -inf, or N == 0),
  * or whose own temperature is NaN or outside 0 .. 1e20 or whose top_p or min_p is NaN or

@@ -715,6 +715,40 @@ template <int DT, int TX> struct Sampler {
         return scan_chunks();
     }
 
+    // The sum of the weights but the maximum's, of the elements that keep(x, column) names, where
+    // `total` (the scanned sums', of fast weights) is less than two: so one maximum counts, the
+    // first, and the sum of its chunk, whose f32 roundings are as large as the digits of a small
+    // rest, is taken again without it.  x: the element of column `col`, which is kept.
+    template <class F> __device__ __forceinline__ uint64_t rest_of(uint64_t total, float x, int col, F&& keep) {
+        if (x != m) {
+            if (tid == 0) sh.r32[0] = 0xffffffffu;
+            row_sync<TX>();
+            for (int i = tid; i < chunks * 32; i += TX)
+                if (maxima[i] == m) atomicMin(&sh.r32[0], static_cast<uint32_t>(i >> 5));
+            row_sync<TX>();
+        }
+        const int c = x != m ? sh.r32[0] : (col + off / EB) / E / chunk;
+        const float dmin = -200.0f / ch;
+        uint64_t acc = 0;
+        for (int s = chunk_begin(c) + tid; s < chunk_end(c); s += TX) {
+            uint32_t w[4];
+            load(s, w);
+            mask(s, w);
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) {
+                float x0, x1;
+                f2_unpack(pair_of(w, e), x0, x1);
+                x0 = x0 != m && keep(x0, column(s, 2 * e)) ? x0 : -kInf;
+                x1 = x1 != m && keep(x1, column(s, 2 * e + 1)) ? x1 : -kInf;
+                acc = add_pair(acc, f2_pack(x0, x1), m, dmin);
+            }
+        }
+        float a, b;
+        f2_unpack(acc, a, b);
+        const uint64_t own = __double2ull_rn(static_cast<double>(a + b) * __hiloint2double((1023 + S) << 20, 0));
+        return row_sum(own) + (total - (sums[c + 1] - sums[c]));
+    }
+
     // -----------------------------------------------------------------------
     // Threshold keys
     // -----------------------------------------------------------------------
@@ -1471,8 +1505,8 @@ __device__ void sample_row(SampleShared<TX>& sh, const uint32_t* powers, unsigne
         return;
     }
     // The maximum is kept and weighs 1: log(1 + rest) keeps the digits of a small rest.
-    const auto finish = [&](int64_t token, float x, uint64_t total) {
-        const uint64_t one = 1ull << r.S, rest = total > one ? total - one : 0;
+    const uint64_t one = 1ull << r.S;
+    const auto finish = [&](int64_t token, float x, uint64_t rest) {
         put_token(a, row, token, (x - r.m) / g.temperature - log1pf(static_cast<float>(rest) * __int_as_float((127 - r.S) << 23)));
     };
     const auto drawn = [&](uint64_t total) -> uint64_t {
@@ -1559,7 +1593,7 @@ __device__ void sample_row(SampleShared<TX>& sh, const uint32_t* powers, unsigne
             float x;
             uint64_t before;
             r.locate(drawn(total), false, kept, &col, &x, &before, &with);
-            if (r.tid == 0) finish(col, x, total);
+            if (r.tid == 0) finish(col, x, total - one);
             return;
         }
         if (g.use_k) {
@@ -1591,7 +1625,9 @@ __device__ void sample_row(SampleShared<TX>& sh, const uint32_t* powers, unsigne
     }
     int col = 0;
     float x = 0.0f;
-    uint64_t before = 0, with = 0;
+    uint64_t before = 0, with = 0, rest = 0;
+    // Where f32 sums hold the maximum's weight, they are good to 1e-7 of that.
+    const auto rest_from = [&](const auto& keep) { return err && total < 2 * one ? r.rest_of(total, x, col, keep) : total > one ? total - one : 0; };
     if (threshold == 0) {  // nothing is cut off
         if (!with_sums || g.use_p) {  // (the sums of chunks are not there, or select() has used their place)
             total = r.exact_chunks(-kInf, [](float, int) -> bool { return true; });
@@ -1604,6 +1640,7 @@ __device__ void sample_row(SampleShared<TX>& sh, const uint32_t* powers, unsigne
             total = r.exact_chunks(-kInf, [](float, int) -> bool { return true; });  // too close to tell
             err = 0;
         }
+        rest = rest_from([](float, int) -> bool { return true; });
     } else {
         const uint32_t bits = static_cast<uint32_t>(threshold >> 32);
         const float low = order_value(bits);
@@ -1626,9 +1663,11 @@ __device__ void sample_row(SampleShared<TX>& sh, const uint32_t* powers, unsigne
         if (err && (!found || target - before <= err || with - target <= err)) {  // too close to tell
             total = r.exact_chunks(low, [&](float v, int c) -> bool { return v > low || (v == low && c <= last); });
             r.locate(drawn(total), true, kept, &col, &x, &before, &with);
+            err = 0;
         }
+        rest = rest_from([&](float v, int c) -> bool { return v > low || (v == low && c <= last); });
     }
-    if (r.tid == 0) finish(col, x, total);
+    if (r.tid == 0) finish(col, x, rest);
 }
 
 template <int TX> __host__ __device__ constexpr int sample_ctas() { return TX == 128 ? 8 : TX == 256 ? 4 : 1; }
@@ -1923,10 +1962,9 @@ template <int DT, int V> __device__ __forceinline__ bool sample_short(const Samp
 #pragma unroll
     for (int j = 0; j < M; ++j) r.w[j] = r.weight(r.x(j));
     if (g.use_k && !r.cut(false, static_cast<float>(g.top_k), 0.0f, 0.0f, keys, bins)) return false;
-    float total = r.sum();
     if (g.use_p) {
-        if (!r.cut(true, g.top_p * total, total, R::kError * total, keys, bins)) return false;
-        total = r.sum();
+        const float all = r.sum();
+        if (!r.cut(true, g.top_p * all, all, R::kError * all, keys, bins)) return false;
     }
     if (g.use_min) {
         // In octaves; the border is good to 2^-21 of the distance and of the logarithm.
@@ -1940,7 +1978,37 @@ template <int DT, int V> __device__ __forceinline__ bool sample_short(const Samp
             if (t < z) r.w[j] = 0.0f;
         }
         if (__any_sync(0xffffffffu, open)) return false;
-        total = r.sum();
+    }
+    const auto over_lanes = [](float s) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        return s;
+    };
+    float sums[V], total = 0.0f;  // of vectors
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        float s = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) s += r.w[v * E + e];
+        sums[v] = over_lanes(s);
+        total += sums[v];
+    }
+    // Without the maximum's weight a small rest keeps its digits.  (Less than two: there is one such
+    // weight, and one vector's sum of 1 or more, which holds it.)
+    float rest = total - 1.0f;
+    if (total < 2.0f) {
+        rest = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (sums[v] >= 1.0f) {
+                float s = 0.0f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) s += r.w[v * E + e] == 1.0f ? 0.0f : r.w[v * E + e];
+                rest += over_lanes(s);
+            } else {
+                rest += sums[v];
+            }
+        }
     }
     // The vector, the lane and the element at which the running sum passes the target.
     const float err = R::kError * total;
@@ -1950,18 +2018,13 @@ template <int DT, int V> __device__ __forceinline__ bool sample_short(const Samp
     int at = -1;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        float s = 0.0f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) s += r.w[v * E + e];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (at < 0 && target < run + s) {
+        if (at < 0 && target < run + sums[v]) {
             at = v;
             before = run;
 #pragma unroll
             for (int e = 0; e < E; ++e) mine[e] = r.w[v * E + e];
         }
-        run += s;
+        run += sums[v];
     }
     if (at < 0) return false;
     float s = 0.0f;
@@ -1997,7 +2060,7 @@ template <int DT, int V> __device__ __forceinline__ bool sample_short(const Samp
 #pragma unroll
         for (int j = 0; j < M; ++j)
             if (j == at * E + e_at) v = r.x(j);
-        put_token(a, row, c, (v - m) / g.temperature - log1pf(fmaxf(total - 1.0f, 0.0f)));
+        put_token(a, row, c, (v - m) / g.temperature - log1pf(rest));
     }
     return true;
 }
