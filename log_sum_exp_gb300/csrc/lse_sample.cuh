@@ -18,14 +18,25 @@
 // the product and a cubic for 2^r - 1; off by at most about 2^-30 of itself.  Sums of whole
 // numbers do not depend on their order.  That takes about 40 instructions, four times what the
 // memory's rate leaves for a bf16 element, so passes over a row use fast weights, of ex2 with the
-// rounding error of its argument carried along.  What is compared is always a part of a sum with
-// u (or top_p) times the whole, and their difference is off by 1 - u times the sum of w e over the
-// part, less u times that over the rest, with e a weight's relative error.  An error that all
-// weights share cancels; where e lies within h of its middle the difference is off by at most
-// 2 u (1 - u) h of the whole, h / 2.  ex2.approx gave e from -1.44e-7 to 1.05e-7 over every f32 in
-// [-32, 0), so that is 6.3e-8; the additions' roundings are independent of each other and far
-// smaller.  fast_error() is twice that.  Where a comparison is closer, about one row of 128256
-// columns in fifty, the row is done again with exact weights.
+// rounding error of its argument carried along.  Such a sum is that of w (1 + e), |e| <= E:
+//
+//     1.46e-7      of ex2.approx (-1.44e-7 to 1.46e-7 over every f32 in [-110, 110])
+//     n 2^-24      of the additions that an element passes through: log2 of the 32 elements (of f32,
+//                  16) that a lane adds by halves at a time, and the chunk's
+//
+// in the worst case, which a row of one or two heavy elements comes near.  Weights are relative to 0
+// where the maximum is -64 to 100 octaves (x log2 e / T) from it, else to a maximum.  Distances from that are
+// rounded where elements are of 16 bits (f32 ones carry what that loses along): by 2^-24 of
+// (m - x) / T, whose mean over the weights is at most log(N / sum of w), the entropy of N equal ones
+// less what w has (and log 2 more in first_pass(), whose shifts lie up to an octave below the
+// elements).
+// What is compared is a part of a sum with u (or top_p) times the whole.  The difference is off by
+// 1 - u times the sum of w e over the part, less u times that over the rest; a share L of the part
+// that has been summed exactly counts with u, in the whole only.  So it is off by at most
+//
+//     E (2 u (1 - u) + max(0, 2 u - 1) L) + 2^-24 log(2 N / sum) max(u, 1 - u)
+//
+// of the whole, the second term only with rounded distances (Doubt).  Where a comparison is closer, the row is done again with exact weights.
 //
 // Threshold.  Every lane's maximum in every chunk is kept in shared memory.  They bound the
 // threshold from below (the k-th largest of them is at most the k-th largest element; the same
@@ -68,9 +79,34 @@ constexpr int kChunk = 128;  // vectors of a chunk, at least
 // Histogram bins and list entries of a row's threads.
 template <int TX> __host__ __device__ constexpr int bins_log2() { return TX == 32 ? 7 : 10; }
 template <int TX> __host__ __device__ constexpr int list_size() { return TX == 32 ? 64 : 2048; }
-// What a comparison of a part of a fast sum with a share of the whole may be off by.
-__device__ __forceinline__ uint64_t fast_error(uint64_t total) { return (total >> 23) + 1; }  // 1.2e-7
 constexpr float kInf = __builtin_inff();
+// Octaves above and below 0 within which fast weights are relative to it: sums stay below 2^127, and
+// 60 octaves below a maximum are still f32 numbers.
+constexpr float kNearAbove = 100.0f, kNearBelow = -64.0f;
+
+// What a comparison of a part of a fast sum with a share u of the whole may be off by (see above).
+template <int DT> __host__ __device__ constexpr float fast_error() { return 1.46e-7f + (DT == kF32 ? 5 : 6) * 0x1p-24f + 4e-9f; }
+struct Doubt {
+    uint64_t any;    // of a sum alone, and at any share; 0: sums are exact
+    uint64_t fixed;
+    float exact;     // times the part's elements that were summed exactly
+    __device__ __forceinline__ Doubt() : any(0), fixed(0), exact(0.0f) {}
+    // each: fast_error().  (Chunks' sums are rounded to whole numbers, a half each.)
+    __device__ __forceinline__ Doubt(uint64_t total, float u, float each, bool whole_distances, int N, int S) {
+        u = fminf(fmaxf(u, 0.0f), 1.0f);
+        const float all = static_cast<float>(total);
+        const float far = whole_distances ? 0.0f : 0x1p-24f * fmaxf(0.0f, __logf(2.0f * static_cast<float>(N) / (all * __int_as_float((127 - S) << 23))));
+        any = static_cast<uint64_t>(all * (each + far)) + 300;
+        fixed = static_cast<uint64_t>(all * (each * 2.0f * u * (1.0f - u) + far * fmaxf(u, 1.0f - u) + 2e-9f)) + 300;
+        exact = each * fmaxf(0.0f, 2.0f * u - 1.0f);
+    }
+    __device__ __forceinline__ uint64_t at(uint64_t summed) const { return any ? fixed + static_cast<uint64_t>(exact * static_cast<float>(summed)) : 0; }
+    // Whether a target between two sums, the second with `summed` of it exact, is next to neither.
+    __device__ __forceinline__ bool sure(uint64_t before, uint64_t target, uint64_t with, uint64_t summed) const {
+        const uint64_t e = at(summed);
+        return target - before > e && with - target > e;
+    }
+};
 
 // 2^(j / 64) in units of 2^-30, rounded to nearest.
 __constant__ uint32_t kPowers[64] = {
@@ -470,10 +506,11 @@ template <int DT, int TX> struct Sampler {
         return warp_sum(__double2ull_rn(v * __hiloint2double((1023 + S) << 20, 0)));
     }
     // The first column at which the running sum of f passes `target`; sums are scanned.
-    // Sets the sums before it and with it; false if there is none in the chunk that the
-    // chunks' sums name (they may be approximate).
+    // Sets the sums before it and with it, and what of the latter is the chunk's own (which is summed
+    // here, by f); false if there is none in the chunk that the chunks' sums name (they may be
+    // approximate).
     template <class F>
-    __device__ __forceinline__ bool locate(uint64_t target, bool clamp, F&& f, int* col, float* value, uint64_t* before, uint64_t* with) {
+    __device__ __forceinline__ bool locate(uint64_t target, bool clamp, F&& f, int* col, float* value, uint64_t* before, uint64_t* with, uint64_t* inside) {
         int c, s0, s1;
         uint64_t own, first, rest;
         bool back = false;
@@ -537,6 +574,7 @@ template <int DT, int TX> struct Sampler {
                         sh.r32[2] = __float_as_uint(x);
                         sh.r64[0] = sums[c] + run;
                         sh.r64[1] = sums[c] + run + v;
+                        sh.r64[2] = run + v;
                         found = true;
                     }
                     run += v;
@@ -549,6 +587,7 @@ template <int DT, int TX> struct Sampler {
         *value = __uint_as_float(sh.r32[2]);
         *before = sh.r64[0];
         *with = sh.r64[1];
+        *inside = sh.r64[2];
         row_sync<TX>();
         return ok;
     }
@@ -557,10 +596,9 @@ template <int DT, int TX> struct Sampler {
     // Pass over the row: maxima, and sums of fast weights relative to a shift of the chunk's
     // (chunks are the same whatever the number of threads, and so are a row's sums in any batch)
     // -----------------------------------------------------------------------
-    // The fast weight of a pair, added to a sum of pairs.
-    __device__ __forceinline__ uint64_t add_pair(uint64_t acc, uint64_t x, float mu, float dmin) const {
+    // The fast weights of a pair, w (1 - e log 2): w is 2^t, and e what t has too much of.
+    __device__ __forceinline__ uint64_t pair_weights(uint64_t x, float mu, float dmin, uint64_t* lost) const {
         const uint64_t mu2 = f2_pack(mu, mu), ch2 = f2_pack(ch, ch), nch2 = f2_pack(-ch, -ch), ncl2 = f2_pack(-cl, -cl);
-        const uint64_t nln2 = f2_pack(-kLn2, -kLn2), one2 = f2_pack(1.0f, 1.0f);
         uint64_t d = f2_sub(x, mu2);
         uint64_t dl = 0;
         float d0, d1;
@@ -580,21 +618,63 @@ template <int DT, int TX> struct Sampler {
         uint64_t e = f2_fma(d, nch2, t);  // minus what the product lost
         e = f2_fma(d, ncl2, e);
         if constexpr (DT == kF32) e = f2_fma(dl, nch2, e);
-        return f2_fma(f2_ex2(t), f2_fma(e, nln2, one2), acc);
+        *lost = e;
+        return f2_ex2(t);
+    }
+    // Pairs A .. A + L - 1 of a batch, the words of which f(i) gives, by halves (log L roundings); w e
+    // is added to `over`.
+    template <int A, int L, class F>
+    __device__ __forceinline__ uint64_t sum_pairs(const F& f, uint64_t& over, float mu, float dmin) const {
+        if constexpr (L == 1) {
+            uint64_t e;
+            const uint64_t w = pair_weights(f(A), mu, dmin, &e);
+            over = f2_fma(w, e, over);
+            return w;
+        } else {
+            const uint64_t s = sum_pairs<A, L / 2>(f, over, mu, dmin);
+            return f2_add(s, sum_pairs<A + L / 2, L / 2>(f, over, mu, dmin));
+        }
+    }
+    template <class F> __device__ __forceinline__ void add_pairs(float& hi, float& lo, const F& f, float mu, float dmin) const {
+        uint64_t over = 0;
+        const uint64_t s = sum_pairs<0, kBatch * E / 2>(f, over, mu, dmin);
+        add_sums(hi, lo, s, over);
     }
     __device__ __forceinline__ static uint64_t pair_of(const uint32_t (&w)[4], int i) {  // i < E / 2
         if constexpr (DT == kF32) return f2_pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
         else return f2_pack(word_lo<DT>(w[i]), word_hi<DT>(w[i]));
     }
-    __device__ __forceinline__ float batch_sum(const uint32_t (&w)[kBatch][4], float mu, float dmin) const {
-        uint64_t acc[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-#pragma unroll
-            for (int i = 0; i < E / 2; ++i) acc[(j * E / 2 + i) & 3] = add_pair(acc[(j * E / 2 + i) & 3], pair_of(w[j], i), mu, dmin);
-        float a, b;
-        f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), a, b);
-        return a + b;
+    // A batch's sums to the lane's, hi + lo.
+    __device__ __forceinline__ static void add_sums(float& hi, float& lo, uint64_t acc, uint64_t over) {
+        float a, b, c, d;
+        f2_unpack(acc, a, b);
+        f2_unpack(over, c, d);
+        add_exact(hi, lo, a + b);
+        lo = fmaf(c + d, -kLn2, lo);
+    }
+    // The lanes' sums hi + lo (|lo| a 2^-17th of hi at most) put together as whole numbers, of 2^-38
+    // of the largest, and rounded once; NaN if one is no number.
+    __device__ __forceinline__ static float over_lanes(float hi, float lo) {
+        const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(hi));
+        if (top == 0) return 0.0f;
+        if (top >= 0x7f800000u) return kInf - kInf;
+        constexpr float magic = 12582912.0f;  // 1.5 2^23: added to it, a number is rounded to a whole one
+        const uint32_t e = max(top >> 23, 23u);
+        const float up = __uint_as_float((275u - e) << 23), down = __uint_as_float((e - 21u) << 23);  // the largest to 2^21 .. 2^22
+        const float t = fmaf(hi, up, magic), r = fmaf(lo, up, fmaf(hi, up, -(t - magic)));
+        const int a = __reduce_add_sync(0xffffffffu, __float_as_int(t) - 0x4b400000);
+        const int b = __reduce_add_sync(0xffffffffu, __float_as_int(fmaf(r, 65536.0f, magic)) - 0x4b400000);
+        return __ll2float_rn((static_cast<long long>(a) << 16) + b) * 0x1p-16f * down;
+    }
+    // What fast weights are relative to, for elements of at most v: 0, which no distance is rounded
+    // from, where 2^(v log2 e / T) and what counts below it are f32 numbers.
+    __device__ __forceinline__ float shift_of(float v) const { return v * ch <= kNearAbove && v * ch >= kNearBelow ? 0.0f : v; }
+    // Whether that makes no difference or holds for all elements that count (one of a chunk that lies
+    // below it weighs less than 2^-48 of the row).
+    __device__ __forceinline__ bool whole_distances() const { return DT == kF32 || (m * ch <= kNearAbove && m * ch >= kNearBelow + 48.0f); }
+    // From sums relative to shift_of(m) to weights.
+    __device__ __forceinline__ double in_weights() const {
+        return factor(shift_of(m)) * __hiloint2double((1023 + S) << 20, 0);
     }
     // hi + lo + v without loss.
     __device__ __forceinline__ static void add_exact(float& hi, float& lo, float v) {
@@ -651,28 +731,30 @@ template <int DT, int TX> struct Sampler {
                     if (nan) hi = kInf - kInf;
                 } else {
                     if (__any_sync(0xffffffffu, bm > lim)) {  // the shift goes up
-                        float wm = bm;
+                        float to = 0.0f, wm = 0.0f;
+                        if (!__all_sync(0xffffffffu, bm * ch <= kNearAbove) || !__any_sync(0xffffffffu, bm * ch >= kNearBelow)) {
+                            wm = bm;
 #pragma unroll
-                        for (int o = 16; o > 0; o >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, o));
+                            for (int o = 16; o > 0; o >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, o));
+                            to = wm;  // (not near 0)
+                        }
                         if (wm < kInf) {
-                            if (hi != 0.0f) {  // sums relative to the old one (rare: a step of 64 octaves)
+                            if (hi != 0.0f) {  // sums relative to the old one (rare: a step of an octave within a chunk)
                                 Sampler t = *this;
-                                t.m = wm;
+                                t.m = to;
                                 const double sum = (static_cast<double>(hi) + static_cast<double>(lo)) * t.factor(mu);
                                 hi = static_cast<float>(sum);
                                 lo = static_cast<float>(sum - static_cast<double>(hi));
                             }
-                            mu = wm;
-                            lim = mu + 64.0f / ch;
-                            if (!(lim > mu)) lim = mu;
+                            mu = to;
+                            lim = to == 0.0f ? kNearAbove / ch : to + 1.0f / ch;
+                            if (!(lim > to)) lim = to;
                         }
                     }
-                    add_exact(hi, lo, batch_sum(w, mu, dmin));
+                    add_pairs(hi, lo, [&](int i) { return pair_of(w[i / (E / 2)], i % (E / 2)); }, mu, dmin);
                 }
                 if (--left == 0) {  // the chunk is complete
-                    float s = hi + lo;
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                    const float s = over_lanes(hi, lo);
                     maxima[c * 32 + lane] = cm;
                     if (lane == 0) fast[c] = make_float2(s, mu);
                     top = fmaxf(top, cm);
@@ -688,35 +770,28 @@ template <int DT, int TX> struct Sampler {
     // all of them at least `low`; the rest counts as -inf, so that no lane waits for another.
     template <class F> __device__ __forceinline__ uint64_t fast_chunks(float low, F&& keep) {
         row_sync<TX>();
-        const float dmin = -200.0f / ch;
+        const float dmin = -200.0f / ch, mu = shift_of(m);
+        const double unit = in_weights();
         float hi = 0.0f, lo = 0.0f;
         dense(low, [&](const uint32_t (&w)[kBatch][4], int s0) {
-            uint64_t acc[2] = {0, 0};
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j)
-#pragma unroll
-                for (int e = 0; e < E / 2; ++e) {
-                    float x0, x1;
-                    f2_unpack(pair_of(w[j], e), x0, x1);
-                    x0 = keep(x0, column(s0 + 32 * j, 2 * e)) ? x0 : -kInf;
-                    x1 = keep(x1, column(s0 + 32 * j, 2 * e + 1)) ? x1 : -kInf;
-                    acc[e & 1] = add_pair(acc[e & 1], f2_pack(x0, x1), m, dmin);
-                }
-            float a, b;
-            f2_unpack(f2_add(acc[0], acc[1]), a, b);
-            add_exact(hi, lo, a + b);
+            add_pairs(hi, lo, [&](int i) {
+                const int j = i / (E / 2), e = i % (E / 2);
+                float x0, x1;
+                f2_unpack(pair_of(w[j], e), x0, x1);
+                x0 = keep(x0, column(s0 + 32 * j, 2 * e)) ? x0 : -kInf;
+                x1 = keep(x1, column(s0 + 32 * j, 2 * e + 1)) ? x1 : -kInf;
+                return f2_pack(x0, x1);
+            }, mu, dmin);
         }, [&](int c) {
-            float s = hi + lo;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if (lane == 0) sums[c] = __double2ull_rn(static_cast<double>(s) * __hiloint2double((1023 + S) << 20, 0));
+            const float s = over_lanes(hi, lo);
+            if (lane == 0) sums[c] = __double2ull_rn(static_cast<double>(s) * unit);
             hi = lo = 0.0f;
         });
         return scan_chunks();
     }
 
     // The sum of the weights but the maximum's, of the elements that keep(x, column) names, where
-    // `total` (the scanned sums', of fast weights) is less than two: so one maximum counts, the
+    // `total` (the scanned sums', of fast weights) is well below two: so one maximum counts, the
     // first, and the sum of its chunk, whose f32 roundings are as large as the digits of a small
     // rest, is taken again without it.  x: the element of column `col`, which is kept.
     template <class F> __device__ __forceinline__ uint64_t rest_of(uint64_t total, float x, int col, F&& keep) {
@@ -729,7 +804,7 @@ template <int DT, int TX> struct Sampler {
         }
         const int c = x != m ? sh.r32[0] : (col + off / EB) / E / chunk;
         const float dmin = -200.0f / ch;
-        uint64_t acc = 0;
+        uint64_t acc = 0, over = 0;
         for (int s = chunk_begin(c) + tid; s < chunk_end(c); s += TX) {
             uint32_t w[4];
             load(s, w);
@@ -740,11 +815,14 @@ template <int DT, int TX> struct Sampler {
                 f2_unpack(pair_of(w, e), x0, x1);
                 x0 = x0 != m && keep(x0, column(s, 2 * e)) ? x0 : -kInf;
                 x1 = x1 != m && keep(x1, column(s, 2 * e + 1)) ? x1 : -kInf;
-                acc = add_pair(acc, f2_pack(x0, x1), m, dmin);
+                uint64_t lost;
+                const uint64_t v = pair_weights(f2_pack(x0, x1), m, dmin, &lost);
+                acc = f2_add(acc, v);
+                over = f2_fma(v, lost, over);
             }
         }
-        float a, b;
-        f2_unpack(acc, a, b);
+        float a = 0.0f, b = 0.0f;
+        add_sums(a, b, acc, over);
         const uint64_t own = __double2ull_rn(static_cast<double>(a + b) * __hiloint2double((1023 + S) << 20, 0));
         return row_sum(own) + (total - (sums[c + 1] - sums[c]));
     }
@@ -1038,6 +1116,12 @@ template <int DT, int TX> struct Sampler {
         }
     }
 
+    // The least sum that is not less than the share p of the whole (at least 1).
+    static __device__ __forceinline__ uint64_t mass_needed(uint64_t whole, float p) {
+        bool exact;
+        const uint64_t n = part_of(whole, p, &exact);
+        return !exact || n == 0 ? n + 1 : n;
+    }
     // A range of values that a threshold lies in, and how many elements reach its lower end.
     struct Range {
         float lo, hi;
@@ -1209,21 +1293,44 @@ template <int DT, int TX> struct Sampler {
         out->lo = edge > low ? edge : low;  // (low may be no number)
         return true;
     }
+    // Weights of pairs A .. A + L - 1 of a batch above the range, and of those below it, by halves.
+    template <int A, int L>
+    __device__ __forceinline__ uint64_t split_pairs(const uint32_t (&w)[kBatch][4], const Range& at, float mu, float dmin, uint64_t& over_above,
+                                                    uint64_t& over_below, uint64_t* below) const {
+        if constexpr (L == 1) {
+            float x0, x1, w0, w1;
+            uint64_t lost;
+            f2_unpack(pair_of(w[A / (E / 2)], A % (E / 2)), x0, x1);
+            f2_unpack(pair_weights(f2_pack(x0, x1), mu, dmin, &lost), w0, w1);
+            const uint64_t u = f2_pack(x0 > at.hi ? w0 : 0.0f, x1 > at.hi ? w1 : 0.0f);
+            *below = f2_pack(x0 < at.lo ? w0 : 0.0f, x1 < at.lo ? w1 : 0.0f);
+            over_above = f2_fma(u, lost, over_above);
+            over_below = f2_fma(*below, lost, over_below);
+            return u;
+        } else {
+            uint64_t b0, b1;
+            const uint64_t s = split_pairs<A, L / 2>(w, at, mu, dmin, over_above, over_below, &b0);
+            const uint64_t r = split_pairs<A + L / 2, L / 2>(w, at, mu, dmin, over_above, over_below, &b1);
+            *below = f2_add(b0, b1);
+            return f2_add(s, r);
+        }
+    }
     // Sums what lies above a range by chunks (left in `added`, not scanned), and puts the range's
     // elements to the list; returns the sum of all chunks and, in *n, how many elements are in the range.
+    // Of fast weights also what lies below the range, *under.
     template <bool EXACT, bool MASS>
-    __device__ __noinline__ uint64_t split(Range at, uint32_t* n, uint32_t* least, uint32_t* most) {
+    __device__ __noinline__ uint64_t split(Range at, uint32_t* n, uint32_t* least, uint32_t* most, uint64_t* under) {
         row_sync<TX>();
         if (tid == 0) sh.r32[3] = 0, sh.r32[0] = 0xffffffffu, sh.r32[1] = 0;
         row_sync<TX>();
         uint32_t a = 0xffffffffu, z = 0;
-        const float dmin = -200.0f / ch;
-        float hi = 0.0f, lo = 0.0f;
+        const float dmin = -200.0f / ch, mu = shift_of(m);
+        const double unit = in_weights();
+        float hi = 0.0f, lo = 0.0f, under_hi = 0.0f, under_lo = 0.0f;
         uint64_t exact = 0, ehi = 0, elo = 0;
         const float high = kHigh[lane], rest = kLow[lane], far60 = -60.0f / ch;
         const bool beyond = !(at.lo > -kInf);  // elements outside the row are -inf
-        dense(at.lo, [&](const uint32_t (&w)[kBatch][4], int s0) {
-            uint64_t acc[2] = {0, 0};
+        dense(EXACT ? at.lo : -kInf, [&](const uint32_t (&w)[kBatch][4], int s0) {
             uint32_t mask = 0;  // of the range's elements, at most 32
 #pragma unroll
             for (int j = 0; j < kBatch; ++j)
@@ -1244,17 +1351,10 @@ template <int DT, int TX> struct Sampler {
                     }
             }
             if constexpr (!EXACT) {
-#pragma unroll
-                for (int j = 0; j < kBatch; ++j)
-#pragma unroll
-                    for (int e = 0; e < E / 2; ++e) {
-                        float x0, x1;
-                        f2_unpack(pair_of(w[j], e), x0, x1);
-                        acc[e & 1] = add_pair(acc[e & 1], f2_pack(x0 > at.hi ? x0 : -kInf, x1 > at.hi ? x1 : -kInf), m, dmin);
-                    }
-                float p, q;
-                f2_unpack(f2_add(acc[0], acc[1]), p, q);
-                add_exact(hi, lo, p + q);
+                uint64_t over_above = 0, over_below = 0, below;
+                const uint64_t above = split_pairs<0, kBatch * E / 2>(w, at, mu, dmin, over_above, over_below, &below);
+                add_sums(hi, lo, above, over_above);
+                add_sums(under_hi, under_lo, below, over_below);
             }
             if (beyond) {
 #pragma unroll
@@ -1283,14 +1383,14 @@ template <int DT, int TX> struct Sampler {
                 if (lane == 0) sums[c] = added[c] = v;
                 exact = ehi = elo = 0;
             } else {
-                float s = hi + lo;
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                if (lane == 0) sums[c] = added[c] = __double2ull_rn(static_cast<double>(s) * __hiloint2double((1023 + S) << 20, 0));
+                const float s = over_lanes(hi, lo);
+                if (lane == 0) sums[c] = added[c] = __double2ull_rn(static_cast<double>(s) * unit);
                 hi = lo = 0.0f;
             }
         });
         const uint64_t sum = scan_chunks();
+        if constexpr (!EXACT)
+            *under = row_sum(__double2ull_rn((static_cast<double>(under_hi) + static_cast<double>(under_lo)) * unit));
         a = __reduce_min_sync(0xffffffffu, a);
         z = __reduce_max_sync(0xffffffffu, z);
         if (lane == 0) atomicMin(&sh.r32[0], a), atomicMax(&sh.r32[1], z);
@@ -1302,12 +1402,13 @@ template <int DT, int TX> struct Sampler {
         return sum;
     }
     // The threshold key of the shortest prefix (of the elements with keys >= base) whose count
-    // or sum of weights reaches `need` (>= 1), given to within `err` (0: exact weights are used
+    // or sum of weights reaches `need` (>= 1), given to within `doubt` (0: exact weights are used
     // throughout); `base_key` where all of them do not.  It lies above lo (ordered bits).
-    // *sure is false where err left it open; *listed: the threshold is in the list of *listed
+    // *sure is false where the doubt left it open; *listed: the threshold is in the list of *listed
     // entries, and what lies above those is summed in `added` (0: it is not).
-    __device__ __noinline__ uint64_t select(bool by_mass, uint64_t need, uint64_t total, uint64_t err, uint64_t base_key, uint32_t lo,
-                                            uint32_t guide, bool* sure, uint32_t* listed) {
+    __device__ __noinline__ uint64_t select(bool by_mass, uint64_t need, uint64_t total, float share, Doubt doubt, uint64_t base_key,
+                                            uint32_t lo, uint32_t guide, bool* sure, uint32_t* listed) {
+        const uint64_t err = doubt.any;
         uint64_t left = need;
         uint32_t hi = order_bits(m);
         const uint32_t lowest = lo, first_guide = guide;
@@ -1328,11 +1429,15 @@ template <int DT, int TX> struct Sampler {
                 continue;
             }
             uint32_t n, least, most;
-            const uint64_t above = !by_mass ? split<true, false>(at, &n, &least, &most)
-                                   : err ? split<false, true>(at, &n, &least, &most) : split<true, true>(at, &n, &least, &most);
-            uint64_t k, under, with;
-            if (above < need && n <= kList && list_cut(by_mass, n, base_key, above, need, &k, &under, &with)) {
-                *sure = err == 0 || (with - need > err && need - under > err);
+            uint64_t k, under = 0, with;
+            const uint64_t above = !by_mass ? split<true, false>(at, &n, &least, &most, &under)
+                                   : err ? split<false, true>(at, &n, &least, &most, &under) : split<true, true>(at, &n, &least, &most, &under);
+            // Of fast weights the same pass sums the whole, so that what is above has the same errors in
+            // both (those of an addition depend on what else is added, and differ from pass to pass).
+            const uint64_t whole = above + under;
+            const uint64_t border = err && n <= kList ? mass_needed(whole + list_sum(n, 0), share) : need;
+            if (above < border && n <= kList && list_cut(by_mass, n, base_key, above, border, &k, &under, &with)) {
+                *sure = err == 0 || doubt.sure(under, border, with, 0);
                 *listed = by_mass ? n : 0;
                 return k;
             }
@@ -1397,7 +1502,8 @@ template <int DT, int TX> struct Sampler {
                 int col = 0;
                 float value;
                 uint64_t b, w;
-                locate(count - 1, false, same, &col, &value, &b, &w);
+                uint64_t inside;
+                locate(count - 1, false, same, &col, &value, &b, &w, &inside);
                 return (static_cast<uint64_t>(least) << 32) | (0xffffffffu - static_cast<uint32_t>(col));
             }
             lo = guide = least;
@@ -1513,17 +1619,17 @@ __device__ void sample_row(SampleShared<TX>& sh, const uint32_t* powers, unsigne
         bool whole;
         return g.u >= 1.0f ? total - 1 : part_of(total, g.u, &whole);
     };
-    const auto mass_needed = [&](uint64_t total) -> uint64_t {
-        bool whole;
-        const uint64_t n = part_of(total, g.top_p, &whole);
-        return !whole || n == 0 ? n + 1 : n;
-    };
     const auto all_weights = [&](float x, int) -> uint64_t { return r.weight(x); };
-    uint64_t total = 0, err = 0;
-    if (with_sums) {
-        total = r.scan_chunks();
-        err = fast_error(total);
-    }
+    uint64_t total = 0;
+    bool rough = with_sums;  // the sums are of fast weights
+    if (with_sums) total = r.scan_chunks();
+    // Whether sums leave no doubt.  (Most are farther from a border than any: 2^-24 (log 2 N + 14).)
+    const auto sure = [&](float share, uint64_t before, uint64_t target, uint64_t with, uint64_t summed) {
+        const uint64_t wide = total >> 18;
+        if (target - before > wide && with - target > wide && total > 1ull << 40) return true;
+        return Doubt(total, share, fast_error<DT>(), r.whole_distances(), r.N, r.S).sure(before, target, with, summed);
+    };
+    const auto doubt = [&](float share) { return rough ? Doubt(total, share, fast_error<DT>(), r.whole_distances(), r.N, r.S) : Doubt(); };
     uint32_t floor_bits = 0;  // of min_p
     if (g.use_min) {
         // x - m >= T log(min_p) in 64 bits, as a comparison of x in 32.
@@ -1540,14 +1646,15 @@ __device__ void sample_row(SampleShared<TX>& sh, const uint32_t* powers, unsigne
     uint32_t listed = 0;  // entries of the list, if what is kept is those and what `added` sums
     if (g.use_k || g.use_p || g.use_min) {
         // Everything that can be kept in a list, if it fits.  lo: a bound that all of it reaches.
-        const uint64_t need = g.use_k ? static_cast<uint64_t>(g.top_k) : g.use_p ? mass_needed(total) : 0;
+        const uint64_t need = g.use_k ? static_cast<uint64_t>(g.top_k) : g.use_p ? R::mass_needed(total, g.top_p) : 0;
         const bool by_mass = !g.use_k;
         uint32_t lo = 0, guide = 0, n = 0;
         bool fits;
         if (need) {
+            const uint64_t err = by_mass ? doubt(g.top_p).any : 0;
             if (by_mass) lo = r.light(total > need + 2 * err ? total - need - 2 * err : 0);
             guide = lo;
-            fits = r.bound(by_mass, need + (by_mass ? err : 0), total, &lo);
+            fits = r.bound(by_mass, need + err, total, &lo);
             if (fits) guide = lo;
             else if (!by_mass) r.bound(false, r.chunks * 24, 0, &guide);  // where three quarters of the maxima lie above
         } else {
@@ -1572,14 +1679,15 @@ __device__ void sample_row(SampleShared<TX>& sh, const uint32_t* powers, unsigne
             if (g.use_p) {
                 const uint64_t base = cut;
                 for (;;) {
-                    const uint64_t mass = mass_needed(g.use_k ? r.list_sum(n, base) : total), e = g.use_k ? 0 : err;
+                    const uint64_t mass = R::mass_needed(g.use_k ? r.list_sum(n, base) : total, g.top_p);
+                    const Doubt e = g.use_k ? Doubt() : doubt(g.top_p);
                     uint64_t k;
                     const bool found = r.list_cut(true, n, base, 0, mass, &k, &under, &with);
                     cut = found ? k : max(cut, static_cast<uint64_t>(lo) << 32);
                     // (Not reached: the cut lies below what min_p keeps.)
-                    if (e == 0 || (found ? with - mass > e && mass - under > e : g.use_min)) break;
+                    if (!e.any || (found ? e.sure(under, mass, with, with) : g.use_min)) break;
                     total = r.exact_chunks(-kInf, [](float, int) -> bool { return true; });  // too close to tell
-                    err = 0;
+                    rough = false;
                 }
             }
             threshold = max(cut, static_cast<uint64_t>(floor_bits) << 32);
@@ -1591,33 +1699,34 @@ __device__ void sample_row(SampleShared<TX>& sh, const uint32_t* powers, unsigne
             const auto kept = [&](float v, int c) -> uint64_t { return R::key(v, c) >= threshold ? r.weight(v) : 0; };
             int col;
             float x;
-            uint64_t before;
-            r.locate(drawn(total), false, kept, &col, &x, &before, &with);
+            uint64_t before, inside;
+            r.locate(drawn(total), false, kept, &col, &x, &before, &with, &inside);
             if (r.tid == 0) finish(col, x, total - one);
             return;
         }
         if (g.use_k) {
             bool sure;
-            threshold = r.select(false, static_cast<uint64_t>(g.top_k), 0, 0, 0, lo, guide, &sure, &listed);
+            threshold = r.select(false, static_cast<uint64_t>(g.top_k), 0, 0.0f, Doubt(), 0, lo, guide, &sure, &listed);
         }
         if (g.use_p) {
             const uint64_t base = threshold;
             if (g.use_k) {
                 total = r.exact_chunks(order_value(static_cast<uint32_t>(base >> 32)), [&](float x, int col) -> bool { return R::key(x, col) >= base; });
-                err = 0;
+                rough = false;
             }
             for (;;) {
                 bool sure;
-                const uint64_t mass = mass_needed(total);
-                const uint32_t from = max(static_cast<uint32_t>(base >> 32), r.light(total > mass + 2 * err ? total - mass - 2 * err : 0));
-                const uint64_t t = r.select(true, mass, total, err, base, from, from, &sure, &listed);
-                if (sure || err == 0) {
+                const uint64_t mass = R::mass_needed(total, g.top_p);
+                const Doubt e = doubt(g.top_p);
+                const uint32_t from = max(static_cast<uint32_t>(base >> 32), r.light(total > mass + 2 * e.any ? total - mass - 2 * e.any : 0));
+                const uint64_t t = r.select(true, mass, total, g.top_p, e, base, from, from, &sure, &listed);
+                if (sure || !rough) {
                     threshold = max(threshold, t);
-                    exact = err == 0;
+                    exact = !rough;
                     break;
                 }
                 total = r.exact_chunks(-kInf, [](float, int) -> bool { return true; });  // too close to tell
-                err = 0;
+                rough = false;
             }
         }
         const uint64_t t = static_cast<uint64_t>(floor_bits) << 32;
@@ -1625,20 +1734,20 @@ __device__ void sample_row(SampleShared<TX>& sh, const uint32_t* powers, unsigne
     }
     int col = 0;
     float x = 0.0f;
-    uint64_t before = 0, with = 0, rest = 0;
+    uint64_t before = 0, with = 0, inside = 0, rest = 0;
     // Where f32 sums hold the maximum's weight, they are good to 1e-7 of that.
-    const auto rest_from = [&](const auto& keep) { return err && total < 2 * one ? r.rest_of(total, x, col, keep) : total > one ? total - one : 0; };
+    const auto rest_from = [&](const auto& keep) { return rough && total < one + one / 4 * 3 ? r.rest_of(total, x, col, keep) : total > one ? total - one : 0; };
     if (threshold == 0) {  // nothing is cut off
         if (!with_sums || g.use_p) {  // (the sums of chunks are not there, or select() has used their place)
             total = r.exact_chunks(-kInf, [](float, int) -> bool { return true; });
-            err = 0;
+            rough = false;
         }
         for (;;) {
             const uint64_t target = drawn(total);
-            const bool found = r.locate(target, err == 0, all_weights, &col, &x, &before, &with);
-            if (err == 0 || (found && target - before > err && with - target > err)) break;
+            const bool found = r.locate(target, !rough, all_weights, &col, &x, &before, &with, &inside);
+            if (!rough || (found && sure(g.u, before, target, with, inside))) break;
             total = r.exact_chunks(-kInf, [](float, int) -> bool { return true; });  // too close to tell
-            err = 0;
+            rough = false;
         }
         rest = rest_from([](float, int) -> bool { return true; });
     } else {
@@ -1653,17 +1762,17 @@ __device__ void sample_row(SampleShared<TX>& sh, const uint32_t* powers, unsigne
             row_sync<TX>();
             r.list_chunks(listed, threshold);
             total = r.scan_chunks();
-            err = exact ? 0 : fast_error(total);
+            rough = !exact;
         } else {
             total = r.fast_chunks(low, [&](float v, int c) -> bool { return v > low || (v == low && c <= last); });
-            err = fast_error(total);
+            rough = true;
         }
         const uint64_t target = drawn(total);
-        const bool found = r.locate(target, err == 0, kept, &col, &x, &before, &with);
-        if (err && (!found || target - before <= err || with - target <= err)) {  // too close to tell
+        const bool found = r.locate(target, !rough, kept, &col, &x, &before, &with, &inside);
+        if (rough && !(found && sure(g.u, before, target, with, inside))) {  // too close to tell
             total = r.exact_chunks(low, [&](float v, int c) -> bool { return v > low || (v == low && c <= last); });
-            r.locate(drawn(total), true, kept, &col, &x, &before, &with);
-            err = 0;
+            r.locate(drawn(total), true, kept, &col, &x, &before, &with, &inside);
+            rough = false;
         }
         rest = rest_from([&](float v, int c) -> bool { return v > low || (v == low && c <= last); });
     }
@@ -1730,10 +1839,15 @@ template <int DT, int V> struct ShortRow {
         const float d = v - m, t = d * ch, e = fmaf(d, cl, fmaf(d, ch, -t));  // e: what t lost (NaN for -inf)
         return t > -126.0f ? fmaf(ex2(t), e * kLn2, ex2(t)) : 0.0f;
     }
-    // The part of a sum that a comparison of two may be off by: twice the 1.45e-7 of ex2, the
-    // rounding of x - m (2^-24 of |z|, at most 8 octaves where the mass is), and chains of
-    // M + 10 additions.
-    static constexpr float kError = 8e-7f + (M + 10) * 6e-8f;
+    // What a comparison of a part with a share u of the whole may be off by, of the whole.  Both add
+    // the same weights, whose errors count half at most (ex2's 1.46e-7 and a rounding) or once (2^-24
+    // of (m - x) / T, at most log 2048 = 7.6 over the weights): 5.6e-7.  The part of a cut passes
+    // through M + 12 additions at most, that of a draw through 2 E + V + 7, and the whole, of which the
+    // share is taken, through log M + 5 (11 at most) or E + V + 4.
+    static __device__ __forceinline__ float cut_error(float u) { return fmaf(fminf(u, 1.0f), 11 * 6e-8f, (M + 12) * 6e-8f + 5.6e-7f); }
+    static __device__ __forceinline__ float draw_error(float u) {
+        return fmaf(fminf(u, 1.0f), (E + V + 4) * 6e-8f, (2 * E + V + 7) * 6e-8f + 5.6e-7f);
+    }
     // By halves: the largest weight passes through log M roundings instead of M.
     template <int A, int L> __device__ __forceinline__ float part() const {
         if constexpr (L == 1) return w[A];
@@ -1964,7 +2078,7 @@ template <int DT, int V> __device__ __forceinline__ bool sample_short(const Samp
     if (g.use_k && !r.cut(false, static_cast<float>(g.top_k), 0.0f, 0.0f, keys, bins)) return false;
     if (g.use_p) {
         const float all = r.sum();
-        if (!r.cut(true, g.top_p * all, all, R::kError * all, keys, bins)) return false;
+        if (!r.cut(true, g.top_p * all, all, R::cut_error(g.top_p) * all, keys, bins)) return false;
     }
     if (g.use_min) {
         // In octaves; the border is good to 2^-21 of the distance and of the logarithm.
@@ -2011,8 +2125,9 @@ template <int DT, int V> __device__ __forceinline__ bool sample_short(const Samp
         }
     }
     // The vector, the lane and the element at which the running sum passes the target.
-    const float err = R::kError * total;
-    float target = fminf(fmaxf(g.u, 0.0f), 1.0f) * total;  // (fmaxf: NaN counts as 0)
+    const float u = fminf(fmaxf(g.u, 0.0f), 1.0f);  // (fmaxf: NaN counts as 0)
+    const float err = R::draw_error(u) * total;
+    float target = u * total;
     float before = 0.0f, run = 0.0f;
     float mine[E];
     int at = -1;
@@ -2065,6 +2180,11 @@ template <int DT, int V> __device__ __forceinline__ bool sample_short(const Samp
     return true;
 }
 
+// (Not inlined: one row in a thousand comes here, and its registers are not the others'.)
+template <int DT> __device__ __noinline__ void sample_long_way(SampleShared<32>& sh, const uint32_t* powers, unsigned char* dynamic, SampleArgs a, int64_t row) {
+    sample_row<DT, 32>(sh, powers, dynamic, a, row);
+}
+
 template <int DT, int V> __global__ void __launch_bounds__(32 * kShortWarps, V <= 4 ? 6 : 3) sample_short_kernel(SampleArgs a) {
     __shared__ ShortShared<DT> sh[kShortWarps];
     __shared__ uint32_t powers[64];
@@ -2076,7 +2196,7 @@ template <int DT, int V> __global__ void __launch_bounds__(32 * kShortWarps, V <
     const int64_t row = static_cast<int64_t>(blockIdx.x) * kShortWarps + warp;
     if (row >= a.B) return;
     if (sample_short<DT, V>(a, row, lane, sh[warp].keys, sh[warp].row.bins)) return;
-    sample_row<DT, 32>(sh[warp].row, powers, reinterpret_cast<unsigned char*>(sh[warp].dynamic), a, row);
+    sample_long_way<DT>(sh[warp].row, powers, reinterpret_cast<unsigned char*>(sh[warp].dynamic), a, row);
 }
 
 template <int DT, int V> cudaError_t launch_sample_short(SampleArgs a, cudaStream_t s) {
