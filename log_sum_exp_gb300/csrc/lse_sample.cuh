@@ -1685,7 +1685,7 @@ __device__ void sample_row(SampleShared<TX>& sh, const uint32_t* powers, unsigne
                     const bool found = r.list_cut(true, n, base, 0, mass, &k, &under, &with);
                     cut = found ? k : max(cut, static_cast<uint64_t>(lo) << 32);
                     // (Not reached: the cut lies below what min_p keeps.)
-                    if (!e.any || (found ? e.sure(under, mass, with, with) : g.use_min)) break;
+                    if (!e.any || (found ? e.sure(under, mass, with, with) : g.use_min && mass - r.list_sum(n, base) > e.any)) break;
                     total = r.exact_chunks(-kInf, [](float, int) -> bool { return true; });  // too close to tell
                     rough = false;
                 }
