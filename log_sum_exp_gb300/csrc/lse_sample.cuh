@@ -199,6 +199,7 @@ template <int DT, int TX> struct Sampler {
     float m, ch, cl;   // maximum; log2 e / T in two floats
     float far;         // the distance from which weights are 0
     int S;             // fractional bits of a weight
+    bool lost = false; // a threshold or a column was not found: the row is marked, not drawn without it
     int lane, warp, tid;  // in the row's group of threads
 
     __device__ __forceinline__ Sampler(SampleShared<TX>& s)
@@ -1423,7 +1424,10 @@ template <int DT, int TX> struct Sampler {
             if (!sampled && !bracket(by_mass, left, err, base_key, lo, guide, hi, &at)) {
                 // (Exact sums and the weights of single elements differ by 2^-30, so that a range can
                 // fall short of what it has to reach by that: all of it is kept then.)
-                if (!tentative) return err == 0 && by_mass ? max(base_key, static_cast<uint64_t>(lo) << 32) : base_key;
+                if (!tentative) {
+                    if (!by_mass) lost = true;  // (fewer than the count: lo was no bound)
+                    return err == 0 && by_mass ? max(base_key, static_cast<uint64_t>(lo) << 32) : base_key;
+                }
                 tentative = false;  // the sample was wrong
                 lo = lowest, guide = first_guide, hi = order_bits(m), left = need;
                 continue;
@@ -1455,13 +1459,14 @@ template <int DT, int TX> struct Sampler {
                 continue;
             }
             if (n <= kList || above >= need) {
-                if (err || !by_mass) return base_key;  // (err is too small, or all of them do not reach)
+                if (err) return base_key;  // not sure
+                if (!by_mass) return lost = true, base_key;
                 // Off by the 2^-30 again: the range's first element, or all of it.
                 if (n <= kList) {
                     const uint64_t in = list_sum(n, base_key);
                     if (in == 0) return max(base_key, (static_cast<uint64_t>(order_bits(at.hi)) + 1) << 32);
                     const uint64_t reached = min(max(need, above + 1), above + in);
-                    if (!list_cut(true, n, base_key, above, reached, &k, &under, &with)) return base_key;
+                    if (!list_cut(true, n, base_key, above, reached, &k, &under, &with)) return lost = true, base_key;
                     *listed = n;
                     return k;
                 }
@@ -1497,18 +1502,19 @@ template <int DT, int TX> struct Sampler {
                     lo = lowest, guide = first_guide, hi = order_bits(m), left = need;
                     continue;
                 }
-                if (all == 0) return base_key;
+                if (all == 0) return lost = true, base_key;
                 if (count > all) count = all;
                 int col = 0;
                 float value;
                 uint64_t b, w;
                 uint64_t inside;
-                locate(count - 1, false, same, &col, &value, &b, &w, &inside);
+                if (!locate(count - 1, false, same, &col, &value, &b, &w, &inside)) lost = true;
                 return (static_cast<uint64_t>(least) << 32) | (0xffffffffu - static_cast<uint32_t>(col));
             }
             lo = guide = least;
             hi = most;
         }
+        lost = err == 0;  // (else it is not sure)
         return base_key;
     }
 };
@@ -1586,10 +1592,10 @@ __device__ void sample_row(SampleShared<TX>& sh, const uint32_t* powers, unsigne
     }
     if constexpr (TX == 32) nan = __any_sync(0xffffffffu, nan);
     else nan = __syncthreads_or(nan);
-    if (bad || nan) {
+    const auto mark = [&]() {
         if (r.tid == 0) put_token(a, row, -1, __int_as_float(0x7fc00000));
-        return;
-    }
+    };
+    if (bad || nan) return mark();
     const uint32_t top = order_bits(r.m);
     if (g.greedy) {
         if (r.tid == 0) sh.r32[0] = 0xffffffffu;
@@ -1675,7 +1681,7 @@ __device__ void sample_row(SampleShared<TX>& sh, const uint32_t* powers, unsigne
         }
         if (fits) {
             uint64_t cut = 0, under, with;
-            if (g.use_k) r.list_cut(false, n, 0, 0, static_cast<uint64_t>(g.top_k), &cut, &under, &with);
+            if (g.use_k && !r.list_cut(false, n, 0, 0, static_cast<uint64_t>(g.top_k), &cut, &under, &with)) return mark();
             if (g.use_p) {
                 const uint64_t base = cut;
                 for (;;) {
@@ -1700,13 +1706,14 @@ __device__ void sample_row(SampleShared<TX>& sh, const uint32_t* powers, unsigne
             int col;
             float x;
             uint64_t before, inside;
-            r.locate(drawn(total), false, kept, &col, &x, &before, &with, &inside);
+            if (!r.locate(drawn(total), false, kept, &col, &x, &before, &with, &inside)) return mark();
             if (r.tid == 0) finish(col, x, total - one);
             return;
         }
         if (g.use_k) {
             bool sure;
             threshold = r.select(false, static_cast<uint64_t>(g.top_k), 0, 0.0f, Doubt(), 0, lo, guide, &sure, &listed);
+            if (r.lost) return mark();
         }
         if (g.use_p) {
             const uint64_t base = threshold;
@@ -1720,6 +1727,7 @@ __device__ void sample_row(SampleShared<TX>& sh, const uint32_t* powers, unsigne
                 const Doubt e = doubt(g.top_p);
                 const uint32_t from = max(static_cast<uint32_t>(base >> 32), r.light(total > mass + 2 * e.any ? total - mass - 2 * e.any : 0));
                 const uint64_t t = r.select(true, mass, total, g.top_p, e, base, from, from, &sure, &listed);
+                if (r.lost) return mark();
                 if (sure || !rough) {
                     threshold = max(threshold, t);
                     exact = !rough;
@@ -1745,6 +1753,7 @@ __device__ void sample_row(SampleShared<TX>& sh, const uint32_t* powers, unsigne
         for (;;) {
             const uint64_t target = drawn(total);
             const bool found = r.locate(target, !rough, all_weights, &col, &x, &before, &with, &inside);
+            if (!rough && !found) return mark();
             if (!rough || (found && sure(g.u, before, target, with, inside))) break;
             total = r.exact_chunks(-kInf, [](float, int) -> bool { return true; });  // too close to tell
             rough = false;
@@ -1771,8 +1780,10 @@ __device__ void sample_row(SampleShared<TX>& sh, const uint32_t* powers, unsigne
         const bool found = r.locate(target, !rough, kept, &col, &x, &before, &with, &inside);
         if (rough && !(found && sure(g.u, before, target, with, inside))) {  // too close to tell
             total = r.exact_chunks(low, [&](float v, int c) -> bool { return v > low || (v == low && c <= last); });
-            r.locate(drawn(total), true, kept, &col, &x, &before, &with, &inside);
+            if (!r.locate(drawn(total), true, kept, &col, &x, &before, &with, &inside)) return mark();
             rough = false;
+        } else if (!found) {
+            return mark();
         }
         rest = rest_from([&](float v, int c) -> bool { return v > low || (v == low && c <= last); });
     }
