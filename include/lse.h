@@ -713,7 +713,7 @@ typedef struct {
  * A row that is no distribution (it holds a NaN or +inf, or nothing but -inf, or N == 0),
  * or whose own temperature is NaN or outside 0 .. 1e20 or whose top_p or min_p is NaN or
  * below 0, gets the token -1 and logprob NaN; a top_k below 0 is off.  For values given for
- * all rows all of those are refused.  B <= INT32_MAX, N < INT32_MAX - 64.
+ * all rows all of those are refused.  B <= INT32_MAX, N <= INT32_MAX - 64.
  */
 LSE_API lse_status lse_sample(const void *x, lse_dtype dtype, int64_t B, int64_t N,
                               int64_t row_stride, const float *u, const lse_sampling *settings,

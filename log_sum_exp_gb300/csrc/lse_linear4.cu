@@ -10,9 +10,10 @@
 // group of 32 columns.  Within a word, nibble i holds q + 8 of column 2 i and nibble i + 4 that
 // of column 2 i + 1: one mask takes out two neighbours as the halves of a register.
 //
-// Into the form and back are bound by memory in f32 (32000 x 4096: 96 us, 5.9 TB/s of 0.59 GB) and
-// by instructions in 16 bits (128256 x 2048 bf16: 228 us, 2.9 TB/s of 0.66 GB); back 143 us, mostly
-// writes.  Products: lse_linear4.cuh.
+// Into the form and back are bound by memory in f32 on 16-byte boundaries (32000 x 4096: 96 us, 5.9
+// TB/s of 0.59 GB), by single-element loads through shared memory off them (50257 x 1001: 73 us, 44 %
+// of the memory's rate) and by instructions in 16 bits (128256 x 2048 bf16: 228 us, 2.9 TB/s of 0.66
+// GB); back 143 us, mostly writes.  Products: lse_linear4.cuh.
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -130,8 +131,8 @@ template <int DT> __device__ __forceinline__ void store_row_part(void* row, int6
 }
 
 // A warp takes 256 columns of a row kFormWords times over; the lanes of a group find its largest
-// magnitude with shuffles.  Per element and lane about ten instructions, which is what the
-// memory's rate leaves for 16-bit weights: a quotient is rounded by adding it to a number whose
+// magnitude with shuffles.  About 14 instructions per element and lane, where the memory's rate
+// leaves about six for 16-bit weights (39 % of it is reached): a quotient is rounded by adding it to a number whose
 // last bit counts 1 (its low bits are then the code).  Quotients of 16-bit numbers are often exact
 // halves, and 2^-13 away from one otherwise (2 w - (2 k + 1) s is a multiple of half the last bit of
 // an 11-bit s): one correction by the remainder brings them to 2^-22 and exact halves out exactly.

@@ -12,10 +12,12 @@
 // 2^-110) take a slower way, times 2^64 in columns of their own.
 //
 // Measured: one bf16 token x 128256 x 2048 39 us, 3.4 TB/s (the same loads without the products 26
-// us); 16 f16 tokens x 32000 x 4096 34 us.  The matrix pipe is busy for 14 % and 21 % of that, the
-// logic pipe for 50 % and 34 %: making floats of codes is what counts, so a matrix instruction
-// of a higher rate (tcgen05, which would also take the floats through shared memory or tensor
-// memory) has little to win before that does.  Deeper prefetching (6 blocks instead of 4: 41 us) and two
+// us); 16 f16 tokens x 32000 x 4096 32 us.  The matrix pipe is busy for 19 % and 21 % of that, the
+// logic pipe for 50 % and 34 %.  For one token making floats of codes is what counts (59 % of the
+// issue slots), so a matrix instruction of a higher rate (tcgen05, which would also take the floats
+// through shared memory or tensor memory) has little to win before that does.  For 16 tokens
+// nothing is busy (40 % of the issue slots): one CTA fits an SM, all of it waits for x before the
+// first product, and 250 groups of tiles are two rounds of 152 CTAs.  Deeper prefetching (6 blocks instead of 4: 41 us) and two
 // tiles per warp (46 us) were slower for one token; more warps sharing a tile's columns, which
 // adds barriers, too (53 us).
 #pragma once
@@ -43,7 +45,8 @@ template <bool F16> __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_
 template <bool F16> __device__ __forceinline__ void word_pairs(uint32_t w, uint32_t (&p)[4]) {
     if constexpr (F16) {
         // 1024 + q + 8 has its last bit at 1; in the second nibble the code counts 16 times,
-        // and (1024 + 16 (q + 8)) / 16 - 72 = q without a shift.
+        // and (1024 + 16 (q + 8)) / 16 - 72 = q without a shift.  (A published method: Kim, Henry,
+        // Fahim, Awadalla, "Who Says Elephants Can't Run", 2022; the constants are the format's.)
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
             const uint32_t v = i ? w >> 8 : w;

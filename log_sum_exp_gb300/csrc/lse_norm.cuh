@@ -599,8 +599,9 @@ cudaError_t launch_norm(const NormArgs& a, int64_t slots, bool few, cudaStream_t
     if (slots <= 64) return go(norm_kernel<DT, 32, 2, MODE>, 32);
     if (slots <= 128) return go(norm_kernel<DT, 32, 4, MODE>, 32);
     if (slots <= 256) return go(norm_kernel<DT, 128, 2, MODE>, 128);
-    // Rows by the thousand: four slots per thread wait less at the rows' sums (16384 x 4096 bf16 97
-    // us, two slots 107, one 154).  A few: one slot answers sooner (300 x 4096 4.3 us, 5.3, 7.1).
+    // Rows by the thousand: four slots per thread wait less at the rows' sums (16384 x 4096 bf16 82 us,
+    // one slot 139; 8192 x 8192 86, two slots 104).  A few: fewer slots answer sooner (300 x 4096 3.1
+    // us, four slots 4.7; 300 x 8192 4.3 and 5.5).
     if (slots <= 512) return few ? go(norm_kernel<DT, 512, 1, MODE>, 512) : go(norm_kernel<DT, 128, 4, MODE>, 128);
     if (slots <= 1024) return few ? go(norm_kernel<DT, 512, 2, MODE>, 512) : go(norm_kernel<DT, 256, 4, MODE>, 256);
     if (slots <= 2048) return go(norm_kernel<DT, 1024, 2, MODE>, 1024);

@@ -36,7 +36,8 @@
 //
 //     E (2 u (1 - u) + max(0, 2 u - 1) L) + 2^-24 log(2 N / sum) max(u, 1 - u)
 //
-// of the whole, the second term only with rounded distances (Doubt).  Where a comparison is closer, the row is done again with exact weights.
+// of the whole, the second term only with rounded distances (Doubt).  Where a comparison is closer, the
+// row is done again with exact weights.
 //
 // Threshold.  Every lane's maximum in every chunk is kept in shared memory.  They bound the
 // threshold from below (the k-th largest of them is at most the k-th largest element; the same
@@ -49,10 +50,12 @@
 // narrows (a run of equal values so heavy that the widths of bins hide where the sum passes) is
 // bisected, a pass for each half.
 //
-// Measured (us): 2048 x 128256 bf16, nothing cut off 216 (2.4 TB/s; the pass alone, without weights,
-// 126, bound by loads at 42 % of the warps), top_k 50 and top_p 0.95 275, top_p 0.9 of rows from peaked
-// to flat 2750 (instructions: three to four passes of 10 to 15 per element); one such row 15, 26 and
-// 69; 65536 x 261 f32 top_p 0.9 174 (1960 instructions per row).  Counters of several
+// Measured (us): 2048 x 128256 bf16, nothing cut off 237 (2.2 TB/s; the pass alone, without weights,
+// 126, bound by loads at 42 % of the warps; without rows too close to tell 195), top_k 50 and top_p
+// 0.95 280, top_p 0.9 of rows from peaked to flat 2680 (instructions: three to four passes of 10 to 15
+// per element); one such row 16, 28 and 55; 65536 x 261 f32 top_p 0.9 150 (68 % of the issue slots).
+// Putting the lanes' sums together by shuffles in f32 instead takes 12 us less for the 2048 rows, and more
+// of them are too close to tell.  Counters of several
 // threads are the slowest part: 26 ns for each addition with a result to one of them, so places in a
 // list are handed out per warp; histograms by the bits of f32, which have two bins for all
 // values within a factor of two, took 11 ms where bins linear in the value take 3.
@@ -1128,7 +1131,8 @@ template <int DT, int TX> struct Sampler {
         float lo, hi;
         uint64_t through;
     };
-    // The range that holds the threshold of top-p, from a sample: one vector in `every` of a lane.
+    // The range that holds the threshold of top-p, from a sample: each lane's first vector in every
+    // so many chunks.
     // What lies below the threshold has a known sum, `rest`, made of many light elements, so the
     // sample's light elements give its place to within a few percent of that, whatever a few heavy
     // elements hold; split() shows whether the threshold is in the range.
@@ -1138,7 +1142,7 @@ template <int DT, int TX> struct Sampler {
         const Bins bins(lo_bits, hi_bits);
         const float low = order_value(lo_bits);
         clear_bins();
-        // every fourth vector, and of every `step`-th chunk: about 2^15 elements
+        // (of every `step`-th chunk: about 2^15 elements, one vector in chunk / 32 of such a chunk)
         int step = 1;
         while (chunks / (2 * step) * 32 * E >= (1 << 15)) step *= 2;
         float light = 0.0f;  // the sample's weights below lo
@@ -1629,7 +1633,8 @@ __device__ void sample_row(SampleShared<TX>& sh, const uint32_t* powers, unsigne
     uint64_t total = 0;
     bool rough = with_sums;  // the sums are of fast weights
     if (with_sums) total = r.scan_chunks();
-    // Whether sums leave no doubt.  (Most are farther from a border than any: 2^-24 (log 2 N + 14).)
+    // Whether sums leave no doubt.  (Most are farther from a border than any doubt, which is less than
+    // 2^-18 of the whole.)
     const auto sure = [&](float share, uint64_t before, uint64_t target, uint64_t with, uint64_t summed) {
         const uint64_t wide = total >> 18;
         if (target - before > wide && with - target > wide && total > 1ull << 40) return true;
